@@ -10,17 +10,19 @@ first call raises ``LibraryNotBuilt``.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import functools
 import os
 import threading
-from typing import Optional
+from typing import Optional, Sequence
 
 import torch
 
 __all__ = [
     "ln_fwd", "rms_fwd", "ln_fwd_add", "rms_fwd_add", "ln_fwd_fp8", "rms_fwd_fp8", "ln_bwd", "rms_bwd",
     "make_plan", "make_bwd_plan", "NormPlan", "NormError", "LibraryNotBuilt", "library", "host_rows_pipeline",
-    "host_rows_wait",
+    "host_rows_wait", "gn_fwd", "gn_bwd", "make_gn_plan", "GnPlan", "grad_norm", "grad_clip",
     "NORM_F32", "NORM_BF16", "NORM_F16", "NORM_MAP_GROUP", "NORM_MAP_CTA",
 ]
 
@@ -54,6 +56,19 @@ class NormPlan(ctypes.Structure):
         for k, v in d.items():
             setattr(p, k, int(v))
         return p
+
+
+class GnPlan(ctypes.Structure):
+    """Mirror of ``gn_plan`` in include/libnorm_group.h."""
+    _fields_ = [(k, ctypes.c_int32) for k in ("path", "vec_elems", "tile", "threads", "per_thread", "cluster",
+                                              "chunks", "out_chunks")]
+
+    def as_dict(self) -> dict:
+        return {k: getattr(self, k) for k, _ in self._fields_}
+
+    @classmethod
+    def from_dict(cls, d: dict) -> "GnPlan":
+        return cls(**{k: int(v) for k, v in d.items()})
 
 
 class NormError(RuntimeError):
@@ -115,6 +130,20 @@ def library() -> ctypes.CDLL:
               "ln_fwd_fp8_planned", "rms_fwd_fp8_planned", "ln_fwd_strided", "rms_fwd_strided",
               "norm_last_cuda_error", "norm_abi_version", "norm_wait_timeouts", "norm_synchronize",
               "norm_set_wait_limit", "norm_wait_limit"):
+        getattr(L, f).restype = ctypes.c_int
+    gp = ctypes.POINTER(GnPlan)
+    L.gn_fwd.argtypes = [vp, i64, i64, vp, vp, vp, i64, i64, vp, vp, vp, sz, i64, i64, i64, i64, f32, i32, i32, vp]
+    L.gn_bwd.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, sz, i64, i64, i64, i64,
+                         i32, i32, vp]
+    L.gn_fwd_planned.argtypes = L.gn_fwd.argtypes + [gp]
+    L.gn_bwd_planned.argtypes = L.gn_bwd.argtypes + [gp]
+    L.gn_make_plan.argtypes = [i64, i64, i64, i64, i32, i32, i32, i32, gp]
+    L.gn_workspace_bytes.argtypes = [i64, i64, i64, i64, i32, i32, i32, gp, ctypes.POINTER(sz)]
+    L.grad_norm.argtypes = [vp, i64, vp, vp, sz, vp]
+    L.grad_clip.argtypes = [vp, i64, f32, vp, vp, sz, vp]
+    L.grad_workspace_bytes.argtypes = [i64, i32, ctypes.POINTER(sz)]
+    for f in ("gn_fwd", "gn_bwd", "gn_fwd_planned", "gn_bwd_planned", "gn_make_plan", "gn_workspace_bytes",
+              "grad_norm", "grad_clip", "grad_workspace_bytes"):
         getattr(L, f).restype = ctypes.c_int
     L.norm_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     L.norm_synchronize.argtypes = []
@@ -567,6 +596,310 @@ def rms_fwd_fp8(x: torch.Tensor, w: torch.Tensor, scale, eps: float = 1e-6, *,
     if residual is not None:
         return hh.view(x.shape), y8
     return y8
+
+
+# ------------------------------------------------------------ group norm
+_ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "gelu": 2}
+_CODES = {torch.float32: NORM_F32, torch.bfloat16: NORM_BF16, torch.float16: NORM_F16}
+
+
+@functools.lru_cache(maxsize=None)
+def _sms(index: int) -> int:
+    return torch.cuda.get_device_properties(index).multi_processor_count
+
+
+def _on_device(index: int, call, stream: Optional[torch.cuda.Stream]) -> int:
+    """``call(stream handle)`` with CUDA device ``index`` current."""
+    if torch.cuda.current_device() == index:
+        return call(stream.cuda_stream if stream is not None else torch.cuda.current_stream(index).cuda_stream)
+    with torch.cuda.device(index):
+        return call(_stream_handle(stream, torch.device("cuda", index)))
+
+
+def make_gn_plan(B: int, S: int, C: int, groups: int, dtype: torch.dtype, backward: bool = False,
+                 vec_elems: Optional[int] = None, num_sms: int = 152) -> dict:
+    """The plan gn_fwd / gn_bwd would choose for a [B, S, C] tensor (host
+    only); ``vec_elems``: channels per access the tensors allow (default: the
+    widest that C allows)."""
+    code = _dtype_code(dtype)
+    if vec_elems is None:
+        vec_elems = next(v for v in ((4, 1) if code == NORM_F32 else (8, 2, 1)) if C % v == 0)
+    p = GnPlan()
+    st = library().gn_make_plan(B, S, C, groups, code, int(backward), vec_elems, num_sms, ctypes.byref(p))
+    if st != NORM_OK:
+        raise NormError(st, "gn_make_plan")
+    return p.as_dict()
+
+
+@functools.lru_cache(maxsize=4096)
+def _gn_workspace_bytes(B: int, S: int, C: int, groups: int, code: int, backward: bool, sms: int) -> int:
+    n = ctypes.c_size_t()
+    st = library().gn_workspace_bytes(B, S, C, groups, code, int(backward), sms, None, ctypes.byref(n))
+    if st != NORM_OK:
+        raise NormError(st, "gn_workspace_bytes")
+    return n.value
+
+
+def gn_workspace_bytes(x: torch.Tensor, groups: int, backward: bool = False, plan=None) -> int:
+    """Bytes of workspace gn_fwd / gn_bwd need for x."""
+    B, C = x.shape[0], x.shape[-1]
+    S = x.numel() // (B * C) if x.numel() else 0
+    code = _dtype_code(x.dtype)
+    if plan is None:
+        return _gn_workspace_bytes(B, S, C, groups, code, bool(backward), _sms(x.get_device()))
+    n = ctypes.c_size_t()
+    p = plan if isinstance(plan, GnPlan) else GnPlan.from_dict(plan)
+    st = library().gn_workspace_bytes(B, S, C, groups, code, int(backward), 0, ctypes.byref(p), ctypes.byref(n))
+    if st != NORM_OK:
+        raise NormError(st, "gn_workspace_bytes")
+    return n.value
+
+
+def _positions(x: torch.Tensor) -> Optional[torch.Tensor]:
+    """x as [B, S, C] without a copy, or None where its strides do not allow
+    one row pitch and one sample pitch."""
+    if x.dim() != 3:
+        if x.dim() > 3:
+            try:
+                x = x.view(x.shape[0], -1, x.shape[-1])
+            except RuntimeError:
+                return None
+        else:
+            x = x.unsqueeze(1)
+    if x.is_contiguous():
+        return x
+    B, S, C = x.shape
+    xb, xr, xc = x.stride()
+    if (C > 1 and xc != 1) or (S > 1 and xr < C) or (B > 1 and xb < (S - 1) * xr + C):
+        return None
+    return x
+
+
+def _gn_input(x: torch.Tensor) -> torch.Tensor:
+    v = _positions(x)
+    return v if v is not None else _positions(x.contiguous())
+
+
+def _gn_output(out: torch.Tensor, x: torch.Tensor, name: str) -> torch.Tensor:
+    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError(f"{name} must have x's shape, dtype and device")
+    v = _positions(out)
+    if v is None:
+        raise ValueError(f"{name} must have evenly strided positions and samples with unit channel stride")
+    return v
+
+
+def _gn_check(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, groups: int, activation, what: str):
+    if not x.is_cuda:
+        raise ValueError(f"{what} needs a CUDA tensor")
+    code = _dtype_code(x.dtype)
+    if x.dim() < 2:
+        raise ValueError("x must be [B, ..., C]: samples first, channels last")
+    C = x.shape[-1]
+    if groups < 1 or C < 1 or C % groups != 0:
+        raise ValueError(f"{C} channels do not form {groups} groups")
+    try:
+        act = _ACTIVATIONS[activation]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation must be None, 'none', 'silu' or 'gelu', got {activation!r}") from None
+    return code, act, C, _param(gamma, x, "gamma"), _param(beta, x, "beta")
+
+
+def _f32(t: Optional[torch.Tensor], shape, x: torch.Tensor, name: str) -> torch.Tensor:
+    """`t`, or a new fp32 tensor of that shape."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.float32, device=x.device)
+    n = 1
+    for v in shape:
+        n *= v
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous() or t.device != x.device:
+        raise ValueError(f"{name} must be a contiguous fp32 tensor of {n} elements on {x.device}")
+    return t
+
+
+def _gn_workspace(ws: Optional[torch.Tensor], need: int, x: torch.Tensor):
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    if ws.device != x.device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
+    return ws
+
+
+def gn_fwd(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, groups: int, eps: float = 1e-5, *,
+           activation: Optional[str] = None, out: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+           rstd: Optional[torch.Tensor] = None, stats: bool = True, workspace: Optional[torch.Tensor] = None,
+           stream: Optional[torch.cuda.Stream] = None, plan=None):
+    """Group norm forward with an activation over a channels-last CUDA tensor
+    ``[B, ..., C]``: ``y = act((x - mean) * rstd * gamma + beta)`` with the
+    statistics of each sample's groups of ``C / groups`` channels over all
+    positions between. ``activation``: None (or "none"), "silu" or "gelu"
+    (erf form). A ``[B, C, H, W]`` tensor in torch's channels_last layout is
+    ``x.permute(0, 2, 3, 1)``.
+
+    Returns ``(y, mean, rstd)``; mean and rstd are fp32 ``[B, groups]`` (None
+    when ``stats=False``). ``out`` may be ``x`` itself (in place).
+    ``workspace`` (gn_workspace_bytes; any dtype) is allocated when not given;
+    calls that share one must not overlap on the GPU."""
+    code, act, C, g, b = _gn_check(x, gamma, beta, groups, activation, "gn_fwd")
+    x3 = _gn_input(x)
+    B, S, _ = x3.shape
+    y3 = torch.empty((B, S, C), dtype=x.dtype, device=x.device) if out is None else _gn_output(out, x, "out")
+    if stats:
+        mean, rstd = _f32(mean, (B, groups), x, "mean"), _f32(rstd, (B, groups), x, "rstd")
+    else:
+        mean = rstd = None
+    index = x.get_device()
+    need = (_gn_workspace_bytes(B, S, C, groups, code, False, _sms(index)) if plan is None
+            else gn_workspace_bytes(x3, groups, False, plan))
+    ws = _gn_workspace(workspace, need, x)
+    L = library()
+    xs, ys = x3.stride(), y3.stride()
+
+    def call(h):
+        args = (x3.data_ptr(), xs[0], xs[1], g.data_ptr(), b.data_ptr(), y3.data_ptr(), ys[0], ys[1], _ptr(mean),
+                _ptr(rstd), _ptr(ws), ws.nbytes if ws is not None else 0, B, S, C, groups, eps, act, code, h)
+        return L.gn_fwd(*args) if plan is None else L.gn_fwd_planned(*args, _gn_plan_ptr(plan))
+
+    st = _on_device(index, call, stream)
+    if st != NORM_OK:
+        raise NormError(st, "gn_fwd")
+    return (out if out is not None else y3 if x.dim() == 3 else y3.view(x.shape)), mean, rstd
+
+
+def _gn_plan_ptr(plan):
+    return ctypes.byref(plan if isinstance(plan, GnPlan) else GnPlan.from_dict(plan))
+
+
+def gn_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, mean: torch.Tensor,
+           rstd: torch.Tensor, groups: int, *, activation: Optional[str] = None, dx: Optional[torch.Tensor] = None,
+           dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+           workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None, plan=None):
+    """Group norm backward: returns ``(dx, dgamma, dbeta)``; dgamma and dbeta
+    are fp32 ``[C]``. ``mean``/``rstd`` are gn_fwd's fp32 statistics and
+    ``activation`` the forward's; the activation's argument is recomputed
+    from x. ``dx`` may be ``dy`` or ``x`` itself (in place)."""
+    code, act, C, g, b = _gn_check(x, gamma, beta, groups, activation, "gn_bwd")
+    if dy.shape != x.shape or dy.dtype != x.dtype or dy.device != x.device:
+        raise ValueError("dy must have x's shape, dtype and device")
+    x3, dy3 = _gn_input(x), _gn_input(dy)
+    B, S, _ = x3.shape
+    mean, rstd = _given_f32(mean, B * groups, x, "mean"), _given_f32(rstd, B * groups, x, "rstd")
+    dx3 = torch.empty((B, S, C), dtype=x.dtype, device=x.device) if dx is None else _gn_output(dx, x, "dx")
+    dg, db = _f32(dgamma, (C,), x, "dgamma"), _f32(dbeta, (C,), x, "dbeta")
+    index = x.get_device()
+    need = (_gn_workspace_bytes(B, S, C, groups, code, True, _sms(index)) if plan is None
+            else gn_workspace_bytes(x3, groups, True, plan))
+    ws = _gn_workspace(workspace, need, x)
+    L = library()
+    ds, xs, os_ = dy3.stride(), x3.stride(), dx3.stride()
+
+    def call(h):
+        args = (dy3.data_ptr(), ds[0], ds[1], x3.data_ptr(), xs[0], xs[1], g.data_ptr(), b.data_ptr(),
+                mean.data_ptr(), rstd.data_ptr(), dx3.data_ptr(), os_[0], os_[1], dg.data_ptr(), db.data_ptr(),
+                _ptr(ws), ws.nbytes if ws is not None else 0, B, S, C, groups, act, code, h)
+        return L.gn_bwd(*args) if plan is None else L.gn_bwd_planned(*args, _gn_plan_ptr(plan))
+
+    st = _on_device(index, call, stream)
+    if st != NORM_OK:
+        raise NormError(st, "gn_bwd")
+    return (dx if dx is not None else dx3 if x.dim() == 3 else dx3.view(x.shape)), dg, db
+
+
+def _given_f32(t: torch.Tensor, n: int, x: torch.Tensor, name: str) -> torch.Tensor:
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous() or t.device != x.device:
+        raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor of {n} elements")
+    return t
+
+
+# ------------------------------------------------------------ gradients
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's values lie one after the other in memory, in any order of
+    its dimensions."""
+    if t.is_contiguous():
+        return True
+    n = 1
+    for size, stride in sorted(zip(t.shape, t.stride()), key=lambda v: v[1]):
+        if size != 1:
+            if stride != n:
+                return False
+            n *= size
+    return True
+
+
+@functools.lru_cache(maxsize=None)
+def _grad_workspace_bytes(count: int, sms: int) -> int:
+    n = ctypes.c_size_t()
+    st = library().grad_workspace_bytes(count, sms, ctypes.byref(n))
+    if st != NORM_OK:
+        raise NormError(st, "grad_workspace_bytes")
+    return n.value
+
+
+def _grad_call(what, grads, outs, max_norm, norm, workspace, stream):
+    if not grads:
+        raise ValueError(f"{what} needs at least one tensor")
+    index = grads[0].get_device()
+    if index < 0:
+        raise ValueError(f"{what} needs CUDA tensors")
+    flat = []
+    for i, t in enumerate(grads):
+        code = _CODES.get(t.dtype)
+        if code is None:
+            _dtype_code(t.dtype)
+        if t.get_device() != index:
+            raise ValueError(f"every gradient must be on cuda:{index}")
+        if not t.is_contiguous() and not _dense(t):
+            raise ValueError(f"gradient {i} has gaps or overlaps between its values")
+        o = t
+        if outs is not None:
+            o = outs[i]
+            if o.shape != t.shape or o.dtype != t.dtype or o.get_device() != index or o.stride() != t.stride():
+                raise ValueError(f"out {i} must have its gradient's shape, strides, dtype and device")
+        flat += (t.data_ptr(), o.data_ptr(), t.numel(), code)  # (dtype, reserved): one 64-bit word
+    device = grads[0].device
+    norm = _f32(norm, (), grads[0], "norm")
+    need = _grad_workspace_bytes(-(-len(grads) // 64) * 64, _sms(index))
+    ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=device)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    table = array.array("q", flat)
+    L = library()
+
+    def call(h):
+        at = table.buffer_info()[0]
+        if max_norm is None:
+            return L.grad_norm(at, len(grads), norm.data_ptr(), ws.data_ptr(), ws.nbytes, h)
+        return L.grad_clip(at, len(grads), max_norm, norm.data_ptr(), ws.data_ptr(), ws.nbytes, h)
+
+    st = _on_device(index, call, stream)
+    if st != NORM_OK:
+        raise NormError(st, what)
+    return norm
+
+
+def grad_norm(grads: Sequence[torch.Tensor], *, norm: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The global norm of a list of CUDA gradients, ``sqrt(sum of all
+    squares)``: one fp32 value on the device. The tensors may differ in shape
+    and type (float32, bfloat16, float16); each must be dense (its values one
+    after the other in any order of the dimensions). ``workspace`` (any
+    dtype) is allocated when not given; calls that share one must not overlap
+    on the GPU."""
+    return _grad_call("grad_norm", grads, None, None, norm, workspace, stream)
+
+
+def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[Sequence[torch.Tensor]] = None,
+              norm: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None):
+    """Scale a list of gradients by ``min(1, max_norm / (norm + 1e-6))`` with
+    norm their global norm (grad_norm): in place, or into ``out``, a list of
+    tensors of the same shapes, strides and types. Returns ``(out, norm)``.
+    With an infinite norm the coefficient is 0, with a NaN norm NaN: read
+    ``norm`` to skip such a step. A tensor may be listed once only."""
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"out must hold one tensor per gradient ({len(grads)}), got {len(out)}")
+    norm = _grad_call("grad_clip", grads, out, float(max_norm), norm, workspace, stream)
+    return (out if out is not None else grads), norm
 
 
 # ------------------------------------------------------------ host buffers

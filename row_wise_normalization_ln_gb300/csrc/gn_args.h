@@ -1,0 +1,70 @@
+// Argument block of the group norm kernels and their launchers, shared by the
+// host side (gn.cpp) and the kernels (gn_kernels.cuh).
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime_api.h>
+
+#include "libnorm_group.h"
+
+namespace libnorm {
+
+constexpr int kGnMaxThreads = 512;
+// Channels of a tile whose accesses span groups (their sums are kept per
+// channel): bounds the shared memory of the reductions.
+constexpr int kGnMaxMixedChannels = 512;
+
+struct GnArgs {
+    const void* x;
+    const void* dy;        // backward
+    const void* gamma;
+    const void* beta;
+    void* y;               // forward: y; backward: dx
+    float* mean;           // [B, G]: written by the forward, read by the backward
+    float* rstd;
+    float* shift;          // SPLIT forward: [B, G], the groups' first elements
+    float2* part;          // SPLIT: [B, G, tpg, parts] group states of the merged row chunks
+    float* colg;           // backward: partial rows of dgamma and dbeta, [B * parts] rows of C values at a
+    float* colb;           // pitch of col_pitch (dgamma and dbeta themselves where one partial row is all)
+    int64_t S;
+    int64_t xb, xr, dyb, dyr, yb, yr;  // pitches in elements
+    int64_t col_pitch;
+    int32_t C, G, D;
+    int32_t ncols;         // accesses per row: C / VEC
+    int32_t tile;          // accesses of a row per CTA
+    int32_t tiles;         // tiles per row
+    int32_t tpg;           // tiles a group may touch (1 when tiles are whole groups)
+    int32_t par;           // rows a CTA works on at once: threads / tile
+    int32_t cluster;
+    int32_t chunks;        // row chunks summed per sample and tile
+    int32_t out_chunks;    // row chunks written per sample and tile
+    int64_t chunk_rows;    // rows per summed chunk (CHIP: per CTA of the cluster)
+    int64_t out_rows;      // rows per written chunk
+    float eps;
+};
+
+// Dynamic shared memory of a kernel, from its plan: the per-thread states
+// ([par][units]) and two arrays of group values. `units` is tile (accesses
+// within one group) or tile * vec_elems (accesses that span groups, and the
+// backward, whose column sums are per channel).
+inline int64_t gn_smem_bytes(int par, int units, int groups) {
+    return (int64_t(par) * units + 2 * int64_t(groups)) * 8;
+}
+
+// Groups a tile of `channels` channels can touch.
+inline int64_t gn_tile_groups(int64_t channels, int64_t D, bool whole) {
+    return whole ? channels / D : (channels - 1 + D - 1) / D + 1;
+}
+
+cudaError_t launch_gn_fwd_f32(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s);
+cudaError_t launch_gn_fwd_bf16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s);
+cudaError_t launch_gn_fwd_f16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s);
+cudaError_t launch_gn_bwd_f32(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, float* dgamma,
+                              float* dbeta, cudaStream_t s);
+cudaError_t launch_gn_bwd_bf16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, float* dgamma,
+                               float* dbeta, cudaStream_t s);
+cudaError_t launch_gn_bwd_f16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, float* dgamma,
+                              float* dbeta, cudaStream_t s);
+
+}  // namespace libnorm

@@ -1,0 +1,221 @@
+// Group norm over channels-last tensors [B, S, C], building blocks shared by
+// the forward (gn_fwd.cuh) and the backward (gn_bwd.cuh).
+//
+// A thread keeps one access column (VEC neighbouring channels) of its CTA's
+// tile and walks rows: channel parameters stay in registers, and `par` rows
+// are in flight per step. Groups of D channels: when D is a multiple of VEC
+// (ONE) an access lies within one group and a thread's state is one per
+// access, otherwise it is one per channel. The states of a CTA meet in shared
+// memory, one warp per group; those of a cluster in distributed shared
+// memory; those of a sample's clusters in the caller's workspace.
+#pragma once
+
+#include "gn_args.h"
+#include "norm_device.cuh"
+#include "norm_kernels.cuh"
+
+namespace libnorm {
+
+// ------------------------------------------------------------ accesses
+// VEC elements: 16 bytes, a 32-bit pair of 16-bit values, or one element.
+// Values are handed out as fp32 pairs (of a single element the second value
+// of the pair is 0 and never counted).
+template <class T>
+struct Gn16 {
+    using Pair = Bf16Pair;
+};
+template <>
+struct Gn16<__half> {
+    using Pair = F16Pair;
+};
+
+template <class T, int VEC>
+struct GnVec {
+    static_assert(sizeof(T) == 2 && VEC == 8, "16-byte access of a 16-bit type");
+    using Raw = uint4;
+    using P = typename Gn16<T>::Pair;
+    static constexpr int H = 4;
+    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
+    static __device__ __forceinline__ Raw load(const T* p) { return *reinterpret_cast<const uint4*>(p); }
+    static __device__ __forceinline__ void store(T* p, const Raw& v) { *reinterpret_cast<uint4*>(p) = v; }
+    static __device__ __forceinline__ float2 get(const Raw& r, int i) {
+        return P::widen(i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w);
+    }
+    static __device__ __forceinline__ void set(Raw& r, int i, float2 v) {
+        const uint32_t w = P::pack(v.x, v.y);
+        if (i == 0) r.x = w;
+        else if (i == 1) r.y = w;
+        else if (i == 2) r.z = w;
+        else r.w = w;
+    }
+};
+
+template <>
+struct GnVec<float, 4> {
+    using Raw = uint4;
+    static constexpr int H = 2;
+    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
+    static __device__ __forceinline__ Raw load(const float* p) { return *reinterpret_cast<const uint4*>(p); }
+    static __device__ __forceinline__ void store(float* p, const Raw& v) { *reinterpret_cast<uint4*>(p) = v; }
+    static __device__ __forceinline__ float2 get(const Raw& r, int i) {
+        return i == 0 ? make_float2(__uint_as_float(r.x), __uint_as_float(r.y))
+                      : make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+    }
+    static __device__ __forceinline__ void set(Raw& r, int i, float2 v) {
+        if (i == 0) {
+            r.x = __float_as_uint(v.x);
+            r.y = __float_as_uint(v.y);
+        } else {
+            r.z = __float_as_uint(v.x);
+            r.w = __float_as_uint(v.y);
+        }
+    }
+};
+
+template <>
+struct GnVec<float, 1> {
+    using Raw = uint32_t;
+    static constexpr int H = 1;
+    static __device__ __forceinline__ Raw zero() { return 0; }
+    static __device__ __forceinline__ Raw load(const float* p) { return *reinterpret_cast<const uint32_t*>(p); }
+    static __device__ __forceinline__ void store(float* p, Raw v) { *reinterpret_cast<uint32_t*>(p) = v; }
+    static __device__ __forceinline__ float2 get(Raw r, int) { return make_float2(__uint_as_float(r), 0.f); }
+    static __device__ __forceinline__ void set(Raw& r, int, float2 v) { r = __float_as_uint(v.x); }
+};
+
+template <class T>
+struct GnVec<T, 2> {
+    using Raw = uint32_t;
+    using P = typename Gn16<T>::Pair;
+    static constexpr int H = 1;
+    static __device__ __forceinline__ Raw zero() { return 0; }
+    static __device__ __forceinline__ Raw load(const T* p) { return *reinterpret_cast<const uint32_t*>(p); }
+    static __device__ __forceinline__ void store(T* p, Raw v) { *reinterpret_cast<uint32_t*>(p) = v; }
+    static __device__ __forceinline__ float2 get(Raw r, int) { return P::widen(r); }
+    static __device__ __forceinline__ void set(Raw& r, int, float2 v) { r = P::pack(v.x, v.y); }
+};
+
+template <class T>
+struct GnVec<T, 1> {
+    using Raw = uint32_t;
+    using P = typename Gn16<T>::Pair;
+    static constexpr int H = 1;
+    static __device__ __forceinline__ Raw zero() { return 0; }
+    static __device__ __forceinline__ Raw load(const T* p) { return *reinterpret_cast<const unsigned short*>(p); }
+    static __device__ __forceinline__ void store(T* p, Raw v) {
+        *reinterpret_cast<unsigned short*>(p) = static_cast<unsigned short>(v);
+    }
+    static __device__ __forceinline__ float2 get(Raw r, int) { return P::widen(r); }
+    static __device__ __forceinline__ void set(Raw& r, int, float2 v) { r = P::pack(v.x, 0.f); }
+};
+
+template <class T>
+__device__ __forceinline__ float gn_elem(const T* p) {
+    return GnVec<T, 1>::get(GnVec<T, 1>::load(p), 0).x;
+}
+
+__device__ __forceinline__ float2 f2_sub(float2 a, float2 b) {
+    return __fadd2_rn(a, make_float2(-b.x, -b.y));
+}
+template <int VEC>
+__device__ __forceinline__ float f2_sum(float2 v) {
+    return VEC == 1 ? v.x : v.x + v.y;
+}
+
+// ------------------------------------------------------------ activations
+template <int ACT>
+__device__ __forceinline__ float gn_act(float z) {
+    if constexpr (ACT == NORM_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    if constexpr (ACT == NORM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    return z;
+}
+
+// act'(z): s (1 + z (1 - s)) with s = 1 / (1 + exp(-z)); Phi(z) + z phi(z).
+template <int ACT>
+__device__ __forceinline__ float gn_act_slope(float z) {
+    if constexpr (ACT == NORM_ACT_SILU) {
+        const float s = __fdividef(1.f, 1.f + __expf(-z));
+        return s * fmaf(z, 1.f - s, 1.f);
+    }
+    if constexpr (ACT == NORM_ACT_GELU)
+        return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f));
+    return 1.f;
+}
+
+// ------------------------------------------------------------ geometry
+// The CTA's tile: which sample, which accesses of a row, which groups, and
+// this thread's place in it.
+struct GnTile {
+    int64_t b;      // sample
+    int t;          // tile of the row
+    int c0, nc;     // first channel, channels
+    int g0, ng;     // first group touched, groups touched
+    int col, r;     // this thread's access column and row slot
+    bool on;        // this thread has an access
+};
+
+template <int VEC>
+__device__ __forceinline__ GnTile gn_tile(const GnArgs& a, int64_t unit) {
+    GnTile w;
+    w.b = unit / a.tiles;
+    w.t = static_cast<int>(unit - w.b * a.tiles);
+    const int k0 = w.t * a.tile;
+    const int nk = min(a.tile, a.ncols - k0);
+    w.c0 = k0 * VEC;
+    w.nc = nk * VEC;
+    w.g0 = w.c0 / a.D;
+    w.ng = (w.c0 + w.nc - 1) / a.D - w.g0 + 1;
+    w.r = static_cast<int>(threadIdx.x) / a.tile;
+    w.col = static_cast<int>(threadIdx.x) - w.r * a.tile;
+    w.on = w.r < a.par && w.col < nk;
+    return w;
+}
+
+// Rows [first, first + n) of chunk k when every chunk has `per` rows.
+__device__ __forceinline__ int64_t gn_chunk_len(int64_t S, int64_t per, int64_t k) {
+    const int64_t left = S - k * per;
+    return left < 0 ? 0 : left < per ? left : per;
+}
+
+// Rows that row slot r visits of `rows` rows walked `par` at a time.
+__device__ __forceinline__ int gn_visits(int64_t rows, int r, int par) {
+    return r < rows ? static_cast<int>((rows - r - 1) / par) + 1 : 0;
+}
+
+// A row of distributed shared memory: float2 at index i of cluster peer
+// `rank`'s copy of `p`.
+__device__ __forceinline__ float2 gn_peer(const float2* p, int i, uint32_t rank) {
+    float2 v;
+    const uint32_t at = peer_smem_addr(p + i, rank);
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+// ------------------------------------------------------------ launch
+// A kernel on `grid` CTAs in clusters of `cluster`, with programmatic stream
+// serialization like every kernel of the library. The dynamic shared memory
+// of these kernels stays below 48 KB (the plan check sees to it).
+inline cudaError_t gn_launch(const void* fn, int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                             const GnArgs& a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    void* args[] = {const_cast<GnArgs*>(&a)};
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace libnorm
