@@ -114,9 +114,11 @@ norm_status derive(const gn_plan& p, const Shape& s, GnArgs* a) {
     a->tiles = static_cast<int32_t>(ceil_div(ncols, a->tile));
     a->par = p.threads / a->tile;
     a->cluster = p.cluster;
-    const int units = one_group(s, p.vec_elems) && !s.bwd ? a->tile : a->tile * p.vec_elems;
+    a->segs = one_group(s, p.vec_elems) ? 1
+                                        : static_cast<int32_t>(std::min<int64_t>(p.vec_elems, (p.vec_elems - 2 + s.D) / s.D + 1));
+    const int units = a->tile * (s.bwd ? p.vec_elems : a->segs);
     const int64_t groups = libnorm::gn_tile_groups(int64_t(a->tile) * p.vec_elems, s.D, false);
-    if (libnorm::gn_smem_bytes(a->par, units, static_cast<int>(groups)) > kMaxSmem) return NORM_ERR_PLAN;
+    if (libnorm::gn_smem_bytes(a->par, units, static_cast<int>(groups), p.threads) > kMaxSmem) return NORM_ERR_PLAN;
     if (p.path == GN_PATH_CHIP) {
         if (!whole || !is_pow2(p.per_thread) || p.per_thread > maxv) return NORM_ERR_PLAN;
         a->tpg = 1;

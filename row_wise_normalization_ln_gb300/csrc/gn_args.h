@@ -35,6 +35,7 @@ struct GnArgs {
     int32_t tile;          // accesses of a row per CTA
     int32_t tiles;         // tiles per row
     int32_t tpg;           // tiles a group may touch (1 when tiles are whole groups)
+    int32_t segs;          // groups an access may touch
     int32_t par;           // rows a CTA works on at once: threads / tile
     int32_t cluster;
     int32_t chunks;        // row chunks summed per sample and tile
@@ -45,11 +46,13 @@ struct GnArgs {
 };
 
 // Dynamic shared memory of a kernel, from its plan: the per-thread states
-// ([par][units]) and two arrays of group values. `units` is tile (accesses
-// within one group) or tile * vec_elems (accesses that span groups, and the
-// backward, whose column sums are per channel).
-inline int64_t gn_smem_bytes(int par, int units, int groups) {
-    return (int64_t(par) * units + 2 * int64_t(groups)) * 8;
+// ([par][units]); per group and warp that shares the group, a state and its
+// count (12 bytes, at most one per warp or per group); per group, two values.
+// `units`: states per row slot; tile * segs in the forward, tile * vec_elems
+// in the backward, whose column sums are per channel.
+inline int64_t gn_smem_bytes(int par, int units, int groups, int threads) {
+    const int64_t shared = groups > threads / 32 ? groups : threads / 32;
+    return int64_t(par) * units * 8 + shared * 12 + int64_t(groups) * 12 + 16;
 }
 
 // Groups a tile of `channels` channels can touch.

@@ -33,13 +33,21 @@ struct GnBwdCh {
         const auto rb = X::load(static_cast<const T*>(a.beta) + c);
         const float* mean = a.mean + b * a.G;
         const float* rstd = a.rstd + b * a.G;
+        GnWalk k(c, a.D);
+        float2 m = f2_splat(mean[k.g]), r = f2_splat(rstd[k.g]);
 #pragma unroll
         for (int i = 0; i < X::H; ++i) {
-            const int ga = (c + (ONE ? 0 : 2 * i)) / a.D;
-            const int gb = ONE || VEC == 1 ? ga : (c + 2 * i + 1) / a.D;
-            const float2 g = X::get(rg, i);
-            if (i < HG) mu[i] = make_float2(mean[ga], mean[gb]);
-            A[i] = make_float2(rstd[ga] * g.x, rstd[gb] * g.y);
+            if constexpr (!ONE) {
+                m.x = mean[k.g];
+                r.x = rstd[k.g];
+                k.next();
+                m.y = mean[min(k.g, a.G - 1)];
+                r.y = rstd[min(k.g, a.G - 1)];
+                k.next();
+                k.g = min(k.g, a.G - 1);
+            }
+            if (i < HG) mu[i] = m;
+            A[i] = __fmul2_rn(r, X::get(rg, i));
             be[i] = X::get(rb, i);
         }
     }
@@ -50,7 +58,7 @@ struct GnBwdCh {
         const float2 v = X::get(dy, i);
         if constexpr (ACT == NORM_ACT_NONE) return v;
         const float2 z = __ffma2_rn(d, A[i], be[i]);
-        return __fmul2_rn(v, make_float2(gn_act_slope<ACT>(z.x), gn_act_slope<ACT>(z.y)));
+        return __fmul2_rn(v, gn_act_slope2<ACT>(z));
     }
 };
 
@@ -63,10 +71,16 @@ struct GnBwdOut {
 
     template <class Fin>
     __device__ __forceinline__ void init(const GnArgs& a, int c, Fin fin) {
+        GnWalk k(c, a.D);
 #pragma unroll
         for (int i = 0; i < HG; ++i) {
-            const float2 fa = fin((c + 2 * i) / a.D);
-            const float2 fb = ONE || VEC == 1 ? fa : fin((c + 2 * i + 1) / a.D);
+            const float2 fa = fin(k.g);
+            float2 fb = fa;
+            if constexpr (!ONE) {
+                k.next();
+                fb = fin(k.g);
+                k.next();
+            }
             u[i] = make_float2(fa.x, fb.x);
             v[i] = make_float2(fa.y, fb.y);
         }
@@ -86,33 +100,74 @@ struct GnBwdOut {
     }
 };
 
-// The CTA's column sums from its threads' (st[r * stride + channel]), left in
-// row 0 of st, and the groups' gamma-weighted sums of them in gs. Every
-// thread of the CTA calls it, after a barrier.
-template <class T>
+// A thread's column sums (S1, S2) into its row slot's states. The state of a
+// tile's channel is at gn_at(channel): the channels of an access lie `tile`
+// states apart, so that the lanes of a warp write side by side.
+template <int VEC>
+__device__ __forceinline__ int gn_at(int ch, int tile) {
+    return VEC == 1 ? ch : (ch % VEC) * tile + ch / VEC;
+}
+template <int VEC>
+__device__ __forceinline__ void gn_bwd_put(float2* st, int tile, int col, const float2* s1, const float2* s2) {
+#pragma unroll
+    for (int i = 0; i < (VEC + 1) / 2; ++i) {
+        st[2 * i * tile + col] = make_float2(s1[i].x, s2[i].x);
+        if (VEC > 1) st[(2 * i + 1) * tile + col] = make_float2(s1[i].y, s2[i].y);
+    }
+}
+
+// The CTA's column sums from its row slots' states (st[r * stride + i]), left
+// in row 0 of st, and the groups' gamma-weighted sums of them in gs. Every
+// thread of the CTA calls it, after a barrier. Order of the additions: fixed
+// by the CTA's shape.
+template <class T, int VEC>
 __device__ __forceinline__ void gn_bwd_merge_threads(const GnArgs& a, const GnTile& w, float2* st, int stride,
                                                      float2* gs) {
-    for (int ch = threadIdx.x; ch < w.nc; ch += blockDim.x) {
-        float2 t = st[ch];
-        for (int r = 1; r < a.par; ++r) t = __fadd2_rn(t, st[r * stride + ch]);
-        st[ch] = t;
+    // `deep` threads per state add every deep-th row slot, then one adds theirs
+    const int deep = min(a.par, max(1, static_cast<int>(blockDim.x) / stride));
+    if (deep > 1) {
+        const int d = static_cast<int>(threadIdx.x) / stride, i = static_cast<int>(threadIdx.x) - d * stride;
+        if (d < deep) {
+            float2 t = st[d * stride + i];
+#pragma unroll 4
+            for (int r = d + deep; r < a.par; r += deep) t = __fadd2_rn(t, st[r * stride + i]);
+            st[d * stride + i] = t;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    const int lane = threadIdx.x & 31;
+    const int left = deep > 1 ? deep : a.par;
+    if (left > 1) {
+        for (int i = threadIdx.x; i < stride; i += blockDim.x) {
+            float2 t = st[i];
+#pragma unroll 4
+            for (int r = 1; r < left; ++r) t = __fadd2_rn(t, st[r * stride + i]);
+            st[i] = t;
+        }
+        __syncthreads();
+    }
     const T* gamma = static_cast<const T*>(a.gamma) + w.c0;
-    for (int g = threadIdx.x >> 5; g < w.ng; g += blockDim.x >> 5) {
-        const int lo = max((w.g0 + g) * a.D - w.c0, 0);
-        const int hi = min((w.g0 + g + 1) * a.D - w.c0, w.nc);
+    int lanes = 32;
+    while (lanes > 1 && lanes * w.ng > static_cast<int>(blockDim.x)) lanes >>= 1;
+    const int lane = threadIdx.x & (lanes - 1);
+    const int rounds = (w.ng * lanes + blockDim.x - 1) / blockDim.x;
+    for (int it = 0; it < rounds; ++it) {
+        const int g = (static_cast<int>(threadIdx.x) + it * static_cast<int>(blockDim.x)) / lanes;
         float2 t = make_float2(0.f, 0.f);
-        for (int ch = lo + lane; ch < hi; ch += 32) t = __ffma2_rn(f2_splat(gn_elem(gamma + ch)), st[ch], t);
-        t.x = group_sum(t.x, 32);
-        t.y = group_sum(t.y, 32);
-        if (lane == 0) gs[g] = t;
+        if (g < w.ng) {
+            const int lo = max((w.g0 + g) * a.D - w.c0, 0);
+            const int hi = min((w.g0 + g + 1) * a.D - w.c0, w.nc);
+            for (int ch = lo + lane; ch < hi; ch += lanes)
+                t = __ffma2_rn(f2_splat(gn_elem(gamma + ch)), st[gn_at<VEC>(ch, a.tile)], t);
+        }
+        t.x = group_sum(t.x, lanes);
+        t.y = group_sum(t.y, lanes);
+        if (g < w.ng && lane == 0) gs[g] = t;
     }
 }
 
 // The cluster's column sums, channels shared out over its CTAs, into partial
 // row `row` of the column gradients (dgamma = rstd S2, dbeta = S1).
+template <int VEC>
 __device__ __forceinline__ void gn_bwd_write_cols(const GnArgs& a, const GnTile& w, const float2* st, int rank,
                                                   int cs, int64_t row) {
     const int per = (w.nc + cs - 1) / cs;
@@ -120,10 +175,10 @@ __device__ __forceinline__ void gn_bwd_write_cols(const GnArgs& a, const GnTile&
     for (int ch = rank * per + static_cast<int>(threadIdx.x); ch < hi; ch += blockDim.x) {
         float2 t;
         if (cs > 1) {
-            t = gn_peer(st, ch, 0);
-            for (int k = 1; k < cs; ++k) t = __fadd2_rn(t, gn_peer(st, ch, k));
+            t = gn_peer(st, gn_at<VEC>(ch, a.tile), 0);
+            for (int k = 1; k < cs; ++k) t = __fadd2_rn(t, gn_peer(st, gn_at<VEC>(ch, a.tile), k));
         } else {
-            t = st[ch];
+            t = st[gn_at<VEC>(ch, a.tile)];
         }
         const int c = w.c0 + ch;
         a.colg[row * a.col_pitch + c] = t.y * a.rstd[w.b * a.G + c / a.D];
@@ -155,7 +210,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_chip(const GnArgs a) {
     const int64_t row0 = int64_t(rank) * a.chunk_rows;
     const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, rank));
     const int c = w.c0 + w.col * VEC;
-    const int visits = w.on ? gn_visits(rows, w.r, a.par) : 0;
+    const int visits = w.on ? GnVisits(rows, a.par).of(w.r) : 0;
     const T* xp = static_cast<const T*>(a.x) + w.b * a.xb + (row0 + w.r) * a.xr + c;
     const T* dyp = static_cast<const T*>(a.dy) + w.b * a.dyb + (row0 + w.r) * a.dyr + c;
     typename X::Raw rx[V], rdy[V];
@@ -182,15 +237,10 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_chip(const GnArgs a) {
                     s2[i] = __ffma2_rn(dz, d, s2[i]);
                 }
             }
-        float2* p = st + w.r * stride + w.col * VEC;
-#pragma unroll
-        for (int i = 0; i < X::H; ++i) {
-            p[2 * i] = make_float2(s1[i].x, s2[i].x);
-            if (VEC > 1) p[2 * i + 1] = make_float2(s1[i].y, s2[i].y);
-        }
+        gn_bwd_put<VEC>(st + w.r * stride, a.tile, w.col, s1, s2);
     }
     __syncthreads();
-    gn_bwd_merge_threads<T>(a, w, st, stride, gs);
+    gn_bwd_merge_threads<T, VEC>(a, w, st, stride, gs);
     if (cs > 1)
         cluster_barrier();
     else
@@ -205,12 +255,12 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_chip(const GnArgs a) {
         }
         fin[g] = gn_bwd_fin(a, t, w.b * a.G + w.g0 + g);
     }
-    gn_bwd_write_cols(a, w, st, rank, cs, w.b);
+    gn_bwd_write_cols<VEC>(a, w, st, rank, cs, w.b);
     __syncthreads();
     if (cs > 1) cluster_arrive();  // this CTA has read its peers' sums
     if (w.on) {
         GnBwdOut<T, VEC, ONE> out;
-        out.init(a, c, [&](int g) { return fin[g - w.g0]; });
+        out.init(a, c, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
         T* yp = static_cast<T*>(a.y) + w.b * a.yb + (row0 + w.r) * a.yr + c;
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -235,10 +285,10 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_sums(const GnArgs a) {
     float2* st = sm;
     float2* gs = st + a.par * stride;
 
-    const int64_t rows = gn_chunk_len(a.S, a.chunk_rows, k);
+    const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, k));
     const int c = w.c0 + w.col * VEC;
     if (w.on) {
-        const int visits = gn_visits(rows, w.r, a.par);
+        const int visits = GnVisits(rows, a.par).of(w.r);
         const int64_t row = k * a.chunk_rows + w.r;
         const T* xp = static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c;
         const T* dyp = static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c;
@@ -282,15 +332,10 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_sums(const GnArgs a) {
                 t2[i] = __fadd2_rn(t2[i], s2[i]);
             }
         }
-        float2* p = st + w.r * stride + w.col * VEC;
-#pragma unroll
-        for (int i = 0; i < X::H; ++i) {
-            p[2 * i] = make_float2(t1[i].x, t2[i].x);
-            if (VEC > 1) p[2 * i + 1] = make_float2(t1[i].y, t2[i].y);
-        }
+        gn_bwd_put<VEC>(st + w.r * stride, a.tile, w.col, t1, t2);
     }
     __syncthreads();
-    gn_bwd_merge_threads<T>(a, w, st, stride, gs);
+    gn_bwd_merge_threads<T, VEC>(a, w, st, stride, gs);
     if (cs > 1)
         cluster_barrier();
     else
@@ -305,10 +350,10 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_sums(const GnArgs a) {
             t = gs[g];
         }
         const int gg = w.g0 + g;
-        const int ti = w.t - static_cast<int>((int64_t(gg) * a.D / VEC) / a.tile);
+        const int ti = a.tpg == 1 ? 0 : w.t - (gg * a.D / VEC) / a.tile;
         a.part[((w.b * a.G + gg) * a.tpg + ti) * parts + p0] = t;
     }
-    gn_bwd_write_cols(a, w, st, rank, cs, w.b * parts + p0);
+    gn_bwd_write_cols<VEC>(a, w, st, rank, cs, w.b * parts + p0);
     if (cs > 1) cluster_barrier();  // no CTA leaves while a peer reads its sums
 }
 
@@ -325,28 +370,32 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_apply(const GnArgs a) {
     const int k = static_cast<int>(id - unit * a.out_chunks);
     const GnTile w = gn_tile<VEC>(a, unit);
     const int parts = a.chunks / a.cluster;
-    const int lane = threadIdx.x & 31;
-    for (int g = threadIdx.x >> 5; g < w.ng; g += blockDim.x >> 5) {
-        const int gg = w.g0 + g;
+    int lanes = 32;
+    while (lanes > 1 && lanes * w.ng > static_cast<int>(blockDim.x)) lanes >>= 1;
+    const int lane = threadIdx.x & (lanes - 1);
+    const int rounds = (w.ng * lanes + blockDim.x - 1) / blockDim.x;
+    for (int it = 0; it < rounds; ++it) {
+        const int g = (static_cast<int>(threadIdx.x) + it * static_cast<int>(blockDim.x)) / lanes;
+        const int gg = w.g0 + (g < w.ng ? g : 0);
         const int64_t bg = w.b * a.G + gg;
-        const int t0 = static_cast<int>((int64_t(gg) * a.D / VEC) / a.tile);
-        const int t1 = static_cast<int>(((int64_t(gg) + 1) * a.D - 1) / VEC / a.tile);
+        const int touched = a.tpg == 1 ? 1 : ((gg + 1) * a.D - 1) / VEC / a.tile - gg * a.D / VEC / a.tile + 1;
         const float2* src = a.part + bg * a.tpg * parts;
         float2 t = make_float2(0.f, 0.f);
-        for (int i = lane; i < (t1 - t0 + 1) * parts; i += 32) t = __fadd2_rn(t, src[i]);
-        t.x = group_sum(t.x, 32);
-        t.y = group_sum(t.y, 32);
-        if (lane == 0) fin[g] = gn_bwd_fin(a, t, bg);
+        if (g < w.ng)
+#pragma unroll 4
+            for (int i = lane; i < touched * parts; i += lanes) t = __fadd2_rn(t, src[i]);
+        t.x = group_sum(t.x, lanes);
+        t.y = group_sum(t.y, lanes);
+        if (g < w.ng && lane == 0) fin[g] = gn_bwd_fin(a, t, bg);
     }
     __syncthreads();
     if (!w.on) return;
-    const int64_t rows = gn_chunk_len(a.S, a.out_rows, k);
-    const int visits = gn_visits(rows, w.r, a.par);
+    const int visits = GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a.par).of(w.r);
     const int c = w.c0 + w.col * VEC;
     GnBwdCh<T, VEC, ONE, ACT> ch;
     ch.init(a, w.b, c);
     GnBwdOut<T, VEC, ONE> out;
-    out.init(a, c, [&](int g) { return fin[g - w.g0]; });
+    out.init(a, c, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
     const int64_t row = k * a.out_rows + w.r;
     const T* xp = static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c;
     const T* dyp = static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c;
@@ -375,7 +424,7 @@ cudaError_t gn_launch_bwd(const gn_plan& p, const GnArgs& a, int64_t B, cudaStre
     const int64_t units = B * a.tiles;
     const int channels = a.tile * VEC;
     const int groups = static_cast<int>(gn_tile_groups(channels, a.D, false));
-    const size_t smem = static_cast<size_t>(gn_smem_bytes(a.par, channels, groups));
+    const size_t smem = static_cast<size_t>(gn_smem_bytes(a.par, channels, groups, p.threads));
     if (p.path == GN_PATH_CHIP) {
         const void* k = nullptr;
         switch (p.per_thread) {
@@ -390,7 +439,7 @@ cudaError_t gn_launch_bwd(const gn_plan& p, const GnArgs& a, int64_t B, cudaStre
                                     p.threads, smem, a.cluster, s, a);
     if (e != cudaSuccess) return e;
     return gn_launch(reinterpret_cast<const void*>(gn_bwd_apply<T, VEC, ONE, ACT>), units * a.out_chunks, p.threads,
-                     static_cast<size_t>(gn_smem_bytes(0, 0, groups)), 1, s, a);
+                     static_cast<size_t>(gn_smem_bytes(0, 0, groups, 0)), 1, s, a);
 }
 
 template <class T, int VEC, bool ONE>

@@ -18,59 +18,177 @@
 
 namespace libnorm {
 
-// Merges the CTA's thread states st[r * stride + u] (mean, M2 of
-// visits(r) * WIDTH values each) into the groups' states gs[g - g0]; one warp
-// per group. Every thread of the CTA calls it, after a barrier.
-template <int WIDTH>
-__device__ __forceinline__ void gn_merge_threads(const GnArgs& a, const GnTile& w, const float2* st, int stride,
-                                                 int64_t rows, float2* gs) {
-    const int lane = threadIdx.x & 31;
-    for (int g = threadIdx.x >> 5; g < w.ng; g += blockDim.x >> 5) {
-        const int lo = max((w.g0 + g) * a.D - w.c0, 0) / WIDTH;
-        const int hi = min((w.g0 + g + 1) * a.D - w.c0, w.nc) / WIDTH;
-        const int n = hi - lo;
-        float s = 0.f;
-        for (int i = lane; i < n * a.par; i += 32) {
-            const int r = i / n;
-            s = fmaf(static_cast<float>(gn_visits(rows, r, a.par)), st[r * stride + lo + (i - r * n)].x, s);
-        }
-        const float count = static_cast<float>(rows) * static_cast<float>(n);
-        const float mean = rows > 0 ? group_sum(s, 32) / count : 0.f;
-        float q = 0.f;
-        for (int i = lane; i < n * a.par; i += 32) {
-            const int r = i / n;
-            const int v = gn_visits(rows, r, a.par);
-            if (v > 0) {
-                const float2 e = st[r * stride + lo + (i - r * n)];
-                const float d = e.x - mean;
-                q += fmaf(static_cast<float>(v * WIDTH) * d, d, e.y);
-            }
-        }
-        q = group_sum(q, 32);
-        if (lane == 0) gs[g] = make_float2(mean, q);
+// How a CTA's threads share its groups in the merges: 2^k lanes per group
+// while there are more groups than warps, otherwise `wpg` whole warps.
+struct GnShare {
+    int lanes, wpg;
+    __device__ __forceinline__ explicit GnShare(int ng) {
+        const int warps = blockDim.x >> 5;
+        wpg = ng >= warps ? 1 : warps / ng;
+        lanes = 32;
+        while (lanes > 1 && lanes * ng > static_cast<int>(blockDim.x)) lanes >>= 1;
     }
+};
+
+// Collapses the per-channel states (m, m2 of `visits` values each) of an
+// access to one state per group it touches: (mean, M2) of visits * channels
+// values, in this thread's slots st[0 .. segs).
+template <int VEC>
+__device__ __forceinline__ void gn_collapse(const float2* m, const float2* m2, float visits, int c, int D, float2* st) {
+    constexpr int H = (VEC + 1) / 2;
+    GnWalk k(c, D);
+    int seg = 0, first = 0;
+    float s = 0.f;
+    // the channels j .. of one group end where the walk steps to the next
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        s += (j & 1) ? m[j / 2].y : m[j / 2].x;
+        const int g = k.g;
+        k.next();
+        if (j == VEC - 1 || k.g != g) {
+            const float mean = __fdividef(s, static_cast<float>(j + 1 - first));
+            float q = 0.f;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float2 d = f2_sub(m[i], f2_splat(mean));
+                const float2 e = __ffma2_rn(__fmul2_rn(d, f2_splat(visits)), d, m2[i]);
+                if (2 * i >= first && 2 * i <= j) q += e.x;
+                if (2 * i + 1 >= first && 2 * i + 1 <= j) q += e.y;
+            }
+            st[seg++] = make_float2(mean, q);
+            s = 0.f;
+            first = j + 1;
+        }
+    }
+}
+
+// Merges the CTA's thread states into states gs[g * wpg + part] = (mean, M2)
+// of counts gn[...]. The states of row slot r and access column u start at
+// st[(r * tile + u) * segs], one per group the access touches. Lanes side by
+// side over the group's accesses, then row slots. Every thread of the CTA
+// calls it, after a barrier.
+template <int VEC>
+__device__ __forceinline__ void gn_merge_threads(const GnArgs& a, const GnTile& w, const float2* st, int segs,
+                                                 const GnVisits& vis, const GnShare& sh, float2* gs, float* gn) {
+    const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
+    const int jobs = w.ng * sh.wpg, rounds = (jobs * lanes + blockDim.x - 1) / blockDim.x;
+    for (int it = 0; it < rounds; ++it) {
+        // (every lane of a warp takes part in the butterflies, with or without a job)
+        const int j = (static_cast<int>(threadIdx.x) + it * static_cast<int>(blockDim.x)) / lanes;
+        const bool on = j < jobs;
+        const int g = on ? j / sh.wpg : 0, part = on ? j - g * sh.wpg : 0;
+        const int lo = max((w.g0 + g) * a.D, w.c0), hi = min((w.g0 + g + 1) * a.D, w.c0 + w.nc);
+        const int u0 = (lo - w.c0) / VEC, n = (hi - 1 - w.c0) / VEC - u0 + 1;
+        const int across = min(n, lanes), deep = lanes / across;
+        const int r0 = lane / across, uf = lane - r0 * across;
+        float s = 0.f, c = 0.f, q = 0.f;
+        auto walk = [&](auto f) {
+            if (on && r0 < deep)
+                for (int u = uf; u < n; u += lanes) {
+                    const int ch = w.c0 + (u0 + u) * VEC;  // the access's first channel
+                    const int len = min(hi, ch + VEC) - max(lo, ch);
+                    const int seg = segs == 1 ? 0 : w.g0 + g - ch / a.D;
+                    for (int r = part + sh.wpg * r0; r < a.par; r += sh.wpg * deep)
+                        f(static_cast<float>(vis.of(r) * len), st[(r * a.tile + u0 + u) * segs + seg]);
+                }
+        };
+        walk([&](float v, float2 e) {
+            s = fmaf(v, v > 0.f ? e.x : 0.f, s);
+            c += v;
+        });
+        c = group_sum(c, lanes);
+        s = group_sum(s, lanes);
+        const float mean = c > 0.f ? __fdividef(s, c) : 0.f;
+        walk([&](float v, float2 e) {
+            const float d = e.x - mean;
+            if (v > 0.f) q += fmaf(v * d, d, e.y);
+        });
+        q = group_sum(q, lanes);
+        if (on && lane == 0) {
+            gs[j] = make_float2(mean, q);
+            gn[j] = c;
+        }
+    }
+}
+
+// The groups' states from their `wpg` states in each of the `cs` CTAs of the
+// cluster: calls done(group, mean, M2, count) once for each of the tile's
+// groups g = first, first + every, ... The lanes of a group take one state
+// each where there are enough.
+template <class F>
+__device__ __forceinline__ void gn_merge_cluster(const float2* gs, const float* gn, int ng, int wpg, int cs, int first,
+                                                 int every, F done) {
+    const int n = cs * wpg;
+    if (n == 1) {
+        for (int g = first + every * static_cast<int>(threadIdx.x); g < ng; g += every * blockDim.x)
+            done(g, gs[g].x, gs[g].y, gn[g]);
+        return;
+    }
+    int lanes = 1;
+    while (lanes < 32 && lanes < n) lanes <<= 1;
+    const int lane = threadIdx.x & (lanes - 1);
+    const int jobs = (ng - first + every - 1) / every;
+    const int rounds = (jobs * lanes + blockDim.x - 1) / blockDim.x;
+    for (int it = 0; it < rounds; ++it) {
+        const int j = (static_cast<int>(threadIdx.x) + it * static_cast<int>(blockDim.x)) / lanes;
+        const int g = first + every * j;
+        const bool on = j < jobs;
+        float c = 0.f, s = 0.f, q = 0.f;
+        auto walk = [&](auto f) {
+            if (on)
+                for (int i = lane; i < n; i += lanes) {
+                    const int k = wpg == 1 ? i : i / wpg, at = g * wpg + (i - k * wpg);
+                    if (cs > 1)
+                        f(ld_peer_f32(peer_smem_addr(gn + at, k)), gn_peer(gs, at, k));
+                    else
+                        f(gn[at], gs[at]);
+                }
+        };
+        walk([&](float v, float2 e) {
+            s = fmaf(v, e.x, s);
+            c += v;
+        });
+        c = group_sum(c, lanes);
+        s = group_sum(s, lanes);
+        const float mean = c > 0.f ? __fdividef(s, c) : 0.f;
+        walk([&](float v, float2 e) {
+            const float d = e.x - mean;
+            if (v > 0.f) q += fmaf(v * d, d, e.y);
+        });
+        q = group_sum(q, lanes);
+        if (on && lane == 0) done(g, mean, q, c);
+    }
+}
+
+// The square root and the division are the correctly rounded ones: there is
+// one per group, and rsqrtf's two ulps would scale every output.
+__device__ __forceinline__ float gn_rstd(float m2, float count, float eps) {
+    return __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(m2, count) + eps));
 }
 
 // y = act(d * s + o) per channel: s = rstd * gamma, o = beta - mu * s, with
 // mu the group's mean relative to the shift K and d = x - K.
-template <class T, int VEC, int ACT>
+template <class T, int VEC, bool ONE, int ACT>
 struct GnOut {
     using X = GnVec<T, VEC>;
-    float2 K[X::H], s[X::H], o[X::H];
+    static constexpr int HG = ONE ? 1 : X::H;
+    float2 K[HG], s[X::H], o[X::H];
 
-    // fin(g): float2 (mu, rstd) of group g; shift(g): K of group g.
-    template <class Fin, class Shift>
-    __device__ __forceinline__ void init(const GnArgs& a, int c, Fin fin, Shift shift) {
-        const T* gamma = static_cast<const T*>(a.gamma) + c;
-        const T* beta = static_cast<const T*>(a.beta) + c;
-        const auto rg = X::load(gamma), rb = X::load(beta);
+    // fin(g): float2 (mu, rstd) of group g.
+    template <class Fin>
+    __device__ __forceinline__ void init(const typename X::Raw& rg, const typename X::Raw& rb, int c, int D, Fin fin) {
+        GnWalk k(c, D);
+        float2 fa = fin(k.g);
 #pragma unroll
         for (int i = 0; i < X::H; ++i) {
-            const int ga = (c + 2 * i) / a.D;
-            const int gb = VEC == 1 ? ga : (c + 2 * i + 1) / a.D;
-            const float2 fa = fin(ga), fb = fin(gb);
+            float2 fb = fa;
+            if constexpr (!ONE) {
+                if (i > 0) fa = fin(k.g);
+                k.next();
+                fb = fin(k.g);
+                k.next();
+            }
             const float2 gm = X::get(rg, i), be = X::get(rb, i);
-            K[i] = make_float2(shift(ga), shift(gb));
             s[i] = make_float2(fa.y * gm.x, fb.y * gm.y);
             o[i] = make_float2(fmaf(-fa.x, s[i].x, be.x), fmaf(-fb.x, s[i].y, be.y));
         }
@@ -79,137 +197,123 @@ struct GnOut {
         typename X::Raw out = X::zero();
 #pragma unroll
         for (int i = 0; i < X::H; ++i) {
-            const float2 z = __ffma2_rn(f2_sub(X::get(r, i), K[i]), s[i], o[i]);
-            X::set(out, i, make_float2(gn_act<ACT>(z.x), gn_act<ACT>(z.y)));
+            const float2 z = __ffma2_rn(f2_sub(X::get(r, i), K[ONE ? 0 : i]), s[i], o[i]);
+            X::set(out, i, gn_act2<ACT>(z));
         }
         return out;
     }
 };
 
+// A value per channel of an access from one per group: v(g).
+template <class T, int VEC, bool ONE, class F>
+__device__ __forceinline__ void gn_per_group(float2* K, int c, int D, F v) {
+    using X = GnVec<T, VEC>;
+    GnWalk k(c, D);
+    if constexpr (ONE) {
+        K[0] = f2_splat(v(k.g));
+        if (VEC == 1) K[0].y = 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < X::H; ++i) {
+            K[i].x = v(k.g);
+            k.next();
+            K[i].y = v(k.g);
+            k.next();
+        }
+    }
+}
+
 template <class T, int VEC, bool ONE, int ACT, int V>
 __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
     using X = GnVec<T, VEC>;
+    constexpr int HG = ONE ? 1 : X::H;
     extern __shared__ float2 sm[];
     grid_release();
-    grid_wait();
     const int cs = a.cluster;
     const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
     const GnTile w = gn_tile<VEC>(a, blockIdx.x / cs);
-    const int stride = ONE ? a.tile : a.tile * VEC;
+    const int segs = ONE ? 1 : a.segs;
+    const GnShare sh(w.ng);
     float2* st = sm;
-    float2* gs = st + a.par * stride;
-    const int gcap = ONE ? (a.tile * VEC) / a.D : (a.tile * VEC - 1 + a.D - 1) / a.D + 1;
-    float2* fin = gs + gcap;
+    float2* gs = st + a.par * a.tile * segs;
+    float2* fin = gs + w.ng * sh.wpg;
+    float* gn = reinterpret_cast<float*>(fin + w.ng);
 
     const int64_t row0 = int64_t(rank) * a.chunk_rows;
     const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, rank));
+    const GnVisits vis(rows, a.par);
+    const int visits = w.on ? vis.of(w.r) : 0;
     const int c = w.c0 + w.col * VEC;
     const T* xs = static_cast<const T*>(a.x) + w.b * a.xb;
     const T* xp = xs + (row0 + w.r) * a.xr + c;
-    typename X::Raw raw[V];
+    grid_wait();
+    typename X::Raw raw[V], rg, rb;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        if (w.on && w.r + v * a.par < rows) raw[v] = X::load(xp + int64_t(v) * a.par * a.xr);
-
+        if (v < visits) raw[v] = X::load(xp + int64_t(v) * a.par * a.xr);
     // the shift of a group: its first element in the sample's first row
-    float2 K[X::H];
-#pragma unroll
-    for (int i = 0; i < X::H; ++i) {
-        K[i] = make_float2(0.f, 0.f);
-        if (w.on) {
-            if (ONE && i > 0)
-                K[i] = K[0];
-            else {
-                const int ga = (c + 2 * i) / a.D;
-                K[i].x = gn_elem(xs + int64_t(ga) * a.D);
-                K[i].y = VEC == 1 ? 0.f : ONE ? K[i].x : gn_elem(xs + int64_t((c + 2 * i + 1) / a.D) * a.D);
-            }
-        }
-    }
-    const int visits = w.on ? gn_visits(rows, w.r, a.par) : 0;
-    float2 s[X::H], q[X::H];
-#pragma unroll
-    for (int i = 0; i < X::H; ++i) s[i] = q[i] = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (v < visits) {
-#pragma unroll
-            for (int i = 0; i < X::H; ++i) s[i] = __fadd2_rn(s[i], f2_sub(X::get(raw[v], i), K[i]));
-        }
-    const float inv = visits > 0 ? 1.f / static_cast<float>(visits) : 0.f;
-    if constexpr (ONE) {
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < X::H; ++i) t += f2_sum<VEC>(s[i]);
-        const float m = t * inv * (1.f / VEC);
-#pragma unroll
-        for (int i = 0; i < X::H; ++i) s[i] = f2_splat(m);
-    } else {
-#pragma unroll
-        for (int i = 0; i < X::H; ++i) s[i] = __fmul2_rn(s[i], f2_splat(inv));
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (v < visits) {
-#pragma unroll
-            for (int i = 0; i < X::H; ++i) {
-                const float2 d = f2_sub(f2_sub(X::get(raw[v], i), K[i]), s[i]);
-                q[i] = __ffma2_rn(d, d, q[i]);
-            }
-        }
+    GnOut<T, VEC, ONE, ACT> out;
     if (w.on) {
-        if constexpr (ONE) {
-            float t = 0.f;
+        gn_per_group<T, VEC, ONE>(out.K, c, a.D, [&](int g) { return gn_elem(xs + int64_t(g) * a.D); });
+        rg = X::load(static_cast<const T*>(a.gamma) + c);
+        rb = X::load(static_cast<const T*>(a.beta) + c);
+    }
+    // The thread's states by two passes over its registers. An access within
+    // one group has one state for its channels.
+    if (w.on) {
+        float2 s[HG], q[HG];
 #pragma unroll
-            for (int i = 0; i < X::H; ++i) t += f2_sum<VEC>(q[i]);
-            st[w.r * stride + w.col] = make_float2(s[0].x, t);
-        } else {
+        for (int i = 0; i < HG; ++i) s[i] = q[i] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < X::H; ++i) {
-                st[w.r * stride + w.col * VEC + 2 * i] = make_float2(s[i].x, q[i].x);
-                st[w.r * stride + w.col * VEC + 2 * i + 1] = make_float2(s[i].y, q[i].y);
+        for (int v = 0; v < V; ++v)
+            if (v < visits) {
+#pragma unroll
+                for (int i = 0; i < X::H; ++i) {
+                    const int j = ONE ? 0 : i;
+                    s[j] = __fadd2_rn(s[j], f2_sub(X::get(raw[v], i), out.K[j]));
+                }
             }
-        }
+        const float inv = visits > 0 ? 1.f / static_cast<float>(visits) : 0.f;
+        if constexpr (ONE)
+            s[0] = f2_splat(f2_sum<VEC>(s[0]) * inv * (1.f / VEC));
+        else
+#pragma unroll
+            for (int i = 0; i < HG; ++i) s[i] = __fmul2_rn(s[i], f2_splat(inv));
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < visits) {
+#pragma unroll
+                for (int i = 0; i < X::H; ++i) {
+                    const int j = ONE ? 0 : i;
+                    const float2 d = f2_sub(f2_sub(X::get(raw[v], i), out.K[j]), s[j]);
+                    q[j] = __ffma2_rn(d, d, q[j]);
+                }
+            }
+        float2* mine = st + (w.r * a.tile + w.col) * segs;
+        if constexpr (ONE)
+            mine[0] = make_float2(s[0].x, f2_sum<VEC>(q[0]));
+        else
+            gn_collapse<VEC>(s, q, static_cast<float>(visits), c, a.D, mine);
     }
     __syncthreads();
-    gn_merge_threads<ONE ? VEC : 1>(a, w, st, stride, rows, gs);
+    gn_merge_threads<VEC>(a, w, st, segs, vis, sh, gs, gn);
     if (cs > 1)
         cluster_barrier();
     else
         __syncthreads();
-    const float count = static_cast<float>(a.S) * static_cast<float>(a.D);
-    for (int g = threadIdx.x; g < w.ng; g += blockDim.x) {
-        float mu, m2;
-        if (cs > 1) {
-            float t = 0.f;
-            for (int k = 0; k < cs; ++k)
-                t = fmaf(static_cast<float>(gn_chunk_len(a.S, a.chunk_rows, k)), gn_peer(gs, g, k).x, t);
-            mu = t / static_cast<float>(a.S);
-            m2 = 0.f;
-            for (int k = 0; k < cs; ++k) {
-                const float2 e = gn_peer(gs, g, k);
-                const float d = e.x - mu;
-                m2 += fmaf(static_cast<float>(gn_chunk_len(a.S, a.chunk_rows, k)) * static_cast<float>(a.D) * d, d, e.y);
-            }
-        } else {
-            mu = gs[g].x;
-            m2 = gs[g].y;
-        }
-        const float rstd = rsqrtf(m2 / count + a.eps);
+    gn_merge_cluster(gs, gn, w.ng, sh.wpg, cs, 0, 1, [&](int g, float mu, float m2, float count) {
+        const float rstd = gn_rstd(m2, count, a.eps);
         fin[g] = make_float2(mu, rstd);
         if (rank == 0) {
             const int64_t at = w.b * a.G + w.g0 + g;
             if (a.mean) a.mean[at] = gn_elem(xs + int64_t(w.g0 + g) * a.D) + mu;
             if (a.rstd) a.rstd[at] = rstd;
         }
-    }
+    });
     __syncthreads();
     if (cs > 1) cluster_arrive();  // this CTA has read its peers' states
     if (w.on) {
-        GnOut<T, VEC, ACT> out;
-        out.init(a, c, [&](int g) { return fin[g - w.g0]; }, [&](int) { return 0.f; });
-#pragma unroll
-        for (int i = 0; i < X::H; ++i) out.K[i] = K[i];
+        out.init(rg, rb, c, a.D, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
         T* yp = static_cast<T*>(a.y) + w.b * a.yb + (row0 + w.r) * a.yr + c;
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -223,202 +327,200 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
 // even where that shift lies far from the other rows.
 constexpr int kGnShiftRows = 128;
 
+// The pairwise merge: (n, m, m2) += (k, mb, b2).
+__device__ __forceinline__ void gn_pair_merge(float& m, float& m2, float mb, float b2, float n, float k) {
+    const float wb = k / (n + k), d = mb - m;
+    m = fmaf(d, wb, m);
+    m2 += fmaf(d * d, n * wb, b2);
+}
+
+// sum and sum of squares of d over k values -> (mean, M2); the subtraction
+// can round below zero, and NaN stays NaN.
+__device__ __forceinline__ float2 gn_mean_m2(float s, float q, float k) {
+    const float m = s / k, b2 = fmaf(-s, m, q);
+    return make_float2(m, b2 < 0.f ? 0.f : b2);
+}
+
 template <class T, int VEC, bool ONE>
-__global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_sums(const GnArgs a) {
+__global__ void __launch_bounds__(kGnMaxThreads, ONE ? 2 : 1) gn_fwd_sums(const GnArgs a) {
     using X = GnVec<T, VEC>;
-    constexpr int U = 4;
+    constexpr int HG = ONE ? 1 : X::H;
+    constexpr int U = 8;
     extern __shared__ float2 sm[];
     grid_release();
-    grid_wait();
     const int cs = a.cluster;
     const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int64_t unit = blockIdx.x / a.chunks;
     const int k = static_cast<int>(blockIdx.x - unit * a.chunks);
     const GnTile w = gn_tile<VEC>(a, unit);
-    const int stride = ONE ? a.tile : a.tile * VEC;
+    const int segs = ONE ? 1 : a.segs;
+    const GnShare sh(w.ng);
     float2* st = sm;
-    float2* gs = st + a.par * stride;
+    float2* gs = st + a.par * a.tile * segs;
+    float* gn = reinterpret_cast<float*>(gs + w.ng * sh.wpg);
 
-    const int64_t rows = gn_chunk_len(a.S, a.chunk_rows, k);
+    const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, k));
+    const GnVisits vis(rows, a.par);
     const int c = w.c0 + w.col * VEC;
     const T* xs = static_cast<const T*>(a.x) + w.b * a.xb;
-    const T* xp = xs + (k * a.chunk_rows + w.r) * a.xr + c;
-    const int visits = w.on ? gn_visits(rows, w.r, a.par) : 0;
-    const int64_t step = int64_t(a.par) * a.xr;
-
-    float2 K[X::H], s[X::H], q[X::H];  // of the rows since the last merge
-    float2 m[X::H], m2[X::H];          // merged: mean relative to the group's first element, M2
-    float2 G0[X::H];
+    grid_wait();
+    if (w.on) {
+        const int visits = vis.of(w.r);
+        const T* xp = xs + (k * a.chunk_rows + w.r) * a.xr + c;
+        const int64_t step = int64_t(a.par) * a.xr;
+        // Blocks of kGnShiftRows rows, shifted by the block's first value:
+        // per channel, or one for the channels of an access within a group.
+        float2 m[HG], m2[HG];
 #pragma unroll
-    for (int i = 0; i < X::H; ++i) {
-        s[i] = q[i] = m[i] = m2[i] = K[i] = G0[i] = make_float2(0.f, 0.f);
-        if (w.on) {
-            if (ONE && i > 0)
-                G0[i] = G0[0];
-            else {
-                G0[i].x = gn_elem(xs + int64_t((c + 2 * i) / a.D) * a.D);
-                G0[i].y = VEC == 1 ? 0.f : ONE ? G0[i].x : gn_elem(xs + int64_t((c + 2 * i + 1) / a.D) * a.D);
-            }
-        }
-    }
-    int merged = 0;
-    for (int v0 = 0; v0 < visits;) {
-        const int stop = min(visits, v0 + kGnShiftRows);
-        const int n = stop - v0;
-        {
-            const auto first = X::load(xp);
+        for (int i = 0; i < HG; ++i) m[i] = m2[i] = make_float2(0.f, 0.f);
+        for (int v0 = 0; v0 < visits;) {
+            const int first = v0, stop = min(visits, v0 + kGnShiftRows);
+            float2 K[HG], s[HG], q[HG];
 #pragma unroll
-            for (int i = 0; i < X::H; ++i) {
-                K[i] = X::get(first, i);
-                s[i] = q[i] = make_float2(0.f, 0.f);
-            }
-        }
-        for (; v0 < stop; v0 += U) {
-            typename X::Raw raw[U];
+            for (int i = 0; i < HG; ++i) s[i] = q[i] = make_float2(0.f, 0.f);
+            for (; v0 < stop; v0 += U) {
+                typename X::Raw raw[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (v0 + u < stop) raw[u] = X::load(xp + u * step);
+                for (int u = 0; u < U; ++u)
+                    if (v0 + u < stop) raw[u] = X::load(xp + u * step);
+                if (v0 == first) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (v0 + u < stop) {
-#pragma unroll
-                    for (int i = 0; i < X::H; ++i) {
-                        const float2 d = f2_sub(X::get(raw[u], i), K[i]);
-                        s[i] = __fadd2_rn(s[i], d);
-                        q[i] = __ffma2_rn(d, d, q[i]);
+                    for (int i = 0; i < HG; ++i) {
+                        K[i] = X::get(raw[0], i);
+                        if (ONE && VEC > 1) K[i].y = K[i].x;
                     }
                 }
-            xp += U * step;
-        }
-        v0 = stop;
-        // merge: this block's mean relative to its own shift is s / n
-        const float fn = static_cast<float>(n), inv = 1.f / fn;
-        const float tot = static_cast<float>(merged + n);
-        const float wb = fn / tot, wab = static_cast<float>(merged) * wb;
 #pragma unroll
-        for (int i = 0; i < X::H; ++i) {
-            const float2 d = __fmul2_rn(s[i], f2_splat(inv));
-            float2 b2 = make_float2(fmaf(-s[i].x, d.x, q[i].x), fmaf(-s[i].y, d.y, q[i].y));
-            b2.x = b2.x < 0.f ? 0.f : b2.x;  // (a NaN stays one)
-            b2.y = b2.y < 0.f ? 0.f : b2.y;
-            const float2 mb = __fadd2_rn(f2_sub(K[i], G0[i]), d);
-            const float2 e = f2_sub(mb, m[i]);
-            m[i] = __ffma2_rn(e, f2_splat(wb), m[i]);
-            m2[i] = __fadd2_rn(__ffma2_rn(__fmul2_rn(e, f2_splat(wab)), e, m2[i]), b2);
-        }
-        merged += n;
-    }
-    if (w.on) {
-        if constexpr (ONE) {
-            float t = 0.f, p = 0.f;
+                for (int u = 0; u < U; ++u)
+                    if (v0 + u < stop) {
 #pragma unroll
-            for (int i = 0; i < X::H; ++i) t += f2_sum<VEC>(m[i]);
-            const float mean = t * (1.f / VEC);
-#pragma unroll
-            for (int i = 0; i < X::H; ++i) {
-                const float2 e = f2_sub(m[i], f2_splat(mean));
-                p += f2_sum<VEC>(__ffma2_rn(__fmul2_rn(e, f2_splat(static_cast<float>(merged))), e, m2[i]));
+                        for (int i = 0; i < X::H; ++i) {
+                            const int j = ONE ? 0 : i;
+                            const float2 d = f2_sub(X::get(raw[u], i), K[j]);
+                            s[j] = __fadd2_rn(s[j], d);
+                            q[j] = __ffma2_rn(d, d, q[j]);
+                        }
+                    }
+                xp += U * step;
             }
-            st[w.r * stride + w.col] = make_float2(mean, p);
-        } else {
+            v0 = stop;
+            // into the running state, relative to the group's first element
+            const float n = static_cast<float>(first), kk = static_cast<float>(stop - first);
+            float2 G0[HG];
+            gn_per_group<T, VEC, ONE>(G0, c, a.D, [&](int g) { return gn_elem(xs + int64_t(g) * a.D); });
+            if constexpr (ONE) {
+                const float2 b = gn_mean_m2(f2_sum<VEC>(s[0]), f2_sum<VEC>(q[0]), kk * VEC);
+                gn_pair_merge(m[0].x, m2[0].x, (K[0].x - G0[0].x) + b.x, b.y, n * VEC, kk * VEC);
+            } else {
 #pragma unroll
-            for (int i = 0; i < X::H; ++i) {
-                st[w.r * stride + w.col * VEC + 2 * i] = make_float2(m[i].x, m2[i].x);
-                st[w.r * stride + w.col * VEC + 2 * i + 1] = make_float2(m[i].y, m2[i].y);
+                for (int i = 0; i < HG; ++i) {
+                    const float2 bx = gn_mean_m2(s[i].x, q[i].x, kk), by = gn_mean_m2(s[i].y, q[i].y, kk);
+                    gn_pair_merge(m[i].x, m2[i].x, (K[i].x - G0[i].x) + bx.x, bx.y, n, kk);
+                    gn_pair_merge(m[i].y, m2[i].y, (K[i].y - G0[i].y) + by.x, by.y, n, kk);
+                }
             }
         }
+        float2* mine = st + (w.r * a.tile + w.col) * segs;
+        if constexpr (ONE)
+            mine[0] = make_float2(m[0].x, m2[0].x);
+        else
+            gn_collapse<VEC>(m, m2, static_cast<float>(visits), c, a.D, mine);
     }
     __syncthreads();
-    gn_merge_threads<ONE ? VEC : 1>(a, w, st, stride, rows, gs);
+    gn_merge_threads<VEC>(a, w, st, segs, vis, sh, gs, gn);
     if (cs > 1)
         cluster_barrier();
     else
         __syncthreads();
     // the cluster's chunks, groups shared out over its CTAs
     const int p0 = k / cs, parts = a.chunks / cs;
-    for (int g = rank + cs * static_cast<int>(threadIdx.x); g < w.ng; g += cs * blockDim.x) {
+    gn_merge_cluster(gs, gn, w.ng, sh.wpg, cs, rank, cs, [&](int g, float mu, float m2, float) {
         const int gg = w.g0 + g;
-        float mu, p2;
-        if (cs > 1) {
-            float t = 0.f, n = 0.f;
-            for (int j = 0; j < cs; ++j) {
-                const float nj = static_cast<float>(gn_chunk_len(a.S, a.chunk_rows, int64_t(p0) * cs + j));
-                t = fmaf(nj, gn_peer(gs, g, j).x, t);
-                n += nj;
-            }
-            mu = n > 0.f ? t / n : 0.f;
-            const float width = static_cast<float>(min((gg + 1) * a.D, w.c0 + w.nc) - max(gg * a.D, w.c0));
-            p2 = 0.f;
-            for (int j = 0; j < cs; ++j) {
-                const float nj = static_cast<float>(gn_chunk_len(a.S, a.chunk_rows, int64_t(p0) * cs + j));
-                if (nj > 0.f) {
-                    const float2 e = gn_peer(gs, g, j);
-                    const float d = e.x - mu;
-                    p2 += fmaf(nj * width * d, d, e.y);
-                }
-            }
-        } else {
-            mu = gs[g].x;
-            p2 = gs[g].y;
-        }
         const int64_t bg = w.b * a.G + gg;
-        const int ti = w.t - static_cast<int>((int64_t(gg) * a.D / VEC) / a.tile);
-        a.part[(bg * a.tpg + ti) * parts + p0] = make_float2(mu, p2);
+        const int ti = a.tpg == 1 ? 0 : w.t - (gg * a.D / VEC) / a.tile;
+        a.part[(bg * a.tpg + ti) * parts + p0] = make_float2(mu, m2);
         if (p0 == 0 && ti == 0) a.shift[bg] = gn_elem(xs + int64_t(gg) * a.D);
-    }
+    });
     if (cs > 1) cluster_barrier();  // no CTA leaves while a peer reads its states
 }
 
-template <class T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_apply(const GnArgs a) {
+// The tiles a group touches, and how many of its channels lie in each.
+struct GnSpan {
+    int t0, t1;
+    int c0, c1;  // the group's channels
+    template <int VEC>
+    static __device__ __forceinline__ GnSpan of(const GnArgs& a, int g, int t) {
+        GnSpan s;
+        s.c0 = g * a.D;
+        s.c1 = s.c0 + a.D;
+        s.t0 = a.tpg == 1 ? t : s.c0 / VEC / a.tile;
+        s.t1 = a.tpg == 1 ? t : (s.c1 - 1) / VEC / a.tile;
+        return s;
+    }
+    __device__ __forceinline__ int width(int t, int tile_channels) const {
+        return min(c1, (t + 1) * tile_channels) - max(c0, t * tile_channels);
+    }
+};
+
+template <class T, int VEC, bool ONE, int ACT>
+__global__ void __launch_bounds__(kGnMaxThreads, 2) gn_fwd_apply(const GnArgs a) {
     using X = GnVec<T, VEC>;
     constexpr int U = 4;
     extern __shared__ float2 sm[];
     grid_release();
-    grid_wait();
-    float2* fin = sm;                                   // (mu, rstd) per group of the tile
-    float* shift = reinterpret_cast<float*>(sm + (a.tile * VEC - 1 + a.D - 1) / a.D + 1);
     // last chunks first: what the sums kernel read last is the likeliest in L2
     const int64_t id = int64_t(gridDim.x) - 1 - blockIdx.x;
     const int64_t unit = id / a.out_chunks;
     const int k = static_cast<int>(id - unit * a.out_chunks);
     const GnTile w = gn_tile<VEC>(a, unit);
+    float2* fin = sm;                                   // (mu, rstd) per group of the tile
+    float* shift = reinterpret_cast<float*>(sm + w.ng);
     const int parts = a.chunks / a.cluster;
     const int64_t part_rows = a.chunk_rows * a.cluster;
-    const int lane = threadIdx.x & 31;
-    for (int g = threadIdx.x >> 5; g < w.ng; g += blockDim.x >> 5) {
-        // every tile and merged chunk of the group, lanes side by side
-        const int gg = w.g0 + g;
+    const int c = w.c0 + w.col * VEC;
+    grid_wait();
+    typename X::Raw rg, rb;
+    if (w.on) {
+        rg = X::load(static_cast<const T*>(a.gamma) + c);
+        rb = X::load(static_cast<const T*>(a.beta) + c);
+    }
+    // The groups' states from every tile and merged chunk, lanes side by side
+    // over the chunks: all have part_rows rows up to the last that has any.
+    const int last = static_cast<int>((a.S - 1) / part_rows);
+    const float full = static_cast<float>(part_rows), rest = static_cast<float>(a.S - last * part_rows);
+    const float count = static_cast<float>(a.S) * static_cast<float>(a.D);
+    const GnShare sh(w.ng);
+    const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
+    const int rounds = (w.ng * lanes + blockDim.x - 1) / blockDim.x;
+    for (int it = 0; it < rounds; ++it) {
+        const int g = (static_cast<int>(threadIdx.x) + it * static_cast<int>(blockDim.x)) / lanes;
+        const bool on = g < w.ng;
+        const int gg = w.g0 + (on ? g : 0);
         const int64_t bg = w.b * a.G + gg;
-        const int t0 = static_cast<int>((int64_t(gg) * a.D / VEC) / a.tile);
-        const int t1 = static_cast<int>(((int64_t(gg) + 1) * a.D - 1) / VEC / a.tile);
-        const int n = (t1 - t0 + 1) * parts;
+        const GnSpan sp = GnSpan::of<VEC>(a, gg, w.t);
         const float2* src = a.part + bg * a.tpg * parts;
-        float s = 0.f;
-        for (int i = lane; i < n; i += 32) {
-            const int ti = i / parts, p = i - ti * parts;
-            const int lo = max(gg * a.D, (t0 + ti) * a.tile * VEC);
-            const int hi = min((gg + 1) * a.D, (t0 + ti + 1) * a.tile * VEC);
-            s = fmaf(static_cast<float>(gn_chunk_len(a.S, part_rows, p)) * static_cast<float>(hi - lo), src[i].x, s);
-        }
-        const float count = static_cast<float>(a.S) * static_cast<float>(a.D);
-        const float mu = group_sum(s, 32) / count;
-        float q = 0.f;
-        for (int i = lane; i < n; i += 32) {
-            const int ti = i / parts, p = i - ti * parts;
-            const int lo = max(gg * a.D, (t0 + ti) * a.tile * VEC);
-            const int hi = min((gg + 1) * a.D, (t0 + ti + 1) * a.tile * VEC);
-            const float2 e = src[i];
+        const float K = a.shift[bg];
+        float s = 0.f, q = 0.f;
+        auto walk = [&](auto f) {
+            for (int t = sp.t0; on && t <= sp.t1; ++t) {
+                const float wd = static_cast<float>(sp.width(t, a.tile * VEC));
+#pragma unroll 4
+                for (int p = lane; p <= last; p += lanes)
+                    f((p < last ? full : rest) * wd, src[(t - sp.t0) * parts + p]);
+            }
+        };
+        walk([&](float v, float2 e) { s = fmaf(v, e.x, s); });
+        const float mu = group_sum(s, lanes) / count;
+        walk([&](float v, float2 e) {
             const float d = e.x - mu;
-            q += fmaf(static_cast<float>(gn_chunk_len(a.S, part_rows, p)) * static_cast<float>(hi - lo) * d, d, e.y);
-        }
-        q = group_sum(q, 32);
-        if (lane == 0) {
-            const float rstd = rsqrtf(q / count + a.eps);
-            const float K = a.shift[bg];
+            q += fmaf(v * d, d, e.y);
+        });
+        q = group_sum(q, lanes);
+        if (on && lane == 0) {
+            const float rstd = gn_rstd(q, count, a.eps);
             fin[g] = make_float2(mu, rstd);
             shift[g] = K;
-            if (k == 0 && t0 == w.t) {
+            if (k == 0 && sp.t0 == w.t) {
                 if (a.mean) a.mean[bg] = K + mu;
                 if (a.rstd) a.rstd[bg] = rstd;
             }
@@ -426,11 +528,10 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_apply(const GnArgs a) {
     }
     __syncthreads();
     if (!w.on) return;
-    const int64_t rows = gn_chunk_len(a.S, a.out_rows, k);
-    const int visits = gn_visits(rows, w.r, a.par);
-    const int c = w.c0 + w.col * VEC;
-    GnOut<T, VEC, ACT> out;
-    out.init(a, c, [&](int g) { return fin[g - w.g0]; }, [&](int g) { return shift[g - w.g0]; });
+    const int visits = GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a.par).of(w.r);
+    GnOut<T, VEC, ONE, ACT> out;
+    gn_per_group<T, VEC, ONE>(out.K, c, a.D, [&](int g) { return shift[min(g - w.g0, w.ng - 1)]; });
+    out.init(rg, rb, c, a.D, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
     const int64_t row = k * a.out_rows + w.r;
     const T* xp = static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c;
     T* yp = static_cast<T*>(a.y) + w.b * a.yb + row * a.yr + c;
@@ -467,7 +568,7 @@ cudaError_t gn_launch_fwd(const gn_plan& p, const GnArgs& a, norm_act act, int64
     const int64_t units = B * a.tiles;
     const int channels = a.tile * VEC;
     const int groups = static_cast<int>(gn_tile_groups(channels, a.D, false));
-    const size_t smem = static_cast<size_t>(gn_smem_bytes(a.par, ONE ? a.tile : channels, groups));
+    const size_t smem = static_cast<size_t>(gn_smem_bytes(a.par, a.tile * (ONE ? 1 : a.segs), groups, p.threads));
     if (p.path == GN_PATH_CHIP) {
         const GnKernel k = act == NORM_ACT_SILU   ? gn_pick_chip<T, VEC, ONE, NORM_ACT_SILU>(p.per_thread)
                            : act == NORM_ACT_GELU ? gn_pick_chip<T, VEC, ONE, NORM_ACT_GELU>(p.per_thread)
@@ -478,11 +579,11 @@ cudaError_t gn_launch_fwd(const gn_plan& p, const GnArgs& a, norm_act act, int64
     const cudaError_t e = gn_launch(reinterpret_cast<const void*>(gn_fwd_sums<T, VEC, ONE>), units * a.chunks,
                                     p.threads, smem, a.cluster, s, a);
     if (e != cudaSuccess) return e;
-    const GnKernel k = act == NORM_ACT_SILU   ? gn_fwd_apply<T, VEC, NORM_ACT_SILU>
-                       : act == NORM_ACT_GELU ? gn_fwd_apply<T, VEC, NORM_ACT_GELU>
-                                              : gn_fwd_apply<T, VEC, NORM_ACT_NONE>;
+    const GnKernel k = act == NORM_ACT_SILU   ? gn_fwd_apply<T, VEC, ONE, NORM_ACT_SILU>
+                       : act == NORM_ACT_GELU ? gn_fwd_apply<T, VEC, ONE, NORM_ACT_GELU>
+                                              : gn_fwd_apply<T, VEC, ONE, NORM_ACT_NONE>;
     return gn_launch(reinterpret_cast<const void*>(k), units * a.out_chunks, p.threads,
-                     static_cast<size_t>(gn_smem_bytes(0, 0, groups)), 1, s, a);
+                     static_cast<size_t>(gn_smem_bytes(0, 0, groups, 0)), 1, s, a);
 }
 
 template <class T>

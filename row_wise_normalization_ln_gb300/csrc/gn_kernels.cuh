@@ -123,23 +123,50 @@ __device__ __forceinline__ float f2_sum(float2 v) {
 }
 
 // ------------------------------------------------------------ activations
+// 1 / (1 + exp(-z)) = 1 / (1 + 2^(-z log2 e)) with the hardware's base-2
+// exponential and reciprocal (each within a few ulp; results below fp32's
+// smallest normal number become 0, exponentials beyond its range infinity,
+// whose reciprocal is 0). One instruction each: with the range handling of
+// __expf and __fdividef the activation was more than half of the
+// instructions of a forward pass.
+__device__ __forceinline__ float gn_sigmoid_of(float t) {  // t = -z log2 e
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+constexpr float kMinusLog2e = -1.4426950408889634f;
+
 template <int ACT>
-__device__ __forceinline__ float gn_act(float z) {
-    if constexpr (ACT == NORM_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
-    if constexpr (ACT == NORM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+__device__ __forceinline__ float2 gn_act2(float2 z) {
+    if constexpr (ACT == NORM_ACT_SILU) {
+        const float2 t = __fmul2_rn(z, f2_splat(kMinusLog2e));
+        return __fmul2_rn(z, make_float2(gn_sigmoid_of(t.x), gn_sigmoid_of(t.y)));
+    }
+    if constexpr (ACT == NORM_ACT_GELU) {
+        const float2 h = __fmul2_rn(z, f2_splat(0.5f)), t = __fmul2_rn(z, f2_splat(0.70710678118654752f));
+        return __ffma2_rn(h, make_float2(erff(t.x), erff(t.y)), h);
+    }
     return z;
 }
 
 // act'(z): s (1 + z (1 - s)) with s = 1 / (1 + exp(-z)); Phi(z) + z phi(z).
 template <int ACT>
-__device__ __forceinline__ float gn_act_slope(float z) {
+__device__ __forceinline__ float2 gn_act_slope2(float2 z) {
     if constexpr (ACT == NORM_ACT_SILU) {
-        const float s = __fdividef(1.f, 1.f + __expf(-z));
-        return s * fmaf(z, 1.f - s, 1.f);
+        const float2 t = __fmul2_rn(z, f2_splat(kMinusLog2e));
+        const float2 s = make_float2(gn_sigmoid_of(t.x), gn_sigmoid_of(t.y));
+        const float2 zs = __fmul2_rn(z, s);               // s + z s (1 - s)
+        return __fadd2_rn(s, __ffma2_rn(make_float2(-zs.x, -zs.y), s, zs));
     }
-    if constexpr (ACT == NORM_ACT_GELU)
-        return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f));
-    return 1.f;
+    if constexpr (ACT == NORM_ACT_GELU) {
+        const float2 t = __fmul2_rn(z, f2_splat(0.70710678118654752f));
+        const float2 u = __fmul2_rn(t, make_float2(-t.x, -t.y));  // -z^2 / 2
+        const float2 phi = __fmul2_rn(z, f2_splat(0.39894228040143268f));
+        const float2 cdf = __ffma2_rn(f2_splat(0.5f), make_float2(erff(t.x), erff(t.y)), f2_splat(0.5f));
+        return __ffma2_rn(phi, make_float2(__expf(u.x), __expf(u.y)), cdf);
+    }
+    return f2_splat(1.f);
 }
 
 // ------------------------------------------------------------ geometry
@@ -177,10 +204,33 @@ __device__ __forceinline__ int64_t gn_chunk_len(int64_t S, int64_t per, int64_t 
     return left < 0 ? 0 : left < per ? left : per;
 }
 
-// Rows that row slot r visits of `rows` rows walked `par` at a time.
-__device__ __forceinline__ int gn_visits(int64_t rows, int r, int par) {
-    return r < rows ? static_cast<int>((rows - r - 1) / par) + 1 : 0;
-}
+// Rows each row slot visits of a chunk's `rows` rows walked `par` at a time:
+// slots below `full` visit `most`, the others one fewer.
+struct GnVisits {
+    int most, full;
+    __device__ __forceinline__ GnVisits(int rows, int par) {
+        most = (rows + par - 1) / par;
+        full = rows - (most - 1) * par;
+    }
+    __device__ __forceinline__ int of(int r) const { return most == 0 ? 0 : most - (r < full ? 0 : 1); }
+};
+
+// The group of each of an access's channels, and where it changes: walks
+// neighbouring channels with one division at the start.
+struct GnWalk {
+    int g, left;  // group of the current channel, channels left in it
+    int D;
+    __device__ __forceinline__ GnWalk(int c, int D_) : D(D_) {
+        g = c / D_;
+        left = (g + 1) * D_ - c;
+    }
+    __device__ __forceinline__ void next() {
+        if (--left == 0) {
+            ++g;
+            left = D;
+        }
+    }
+};
 
 // A row of distributed shared memory: float2 at index i of cluster peer
 // `rank`'s copy of `p`.
