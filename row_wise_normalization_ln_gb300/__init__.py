@@ -13,6 +13,7 @@ from __future__ import annotations
 import array
 import ctypes
 import functools
+import operator
 import os
 import threading
 from typing import Optional, Sequence
@@ -61,7 +62,7 @@ class NormPlan(ctypes.Structure):
 class GnPlan(ctypes.Structure):
     """Mirror of ``gn_plan`` in include/libnorm_group.h."""
     _fields_ = [(k, ctypes.c_int32) for k in ("path", "vec_elems", "tile", "threads", "per_thread", "cluster",
-                                              "chunks", "out_chunks")]
+                                              "chunks", "out_chunks", "bands")]
 
     def as_dict(self) -> dict:
         return {k: getattr(self, k) for k, _ in self._fields_}
@@ -608,12 +609,12 @@ def _sms(index: int) -> int:
     return torch.cuda.get_device_properties(index).multi_processor_count
 
 
-def _on_device(index: int, call, stream: Optional[torch.cuda.Stream]) -> int:
-    """``call(stream handle)`` with CUDA device ``index`` current."""
+def _on_device(index: int, stream: Optional[torch.cuda.Stream], fn, *args) -> int:
+    """``fn(*args, stream handle)`` with CUDA device ``index`` current."""
     if torch.cuda.current_device() == index:
-        return call(stream.cuda_stream if stream is not None else torch.cuda.current_stream(index).cuda_stream)
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     with torch.cuda.device(index):
-        return call(_stream_handle(stream, torch.device("cuda", index)))
+        return fn(*args, _stream_handle(stream, torch.device("cuda", index)))
 
 
 def make_gn_plan(B: int, S: int, C: int, groups: int, dtype: torch.dtype, backward: bool = False,
@@ -675,54 +676,74 @@ def _positions(x: torch.Tensor) -> Optional[torch.Tensor]:
     return x
 
 
-def _gn_input(x: torch.Tensor) -> torch.Tensor:
+def _pitched(x: torch.Tensor, what: Optional[str] = None):
+    """x (a copy where its strides need one, unless ``what`` names an output,
+    which is then refused) and its positions, sample pitch and row pitch."""
+    shape = x.shape
+    C = shape[-1]
+    if x.is_contiguous():
+        rows = shape[0] * C
+        S = x.numel() // rows if rows else 0
+        return x, S, S * C, C
     v = _positions(x)
-    return v if v is not None else _positions(x.contiguous())
-
-
-def _gn_output(out: torch.Tensor, x: torch.Tensor, name: str) -> torch.Tensor:
-    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-        raise ValueError(f"{name} must have x's shape, dtype and device")
-    v = _positions(out)
     if v is None:
-        raise ValueError(f"{name} must have evenly strided positions and samples with unit channel stride")
-    return v
+        if what is not None:
+            raise ValueError(f"{what} must have evenly strided positions and samples with unit channel stride")
+        x = x.contiguous()
+        v = _positions(x)
+    return x, v.shape[1], v.stride(0), v.stride(1)
 
 
 def _gn_check(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, groups: int, activation, what: str):
-    if not x.is_cuda:
+    index, dtype = x.get_device(), x.dtype
+    if index < 0:
         raise ValueError(f"{what} needs a CUDA tensor")
-    code = _dtype_code(x.dtype)
-    if x.dim() < 2:
+    code = _CODES.get(dtype)
+    if code is None:
+        _dtype_code(dtype)
+    shape = x.shape
+    if len(shape) < 2:
         raise ValueError("x must be [B, ..., C]: samples first, channels last")
-    C = x.shape[-1]
+    C = shape[-1]
     if groups < 1 or C < 1 or C % groups != 0:
         raise ValueError(f"{C} channels do not form {groups} groups")
-    try:
-        act = _ACTIVATIONS[activation]
-    except (KeyError, TypeError):
-        raise ValueError(f"activation must be None, 'none', 'silu' or 'gelu', got {activation!r}") from None
-    return code, act, C, _param(gamma, x, "gamma"), _param(beta, x, "beta")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be None, 'none', 'silu' or 'gelu', got {activation!r}")
+    if gamma.dtype is not dtype or gamma.get_device() != index or gamma.numel() != C or not gamma.is_contiguous():
+        gamma = _param(gamma, x, "gamma")
+    if beta.dtype is not dtype or beta.get_device() != index or beta.numel() != C or not beta.is_contiguous():
+        beta = _param(beta, x, "beta")
+    return index, code, act, shape[0], C, gamma, beta
 
 
-def _f32(t: Optional[torch.Tensor], shape, x: torch.Tensor, name: str) -> torch.Tensor:
-    """`t`, or a new fp32 tensor of that shape."""
-    if t is None:
-        return torch.empty(shape, dtype=torch.float32, device=x.device)
-    n = 1
-    for v in shape:
-        n *= v
-    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous() or t.device != x.device:
+def _gn_out(out: Optional[torch.Tensor], x: torch.Tensor, name: str):
+    """The output tensor, its sample pitch and its row pitch."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError(f"{name} must have x's shape, dtype and device")
+    _, _, batch, row = _pitched(out, name)
+    return out, batch, row
+
+
+def _f32(t: torch.Tensor, n: int, x: torch.Tensor, name: str) -> torch.Tensor:
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous() or t.device != x.device:
         raise ValueError(f"{name} must be a contiguous fp32 tensor of {n} elements on {x.device}")
     return t
 
 
-def _gn_workspace(ws: Optional[torch.Tensor], need: int, x: torch.Tensor):
+def _workspace(ws: Optional[torch.Tensor], need: int, x: torch.Tensor):
+    """(tensor, its bytes): the caller's workspace, or a new one."""
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        return (torch.empty(need, dtype=torch.uint8, device=x.device), need) if need else (None, 0)
     if ws.device != x.device or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
-    return ws
+    return ws, ws.nbytes
+
+
+def _gn_plan_ptr(plan):
+    return ctypes.byref(plan if isinstance(plan, GnPlan) else GnPlan.from_dict(plan))
 
 
 def gn_fwd(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, groups: int, eps: float = 1e-5, *,
@@ -740,34 +761,32 @@ def gn_fwd(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, groups: int
     when ``stats=False``). ``out`` may be ``x`` itself (in place).
     ``workspace`` (gn_workspace_bytes; any dtype) is allocated when not given;
     calls that share one must not overlap on the GPU."""
-    code, act, C, g, b = _gn_check(x, gamma, beta, groups, activation, "gn_fwd")
-    x3 = _gn_input(x)
-    B, S, _ = x3.shape
-    y3 = torch.empty((B, S, C), dtype=x.dtype, device=x.device) if out is None else _gn_output(out, x, "out")
+    index, code, act, B, C, g, b = _gn_check(x, gamma, beta, groups, activation, "gn_fwd")
+    y, yb, yr = _gn_out(out, x, "out")
+    x, S, xb, xr = _pitched(x)
+    mp = rp = None
     if stats:
-        mean, rstd = _f32(mean, (B, groups), x, "mean"), _f32(rstd, (B, groups), x, "rstd")
+        if mean is None and rstd is None:  # one allocation costs more than a view
+            mean, rstd = torch.empty((2, B, groups), dtype=torch.float32, device=x.device).unbind()
+        mean = torch.empty((B, groups), dtype=torch.float32, device=x.device) if mean is None \
+            else _f32(mean, B * groups, x, "mean")
+        rstd = torch.empty((B, groups), dtype=torch.float32, device=x.device) if rstd is None \
+            else _f32(rstd, B * groups, x, "rstd")
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
     else:
         mean = rstd = None
-    index = x.get_device()
     need = (_gn_workspace_bytes(B, S, C, groups, code, False, _sms(index)) if plan is None
-            else gn_workspace_bytes(x3, groups, False, plan))
-    ws = _gn_workspace(workspace, need, x)
-    L = library()
-    xs, ys = x3.stride(), y3.stride()
-
-    def call(h):
-        args = (x3.data_ptr(), xs[0], xs[1], g.data_ptr(), b.data_ptr(), y3.data_ptr(), ys[0], ys[1], _ptr(mean),
-                _ptr(rstd), _ptr(ws), ws.nbytes if ws is not None else 0, B, S, C, groups, eps, act, code, h)
-        return L.gn_fwd(*args) if plan is None else L.gn_fwd_planned(*args, _gn_plan_ptr(plan))
-
-    st = _on_device(index, call, stream)
+            else gn_workspace_bytes(x, groups, False, plan))
+    ws, nbytes = _workspace(workspace, need, x)
+    args = (x.data_ptr(), xb, xr, g.data_ptr(), b.data_ptr(), y.data_ptr(), yb, yr, mp, rp,
+            ws.data_ptr() if ws is not None else None, nbytes, B, S, C, groups, eps, act, code)
+    if plan is None:
+        st = _on_device(index, stream, library().gn_fwd, *args)
+    else:
+        st = _on_device(index, stream, lambda *v: library().gn_fwd_planned(*v, _gn_plan_ptr(plan)), *args)
     if st != NORM_OK:
         raise NormError(st, "gn_fwd")
-    return (out if out is not None else y3 if x.dim() == 3 else y3.view(x.shape)), mean, rstd
-
-
-def _gn_plan_ptr(plan):
-    return ctypes.byref(plan if isinstance(plan, GnPlan) else GnPlan.from_dict(plan))
+    return y, mean, rstd
 
 
 def gn_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, mean: torch.Tensor,
@@ -778,37 +797,31 @@ def gn_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, beta: torch.T
     are fp32 ``[C]``. ``mean``/``rstd`` are gn_fwd's fp32 statistics and
     ``activation`` the forward's; the activation's argument is recomputed
     from x. ``dx`` may be ``dy`` or ``x`` itself (in place)."""
-    code, act, C, g, b = _gn_check(x, gamma, beta, groups, activation, "gn_bwd")
-    if dy.shape != x.shape or dy.dtype != x.dtype or dy.device != x.device:
+    index, code, act, B, C, g, b = _gn_check(x, gamma, beta, groups, activation, "gn_bwd")
+    if dy.shape != x.shape or dy.dtype is not x.dtype or dy.get_device() != index:
         raise ValueError("dy must have x's shape, dtype and device")
-    x3, dy3 = _gn_input(x), _gn_input(dy)
-    B, S, _ = x3.shape
-    mean, rstd = _given_f32(mean, B * groups, x, "mean"), _given_f32(rstd, B * groups, x, "rstd")
-    dx3 = torch.empty((B, S, C), dtype=x.dtype, device=x.device) if dx is None else _gn_output(dx, x, "dx")
-    dg, db = _f32(dgamma, (C,), x, "dgamma"), _f32(dbeta, (C,), x, "dbeta")
-    index = x.get_device()
+    _f32(mean, B * groups, x, "mean")
+    _f32(rstd, B * groups, x, "rstd")
+    dx, db_, dr = _gn_out(dx, x, "dx")
+    x, S, xb, xr = _pitched(x)
+    dy, _, dyb, dyr = _pitched(dy)
+    if dgamma is None and dbeta is None:
+        dgamma, dbeta = torch.empty((2, C), dtype=torch.float32, device=x.device).unbind()
+    dgamma = torch.empty(C, dtype=torch.float32, device=x.device) if dgamma is None else _f32(dgamma, C, x, "dgamma")
+    dbeta = torch.empty(C, dtype=torch.float32, device=x.device) if dbeta is None else _f32(dbeta, C, x, "dbeta")
     need = (_gn_workspace_bytes(B, S, C, groups, code, True, _sms(index)) if plan is None
-            else gn_workspace_bytes(x3, groups, True, plan))
-    ws = _gn_workspace(workspace, need, x)
-    L = library()
-    ds, xs, os_ = dy3.stride(), x3.stride(), dx3.stride()
-
-    def call(h):
-        args = (dy3.data_ptr(), ds[0], ds[1], x3.data_ptr(), xs[0], xs[1], g.data_ptr(), b.data_ptr(),
-                mean.data_ptr(), rstd.data_ptr(), dx3.data_ptr(), os_[0], os_[1], dg.data_ptr(), db.data_ptr(),
-                _ptr(ws), ws.nbytes if ws is not None else 0, B, S, C, groups, act, code, h)
-        return L.gn_bwd(*args) if plan is None else L.gn_bwd_planned(*args, _gn_plan_ptr(plan))
-
-    st = _on_device(index, call, stream)
+            else gn_workspace_bytes(x, groups, True, plan))
+    ws, nbytes = _workspace(workspace, need, x)
+    args = (dy.data_ptr(), dyb, dyr, x.data_ptr(), xb, xr, g.data_ptr(), b.data_ptr(), mean.data_ptr(),
+            rstd.data_ptr(), dx.data_ptr(), db_, dr, dgamma.data_ptr(), dbeta.data_ptr(),
+            ws.data_ptr() if ws is not None else None, nbytes, B, S, C, groups, act, code)
+    if plan is None:
+        st = _on_device(index, stream, library().gn_bwd, *args)
+    else:
+        st = _on_device(index, stream, lambda *v: library().gn_bwd_planned(*v, _gn_plan_ptr(plan)), *args)
     if st != NORM_OK:
         raise NormError(st, "gn_bwd")
-    return (dx if dx is not None else dx3 if x.dim() == 3 else dx3.view(x.shape)), dg, db
-
-
-def _given_f32(t: torch.Tensor, n: int, x: torch.Tensor, name: str) -> torch.Tensor:
-    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous() or t.device != x.device:
-        raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor of {n} elements")
-    return t
+    return dx, dgamma, dbeta
 
 
 # ------------------------------------------------------------ gradients
@@ -835,43 +848,50 @@ def _grad_workspace_bytes(count: int, sms: int) -> int:
     return n.value
 
 
+_data_ptr, _numel, _get_device, _is_contiguous = (
+    torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.is_contiguous)
+_dtype_of, _shape_of, _stride_of = operator.attrgetter("dtype"), operator.attrgetter("shape"), torch.Tensor.stride
+
+
 def _grad_call(what, grads, outs, max_norm, norm, workspace, stream):
-    if not grads:
+    # (whole-list maps: a step has hundreds of tensors, and a loop body in
+    # Python costs several times what the kernels of a small list take)
+    n = len(grads)
+    if n == 0:
         raise ValueError(f"{what} needs at least one tensor")
-    index = grads[0].get_device()
+    first = grads[0]
+    index = first.get_device()
     if index < 0:
         raise ValueError(f"{what} needs CUDA tensors")
-    flat = []
-    for i, t in enumerate(grads):
-        code = _CODES.get(t.dtype)
-        if code is None:
-            _dtype_code(t.dtype)
-        if t.get_device() != index:
-            raise ValueError(f"every gradient must be on cuda:{index}")
-        if not t.is_contiguous() and not _dense(t):
-            raise ValueError(f"gradient {i} has gaps or overlaps between its values")
-        o = t
-        if outs is not None:
-            o = outs[i]
-            if o.shape != t.shape or o.dtype != t.dtype or o.get_device() != index or o.stride() != t.stride():
-                raise ValueError(f"out {i} must have its gradient's shape, strides, dtype and device")
-        flat += (t.data_ptr(), o.data_ptr(), t.numel(), code)  # (dtype, reserved): one 64-bit word
-    device = grads[0].device
-    norm = _f32(norm, (), grads[0], "norm")
-    need = _grad_workspace_bytes(-(-len(grads) // 64) * 64, _sms(index))
-    ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=device)
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    if set(map(_get_device, grads)) != {index}:
+        raise ValueError(f"every gradient must be on cuda:{index}")
+    dtypes = list(map(_dtype_of, grads))
+    try:
+        codes = list(map(_CODES.__getitem__, dtypes))
+    except KeyError as e:
+        _dtype_code(e.args[0])
+    if not all(map(_is_contiguous, grads)) and not all(map(_dense, grads)):
+        raise ValueError("every gradient must be dense (no gaps or overlaps between its values)")
+    flat = [0] * (4 * n)
+    flat[0::4] = map(_data_ptr, grads)
+    flat[2::4] = map(_numel, grads)
+    flat[3::4] = codes  # (dtype, reserved): one 64-bit word
+    if outs is not None and outs is not grads:
+        if set(map(_get_device, outs)) != {index} or list(map(_dtype_of, outs)) != dtypes or \
+                list(map(_shape_of, outs)) != list(map(_shape_of, grads)) or \
+                list(map(_stride_of, outs)) != list(map(_stride_of, grads)):
+            raise ValueError("every out must have its gradient's shape, strides, dtype and device")
+        flat[1::4] = map(_data_ptr, outs)
+    else:
+        flat[1::4] = flat[0::4]
+    norm = torch.empty((), dtype=torch.float32, device=first.device) if norm is None else _f32(norm, 1, first, "norm")
+    ws, nbytes = _workspace(workspace, _grad_workspace_bytes(-(-n // 64) * 64, _sms(index)), first)
     table = array.array("q", flat)
-    L = library()
-
-    def call(h):
-        at = table.buffer_info()[0]
-        if max_norm is None:
-            return L.grad_norm(at, len(grads), norm.data_ptr(), ws.data_ptr(), ws.nbytes, h)
-        return L.grad_clip(at, len(grads), max_norm, norm.data_ptr(), ws.data_ptr(), ws.nbytes, h)
-
-    st = _on_device(index, call, stream)
+    at = table.buffer_info()[0]
+    if max_norm is None:
+        st = _on_device(index, stream, library().grad_norm, at, n, norm.data_ptr(), ws.data_ptr(), nbytes)
+    else:
+        st = _on_device(index, stream, library().grad_clip, at, n, max_norm, norm.data_ptr(), ws.data_ptr(), nbytes)
     if st != NORM_OK:
         raise NormError(st, what)
     return norm

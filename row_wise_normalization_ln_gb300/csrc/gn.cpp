@@ -1,6 +1,7 @@
 // Group norm entry points of the C ABI: argument checks, the launch planner
 // and dispatch. Every argument error is caught here, before any CUDA call.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -21,6 +22,7 @@ constexpr int64_t kMaxC = int64_t(1) << 24;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSmem = 48 * 1024;
 constexpr int kMaxCluster = 8;
+constexpr int64_t kBandBytes = int64_t(32) << 20;  // of x (and dy) that stay in L2 until they are read again
 constexpr int kFwdMaxRows = 8, kBwdMaxRows = 4;  // rows a thread of the on-chip kernels can hold
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -113,29 +115,45 @@ norm_status derive(const gn_plan& p, const Shape& s, GnArgs* a) {
     a->tile = static_cast<int32_t>(std::min<int64_t>(p.tile, ncols));
     a->tiles = static_cast<int32_t>(ceil_div(ncols, a->tile));
     a->par = p.threads / a->tile;
+    a->by_tile = libnorm::fast_div(a->tile);
+    a->by_tiles = libnorm::fast_div(a->tiles);
+    a->by_par = libnorm::fast_div(a->par);
+    a->by_D = libnorm::fast_div(s.D);
     a->cluster = p.cluster;
+    a->cluster_bits = p.cluster == 8 ? 3 : p.cluster >> 1;
+    a->join = 1;
     a->segs = one_group(s, p.vec_elems) ? 1
                                         : static_cast<int32_t>(std::min<int64_t>(p.vec_elems, (p.vec_elems - 2 + s.D) / s.D + 1));
-    const int units = a->tile * (s.bwd ? p.vec_elems : a->segs);
+    const int states = a->tile * (s.bwd ? p.vec_elems : a->segs);
     const int64_t groups = libnorm::gn_tile_groups(int64_t(a->tile) * p.vec_elems, s.D, false);
-    if (libnorm::gn_smem_bytes(a->par, units, static_cast<int>(groups), p.threads) > kMaxSmem) return NORM_ERR_PLAN;
+    if (libnorm::gn_smem_bytes(a->par, states, static_cast<int>(groups), p.threads) > kMaxSmem) return NORM_ERR_PLAN;
     if (p.path == GN_PATH_CHIP) {
         if (!whole || !is_pow2(p.per_thread) || p.per_thread > maxv) return NORM_ERR_PLAN;
         a->tpg = 1;
         a->chunks = a->out_chunks = 1;
         a->chunk_rows = a->out_rows = std::max<int64_t>(1, ceil_div(s.S, p.cluster));
         if (a->chunk_rows > int64_t(a->par) * p.per_thread) return NORM_ERR_PLAN;
+        // the backward's samples meet in one cluster where they fit
+        if (s.bwd && s.B * p.cluster <= kMaxCluster) a->join = static_cast<int32_t>(s.B);
+        a->by_cluster = libnorm::fast_div(int64_t(p.cluster) * a->join);
+        a->partials = static_cast<int32_t>(a->join > 1 ? 1 : s.B);
         if (s.B * a->tiles > kMaxGrid / p.cluster) return NORM_ERR_PLAN;
         return NORM_OK;
     }
-    if (p.chunks < 1 || p.chunks % p.cluster != 0 || p.out_chunks < 1) return NORM_ERR_PLAN;
+    if (p.cluster != 1 || p.chunks < 1 || p.out_chunks < 1 || p.bands < 1) return NORM_ERR_PLAN;
     a->tpg = static_cast<int32_t>(whole ? 1 : ceil_div(s.D - 1, int64_t(a->tile) * p.vec_elems) + 1);
     a->chunks = p.chunks;
     a->out_chunks = p.out_chunks;
+    a->by_chunks = libnorm::fast_div(p.chunks);
+    a->by_out_chunks = libnorm::fast_div(p.out_chunks);
     a->chunk_rows = std::max<int64_t>(1, ceil_div(s.S, p.chunks));
     a->out_rows = std::max<int64_t>(1, ceil_div(s.S, p.out_chunks));
+    a->last_part = static_cast<int32_t>((s.S - 1) / a->chunk_rows);
     if (a->chunk_rows > (int64_t(1) << 30) || a->out_rows > (int64_t(1) << 30)) return NORM_ERR_PLAN;
-    if (s.B * a->tiles > kMaxGrid / std::max(p.chunks, p.out_chunks)) return NORM_ERR_PLAN;
+    // CTAs of a launch, and partial rows of the column gradients
+    const int64_t units = s.B * a->tiles, tall = std::max(p.chunks, p.out_chunks);
+    if (p.bands > units || tall > kMaxGrid / 4 / units || s.B > kMaxGrid / p.chunks) return NORM_ERR_PLAN;
+    a->partials = static_cast<int32_t>(s.B * p.chunks);
     return NORM_OK;
 }
 
@@ -171,40 +189,31 @@ bool chip_plan(const Shape& s, int vec, int sms, gn_plan* p) {
 }
 
 void split_plan(const Shape& s, int vec, int sms, gn_plan* p) {
-    const int64_t ncols = s.C / vec, unit = group_unit(s.D, vec), cap = tile_cap(s, vec);
+    const int es = elem_size(s.dtype);
+    const int64_t ncols = s.C / vec, unit = group_unit(s.D, vec), cap = std::min<int64_t>(tile_cap(s, vec), 256);
+    // tiles of at least 128 bytes of a row, whole groups
     int64_t tile = std::min(ncols, cap);
-    if (tile < ncols) {
-        if (unit <= cap) {
-            const int64_t tiles = ceil_div(ncols, cap / unit * unit);
-            tile = round_up(ceil_div(ncols, tiles), unit);
-        } else {
-            tile = std::min<int64_t>(cap, 256);
-        }
-    }
-    const int64_t par = std::max<int64_t>(1, (256 + tile / 2) / tile);
+    if (unit <= cap) tile = std::min(tile, unit * std::max<int64_t>(1, ceil_div(128, unit * vec * es)));
+    if (tile > cap) tile = unit;
     p->path = GN_PATH_SPLIT;
     p->vec_elems = vec;
     p->tile = static_cast<int32_t>(tile);
-    p->threads = static_cast<int32_t>(std::min<int64_t>(kGnMaxThreads, round_up(par * tile, 32)));
+    p->threads = static_cast<int32_t>(round_up(std::max<int64_t>(1, 256 / tile) * tile, 32));
+    p->cluster = 1;
     const int64_t units = std::max<int64_t>(1, s.B * ceil_div(ncols, tile));
+    const int64_t bytes = s.B * s.S * s.C * es * (s.bwd ? 2 : 1);
+    p->bands = static_cast<int32_t>(std::min<int64_t>(units, std::max<int64_t>(1, bytes / kBandBytes)));
+    const int64_t per_band = ceil_div(units, p->bands);
     const int64_t most = std::max<int64_t>(1, s.S / (p->threads / tile * 4));
-    int64_t chunks = std::max<int64_t>(1, std::min(most, ceil_div(int64_t(sms) * 4, units)));
-    int cluster = 1;
-    while (cluster * 2 <= std::min<int64_t>(chunks, kMaxCluster)) cluster *= 2;
-    p->cluster = cluster;
-    p->chunks = static_cast<int32_t>(round_up(chunks, cluster));
-    p->out_chunks = static_cast<int32_t>(std::max<int64_t>(1, std::min(most, ceil_div(int64_t(sms) * 8, units))));
-    // no chunk beyond 2^30 rows
-    const int64_t least = ceil_div(s.S, int64_t(1) << 30);
-    if (p->chunks < least) p->chunks = static_cast<int32_t>(round_up(least, cluster));
-    if (p->out_chunks < least) p->out_chunks = static_cast<int32_t>(least);
+    const int64_t chunks = std::max<int64_t>(1, std::min(most, int64_t(sms) * 2 / per_band));
+    p->chunks = p->out_chunks = static_cast<int32_t>(std::max(chunks, ceil_div(s.S, int64_t(1) << 30)));
 }
 
 // The plan for accesses of `vec` elements.
 norm_status make_plan(const Shape& s, int vec, int sms, gn_plan* p) {
     std::memset(p, 0, sizeof *p);
     GnArgs a;
-    p->chunks = p->out_chunks = 1;
+    p->chunks = p->out_chunks = p->bands = 1;
     if (!chip_plan(s, vec, sms, p) || derive(*p, s, &a) != NORM_OK) {
         std::memset(p, 0, sizeof *p);
         p->per_thread = 1;
@@ -220,21 +229,24 @@ struct Workspace {
 Workspace layout(const gn_plan& p, const Shape& s, const GnArgs& a) {
     Workspace w{0, 0, 0, 0};
     if (s.B == 0 || s.S == 0) return w;
-    int64_t partials = s.B;
     if (p.path == GN_PATH_SPLIT) {
-        const int64_t parts = a.chunks / a.cluster;
-        partials = s.B * parts;
         w.part = w.shift + (s.bwd ? 0 : round_up(s.B * s.G * 4, 16));
-        w.cols = w.part + round_up(s.B * s.G * a.tpg * parts * 8, 16);
+        w.cols = w.part + round_up(s.B * s.G * a.tpg * a.chunks * 8, 16);
     }
-    w.bytes = w.cols + (s.bwd && partials > 1 ? partials * 2 * s.C * 4 : 0);
+    w.bytes = w.cols + (s.bwd && a.partials > 1 ? int64_t(a.partials) * 2 * s.C * 4 : 0);
     return w;
 }
 
+// SM count of the current device, asked once per device.
 int device_sms() {
+    static std::atomic<int> cache[64];
     int dev = 0, n = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) n = cache[dev].load(std::memory_order_relaxed);
+    if (e == cudaSuccess && n <= 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess && dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess || n <= 0) {
         libnorm::note_cuda_error(static_cast<int>(e));
         return -1;
@@ -340,6 +352,8 @@ norm_status gn_bwd_planned(const void* dy, int64_t dy_batch, int64_t dy_row, con
     gn_plan p{};
     GnArgs a{};
     a.C = static_cast<int32_t>(C);
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
     if (B > 0 && S > 0) {
         if (!gamma || !beta || !mean || !rstd) return NORM_ERR_ARG;
         Tensor t[3] = {{dy, dy_batch, dy_row}, {x, x_batch, x_row}, {dx, dx_batch, dx_row}};
@@ -361,8 +375,7 @@ norm_status gn_bwd_planned(const void* dy, int64_t dy_batch, int64_t dy_row, con
         a.xr = t[1].row;
         a.yb = t[2].batch;
         a.yr = t[2].row;
-        const int64_t partials = p.path == GN_PATH_CHIP ? B : B * (a.chunks / a.cluster);
-        if (partials == 1) {  // dgamma and dbeta are written without partial rows
+        if (a.partials == 1) {  // dgamma and dbeta are written without partial rows
             a.colg = dgamma;
             a.colb = dbeta;
         } else {
@@ -371,9 +384,9 @@ norm_status gn_bwd_planned(const void* dy, int64_t dy_batch, int64_t dy_row, con
         }
     }
     switch (dtype) {
-        case NORM_F32: return done(libnorm::launch_gn_bwd_f32(p, a, act, B, dgamma, dbeta, stream));
-        case NORM_BF16: return done(libnorm::launch_gn_bwd_bf16(p, a, act, B, dgamma, dbeta, stream));
-        default: return done(libnorm::launch_gn_bwd_f16(p, a, act, B, dgamma, dbeta, stream));
+        case NORM_F32: return done(libnorm::launch_gn_bwd_f32(p, a, act, B, stream));
+        case NORM_BF16: return done(libnorm::launch_gn_bwd_bf16(p, a, act, B, stream));
+        default: return done(libnorm::launch_gn_bwd_f16(p, a, act, B, stream));
     }
 }
 

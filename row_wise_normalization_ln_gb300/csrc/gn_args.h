@@ -15,6 +15,19 @@ constexpr int kGnMaxThreads = 512;
 // channel): bounds the shared memory of the reductions.
 constexpr int kGnMaxMixedChannels = 512;
 
+// Division of n in [0, 2^31) by a fixed d >= 1: n / d = (mulhi(n, m) + n) >> s
+// with s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1 (Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994).
+struct FastDiv {
+    uint32_t m, s;
+};
+inline FastDiv fast_div(int64_t d) {
+    uint32_t s = 0;
+    while ((int64_t(1) << s) < d) ++s;
+    const uint64_t m = ((uint64_t(1) << 32) * ((uint64_t(1) << s) - static_cast<uint64_t>(d))) / static_cast<uint64_t>(d) + 1;
+    return FastDiv{static_cast<uint32_t>(m), s};
+}
+
 struct GnArgs {
     const void* x;
     const void* dy;        // backward
@@ -24,8 +37,8 @@ struct GnArgs {
     float* mean;           // [B, G]: written by the forward, read by the backward
     float* rstd;
     float* shift;          // SPLIT forward: [B, G], the groups' first elements
-    float2* part;          // SPLIT: [B, G, tpg, parts] group states of the merged row chunks
-    float* colg;           // backward: partial rows of dgamma and dbeta, [B * parts] rows of C values at a
+    float2* part;          // SPLIT: [B, G, tpg, chunks] group states of the row chunks
+    float* colg;           // backward: partial rows of dgamma and dbeta, [partials] rows of C values at a
     float* colb;           // pitch of col_pitch (dgamma and dbeta themselves where one partial row is all)
     int64_t S;
     int64_t xb, xr, dyb, dyr, yb, yr;  // pitches in elements
@@ -37,22 +50,33 @@ struct GnArgs {
     int32_t tpg;           // tiles a group may touch (1 when tiles are whole groups)
     int32_t segs;          // groups an access may touch
     int32_t par;           // rows a CTA works on at once: threads / tile
-    int32_t cluster;
+    int32_t cluster, cluster_bits;  // CHIP: CTAs per sample and tile
+    int32_t join;          // CHIP backward: samples in one cluster (all of them), or 1
     int32_t chunks;        // row chunks summed per sample and tile
+    int32_t last_part;     // the last of them that has rows
     int32_t out_chunks;    // row chunks written per sample and tile
     int64_t chunk_rows;    // rows per summed chunk (CHIP: per CTA of the cluster)
     int64_t out_rows;      // rows per written chunk
+    // SPLIT, of one launch: the CTAs that sum the tiles from sum_unit on, that
+    // write the tiles from out_unit on, and (backward) that add columns
+    int32_t sum_ctas, out_ctas, col_ctas, sum_unit, out_unit;
+    int32_t partials;      // partial rows the column adders find
+    float *dgamma, *dbeta;
+    FastDiv by_cluster;
+    FastDiv by_tiles, by_tile, by_D, by_par, by_chunks, by_out_chunks;
     float eps;
 };
 
 // Dynamic shared memory of a kernel, from its plan: the per-thread states
 // ([par][units]); per group and warp that shares the group, a state and its
 // count (12 bytes, at most one per warp or per group); per group, two values.
-// `units`: states per row slot; tile * segs in the forward, tile * vec_elems
+// (The column adders of the backward keep 8 bytes per thread.) `units`: states
+// per row slot; tile * segs in the forward, tile * vec_elems
 // in the backward, whose column sums are per channel.
 inline int64_t gn_smem_bytes(int par, int units, int groups, int threads) {
     const int64_t shared = groups > threads / 32 ? groups : threads / 32;
-    return int64_t(par) * units * 8 + shared * 12 + int64_t(groups) * 12 + 16;
+    const int64_t merge = int64_t(par) * units * 8 + shared * 12 + int64_t(groups) * 12 + 16;
+    return merge > int64_t(threads) * 8 ? merge : int64_t(threads) * 8;
 }
 
 // Groups a tile of `channels` channels can touch.
@@ -63,11 +87,8 @@ inline int64_t gn_tile_groups(int64_t channels, int64_t D, bool whole) {
 cudaError_t launch_gn_fwd_f32(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s);
 cudaError_t launch_gn_fwd_bf16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s);
 cudaError_t launch_gn_fwd_f16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s);
-cudaError_t launch_gn_bwd_f32(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, float* dgamma,
-                              float* dbeta, cudaStream_t s);
-cudaError_t launch_gn_bwd_bf16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, float* dgamma,
-                               float* dbeta, cudaStream_t s);
-cudaError_t launch_gn_bwd_f16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, float* dgamma,
-                              float* dbeta, cudaStream_t s);
+cudaError_t launch_gn_bwd_f32(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s);
+cudaError_t launch_gn_bwd_bf16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s);
+cudaError_t launch_gn_bwd_f16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s);
 
 }  // namespace libnorm

@@ -2,9 +2,9 @@
 //
 //   gn_bwd_chip   a CTA, or a cluster, holds all rows of a sample's tile (x
 //                 and dy) in registers: the sums and dx from one read.
-//   gn_bwd_sums,  for tiles that do not fit a cluster: the first kernel sums
-//   gn_bwd_apply  row chunks into the workspace, the second merges the chunks
-//                 and writes dx from a second read of x and dy.
+//   gn_bwd_split  for tiles that do not fit a cluster: row chunks are summed
+//                 into the workspace, and a later launch merges them and
+//                 writes dx from a second read of x and dy, from L2.
 //
 // With d = x - mean, A = rstd gamma, z = d A + beta, dz = dy act'(z), the two
 // sums S1 = sum dz and S2 = sum dz d per channel give everything: dbeta = S1,
@@ -33,7 +33,7 @@ struct GnBwdCh {
         const auto rb = X::load(static_cast<const T*>(a.beta) + c);
         const float* mean = a.mean + b * a.G;
         const float* rstd = a.rstd + b * a.G;
-        GnWalk k(c, a.D);
+        GnWalk k(c, a);
         float2 m = f2_splat(mean[k.g]), r = f2_splat(rstd[k.g]);
 #pragma unroll
         for (int i = 0; i < X::H; ++i) {
@@ -71,7 +71,7 @@ struct GnBwdOut {
 
     template <class Fin>
     __device__ __forceinline__ void init(const GnArgs& a, int c, Fin fin) {
-        GnWalk k(c, a.D);
+        GnWalk k(c, a);
 #pragma unroll
         for (int i = 0; i < HG; ++i) {
             const float2 fa = fin(k.g);
@@ -117,16 +117,17 @@ __device__ __forceinline__ void gn_bwd_put(float2* st, int tile, int col, const 
 }
 
 // The CTA's column sums from its row slots' states (st[r * stride + i]), left
-// in row 0 of st, and the groups' gamma-weighted sums of them in gs. Every
+// in row 0 of st as (S1, rstd S2), its share of (dbeta, dgamma), and the
+// groups' gamma-weighted sums of them in gs. Every
 // thread of the CTA calls it, after a barrier. Order of the additions: fixed
 // by the CTA's shape.
 template <class T, int VEC>
 __device__ __forceinline__ void gn_bwd_merge_threads(const GnArgs& a, const GnTile& w, float2* st, int stride,
                                                      float2* gs) {
     // `deep` threads per state add every deep-th row slot, then one adds theirs
-    const int deep = min(a.par, max(1, static_cast<int>(blockDim.x) / stride));
+    const int deep = min(a.par, max(1, small_quot(blockDim.x, stride)));
     if (deep > 1) {
-        const int d = static_cast<int>(threadIdx.x) / stride, i = static_cast<int>(threadIdx.x) - d * stride;
+        const int d = small_quot(threadIdx.x, stride), i = static_cast<int>(threadIdx.x) - d * stride;
         if (d < deep) {
             float2 t = st[d * stride + i];
 #pragma unroll 4
@@ -136,22 +137,20 @@ __device__ __forceinline__ void gn_bwd_merge_threads(const GnArgs& a, const GnTi
         __syncthreads();
     }
     const int left = deep > 1 ? deep : a.par;
-    if (left > 1) {
-        for (int i = threadIdx.x; i < stride; i += blockDim.x) {
-            float2 t = st[i];
+    for (int i = threadIdx.x; i < stride; i += blockDim.x) {
+        float2 t = st[i];
 #pragma unroll 4
-            for (int r = 1; r < left; ++r) t = __fadd2_rn(t, st[r * stride + i]);
-            st[i] = t;
-        }
-        __syncthreads();
+        for (int r = 1; r < left; ++r) t = __fadd2_rn(t, st[r * stride + i]);
+        const int j = VEC == 1 ? 0 : quot(i, a.by_tile);
+        const int ch = VEC == 1 ? i : (i - j * a.tile) * VEC + j;
+        if (ch < w.nc) st[i] = make_float2(t.x, t.y * a.rstd[w.b * a.G + quot(w.c0 + ch, a.by_D)]);
     }
+    __syncthreads();
     const T* gamma = static_cast<const T*>(a.gamma) + w.c0;
-    int lanes = 32;
-    while (lanes > 1 && lanes * w.ng > static_cast<int>(blockDim.x)) lanes >>= 1;
-    const int lane = threadIdx.x & (lanes - 1);
-    const int rounds = (w.ng * lanes + blockDim.x - 1) / blockDim.x;
-    for (int it = 0; it < rounds; ++it) {
-        const int g = (static_cast<int>(threadIdx.x) + it * static_cast<int>(blockDim.x)) / lanes;
+    const GnShare sh(w.ng);
+    const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
+    for (int base = 0; base < w.ng << sh.bits; base += blockDim.x) {
+        const int g = (base + static_cast<int>(threadIdx.x)) >> sh.bits;
         float2 t = make_float2(0.f, 0.f);
         if (g < w.ng) {
             const int lo = max((w.g0 + g) * a.D - w.c0, 0);
@@ -159,38 +158,37 @@ __device__ __forceinline__ void gn_bwd_merge_threads(const GnArgs& a, const GnTi
             for (int ch = lo + lane; ch < hi; ch += lanes)
                 t = __ffma2_rn(f2_splat(gn_elem(gamma + ch)), st[gn_at<VEC>(ch, a.tile)], t);
         }
-        t.x = group_sum(t.x, lanes);
-        t.y = group_sum(t.y, lanes);
+        group_sum2(t.x, t.y, lanes);
         if (g < w.ng && lane == 0) gs[g] = t;
     }
 }
 
-// The cluster's column sums, channels shared out over its CTAs, into partial
-// row `row` of the column gradients (dgamma = rstd S2, dbeta = S1).
+// The column sums of the cluster's `cl` CTAs, channels shared out over them,
+// into partial row `row` of the column gradients.
 template <int VEC>
 __device__ __forceinline__ void gn_bwd_write_cols(const GnArgs& a, const GnTile& w, const float2* st, int rank,
-                                                  int cs, int64_t row) {
-    const int per = (w.nc + cs - 1) / cs;
+                                                  int cl, int64_t row) {
+    const int per = cl == 1 ? w.nc : small_quot(w.nc + cl - 1, cl);
     const int hi = min(w.nc, (rank + 1) * per);
     for (int ch = rank * per + static_cast<int>(threadIdx.x); ch < hi; ch += blockDim.x) {
+        const int at = gn_at<VEC>(ch, a.tile);
         float2 t;
-        if (cs > 1) {
-            t = gn_peer(st, gn_at<VEC>(ch, a.tile), 0);
-            for (int k = 1; k < cs; ++k) t = __fadd2_rn(t, gn_peer(st, gn_at<VEC>(ch, a.tile), k));
+        if (cl > 1) {
+            t = gn_peer(st, at, 0);
+            for (int k = 1; k < cl; ++k) t = __fadd2_rn(t, gn_peer(st, at, k));
         } else {
-            t = st[gn_at<VEC>(ch, a.tile)];
+            t = st[at];
         }
-        const int c = w.c0 + ch;
-        a.colg[row * a.col_pitch + c] = t.y * a.rstd[w.b * a.G + c / a.D];
-        a.colb[row * a.col_pitch + c] = t.x;
+        a.colg[row * a.col_pitch + w.c0 + ch] = t.y;
+        a.colb[row * a.col_pitch + w.c0 + ch] = t.x;
     }
 }
 
-// (u, v) of a group from its sums (m1 n, m2 n).
+// (u, v) of a group from its sums (m1 n, rstd m2 n).
 __device__ __forceinline__ float2 gn_bwd_fin(const GnArgs& a, float2 t, int64_t bg) {
     const float inv = 1.f / (static_cast<float>(a.S) * static_cast<float>(a.D));
     const float r = a.rstd[bg];
-    return make_float2(r * (t.x * inv), r * (r * (r * (t.y * inv))));
+    return make_float2(r * (t.x * inv), r * (r * (t.y * inv)));
 }
 
 template <class T, int VEC, bool ONE, int ACT, int V>
@@ -199,18 +197,23 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_chip(const GnArgs a) {
     extern __shared__ float2 sm[];
     grid_release();
     grid_wait();
-    const int cs = a.cluster;
-    const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const GnTile w = gn_tile<VEC>(a, blockIdx.x / cs);
+    // A cluster holds a sample's tile (cs CTAs), or, where all samples fit
+    // (join), every sample's, so that the column sums meet in it too.
+    const int cs = a.cluster, cl = cs * a.join;
+    const int place = cl > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int own = place & ~(cs - 1);  // the first CTA of this sample
+    const int rank = place - own;
+    const int unit = quot(blockIdx.x, a.by_cluster);
+    const GnTile w = gn_tile<VEC>(a, a.join > 1 ? (own >> a.cluster_bits) * a.tiles + unit : unit);
     const int stride = a.tile * VEC;
     float2* st = sm;
     float2* gs = st + a.par * stride;
-    float2* fin = gs + (a.tile * VEC - 1 + a.D - 1) / a.D + 1;
+    float2* fin = gs + w.ng;
 
     const int64_t row0 = int64_t(rank) * a.chunk_rows;
     const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, rank));
     const int c = w.c0 + w.col * VEC;
-    const int visits = w.on ? GnVisits(rows, a.par).of(w.r) : 0;
+    const int visits = w.on ? GnVisits(rows, a).of(w.r) : 0;
     const T* xp = static_cast<const T*>(a.x) + w.b * a.xb + (row0 + w.r) * a.xr + c;
     const T* dyp = static_cast<const T*>(a.dy) + w.b * a.dyb + (row0 + w.r) * a.dyr + c;
     typename X::Raw rx[V], rdy[V];
@@ -241,23 +244,26 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_chip(const GnArgs a) {
     }
     __syncthreads();
     gn_bwd_merge_threads<T, VEC>(a, w, st, stride, gs);
-    if (cs > 1)
+    if (cl > 1)
         cluster_barrier();
     else
         __syncthreads();
     for (int g = threadIdx.x; g < w.ng; g += blockDim.x) {
         float2 t;
         if (cs > 1) {
-            t = gn_peer(gs, g, 0);
-            for (int k = 1; k < cs; ++k) t = __fadd2_rn(t, gn_peer(gs, g, k));
+            t = gn_peer(gs, g, own);
+            for (int k = 1; k < cs; ++k) t = __fadd2_rn(t, gn_peer(gs, g, own + k));
         } else {
             t = gs[g];
         }
         fin[g] = gn_bwd_fin(a, t, w.b * a.G + w.g0 + g);
     }
-    gn_bwd_write_cols<VEC>(a, w, st, rank, cs, w.b);
+    if (a.join > 1)
+        gn_bwd_write_cols<VEC>(a, w, st, place, cl, 0);
+    else
+        gn_bwd_write_cols<VEC>(a, w, st, rank, cs, w.b);
     __syncthreads();
-    if (cs > 1) cluster_arrive();  // this CTA has read its peers' sums
+    if (cl > 1) cluster_arrive();  // this CTA has read its peers' sums
     if (w.on) {
         GnBwdOut<T, VEC, ONE> out;
         out.init(a, c, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
@@ -266,29 +272,24 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_chip(const GnArgs a) {
         for (int v = 0; v < V; ++v)
             if (v < visits) X::store(yp + int64_t(v) * a.par * a.yr, out.apply(ch, rx[v], rdy[v]));
     }
-    if (cs > 1) cluster_wait();
+    if (cl > 1) cluster_wait();
 }
 
+// Row chunk k of a tile: its groups' sums and its partial row of the column
+// gradients into the workspace.
 template <class T, int VEC, bool ONE, int ACT>
-__global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_sums(const GnArgs a) {
+__device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, int k, float2* sm) {
     using X = GnVec<T, VEC>;
     constexpr int U = 4;
-    extern __shared__ float2 sm[];
-    grid_release();
-    grid_wait();
-    const int cs = a.cluster;
-    const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int64_t unit = blockIdx.x / a.chunks;
-    const int k = static_cast<int>(blockIdx.x - unit * a.chunks);
-    const GnTile w = gn_tile<VEC>(a, unit);
     const int stride = a.tile * VEC;
     float2* st = sm;
     float2* gs = st + a.par * stride;
 
     const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, k));
     const int c = w.c0 + w.col * VEC;
+    grid_wait();
     if (w.on) {
-        const int visits = GnVisits(rows, a.par).of(w.r);
+        const int visits = GnVisits(rows, a).of(w.r);
         const int64_t row = k * a.chunk_rows + w.r;
         const T* xp = static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c;
         const T* dyp = static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c;
@@ -336,61 +337,40 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_sums(const GnArgs a) {
     }
     __syncthreads();
     gn_bwd_merge_threads<T, VEC>(a, w, st, stride, gs);
-    if (cs > 1)
-        cluster_barrier();
-    else
-        __syncthreads();
-    const int p0 = k / cs, parts = a.chunks / cs;
-    for (int g = rank + cs * static_cast<int>(threadIdx.x); g < w.ng; g += cs * blockDim.x) {
-        float2 t;
-        if (cs > 1) {
-            t = gn_peer(gs, g, 0);
-            for (int j = 1; j < cs; ++j) t = __fadd2_rn(t, gn_peer(gs, g, j));
-        } else {
-            t = gs[g];
-        }
+    __syncthreads();
+    for (int g = threadIdx.x; g < w.ng; g += blockDim.x) {
         const int gg = w.g0 + g;
-        const int ti = a.tpg == 1 ? 0 : w.t - (gg * a.D / VEC) / a.tile;
-        a.part[((w.b * a.G + gg) * a.tpg + ti) * parts + p0] = t;
+        const int ti = a.tpg == 1 ? 0 : w.t - quot(gg * a.D / VEC, a.by_tile);
+        a.part[((w.b * a.G + gg) * a.tpg + ti) * a.chunks + k] = gs[g];
     }
-    gn_bwd_write_cols<VEC>(a, w, st, rank, cs, w.b * parts + p0);
-    if (cs > 1) cluster_barrier();  // no CTA leaves while a peer reads its sums
+    gn_bwd_write_cols<VEC>(a, w, st, 0, 1, w.b * a.chunks + k);
 }
 
+// Output row chunk k of a tile.
 template <class T, int VEC, bool ONE, int ACT>
-__global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_apply(const GnArgs a) {
+__device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, int k, float2* sm) {
     using X = GnVec<T, VEC>;
     constexpr int U = 4;
-    extern __shared__ float2 sm[];
-    grid_release();
-    grid_wait();
     float2* fin = sm;
-    const int64_t id = int64_t(gridDim.x) - 1 - blockIdx.x;  // last chunks first, as in the forward
-    const int64_t unit = id / a.out_chunks;
-    const int k = static_cast<int>(id - unit * a.out_chunks);
-    const GnTile w = gn_tile<VEC>(a, unit);
-    const int parts = a.chunks / a.cluster;
-    int lanes = 32;
-    while (lanes > 1 && lanes * w.ng > static_cast<int>(blockDim.x)) lanes >>= 1;
-    const int lane = threadIdx.x & (lanes - 1);
-    const int rounds = (w.ng * lanes + blockDim.x - 1) / blockDim.x;
-    for (int it = 0; it < rounds; ++it) {
-        const int g = (static_cast<int>(threadIdx.x) + it * static_cast<int>(blockDim.x)) / lanes;
+    grid_wait();
+    const GnShare sh(w.ng);
+    const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
+    for (int base = 0; base < w.ng << sh.bits; base += blockDim.x) {
+        const int g = (base + static_cast<int>(threadIdx.x)) >> sh.bits;
         const int gg = w.g0 + (g < w.ng ? g : 0);
         const int64_t bg = w.b * a.G + gg;
-        const int touched = a.tpg == 1 ? 1 : ((gg + 1) * a.D - 1) / VEC / a.tile - gg * a.D / VEC / a.tile + 1;
-        const float2* src = a.part + bg * a.tpg * parts;
+        const int touched = a.tpg == 1 ? 1 : quot(((gg + 1) * a.D - 1) / VEC, a.by_tile) - quot(gg * a.D / VEC, a.by_tile) + 1;
+        const float2* src = a.part + bg * a.tpg * a.chunks;
         float2 t = make_float2(0.f, 0.f);
         if (g < w.ng)
 #pragma unroll 4
-            for (int i = lane; i < touched * parts; i += lanes) t = __fadd2_rn(t, src[i]);
-        t.x = group_sum(t.x, lanes);
-        t.y = group_sum(t.y, lanes);
+            for (int i = lane; i < touched * a.chunks; i += lanes) t = __fadd2_rn(t, src[i]);
+        group_sum2(t.x, t.y, lanes);
         if (g < w.ng && lane == 0) fin[g] = gn_bwd_fin(a, t, bg);
     }
     __syncthreads();
     if (!w.on) return;
-    const int visits = GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a.par).of(w.r);
+    const int visits = GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a).of(w.r);
     const int c = w.c0 + w.col * VEC;
     GnBwdCh<T, VEC, ONE, ACT> ch;
     ch.init(a, w.b, c);
@@ -418,10 +398,52 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_apply(const GnArgs a) {
     }
 }
 
+// dgamma and dbeta of 32 columns from the partial rows: warp w adds rows w,
+// w + warps, ... in that order, then the warps' sums in warp order.
+__device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, float2* sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int c = block * 32 + lane;
+    float2 t = make_float2(0.f, 0.f);
+    grid_wait();
+    if (c < a.C)
+#pragma unroll 8
+        for (int p = warp; p < a.partials; p += warps)
+            t = __fadd2_rn(t, make_float2(a.colg[p * a.col_pitch + c], a.colb[p * a.col_pitch + c]));
+    sm[threadIdx.x] = t;
+    __syncthreads();
+    if (warp == 0 && c < a.C) {
+        for (int w = 1; w < warps; ++w) t = __fadd2_rn(t, sm[w * 32 + lane]);
+        a.dgamma[c] = t.x;
+        a.dbeta[c] = t.y;
+    }
+}
+
+// One launch of the split path, as in the forward; the last one also adds
+// the partial rows of the column gradients, in its first CTAs.
+template <class T, int VEC, bool ONE, int ACT>
+__global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_split(const GnArgs a) {
+    extern __shared__ float2 sm[];
+    grid_release();
+    const int first = static_cast<int>(blockIdx.x) - a.col_ctas;
+    if (first < 0) {
+        gn_bwd_add_cols(a, blockIdx.x, sm);
+        return;
+    }
+    bool out;
+    const int i = gn_role(first, a.out_ctas, a.sum_ctas, &out);
+    if (out) {
+        const int id = a.out_ctas - 1 - i;  // last chunks first
+        const int unit = quot(id, a.by_out_chunks);
+        gn_bwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.out_unit + unit), id - unit * a.out_chunks, sm);
+    } else {
+        const int unit = quot(i, a.by_chunks);
+        gn_bwd_sums<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.sum_unit + unit), i - unit * a.chunks, sm);
+    }
+}
+
 // ------------------------------------------------------------ launch
 template <class T, int VEC, bool ONE, int ACT>
 cudaError_t gn_launch_bwd(const gn_plan& p, const GnArgs& a, int64_t B, cudaStream_t s) {
-    const int64_t units = B * a.tiles;
     const int channels = a.tile * VEC;
     const int groups = static_cast<int>(gn_tile_groups(channels, a.D, false));
     const size_t smem = static_cast<size_t>(gn_smem_bytes(a.par, channels, groups, p.threads));
@@ -433,13 +455,10 @@ cudaError_t gn_launch_bwd(const gn_plan& p, const GnArgs& a, int64_t B, cudaStre
             case 4: k = reinterpret_cast<const void*>(gn_bwd_chip<T, VEC, ONE, ACT, 4>); break;
             default: return cudaErrorInvalidValue;
         }
-        return gn_launch(k, units * a.cluster, p.threads, smem, a.cluster, s, a);
+        return gn_launch(k, B * a.tiles * a.cluster, p.threads, smem, a.cluster * a.join, s, a);
     }
-    const cudaError_t e = gn_launch(reinterpret_cast<const void*>(gn_bwd_sums<T, VEC, ONE, ACT>), units * a.chunks,
-                                    p.threads, smem, a.cluster, s, a);
-    if (e != cudaSuccess) return e;
-    return gn_launch(reinterpret_cast<const void*>(gn_bwd_apply<T, VEC, ONE, ACT>), units * a.out_chunks, p.threads,
-                     static_cast<size_t>(gn_smem_bytes(0, 0, groups, 0)), 1, s, a);
+    return gn_launch_bands(reinterpret_cast<const void*>(gn_bwd_split<T, VEC, ONE, ACT>), p, a, B * a.tiles,
+                           a.partials > 1 ? (a.C + 31) / 32 : 0, smem, s);
 }
 
 template <class T, int VEC, bool ONE>
@@ -452,30 +471,29 @@ cudaError_t gn_launch_bwd_act(const gn_plan& p, const GnArgs& a, norm_act act, i
 }
 
 template <class T>
-cudaError_t gn_dispatch_bwd(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, float* dgamma, float* dbeta,
-                            cudaStream_t s) {
+cudaError_t gn_dispatch_bwd(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s) {
     constexpr int full = 16 / sizeof(T);
-    const bool one = a.D % p.vec_elems == 0;
-    int64_t partials = 0;
+    constexpr int pair = sizeof(T) == 2 ? 2 : full;  // (fp32 has no 2-element accesses)
     if (B > 0 && a.S > 0) {
-        partials = p.path == GN_PATH_CHIP ? B : B * (a.chunks / a.cluster);
+        const bool one = a.D % p.vec_elems == 0;
         cudaError_t e;
         if (p.vec_elems == full)
             e = one ? gn_launch_bwd_act<T, full, true>(p, a, act, B, s) : gn_launch_bwd_act<T, full, false>(p, a, act, B, s);
-        else if (sizeof(T) == 2 && p.vec_elems == 2)
-            e = one ? gn_launch_bwd_act<T, sizeof(T) == 2 ? 2 : 1, true>(p, a, act, B, s)
-                    : gn_launch_bwd_act<T, sizeof(T) == 2 ? 2 : full, false>(p, a, act, B, s);
+        else if (p.vec_elems == pair)
+            e = one ? gn_launch_bwd_act<T, pair, true>(p, a, act, B, s) : gn_launch_bwd_act<T, pair, false>(p, a, act, B, s);
         else
             e = gn_launch_bwd_act<T, 1, true>(p, a, act, B, s);
-        if (e != cudaSuccess) return e;
-        if (partials == 1) return cudaSuccess;  // the kernel wrote dgamma and dbeta themselves
+        // one partial row: the kernel wrote dgamma and dbeta; the split path's
+        // last launch adds its partial rows itself
+        if (e != cudaSuccess || a.partials == 1 || p.path == GN_PATH_SPLIT) return e;
     }
-    // the partial rows of the column gradients, in a fixed order (none: zeros)
+    // The partial rows of the column gradients (none: zeros), in a fixed order.
     const float* ws = a.colg;
+    int64_t partials = a.partials;
     int32_t N = a.C;
-    float *o0 = dgamma, *o1 = dbeta;
+    float *o0 = a.dgamma, *o1 = a.dbeta;
     void* cargs[] = {&ws, &partials, &N, &o0, &o1};
-    const bool wide = N % 4 == 0 && (reinterpret_cast<uintptr_t>(ws) & 15u) == 0;
+    const bool wide = N % 4 == 0;
     const bool many = partials > 64;
     const int cols = wide ? 128 : 32;
     const void* fn = wide ? (many ? reinterpret_cast<const void*>(norm_bwd_colsum<2, 4, 32>)

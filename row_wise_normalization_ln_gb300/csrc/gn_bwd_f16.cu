@@ -3,9 +3,8 @@
 
 namespace libnorm {
 
-cudaError_t launch_gn_bwd_f16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, float* dgamma,
-                             float* dbeta, cudaStream_t s) {
-    return gn_dispatch_bwd<__half>(p, a, act, B, dgamma, dbeta, s);
+cudaError_t launch_gn_bwd_f16(const gn_plan& p, const GnArgs& a, norm_act act, int64_t B, cudaStream_t s) {
+    return gn_dispatch_bwd<__half>(p, a, act, B, s);
 }
 
 }  // namespace libnorm

@@ -2,9 +2,9 @@
 //
 //   gn_fwd_chip   a CTA, or a cluster, holds all rows of a sample's tile in
 //                 registers: statistics, activation and output from one read.
-//   gn_fwd_sums,  for tiles that do not fit a cluster: the first kernel sums
-//   gn_fwd_apply  row chunks into the workspace, the second merges the chunks
-//                 and writes y from a second read of x (from L2 where it fits).
+//   gn_fwd_split  for tiles that do not fit a cluster: row chunks are summed
+//                 into the workspace, and a later launch merges them and
+//                 writes y from a second read of x, from L2.
 //
 // Statistics: differences d = x - K from a shift K near the data, so that a
 // group whose mean dwarfs its spread keeps its digits (x - K of nearby values
@@ -18,25 +18,14 @@
 
 namespace libnorm {
 
-// How a CTA's threads share its groups in the merges: 2^k lanes per group
-// while there are more groups than warps, otherwise `wpg` whole warps.
-struct GnShare {
-    int lanes, wpg;
-    __device__ __forceinline__ explicit GnShare(int ng) {
-        const int warps = blockDim.x >> 5;
-        wpg = ng >= warps ? 1 : warps / ng;
-        lanes = 32;
-        while (lanes > 1 && lanes * ng > static_cast<int>(blockDim.x)) lanes >>= 1;
-    }
-};
-
 // Collapses the per-channel states (m, m2 of `visits` values each) of an
 // access to one state per group it touches: (mean, M2) of visits * channels
 // values, in this thread's slots st[0 .. segs).
 template <int VEC>
-__device__ __forceinline__ void gn_collapse(const float2* m, const float2* m2, float visits, int c, int D, float2* st) {
+__device__ __forceinline__ void gn_collapse(const float2* m, const float2* m2, float visits, int c, const GnArgs& a,
+                                            float2* st) {
     constexpr int H = (VEC + 1) / 2;
-    GnWalk k(c, D);
+    GnWalk k(c, a);
     int seg = 0, first = 0;
     float s = 0.f;
     // the channels j .. of one group end where the walk steps to the next
@@ -71,23 +60,23 @@ template <int VEC>
 __device__ __forceinline__ void gn_merge_threads(const GnArgs& a, const GnTile& w, const float2* st, int segs,
                                                  const GnVisits& vis, const GnShare& sh, float2* gs, float* gn) {
     const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
-    const int jobs = w.ng * sh.wpg, rounds = (jobs * lanes + blockDim.x - 1) / blockDim.x;
-    for (int it = 0; it < rounds; ++it) {
+    const int jobs = w.ng * sh.wpg;
+    for (int base = 0; base < jobs << sh.bits; base += blockDim.x) {
         // (every lane of a warp takes part in the butterflies, with or without a job)
-        const int j = (static_cast<int>(threadIdx.x) + it * static_cast<int>(blockDim.x)) / lanes;
+        const int j = (base + static_cast<int>(threadIdx.x)) >> sh.bits;
         const bool on = j < jobs;
-        const int g = on ? j / sh.wpg : 0, part = on ? j - g * sh.wpg : 0;
+        const int g = !on ? 0 : sh.wpg == 1 ? j : small_quot(j, sh.wpg), part = on ? j - g * sh.wpg : 0;
         const int lo = max((w.g0 + g) * a.D, w.c0), hi = min((w.g0 + g + 1) * a.D, w.c0 + w.nc);
         const int u0 = (lo - w.c0) / VEC, n = (hi - 1 - w.c0) / VEC - u0 + 1;
-        const int across = min(n, lanes), deep = lanes / across;
-        const int r0 = lane / across, uf = lane - r0 * across;
+        const int across = min(n, lanes), deep = small_quot(lanes, across);
+        const int r0 = small_quot(lane, across), uf = lane - r0 * across;
         float s = 0.f, c = 0.f, q = 0.f;
         auto walk = [&](auto f) {
             if (on && r0 < deep)
                 for (int u = uf; u < n; u += lanes) {
                     const int ch = w.c0 + (u0 + u) * VEC;  // the access's first channel
                     const int len = min(hi, ch + VEC) - max(lo, ch);
-                    const int seg = segs == 1 ? 0 : w.g0 + g - ch / a.D;
+                    const int seg = segs == 1 ? 0 : w.g0 + g - quot(ch, a.by_D);
                     for (int r = part + sh.wpg * r0; r < a.par; r += sh.wpg * deep)
                         f(static_cast<float>(vis.of(r) * len), st[(r * a.tile + u0 + u) * segs + seg]);
                 }
@@ -96,8 +85,7 @@ __device__ __forceinline__ void gn_merge_threads(const GnArgs& a, const GnTile& 
             s = fmaf(v, v > 0.f ? e.x : 0.f, s);
             c += v;
         });
-        c = group_sum(c, lanes);
-        s = group_sum(s, lanes);
+        group_sum2(c, s, lanes);
         const float mean = c > 0.f ? __fdividef(s, c) : 0.f;
         walk([&](float v, float2 e) {
             const float d = e.x - mean;
@@ -113,31 +101,25 @@ __device__ __forceinline__ void gn_merge_threads(const GnArgs& a, const GnTile& 
 
 // The groups' states from their `wpg` states in each of the `cs` CTAs of the
 // cluster: calls done(group, mean, M2, count) once for each of the tile's
-// groups g = first, first + every, ... The lanes of a group take one state
-// each where there are enough.
+// groups. The lanes of a group take one state each where there are enough.
 template <class F>
-__device__ __forceinline__ void gn_merge_cluster(const float2* gs, const float* gn, int ng, int wpg, int cs, int first,
-                                                 int every, F done) {
+__device__ __forceinline__ void gn_merge_cluster(const float2* gs, const float* gn, int ng, int wpg, int cs, F done) {
     const int n = cs * wpg;
     if (n == 1) {
-        for (int g = first + every * static_cast<int>(threadIdx.x); g < ng; g += every * blockDim.x)
-            done(g, gs[g].x, gs[g].y, gn[g]);
+        for (int g = threadIdx.x; g < ng; g += blockDim.x) done(g, gs[g].x, gs[g].y, gn[g]);
         return;
     }
-    int lanes = 1;
-    while (lanes < 32 && lanes < n) lanes <<= 1;
-    const int lane = threadIdx.x & (lanes - 1);
-    const int jobs = (ng - first + every - 1) / every;
-    const int rounds = (jobs * lanes + blockDim.x - 1) / blockDim.x;
-    for (int it = 0; it < rounds; ++it) {
-        const int j = (static_cast<int>(threadIdx.x) + it * static_cast<int>(blockDim.x)) / lanes;
-        const int g = first + every * j;
-        const bool on = j < jobs;
+    int bits = 0;
+    while (bits < 5 && (1 << bits) < n) ++bits;
+    const int lanes = 1 << bits, lane = threadIdx.x & (lanes - 1);
+    for (int base = 0; base < ng << bits; base += blockDim.x) {
+        const int g = (base + static_cast<int>(threadIdx.x)) >> bits;
+        const bool on = g < ng;
         float c = 0.f, s = 0.f, q = 0.f;
         auto walk = [&](auto f) {
             if (on)
                 for (int i = lane; i < n; i += lanes) {
-                    const int k = wpg == 1 ? i : i / wpg, at = g * wpg + (i - k * wpg);
+                    const int k = wpg == 1 ? i : small_quot(i, wpg), at = g * wpg + (i - k * wpg);
                     if (cs > 1)
                         f(ld_peer_f32(peer_smem_addr(gn + at, k)), gn_peer(gs, at, k));
                     else
@@ -148,8 +130,7 @@ __device__ __forceinline__ void gn_merge_cluster(const float2* gs, const float* 
             s = fmaf(v, e.x, s);
             c += v;
         });
-        c = group_sum(c, lanes);
-        s = group_sum(s, lanes);
+        group_sum2(c, s, lanes);
         const float mean = c > 0.f ? __fdividef(s, c) : 0.f;
         walk([&](float v, float2 e) {
             const float d = e.x - mean;
@@ -176,8 +157,9 @@ struct GnOut {
 
     // fin(g): float2 (mu, rstd) of group g.
     template <class Fin>
-    __device__ __forceinline__ void init(const typename X::Raw& rg, const typename X::Raw& rb, int c, int D, Fin fin) {
-        GnWalk k(c, D);
+    __device__ __forceinline__ void init(const typename X::Raw& rg, const typename X::Raw& rb, int c, const GnArgs& a,
+                                         Fin fin) {
+        GnWalk k(c, a);
         float2 fa = fin(k.g);
 #pragma unroll
         for (int i = 0; i < X::H; ++i) {
@@ -206,9 +188,9 @@ struct GnOut {
 
 // A value per channel of an access from one per group: v(g).
 template <class T, int VEC, bool ONE, class F>
-__device__ __forceinline__ void gn_per_group(float2* K, int c, int D, F v) {
+__device__ __forceinline__ void gn_per_group(float2* K, int c, const GnArgs& a, F v) {
     using X = GnVec<T, VEC>;
-    GnWalk k(c, D);
+    GnWalk k(c, a);
     if constexpr (ONE) {
         K[0] = f2_splat(v(k.g));
         if (VEC == 1) K[0].y = 0.f;
@@ -231,7 +213,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
     grid_release();
     const int cs = a.cluster;
     const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const GnTile w = gn_tile<VEC>(a, blockIdx.x / cs);
+    const GnTile w = gn_tile<VEC>(a, static_cast<int>(blockIdx.x) >> a.cluster_bits);
     const int segs = ONE ? 1 : a.segs;
     const GnShare sh(w.ng);
     float2* st = sm;
@@ -241,7 +223,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
 
     const int64_t row0 = int64_t(rank) * a.chunk_rows;
     const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, rank));
-    const GnVisits vis(rows, a.par);
+    const GnVisits vis(rows, a);
     const int visits = w.on ? vis.of(w.r) : 0;
     const int c = w.c0 + w.col * VEC;
     const T* xs = static_cast<const T*>(a.x) + w.b * a.xb;
@@ -254,7 +236,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
     // the shift of a group: its first element in the sample's first row
     GnOut<T, VEC, ONE, ACT> out;
     if (w.on) {
-        gn_per_group<T, VEC, ONE>(out.K, c, a.D, [&](int g) { return gn_elem(xs + int64_t(g) * a.D); });
+        gn_per_group<T, VEC, ONE>(out.K, c, a, [&](int g) { return gn_elem(xs + int64_t(g) * a.D); });
         rg = X::load(static_cast<const T*>(a.gamma) + c);
         rb = X::load(static_cast<const T*>(a.beta) + c);
     }
@@ -293,7 +275,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
         if constexpr (ONE)
             mine[0] = make_float2(s[0].x, f2_sum<VEC>(q[0]));
         else
-            gn_collapse<VEC>(s, q, static_cast<float>(visits), c, a.D, mine);
+            gn_collapse<VEC>(s, q, static_cast<float>(visits), c, a, mine);
     }
     __syncthreads();
     gn_merge_threads<VEC>(a, w, st, segs, vis, sh, gs, gn);
@@ -301,9 +283,10 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
         cluster_barrier();
     else
         __syncthreads();
-    gn_merge_cluster(gs, gn, w.ng, sh.wpg, cs, 0, 1, [&](int g, float mu, float m2, float count) {
+    gn_merge_cluster(gs, gn, w.ng, sh.wpg, cs, [&](int g, float mu, float m2, float count) {
         const float rstd = gn_rstd(m2, count, a.eps);
         fin[g] = make_float2(mu, rstd);
+        // (in place: row 0 is this CTA's own, written after the barrier)
         if (rank == 0) {
             const int64_t at = w.b * a.G + w.g0 + g;
             if (a.mean) a.mean[at] = gn_elem(xs + int64_t(w.g0 + g) * a.D) + mu;
@@ -313,7 +296,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
     __syncthreads();
     if (cs > 1) cluster_arrive();  // this CTA has read its peers' states
     if (w.on) {
-        out.init(rg, rb, c, a.D, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
+        out.init(rg, rb, c, a, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
         T* yp = static_cast<T*>(a.y) + w.b * a.yb + (row0 + w.r) * a.yr + c;
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -341,18 +324,12 @@ __device__ __forceinline__ float2 gn_mean_m2(float s, float q, float k) {
     return make_float2(m, b2 < 0.f ? 0.f : b2);
 }
 
+// Row chunk k of a tile: its groups' states into the workspace.
 template <class T, int VEC, bool ONE>
-__global__ void __launch_bounds__(kGnMaxThreads, ONE ? 2 : 1) gn_fwd_sums(const GnArgs a) {
+__device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, int k, float2* sm) {
     using X = GnVec<T, VEC>;
     constexpr int HG = ONE ? 1 : X::H;
     constexpr int U = 8;
-    extern __shared__ float2 sm[];
-    grid_release();
-    const int cs = a.cluster;
-    const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int64_t unit = blockIdx.x / a.chunks;
-    const int k = static_cast<int>(blockIdx.x - unit * a.chunks);
-    const GnTile w = gn_tile<VEC>(a, unit);
     const int segs = ONE ? 1 : a.segs;
     const GnShare sh(w.ng);
     float2* st = sm;
@@ -360,7 +337,7 @@ __global__ void __launch_bounds__(kGnMaxThreads, ONE ? 2 : 1) gn_fwd_sums(const 
     float* gn = reinterpret_cast<float*>(gs + w.ng * sh.wpg);
 
     const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, k));
-    const GnVisits vis(rows, a.par);
+    const GnVisits vis(rows, a);
     const int c = w.c0 + w.col * VEC;
     const T* xs = static_cast<const T*>(a.x) + w.b * a.xb;
     grid_wait();
@@ -407,7 +384,7 @@ __global__ void __launch_bounds__(kGnMaxThreads, ONE ? 2 : 1) gn_fwd_sums(const 
             // into the running state, relative to the group's first element
             const float n = static_cast<float>(first), kk = static_cast<float>(stop - first);
             float2 G0[HG];
-            gn_per_group<T, VEC, ONE>(G0, c, a.D, [&](int g) { return gn_elem(xs + int64_t(g) * a.D); });
+            gn_per_group<T, VEC, ONE>(G0, c, a, [&](int g) { return gn_elem(xs + int64_t(g) * a.D); });
             if constexpr (ONE) {
                 const float2 b = gn_mean_m2(f2_sum<VEC>(s[0]), f2_sum<VEC>(q[0]), kk * VEC);
                 gn_pair_merge(m[0].x, m2[0].x, (K[0].x - G0[0].x) + b.x, b.y, n * VEC, kk * VEC);
@@ -424,24 +401,18 @@ __global__ void __launch_bounds__(kGnMaxThreads, ONE ? 2 : 1) gn_fwd_sums(const 
         if constexpr (ONE)
             mine[0] = make_float2(m[0].x, m2[0].x);
         else
-            gn_collapse<VEC>(m, m2, static_cast<float>(visits), c, a.D, mine);
+            gn_collapse<VEC>(m, m2, static_cast<float>(visits), c, a, mine);
     }
     __syncthreads();
     gn_merge_threads<VEC>(a, w, st, segs, vis, sh, gs, gn);
-    if (cs > 1)
-        cluster_barrier();
-    else
-        __syncthreads();
-    // the cluster's chunks, groups shared out over its CTAs
-    const int p0 = k / cs, parts = a.chunks / cs;
-    gn_merge_cluster(gs, gn, w.ng, sh.wpg, cs, rank, cs, [&](int g, float mu, float m2, float) {
+    __syncthreads();
+    gn_merge_cluster(gs, gn, w.ng, sh.wpg, 1, [&](int g, float mu, float m2, float) {
         const int gg = w.g0 + g;
         const int64_t bg = w.b * a.G + gg;
-        const int ti = a.tpg == 1 ? 0 : w.t - (gg * a.D / VEC) / a.tile;
-        a.part[(bg * a.tpg + ti) * parts + p0] = make_float2(mu, m2);
-        if (p0 == 0 && ti == 0) a.shift[bg] = gn_elem(xs + int64_t(gg) * a.D);
+        const int ti = a.tpg == 1 ? 0 : w.t - quot(gg * a.D / VEC, a.by_tile);
+        a.part[(bg * a.tpg + ti) * a.chunks + k] = make_float2(mu, m2);
+        if (k == 0 && ti == 0) a.shift[bg] = gn_elem(xs + int64_t(gg) * a.D);
     });
-    if (cs > 1) cluster_barrier();  // no CTA leaves while a peer reads its states
 }
 
 // The tiles a group touches, and how many of its channels lie in each.
@@ -453,8 +424,8 @@ struct GnSpan {
         GnSpan s;
         s.c0 = g * a.D;
         s.c1 = s.c0 + a.D;
-        s.t0 = a.tpg == 1 ? t : s.c0 / VEC / a.tile;
-        s.t1 = a.tpg == 1 ? t : (s.c1 - 1) / VEC / a.tile;
+        s.t0 = a.tpg == 1 ? t : quot(s.c0 / VEC, a.by_tile);
+        s.t1 = a.tpg == 1 ? t : quot((s.c1 - 1) / VEC, a.by_tile);
         return s;
     }
     __device__ __forceinline__ int width(int t, int tile_channels) const {
@@ -462,21 +433,13 @@ struct GnSpan {
     }
 };
 
+// Output row chunk k of a tile.
 template <class T, int VEC, bool ONE, int ACT>
-__global__ void __launch_bounds__(kGnMaxThreads, 2) gn_fwd_apply(const GnArgs a) {
+__device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, int k, float2* sm) {
     using X = GnVec<T, VEC>;
     constexpr int U = 4;
-    extern __shared__ float2 sm[];
-    grid_release();
-    // last chunks first: what the sums kernel read last is the likeliest in L2
-    const int64_t id = int64_t(gridDim.x) - 1 - blockIdx.x;
-    const int64_t unit = id / a.out_chunks;
-    const int k = static_cast<int>(id - unit * a.out_chunks);
-    const GnTile w = gn_tile<VEC>(a, unit);
     float2* fin = sm;                                   // (mu, rstd) per group of the tile
     float* shift = reinterpret_cast<float*>(sm + w.ng);
-    const int parts = a.chunks / a.cluster;
-    const int64_t part_rows = a.chunk_rows * a.cluster;
     const int c = w.c0 + w.col * VEC;
     grid_wait();
     typename X::Raw rg, rb;
@@ -484,21 +447,20 @@ __global__ void __launch_bounds__(kGnMaxThreads, 2) gn_fwd_apply(const GnArgs a)
         rg = X::load(static_cast<const T*>(a.gamma) + c);
         rb = X::load(static_cast<const T*>(a.beta) + c);
     }
-    // The groups' states from every tile and merged chunk, lanes side by side
-    // over the chunks: all have part_rows rows up to the last that has any.
-    const int last = static_cast<int>((a.S - 1) / part_rows);
-    const float full = static_cast<float>(part_rows), rest = static_cast<float>(a.S - last * part_rows);
+    // The groups' states from every tile and chunk, lanes side by side
+    // over the chunks: all have chunk_rows rows up to the last that has any.
+    const int last = a.last_part;
+    const float full = static_cast<float>(a.chunk_rows), rest = static_cast<float>(a.S - last * a.chunk_rows);
     const float count = static_cast<float>(a.S) * static_cast<float>(a.D);
     const GnShare sh(w.ng);
     const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
-    const int rounds = (w.ng * lanes + blockDim.x - 1) / blockDim.x;
-    for (int it = 0; it < rounds; ++it) {
-        const int g = (static_cast<int>(threadIdx.x) + it * static_cast<int>(blockDim.x)) / lanes;
+    for (int base = 0; base < w.ng << sh.bits; base += blockDim.x) {
+        const int g = (base + static_cast<int>(threadIdx.x)) >> sh.bits;
         const bool on = g < w.ng;
         const int gg = w.g0 + (on ? g : 0);
         const int64_t bg = w.b * a.G + gg;
         const GnSpan sp = GnSpan::of<VEC>(a, gg, w.t);
-        const float2* src = a.part + bg * a.tpg * parts;
+        const float2* src = a.part + bg * a.tpg * a.chunks;
         const float K = a.shift[bg];
         float s = 0.f, q = 0.f;
         auto walk = [&](auto f) {
@@ -506,7 +468,7 @@ __global__ void __launch_bounds__(kGnMaxThreads, 2) gn_fwd_apply(const GnArgs a)
                 const float wd = static_cast<float>(sp.width(t, a.tile * VEC));
 #pragma unroll 4
                 for (int p = lane; p <= last; p += lanes)
-                    f((p < last ? full : rest) * wd, src[(t - sp.t0) * parts + p]);
+                    f((p < last ? full : rest) * wd, src[(t - sp.t0) * a.chunks + p]);
             }
         };
         walk([&](float v, float2 e) { s = fmaf(v, e.x, s); });
@@ -528,10 +490,10 @@ __global__ void __launch_bounds__(kGnMaxThreads, 2) gn_fwd_apply(const GnArgs a)
     }
     __syncthreads();
     if (!w.on) return;
-    const int visits = GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a.par).of(w.r);
+    const int visits = GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a).of(w.r);
     GnOut<T, VEC, ONE, ACT> out;
-    gn_per_group<T, VEC, ONE>(out.K, c, a.D, [&](int g) { return shift[min(g - w.g0, w.ng - 1)]; });
-    out.init(rg, rb, c, a.D, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
+    gn_per_group<T, VEC, ONE>(out.K, c, a, [&](int g) { return shift[min(g - w.g0, w.ng - 1)]; });
+    out.init(rg, rb, c, a, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
     const int64_t row = k * a.out_rows + w.r;
     const T* xp = static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c;
     T* yp = static_cast<T*>(a.y) + w.b * a.yb + row * a.yr + c;
@@ -546,6 +508,28 @@ __global__ void __launch_bounds__(kGnMaxThreads, 2) gn_fwd_apply(const GnArgs a)
             if (v + u < visits) X::store(yp + u * ystep, out.apply(raw[u]));
         xp += U * xstep;
         yp += U * ystep;
+    }
+}
+
+// One launch of the split path: some CTAs sum the row chunks of one band's
+// tiles, others write the tiles of the band before, which is still in L2.
+// Sums read from HBM while outputs are written there; side by side they keep
+// it busy in both directions. The two kinds of CTAs alternate so that each
+// SM has both.
+template <class T, int VEC, bool ONE, int ACT>
+__global__ void __launch_bounds__(kGnMaxThreads, ONE ? 2 : 1) gn_fwd_split(const GnArgs a) {
+    extern __shared__ float2 sm[];
+    grid_release();
+    bool out;
+    const int i = gn_role(blockIdx.x, a.out_ctas, a.sum_ctas, &out);
+    if (out) {
+        // last chunks first: what was summed last is the likeliest in L2
+        const int id = a.out_ctas - 1 - i;
+        const int unit = quot(id, a.by_out_chunks);
+        gn_fwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.out_unit + unit), id - unit * a.out_chunks, sm);
+    } else {
+        const int unit = quot(i, a.by_chunks);
+        gn_fwd_sums<T, VEC, ONE>(a, gn_tile<VEC>(a, a.sum_unit + unit), i - unit * a.chunks, sm);
     }
 }
 
@@ -576,14 +560,10 @@ cudaError_t gn_launch_fwd(const gn_plan& p, const GnArgs& a, norm_act act, int64
         if (k == nullptr) return cudaErrorInvalidValue;
         return gn_launch(reinterpret_cast<const void*>(k), units * a.cluster, p.threads, smem, a.cluster, s, a);
     }
-    const cudaError_t e = gn_launch(reinterpret_cast<const void*>(gn_fwd_sums<T, VEC, ONE>), units * a.chunks,
-                                    p.threads, smem, a.cluster, s, a);
-    if (e != cudaSuccess) return e;
-    const GnKernel k = act == NORM_ACT_SILU   ? gn_fwd_apply<T, VEC, ONE, NORM_ACT_SILU>
-                       : act == NORM_ACT_GELU ? gn_fwd_apply<T, VEC, ONE, NORM_ACT_GELU>
-                                              : gn_fwd_apply<T, VEC, ONE, NORM_ACT_NONE>;
-    return gn_launch(reinterpret_cast<const void*>(k), units * a.out_chunks, p.threads,
-                     static_cast<size_t>(gn_smem_bytes(0, 0, groups, 0)), 1, s, a);
+    const GnKernel k = act == NORM_ACT_SILU   ? gn_fwd_split<T, VEC, ONE, NORM_ACT_SILU>
+                       : act == NORM_ACT_GELU ? gn_fwd_split<T, VEC, ONE, NORM_ACT_GELU>
+                                              : gn_fwd_split<T, VEC, ONE, NORM_ACT_NONE>;
+    return gn_launch_bands(reinterpret_cast<const void*>(k), p, a, units, 0, smem, s);
 }
 
 template <class T>

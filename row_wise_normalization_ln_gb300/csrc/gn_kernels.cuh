@@ -170,6 +170,15 @@ __device__ __forceinline__ float2 gn_act_slope2(float2 z) {
 }
 
 // ------------------------------------------------------------ geometry
+__device__ __forceinline__ int quot(int n, const FastDiv& d) {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), d.m) + static_cast<uint32_t>(n)) >> d.s);
+}
+// n / d of small numbers (both below 2^20): (n + 1/2) / d is at least
+// 1 / (2 d) away from a whole number, far more than the division's error.
+__device__ __forceinline__ int small_quot(int n, int d) {
+    return static_cast<int>(__fdividef(static_cast<float>(n) + 0.5f, static_cast<float>(d)));
+}
+
 // The CTA's tile: which sample, which accesses of a row, which groups, and
 // this thread's place in it.
 struct GnTile {
@@ -182,17 +191,18 @@ struct GnTile {
 };
 
 template <int VEC>
-__device__ __forceinline__ GnTile gn_tile(const GnArgs& a, int64_t unit) {
+__device__ __forceinline__ GnTile gn_tile(const GnArgs& a, int unit) {
     GnTile w;
-    w.b = unit / a.tiles;
-    w.t = static_cast<int>(unit - w.b * a.tiles);
+    const int b = quot(unit, a.by_tiles);
+    w.b = b;
+    w.t = unit - b * a.tiles;
     const int k0 = w.t * a.tile;
     const int nk = min(a.tile, a.ncols - k0);
     w.c0 = k0 * VEC;
     w.nc = nk * VEC;
-    w.g0 = w.c0 / a.D;
-    w.ng = (w.c0 + w.nc - 1) / a.D - w.g0 + 1;
-    w.r = static_cast<int>(threadIdx.x) / a.tile;
+    w.g0 = quot(w.c0, a.by_D);
+    w.ng = quot(w.c0 + w.nc - 1, a.by_D) - w.g0 + 1;
+    w.r = quot(threadIdx.x, a.by_tile);
     w.col = static_cast<int>(threadIdx.x) - w.r * a.tile;
     w.on = w.r < a.par && w.col < nk;
     return w;
@@ -208,9 +218,9 @@ __device__ __forceinline__ int64_t gn_chunk_len(int64_t S, int64_t per, int64_t 
 // slots below `full` visit `most`, the others one fewer.
 struct GnVisits {
     int most, full;
-    __device__ __forceinline__ GnVisits(int rows, int par) {
-        most = (rows + par - 1) / par;
-        full = rows - (most - 1) * par;
+    __device__ __forceinline__ GnVisits(int rows, const GnArgs& a) {
+        most = quot(rows + a.par - 1, a.by_par);
+        full = rows - (most - 1) * a.par;
     }
     __device__ __forceinline__ int of(int r) const { return most == 0 ? 0 : most - (r < full ? 0 : 1); }
 };
@@ -220,9 +230,9 @@ struct GnVisits {
 struct GnWalk {
     int g, left;  // group of the current channel, channels left in it
     int D;
-    __device__ __forceinline__ GnWalk(int c, int D_) : D(D_) {
-        g = c / D_;
-        left = (g + 1) * D_ - c;
+    __device__ __forceinline__ GnWalk(int c, const GnArgs& a) : D(a.D) {
+        g = quot(c, a.by_D);
+        left = (g + 1) * D - c;
     }
     __device__ __forceinline__ void next() {
         if (--left == 0) {
@@ -232,6 +242,29 @@ struct GnWalk {
     }
 };
 
+// How a CTA's threads share its groups in the merges: 2^bits lanes per group
+// while there are more groups than warps, otherwise `wpg` whole warps.
+struct GnShare {
+    int lanes, bits, wpg;
+    __device__ __forceinline__ explicit GnShare(int ng) {
+        const int warps = blockDim.x >> 5;
+        wpg = ng >= warps ? 1 : small_quot(warps, ng);
+        bits = 5;
+        while (bits > 0 && (ng << bits) > static_cast<int>(blockDim.x)) --bits;
+        lanes = 1 << bits;
+    }
+};
+
+// Sums of two values over aligned groups of `width` lanes, their butterflies
+// side by side.
+__device__ __forceinline__ void group_sum2(float& a, float& b, int width) {
+    for (int off = width >> 1; off > 0; off >>= 1) {
+        const float x = __shfl_xor_sync(kFullMask, a, off), y = __shfl_xor_sync(kFullMask, b, off);
+        a += x;
+        b += y;
+    }
+}
+
 // A row of distributed shared memory: float2 at index i of cluster peer
 // `rank`'s copy of `p`.
 __device__ __forceinline__ float2 gn_peer(const float2* p, int i, uint32_t rank) {
@@ -239,6 +272,19 @@ __device__ __forceinline__ float2 gn_peer(const float2* p, int i, uint32_t rank)
     const uint32_t at = peer_smem_addr(p + i, rank);
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
     return v;
+}
+
+// The part of a split launch this CTA takes: writing (`out`) and summing CTAs
+// alternate while both are left; `i` counts both. Returns the number of the
+// CTA among its kind.
+__device__ __forceinline__ int gn_role(int i, int out_ctas, int sum_ctas, bool* out) {
+    const int both = min(out_ctas, sum_ctas);
+    if (i < 2 * both) {
+        *out = (i & 1) == 0;
+        return i >> 1;
+    }
+    *out = out_ctas > sum_ctas;
+    return i - both;
 }
 
 // ------------------------------------------------------------ launch
@@ -266,6 +312,26 @@ inline cudaError_t gn_launch(const void* fn, int64_t grid, int threads, size_t s
     }
     void* args[] = {const_cast<GnArgs*>(&a)};
     return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// The launches of the split path over `units` tiles in the plan's bands:
+// launch j sums band j and writes band j - 1. The last one also has the
+// `col_ctas` CTAs that add the partial rows of the column gradients.
+inline cudaError_t gn_launch_bands(const void* fn, const gn_plan& p, const GnArgs& a, int64_t units, int col_ctas,
+                                   size_t smem, cudaStream_t s) {
+    for (int j = 0; j <= p.bands; ++j) {
+        GnArgs b = a;
+        const int64_t u0 = j > 0 ? units * (j - 1) / p.bands : 0, u1 = units * j / p.bands;
+        const int64_t u2 = j < p.bands ? units * (j + 1) / p.bands : u1;
+        b.out_unit = static_cast<int32_t>(u0);
+        b.out_ctas = static_cast<int32_t>((u1 - u0) * a.out_chunks);
+        b.sum_unit = static_cast<int32_t>(u1);
+        b.sum_ctas = static_cast<int32_t>((u2 - u1) * a.chunks);
+        b.col_ctas = j == p.bands ? col_ctas : 0;
+        const cudaError_t e = gn_launch(fn, int64_t(b.out_ctas) + b.sum_ctas + b.col_ctas, p.threads, smem, 1, s, b);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace libnorm

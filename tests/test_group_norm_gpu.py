@@ -198,15 +198,15 @@ def gn_plans(B, S, C, G, dtype, backward):
                     threads = -(-par * tile // 32) * 32
                     if threads <= 512:
                         out.append(dict(path=0, vec_elems=vec, tile=tile, threads=threads, per_thread=v,
-                                        cluster=cluster, chunks=1, out_chunks=1))
+                                        cluster=cluster, chunks=1, out_chunks=1, bands=1))
                 for threads in (128, 512):
                     if tile <= threads:
-                        for chunks, oc in ((cluster, 1), (3 * cluster, 5), (8 * cluster, 100)):
+                        for bands in range(1, 1 + min(3, B * -(-(C // vec) // tile))):
                             out.append(dict(path=1, vec_elems=vec, tile=tile, threads=threads, per_thread=1,
-                                            cluster=cluster, chunks=chunks, out_chunks=oc))
+                                            cluster=1, chunks=2 * cluster - 1, out_chunks=9 - cluster, bands=bands))
             for tile in (8, 37):  # groups that straddle tiles
-                out.append(dict(path=1, vec_elems=vec, tile=tile, threads=64, per_thread=1, cluster=cluster,
-                                chunks=2 * cluster, out_chunks=3))
+                out.append(dict(path=1, vec_elems=vec, tile=tile, threads=64, per_thread=1, cluster=1,
+                                chunks=3 * cluster, out_chunks=5, bands=1))
     return out
 
 
@@ -482,7 +482,8 @@ def test_plans_that_do_not_fit_are_refused():
     good = rn.make_gn_plan(1, 1000, 64, 8, torch.bfloat16)
     for kw in (dict(path=7), dict(vec_elems=4), dict(threads=0), dict(threads=1024), dict(tile=0), dict(tile=10 ** 6),
                dict(cluster=3), dict(cluster=16), dict(path=0, per_thread=1, cluster=1, threads=32, tile=1),
-               dict(path=1, chunks=3, cluster=2), dict(path=1, chunks=0), dict(path=1, out_chunks=0)):
+               dict(path=1, cluster=2), dict(path=1, cluster=1, chunks=0), dict(path=1, cluster=1, out_chunks=0),
+               dict(path=1, cluster=1, bands=0), dict(path=1, cluster=1, bands=10 ** 6)):
         with pytest.raises(rn.NormError):
             rn.gn_fwd(x, gamma, beta, 8, plan={**good, **kw})
     odd = torch.zeros(1000 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(1, 1000, 64)
