@@ -10,10 +10,7 @@ first call raises ``LibraryNotBuilt``.
 """
 from __future__ import annotations
 
-import array
 import ctypes
-import functools
-import operator
 import os
 import threading
 from typing import Optional, Sequence
@@ -601,20 +598,38 @@ def rms_fwd_fp8(x: torch.Tensor, w: torch.Tensor, scale, eps: float = 1e-6, *,
 
 # ------------------------------------------------------------ group norm
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "gelu": 2}
-_CODES = {torch.float32: NORM_F32, torch.bfloat16: NORM_BF16, torch.float16: NORM_F16}
+_binding_module = None
 
 
-@functools.lru_cache(maxsize=None)
-def _sms(index: int) -> int:
-    return torch.cuda.get_device_properties(index).multi_processor_count
+def _native():
+    """The native half of this binding (native/binding.cpp): the checks and
+    the marshalling of the calls below."""
+    global _binding_module
+    if _binding_module is None:
+        try:
+            from . import _binding as m
+        except ImportError as e:
+            raise LibraryNotBuilt(
+                "_binding.so is missing or does not load: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'` (needs nvcc and g++)") from e
+        _binding_module = m
+    return _binding_module
 
 
-def _on_device(index: int, stream: Optional[torch.cuda.Stream], fn, *args) -> int:
-    """``fn(*args, stream handle)`` with CUDA device ``index`` current."""
-    if torch.cuda.current_device() == index:
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
-    with torch.cuda.device(index):
-        return fn(*args, _stream_handle(stream, torch.device("cuda", index)))
+def _act_code(activation) -> int:
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be None, 'none', 'silu' or 'gelu', got {activation!r}")
+    return act
+
+
+def _on_stream(stream: torch.cuda.Stream, x: torch.Tensor, call):
+    """`call()` with `stream` current: what it allocates then belongs to that
+    stream too."""
+    if stream.device != x.device:
+        raise ValueError(f"stream must be on {x.device}, got {stream.device}")
+    with torch.cuda.stream(stream):
+        return call()
 
 
 def make_gn_plan(B: int, S: int, C: int, groups: int, dtype: torch.dtype, backward: bool = False,
@@ -632,118 +647,21 @@ def make_gn_plan(B: int, S: int, C: int, groups: int, dtype: torch.dtype, backwa
     return p.as_dict()
 
 
-@functools.lru_cache(maxsize=4096)
-def _gn_workspace_bytes(B: int, S: int, C: int, groups: int, code: int, backward: bool, sms: int) -> int:
-    n = ctypes.c_size_t()
-    st = library().gn_workspace_bytes(B, S, C, groups, code, int(backward), sms, None, ctypes.byref(n))
-    if st != NORM_OK:
-        raise NormError(st, "gn_workspace_bytes")
-    return n.value
-
-
 def gn_workspace_bytes(x: torch.Tensor, groups: int, backward: bool = False, plan=None) -> int:
-    """Bytes of workspace gn_fwd / gn_bwd need for x."""
+    """Bytes of workspace gn_fwd / gn_bwd need for a [B, ..., C] CUDA tensor."""
     B, C = x.shape[0], x.shape[-1]
     S = x.numel() // (B * C) if x.numel() else 0
-    code = _dtype_code(x.dtype)
-    if plan is None:
-        return _gn_workspace_bytes(B, S, C, groups, code, bool(backward), _sms(x.get_device()))
+    sms = torch.cuda.get_device_properties(x.device).multi_processor_count if plan is None else 0
     n = ctypes.c_size_t()
-    p = plan if isinstance(plan, GnPlan) else GnPlan.from_dict(plan)
-    st = library().gn_workspace_bytes(B, S, C, groups, code, int(backward), 0, ctypes.byref(p), ctypes.byref(n))
+    st = library().gn_workspace_bytes(B, S, C, groups, _dtype_code(x.dtype), int(backward), sms,
+                                      None if plan is None else ctypes.byref(_gn_plan(plan)), ctypes.byref(n))
     if st != NORM_OK:
         raise NormError(st, "gn_workspace_bytes")
     return n.value
 
 
-def _positions(x: torch.Tensor) -> Optional[torch.Tensor]:
-    """x as [B, S, C] without a copy, or None where its strides do not allow
-    one row pitch and one sample pitch."""
-    if x.dim() != 3:
-        if x.dim() > 3:
-            try:
-                x = x.view(x.shape[0], -1, x.shape[-1])
-            except RuntimeError:
-                return None
-        else:
-            x = x.unsqueeze(1)
-    if x.is_contiguous():
-        return x
-    B, S, C = x.shape
-    xb, xr, xc = x.stride()
-    if (C > 1 and xc != 1) or (S > 1 and xr < C) or (B > 1 and xb < (S - 1) * xr + C):
-        return None
-    return x
-
-
-def _pitched(x: torch.Tensor, what: Optional[str] = None):
-    """x (a copy where its strides need one, unless ``what`` names an output,
-    which is then refused) and its positions, sample pitch and row pitch."""
-    shape = x.shape
-    C = shape[-1]
-    if x.is_contiguous():
-        rows = shape[0] * C
-        S = x.numel() // rows if rows else 0
-        return x, S, S * C, C
-    v = _positions(x)
-    if v is None:
-        if what is not None:
-            raise ValueError(f"{what} must have evenly strided positions and samples with unit channel stride")
-        x = x.contiguous()
-        v = _positions(x)
-    return x, v.shape[1], v.stride(0), v.stride(1)
-
-
-def _gn_check(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, groups: int, activation, what: str):
-    index, dtype = x.get_device(), x.dtype
-    if index < 0:
-        raise ValueError(f"{what} needs a CUDA tensor")
-    code = _CODES.get(dtype)
-    if code is None:
-        _dtype_code(dtype)
-    shape = x.shape
-    if len(shape) < 2:
-        raise ValueError("x must be [B, ..., C]: samples first, channels last")
-    C = shape[-1]
-    if groups < 1 or C < 1 or C % groups != 0:
-        raise ValueError(f"{C} channels do not form {groups} groups")
-    act = _ACTIVATIONS.get(activation)
-    if act is None:
-        raise ValueError(f"activation must be None, 'none', 'silu' or 'gelu', got {activation!r}")
-    if gamma.dtype is not dtype or gamma.get_device() != index or gamma.numel() != C or not gamma.is_contiguous():
-        gamma = _param(gamma, x, "gamma")
-    if beta.dtype is not dtype or beta.get_device() != index or beta.numel() != C or not beta.is_contiguous():
-        beta = _param(beta, x, "beta")
-    return index, code, act, shape[0], C, gamma, beta
-
-
-def _gn_out(out: Optional[torch.Tensor], x: torch.Tensor, name: str):
-    """The output tensor, its sample pitch and its row pitch."""
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-        raise ValueError(f"{name} must have x's shape, dtype and device")
-    _, _, batch, row = _pitched(out, name)
-    return out, batch, row
-
-
-def _f32(t: torch.Tensor, n: int, x: torch.Tensor, name: str) -> torch.Tensor:
-    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous() or t.device != x.device:
-        raise ValueError(f"{name} must be a contiguous fp32 tensor of {n} elements on {x.device}")
-    return t
-
-
-def _workspace(ws: Optional[torch.Tensor], need: int, x: torch.Tensor):
-    """(tensor, its bytes): the caller's workspace, or a new one."""
-    if ws is None:
-        return (torch.empty(need, dtype=torch.uint8, device=x.device), need) if need else (None, 0)
-    if ws.device != x.device or not ws.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
-    return ws, ws.nbytes
-
-
-def _gn_plan_ptr(plan):
-    return ctypes.byref(plan if isinstance(plan, GnPlan) else GnPlan.from_dict(plan))
+def _gn_plan(plan) -> GnPlan:
+    return plan if isinstance(plan, GnPlan) else GnPlan.from_dict(plan)
 
 
 def gn_fwd(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, groups: int, eps: float = 1e-5, *,
@@ -761,32 +679,15 @@ def gn_fwd(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, groups: int
     when ``stats=False``). ``out`` may be ``x`` itself (in place).
     ``workspace`` (gn_workspace_bytes; any dtype) is allocated when not given;
     calls that share one must not overlap on the GPU."""
-    index, code, act, B, C, g, b = _gn_check(x, gamma, beta, groups, activation, "gn_fwd")
-    y, yb, yr = _gn_out(out, x, "out")
-    x, S, xb, xr = _pitched(x)
-    mp = rp = None
-    if stats:
-        if mean is None and rstd is None:  # one allocation costs more than a view
-            mean, rstd = torch.empty((2, B, groups), dtype=torch.float32, device=x.device).unbind()
-        mean = torch.empty((B, groups), dtype=torch.float32, device=x.device) if mean is None \
-            else _f32(mean, B * groups, x, "mean")
-        rstd = torch.empty((B, groups), dtype=torch.float32, device=x.device) if rstd is None \
-            else _f32(rstd, B * groups, x, "rstd")
-        mp, rp = mean.data_ptr(), rstd.data_ptr()
-    else:
-        mean = rstd = None
-    need = (_gn_workspace_bytes(B, S, C, groups, code, False, _sms(index)) if plan is None
-            else gn_workspace_bytes(x, groups, False, plan))
-    ws, nbytes = _workspace(workspace, need, x)
-    args = (x.data_ptr(), xb, xr, g.data_ptr(), b.data_ptr(), y.data_ptr(), yb, yr, mp, rp,
-            ws.data_ptr() if ws is not None else None, nbytes, B, S, C, groups, eps, act, code)
-    if plan is None:
-        st = _on_device(index, stream, library().gn_fwd, *args)
-    else:
-        st = _on_device(index, stream, lambda *v: library().gn_fwd_planned(*v, _gn_plan_ptr(plan)), *args)
-    if st != NORM_OK:
-        raise NormError(st, "gn_fwd")
-    return y, mean, rstd
+    if stream is not None:
+        return _on_stream(stream, x, lambda: gn_fwd(x, gamma, beta, groups, eps, activation=activation, out=out,
+                                                    mean=mean, rstd=rstd, stats=stats, workspace=workspace, plan=plan))
+    p = None if plan is None else _gn_plan(plan)
+    r = _native().gn_fwd(x, gamma, beta, groups, eps, _act_code(activation), out, mean, rstd, bool(stats), workspace,
+                         None if p is None else ctypes.addressof(p))
+    if type(r) is int:
+        raise NormError(r, "gn_fwd")
+    return r
 
 
 def gn_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, mean: torch.Tensor,
@@ -797,104 +698,27 @@ def gn_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, beta: torch.T
     are fp32 ``[C]``. ``mean``/``rstd`` are gn_fwd's fp32 statistics and
     ``activation`` the forward's; the activation's argument is recomputed
     from x. ``dx`` may be ``dy`` or ``x`` itself (in place)."""
-    index, code, act, B, C, g, b = _gn_check(x, gamma, beta, groups, activation, "gn_bwd")
-    if dy.shape != x.shape or dy.dtype is not x.dtype or dy.get_device() != index:
-        raise ValueError("dy must have x's shape, dtype and device")
-    _f32(mean, B * groups, x, "mean")
-    _f32(rstd, B * groups, x, "rstd")
-    dx, db_, dr = _gn_out(dx, x, "dx")
-    x, S, xb, xr = _pitched(x)
-    dy, _, dyb, dyr = _pitched(dy)
-    if dgamma is None and dbeta is None:
-        dgamma, dbeta = torch.empty((2, C), dtype=torch.float32, device=x.device).unbind()
-    dgamma = torch.empty(C, dtype=torch.float32, device=x.device) if dgamma is None else _f32(dgamma, C, x, "dgamma")
-    dbeta = torch.empty(C, dtype=torch.float32, device=x.device) if dbeta is None else _f32(dbeta, C, x, "dbeta")
-    need = (_gn_workspace_bytes(B, S, C, groups, code, True, _sms(index)) if plan is None
-            else gn_workspace_bytes(x, groups, True, plan))
-    ws, nbytes = _workspace(workspace, need, x)
-    args = (dy.data_ptr(), dyb, dyr, x.data_ptr(), xb, xr, g.data_ptr(), b.data_ptr(), mean.data_ptr(),
-            rstd.data_ptr(), dx.data_ptr(), db_, dr, dgamma.data_ptr(), dbeta.data_ptr(),
-            ws.data_ptr() if ws is not None else None, nbytes, B, S, C, groups, act, code)
-    if plan is None:
-        st = _on_device(index, stream, library().gn_bwd, *args)
-    else:
-        st = _on_device(index, stream, lambda *v: library().gn_bwd_planned(*v, _gn_plan_ptr(plan)), *args)
-    if st != NORM_OK:
-        raise NormError(st, "gn_bwd")
-    return dx, dgamma, dbeta
+    if stream is not None:
+        return _on_stream(stream, x, lambda: gn_bwd(dy, x, gamma, beta, mean, rstd, groups, activation=activation,
+                                                    dx=dx, dgamma=dgamma, dbeta=dbeta, workspace=workspace, plan=plan))
+    p = None if plan is None else _gn_plan(plan)
+    r = _native().gn_bwd(dy, x, gamma, beta, mean, rstd, groups, _act_code(activation), dx, dgamma, dbeta, workspace,
+                         None if p is None else ctypes.addressof(p))
+    if type(r) is int:
+        raise NormError(r, "gn_bwd")
+    return r
 
 
 # ------------------------------------------------------------ gradients
-def _dense(t: torch.Tensor) -> bool:
-    """Whether t's values lie one after the other in memory, in any order of
-    its dimensions."""
-    if t.is_contiguous():
-        return True
-    n = 1
-    for size, stride in sorted(zip(t.shape, t.stride()), key=lambda v: v[1]):
-        if size != 1:
-            if stride != n:
-                return False
-            n *= size
-    return True
-
-
-@functools.lru_cache(maxsize=None)
-def _grad_workspace_bytes(count: int, sms: int) -> int:
-    n = ctypes.c_size_t()
-    st = library().grad_workspace_bytes(count, sms, ctypes.byref(n))
-    if st != NORM_OK:
-        raise NormError(st, "grad_workspace_bytes")
-    return n.value
-
-
-_data_ptr, _numel, _get_device, _is_contiguous = (
-    torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.is_contiguous)
-_dtype_of, _shape_of, _stride_of = operator.attrgetter("dtype"), operator.attrgetter("shape"), torch.Tensor.stride
-
-
 def _grad_call(what, grads, outs, max_norm, norm, workspace, stream):
-    # (whole-list maps: a step has hundreds of tensors, and a loop body in
-    # Python costs several times what the kernels of a small list take)
-    n = len(grads)
-    if n == 0:
-        raise ValueError(f"{what} needs at least one tensor")
-    first = grads[0]
-    index = first.get_device()
-    if index < 0:
-        raise ValueError(f"{what} needs CUDA tensors")
-    if set(map(_get_device, grads)) != {index}:
-        raise ValueError(f"every gradient must be on cuda:{index}")
-    dtypes = list(map(_dtype_of, grads))
-    try:
-        codes = list(map(_CODES.__getitem__, dtypes))
-    except KeyError as e:
-        _dtype_code(e.args[0])
-    if not all(map(_is_contiguous, grads)) and not all(map(_dense, grads)):
-        raise ValueError("every gradient must be dense (no gaps or overlaps between its values)")
-    flat = [0] * (4 * n)
-    flat[0::4] = map(_data_ptr, grads)
-    flat[2::4] = map(_numel, grads)
-    flat[3::4] = codes  # (dtype, reserved): one 64-bit word
-    if outs is not None and outs is not grads:
-        if set(map(_get_device, outs)) != {index} or list(map(_dtype_of, outs)) != dtypes or \
-                list(map(_shape_of, outs)) != list(map(_shape_of, grads)) or \
-                list(map(_stride_of, outs)) != list(map(_stride_of, grads)):
-            raise ValueError("every out must have its gradient's shape, strides, dtype and device")
-        flat[1::4] = map(_data_ptr, outs)
-    else:
-        flat[1::4] = flat[0::4]
-    norm = torch.empty((), dtype=torch.float32, device=first.device) if norm is None else _f32(norm, 1, first, "norm")
-    ws, nbytes = _workspace(workspace, _grad_workspace_bytes(-(-n // 64) * 64, _sms(index)), first)
-    table = array.array("q", flat)
-    at = table.buffer_info()[0]
-    if max_norm is None:
-        st = _on_device(index, stream, library().grad_norm, at, n, norm.data_ptr(), ws.data_ptr(), nbytes)
-    else:
-        st = _on_device(index, stream, library().grad_clip, at, n, max_norm, norm.data_ptr(), ws.data_ptr(), nbytes)
-    if st != NORM_OK:
-        raise NormError(st, what)
-    return norm
+    if stream is not None:
+        if not grads:
+            raise ValueError(f"{what} needs at least one tensor")
+        return _on_stream(stream, grads[0], lambda: _grad_call(what, grads, outs, max_norm, norm, workspace, None))
+    r = _native().grad(grads, outs, max_norm, norm, workspace)
+    if type(r) is int:
+        raise NormError(r, what)
+    return r
 
 
 def grad_norm(grads: Sequence[torch.Tensor], *, norm: Optional[torch.Tensor] = None,
@@ -916,8 +740,6 @@ def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[S
     tensors of the same shapes, strides and types. Returns ``(out, norm)``.
     With an infinite norm the coefficient is 0, with a NaN norm NaN: read
     ``norm`` to skip such a step. A tensor may be listed once only."""
-    if out is not None and len(out) != len(grads):
-        raise ValueError(f"out must hold one tensor per gradient ({len(grads)}), got {len(out)}")
     norm = _grad_call("grad_clip", grads, out, float(max_norm), norm, workspace, stream)
     return (out if out is not None else grads), norm
 

@@ -22,7 +22,7 @@ constexpr int64_t kMaxC = int64_t(1) << 24;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSmem = 48 * 1024;
 constexpr int kMaxCluster = 8;
-constexpr int64_t kBandBytes = int64_t(32) << 20;  // of x (and dy) that stay in L2 until they are read again
+constexpr int64_t kBandBytes = int64_t(1) << 50;  // of x (and dy) that stay in L2 until they are read again
 constexpr int kFwdMaxRows = 8, kBwdMaxRows = 4;  // rows a thread of the on-chip kernels can hold
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
