@@ -278,9 +278,8 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_chip(const GnArgs a) {
 // Row chunk k of a tile: its groups' sums and its partial row of the column
 // gradients into the workspace.
 template <class T, int VEC, bool ONE, int ACT>
-__device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, int k, float2* sm) {
+__device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, int k, float2* sm, void* ring) {
     using X = GnVec<T, VEC>;
-    constexpr int U = 4;
     const int stride = a.tile * VEC;
     float2* st = sm;
     float2* gs = st + a.par * stride;
@@ -291,47 +290,35 @@ __device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, in
     if (w.on) {
         const int visits = GnVisits(rows, a).of(w.r);
         const int64_t row = k * a.chunk_rows + w.r;
-        const T* xp = static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c;
-        const T* dyp = static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c;
-        const int64_t xstep = int64_t(a.par) * a.xr, dystep = int64_t(a.par) * a.dyr;
+        const T* p[2] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c,
+                         static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c};
+        const int64_t step[2] = {int64_t(a.par) * a.xr, int64_t(a.par) * a.dyr};
         GnBwdCh<T, VEC, ONE, ACT> ch;
         ch.init(a, w.b, c);
-        float2 t1[X::H], t2[X::H];
+        float2 t1[X::H], t2[X::H], s1[X::H], s2[X::H];
 #pragma unroll
-        for (int i = 0; i < X::H; ++i) t1[i] = t2[i] = make_float2(0.f, 0.f);
-        for (int v0 = 0; v0 < visits;) {
-            const int stop = min(visits, v0 + kGnSumRows);
-            float2 s1[X::H], s2[X::H];
+        for (int i = 0; i < X::H; ++i) t1[i] = t2[i] = s1[i] = s2[i] = make_float2(0.f, 0.f);
+        GnStream<T, VEC, 2>::run(p, step, visits, ring, [&](int v, const auto& raw) {
+            if ((v & (kGnSumRows - 1)) == 0) {
 #pragma unroll
-            for (int i = 0; i < X::H; ++i) s1[i] = s2[i] = make_float2(0.f, 0.f);
-            for (; v0 < stop; v0 += U) {
-                typename X::Raw rx[U], rdy[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (v0 + u < stop) {
-                        rx[u] = X::load(xp + u * xstep);
-                        rdy[u] = X::load(dyp + u * dystep);
-                    }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (v0 + u < stop) {
-#pragma unroll
-                        for (int i = 0; i < X::H; ++i) {
-                            const float2 d = ch.diff(rx[u], i);
-                            const float2 dz = ch.dz(rdy[u], d, i);
-                            s1[i] = __fadd2_rn(s1[i], dz);
-                            s2[i] = __ffma2_rn(dz, d, s2[i]);
-                        }
-                    }
-                xp += U * xstep;
-                dyp += U * dystep;
+                for (int i = 0; i < X::H; ++i) {
+                    t1[i] = __fadd2_rn(t1[i], s1[i]);
+                    t2[i] = __fadd2_rn(t2[i], s2[i]);
+                    s1[i] = s2[i] = make_float2(0.f, 0.f);
+                }
             }
-            v0 = stop;
 #pragma unroll
             for (int i = 0; i < X::H; ++i) {
-                t1[i] = __fadd2_rn(t1[i], s1[i]);
-                t2[i] = __fadd2_rn(t2[i], s2[i]);
+                const float2 d = ch.diff(raw[0], i);
+                const float2 dz = ch.dz(raw[1], d, i);
+                s1[i] = __fadd2_rn(s1[i], dz);
+                s2[i] = __ffma2_rn(dz, d, s2[i]);
             }
+        });
+#pragma unroll
+        for (int i = 0; i < X::H; ++i) {
+            t1[i] = __fadd2_rn(t1[i], s1[i]);
+            t2[i] = __fadd2_rn(t2[i], s2[i]);
         }
         gn_bwd_put<VEC>(st + w.r * stride, a.tile, w.col, t1, t2);
     }
@@ -348,9 +335,8 @@ __device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, in
 
 // Output row chunk k of a tile.
 template <class T, int VEC, bool ONE, int ACT>
-__device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, int k, float2* sm) {
+__device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, int k, float2* sm, void* ring) {
     using X = GnVec<T, VEC>;
-    constexpr int U = 4;
     float2* fin = sm;
     grid_wait();
     const GnShare sh(w.ng);
@@ -377,25 +363,15 @@ __device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, i
     GnBwdOut<T, VEC, ONE> out;
     out.init(a, c, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
     const int64_t row = k * a.out_rows + w.r;
-    const T* xp = static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c;
-    const T* dyp = static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c;
+    const T* p[2] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c,
+                     static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c};
+    const int64_t step[2] = {int64_t(a.par) * a.xr, int64_t(a.par) * a.dyr};
     T* yp = static_cast<T*>(a.y) + w.b * a.yb + row * a.yr + c;
-    const int64_t xstep = int64_t(a.par) * a.xr, dystep = int64_t(a.par) * a.dyr, ystep = int64_t(a.par) * a.yr;
-    for (int v = 0; v < visits; v += U) {
-        typename X::Raw rx[U], rdy[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v + u < visits) {
-                rx[u] = X::load(xp + u * xstep);
-                rdy[u] = X::load(dyp + u * dystep);
-            }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v + u < visits) X::store(yp + u * ystep, out.apply(ch, rx[u], rdy[u]));
-        xp += U * xstep;
-        dyp += U * dystep;
-        yp += U * ystep;
-    }
+    const int64_t ystep = int64_t(a.par) * a.yr;
+    GnStream<T, VEC, 2>::run(p, step, visits, ring, [&](int, const auto& raw) {
+        X::store(yp, out.apply(ch, raw[0], raw[1]));
+        yp += ystep;
+    });
 }
 
 // dgamma and dbeta of 32 columns from the partial rows: warp w adds rows w,
@@ -422,7 +398,8 @@ __device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, floa
 // the partial rows of the column gradients, in its first CTAs.
 template <class T, int VEC, bool ONE, int ACT>
 __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_split(const GnArgs a) {
-    extern __shared__ float2 sm[];
+    extern __shared__ __align__(16) float2 slots[];  // the row stream's slots, then the merges' states
+    float2* sm = slots + GnStream<T, VEC, 2>::kRing / 8 * blockDim.x;
     grid_release();
     const int first = static_cast<int>(blockIdx.x) - a.col_ctas;
     if (first < 0) {
@@ -434,10 +411,10 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_split(const GnArgs a) {
     if (out) {
         const int id = a.out_ctas - 1 - i;  // last chunks first
         const int unit = quot(id, a.by_out_chunks);
-        gn_bwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.out_unit + unit), id - unit * a.out_chunks, sm);
+        gn_bwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.out_unit + unit), id - unit * a.out_chunks, sm, slots);
     } else {
         const int unit = quot(i, a.by_chunks);
-        gn_bwd_sums<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.sum_unit + unit), i - unit * a.chunks, sm);
+        gn_bwd_sums<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.sum_unit + unit), i - unit * a.chunks, sm, slots);
     }
 }
 
@@ -458,7 +435,8 @@ cudaError_t gn_launch_bwd(const gn_plan& p, const GnArgs& a, int64_t B, cudaStre
         return gn_launch(k, B * a.tiles * a.cluster, p.threads, smem, a.cluster * a.join, s, a);
     }
     return gn_launch_bands(reinterpret_cast<const void*>(gn_bwd_split<T, VEC, ONE, ACT>), p, a, B * a.tiles,
-                           a.partials > 1 ? (a.C + 31) / 32 : 0, smem, s);
+                           a.partials > 1 ? (a.C + 31) / 32 : 0,
+                           smem + static_cast<size_t>(GnStream<T, VEC, 2>::kRing) * p.threads, s);
 }
 
 template <class T, int VEC, bool ONE>

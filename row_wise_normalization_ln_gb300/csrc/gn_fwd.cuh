@@ -326,10 +326,9 @@ __device__ __forceinline__ float2 gn_mean_m2(float s, float q, float k) {
 
 // Row chunk k of a tile: its groups' states into the workspace.
 template <class T, int VEC, bool ONE>
-__device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, int k, float2* sm) {
+__device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, int k, float2* sm, void* ring) {
     using X = GnVec<T, VEC>;
     constexpr int HG = ONE ? 1 : X::H;
-    constexpr int U = 8;
     const int segs = ONE ? 1 : a.segs;
     const GnShare sh(w.ng);
     float2* st = sm;
@@ -343,45 +342,14 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
     grid_wait();
     if (w.on) {
         const int visits = vis.of(w.r);
-        const T* xp = xs + (k * a.chunk_rows + w.r) * a.xr + c;
-        const int64_t step = int64_t(a.par) * a.xr;
         // Blocks of kGnShiftRows rows, shifted by the block's first value:
         // per channel, or one for the channels of an access within a group.
-        float2 m[HG], m2[HG];
+        // A full block goes into the running state (m, m2), whose means are
+        // relative to the group's first element.
+        float2 m[HG], m2[HG], K[HG], s[HG], q[HG];
 #pragma unroll
-        for (int i = 0; i < HG; ++i) m[i] = m2[i] = make_float2(0.f, 0.f);
-        for (int v0 = 0; v0 < visits;) {
-            const int first = v0, stop = min(visits, v0 + kGnShiftRows);
-            float2 K[HG], s[HG], q[HG];
-#pragma unroll
-            for (int i = 0; i < HG; ++i) s[i] = q[i] = make_float2(0.f, 0.f);
-            for (; v0 < stop; v0 += U) {
-                typename X::Raw raw[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (v0 + u < stop) raw[u] = X::load(xp + u * step);
-                if (v0 == first) {
-#pragma unroll
-                    for (int i = 0; i < HG; ++i) {
-                        K[i] = X::get(raw[0], i);
-                        if (ONE && VEC > 1) K[i].y = K[i].x;
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (v0 + u < stop) {
-#pragma unroll
-                        for (int i = 0; i < X::H; ++i) {
-                            const int j = ONE ? 0 : i;
-                            const float2 d = f2_sub(X::get(raw[u], i), K[j]);
-                            s[j] = __fadd2_rn(s[j], d);
-                            q[j] = __ffma2_rn(d, d, q[j]);
-                        }
-                    }
-                xp += U * step;
-            }
-            v0 = stop;
-            // into the running state, relative to the group's first element
+        for (int i = 0; i < HG; ++i) m[i] = m2[i] = s[i] = q[i] = make_float2(0.f, 0.f);
+        auto merge = [&](int first, int stop) {
             const float n = static_cast<float>(first), kk = static_cast<float>(stop - first);
             float2 G0[HG];
             gn_per_group<T, VEC, ONE>(G0, c, a, [&](int g) { return gn_elem(xs + int64_t(g) * a.D); });
@@ -396,7 +364,28 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
                     gn_pair_merge(m[i].y, m2[i].y, (K[i].y - G0[i].y) + by.x, by.y, n, kk);
                 }
             }
-        }
+        };
+        const T* p[1] = {xs + (k * a.chunk_rows + w.r) * a.xr + c};
+        const int64_t step[1] = {int64_t(a.par) * a.xr};
+        GnStream<T, VEC, 1>::run(p, step, visits, ring, [&](int v, const auto& raw) {
+            if ((v & (kGnShiftRows - 1)) == 0) {
+                if (v > 0) merge(v - kGnShiftRows, v);
+#pragma unroll
+                for (int i = 0; i < HG; ++i) {
+                    K[i] = X::get(raw[0], i);
+                    if (ONE && VEC > 1) K[i].y = K[i].x;
+                    s[i] = q[i] = make_float2(0.f, 0.f);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < X::H; ++i) {
+                const int j = ONE ? 0 : i;
+                const float2 d = f2_sub(X::get(raw[0], i), K[j]);
+                s[j] = __fadd2_rn(s[j], d);
+                q[j] = __ffma2_rn(d, d, q[j]);
+            }
+        });
+        if (visits > 0) merge((visits - 1) & ~(kGnShiftRows - 1), visits);
         float2* mine = st + (w.r * a.tile + w.col) * segs;
         if constexpr (ONE)
             mine[0] = make_float2(m[0].x, m2[0].x);
@@ -435,9 +424,8 @@ struct GnSpan {
 
 // Output row chunk k of a tile.
 template <class T, int VEC, bool ONE, int ACT>
-__device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, int k, float2* sm) {
+__device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, int k, float2* sm, void* ring) {
     using X = GnVec<T, VEC>;
-    constexpr int U = 4;
     float2* fin = sm;                                   // (mu, rstd) per group of the tile
     float* shift = reinterpret_cast<float*>(sm + w.ng);
     const int c = w.c0 + w.col * VEC;
@@ -495,20 +483,14 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
     gn_per_group<T, VEC, ONE>(out.K, c, a, [&](int g) { return shift[min(g - w.g0, w.ng - 1)]; });
     out.init(rg, rb, c, a, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
     const int64_t row = k * a.out_rows + w.r;
-    const T* xp = static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c;
+    const T* p[1] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c};
+    const int64_t step[1] = {int64_t(a.par) * a.xr};
     T* yp = static_cast<T*>(a.y) + w.b * a.yb + row * a.yr + c;
-    const int64_t xstep = int64_t(a.par) * a.xr, ystep = int64_t(a.par) * a.yr;
-    for (int v = 0; v < visits; v += U) {
-        typename X::Raw raw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v + u < visits) raw[u] = X::load(xp + u * xstep);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v + u < visits) X::store(yp + u * ystep, out.apply(raw[u]));
-        xp += U * xstep;
-        yp += U * ystep;
-    }
+    const int64_t ystep = int64_t(a.par) * a.yr;
+    GnStream<T, VEC, 1>::run(p, step, visits, ring, [&](int, const auto& raw) {
+        X::store(yp, out.apply(raw[0]));
+        yp += ystep;
+    });
 }
 
 // One launch of the split path: some CTAs sum the row chunks of one band's
@@ -518,7 +500,8 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
 // SM has both.
 template <class T, int VEC, bool ONE, int ACT>
 __global__ void __launch_bounds__(kGnMaxThreads, ONE ? 2 : 1) gn_fwd_split(const GnArgs a) {
-    extern __shared__ float2 sm[];
+    extern __shared__ __align__(16) float2 slots[];  // the row stream's slots, then the merges' states
+    float2* sm = slots + GnStream<T, VEC, 1>::kRing / 8 * blockDim.x;
     grid_release();
     bool out;
     const int i = gn_role(blockIdx.x, a.out_ctas, a.sum_ctas, &out);
@@ -526,10 +509,10 @@ __global__ void __launch_bounds__(kGnMaxThreads, ONE ? 2 : 1) gn_fwd_split(const
         // last chunks first: what was summed last is the likeliest in L2
         const int id = a.out_ctas - 1 - i;
         const int unit = quot(id, a.by_out_chunks);
-        gn_fwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.out_unit + unit), id - unit * a.out_chunks, sm);
+        gn_fwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.out_unit + unit), id - unit * a.out_chunks, sm, slots);
     } else {
         const int unit = quot(i, a.by_chunks);
-        gn_fwd_sums<T, VEC, ONE>(a, gn_tile<VEC>(a, a.sum_unit + unit), i - unit * a.chunks, sm);
+        gn_fwd_sums<T, VEC, ONE>(a, gn_tile<VEC>(a, a.sum_unit + unit), i - unit * a.chunks, sm, slots);
     }
 }
 
@@ -563,7 +546,8 @@ cudaError_t gn_launch_fwd(const gn_plan& p, const GnArgs& a, norm_act act, int64
     const GnKernel k = act == NORM_ACT_SILU   ? gn_fwd_split<T, VEC, ONE, NORM_ACT_SILU>
                        : act == NORM_ACT_GELU ? gn_fwd_split<T, VEC, ONE, NORM_ACT_GELU>
                                               : gn_fwd_split<T, VEC, ONE, NORM_ACT_NONE>;
-    return gn_launch_bands(reinterpret_cast<const void*>(k), p, a, units, 0, smem, s);
+    return gn_launch_bands(reinterpret_cast<const void*>(k), p, a, units, 0,
+                           smem + static_cast<size_t>(GnStream<T, VEC, 1>::kRing) * p.threads, s);
 }
 
 template <class T>

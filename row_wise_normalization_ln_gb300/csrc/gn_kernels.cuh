@@ -274,6 +274,102 @@ __device__ __forceinline__ float2 gn_peer(const float2* p, int i, uint32_t rank)
     return v;
 }
 
+// ------------------------------------------------------------ row streams
+// Walks a thread's rows of N tensors with the next rows' accesses in flight:
+// every thread copies its own accesses asynchronously into slots of shared
+// memory of its own (no barrier: a thread waits for its own copies only),
+// kRows rows ahead, which costs no registers while they travel. A slot is
+// refilled one step after it was read. Accesses of one 16-bit value, which
+// asynchronous copies do not have, are loaded kBatch rows at a time instead.
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+template <class T, int VEC, int N>
+struct GnStream {
+    using X = GnVec<T, VEC>;
+    using Raw = typename X::Raw;
+    static constexpr int kBytes = VEC * static_cast<int>(sizeof(T));
+    static constexpr bool kAsync = kBytes >= 4;
+    static constexpr int kStep = 2, kSteps = 4;  // rows per step, steps in the ring
+    static constexpr int kBatch = 4;
+    static constexpr int kRing = kAsync ? kStep * kSteps * N * kBytes : 0;  // bytes per thread
+
+    // Calls f(v, raw) for rows v = 0 .. visits - 1 in order; row v of tensor
+    // n is at p[n] + v * step[n].
+    template <class F>
+    static __device__ __forceinline__ void run(const T* (&p)[N], const int64_t (&step)[N], int visits, void* ring, F f) {
+        if constexpr (kAsync) {
+            const uint32_t pitch = blockDim.x * kBytes;  // between a thread's slots
+            const uint32_t base = smem_addr(ring) + threadIdx.x * kBytes;
+            int sent = 0;  // rows whose copies have been issued
+            auto send = [&](int slot) {
+#pragma unroll
+                for (int u = 0; u < kStep; ++u) {
+                    if (sent < visits) {
+#pragma unroll
+                        for (int n = 0; n < N; ++n) {
+                            copy_async<kBytes>(base + ((slot * kStep + u) * N + n) * pitch, p[n]);
+                            p[n] += step[n];
+                        }
+                    }
+                    ++sent;
+                }
+                copy_async_commit();
+            };
+#pragma unroll
+            for (int s = 0; s < kSteps - 1; ++s) send(s);
+            int slot = 0;
+            for (int v = 0; v < visits; v += kStep) {
+                copy_async_wait<kSteps - 2>();  // this step's copies have landed
+                Raw raw[kStep][N];
+#pragma unroll
+                for (int u = 0; u < kStep; ++u)
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        const uint32_t at = base + ((slot * kStep + u) * N + n) * pitch;
+                        if constexpr (kBytes == 16)
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(raw[u][n].x), "=r"(raw[u][n].y), "=r"(raw[u][n].z), "=r"(raw[u][n].w)
+                                         : "r"(at)
+                                         : "memory");
+                        else
+                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(raw[u][n]) : "r"(at) : "memory");
+                    }
+                // the slots read one step ago
+                send((slot + kSteps - 1) & (kSteps - 1));
+                slot = (slot + 1) & (kSteps - 1);
+#pragma unroll
+                for (int u = 0; u < kStep; ++u)
+                    if (v + u < visits) f(v + u, raw[u]);
+            }
+        } else {
+            for (int v = 0; v < visits; v += kBatch) {
+                Raw raw[kBatch][N];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (v + u < visits)
+#pragma unroll
+                        for (int n = 0; n < N; ++n) raw[u][n] = X::load(p[n] + u * step[n]);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (v + u < visits) f(v + u, raw[u]);
+#pragma unroll
+                for (int n = 0; n < N; ++n) p[n] += kBatch * step[n];
+            }
+        }
+    }
+};
+
 // The part of a split launch this CTA takes: writing (`out`) and summing CTAs
 // alternate while both are left; `i` counts both. Returns the number of the
 // CTA among its kind.
@@ -288,11 +384,33 @@ __device__ __forceinline__ int gn_role(int i, int out_ctas, int sum_ctas, bool* 
 }
 
 // ------------------------------------------------------------ launch
+// Opts a kernel in to the device's largest dynamic shared memory per block
+// (once per kernel and device; not a stream operation).
+inline cudaError_t gn_opt_in(const void* fn) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, bool> done;
+    int dev = 0, most = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count({fn, dev})) return cudaSuccess;
+    e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, fn);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most - static_cast<int>(fa.sharedSizeBytes));
+    if (e == cudaSuccess) done[{fn, dev}] = true;
+    return e;
+}
+
 // A kernel on `grid` CTAs in clusters of `cluster`, with programmatic stream
-// serialization like every kernel of the library. The dynamic shared memory
-// of these kernels stays below 48 KB (the plan check sees to it).
+// serialization like every kernel of the library.
 inline cudaError_t gn_launch(const void* fn, int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream,
                              const GnArgs& a) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = gn_opt_in(fn);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
