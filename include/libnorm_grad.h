@@ -25,13 +25,13 @@ typedef struct {
 
 /*
  * norm = sqrt(sum over all tensors of v^2), one fp32 value in device memory.
- * Squares are added in fp32 over at most 64 values per thread, and in fp64
- * beyond; where fp32 squares leave the range (values above 2^63 or sums
- * below 2^-80) the tensor's part is summed again in fp64, so the norm is
- * right wherever it fits fp32, infinite or NaN where a value is. A tensor
+ * Squares are added in fp32 over at most 1024 values (in chains of at most
+ * 16 and trees) and in fp64 beyond; where fp32 squares leave the range (values
+ * above 2^63 or sums below 2^-80) that part is summed again in fp64, so the
+ * norm is right wherever it fits fp32, infinite or NaN where a value is. A tensor
  * that is listed twice counts twice. No tensors (or only empty ones): 0.
  * `workspace`: 8-byte aligned device memory of the caller, at least
- * grad_workspace_bytes(); nothing in it needs a value before the call. Calls
+ * grad_workspace_bytes() (may be NULL when that is 0); nothing in it needs a value before the call. Calls
  * that share a workspace must not overlap on the GPU. The sums are added in a
  * fixed order: the same tensors give the same bits on one device.
  */
@@ -50,9 +50,10 @@ norm_status grad_norm(const norm_tensor* tensors, int64_t count, float* norm, vo
 norm_status grad_clip(const norm_tensor* tensors, int64_t count, float max_norm, float* norm, void* workspace,
                       size_t workspace_bytes, cudaStream_t stream);
 
-/* Workspace bytes for `count` tensors on a device with `num_sms` SMs. Host
- * only: makes no CUDA call. */
-norm_status grad_workspace_bytes(int64_t count, int num_sms, size_t* bytes);
+/* Workspace bytes for these tensors on a device with `num_sms` SMs, by their
+ * sizes, types and number (a short list needs none). Host only: makes no CUDA
+ * call. */
+norm_status grad_workspace_bytes(const norm_tensor* tensors, int64_t count, int num_sms, size_t* bytes);
 
 #ifdef __cplusplus
 }

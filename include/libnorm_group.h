@@ -47,7 +47,7 @@ typedef struct {
     int32_t path;       /* gn_path */
     int32_t vec_elems;  /* channels per access: 16 / sizeof(element), 2 (16-bit types) or 1 */
     int32_t tile;       /* accesses per row a CTA covers: whole groups for GN_PATH_CHIP */
-    int32_t threads;    /* threads per CTA, a multiple of 32, tile <= threads <= 512 */
+    int32_t threads;    /* threads per CTA, a multiple of 32, tile <= threads <= 256 */
     int32_t per_thread; /* CHIP: rows each thread holds, 1, 2, 4 or 8 (backward: up to 4) */
     int32_t cluster;    /* CHIP: the CTAs that share a sample's tile, 1, 2, 4 or 8; SPLIT: 1 */
     int32_t chunks;     /* SPLIT: row chunks per sample and tile that are summed */

@@ -139,7 +139,7 @@ def library() -> ctypes.CDLL:
     L.gn_workspace_bytes.argtypes = [i64, i64, i64, i64, i32, i32, i32, gp, ctypes.POINTER(sz)]
     L.grad_norm.argtypes = [vp, i64, vp, vp, sz, vp]
     L.grad_clip.argtypes = [vp, i64, f32, vp, vp, sz, vp]
-    L.grad_workspace_bytes.argtypes = [i64, i32, ctypes.POINTER(sz)]
+    L.grad_workspace_bytes.argtypes = [vp, i64, i32, ctypes.POINTER(sz)]
     for f in ("gn_fwd", "gn_bwd", "gn_fwd_planned", "gn_bwd_planned", "gn_make_plan", "gn_workspace_bytes",
               "grad_norm", "grad_clip", "grad_workspace_bytes"):
         getattr(L, f).restype = ctypes.c_int

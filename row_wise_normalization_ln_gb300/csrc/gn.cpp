@@ -175,6 +175,10 @@ bool chip_plan(const Shape& s, int vec, int sms, gn_plan* p) {
         int v = 1;
         while (v <= maxv && ceil_div(rows, v) * tile > kGnMaxThreads) v *= 2;
         if (v > maxv) continue;
+        // a backward whose samples do not meet in one cluster needs another
+        // launch for the column sums, and clusters then lose to the split path
+        // (gn_bwd f32 3x1517x180 13 us against 10)
+        if (s.bwd && cs > 1 && s.B * cs > kMaxCluster) break;
         if (found && (rows * tile < 256 || units * cs > 4 * int64_t(sms))) break;
         p->path = GN_PATH_CHIP;
         p->vec_elems = vec;
@@ -190,7 +194,7 @@ bool chip_plan(const Shape& s, int vec, int sms, gn_plan* p) {
 
 void split_plan(const Shape& s, int vec, int sms, gn_plan* p) {
     const int es = elem_size(s.dtype);
-    const int64_t ncols = s.C / vec, unit = group_unit(s.D, vec), cap = std::min<int64_t>(tile_cap(s, vec), 256);
+    const int64_t ncols = s.C / vec, unit = group_unit(s.D, vec), cap = tile_cap(s, vec);
     // tiles of at least 128 bytes of a row, whole groups
     int64_t tile = std::min(ncols, cap);
     if (unit <= cap) tile = std::min(tile, unit * std::max<int64_t>(1, ceil_div(128, unit * vec * es)));
@@ -204,9 +208,15 @@ void split_plan(const Shape& s, int vec, int sms, gn_plan* p) {
     const int64_t bytes = s.B * s.S * s.C * es * (s.bwd ? 2 : 1);
     p->bands = static_cast<int32_t>(std::min<int64_t>(units, std::max<int64_t>(1, bytes / kBandBytes)));
     const int64_t per_band = ceil_div(units, p->bands);
-    const int64_t most = std::max<int64_t>(1, s.S / (p->threads / tile * 4));
-    const int64_t chunks = std::max<int64_t>(1, std::min(most, int64_t(sms) * 2 / per_band));
-    p->chunks = p->out_chunks = static_cast<int32_t>(std::max(chunks, ceil_div(s.S, int64_t(1) << 30)));
+    // Two CTAs per SM; one where that leaves a thread fewer than 8 rows (the
+    // merges then cost more than the rows: gn_fwd bf16 2x4096x320 9.6 us with
+    // 152 CTAs, 12.0 with 304; gn_bwd f16 8x4096x320, 18 rows each, 23 us with
+    // 288 and 28 with 152).
+    const int64_t rows = p->threads / tile;
+    const int64_t chunks = std::min(int64_t(sms) * 2 / per_band, std::max(int64_t(sms) / per_band, s.S / (rows * 8)));
+    const int64_t most = std::max<int64_t>(1, ceil_div(s.S, rows));
+    p->chunks = p->out_chunks =
+        static_cast<int32_t>(std::max(std::min(std::max<int64_t>(1, chunks), most), ceil_div(s.S, int64_t(1) << 30)));
 }
 
 // The plan for accesses of `vec` elements.

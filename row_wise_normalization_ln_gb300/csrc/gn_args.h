@@ -10,7 +10,7 @@
 
 namespace libnorm {
 
-constexpr int kGnMaxThreads = 512;
+constexpr int kGnMaxThreads = 256;
 // Channels of a tile whose accesses span groups (their sums are kept per
 // channel): bounds the shared memory of the reductions.
 constexpr int kGnMaxMixedChannels = 512;

@@ -295,17 +295,23 @@ __device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, in
         const int64_t step[2] = {int64_t(a.par) * a.xr, int64_t(a.par) * a.dyr};
         GnBwdCh<T, VEC, ONE, ACT> ch;
         ch.init(a, w.b, c);
-        float2 t1[X::H], t2[X::H], s1[X::H], s2[X::H];
+        // full blocks of rows are added up in the row slot's states
+        float2 s1[X::H], s2[X::H];
+        float2* mine = st + w.r * stride + w.col;
+        auto fold = [&](bool first) {
 #pragma unroll
-        for (int i = 0; i < X::H; ++i) t1[i] = t2[i] = s1[i] = s2[i] = make_float2(0.f, 0.f);
+            for (int j = 0; j < VEC; ++j) {
+                const float2 t = make_float2((j & 1) ? s1[j / 2].y : s1[j / 2].x, (j & 1) ? s2[j / 2].y : s2[j / 2].x);
+                mine[j * a.tile] = first ? t : __fadd2_rn(mine[j * a.tile], t);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < X::H; ++i) s1[i] = s2[i] = make_float2(0.f, 0.f);
         GnStream<T, VEC, 2>::run(p, step, visits, ring, [&](int v, const auto& raw) {
-            if ((v & (kGnSumRows - 1)) == 0) {
+            if (v > 0 && (v & (kGnSumRows - 1)) == 0) {
+                fold(v == kGnSumRows);
 #pragma unroll
-                for (int i = 0; i < X::H; ++i) {
-                    t1[i] = __fadd2_rn(t1[i], s1[i]);
-                    t2[i] = __fadd2_rn(t2[i], s2[i]);
-                    s1[i] = s2[i] = make_float2(0.f, 0.f);
-                }
+                for (int i = 0; i < X::H; ++i) s1[i] = s2[i] = make_float2(0.f, 0.f);
             }
 #pragma unroll
             for (int i = 0; i < X::H; ++i) {
@@ -315,12 +321,7 @@ __device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, in
                 s2[i] = __ffma2_rn(dz, d, s2[i]);
             }
         });
-#pragma unroll
-        for (int i = 0; i < X::H; ++i) {
-            t1[i] = __fadd2_rn(t1[i], s1[i]);
-            t2[i] = __fadd2_rn(t2[i], s2[i]);
-        }
-        gn_bwd_put<VEC>(st + w.r * stride, a.tile, w.col, t1, t2);
+        fold(visits <= kGnSumRows);
     }
     __syncthreads();
     gn_bwd_merge_threads<T, VEC>(a, w, st, stride, gs);
@@ -397,7 +398,7 @@ __device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, floa
 // One launch of the split path, as in the forward; the last one also adds
 // the partial rows of the column gradients, in its first CTAs.
 template <class T, int VEC, bool ONE, int ACT>
-__global__ void __launch_bounds__(kGnMaxThreads) gn_bwd_split(const GnArgs a) {
+__global__ void __launch_bounds__(kGnMaxThreads, 2) gn_bwd_split(const GnArgs a) {
     extern __shared__ __align__(16) float2 slots[];  // the row stream's slots, then the merges' states
     float2* sm = slots + GnStream<T, VEC, 2>::kRing / 8 * blockDim.x;
     grid_release();

@@ -312,7 +312,7 @@ constexpr int kGnShiftRows = 128;
 
 // The pairwise merge: (n, m, m2) += (k, mb, b2).
 __device__ __forceinline__ void gn_pair_merge(float& m, float& m2, float mb, float b2, float n, float k) {
-    const float wb = k / (n + k), d = mb - m;
+    const float wb = __fdividef(k, n + k), d = mb - m;
     m = fmaf(d, wb, m);
     m2 += fmaf(d * d, n * wb, b2);
 }
@@ -320,7 +320,7 @@ __device__ __forceinline__ void gn_pair_merge(float& m, float& m2, float mb, flo
 // sum and sum of squares of d over k values -> (mean, M2); the subtraction
 // can round below zero, and NaN stays NaN.
 __device__ __forceinline__ float2 gn_mean_m2(float s, float q, float k) {
-    const float m = s / k, b2 = fmaf(-s, m, q);
+    const float m = __fdividef(s, k), b2 = fmaf(-s, m, q);
     return make_float2(m, b2 < 0.f ? 0.f : b2);
 }
 
@@ -348,7 +348,7 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
         // relative to the group's first element.
         float2 m[HG], m2[HG], K[HG], s[HG], q[HG];
 #pragma unroll
-        for (int i = 0; i < HG; ++i) m[i] = m2[i] = s[i] = q[i] = make_float2(0.f, 0.f);
+        for (int i = 0; i < HG; ++i) m[i] = m2[i] = K[i] = s[i] = q[i] = make_float2(0.f, 0.f);
         auto merge = [&](int first, int stop) {
             const float n = static_cast<float>(first), kk = static_cast<float>(stop - first);
             float2 G0[HG];
@@ -499,7 +499,7 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
 // it busy in both directions. The two kinds of CTAs alternate so that each
 // SM has both.
 template <class T, int VEC, bool ONE, int ACT>
-__global__ void __launch_bounds__(kGnMaxThreads, ONE ? 2 : 1) gn_fwd_split(const GnArgs a) {
+__global__ void __launch_bounds__(kGnMaxThreads, ONE ? 4 : 3) gn_fwd_split(const GnArgs a) {
     extern __shared__ __align__(16) float2 slots[];  // the row stream's slots, then the merges' states
     float2* sm = slots + GnStream<T, VEC, 1>::kRing / 8 * blockDim.x;
     grid_release();

@@ -1,23 +1,25 @@
 // The global norm of a list of gradients, and clipping by it.
 //
-//   grad_sums    every CTA adds the squares of its share of the values and
-//                leaves one fp64 partial sum.
+//   grad_sums    every team of 256 threads adds the squares of its share of
+//                the values, every CTA leaves one fp64 partial sum.
 //   grad_finish  one CTA adds the partial sums: the norm.
 //   grad_scale   every CTA adds the partial sums itself (the same bits in
 //                each) and multiplies its share by the coefficient.
+//   grad_small   one CTA does it all for short lists, in one launch.
 //
-// Both kernels stream: each value is read once per kernel, which is all the
+// The kernels stream: each value is read once per pass, which is all the
 // arithmetic needs (bound: HBM). The list is cut into units of one 16-byte
-// access per thread; CTA i takes the units [U i / G, U (i + 1) / G), so the
-// shares differ by one unit at most however the sizes are mixed, and a share
-// is a run of neighbouring addresses but for the steps between tensors. The
-// scale kernel walks its shares from the end: what a CTA of the sums kernel
-// read last is what L2 still holds.
+// access per thread of a team; team i of G takes the units
+// [U i / G, U (i + 1) / G), so the shares differ by one unit at most however
+// the sizes are mixed, and a share is a run of neighbouring addresses but for
+// the steps between tensors. The scaling walks its shares from the end: what
+// a team read last for the sums is what L2 still holds.
 //
 // The table of tensors travels in the kernel's argument block (up to 960
 // tensors per launch), so nothing is copied to the device and a captured
 // graph holds its own.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <memory>
@@ -33,7 +35,10 @@
 namespace libnorm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;          // of a team
+constexpr int kSmallTeams = 4;         // of the one CTA of grad_small
+constexpr int kSmallUnits = 64;        // the longest list it takes: 256 KB
+constexpr int kSmallTensors = 64;      // and the most tensors
 constexpr int kUnroll = 8;             // accesses per thread in flight
 constexpr int kUnitBytes = kThreads * 16;
 constexpr int kCtasPerSm = 4;
@@ -48,6 +53,7 @@ struct GradTable {
     uint8_t dtype[CAP];
     int32_t count;
 };
+static_assert(kThreads * kSmallTeams == 1024, "grad_small sums its 32 warps in one");
 static_assert(sizeof(GradTable<kMaxTable>) + 64 <= 32764, "kernel arguments: 32764 bytes");
 
 // A tensor's values: the few before the first 16-byte boundary, whole
@@ -113,22 +119,27 @@ __device__ __forceinline__ float2 add_squares(const uint4& r, float2 acc) {
     return acc;
 }
 
+// The squares of n accesses, kThreads apart from v on, in fp64: the values
+// are read again, so that the usual path holds no registers for this one.
 template <int DT>
-__device__ __noinline__ double exact_squares(const uint4* r, int n) {
+__device__ __noinline__ double exact_squares(const uint4* v, int n) {
     double s = 0.0;
-    for (int k = 0; k < n; ++k)
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+        const uint4 r = v[k * kThreads];
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-            const uint32_t w = word(r[k], i);
+            const uint32_t w = word(r, i);
             if constexpr (DT == NORM_F32) {
-                const double v = __uint_as_float(w);
-                s = fma(v, v, s);
+                const double x = __uint_as_float(w);
+                s = fma(x, x, s);
             } else {
                 const float2 p = DT == NORM_BF16 ? Bf16Pair::widen(w) : F16Pair::widen(w);
-                const double x = p.x, y = p.y;
-                s = fma(x, x, s);
-                s = fma(y, y, s);
+                s = fma(static_cast<double>(p.x), static_cast<double>(p.x), s);
+                s = fma(static_cast<double>(p.y), static_cast<double>(p.y), s);
             }
         }
+    }
     return s;
 }
 
@@ -138,27 +149,25 @@ __device__ __noinline__ double exact_squares(const uint4* r, int n) {
 // below 2^-60 of the sum.
 constexpr float kSmallSum = 8.27180613e-25f;  // 2^-80
 
+// The squares of the n accesses r (the rest zero), kThreads apart from v on.
+// (Accesses that a thread does not have are set, not skipped: a register that
+// is written under a predicate alone stays live through the whole loop, which
+// tripled the registers.)
 template <int DT>
-__device__ __forceinline__ double squares(const uint4 (&r)[kUnroll], int n) {
+__device__ __forceinline__ double squares(const uint4 (&r)[kUnroll], int n, const uint4* v) {
     float2 a = make_float2(0.f, 0.f), b = a;
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
-        if (k < n) {
-            if (k & 1) b = add_squares<DT>(r[k], b);
-            else a = add_squares<DT>(r[k], a);
-        }
+    for (int k = 0; k < kUnroll; ++k) {
+        if (k & 1) b = add_squares<DT>(r[k], b);
+        else a = add_squares<DT>(r[k], a);
+    }
     const float s = (a.x + a.y) + (b.x + b.y);
     if (!(s >= kSmallSum && s <= 3.0e38f)) {
         uint32_t any = 0;
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
-            if (k < n) any |= r[k].x | r[k].y | r[k].z | r[k].w;
-        if (any != 0) {
-            uint4 copy[kUnroll];
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) copy[k] = r[k];
-            return exact_squares<DT>(copy, n);
-        }
+            any |= r[k].x | r[k].y | r[k].z | r[k].w;
+        if (any != 0) return exact_squares<DT>(v, n);
     }
     return static_cast<double>(s);
 }
@@ -168,86 +177,118 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// Sum over the CTA, the same bits in every thread.
+// Sum over a CTA, in thread 0 (elsewhere undefined).
 __device__ __forceinline__ double cta_sum(double v, double* part) {
     v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) s += part[i];
-    return s;
+    const int warps = blockDim.x >> 5;
+    if (threadIdx.x >= 32) return 0.0;
+    return warp_sum(static_cast<int>(threadIdx.x) < warps ? part[threadIdx.x] : 0.0);
+}
+
+// sqrt(s) by one Newton step in fp64 from fp32's root (48 bits or more):
+// the device's fp64 unit is a sixty-fourth of its fp32 ones, and its root and
+// division took longer than a short list's memory.
+__device__ __forceinline__ double root(double s) {
+    if (!(s > 1e-30 && s < 1e30)) return sqrt(s);  // outside fp32's reach: rare
+    const float r = sqrtf(static_cast<float>(s));
+    const double y = r;
+    return fma(fma(-y, y, s), static_cast<double>(0.5f / r), y);
+}
+
+// The coefficient of a norm, rounded once; NaN from a NaN norm.
+__device__ __forceinline__ float coef_of(float max_norm, double norm) {
+    const double d = norm + 1e-6, m = max_norm;
+    if (!(d < 1e30)) return static_cast<float>(m / d);  // infinite, NaN or beyond fp32's reach
+    const float r = 1.f / static_cast<float>(d);
+    const double c0 = m * static_cast<double>(r), c = fma(fma(-c0, d, m), static_cast<double>(r), c0);
+    return c > 1.0 ? 1.f : static_cast<float>(c);
+}
+
+// How many of the next kUnroll accesses, kThreads apart, there are for a
+// thread with `left` accesses from its first one to the tensor's end, in
+// `units` units.
+__device__ __forceinline__ int accesses(int64_t left, int64_t units) {
+    const int64_t n = left <= 0 ? 0 : min(units, (left + kThreads - 1) / kThreads);
+    return n < kUnroll ? static_cast<int>(n) : kUnroll;
 }
 
 // The units [u, stop) of one tensor: squares of this thread's values.
 template <int DT>
-__device__ __forceinline__ double piece_squares(const void* p, int64_t numel, int64_t u, int64_t stop, int64_t units) {
+__device__ __forceinline__ double piece_squares(const void* p, int64_t numel, int64_t u, int64_t stop, int64_t units, int tid) {
     const Span s = span_of(p, numel, DT == NORM_F32 ? 4 : 2);
     const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + s.head * (DT == NORM_F32 ? 4 : 2));
     double sum = 0.0;
-    if (u == 0 && static_cast<int64_t>(threadIdx.x) < s.head) {
-        const double x = value_at(p, threadIdx.x, DT);
+    if (u == 0 && tid < s.head) {
+        const double x = value_at(p, tid, DT);
         sum = fma(x, x, sum);
     }
     const int64_t tail = s.head + s.vecs * s.per;
-    if (stop == units && tail + static_cast<int64_t>(threadIdx.x) < numel) {
-        const double x = value_at(p, tail + threadIdx.x, DT);
+    if (stop == units && tail + tid < numel) {
+        const double x = value_at(p, tail + tid, DT);
         sum = fma(x, x, sum);
     }
+#pragma unroll 1
     for (; u < stop; u += kUnroll) {
+        const uint4* at = v + u * kThreads + tid;
+        const int n = accesses(s.vecs - u * kThreads - tid, stop - u);
         uint4 r[kUnroll];
-        int n = 0;
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int64_t i = (u + k) * kThreads + threadIdx.x;
-            if (u + k < stop && i < s.vecs) {
-                r[k] = v[i];
-                n = k + 1;
-            }
+        for (int k = 0; k < kUnroll; ++k)
+            r[k] = k < n ? at[k * kThreads] : make_uint4(0, 0, 0, 0);
+        if (n > 0) sum += squares<DT>(r, n, at);
+    }
+    return sum;
+}
+
+// Share i of n of the list: the sum of squares of this thread's values.
+template <int CAP>
+__device__ __forceinline__ double share_squares(const GradTable<CAP>& t, int64_t i, int64_t n, int tid) {
+    const int64_t all = t.first[t.count];
+    int64_t u = all * i / n;
+    const int64_t end = all * (i + 1) / n;
+    double sum = 0.0;
+    if (u < end) {
+#pragma unroll 1
+        for (int k = tensor_of(t, u); u < end; ++k) {
+            const int64_t first = t.first[k], units = t.first[k + 1] - first;
+            if (units == 0) continue;
+            const int64_t a = u - first, b = min(units, end - first);
+            const void* p = t.data[k];
+            const int dt = t.dtype[k];
+            if (dt == NORM_F32) sum += piece_squares<NORM_F32>(p, t.numel[k], a, b, units, tid);
+            else if (dt == NORM_BF16) sum += piece_squares<NORM_BF16>(p, t.numel[k], a, b, units, tid);
+            else sum += piece_squares<NORM_F16>(p, t.numel[k], a, b, units, tid);
+            u = first + b;
         }
-        if (n > 0) sum += squares<DT>(r, n);
     }
     return sum;
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) grad_sums(const __grid_constant__ GradTable<CAP> t, double* partial) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_sums(const __grid_constant__ GradTable<CAP> t,
+                                                                  double* partial) {
     __shared__ double part[kThreads / 32];
     grid_release();
     grid_wait();
-    const int64_t all = t.first[t.count];
-    int64_t u = all * blockIdx.x / gridDim.x;
-    const int64_t end = all * (blockIdx.x + 1ll) / gridDim.x;
-    double sum = 0.0;
-    if (u < end) {
-        for (int i = tensor_of(t, u); u < end; ++i) {
-            const int64_t first = t.first[i], units = t.first[i + 1] - first;
-            if (units == 0) continue;
-            const int64_t a = u - first, b = min(units, end - first);
-            const void* p = t.data[i];
-            const int dt = t.dtype[i];
-            if (dt == NORM_F32) sum += piece_squares<NORM_F32>(p, t.numel[i], a, b, units);
-            else if (dt == NORM_BF16) sum += piece_squares<NORM_BF16>(p, t.numel[i], a, b, units);
-            else sum += piece_squares<NORM_F16>(p, t.numel[i], a, b, units);
-            u = first + b;
-        }
-    }
-    sum = cta_sum(sum, part);
+    const double sum = cta_sum(share_squares(t, blockIdx.x, gridDim.x, threadIdx.x), part);
     if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-__device__ __forceinline__ double sum_partials(const double* partial, int64_t n, double* part) {
+// The sum of the n partial sums, in every lane of the one warp that calls it.
+__device__ __forceinline__ double sum_partials(const double* partial, int64_t n) {
     double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) s += partial[i];
-    return cta_sum(s, part);
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < n; i += 32) s += partial[i];
+    return warp_sum(s);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_finish(const double* partial, int64_t n, float* norm) {
-    __shared__ double part[kThreads / 32];
+__global__ void __launch_bounds__(32) grad_finish(const double* partial, int64_t n, float* norm) {
     grid_release();
     grid_wait();
-    const double s = sum_partials(partial, n, part);
-    if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(s));
+    const double s = sum_partials(partial, n);
+    if (threadIdx.x == 0) *norm = static_cast<float>(root(s));
 }
 
 template <int DT>
@@ -269,74 +310,248 @@ __device__ __forceinline__ uint4 scaled(const uint4& r, float coef) {
 // The units [u, stop) of one tensor, from the last to the first.
 template <int DT>
 __device__ __forceinline__ void piece_scale(const void* p, void* out, int64_t numel, int64_t u, int64_t stop,
-                                            int64_t units, float coef) {
+                                            int64_t units, float coef, int tid) {
     constexpr int es = DT == NORM_F32 ? 4 : 2;
     const Span s = span_of(p, numel, es);
     const int64_t tail = s.head + s.vecs * s.per;
-    if (u == 0 && static_cast<int64_t>(threadIdx.x) < s.head)
-        put_at(out, threadIdx.x, DT, value_at(p, threadIdx.x, DT) * coef);
-    if (stop == units && tail + static_cast<int64_t>(threadIdx.x) < numel)
-        put_at(out, tail + threadIdx.x, DT, value_at(p, tail + threadIdx.x, DT) * coef);
+    if (u == 0 && tid < s.head)
+        put_at(out, tid, DT, value_at(p, tid, DT) * coef);
+    if (stop == units && tail + tid < numel)
+        put_at(out, tail + tid, DT, value_at(p, tail + tid, DT) * coef);
     if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
-        // out lies at another offset within 16 bytes: value by value
+        // out lies at another offset within 16 bytes: value by value, kUnroll
+        // of them in flight per thread, neighbours side by side
         const int64_t lo = s.head + min(s.vecs, u * kThreads) * s.per, hi = s.head + min(s.vecs, stop * kThreads) * s.per;
-        for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) put_at(out, i, DT, value_at(p, i, DT) * coef);
+#pragma unroll 1
+        for (int64_t i = lo + tid; i < hi; i += kUnroll * kThreads) {
+            const int n = accesses(hi - i, kUnroll);
+            const void* from = static_cast<const char*>(p) + i * es;
+            void* to = static_cast<char*>(out) + i * es;
+            float r[kUnroll];
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+                r[k] = k < n ? value_at(from, k * kThreads, DT) : 0.f;
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+                if (k < n) put_at(to, k * kThreads, DT, r[k] * coef);
+        }
         return;
     }
     const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + s.head * es);
     uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(out) + s.head * es);
+#pragma unroll 1
     for (int64_t e = stop; e > u; e -= kUnroll) {
+        const int64_t f = max(u, e - kUnroll);
+        const int64_t i = f * kThreads + tid;
+        const int n = accesses(s.vecs - i, e - f);
         uint4 r[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int64_t i = (e - 1 - k) * kThreads + threadIdx.x;
-            if (e - 1 - k >= u && i < s.vecs) r[k] = v[i];
-        }
+        for (int k = 0; k < kUnroll; ++k)
+            r[k] = k < n ? v[i + k * kThreads] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int64_t i = (e - 1 - k) * kThreads + threadIdx.x;
-            if (e - 1 - k >= u && i < s.vecs) o[i] = scaled<DT>(r[k], coef);
-        }
+        for (int k = 0; k < kUnroll; ++k)
+            if (k < n) o[i + k * kThreads] = scaled<DT>(r[k], coef);
     }
 }
 
-// norm: written by the first launch's first CTA only (null elsewhere).
+// Share i of n of the list, from its end: times coef.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) grad_scale(const __grid_constant__ GradTable<CAP> t, const double* partial,
-                                                       int64_t n, float max_norm, float* norm) {
-    __shared__ double part[kThreads / 32];
-    grid_release();
-    grid_wait();
-    const double total = sqrt(sum_partials(partial, n, part));
-    if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
-    // in fp64, rounded once; a NaN norm gives a NaN coefficient
-    const double c = static_cast<double>(max_norm) / (total + 1e-6);
-    const float coef = c > 1.0 ? 1.f : static_cast<float>(c);
+__device__ __forceinline__ void share_scale(const GradTable<CAP>& t, int64_t i, int64_t n, float coef, int tid) {
     const int64_t all = t.first[t.count];
-    const int64_t begin = all * blockIdx.x / gridDim.x;
-    int64_t e = all * (blockIdx.x + 1ll) / gridDim.x;
+    const int64_t begin = all * i / n;
+    int64_t e = all * (i + 1) / n;
     if (begin >= e) return;
-    for (int i = tensor_of(t, e - 1); e > begin; --i) {
-        const int64_t first = t.first[i], units = t.first[i + 1] - first;
+#pragma unroll 1
+    for (int k = tensor_of(t, e - 1); e > begin; --k) {
+        const int64_t first = t.first[k], units = t.first[k + 1] - first;
         if (units == 0) continue;
         const int64_t a = max(begin - first, int64_t(0)), b = e - first;
-        const void* p = t.data[i];
-        void* o = t.out[i];
+        const void* p = t.data[k];
+        void* o = t.out[k];
         // x * 1 is x: in place there is nothing to do
         if (!(coef == 1.f && p == o)) {
-            const int dt = t.dtype[i];
-            if (dt == NORM_F32) piece_scale<NORM_F32>(p, o, t.numel[i], a, b, units, coef);
-            else if (dt == NORM_BF16) piece_scale<NORM_BF16>(p, o, t.numel[i], a, b, units, coef);
-            else piece_scale<NORM_F16>(p, o, t.numel[i], a, b, units, coef);
+            const int dt = t.dtype[k];
+            if (dt == NORM_F32) piece_scale<NORM_F32>(p, o, t.numel[k], a, b, units, coef, tid);
+            else if (dt == NORM_BF16) piece_scale<NORM_BF16>(p, o, t.numel[k], a, b, units, coef, tid);
+            else piece_scale<NORM_F16>(p, o, t.numel[k], a, b, units, coef, tid);
         }
         e = first + a;
     }
 }
 
-cudaError_t launch(const void* fn, int64_t grid, cudaStream_t stream, void** args) {
+// norm: written by the first launch's first CTA only (null elsewhere).
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale(const __grid_constant__ GradTable<CAP> t,
+                                                                   const double* partial, int64_t n, float max_norm,
+                                                                   float* norm) {
+    __shared__ float coef;
+    grid_release();
+    grid_wait();
+    if (threadIdx.x < 32) {  // (one warp: fp64 is scarce)
+        const double total = root(sum_partials(partial, n));
+        if (threadIdx.x == 0) {
+            coef = coef_of(max_norm, total);
+            if (norm != nullptr && blockIdx.x == 0) *norm = static_cast<float>(total);
+        }
+    }
+    __syncthreads();
+    share_scale(t, blockIdx.x, gridDim.x, coef, threadIdx.x);
+}
+
+// ------------------------------------------------------------ short lists
+// One access of a tensor: values [j * per, (j + 1) * per), zeros past the end.
+template <int DT>
+__device__ __forceinline__ uint4 load_slot(const void* p, int64_t j, int64_t numel) {
+    constexpr int per = DT == NORM_F32 ? 4 : 8;
+    const int64_t at = j * per, left = numel - at;
+    if (left >= per && (reinterpret_cast<uintptr_t>(p) & 15) == 0) return static_cast<const uint4*>(p)[j];
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < per; ++i)
+        if (i < left) {
+            if constexpr (DT == NORM_F32) w[i] = static_cast<const uint32_t*>(p)[at + i];
+            else w[i / 2] |= uint32_t(static_cast<const unsigned short*>(p)[at + i]) << (16 * (i & 1));
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int DT>
+__device__ __forceinline__ void store_slot(void* p, int64_t j, int64_t numel, const uint4& r) {
+    constexpr int per = DT == NORM_F32 ? 4 : 8;
+    const int64_t at = j * per, left = numel - at;
+    if (left >= per && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        static_cast<uint4*>(p)[j] = r;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < per; ++i)
+        if (i < left) {
+            if constexpr (DT == NORM_F32) static_cast<uint32_t*>(p)[at + i] = word(r, i);
+            else static_cast<unsigned short*>(p)[at + i] = static_cast<unsigned short>(word(r, i / 2) >> (16 * (i & 1)));
+        }
+}
+template <int DT>
+__device__ __forceinline__ float slot_squares(const uint4& r) {
+    const float2 a = add_squares<DT>(r, make_float2(0.f, 0.f));
+    return a.x + a.y;
+}
+
+// The whole of a list of at most kSmallTensors tensors and kSmallUnits units
+// in one CTA and one launch: the norm, and with CLIP the scaling. Its teams
+// take the units in turn, kInFlight at a time, so that a list of many small
+// tensors waits for memory once or twice.
+constexpr int kInFlight = 4;
+
+template <bool CLIP>
+__global__ void __launch_bounds__(kThreads* kSmallTeams) grad_small(const __grid_constant__ GradTable<kSmallTensors> t,
+                                                                    float max_norm, float* norm) {
+    __shared__ double part[kThreads * kSmallTeams / 32];
+    __shared__ float coefficient;
+    __shared__ int ends[kSmallTensors];  // the unit after each tensor's last
+    grid_release();
+    const int team = threadIdx.x / kThreads, tid = threadIdx.x & (kThreads - 1), lane = threadIdx.x & 31;
+    if (threadIdx.x < kSmallTensors)
+        ends[threadIdx.x] = threadIdx.x < t.count ? static_cast<int>(t.first[threadIdx.x + 1]) : 1 << 30;
+    __syncthreads();
+    const int all = static_cast<int>(t.first[t.count]);
+    // the tensor of a unit: how many end at or before it
+    auto tensor = [&](int u) {
+        int i = 0;
+#pragma unroll
+        for (int k = 0; k < kSmallTensors; k += 32) i += __popc(__ballot_sync(kFullMask, ends[k + lane] <= u));
+        return i;
+    };
+    auto first = [&](int i) { return i > 0 ? ends[i - 1] : 0; };
+    auto load = [&](int i, int64_t j) {
+        const int dt = t.dtype[i];
+        return dt == NORM_F32    ? load_slot<NORM_F32>(t.data[i], j, t.numel[i])
+               : dt == NORM_BF16 ? load_slot<NORM_BF16>(t.data[i], j, t.numel[i])
+                                 : load_slot<NORM_F16>(t.data[i], j, t.numel[i]);
+    };
+    grid_wait();
+    // fp32 over a warp's values of one round (1024 at most), fp64 beyond:
+    // the whole warp goes to fp64 where a lane's or the warp's sum may have
+    // left fp32's range.
+    double sum = 0.0;  // lane 0
+#pragma unroll 1
+    for (int base = team; base < all; base += kSmallTeams * kInFlight) {
+        uint4 r[kInFlight];
+        int dt[kInFlight];
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) {
+            const int u = base + k * kSmallTeams;
+            const int i = tensor(min(u, all - 1));
+            dt[k] = t.dtype[i];
+            r[k] = u < all ? load(i, int64_t(u - first(i)) * kThreads + tid) : make_uint4(0, 0, 0, 0);
+        }
+        float s[kInFlight], v = 0.f;
+        bool lost = false;
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) {
+            s[k] = dt[k] == NORM_F32    ? slot_squares<NORM_F32>(r[k])
+                   : dt[k] == NORM_BF16 ? slot_squares<NORM_BF16>(r[k])
+                                        : slot_squares<NORM_F16>(r[k]);
+            lost |= !(s[k] >= kSmallSum) && (r[k].x | r[k].y | r[k].z | r[k].w) != 0;
+            v += s[k];
+        }
+        v = group_sum(v, 32);
+        if (__any_sync(kFullMask, lost) || !(v <= 3.0e38f)) {
+            double d = 0.0;
+#pragma unroll 1
+            for (int k = 0; k < kInFlight; ++k) {
+                const int u = base + k * kSmallTeams;
+                const int i = tensor(min(u, all - 1));
+                const uint4 w = u < all ? load(i, int64_t(u - first(i)) * kThreads + tid) : make_uint4(0, 0, 0, 0);
+                d += t.dtype[i] == NORM_F32    ? exact_squares<NORM_F32>(&w, 1)
+                     : t.dtype[i] == NORM_BF16 ? exact_squares<NORM_BF16>(&w, 1)
+                                               : exact_squares<NORM_F16>(&w, 1);
+            }
+            sum += warp_sum(d);
+        } else {
+            sum += static_cast<double>(v);
+        }
+    }
+    if (lane == 0) part[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const double total = root(warp_sum(part[lane]));
+        if (threadIdx.x == 0) {
+            *norm = static_cast<float>(total);
+            if constexpr (CLIP) coefficient = coef_of(max_norm, total);
+        }
+    }
+    if constexpr (CLIP) {
+        // (every thread scales the values that it read itself)
+        __syncthreads();
+        const float coef = coefficient;
+#pragma unroll 1
+        for (int base = team; base < all; base += kSmallTeams * kInFlight) {
+            uint4 r[kInFlight];
+            int at[kInFlight];
+#pragma unroll
+            for (int k = 0; k < kInFlight; ++k) {
+                const int u = base + k * kSmallTeams;
+                const int i = tensor(min(u, all - 1));
+                at[k] = u < all && !(coef == 1.f && t.data[i] == t.out[i]) ? i : -1;  // x * 1 is x
+                r[k] = at[k] >= 0 ? load(i, int64_t(u - first(i)) * kThreads + tid) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < kInFlight; ++k) {
+                const int i = at[k];
+                if (i < 0) continue;
+                const int64_t j = int64_t(base + k * kSmallTeams - first(i)) * kThreads + tid;
+                const int dt = t.dtype[i];
+                if (dt == NORM_F32) store_slot<NORM_F32>(t.out[i], j, t.numel[i], scaled<NORM_F32>(r[k], coef));
+                else if (dt == NORM_BF16) store_slot<NORM_BF16>(t.out[i], j, t.numel[i], scaled<NORM_BF16>(r[k], coef));
+                else store_slot<NORM_F16>(t.out[i], j, t.numel[i], scaled<NORM_F16>(r[k], coef));
+            }
+        }
+    }
+}
+
+cudaError_t launch(const void* fn, int64_t grid, int threads, cudaStream_t stream, void** args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -374,18 +589,37 @@ cudaError_t pass(const norm_tensor* ts, int64_t count, bool clip, int64_t ctas, 
     fill(&t, ts, count);
     if (!clip) {
         void* args[] = {&t, &partial};
-        return launch(reinterpret_cast<const void*>(grad_sums<CAP>), ctas, stream, args);
+        return launch(reinterpret_cast<const void*>(grad_sums<CAP>), ctas, kThreads, stream, args);
     }
     const int64_t grid = std::max<int64_t>(1, std::min(ctas, t.first[count]));
     const double* src = partial;
     void* args[] = {&t, &src, &n, &max_norm, &norm};
-    return launch(reinterpret_cast<const void*>(grad_scale<CAP>), grid, stream, args);
+    return launch(reinterpret_cast<const void*>(grad_scale<CAP>), grid, kThreads, stream, args);
 }
 
 cudaError_t any_pass(const norm_tensor* ts, int64_t count, bool clip, int64_t ctas, double* partial, int64_t n,
                      float max_norm, float* norm, cudaStream_t stream) {
     return count <= 64 ? pass<64>(ts, count, clip, ctas, partial, n, max_norm, norm, stream)
                        : pass<kMaxTable>(ts, count, clip, ctas, partial, n, max_norm, norm, stream);
+}
+
+cudaError_t small(const norm_tensor* ts, int64_t count, bool clip, float max_norm, float* norm, cudaStream_t stream) {
+    GradTable<kSmallTensors> t;
+    fill(&t, ts, count);
+    void* args[] = {&t, &max_norm, &norm};
+    const void* fn = clip ? reinterpret_cast<const void*>(grad_small<true>) : reinterpret_cast<const void*>(grad_small<false>);
+    return launch(fn, 1, kThreads * kSmallTeams, stream, args);
+}
+
+int64_t units_of(const norm_tensor* ts, int64_t count) {
+    int64_t u = 0;
+    for (int64_t i = 0; i < count; ++i) u += ceil_div(ts[i].numel * elem_size(ts[i].dtype), kUnitBytes);
+    return u;
+}
+
+// Lists that grad_small takes.
+bool is_short(const norm_tensor* ts, int64_t count) {
+    return count <= kSmallTensors && units_of(ts, count) <= kSmallUnits;
 }
 
 norm_status check_tensors(const norm_tensor* ts, int64_t count, bool clip) {
@@ -434,25 +668,38 @@ norm_status run(const norm_tensor* ts, int64_t count, bool clip, float max_norm,
     norm_status st = check_tensors(ts, count, clip);
     if (st != NORM_OK) return st;
     if (!norm || (clip && (!std::isfinite(max_norm) || max_norm < 0.f))) return NORM_ERR_ARG;
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 7u)) return NORM_ERR_ARG;
+    const bool shortlist = is_short(ts, count);
+    if (!shortlist && (!ws || (reinterpret_cast<uintptr_t>(ws) & 7u))) return NORM_ERR_ARG;
     if (clip && (st = check_apart(ts, count)) != NORM_OK) return st;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    static std::atomic<int> cache[64];
+    if (e == cudaSuccess && dev >= 0 && dev < 64) sms = cache[dev].load(std::memory_order_relaxed);
+    if (e == cudaSuccess && sms <= 0) {
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess && dev >= 0 && dev < 64) cache[dev].store(sms, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess) {
         note_cuda_error(static_cast<int>(e));
         return NORM_ERR_CUDA;
     }
     size_t need = 0;
-    grad_workspace_bytes(count, sms, &need);
+    grad_workspace_bytes(ts, count, sms, &need);
     if (ws_bytes < need) return NORM_ERR_ARG;
+    // Short lists: one launch and no workspace (24 tensors of 1024 fp32 values,
+    // on the host and the GPU: 3.8 and 4.5 us against 5.1 and 4.8 with two).
+    if (shortlist) {
+        e = small(ts, count, clip, max_norm, norm, stream);
+        if (e == cudaSuccess) return NORM_OK;
+        note_cuda_error(static_cast<int>(e));
+        return NORM_ERR_CUDA;
+    }
     double* partial = static_cast<double*>(ws);
     const int64_t most = int64_t(sms) * kCtasPerSm;
     int64_t n = 0;
     for (int64_t at = 0; at < count; at += kMaxTable) {
         const int64_t k = std::min<int64_t>(kMaxTable, count - at);
-        int64_t units = 0;
-        for (int64_t i = at; i < at + k; ++i) units += ceil_div(ts[i].numel * elem_size(ts[i].dtype), kUnitBytes);
+        const int64_t units = units_of(ts + at, k);
         const int64_t ctas = std::min(most, units);
         if (ctas == 0) continue;
         e = any_pass(ts + at, k, false, ctas, partial + n, 0, 0.f, nullptr, stream);
@@ -462,7 +709,7 @@ norm_status run(const norm_tensor* ts, int64_t count, bool clip, float max_norm,
     if (e == cudaSuccess && !clip) {
         const double* src = partial;
         void* args[] = {&src, &n, &norm};
-        e = launch(reinterpret_cast<const void*>(grad_finish), 1, stream, args);
+        e = launch(reinterpret_cast<const void*>(grad_finish), 1, 32, stream, args);
     }
     for (int64_t at = 0; e == cudaSuccess && clip && at < std::max<int64_t>(count, 1); at += kMaxTable)
         e = any_pass(ts + at, std::min<int64_t>(kMaxTable, count - at), true, most, partial, n, max_norm,
@@ -489,9 +736,13 @@ norm_status grad_clip(const norm_tensor* tensors, int64_t count, float max_norm,
     return libnorm::run(tensors, count, true, max_norm, norm, workspace, workspace_bytes, stream);
 }
 
-norm_status grad_workspace_bytes(int64_t count, int num_sms, size_t* bytes) {
-    if (!bytes || count < 0 || num_sms < 1) return NORM_ERR_ARG;
-    *bytes = static_cast<size_t>(libnorm::launches_of(count)) * static_cast<size_t>(num_sms) * libnorm::kCtasPerSm * 8;
+norm_status grad_workspace_bytes(const norm_tensor* tensors, int64_t count, int num_sms, size_t* bytes) {
+    const norm_status st = libnorm::check_tensors(tensors, count, false);
+    if (st != NORM_OK) return st;
+    if (!bytes || num_sms < 1) return NORM_ERR_ARG;
+    *bytes = libnorm::is_short(tensors, count)
+                 ? 0
+                 : static_cast<size_t>(libnorm::launches_of(count)) * static_cast<size_t>(num_sms) * libnorm::kCtasPerSm * 8;
     return NORM_OK;
 }
 

@@ -328,7 +328,7 @@ PyObject* grad_py(PyObject* const* a) {
     const c10::cuda::CUDAGuard guard(first.device());
     const at::Tensor norm = f32(a[3], {}, first, "norm");
     size_t bytes = 0;
-    if (a[4] == Py_None) grad_workspace_bytes(n, sm_count(first.get_device()), &bytes);
+    if (a[4] == Py_None) grad_workspace_bytes(table.data(), n, sm_count(first.get_device()), &bytes);
     const at::Tensor ws = scratch(a[4], bytes, first);
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(first.get_device()).stream();
     norm_status st;

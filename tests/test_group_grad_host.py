@@ -145,9 +145,11 @@ def test_gradient_arguments_refused(lib):
         assert clip(lib, [ok, bad], call="grad_norm") == rn.NORM_ERR_ARG
         assert clip(lib, [ok, bad]) == rn.NORM_ERR_ARG
     assert clip(lib, [(0x1000, 0x1000, 4, 9)]) == rn.NORM_ERR_DTYPE
+    long = (0x100000, 0x100000, 1 << 20, rn.NORM_F32)
     for kw in (dict(norm=None), dict(ws=None), dict(ws=ctypes.c_void_p(0x1004))):
-        assert clip(lib, [ok], **kw) == rn.NORM_ERR_ARG
-        assert clip(lib, [ok], call="grad_norm", **kw) == rn.NORM_ERR_ARG
+        assert clip(lib, [long], **kw) == rn.NORM_ERR_ARG
+        assert clip(lib, [long], call="grad_norm", **kw) == rn.NORM_ERR_ARG
+    assert clip(lib, [ok], norm=None) == rn.NORM_ERR_ARG
     for m in (-1.0, float("nan"), float("inf")):
         assert clip(lib, [ok], max_norm=m) == rn.NORM_ERR_ARG
     assert clip(lib, [(0x1000, None, 4, 0)]) == rn.NORM_ERR_ARG
@@ -168,9 +170,16 @@ def test_overlapping_outputs_refused(lib, entries):
 
 def test_workspace_bytes(lib):
     n = ctypes.c_size_t()
-    assert lib.grad_workspace_bytes(0, 152, ctypes.byref(n)) == rn.NORM_OK and n.value >= 8
+
+    def need(sizes, sms=152):
+        ts = (NormTensor * max(1, len(sizes)))(*[NormTensor(0x1000, None, v, rn.NORM_F32, 0) for v in sizes])
+        return lib.grad_workspace_bytes(ctypes.addressof(ts), len(sizes), sms, ctypes.byref(n))
+
+    assert need([]) == rn.NORM_OK and n.value == 0
+    assert need([1024] * 24) == rn.NORM_OK and n.value == 0  # short: none
+    assert need([1 << 20]) == rn.NORM_OK and n.value > 0
     one = n.value
-    assert lib.grad_workspace_bytes(5000, 152, ctypes.byref(n)) == rn.NORM_OK and n.value > one
-    assert lib.grad_workspace_bytes(-1, 152, ctypes.byref(n)) == rn.NORM_ERR_ARG
-    assert lib.grad_workspace_bytes(1, 0, ctypes.byref(n)) == rn.NORM_ERR_ARG
-    assert lib.grad_workspace_bytes(1, 152, None) == rn.NORM_ERR_ARG
+    assert need([1] * 5000) == rn.NORM_OK and n.value > one
+    assert need([-1]) == rn.NORM_ERR_ARG and need([1], 0) == rn.NORM_ERR_ARG
+    assert lib.grad_workspace_bytes(None, 1, 152, ctypes.byref(n)) == rn.NORM_ERR_ARG
+    assert lib.grad_workspace_bytes(None, 0, 152, None) == rn.NORM_ERR_ARG

@@ -191,15 +191,15 @@ def gn_plans(B, S, C, G, dtype, backward):
         for cluster in (1, 2, 4, 8):
             rows = -(-S // cluster)
             for tile in {unit, min(2 * unit, C // vec), C // vec}:
-                if tile > 512 or (D % vec and tile * vec > 512):
+                if tile > 256 or (D % vec and tile * vec > 512):
                     continue
                 for v in (1, 2, 4) + (() if backward else (8,)):
                     par = -(-rows // v)
                     threads = -(-par * tile // 32) * 32
-                    if threads <= 512:
+                    if threads <= 256:
                         out.append(dict(path=0, vec_elems=vec, tile=tile, threads=threads, per_thread=v,
                                         cluster=cluster, chunks=1, out_chunks=1, bands=1))
-                for threads in (128, 512):
+                for threads in (128, 256):
                     if tile <= threads:
                         for bands in range(1, 1 + min(3, B * -(-(C // vec) // tile))):
                             out.append(dict(path=1, vec_elems=vec, tile=tile, threads=threads, per_thread=1,
@@ -480,7 +480,7 @@ def test_random_shapes():
 def test_plans_that_do_not_fit_are_refused():
     x, dy, gamma, beta = make(1, 1000, 64, torch.bfloat16, 0)
     good = rn.make_gn_plan(1, 1000, 64, 8, torch.bfloat16)
-    for kw in (dict(path=7), dict(vec_elems=4), dict(threads=0), dict(threads=1024), dict(tile=0), dict(tile=10 ** 6),
+    for kw in (dict(path=7), dict(vec_elems=4), dict(threads=0), dict(threads=288), dict(tile=0), dict(tile=10 ** 6),
                dict(cluster=3), dict(cluster=16), dict(path=0, per_thread=1, cluster=1, threads=32, tile=1),
                dict(path=1, cluster=2), dict(path=1, cluster=1, chunks=0), dict(path=1, cluster=1, out_chunks=0),
                dict(path=1, cluster=1, bands=0), dict(path=1, cluster=1, bands=10 ** 6)):
