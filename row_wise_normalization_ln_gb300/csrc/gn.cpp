@@ -148,7 +148,6 @@ norm_status derive(const gn_plan& p, const Shape& s, GnArgs* a) {
     a->by_out_chunks = libnorm::fast_div(p.out_chunks);
     a->chunk_rows = std::max<int64_t>(1, ceil_div(s.S, p.chunks));
     a->out_rows = std::max<int64_t>(1, ceil_div(s.S, p.out_chunks));
-    a->last_part = static_cast<int32_t>((s.S - 1) / a->chunk_rows);
     if (a->chunk_rows > (int64_t(1) << 30) || a->out_rows > (int64_t(1) << 30)) return NORM_ERR_PLAN;
     // CTAs of a launch, and partial rows of the column gradients
     const int64_t units = s.B * a->tiles, tall = std::max(p.chunks, p.out_chunks);
@@ -241,7 +240,7 @@ Workspace layout(const gn_plan& p, const Shape& s, const GnArgs& a) {
     if (s.B == 0 || s.S == 0) return w;
     if (p.path == GN_PATH_SPLIT) {
         w.part = w.shift + (s.bwd ? 0 : round_up(s.B * s.G * 4, 16));
-        w.cols = w.part + round_up(s.B * s.G * a.tpg * a.chunks * 8, 16);
+        w.cols = w.part + s.B * s.G * a.tpg * a.chunks * 16;
     }
     w.bytes = w.cols + (s.bwd && a.partials > 1 ? int64_t(a.partials) * 2 * s.C * 4 : 0);
     return w;
@@ -284,7 +283,7 @@ norm_status settle(const Shape& s, int vec, const gn_plan* user, void* ws, size_
         if (!ws || reinterpret_cast<uintptr_t>(ws) % 16 != 0 || ws_bytes < static_cast<size_t>(w.bytes)) return NORM_ERR_ARG;
         char* base = static_cast<char*>(ws);
         a->shift = reinterpret_cast<float*>(base + w.shift);
-        a->part = reinterpret_cast<float2*>(base + w.part);
+        a->part = base + w.part;
         a->colg = reinterpret_cast<float*>(base + w.cols);
     }
     return NORM_OK;

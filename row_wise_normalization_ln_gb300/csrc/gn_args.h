@@ -37,7 +37,7 @@ struct GnArgs {
     float* mean;           // [B, G]: written by the forward, read by the backward
     float* rstd;
     float* shift;          // SPLIT forward: [B, G], the groups' first elements
-    float2* part;          // SPLIT: [B, G, tpg, chunks] group states of the row chunks
+    void* part;            // SPLIT: [B, G, tpg, chunks] group states of the row chunks (float4; backward float2)
     float* colg;           // backward: partial rows of dgamma and dbeta, [partials] rows of C values at a
     float* colb;           // pitch of col_pitch (dgamma and dbeta themselves where one partial row is all)
     int64_t S;
@@ -53,7 +53,6 @@ struct GnArgs {
     int32_t cluster, cluster_bits;  // CHIP: CTAs per sample and tile
     int32_t join;          // CHIP backward: samples in one cluster (all of them), or 1
     int32_t chunks;        // row chunks summed per sample and tile
-    int32_t last_part;     // the last of them that has rows
     int32_t out_chunks;    // row chunks written per sample and tile
     int64_t chunk_rows;    // rows per summed chunk (CHIP: per CTA of the cluster)
     int64_t out_rows;      // rows per written chunk
@@ -67,15 +66,15 @@ struct GnArgs {
     float eps;
 };
 
-// Dynamic shared memory of a kernel, from its plan: the per-thread states
-// ([par][units]); per group and warp that shares the group, a state and its
-// count (12 bytes, at most one per warp or per group); per group, two values.
-// (The column adders of the backward keep 8 bytes per thread.) `units`: states
-// per row slot; tile * segs in the forward, tile * vec_elems
-// in the backward, whose column sums are per channel.
+// Dynamic shared memory of a kernel, from its plan: per group and warp that
+// shares the group, a state (16 bytes, at most one per warp or per group); per
+// group, 12 bytes of values; the per-thread states ([par][units]). (The
+// column adders of the backward keep 8 bytes per thread.) `units`: states per
+// row slot; tile * segs in the forward, tile * vec_elems in the backward,
+// whose column sums are per channel.
 inline int64_t gn_smem_bytes(int par, int units, int groups, int threads) {
     const int64_t shared = groups > threads / 32 ? groups : threads / 32;
-    const int64_t merge = int64_t(par) * units * 8 + shared * 12 + int64_t(groups) * 12 + 16;
+    const int64_t merge = int64_t(par) * units * 8 + shared * 16 + int64_t(groups) * 12 + 16;
     return merge > int64_t(threads) * 8 ? merge : int64_t(threads) * 8;
 }
 

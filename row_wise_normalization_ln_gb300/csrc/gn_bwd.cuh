@@ -329,7 +329,7 @@ __device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, in
     for (int g = threadIdx.x; g < w.ng; g += blockDim.x) {
         const int gg = w.g0 + g;
         const int ti = a.tpg == 1 ? 0 : w.t - quot(gg * a.D / VEC, a.by_tile);
-        a.part[((w.b * a.G + gg) * a.tpg + ti) * a.chunks + k] = gs[g];
+        static_cast<float2*>(a.part)[((w.b * a.G + gg) * a.tpg + ti) * a.chunks + k] = gs[g];
     }
     gn_bwd_write_cols<VEC>(a, w, st, 0, 1, w.b * a.chunks + k);
 }
@@ -347,7 +347,7 @@ __device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, i
         const int gg = w.g0 + (g < w.ng ? g : 0);
         const int64_t bg = w.b * a.G + gg;
         const int touched = a.tpg == 1 ? 1 : quot(((gg + 1) * a.D - 1) / VEC, a.by_tile) - quot(gg * a.D / VEC, a.by_tile) + 1;
-        const float2* src = a.part + bg * a.tpg * a.chunks;
+        const float2* src = static_cast<const float2*>(a.part) + bg * a.tpg * a.chunks;
         float2 t = make_float2(0.f, 0.f);
         if (g < w.ng)
 #pragma unroll 4

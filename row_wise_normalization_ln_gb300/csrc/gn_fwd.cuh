@@ -8,57 +8,93 @@
 //
 // Statistics: differences d = x - K from a shift K near the data, so that a
 // group whose mean dwarfs its spread keeps its digits (x - K of nearby values
-// is exact). Per-thread states (count, mean, M2 = sum (d - mean)^2) merge in
-// the k-way form mean = sum n_t m_t / n, M2 = sum M2_t + n_t (m_t - mean)^2,
+// is exact). Per-thread states (count, sum, M2 = sum (d - mean)^2) merge in
+// the k-way form mean = sum s_t / n, M2 = sum M2_t + n_t (m_t - mean)^2,
 // which is what any sequence of pairwise merges reaches; the variance is
-// never formed as E[x^2] - E[x]^2 of unshifted values. All in fp32.
+// never formed as E[x^2] - E[x]^2 of unshifted values. All in fp32, the merged
+// sums in pairs of fp32.
 #pragma once
 
 #include "gn_kernels.cuh"
 
 namespace libnorm {
 
-// Collapses the per-channel states (m, m2 of `visits` values each) of an
-// access to one state per group it touches: (mean, M2) of visits * channels
+// Collapses the per-channel states (sum s, M2 m2 of `visits` values each) of
+// an access to one per group it touches: (sum, M2) of visits * channels
 // values, in this thread's slots st[0 .. segs).
 template <int VEC>
-__device__ __forceinline__ void gn_collapse(const float2* m, const float2* m2, float visits, int c, const GnArgs& a,
+__device__ __forceinline__ void gn_collapse(const float2* s, const float2* m2, float visits, int c, const GnArgs& a,
                                             float2* st) {
     constexpr int H = (VEC + 1) / 2;
     GnWalk k(c, a);
+    const float inv = visits > 0.f ? __fdividef(1.f, visits) : 0.f;
     int seg = 0, first = 0;
-    float s = 0.f;
-    // the channels j .. of one group end where the walk steps to the next
+    float t = 0.f;
+    // the channels of one group end where the walk steps to the next
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-        s += (j & 1) ? m[j / 2].y : m[j / 2].x;
+        t += (j & 1) ? s[j / 2].y : s[j / 2].x;
         const int g = k.g;
         k.next();
         if (j == VEC - 1 || k.g != g) {
-            const float mean = __fdividef(s, static_cast<float>(j + 1 - first));
+            const float mean = __fdividef(t, static_cast<float>(j + 1 - first)) * inv;
             float q = 0.f;
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                const float2 d = f2_sub(m[i], f2_splat(mean));
+                const float2 d = __ffma2_rn(s[i], f2_splat(inv), f2_splat(-mean));
                 const float2 e = __ffma2_rn(__fmul2_rn(d, f2_splat(visits)), d, m2[i]);
                 if (2 * i >= first && 2 * i <= j) q += e.x;
                 if (2 * i + 1 >= first && 2 * i + 1 <= j) q += e.y;
             }
-            st[seg++] = make_float2(mean, q);
-            s = 0.f;
+            st[seg++] = make_float2(t, q);
+            t = 0.f;
             first = j + 1;
         }
     }
 }
 
-// Merges the CTA's thread states into states gs[g * wpg + part] = (mean, M2)
-// of counts gn[...]. The states of row slot r and access column u start at
-// st[(r * tile + u) * segs], one per group the access touches. Lanes side by
-// side over the group's accesses, then row slots. Every thread of the CTA
-// calls it, after a barrier.
+// A merged state: the sum of the differences from the group's first element
+// as an unevaluated pair (x + y, |y| within half an ulp of x), M2 in z, the
+// count in w. The pair keeps the mean's last bits where it is small against
+// the spread: one rounding of a sum of that size would be a large error of
+// such a mean.
+__device__ __forceinline__ void ff_add(float& hi, float& lo, float a, float b) {
+    const float s = hi + a, t = s - hi;  // Knuth's two-sum
+    lo += ((hi - (s - t)) + (a - t)) + b;
+    hi = s;
+}
+
+// Merges the states that walk(f) hands to f one by one over aligned groups of
+// `lanes` lanes (every lane of the warp calls it).
+template <class Walk>
+__device__ __forceinline__ float4 gn_merge(Walk walk, int lanes) {
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    walk([&](const float4& e) {
+        ff_add(t.x, t.y, e.x, e.y);
+        t.w += e.w;
+    });
+    for (int off = lanes >> 1; off > 0; off >>= 1) {
+        const float x = __shfl_xor_sync(kFullMask, t.x, off), y = __shfl_xor_sync(kFullMask, t.y, off);
+        t.w += __shfl_xor_sync(kFullMask, t.w, off);
+        ff_add(t.x, t.y, x, y);
+    }
+    const float mean = t.w > 0.f ? __fdividef(t.x, t.w) : 0.f;
+    walk([&](const float4& e) {
+        const float d = __fdividef(e.x, e.w) - mean;
+        if (e.w > 0.f) t.z += fmaf(e.w * d, d, e.z);
+    });
+    t.z = group_sum(t.z, lanes);
+    return t;
+}
+
+// Merges the CTA's thread states into states gs[g * wpg + part]. The states
+// (sum, M2) of row slot r and access column u start at st[(r * tile + u) *
+// segs], one per group the access touches. Lanes side by side over the
+// group's accesses, then row slots. Every thread of the CTA calls it, after a
+// barrier.
 template <int VEC>
 __device__ __forceinline__ void gn_merge_threads(const GnArgs& a, const GnTile& w, const float2* st, int segs,
-                                                 const GnVisits& vis, const GnShare& sh, float2* gs, float* gn) {
+                                                 const GnVisits& vis, const GnShare& sh, float4* gs) {
     const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
     const int jobs = w.ng * sh.wpg;
     for (int base = 0; base < jobs << sh.bits; base += blockDim.x) {
@@ -70,43 +106,30 @@ __device__ __forceinline__ void gn_merge_threads(const GnArgs& a, const GnTile& 
         const int u0 = (lo - w.c0) / VEC, n = (hi - 1 - w.c0) / VEC - u0 + 1;
         const int across = min(n, lanes), deep = small_quot(lanes, across);
         const int r0 = small_quot(lane, across), uf = lane - r0 * across;
-        float s = 0.f, c = 0.f, q = 0.f;
-        auto walk = [&](auto f) {
+        const float4 t = gn_merge([&](auto f) {
             if (on && r0 < deep)
                 for (int u = uf; u < n; u += lanes) {
                     const int ch = w.c0 + (u0 + u) * VEC;  // the access's first channel
                     const int len = min(hi, ch + VEC) - max(lo, ch);
                     const int seg = segs == 1 ? 0 : w.g0 + g - quot(ch, a.by_D);
-                    for (int r = part + sh.wpg * r0; r < a.par; r += sh.wpg * deep)
-                        f(static_cast<float>(vis.of(r) * len), st[(r * a.tile + u0 + u) * segs + seg]);
+                    for (int r = part + sh.wpg * r0; r < a.par; r += sh.wpg * deep) {
+                        const float2 e = st[(r * a.tile + u0 + u) * segs + seg];
+                        f(make_float4(e.x, 0.f, e.y, static_cast<float>(vis.of(r) * len)));
+                    }
                 }
-        };
-        walk([&](float v, float2 e) {
-            s = fmaf(v, v > 0.f ? e.x : 0.f, s);
-            c += v;
-        });
-        group_sum2(c, s, lanes);
-        const float mean = c > 0.f ? __fdividef(s, c) : 0.f;
-        walk([&](float v, float2 e) {
-            const float d = e.x - mean;
-            if (v > 0.f) q += fmaf(v * d, d, e.y);
-        });
-        q = group_sum(q, lanes);
-        if (on && lane == 0) {
-            gs[j] = make_float2(mean, q);
-            gn[j] = c;
-        }
+        }, lanes);
+        if (on && lane == 0) gs[j] = t;
     }
 }
 
 // The groups' states from their `wpg` states in each of the `cs` CTAs of the
-// cluster: calls done(group, mean, M2, count) once for each of the tile's
-// groups. The lanes of a group take one state each where there are enough.
+// cluster: calls done(group, state) once for each of the tile's groups. The
+// lanes of a group take one state each where there are enough.
 template <class F>
-__device__ __forceinline__ void gn_merge_cluster(const float2* gs, const float* gn, int ng, int wpg, int cs, F done) {
+__device__ __forceinline__ void gn_merge_cluster(const float4* gs, int ng, int wpg, int cs, F done) {
     const int n = cs * wpg;
     if (n == 1) {
-        for (int g = threadIdx.x; g < ng; g += blockDim.x) done(g, gs[g].x, gs[g].y, gn[g]);
+        for (int g = threadIdx.x; g < ng; g += blockDim.x) done(g, gs[g]);
         return;
     }
     int bits = 0;
@@ -115,30 +138,32 @@ __device__ __forceinline__ void gn_merge_cluster(const float2* gs, const float* 
     for (int base = 0; base < ng << bits; base += blockDim.x) {
         const int g = (base + static_cast<int>(threadIdx.x)) >> bits;
         const bool on = g < ng;
-        float c = 0.f, s = 0.f, q = 0.f;
-        auto walk = [&](auto f) {
+        const float4 t = gn_merge([&](auto f) {
             if (on)
                 for (int i = lane; i < n; i += lanes) {
                     const int k = wpg == 1 ? i : small_quot(i, wpg), at = g * wpg + (i - k * wpg);
-                    if (cs > 1)
-                        f(ld_peer_f32(peer_smem_addr(gn + at, k)), gn_peer(gs, at, k));
-                    else
-                        f(gn[at], gs[at]);
+                    f(cs > 1 ? ld_peer_f32x4(peer_smem_addr(gs + at, k)) : gs[at]);
                 }
-        };
-        walk([&](float v, float2 e) {
-            s = fmaf(v, e.x, s);
-            c += v;
-        });
-        group_sum2(c, s, lanes);
-        const float mean = c > 0.f ? __fdividef(s, c) : 0.f;
-        walk([&](float v, float2 e) {
-            const float d = e.x - mean;
-            if (v > 0.f) q += fmaf(v * d, d, e.y);
-        });
-        q = group_sum(q, lanes);
-        if (on && lane == 0) done(g, mean, q, c);
+        }, lanes);
+        if (on && lane == 0) done(g, t);
     }
+}
+
+// The mean relative to the shift of a merged state, rounded once, and K plus
+// it, rounded once.
+__device__ __forceinline__ float2 gn_quotient(const float4& t) {
+    const float q = __fdiv_rn(t.x, t.w);
+    return make_float2(q, __fdividef(fmaf(-q, t.w, t.x) + t.y, t.w));  // the quotient and what it leaves
+}
+__device__ __forceinline__ float gn_mu(const float4& t) {
+    const float2 q = gn_quotient(t);
+    return q.x + q.y;
+}
+__device__ __forceinline__ float gn_mean(float K, const float4& t) {
+    const float2 q = gn_quotient(t);
+    float hi = K, lo = 0.f;
+    ff_add(hi, lo, q.x, q.y);
+    return hi + lo;
 }
 
 // The square root and the division are the correctly rounded ones: there is
@@ -191,16 +216,17 @@ template <class T, int VEC, bool ONE, class F>
 __device__ __forceinline__ void gn_per_group(float2* K, int c, const GnArgs& a, F v) {
     using X = GnVec<T, VEC>;
     GnWalk k(c, a);
+    float last = v(k.g);
     if constexpr (ONE) {
-        K[0] = f2_splat(v(k.g));
-        if (VEC == 1) K[0].y = 0.f;
+        K[0] = make_float2(last, VEC == 1 ? 0.f : last);
     } else {
 #pragma unroll
-        for (int i = 0; i < X::H; ++i) {
-            K[i].x = v(k.g);
+        for (int j = 0; j < VEC; ++j) {
+            if (j & 1) K[j / 2].y = last;
+            else K[j / 2].x = last;
+            const int g = k.g;
             k.next();
-            K[i].y = v(k.g);
-            k.next();
+            if (j + 1 < VEC && k.g != g) last = v(k.g);
         }
     }
 }
@@ -209,17 +235,16 @@ template <class T, int VEC, bool ONE, int ACT, int V>
 __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
     using X = GnVec<T, VEC>;
     constexpr int HG = ONE ? 1 : X::H;
-    extern __shared__ float2 sm[];
+    extern __shared__ __align__(16) float2 sm[];
     grid_release();
     const int cs = a.cluster;
     const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
     const GnTile w = gn_tile<VEC>(a, static_cast<int>(blockIdx.x) >> a.cluster_bits);
     const int segs = ONE ? 1 : a.segs;
     const GnShare sh(w.ng);
-    float2* st = sm;
-    float2* gs = st + a.par * a.tile * segs;
-    float2* fin = gs + w.ng * sh.wpg;
-    float* gn = reinterpret_cast<float*>(fin + w.ng);
+    float4* gs = reinterpret_cast<float4*>(sm);  // (16-byte aligned: first)
+    float2* fin = reinterpret_cast<float2*>(gs + w.ng * sh.wpg);
+    float2* st = fin + w.ng;
 
     const int64_t row0 = int64_t(rank) * a.chunk_rows;
     const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, rank));
@@ -255,19 +280,22 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
                     s[j] = __fadd2_rn(s[j], f2_sub(X::get(raw[v], i), out.K[j]));
                 }
             }
-        const float inv = visits > 0 ? 1.f / static_cast<float>(visits) : 0.f;
-        if constexpr (ONE)
-            s[0] = f2_splat(f2_sum<VEC>(s[0]) * inv * (1.f / VEC));
-        else
+        const float inv = visits > 0 ? __fdividef(1.f, static_cast<float>(visits)) : 0.f;
+        float2 m[HG];  // the means
+        if constexpr (ONE) {
+            s[0].x = f2_sum<VEC>(s[0]);
+            m[0] = f2_splat(s[0].x * inv * (1.f / VEC));
+        } else {
 #pragma unroll
-            for (int i = 0; i < HG; ++i) s[i] = __fmul2_rn(s[i], f2_splat(inv));
+            for (int i = 0; i < HG; ++i) m[i] = __fmul2_rn(s[i], f2_splat(inv));
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (v < visits) {
 #pragma unroll
                 for (int i = 0; i < X::H; ++i) {
                     const int j = ONE ? 0 : i;
-                    const float2 d = f2_sub(f2_sub(X::get(raw[v], i), out.K[j]), s[j]);
+                    const float2 d = f2_sub(f2_sub(X::get(raw[v], i), out.K[j]), m[j]);
                     q[j] = __ffma2_rn(d, d, q[j]);
                 }
             }
@@ -278,18 +306,18 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
             gn_collapse<VEC>(s, q, static_cast<float>(visits), c, a, mine);
     }
     __syncthreads();
-    gn_merge_threads<VEC>(a, w, st, segs, vis, sh, gs, gn);
+    gn_merge_threads<VEC>(a, w, st, segs, vis, sh, gs);
     if (cs > 1)
         cluster_barrier();
     else
         __syncthreads();
-    gn_merge_cluster(gs, gn, w.ng, sh.wpg, cs, [&](int g, float mu, float m2, float count) {
-        const float rstd = gn_rstd(m2, count, a.eps);
-        fin[g] = make_float2(mu, rstd);
+    gn_merge_cluster(gs, w.ng, sh.wpg, cs, [&](int g, const float4& t) {
+        const float rstd = gn_rstd(t.z, t.w, a.eps);
+        fin[g] = make_float2(gn_mu(t), rstd);
         // (in place: row 0 is this CTA's own, written after the barrier)
         if (rank == 0) {
             const int64_t at = w.b * a.G + w.g0 + g;
-            if (a.mean) a.mean[at] = gn_elem(xs + int64_t(w.g0 + g) * a.D) + mu;
+            if (a.mean) a.mean[at] = gn_mean(gn_elem(xs + int64_t(w.g0 + g) * a.D), t);
             if (a.rstd) a.rstd[at] = rstd;
         }
     });
@@ -306,22 +334,19 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
 }
 
 // Rows a thread adds with one shift before it merges them into its running
-// state: the shifted sum of squares then loses at most a few of fp32's bits
-// even where that shift lies far from the other rows.
-constexpr int kGnShiftRows = 128;
+// state. The shift may lie far from the other rows, and a long chain of fp32
+// additions of squares is biased (each add rounds to a multiple of the sum's
+// ulp, and more squares lie below half of it than above): 512 in a row lose
+// 2e-6 of the sum, 64 2e-7.
+constexpr int kGnShiftRows = 32;
 
-// The pairwise merge: (n, m, m2) += (k, mb, b2).
-__device__ __forceinline__ void gn_pair_merge(float& m, float& m2, float mb, float b2, float n, float k) {
-    const float wb = __fdividef(k, n + k), d = mb - m;
-    m = fmaf(d, wb, m);
-    m2 += fmaf(d * d, n * wb, b2);
-}
-
-// sum and sum of squares of d over k values -> (mean, M2); the subtraction
-// can round below zero, and NaN stays NaN.
-__device__ __forceinline__ float2 gn_mean_m2(float s, float q, float k) {
+// The pairwise merge (S, m2) of n values += k values with sum s and sum of
+// squares q about K, with `to` = K - the reference of S.
+__device__ __forceinline__ void gn_pair_merge(float& S, float& m2, float n, float s, float q, float k, float to) {
     const float m = __fdividef(s, k), b2 = fmaf(-s, m, q);
-    return make_float2(m, b2 < 0.f ? 0.f : b2);
+    const float d = n > 0.f ? (to + m) - __fdividef(S, n) : 0.f;
+    m2 += fmaf(d * d, __fdividef(n * k, n + k), b2 < 0.f ? 0.f : b2);  // (the subtraction can round below 0; NaN stays)
+    S += fmaf(to, k, s);
 }
 
 // Row chunk k of a tile: its groups' states into the workspace.
@@ -331,9 +356,8 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
     constexpr int HG = ONE ? 1 : X::H;
     const int segs = ONE ? 1 : a.segs;
     const GnShare sh(w.ng);
-    float2* st = sm;
-    float2* gs = st + a.par * a.tile * segs;
-    float* gn = reinterpret_cast<float*>(gs + w.ng * sh.wpg);
+    float4* gs = reinterpret_cast<float4*>(sm);
+    float2* st = reinterpret_cast<float2*>(gs + w.ng * sh.wpg);
 
     const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, k));
     const GnVisits vis(rows, a);
@@ -343,25 +367,31 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
     if (w.on) {
         const int visits = vis.of(w.r);
         // Blocks of kGnShiftRows rows, shifted by the block's first value:
-        // per channel, or one for the channels of an access within a group.
-        // A full block goes into the running state (m, m2), whose means are
-        // relative to the group's first element.
-        float2 m[HG], m2[HG], K[HG], s[HG], q[HG];
+        // per channel, or for an access within a group in two chains over its
+        // channels. A full block goes into the running state (S, m2), whose
+        // sum is relative to the group's first element.
+        constexpr int HS = ONE ? (X::H < 2 ? X::H : 2) : X::H;
+        float2 S[HG], m2[HG], K[HG], s[HS], q[HS];
 #pragma unroll
-        for (int i = 0; i < HG; ++i) m[i] = m2[i] = K[i] = s[i] = q[i] = make_float2(0.f, 0.f);
+        for (int i = 0; i < HG; ++i) S[i] = m2[i] = K[i] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < HS; ++i) s[i] = q[i] = make_float2(0.f, 0.f);
         auto merge = [&](int first, int stop) {
             const float n = static_cast<float>(first), kk = static_cast<float>(stop - first);
             float2 G0[HG];
             gn_per_group<T, VEC, ONE>(G0, c, a, [&](int g) { return gn_elem(xs + int64_t(g) * a.D); });
             if constexpr (ONE) {
-                const float2 b = gn_mean_m2(f2_sum<VEC>(s[0]), f2_sum<VEC>(q[0]), kk * VEC);
-                gn_pair_merge(m[0].x, m2[0].x, (K[0].x - G0[0].x) + b.x, b.y, n * VEC, kk * VEC);
+                float ts = f2_sum<VEC>(s[0]), tq = f2_sum<VEC>(q[0]);
+                if constexpr (HS > 1) {
+                    ts += f2_sum<VEC>(s[HS - 1]);
+                    tq += f2_sum<VEC>(q[HS - 1]);
+                }
+                gn_pair_merge(S[0].x, m2[0].x, n * VEC, ts, tq, kk * VEC, K[0].x - G0[0].x);
             } else {
 #pragma unroll
                 for (int i = 0; i < HG; ++i) {
-                    const float2 bx = gn_mean_m2(s[i].x, q[i].x, kk), by = gn_mean_m2(s[i].y, q[i].y, kk);
-                    gn_pair_merge(m[i].x, m2[i].x, (K[i].x - G0[i].x) + bx.x, bx.y, n, kk);
-                    gn_pair_merge(m[i].y, m2[i].y, (K[i].y - G0[i].y) + by.x, by.y, n, kk);
+                    gn_pair_merge(S[i].x, m2[i].x, n, s[i].x, q[i].x, kk, K[i].x - G0[i].x);
+                    gn_pair_merge(S[i].y, m2[i].y, n, s[i].y, q[i].y, kk, K[i].y - G0[i].y);
                 }
             }
         };
@@ -374,13 +404,14 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
                 for (int i = 0; i < HG; ++i) {
                     K[i] = X::get(raw[0], i);
                     if (ONE && VEC > 1) K[i].y = K[i].x;
-                    s[i] = q[i] = make_float2(0.f, 0.f);
                 }
+#pragma unroll
+                for (int i = 0; i < HS; ++i) s[i] = q[i] = make_float2(0.f, 0.f);
             }
 #pragma unroll
             for (int i = 0; i < X::H; ++i) {
-                const int j = ONE ? 0 : i;
-                const float2 d = f2_sub(X::get(raw[0], i), K[j]);
+                const int j = ONE ? i & (HS - 1) : i;
+                const float2 d = f2_sub(X::get(raw[0], i), K[ONE ? 0 : i]);
                 s[j] = __fadd2_rn(s[j], d);
                 q[j] = __ffma2_rn(d, d, q[j]);
             }
@@ -388,39 +419,21 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
         if (visits > 0) merge((visits - 1) & ~(kGnShiftRows - 1), visits);
         float2* mine = st + (w.r * a.tile + w.col) * segs;
         if constexpr (ONE)
-            mine[0] = make_float2(m[0].x, m2[0].x);
+            mine[0] = make_float2(S[0].x, m2[0].x);
         else
-            gn_collapse<VEC>(m, m2, static_cast<float>(visits), c, a, mine);
+            gn_collapse<VEC>(S, m2, static_cast<float>(visits), c, a, mine);
     }
     __syncthreads();
-    gn_merge_threads<VEC>(a, w, st, segs, vis, sh, gs, gn);
+    gn_merge_threads<VEC>(a, w, st, segs, vis, sh, gs);
     __syncthreads();
-    gn_merge_cluster(gs, gn, w.ng, sh.wpg, 1, [&](int g, float mu, float m2, float) {
+    gn_merge_cluster(gs, w.ng, sh.wpg, 1, [&](int g, const float4& t) {
         const int gg = w.g0 + g;
         const int64_t bg = w.b * a.G + gg;
         const int ti = a.tpg == 1 ? 0 : w.t - quot(gg * a.D / VEC, a.by_tile);
-        a.part[(bg * a.tpg + ti) * a.chunks + k] = make_float2(mu, m2);
+        reinterpret_cast<float4*>(a.part)[(bg * a.tpg + ti) * a.chunks + k] = t;
         if (k == 0 && ti == 0) a.shift[bg] = gn_elem(xs + int64_t(gg) * a.D);
     });
 }
-
-// The tiles a group touches, and how many of its channels lie in each.
-struct GnSpan {
-    int t0, t1;
-    int c0, c1;  // the group's channels
-    template <int VEC>
-    static __device__ __forceinline__ GnSpan of(const GnArgs& a, int g, int t) {
-        GnSpan s;
-        s.c0 = g * a.D;
-        s.c1 = s.c0 + a.D;
-        s.t0 = a.tpg == 1 ? t : quot(s.c0 / VEC, a.by_tile);
-        s.t1 = a.tpg == 1 ? t : quot((s.c1 - 1) / VEC, a.by_tile);
-        return s;
-    }
-    __device__ __forceinline__ int width(int t, int tile_channels) const {
-        return min(c1, (t + 1) * tile_channels) - max(c0, t * tile_channels);
-    }
-};
 
 // Output row chunk k of a tile.
 template <class T, int VEC, bool ONE, int ACT>
@@ -435,11 +448,7 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
         rg = X::load(static_cast<const T*>(a.gamma) + c);
         rb = X::load(static_cast<const T*>(a.beta) + c);
     }
-    // The groups' states from every tile and chunk, lanes side by side
-    // over the chunks: all have chunk_rows rows up to the last that has any.
-    const int last = a.last_part;
-    const float full = static_cast<float>(a.chunk_rows), rest = static_cast<float>(a.S - last * a.chunk_rows);
-    const float count = static_cast<float>(a.S) * static_cast<float>(a.D);
+    // The groups' states from every tile and chunk, lanes side by side.
     const GnShare sh(w.ng);
     const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
     for (int base = 0; base < w.ng << sh.bits; base += blockDim.x) {
@@ -447,31 +456,22 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
         const bool on = g < w.ng;
         const int gg = w.g0 + (on ? g : 0);
         const int64_t bg = w.b * a.G + gg;
-        const GnSpan sp = GnSpan::of<VEC>(a, gg, w.t);
-        const float2* src = a.part + bg * a.tpg * a.chunks;
+        const float4* src = reinterpret_cast<const float4*>(a.part) + bg * a.tpg * a.chunks;
+        const int t0 = a.tpg == 1 ? w.t : quot(gg * a.D / VEC, a.by_tile);
+        const int t1 = a.tpg == 1 ? w.t : quot(((gg + 1) * a.D - 1) / VEC, a.by_tile);
+        const int n = (t1 - t0 + 1) * a.chunks;
         const float K = a.shift[bg];
-        float s = 0.f, q = 0.f;
-        auto walk = [&](auto f) {
-            for (int t = sp.t0; on && t <= sp.t1; ++t) {
-                const float wd = static_cast<float>(sp.width(t, a.tile * VEC));
+        const float4 t = gn_merge([&](auto f) {
+            if (on)
 #pragma unroll 4
-                for (int p = lane; p <= last; p += lanes)
-                    f((p < last ? full : rest) * wd, src[(t - sp.t0) * a.chunks + p]);
-            }
-        };
-        walk([&](float v, float2 e) { s = fmaf(v, e.x, s); });
-        const float mu = group_sum(s, lanes) / count;
-        walk([&](float v, float2 e) {
-            const float d = e.x - mu;
-            q += fmaf(v * d, d, e.y);
-        });
-        q = group_sum(q, lanes);
+                for (int i = lane; i < n; i += lanes) f(src[i]);
+        }, lanes);
         if (on && lane == 0) {
-            const float rstd = gn_rstd(q, count, a.eps);
-            fin[g] = make_float2(mu, rstd);
+            const float rstd = gn_rstd(t.z, t.w, a.eps);
+            fin[g] = make_float2(gn_mu(t), rstd);
             shift[g] = K;
-            if (k == 0 && sp.t0 == w.t) {
-                if (a.mean) a.mean[bg] = K + mu;
+            if (k == 0 && t0 == w.t) {
+                if (a.mean) a.mean[bg] = gn_mean(K, t);
                 if (a.rstd) a.rstd[bg] = rstd;
             }
         }
