@@ -38,7 +38,7 @@ typedef enum {
 
 typedef enum {
     GN_PATH_CHIP = 0, /* a CTA or a cluster holds a sample's tile on chip: x (and dy) is read once */
-    GN_PATH_SPLIT = 1 /* row chunks are summed into the workspace, then read again (from L2) and written */
+    GN_PATH_SPLIT = 1 /* one launch sums row chunks into the workspace, a second reads the rows again and writes */
 } gn_path;
 
 /* A launch plan of gn_fwd / gn_bwd. Every CTA works on a tile of `tile`
@@ -49,11 +49,9 @@ typedef struct {
     int32_t tile;       /* accesses per row a CTA covers: whole groups for GN_PATH_CHIP */
     int32_t threads;    /* threads per CTA, a multiple of 32, tile <= threads <= 256 */
     int32_t per_thread; /* CHIP: rows each thread holds, 1, 2, 4 or 8 (backward: up to 4) */
-    int32_t cluster;    /* CHIP: the CTAs that share a sample's tile, 1, 2, 4 or 8; SPLIT: 1 */
+    int32_t cluster;    /* CHIP: the CTAs that share a sample's tile, 1, 2, 4 or 8; otherwise 1 */
     int32_t chunks;     /* SPLIT: row chunks per sample and tile that are summed */
     int32_t out_chunks; /* SPLIT: row chunks per sample and tile that are written */
-    int32_t bands;      /* SPLIT: the samples' tiles are taken in this many bands, each small enough to stay in
-                           L2 until it is read again: one launch sums a band and writes the one before */
 } gn_plan;
 
 /*

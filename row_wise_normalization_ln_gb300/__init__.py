@@ -59,7 +59,7 @@ class NormPlan(ctypes.Structure):
 class GnPlan(ctypes.Structure):
     """Mirror of ``gn_plan`` in include/libnorm_group.h."""
     _fields_ = [(k, ctypes.c_int32) for k in ("path", "vec_elems", "tile", "threads", "per_thread", "cluster",
-                                              "chunks", "out_chunks", "bands")]
+                                              "chunks", "out_chunks")]
 
     def as_dict(self) -> dict:
         return {k: getattr(self, k) for k, _ in self._fields_}

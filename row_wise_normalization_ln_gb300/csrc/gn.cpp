@@ -22,7 +22,6 @@ constexpr int64_t kMaxC = int64_t(1) << 24;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSmem = 48 * 1024;
 constexpr int kMaxCluster = 8;
-constexpr int64_t kBandBytes = int64_t(1) << 50;  // of x (and dy) that stay in L2 until they are read again
 constexpr int kFwdMaxRows = 8, kBwdMaxRows = 4;  // rows a thread of the on-chip kernels can hold
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -140,7 +139,7 @@ norm_status derive(const gn_plan& p, const Shape& s, GnArgs* a) {
         if (s.B * a->tiles > kMaxGrid / p.cluster) return NORM_ERR_PLAN;
         return NORM_OK;
     }
-    if (p.cluster != 1 || p.chunks < 1 || p.out_chunks < 1 || p.bands < 1) return NORM_ERR_PLAN;
+    if (p.cluster != 1 || p.chunks < 1 || p.out_chunks < 1) return NORM_ERR_PLAN;
     a->tpg = static_cast<int32_t>(whole ? 1 : ceil_div(s.D - 1, int64_t(a->tile) * p.vec_elems) + 1);
     a->chunks = p.chunks;
     a->out_chunks = p.out_chunks;
@@ -151,7 +150,7 @@ norm_status derive(const gn_plan& p, const Shape& s, GnArgs* a) {
     if (a->chunk_rows > (int64_t(1) << 30) || a->out_rows > (int64_t(1) << 30)) return NORM_ERR_PLAN;
     // CTAs of a launch, and partial rows of the column gradients
     const int64_t units = s.B * a->tiles, tall = std::max(p.chunks, p.out_chunks);
-    if (p.bands > units || tall > kMaxGrid / 4 / units || s.B > kMaxGrid / p.chunks) return NORM_ERR_PLAN;
+    if (tall > kMaxGrid / 4 / std::max<int64_t>(1, units) || s.B > kMaxGrid / p.chunks) return NORM_ERR_PLAN;
     a->partials = static_cast<int32_t>(s.B * p.chunks);
     return NORM_OK;
 }
@@ -204,25 +203,22 @@ void split_plan(const Shape& s, int vec, int sms, gn_plan* p) {
     p->threads = static_cast<int32_t>(round_up(std::max<int64_t>(1, 256 / tile) * tile, 32));
     p->cluster = 1;
     const int64_t units = std::max<int64_t>(1, s.B * ceil_div(ncols, tile));
-    const int64_t bytes = s.B * s.S * s.C * es * (s.bwd ? 2 : 1);
-    p->bands = static_cast<int32_t>(std::min<int64_t>(units, std::max<int64_t>(1, bytes / kBandBytes)));
-    const int64_t per_band = ceil_div(units, p->bands);
+    const int64_t rows = p->threads / tile;
     // Two CTAs per SM; one where that leaves a thread fewer than 8 rows (the
     // merges then cost more than the rows: gn_fwd bf16 2x4096x320 9.6 us with
     // 152 CTAs, 12.0 with 304; gn_bwd f16 8x4096x320, 18 rows each, 23 us with
     // 288 and 28 with 152).
-    const int64_t rows = p->threads / tile;
-    const int64_t chunks = std::min(int64_t(sms) * 2 / per_band, std::max(int64_t(sms) / per_band, s.S / (rows * 8)));
+    const int64_t chunks = std::min(int64_t(sms) * 2 / units, std::max(int64_t(sms) / units, s.S / (rows * 8)));
     const int64_t most = std::max<int64_t>(1, ceil_div(s.S, rows));
-    p->chunks = p->out_chunks =
-        static_cast<int32_t>(std::max(std::min(std::max<int64_t>(1, chunks), most), ceil_div(s.S, int64_t(1) << 30)));
+    p->chunks = static_cast<int32_t>(std::max(std::min(std::max<int64_t>(1, chunks), most), ceil_div(s.S, int64_t(1) << 30)));
+    p->out_chunks = p->chunks;
 }
 
 // The plan for accesses of `vec` elements.
 norm_status make_plan(const Shape& s, int vec, int sms, gn_plan* p) {
     std::memset(p, 0, sizeof *p);
     GnArgs a;
-    p->chunks = p->out_chunks = p->bands = 1;
+    p->chunks = p->out_chunks = 1;
     if (!chip_plan(s, vec, sms, p) || derive(*p, s, &a) != NORM_OK) {
         std::memset(p, 0, sizeof *p);
         p->per_thread = 1;
@@ -238,7 +234,7 @@ struct Workspace {
 Workspace layout(const gn_plan& p, const Shape& s, const GnArgs& a) {
     Workspace w{0, 0, 0, 0};
     if (s.B == 0 || s.S == 0) return w;
-    if (p.path == GN_PATH_SPLIT) {
+    if (p.path != GN_PATH_CHIP) {
         w.part = w.shift + (s.bwd ? 0 : round_up(s.B * s.G * 4, 16));
         w.cols = w.part + s.B * s.G * a.tpg * a.chunks * 16;
     }

@@ -56,10 +56,7 @@ struct GnArgs {
     int32_t out_chunks;    // row chunks written per sample and tile
     int64_t chunk_rows;    // rows per summed chunk (CHIP: per CTA of the cluster)
     int64_t out_rows;      // rows per written chunk
-    // SPLIT, of one launch: the CTAs that sum the tiles from sum_unit on, that
-    // write the tiles from out_unit on, and (backward) that add columns
-    int32_t sum_ctas, out_ctas, col_ctas, sum_unit, out_unit;
-    int32_t partials;      // partial rows the column adders find
+    int32_t partials;      // partial rows of the column gradients
     float *dgamma, *dbeta;
     FastDiv by_cluster;
     FastDiv by_tiles, by_tile, by_D, by_par, by_chunks, by_out_chunks;

@@ -2,9 +2,9 @@
 //
 //   gn_bwd_chip   a CTA, or a cluster, holds all rows of a sample's tile (x
 //                 and dy) in registers: the sums and dx from one read.
-//   gn_bwd_split  for tiles that do not fit a cluster: row chunks are summed
-//                 into the workspace, and a later launch merges them and
-//                 writes dx from a second read of x and dy, from L2.
+//   gn_bwd_split_sums,  for tiles that do not fit a cluster: row chunks are
+//   gn_bwd_split_apply  summed into the workspace; the second launch merges
+//                       them and writes dx from a second read of x and dy.
 //
 // With d = x - mean, A = rstd gamma, z = d A + beta, dz = dy act'(z), the two
 // sums S1 = sum dz and S2 = sum dz d per channel give everything: dbeta = S1,
@@ -363,12 +363,13 @@ __device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, i
     ch.init(a, w.b, c);
     GnBwdOut<T, VEC, ONE> out;
     out.init(a, c, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
-    const int64_t row = k * a.out_rows + w.r;
+    // last rows first: what was summed last is the likeliest in L2
+    const int64_t row = k * a.out_rows + w.r + int64_t(visits - 1) * a.par;
     const T* p[2] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c,
                      static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c};
-    const int64_t step[2] = {int64_t(a.par) * a.xr, int64_t(a.par) * a.dyr};
+    const int64_t step[2] = {-int64_t(a.par) * a.xr, -int64_t(a.par) * a.dyr};
     T* yp = static_cast<T*>(a.y) + w.b * a.yb + row * a.yr + c;
-    const int64_t ystep = int64_t(a.par) * a.yr;
+    const int64_t ystep = -int64_t(a.par) * a.yr;
     GnStream<T, VEC, 2>::run(p, step, visits, ring, [&](int, const auto& raw) {
         X::store(yp, out.apply(ch, raw[0], raw[1]));
         yp += ystep;
@@ -381,7 +382,6 @@ __device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, floa
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int c = block * 32 + lane;
     float2 t = make_float2(0.f, 0.f);
-    grid_wait();
     if (c < a.C)
 #pragma unroll 8
         for (int p = warp; p < a.partials; p += warps)
@@ -395,28 +395,31 @@ __device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, floa
     }
 }
 
-// One launch of the split path, as in the forward; the last one also adds
-// the partial rows of the column gradients, in its first CTAs.
+// The split path's two launches; the second also adds the partial rows of the
+// column gradients, in its first CTAs.
 template <class T, int VEC, bool ONE, int ACT>
-__global__ void __launch_bounds__(kGnMaxThreads, 2) gn_bwd_split(const GnArgs a) {
+__global__ void __launch_bounds__(kGnMaxThreads, 2) gn_bwd_split_sums(const GnArgs a) {
     extern __shared__ __align__(16) float2 slots[];  // the row stream's slots, then the merges' states
+    grid_release();
+    const int unit = quot(blockIdx.x, a.by_chunks);
+    gn_bwd_sums<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, unit), static_cast<int>(blockIdx.x) - unit * a.chunks,
+                                  slots + GnStream<T, VEC, 2>::kRing / 8 * blockDim.x, slots);
+}
+
+template <class T, int VEC, bool ONE, int ACT>
+__global__ void __launch_bounds__(kGnMaxThreads, 2) gn_bwd_split_apply(const GnArgs a) {
+    extern __shared__ __align__(16) float2 slots[];
     float2* sm = slots + GnStream<T, VEC, 2>::kRing / 8 * blockDim.x;
     grid_release();
-    const int first = static_cast<int>(blockIdx.x) - a.col_ctas;
-    if (first < 0) {
+    const int adders = a.partials > 1 ? (a.C + 31) / 32 : 0;
+    const int i = static_cast<int>(blockIdx.x) - adders;
+    if (i < 0) {
+        grid_wait();
         gn_bwd_add_cols(a, blockIdx.x, sm);
         return;
     }
-    bool out;
-    const int i = gn_role(first, a.out_ctas, a.sum_ctas, &out);
-    if (out) {
-        const int id = a.out_ctas - 1 - i;  // last chunks first
-        const int unit = quot(id, a.by_out_chunks);
-        gn_bwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.out_unit + unit), id - unit * a.out_chunks, sm, slots);
-    } else {
-        const int unit = quot(i, a.by_chunks);
-        gn_bwd_sums<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.sum_unit + unit), i - unit * a.chunks, sm, slots);
-    }
+    const int unit = quot(i, a.by_out_chunks);
+    gn_bwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, unit), i - unit * a.out_chunks, sm, slots);
 }
 
 // ------------------------------------------------------------ launch
@@ -435,9 +438,14 @@ cudaError_t gn_launch_bwd(const gn_plan& p, const GnArgs& a, int64_t B, cudaStre
         }
         return gn_launch(k, B * a.tiles * a.cluster, p.threads, smem, a.cluster * a.join, s, a);
     }
-    return gn_launch_bands(reinterpret_cast<const void*>(gn_bwd_split<T, VEC, ONE, ACT>), p, a, B * a.tiles,
-                           a.partials > 1 ? (a.C + 31) / 32 : 0,
-                           smem + static_cast<size_t>(GnStream<T, VEC, 2>::kRing) * p.threads, s);
+    const int64_t units = B * a.tiles;
+    const size_t all = smem + static_cast<size_t>(GnStream<T, VEC, 2>::kRing) * p.threads;
+    const cudaError_t e = gn_launch(reinterpret_cast<const void*>(gn_bwd_split_sums<T, VEC, ONE, ACT>),
+                                    units * a.chunks, p.threads, all, 1, s, a);
+    if (e != cudaSuccess) return e;
+    const int64_t adders = a.partials > 1 ? (a.C + 31) / 32 : 0;
+    return gn_launch(reinterpret_cast<const void*>(gn_bwd_split_apply<T, VEC, ONE, ACT>),
+                     units * a.out_chunks + adders, p.threads, all, 1, s, a);
 }
 
 template <class T, int VEC, bool ONE>
@@ -463,8 +471,8 @@ cudaError_t gn_dispatch_bwd(const gn_plan& p, const GnArgs& a, norm_act act, int
         else
             e = gn_launch_bwd_act<T, 1, true>(p, a, act, B, s);
         // one partial row: the kernel wrote dgamma and dbeta; the split path's
-        // last launch adds its partial rows itself
-        if (e != cudaSuccess || a.partials == 1 || p.path == GN_PATH_SPLIT) return e;
+        // second launch adds its partial rows itself
+        if (e != cudaSuccess || a.partials == 1 || p.path != GN_PATH_CHIP) return e;
     }
     // The partial rows of the column gradients (none: zeros), in a fixed order.
     const float* ws = a.colg;

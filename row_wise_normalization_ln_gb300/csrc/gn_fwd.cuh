@@ -2,9 +2,10 @@
 //
 //   gn_fwd_chip   a CTA, or a cluster, holds all rows of a sample's tile in
 //                 registers: statistics, activation and output from one read.
-//   gn_fwd_split  for tiles that do not fit a cluster: row chunks are summed
-//                 into the workspace, and a later launch merges them and
-//                 writes y from a second read of x, from L2.
+//   gn_fwd_split_sums,  for tiles that do not fit a cluster: row chunks are
+//   gn_fwd_split_apply  summed into the workspace; the second launch merges
+//                       them and writes y from a second read of x (from L2
+//                       where x fits).
 //
 // Statistics: differences d = x - K from a shift K near the data, so that a
 // group whose mean dwarfs its spread keeps its digits (x - K of nearby values
@@ -482,38 +483,35 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
     GnOut<T, VEC, ONE, ACT> out;
     gn_per_group<T, VEC, ONE>(out.K, c, a, [&](int g) { return shift[min(g - w.g0, w.ng - 1)]; });
     out.init(rg, rb, c, a, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
-    const int64_t row = k * a.out_rows + w.r;
+    // last rows first: what was summed last is the likeliest in L2
+    const int64_t row = k * a.out_rows + w.r + int64_t(visits - 1) * a.par;
     const T* p[1] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c};
-    const int64_t step[1] = {int64_t(a.par) * a.xr};
+    const int64_t step[1] = {-int64_t(a.par) * a.xr};
     T* yp = static_cast<T*>(a.y) + w.b * a.yb + row * a.yr + c;
-    const int64_t ystep = int64_t(a.par) * a.yr;
+    const int64_t ystep = -int64_t(a.par) * a.yr;
     GnStream<T, VEC, 1>::run(p, step, visits, ring, [&](int, const auto& raw) {
         X::store(yp, out.apply(raw[0]));
         yp += ystep;
     });
 }
 
-// One launch of the split path: some CTAs sum the row chunks of one band's
-// tiles, others write the tiles of the band before, which is still in L2.
-// Sums read from HBM while outputs are written there; side by side they keep
-// it busy in both directions. The two kinds of CTAs alternate so that each
-// SM has both.
-template <class T, int VEC, bool ONE, int ACT>
-__global__ void __launch_bounds__(kGnMaxThreads, ONE ? 4 : 3) gn_fwd_split(const GnArgs a) {
+// The split path's two launches, one CTA per tile and chunk.
+template <class T, int VEC, bool ONE>
+__global__ void __launch_bounds__(kGnMaxThreads, ONE ? 4 : 3) gn_fwd_split_sums(const GnArgs a) {
     extern __shared__ __align__(16) float2 slots[];  // the row stream's slots, then the merges' states
-    float2* sm = slots + GnStream<T, VEC, 1>::kRing / 8 * blockDim.x;
     grid_release();
-    bool out;
-    const int i = gn_role(blockIdx.x, a.out_ctas, a.sum_ctas, &out);
-    if (out) {
-        // last chunks first: what was summed last is the likeliest in L2
-        const int id = a.out_ctas - 1 - i;
-        const int unit = quot(id, a.by_out_chunks);
-        gn_fwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, a.out_unit + unit), id - unit * a.out_chunks, sm, slots);
-    } else {
-        const int unit = quot(i, a.by_chunks);
-        gn_fwd_sums<T, VEC, ONE>(a, gn_tile<VEC>(a, a.sum_unit + unit), i - unit * a.chunks, sm, slots);
-    }
+    const int unit = quot(blockIdx.x, a.by_chunks);
+    gn_fwd_sums<T, VEC, ONE>(a, gn_tile<VEC>(a, unit), static_cast<int>(blockIdx.x) - unit * a.chunks,
+                             slots + GnStream<T, VEC, 1>::kRing / 8 * blockDim.x, slots);
+}
+
+template <class T, int VEC, bool ONE, int ACT>
+__global__ void __launch_bounds__(kGnMaxThreads, ONE ? 4 : 3) gn_fwd_split_apply(const GnArgs a) {
+    extern __shared__ __align__(16) float2 slots[];
+    grid_release();
+    const int unit = quot(blockIdx.x, a.by_out_chunks);
+    gn_fwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, unit), static_cast<int>(blockIdx.x) - unit * a.out_chunks,
+                                   slots + GnStream<T, VEC, 1>::kRing / 8 * blockDim.x, slots);
 }
 
 // ------------------------------------------------------------ launch
@@ -543,11 +541,14 @@ cudaError_t gn_launch_fwd(const gn_plan& p, const GnArgs& a, norm_act act, int64
         if (k == nullptr) return cudaErrorInvalidValue;
         return gn_launch(reinterpret_cast<const void*>(k), units * a.cluster, p.threads, smem, a.cluster, s, a);
     }
-    const GnKernel k = act == NORM_ACT_SILU   ? gn_fwd_split<T, VEC, ONE, NORM_ACT_SILU>
-                       : act == NORM_ACT_GELU ? gn_fwd_split<T, VEC, ONE, NORM_ACT_GELU>
-                                              : gn_fwd_split<T, VEC, ONE, NORM_ACT_NONE>;
-    return gn_launch_bands(reinterpret_cast<const void*>(k), p, a, units, 0,
-                           smem + static_cast<size_t>(GnStream<T, VEC, 1>::kRing) * p.threads, s);
+    const size_t all = smem + static_cast<size_t>(GnStream<T, VEC, 1>::kRing) * p.threads;
+    const cudaError_t e = gn_launch(reinterpret_cast<const void*>(gn_fwd_split_sums<T, VEC, ONE>), units * a.chunks,
+                                    p.threads, all, 1, s, a);
+    if (e != cudaSuccess) return e;
+    const GnKernel k = act == NORM_ACT_SILU   ? gn_fwd_split_apply<T, VEC, ONE, NORM_ACT_SILU>
+                       : act == NORM_ACT_GELU ? gn_fwd_split_apply<T, VEC, ONE, NORM_ACT_GELU>
+                                              : gn_fwd_split_apply<T, VEC, ONE, NORM_ACT_NONE>;
+    return gn_launch(reinterpret_cast<const void*>(k), units * a.out_chunks, p.threads, all, 1, s, a);
 }
 
 template <class T>

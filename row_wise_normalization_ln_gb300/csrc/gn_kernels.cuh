@@ -372,19 +372,6 @@ struct GnStream {
     }
 };
 
-// The part of a split launch this CTA takes: writing (`out`) and summing CTAs
-// alternate while both are left; `i` counts both. Returns the number of the
-// CTA among its kind.
-__device__ __forceinline__ int gn_role(int i, int out_ctas, int sum_ctas, bool* out) {
-    const int both = min(out_ctas, sum_ctas);
-    if (i < 2 * both) {
-        *out = (i & 1) == 0;
-        return i >> 1;
-    }
-    *out = out_ctas > sum_ctas;
-    return i - both;
-}
-
 // ------------------------------------------------------------ launch
 // Opts a kernel in to the device's largest dynamic shared memory per block
 // (once per kernel and device; not a stream operation).
@@ -432,26 +419,6 @@ inline cudaError_t gn_launch(const void* fn, int64_t grid, int threads, size_t s
     }
     void* args[] = {const_cast<GnArgs*>(&a)};
     return cudaLaunchKernelExC(&cfg, fn, args);
-}
-
-// The launches of the split path over `units` tiles in the plan's bands:
-// launch j sums band j and writes band j - 1. The last one also has the
-// `col_ctas` CTAs that add the partial rows of the column gradients.
-inline cudaError_t gn_launch_bands(const void* fn, const gn_plan& p, const GnArgs& a, int64_t units, int col_ctas,
-                                   size_t smem, cudaStream_t s) {
-    for (int j = 0; j <= p.bands; ++j) {
-        GnArgs b = a;
-        const int64_t u0 = j > 0 ? units * (j - 1) / p.bands : 0, u1 = units * j / p.bands;
-        const int64_t u2 = j < p.bands ? units * (j + 1) / p.bands : u1;
-        b.out_unit = static_cast<int32_t>(u0);
-        b.out_ctas = static_cast<int32_t>((u1 - u0) * a.out_chunks);
-        b.sum_unit = static_cast<int32_t>(u1);
-        b.sum_ctas = static_cast<int32_t>((u2 - u1) * a.chunks);
-        b.col_ctas = j == p.bands ? col_ctas : 0;
-        const cudaError_t e = gn_launch(fn, int64_t(b.out_ctas) + b.sum_ctas + b.col_ctas, p.threads, smem, 1, s, b);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
 }
 
 }  // namespace libnorm

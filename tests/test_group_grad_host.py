@@ -68,7 +68,7 @@ def test_empty_is_a_noop(lib):
 
 def test_workspace_refused_before_any_cuda_call(lib):
     plan = rn.GnPlan.from_dict(dict(path=1, vec_elems=4, tile=16, threads=256, per_thread=1, cluster=1, chunks=2,
-                                    out_chunks=1, bands=1))
+                                    out_chunks=1))
     n = ctypes.c_size_t()
     assert lib.gn_workspace_bytes(2, 8, 64, 4, rn.NORM_F32, 0, 0, ctypes.byref(plan), ctypes.byref(n)) == rn.NORM_OK
     assert n.value > 0

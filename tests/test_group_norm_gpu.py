@@ -198,15 +198,14 @@ def gn_plans(B, S, C, G, dtype, backward):
                     threads = -(-par * tile // 32) * 32
                     if threads <= 256:
                         out.append(dict(path=0, vec_elems=vec, tile=tile, threads=threads, per_thread=v,
-                                        cluster=cluster, chunks=1, out_chunks=1, bands=1))
+                                        cluster=cluster, chunks=1, out_chunks=1))
                 for threads in (128, 256):
                     if tile <= threads:
-                        for bands in range(1, 1 + min(3, B * -(-(C // vec) // tile))):
-                            out.append(dict(path=1, vec_elems=vec, tile=tile, threads=threads, per_thread=1,
-                                            cluster=1, chunks=2 * cluster - 1, out_chunks=9 - cluster, bands=bands))
+                        out.append(dict(path=1, vec_elems=vec, tile=tile, threads=threads, per_thread=1, cluster=1,
+                                        chunks=2 * cluster - 1, out_chunks=9 - cluster))
             for tile in (8, 37):  # groups that straddle tiles
                 out.append(dict(path=1, vec_elems=vec, tile=tile, threads=64, per_thread=1, cluster=1,
-                                chunks=3 * cluster, out_chunks=5, bands=1))
+                                chunks=3 * cluster, out_chunks=5))
     return out
 
 
@@ -463,6 +462,36 @@ def test_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip(res, want[k]))
 
 
+def test_large_tensors():
+    """Tensors beyond L2, forward and backward, in place too."""
+    for B, S, C, G, dt, act in ((1, 130001, 256, 32, torch.bfloat16, "silu"), (3, 70003, 320, 32, torch.float16, "gelu"),
+                                (2, 40009, 384, 2, torch.float32, None)):
+        x, dy, gamma, beta = make(B, S, C, dt, 8, loc=1.0)
+        y, mean, rstd = rn.gn_fwd(x, gamma, beta, G, EPS, activation=act)
+        dx, dg, db = rn.gn_bwd(dy, x, gamma, beta, mean, rstd, G, activation=act)
+        for b in range(B):  # (sample by sample: the 64-bit copies stay small)
+            check_fwd(x[b:b + 1], gamma, beta, G, act, y[b:b + 1], mean[b:b + 1], rstd[b:b + 1])
+        if B == 1:
+            check_bwd(dy, x, gamma, beta, mean, rstd, G, act, dx, dg, db)
+        else:
+            parts = [rn.gn_bwd(dy[b:b + 1], x[b:b + 1], gamma, beta, mean[b:b + 1], rstd[b:b + 1], G, activation=act)
+                     for b in range(B)]
+            for b in range(B):
+                check_bwd(dy[b:b + 1], x[b:b + 1], gamma, beta, mean[b:b + 1], rstd[b:b + 1], G, act, dx[b:b + 1],
+                          parts[b][1], parts[b][2])
+            # the columns of all samples: each sample's within its bound, one more fp32 addition each
+            for got, k in ((dg, 1), (db, 2)):
+                each = torch.stack([p[k] for p in parts]).to(F)
+                assert ((got.to(F) - each.sum(0)).abs() <= 64 * U * (S ** 0.5) * (each.abs().sum(0) + 8)).all()
+        y2 = rn.gn_fwd(x.clone(), gamma, beta, G, EPS, activation=act)[0]
+        x2 = x.clone()
+        rn.gn_fwd(x2, gamma, beta, G, EPS, activation=act, out=x2)
+        assert torch.equal(x2, y) and torch.equal(y2, y)
+        d2 = dy.clone()
+        rn.gn_bwd(d2, x, gamma, beta, mean, rstd, G, activation=act, dx=d2)
+        assert torch.equal(d2, dx)
+
+
 def test_random_shapes():
     rng = random.Random(7)
     for i in range(60):
@@ -482,8 +511,7 @@ def test_plans_that_do_not_fit_are_refused():
     good = rn.make_gn_plan(1, 1000, 64, 8, torch.bfloat16)
     for kw in (dict(path=7), dict(vec_elems=4), dict(threads=0), dict(threads=288), dict(tile=0), dict(tile=10 ** 6),
                dict(cluster=3), dict(cluster=16), dict(path=0, per_thread=1, cluster=1, threads=32, tile=1),
-               dict(path=1, cluster=2), dict(path=1, cluster=1, chunks=0), dict(path=1, cluster=1, out_chunks=0),
-               dict(path=1, cluster=1, bands=0), dict(path=1, cluster=1, bands=10 ** 6)):
+               dict(path=1, cluster=2), dict(path=1, cluster=1, chunks=0), dict(path=1, cluster=1, out_chunks=0)):
         with pytest.raises(rn.NormError):
             rn.gn_fwd(x, gamma, beta, 8, plan={**good, **kw})
     odd = torch.zeros(1000 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(1, 1000, 64)
