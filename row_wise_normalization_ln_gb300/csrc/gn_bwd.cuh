@@ -286,13 +286,16 @@ __device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, in
 
     const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, k));
     const int c = w.c0 + w.col * VEC;
+    const int visits = w.on ? GnVisits(rows, a).of(w.r) : 0;
+    const int64_t row = k * a.chunk_rows + w.r;
+    const T* const p[2] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c,
+                           static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c};
+    const int64_t step[2] = {int64_t(a.par) * a.xr, int64_t(a.par) * a.dyr};
     grid_wait();
+    // (the second launch may now start, and read its inputs before it waits for this one)
+    grid_release();
+    GnStream<T, VEC, 2> rows_in(p, step, visits, ring);
     if (w.on) {
-        const int visits = GnVisits(rows, a).of(w.r);
-        const int64_t row = k * a.chunk_rows + w.r;
-        const T* p[2] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c,
-                         static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c};
-        const int64_t step[2] = {int64_t(a.par) * a.xr, int64_t(a.par) * a.dyr};
         GnBwdCh<T, VEC, ONE, ACT> ch;
         ch.init(a, w.b, c);
         // full blocks of rows are added up in the row slot's states
@@ -307,7 +310,7 @@ __device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, in
         };
 #pragma unroll
         for (int i = 0; i < X::H; ++i) s1[i] = s2[i] = make_float2(0.f, 0.f);
-        GnStream<T, VEC, 2>::run(p, step, visits, ring, [&](int v, const auto& raw) {
+        rows_in.run([&](int v, const auto& raw) {
             if (v > 0 && (v & (kGnSumRows - 1)) == 0) {
                 fold(v == kGnSumRows);
 #pragma unroll
@@ -339,6 +342,17 @@ template <class T, int VEC, bool ONE, int ACT>
 __device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, int k, float2* sm, void* ring) {
     using X = GnVec<T, VEC>;
     float2* fin = sm;
+    const int c = w.c0 + w.col * VEC;
+    const int visits = w.on ? GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a).of(w.r) : 0;
+    // last rows first: what was summed last is the likeliest in L2
+    const int64_t row = k * a.out_rows + w.r + int64_t(visits - 1) * a.par;
+    const T* const p[2] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c,
+                           static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c};
+    const int64_t step[2] = {-int64_t(a.par) * a.xr, -int64_t(a.par) * a.dyr};
+    // (read before the wait for the sums, as in the forward)
+    GnStream<T, VEC, 2> rows_in(p, step, visits, ring);
+    GnBwdCh<T, VEC, ONE, ACT> ch;
+    if (w.on) ch.init(a, w.b, c);
     grid_wait();
     const GnShare sh(w.ng);
     const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
@@ -357,20 +371,11 @@ __device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, i
     }
     __syncthreads();
     if (!w.on) return;
-    const int visits = GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a).of(w.r);
-    const int c = w.c0 + w.col * VEC;
-    GnBwdCh<T, VEC, ONE, ACT> ch;
-    ch.init(a, w.b, c);
     GnBwdOut<T, VEC, ONE> out;
     out.init(a, c, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
-    // last rows first: what was summed last is the likeliest in L2
-    const int64_t row = k * a.out_rows + w.r + int64_t(visits - 1) * a.par;
-    const T* p[2] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c,
-                     static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c};
-    const int64_t step[2] = {-int64_t(a.par) * a.xr, -int64_t(a.par) * a.dyr};
     T* yp = static_cast<T*>(a.y) + w.b * a.yb + row * a.yr + c;
     const int64_t ystep = -int64_t(a.par) * a.yr;
-    GnStream<T, VEC, 2>::run(p, step, visits, ring, [&](int, const auto& raw) {
+    rows_in.run([&](int, const auto& raw) {
         X::store(yp, out.apply(ch, raw[0], raw[1]));
         yp += ystep;
     });
@@ -400,7 +405,6 @@ __device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, floa
 template <class T, int VEC, bool ONE, int ACT>
 __global__ void __launch_bounds__(kGnMaxThreads, 2) gn_bwd_split_sums(const GnArgs a) {
     extern __shared__ __align__(16) float2 slots[];  // the row stream's slots, then the merges' states
-    grid_release();
     const int unit = quot(blockIdx.x, a.by_chunks);
     gn_bwd_sums<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, unit), static_cast<int>(blockIdx.x) - unit * a.chunks,
                                   slots + GnStream<T, VEC, 2>::kRing / 8 * blockDim.x, slots);

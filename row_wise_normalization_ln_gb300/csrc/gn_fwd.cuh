@@ -364,9 +364,14 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
     const GnVisits vis(rows, a);
     const int c = w.c0 + w.col * VEC;
     const T* xs = static_cast<const T*>(a.x) + w.b * a.xb;
+    const int visits = w.on ? vis.of(w.r) : 0;
+    const T* const p[1] = {xs + (k * a.chunk_rows + w.r) * a.xr + c};
+    const int64_t step[1] = {int64_t(a.par) * a.xr};
     grid_wait();
+    // (the second launch may now start, and read x before it waits for this one)
+    grid_release();
+    GnStream<T, VEC, 1> rows_in(p, step, visits, ring);
     if (w.on) {
-        const int visits = vis.of(w.r);
         // Blocks of kGnShiftRows rows, shifted by the block's first value:
         // per channel, or for an access within a group in two chains over its
         // channels. A full block goes into the running state (S, m2), whose
@@ -396,9 +401,7 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
                 }
             }
         };
-        const T* p[1] = {xs + (k * a.chunk_rows + w.r) * a.xr + c};
-        const int64_t step[1] = {int64_t(a.par) * a.xr};
-        GnStream<T, VEC, 1>::run(p, step, visits, ring, [&](int v, const auto& raw) {
+        rows_in.run([&](int v, const auto& raw) {
             if ((v & (kGnShiftRows - 1)) == 0) {
                 if (v > 0) merge(v - kGnShiftRows, v);
 #pragma unroll
@@ -443,12 +446,21 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
     float2* fin = sm;                                   // (mu, rstd) per group of the tile
     float* shift = reinterpret_cast<float*>(sm + w.ng);
     const int c = w.c0 + w.col * VEC;
-    grid_wait();
-    typename X::Raw rg, rb;
+    const int visits = w.on ? GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a).of(w.r) : 0;
+    // last rows first: what was summed last is the likeliest in L2
+    const int64_t row = k * a.out_rows + w.r + int64_t(visits - 1) * a.par;
+    const T* const p[1] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c};
+    const int64_t step[1] = {-int64_t(a.par) * a.xr};
+    // The sums' launch lets this one start only once its own inputs are
+    // there (x, gamma, beta), and does not write them: they are read before
+    // the wait for the sums.
+    GnStream<T, VEC, 1> rows_in(p, step, visits, ring);
+    typename X::Raw rg = X::zero(), rb = X::zero();
     if (w.on) {
         rg = X::load(static_cast<const T*>(a.gamma) + c);
         rb = X::load(static_cast<const T*>(a.beta) + c);
     }
+    grid_wait();
     // The groups' states from every tile and chunk, lanes side by side.
     const GnShare sh(w.ng);
     const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
@@ -479,17 +491,12 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
     }
     __syncthreads();
     if (!w.on) return;
-    const int visits = GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a).of(w.r);
     GnOut<T, VEC, ONE, ACT> out;
     gn_per_group<T, VEC, ONE>(out.K, c, a, [&](int g) { return shift[min(g - w.g0, w.ng - 1)]; });
     out.init(rg, rb, c, a, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
-    // last rows first: what was summed last is the likeliest in L2
-    const int64_t row = k * a.out_rows + w.r + int64_t(visits - 1) * a.par;
-    const T* p[1] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c};
-    const int64_t step[1] = {-int64_t(a.par) * a.xr};
     T* yp = static_cast<T*>(a.y) + w.b * a.yb + row * a.yr + c;
     const int64_t ystep = -int64_t(a.par) * a.yr;
-    GnStream<T, VEC, 1>::run(p, step, visits, ring, [&](int, const auto& raw) {
+    rows_in.run([&](int, const auto& raw) {
         X::store(yp, out.apply(raw[0]));
         yp += ystep;
     });
@@ -499,7 +506,6 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
 template <class T, int VEC, bool ONE>
 __global__ void __launch_bounds__(kGnMaxThreads, ONE ? 4 : 3) gn_fwd_split_sums(const GnArgs a) {
     extern __shared__ __align__(16) float2 slots[];  // the row stream's slots, then the merges' states
-    grid_release();
     const int unit = quot(blockIdx.x, a.by_chunks);
     gn_fwd_sums<T, VEC, ONE>(a, gn_tile<VEC>(a, unit), static_cast<int>(blockIdx.x) - unit * a.chunks,
                              slots + GnStream<T, VEC, 1>::kRing / 8 * blockDim.x, slots);

@@ -306,30 +306,44 @@ struct GnStream {
     static constexpr int kBatch = 4;
     static constexpr int kRing = kAsync ? kStep * kSteps * N * kBytes : 0;  // bytes per thread
 
-    // Calls f(v, raw) for rows v = 0 .. visits - 1 in order; row v of tensor
-    // n is at p[n] + v * step[n].
-    template <class F>
-    static __device__ __forceinline__ void run(const T* (&p)[N], const int64_t (&step)[N], int visits, void* ring, F f) {
+    const T* p[N];      // the next row to copy (or load)
+    int64_t step[N];    // to the row after it
+    const int visits;
+    uint32_t base, pitch;  // this thread's first slot, and from one slot to the next
+    int sent = 0;          // rows whose copies have been issued
+
+    // Row v of tensor n is at first[n] + v * step_[n]; the first copies are
+    // issued at once, so that what is done until run() overlaps them.
+    __device__ __forceinline__ GnStream(const T* const (&first)[N], const int64_t (&step_)[N], int visits_, void* ring)
+        : visits(visits_), base(smem_addr(ring) + threadIdx.x * kBytes), pitch(blockDim.x * kBytes) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            p[n] = first[n];
+            step[n] = step_[n];
+        }
         if constexpr (kAsync) {
-            const uint32_t pitch = blockDim.x * kBytes;  // between a thread's slots
-            const uint32_t base = smem_addr(ring) + threadIdx.x * kBytes;
-            int sent = 0;  // rows whose copies have been issued
-            auto send = [&](int slot) {
-#pragma unroll
-                for (int u = 0; u < kStep; ++u) {
-                    if (sent < visits) {
-#pragma unroll
-                        for (int n = 0; n < N; ++n) {
-                            copy_async<kBytes>(base + ((slot * kStep + u) * N + n) * pitch, p[n]);
-                            p[n] += step[n];
-                        }
-                    }
-                    ++sent;
-                }
-                copy_async_commit();
-            };
 #pragma unroll
             for (int s = 0; s < kSteps - 1; ++s) send(s);
+        }
+    }
+    __device__ __forceinline__ void send(int slot) {
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+            if (sent < visits) {
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    copy_async<kBytes>(base + ((slot * kStep + u) * N + n) * pitch, p[n]);
+                    p[n] += step[n];
+                }
+            }
+            ++sent;
+        }
+        copy_async_commit();
+    }
+    // Calls f(v, raw) for rows v = 0 .. visits - 1 in order.
+    template <class F>
+    __device__ __forceinline__ void run(F f) {
+        if constexpr (kAsync) {
             int slot = 0;
             for (int v = 0; v < visits; v += kStep) {
                 copy_async_wait<kSteps - 2>();  // this step's copies have landed
@@ -359,9 +373,8 @@ struct GnStream {
                 Raw raw[kBatch][N];
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u)
-                    if (v + u < visits)
 #pragma unroll
-                        for (int n = 0; n < N; ++n) raw[u][n] = X::load(p[n] + u * step[n]);
+                    for (int n = 0; n < N; ++n) raw[u][n] = v + u < visits ? X::load(p[n] + u * step[n]) : X::zero();
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u)
                     if (v + u < visits) f(v + u, raw[u]);
