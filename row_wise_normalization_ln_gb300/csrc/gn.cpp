@@ -125,7 +125,9 @@ norm_status derive(const gn_plan& p, const Shape& s, GnArgs* a) {
                                         : static_cast<int32_t>(std::min<int64_t>(p.vec_elems, (p.vec_elems - 2 + s.D) / s.D + 1));
     const int states = a->tile * (s.bwd ? p.vec_elems : a->segs);
     const int64_t groups = libnorm::gn_tile_groups(int64_t(a->tile) * p.vec_elems, s.D, false);
-    if (libnorm::gn_smem_bytes(a->par, states, static_cast<int>(groups), p.threads) > kMaxSmem) return NORM_ERR_PLAN;
+    const int64_t smem = libnorm::gn_smem_bytes(a->par, states, static_cast<int>(groups), p.threads);
+    if (smem > kMaxSmem) return NORM_ERR_PLAN;
+    a->ring_at = static_cast<int32_t>(smem / 16);
     if (p.path == GN_PATH_CHIP) {
         if (!whole || !is_pow2(p.per_thread) || p.per_thread > maxv) return NORM_ERR_PLAN;
         a->tpg = 1;

@@ -404,26 +404,26 @@ __device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, floa
 // column gradients, in its first CTAs.
 template <class T, int VEC, bool ONE, int ACT>
 __global__ void __launch_bounds__(kGnMaxThreads, 2) gn_bwd_split_sums(const GnArgs a) {
-    extern __shared__ __align__(16) float2 slots[];  // the row stream's slots, then the merges' states
+    extern __shared__ __align__(16) float2 states[];  // the merges' states, then the row stream's slots
     const int unit = quot(blockIdx.x, a.by_chunks);
     gn_bwd_sums<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, unit), static_cast<int>(blockIdx.x) - unit * a.chunks,
-                                  slots + GnStream<T, VEC, 2>::kRing / 8 * blockDim.x, slots);
+                                  states, states + 2 * a.ring_at);
 }
 
 template <class T, int VEC, bool ONE, int ACT>
 __global__ void __launch_bounds__(kGnMaxThreads, 2) gn_bwd_split_apply(const GnArgs a) {
-    extern __shared__ __align__(16) float2 slots[];
-    float2* sm = slots + GnStream<T, VEC, 2>::kRing / 8 * blockDim.x;
+    extern __shared__ __align__(16) float2 states[];
     grid_release();
     const int adders = a.partials > 1 ? (a.C + 31) / 32 : 0;
     const int i = static_cast<int>(blockIdx.x) - adders;
     if (i < 0) {
         grid_wait();
-        gn_bwd_add_cols(a, blockIdx.x, sm);
+        gn_bwd_add_cols(a, blockIdx.x, states);
         return;
     }
     const int unit = quot(i, a.by_out_chunks);
-    gn_bwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, unit), i - unit * a.out_chunks, sm, slots);
+    gn_bwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, unit), i - unit * a.out_chunks, states,
+                                   states + 2 * a.ring_at);
 }
 
 // ------------------------------------------------------------ launch
@@ -443,13 +443,15 @@ cudaError_t gn_launch_bwd(const gn_plan& p, const GnArgs& a, int64_t B, cudaStre
         return gn_launch(k, B * a.tiles * a.cluster, p.threads, smem, a.cluster * a.join, s, a);
     }
     const int64_t units = B * a.tiles;
-    const size_t all = smem + static_cast<size_t>(GnStream<T, VEC, 2>::kRing) * p.threads;
+    const auto all = [&](int64_t rows) {
+        return smem + GnStream<T, VEC, 2>::ring_bytes((rows + a.par - 1) / a.par, p.threads);
+    };
     const cudaError_t e = gn_launch(reinterpret_cast<const void*>(gn_bwd_split_sums<T, VEC, ONE, ACT>),
-                                    units * a.chunks, p.threads, all, 1, s, a);
+                                    units * a.chunks, p.threads, all(a.chunk_rows), 1, s, a);
     if (e != cudaSuccess) return e;
     const int64_t adders = a.partials > 1 ? (a.C + 31) / 32 : 0;
     return gn_launch(reinterpret_cast<const void*>(gn_bwd_split_apply<T, VEC, ONE, ACT>),
-                     units * a.out_chunks + adders, p.threads, all, 1, s, a);
+                     units * a.out_chunks + adders, p.threads, all(a.out_rows), 1, s, a);
 }
 
 template <class T, int VEC, bool ONE>

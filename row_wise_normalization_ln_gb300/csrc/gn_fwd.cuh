@@ -505,19 +505,19 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
 // The split path's two launches, one CTA per tile and chunk.
 template <class T, int VEC, bool ONE>
 __global__ void __launch_bounds__(kGnMaxThreads, ONE ? 4 : 3) gn_fwd_split_sums(const GnArgs a) {
-    extern __shared__ __align__(16) float2 slots[];  // the row stream's slots, then the merges' states
+    extern __shared__ __align__(16) float2 states[];  // the merges' states, then the row stream's slots
     const int unit = quot(blockIdx.x, a.by_chunks);
     gn_fwd_sums<T, VEC, ONE>(a, gn_tile<VEC>(a, unit), static_cast<int>(blockIdx.x) - unit * a.chunks,
-                             slots + GnStream<T, VEC, 1>::kRing / 8 * blockDim.x, slots);
+                             states, states + 2 * a.ring_at);
 }
 
 template <class T, int VEC, bool ONE, int ACT>
 __global__ void __launch_bounds__(kGnMaxThreads, ONE ? 4 : 3) gn_fwd_split_apply(const GnArgs a) {
-    extern __shared__ __align__(16) float2 slots[];
+    extern __shared__ __align__(16) float2 states[];
     grid_release();
     const int unit = quot(blockIdx.x, a.by_out_chunks);
     gn_fwd_apply<T, VEC, ONE, ACT>(a, gn_tile<VEC>(a, unit), static_cast<int>(blockIdx.x) - unit * a.out_chunks,
-                                   slots + GnStream<T, VEC, 1>::kRing / 8 * blockDim.x, slots);
+                                   states, states + 2 * a.ring_at);
 }
 
 // ------------------------------------------------------------ launch
@@ -547,14 +547,16 @@ cudaError_t gn_launch_fwd(const gn_plan& p, const GnArgs& a, norm_act act, int64
         if (k == nullptr) return cudaErrorInvalidValue;
         return gn_launch(reinterpret_cast<const void*>(k), units * a.cluster, p.threads, smem, a.cluster, s, a);
     }
-    const size_t all = smem + static_cast<size_t>(GnStream<T, VEC, 1>::kRing) * p.threads;
+    const auto all = [&](int64_t rows) {
+        return smem + GnStream<T, VEC, 1>::ring_bytes((rows + a.par - 1) / a.par, p.threads);
+    };
     const cudaError_t e = gn_launch(reinterpret_cast<const void*>(gn_fwd_split_sums<T, VEC, ONE>), units * a.chunks,
-                                    p.threads, all, 1, s, a);
+                                    p.threads, all(a.chunk_rows), 1, s, a);
     if (e != cudaSuccess) return e;
     const GnKernel k = act == NORM_ACT_SILU   ? gn_fwd_split_apply<T, VEC, ONE, NORM_ACT_SILU>
                        : act == NORM_ACT_GELU ? gn_fwd_split_apply<T, VEC, ONE, NORM_ACT_GELU>
                                               : gn_fwd_split_apply<T, VEC, ONE, NORM_ACT_NONE>;
-    return gn_launch(reinterpret_cast<const void*>(k), units * a.out_chunks, p.threads, all, 1, s, a);
+    return gn_launch(reinterpret_cast<const void*>(k), units * a.out_chunks, p.threads, all(a.out_rows), 1, s, a);
 }
 
 template <class T>
