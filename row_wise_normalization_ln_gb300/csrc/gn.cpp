@@ -180,6 +180,12 @@ bool chip_plan(const Shape& s, int vec, int sms, gn_plan* p) {
         // (gn_bwd f32 3x1517x180 13 us against 10)
         if (s.bwd && cs > 1 && s.B * cs > kMaxCluster) break;
         if (found && (rows * tile < 256 || units * cs > 4 * int64_t(sms))) break;
+        // The largest clusters lose to the split path where they are many CTAs
+        // per SM (gn_fwd f32 16x1024x1280 58 us against 45; in clusters of 4,
+        // f32 8x1024x640, 16.8 against 18.5), and, at the most rows per thread,
+        // where they leave SMs without one (bf16 1x4096x512 9.6 us against
+        // 7.8, 2x2048x320 8.6 against 7.7).
+        if (cs == kMaxCluster && (units * cs > 4 * int64_t(sms) || (v == maxv && units * cs < sms))) break;
         p->path = GN_PATH_CHIP;
         p->vec_elems = vec;
         p->tile = static_cast<int32_t>(tile);
@@ -206,11 +212,15 @@ void split_plan(const Shape& s, int vec, int sms, gn_plan* p) {
     p->cluster = 1;
     const int64_t units = std::max<int64_t>(1, s.B * ceil_div(ncols, tile));
     const int64_t rows = p->threads / tile;
-    // Two CTAs per SM; one where that leaves a thread fewer than 8 rows (the
-    // merges then cost more than the rows: gn_fwd bf16 2x4096x320 9.6 us with
-    // 152 CTAs, 12.0 with 304; gn_bwd f16 8x4096x320, 18 rows each, 23 us with
-    // 288 and 28 with 152).
-    const int64_t chunks = std::min(int64_t(sms) * 2 / units, std::max(int64_t(sms) / units, s.S / (rows * 8)));
+    // One CTA per SM while a thread has few rows, two per SM otherwise; counts
+    // between leave some SMs with twice the rows of others. Measured in us with
+    // one / two per SM, at the rows per thread that one gives: gn_fwd bf16
+    // 2x4096x320 (9 rows) 9.1 / 11.5, 1x16384x256 (14) 9.6 / 9.9, 2x8192x320
+    // (18) 11.9 / 14.3, f32 2x4096x320 (19) 11.9 / 11.7, bf16 8x4096x320 (41)
+    // 23.2 / 20.0; gn_bwd f32 3x1517x180 (6) 8.1 / 8.9, bf16 1x4096x512 (7)
+    // 11.1 / 9.7, 2x4096x320 (9) 12.9 / 12.5, 4x4096x320 (19) 19.4 / 16.0.
+    const int64_t once = std::max<int64_t>(1, sms / units);
+    const int64_t chunks = ceil_div(ceil_div(s.S, once), rows) <= (s.bwd ? 6 : 18) ? once : int64_t(sms) * 2 / units;
     const int64_t most = std::max<int64_t>(1, ceil_div(s.S, rows));
     p->chunks = static_cast<int32_t>(std::max(std::min(std::max<int64_t>(1, chunks), most), ceil_div(s.S, int64_t(1) << 30)));
     p->out_chunks = p->chunks;
