@@ -143,18 +143,49 @@ __device__ __noinline__ double exact_squares(const uint4* v, int n) {
     return s;
 }
 
-// Whether fp32 squares may have left the range: the sum is not finite, or so
-// small that squares may have been lost below fp32's smallest values (which
-// is fine where every value is 0). Otherwise what a lost square was worth is
-// below 2^-60 of the sum.
+// Whether fp32 squares may have left the range: the sum is not finite or near
+// the end of the range, or so small that squares may have been lost below
+// fp32's smallest values (which is fine where every value is 0). Otherwise
+// what a lost square was worth is below 2^-60 of the sum.
 constexpr float kSmallSum = 8.27180613e-25f;  // 2^-80
+constexpr float kLargeSum = 1.32922800e36f;   // 2^120
+__device__ __forceinline__ bool in_range(float s) { return s >= kSmallSum && s <= kLargeSum; }
 
-// The squares of the n accesses r (the rest zero), kThreads apart from v on.
+// A thread's sum: fp32 sums in range are added as an unevaluated pair with
+// the error of each addition kept (Knuth's two-sum), 46 bits or more, and the
+// rest in fp64, which stays 0 in the usual case. (The fp64 unit is a
+// sixty-fourth of the fp32 ones: fp64 additions across the lanes of 32 warps
+// per SM were a microsecond at the end of every launch.)
+struct Sum {
+    float hi = 0.f, lo = 0.f;
+    double far = 0.0;
+
+    __device__ __forceinline__ void pair(float h, float l) {
+        const float t = hi + h, b = t - hi;
+        lo += ((hi - (t - b)) + (h - b)) + l;
+        hi = t;
+    }
+    __device__ __forceinline__ void add(float s) {
+        pair(s, 0.f);
+        if (hi > kLargeSum) {
+            far += static_cast<double>(hi) + static_cast<double>(lo);
+            hi = lo = 0.f;
+        }
+    }
+    __device__ __forceinline__ void add_square(float v) {
+        const float s = v * v;
+        if (in_range(s)) add(s);
+        else far = fma(static_cast<double>(v), static_cast<double>(v), far);
+    }
+};
+
+// Adds the squares of the n accesses r (the rest zero), kThreads apart from v
+// on.
 // (Accesses that a thread does not have are set, not skipped: a register that
 // is written under a predicate alone stays live through the whole loop, which
 // tripled the registers.)
 template <int DT>
-__device__ __forceinline__ double squares(const uint4 (&r)[kUnroll], int n, const uint4* v) {
+__device__ __forceinline__ void squares(const uint4 (&r)[kUnroll], int n, const uint4* v, Sum& sum) {
     float2 a = make_float2(0.f, 0.f), b = a;
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
@@ -162,14 +193,15 @@ __device__ __forceinline__ double squares(const uint4 (&r)[kUnroll], int n, cons
         else a = add_squares<DT>(r[k], a);
     }
     const float s = (a.x + a.y) + (b.x + b.y);
-    if (!(s >= kSmallSum && s <= 3.0e38f)) {
-        uint32_t any = 0;
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-            any |= r[k].x | r[k].y | r[k].z | r[k].w;
-        if (any != 0) return exact_squares<DT>(v, n);
+    if (in_range(s)) {
+        sum.add(s);
+        return;
     }
-    return static_cast<double>(s);
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+        any |= r[k].x | r[k].y | r[k].z | r[k].w;
+    if (any != 0) sum.far += exact_squares<DT>(v, n);
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -178,13 +210,22 @@ __device__ __forceinline__ double warp_sum(double v) {
 }
 
 // Sum over a CTA, in thread 0 (elsewhere undefined).
-__device__ __forceinline__ double cta_sum(double v, double* part) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+__device__ __forceinline__ double cta_sum(Sum v, double* part) {
+    double w;
+    if (__any_sync(kFullMask, v.far != 0.0)) {  // (NaN too)
+        w = warp_sum(v.far + (static_cast<double>(v.hi) + static_cast<double>(v.lo)));
+    } else {
+        for (int off = 16; off > 0; off >>= 1) {
+            const float h = __shfl_xor_sync(kFullMask, v.hi, off), l = __shfl_xor_sync(kFullMask, v.lo, off);
+            v.pair(h, l);
+        }
+        w = static_cast<double>(v.hi) + static_cast<double>(v.lo);
+    }
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = w;
     __syncthreads();
-    const int warps = blockDim.x >> 5;
-    if (threadIdx.x >= 32) return 0.0;
-    return warp_sum(static_cast<int>(threadIdx.x) < warps ? part[threadIdx.x] : 0.0);
+    if (threadIdx.x != 0) return 0.0;
+    static_assert(kThreads / 32 == 8, "eight partial sums");
+    return ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
 }
 
 // sqrt(s) by one Newton step in fp64 from fp32's root (48 bits or more):
@@ -216,19 +257,13 @@ __device__ __forceinline__ int accesses(int64_t left, int64_t units) {
 
 // The units [u, stop) of one tensor: squares of this thread's values.
 template <int DT>
-__device__ __forceinline__ double piece_squares(const void* p, int64_t numel, int64_t u, int64_t stop, int64_t units, int tid) {
+__device__ __forceinline__ void piece_squares(const void* p, int64_t numel, int64_t u, int64_t stop, int64_t units, int tid,
+                                              Sum& sum) {
     const Span s = span_of(p, numel, DT == NORM_F32 ? 4 : 2);
     const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + s.head * (DT == NORM_F32 ? 4 : 2));
-    double sum = 0.0;
-    if (u == 0 && tid < s.head) {
-        const double x = value_at(p, tid, DT);
-        sum = fma(x, x, sum);
-    }
+    if (u == 0 && tid < s.head) sum.add_square(value_at(p, tid, DT));
     const int64_t tail = s.head + s.vecs * s.per;
-    if (stop == units && tail + tid < numel) {
-        const double x = value_at(p, tail + tid, DT);
-        sum = fma(x, x, sum);
-    }
+    if (stop == units && tail + tid < numel) sum.add_square(value_at(p, tail + tid, DT));
 #pragma unroll 1
     for (; u < stop; u += kUnroll) {
         const uint4* at = v + u * kThreads + tid;
@@ -237,18 +272,17 @@ __device__ __forceinline__ double piece_squares(const void* p, int64_t numel, in
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
             r[k] = k < n ? at[k * kThreads] : make_uint4(0, 0, 0, 0);
-        if (n > 0) sum += squares<DT>(r, n, at);
+        if (n > 0) squares<DT>(r, n, at, sum);
     }
-    return sum;
 }
 
 // Share i of n of the list: the sum of squares of this thread's values.
 template <int CAP>
-__device__ __forceinline__ double share_squares(const GradTable<CAP>& t, int64_t i, int64_t n, int tid) {
+__device__ __forceinline__ Sum share_squares(const GradTable<CAP>& t, int64_t i, int64_t n, int tid) {
     const int64_t all = t.first[t.count];
     int64_t u = all * i / n;
     const int64_t end = all * (i + 1) / n;
-    double sum = 0.0;
+    Sum sum;
     if (u < end) {
 #pragma unroll 1
         for (int k = tensor_of(t, u); u < end; ++k) {
@@ -257,9 +291,9 @@ __device__ __forceinline__ double share_squares(const GradTable<CAP>& t, int64_t
             const int64_t a = u - first, b = min(units, end - first);
             const void* p = t.data[k];
             const int dt = t.dtype[k];
-            if (dt == NORM_F32) sum += piece_squares<NORM_F32>(p, t.numel[k], a, b, units, tid);
-            else if (dt == NORM_BF16) sum += piece_squares<NORM_BF16>(p, t.numel[k], a, b, units, tid);
-            else sum += piece_squares<NORM_F16>(p, t.numel[k], a, b, units, tid);
+            if (dt == NORM_F32) piece_squares<NORM_F32>(p, t.numel[k], a, b, units, tid, sum);
+            else if (dt == NORM_BF16) piece_squares<NORM_BF16>(p, t.numel[k], a, b, units, tid, sum);
+            else piece_squares<NORM_F16>(p, t.numel[k], a, b, units, tid, sum);
             u = first + b;
         }
     }
@@ -307,36 +341,77 @@ __device__ __forceinline__ uint4 scaled(const uint4& r, float coef) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// A thread's value of the first few and of the last few (0 where it has
+// none): read before the whole accesses, used after them, so that a piece
+// waits for memory once.
+template <int DT>
+struct Edges {
+    float head = 0.f, tail = 0.f;
+    int first, last;  // how many there are
+    __device__ __forceinline__ Edges(const void* p, int64_t numel, int64_t head_values, int64_t tail_at, bool has_head,
+                                     bool has_tail, int tid)
+        : first(has_head ? static_cast<int>(head_values) : 0), last(has_tail ? static_cast<int>(numel - tail_at) : 0) {
+        if (tid < first) head = value_at(p, tid, DT);
+        if (tid < last) tail = value_at(p, numel - last + tid, DT);
+    }
+    __device__ __forceinline__ void put(void* out, int64_t numel, float coef, int tid) const {
+        if (tid < first) put_at(out, tid, DT, head * coef);
+        if (tid < last) put_at(out, numel - last + tid, DT, tail * coef);
+    }
+};
+
+// The 16 bytes from byte `by` of (a, b) on.
+__device__ __forceinline__ uint4 straddled(const uint4& a, const uint4& b, int by) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = by & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = by & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (by & 2) * 8);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The units [u, stop) of one tensor, from the last to the first.
 template <int DT>
 __device__ __forceinline__ void piece_scale(const void* p, void* out, int64_t numel, int64_t u, int64_t stop,
                                             int64_t units, float coef, int tid) {
     constexpr int es = DT == NORM_F32 ? 4 : 2;
-    const Span s = span_of(p, numel, es);
-    const int64_t tail = s.head + s.vecs * s.per;
-    if (u == 0 && tid < s.head)
-        put_at(out, tid, DT, value_at(p, tid, DT) * coef);
-    if (stop == units && tail + tid < numel)
-        put_at(out, tail + tid, DT, value_at(p, tail + tid, DT) * coef);
-    if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
-        // out lies at another offset within 16 bytes: value by value, kUnroll
-        // of them in flight per thread, neighbours side by side
-        const int64_t lo = s.head + min(s.vecs, u * kThreads) * s.per, hi = s.head + min(s.vecs, stop * kThreads) * s.per;
+    const uintptr_t from = reinterpret_cast<uintptr_t>(p), to = reinterpret_cast<uintptr_t>(out);
+    if (((from ^ to) & 15) != 0) {
+        // out lies at another offset within 16 bytes: whole accesses of out,
+        // each from the two accesses of p that it straddles, where both lie
+        // within the tensor
+        Span s = span_of(out, numel, es);
+        if (s.head < numel && ((from + s.head * es) & ~uintptr_t(15)) < from) s.head += s.per;
+        s.head = min(s.head, numel);
+        const uintptr_t base = (from + s.head * es) & ~uintptr_t(15);
+        const int by = static_cast<int>((from + s.head * es) & 15);
+        s.vecs = max(int64_t(0), static_cast<int64_t>(from + numel * es - base) / 16 - 1);
+        const Edges<DT> edges(p, numel, s.head, s.head + s.vecs * s.per, u == 0, stop == units, tid);
+        const uint4* v = reinterpret_cast<const uint4*>(base);
+        uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(out) + s.head * es);
+        constexpr int kPairs = 3;  // (4 spill)
 #pragma unroll 1
-        for (int64_t i = lo + tid; i < hi; i += kUnroll * kThreads) {
-            const int n = accesses(hi - i, kUnroll);
-            const void* from = static_cast<const char*>(p) + i * es;
-            void* to = static_cast<char*>(out) + i * es;
-            float r[kUnroll];
+        for (int64_t e = stop; e > u; e -= kPairs) {
+            const int64_t f = max(u, e - kPairs);
+            const int64_t i = f * kThreads + tid;
+            const int n = accesses(s.vecs - i, e - f);
+            uint4 a[kPairs], b[kPairs];
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
-                r[k] = k < n ? value_at(from, k * kThreads, DT) : 0.f;
+            for (int k = 0; k < kPairs; ++k) {
+                a[k] = k < n ? v[i + k * kThreads] : make_uint4(0, 0, 0, 0);
+                b[k] = k < n ? v[i + k * kThreads + 1] : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
-                if (k < n) put_at(to, k * kThreads, DT, r[k] * coef);
+            for (int k = 0; k < kPairs; ++k)
+                if (k < n) o[i + k * kThreads] = scaled<DT>(straddled(a[k], b[k], by), coef);
         }
+        edges.put(out, numel, coef, tid);
         return;
     }
+    const Span s = span_of(p, numel, es);
+    const Edges<DT> edges(p, numel, s.head, s.head + s.vecs * s.per, u == 0, stop == units, tid);
     const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + s.head * es);
     uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(out) + s.head * es);
 #pragma unroll 1
@@ -352,6 +427,7 @@ __device__ __forceinline__ void piece_scale(const void* p, void* out, int64_t nu
         for (int k = 0; k < kUnroll; ++k)
             if (k < n) o[i + k * kThreads] = scaled<DT>(r[k], coef);
     }
+    edges.put(out, numel, coef, tid);
 }
 
 // Share i of n of the list, from its end: times coef.
@@ -591,10 +667,9 @@ cudaError_t pass(const norm_tensor* ts, int64_t count, bool clip, int64_t ctas, 
         void* args[] = {&t, &partial};
         return launch(reinterpret_cast<const void*>(grad_sums<CAP>), ctas, kThreads, stream, args);
     }
-    const int64_t grid = std::max<int64_t>(1, std::min(ctas, t.first[count]));
     const double* src = partial;
     void* args[] = {&t, &src, &n, &max_norm, &norm};
-    return launch(reinterpret_cast<const void*>(grad_scale<CAP>), grid, kThreads, stream, args);
+    return launch(reinterpret_cast<const void*>(grad_scale<CAP>), ctas, kThreads, stream, args);
 }
 
 cudaError_t any_pass(const norm_tensor* ts, int64_t count, bool clip, int64_t ctas, double* partial, int64_t n,
@@ -695,12 +770,19 @@ norm_status run(const norm_tensor* ts, int64_t count, bool clip, float max_norm,
         return NORM_ERR_CUDA;
     }
     double* partial = static_cast<double*>(ws);
-    const int64_t most = int64_t(sms) * kCtasPerSm;
+    // As many CTAs on each SM as let one read its share in one step of kUnroll
+    // units, kCtasPerSm at most: grad_clip of 24 fp32 and 24 bf16 tensors of
+    // 45009 values 12.6 us with the 304 of this rule, 14.0 with 152 or 608;
+    // of 16 MB in one tensor 14.3 with 608, 17.6 with 456.
+    const auto ctas_of = [&](int64_t units) {
+        const int64_t per_sm = ceil_div(units, int64_t(sms) * kUnroll);
+        return std::min(units, sms * std::max<int64_t>(1, std::min<int64_t>(kCtasPerSm, per_sm)));
+    };
     int64_t n = 0;
     for (int64_t at = 0; at < count; at += kMaxTable) {
         const int64_t k = std::min<int64_t>(kMaxTable, count - at);
         const int64_t units = units_of(ts + at, k);
-        const int64_t ctas = std::min(most, units);
+        const int64_t ctas = ctas_of(units);
         if (ctas == 0) continue;
         e = any_pass(ts + at, k, false, ctas, partial + n, 0, 0.f, nullptr, stream);
         if (e != cudaSuccess) break;
@@ -711,9 +793,11 @@ norm_status run(const norm_tensor* ts, int64_t count, bool clip, float max_norm,
         void* args[] = {&src, &n, &norm};
         e = launch(reinterpret_cast<const void*>(grad_finish), 1, 32, stream, args);
     }
-    for (int64_t at = 0; e == cudaSuccess && clip && at < std::max<int64_t>(count, 1); at += kMaxTable)
-        e = any_pass(ts + at, std::min<int64_t>(kMaxTable, count - at), true, most, partial, n, max_norm,
+    for (int64_t at = 0; e == cudaSuccess && clip && at < std::max<int64_t>(count, 1); at += kMaxTable) {
+        const int64_t k = std::min<int64_t>(kMaxTable, count - at);
+        e = any_pass(ts + at, k, true, std::max<int64_t>(1, ctas_of(units_of(ts + at, k))), partial, n, max_norm,
                      at == 0 ? norm : nullptr, stream);
+    }
     if (e != cudaSuccess) {
         note_cuda_error(static_cast<int>(e));
         return NORM_ERR_CUDA;

@@ -2,8 +2,9 @@
 arithmetic.
 
 Tolerances: the norm's squares are added in fp32 over at most 64 values in
-two chains or more, then in fp64: relative error of the sum at most 33 u
-(u = 2^-24), of the norm 17 u, plus its own rounding: 18 u. A clipped value is
+two chains or more (short lists: 32 values, then a tree of 5 levels), then in
+fp64 or as pairs of fp32 numbers with every error kept: relative error of the
+sum at most 33 u (u = 2^-24), of the norm 17 u, plus its own rounding: 18 u. A clipped value is
 v * coef with coef rounded once from fp64 (its error: u, and the norm's does
 not enter, the coefficient comes from the fp64 sum: 17 u) and the product
 rounded once in fp32 and once to the type: 20 u |v coef| + eta |v coef| + half
@@ -108,6 +109,31 @@ def test_offsets_and_guards(dtype, off_in, off_out):
         assert not a.any()
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_every_pair_of_phases(dtype):
+    """Inputs and outputs at every pair of offsets within 16 bytes, lengths
+    around one and two accesses, one and several units: every value clipped,
+    nothing beside it written."""
+    per = 16 // dtype.itemsize
+    lengths = [1, per - 1, per, per + 1, 2 * per - 1, 2 * per + 1, 3 * per, 256 * per - 1, 256 * per + per + 1, 2000 * per + 3]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ins, outs, pads = [], [], []
+    for a in range(per):
+        for b in range(per):
+            for n in lengths:
+                ins.append(torch.randn(n + 2 * per, generator=g, device="cuda").to(dtype)[a:a + n])
+                pads.append(torch.full((n + 3 * per,), 7.0, device="cuda", dtype=dtype))
+                outs.append(pads[-1][per + b:per + b + n])
+    _, norm = rn.grad_clip(ins, 1.0, out=outs)
+    check_clip(ins, outs, 1.0, norm)
+    at = 0
+    for a in range(per):
+        for b in range(per):
+            for n in lengths:
+                assert (pads[at][:per + b] == 7).all() and (pads[at][per + b + n:] == 7).all()
+                at += 1
+
+
 def test_flat_buffer_of_neighbours():
     """Neighbouring views of one buffer, clipped in place: each once."""
     flat = torch.randn(30000, device="cuda").bfloat16()
@@ -119,7 +145,7 @@ def test_flat_buffer_of_neighbours():
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
-@pytest.mark.parametrize("size", [1e25, 1e19, 1e-19, 1e-25, 1e-37])
+@pytest.mark.parametrize("size", [1e25, 1e19, 3e17, 1e17, 1e-12, 1e-13, 1e-19, 1e-25, 1e-37])
 def test_squares_beyond_fp32(dtype, size):
     """Values whose squares overflow or vanish in fp32."""
     ts = tensors([(1000,), (33, 77), (5,)], [dtype], 3, size)
@@ -127,6 +153,18 @@ def test_squares_beyond_fp32(dtype, size):
     ts.append(torch.zeros(5000, dtype=dtype, device="cuda"))
     check_norm(ts, rn.grad_norm(ts))
     ts.append(tensors([(3000,)], [dtype], 4, 1.0)[0])
+    check_norm(ts, rn.grad_norm(ts))
+
+
+@pytest.mark.parametrize("size", [1e25, 1e19, 3e17, 1e17, 1e-12, 1e-13, 1e-19, 1e-25, 1e-37])
+@pytest.mark.parametrize("numel", [300001, 40 * (1 << 20) + 3])
+def test_long_lists_beyond_fp32(numel, size):
+    """The same over many CTAs and, for the longer list, many steps of each:
+    sums that leave fp32's range although every step's is within it."""
+    ts = tensors([(numel,)], [torch.float32], 3, size)
+    ts[0] = ts[0][1:]
+    check_norm(ts, rn.grad_norm(ts))
+    ts.append(tensors([(70001,)], [torch.bfloat16], 4, 1.0)[0][3:])
     check_norm(ts, rn.grad_norm(ts))
 
 
