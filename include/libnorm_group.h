@@ -60,6 +60,7 @@ typedef struct {
  *   rstd_bg = 1 / sqrt(var_bg + eps)
  *   y = act((x - mean_bg) * rstd_bg * gamma_c + beta_c)
  * x, gamma, beta, y of `dtype`; mean, rstd fp32 [B, G], each may be NULL.
+ * A group that holds an infinity or a NaN has NaN for mean, rstd and y.
  * y may be x itself (same pitches); any other overlap is undefined.
  * `workspace`: device memory of the caller, 16-byte aligned, of at least
  * gn_workspace_bytes() (may be NULL when that is 0); nothing in it needs a

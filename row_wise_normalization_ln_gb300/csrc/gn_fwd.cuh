@@ -150,21 +150,15 @@ __device__ __forceinline__ void gn_merge_cluster(const float4* gs, int ng, int w
     }
 }
 
-// The mean relative to the shift of a merged state, rounded once, and K plus
-// it, rounded once.
-__device__ __forceinline__ float2 gn_quotient(const float4& t) {
+// The mean of a group from its first element K and its merged state, rounded
+// once, and what the rounding left.
+__device__ __forceinline__ float2 gn_mean(float K, const float4& t) {
     const float q = __fdiv_rn(t.x, t.w);
-    return make_float2(q, __fdividef(fmaf(-q, t.w, t.x) + t.y, t.w));  // the quotient and what it leaves
-}
-__device__ __forceinline__ float gn_mu(const float4& t) {
-    const float2 q = gn_quotient(t);
-    return q.x + q.y;
-}
-__device__ __forceinline__ float gn_mean(float K, const float4& t) {
-    const float2 q = gn_quotient(t);
+    const float rest = __fdividef(fmaf(-q, t.w, t.x) + t.y, t.w);  // what the quotient leaves
     float hi = K, lo = 0.f;
-    ff_add(hi, lo, q.x, q.y);
-    return hi + lo;
+    ff_add(hi, lo, q, rest);
+    const float mean = hi + lo;
+    return make_float2(mean, (hi - mean) + lo);
 }
 
 // The square root and the division are the correctly rounded ones: there is
@@ -173,15 +167,15 @@ __device__ __forceinline__ float gn_rstd(float m2, float count, float eps) {
     return __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(m2, count) + eps));
 }
 
-// y = act(d * s + o) per channel: s = rstd * gamma, o = beta - mu * s, with
-// mu the group's mean relative to the shift K and d = x - K.
+// y = act(d * s + o) per channel: s = rstd * gamma, o = beta - rest * s, with
+// K the group's rounded mean, rest what the rounding left, and d = x - K.
 template <class T, int VEC, bool ONE, int ACT>
 struct GnOut {
     using X = GnVec<T, VEC>;
     static constexpr int HG = ONE ? 1 : X::H;
     float2 K[HG], s[X::H], o[X::H];
 
-    // fin(g): float2 (mu, rstd) of group g.
+    // fin(g): float2 (rest, rstd) of group g.
     template <class Fin>
     __device__ __forceinline__ void init(const typename X::Raw& rg, const typename X::Raw& rb, int c, const GnArgs& a,
                                          Fin fin) {
@@ -246,6 +240,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
     float4* gs = reinterpret_cast<float4*>(sm);  // (16-byte aligned: first)
     float2* fin = reinterpret_cast<float2*>(gs + w.ng * sh.wpg);
     float2* st = fin + w.ng;
+    float* mid = reinterpret_cast<float*>(st + a.par * a.tile * segs);  // the first element of each group, then its mean
 
     const int64_t row0 = int64_t(rank) * a.chunk_rows;
     const int rows = static_cast<int>(gn_chunk_len(a.S, a.chunk_rows, rank));
@@ -306,6 +301,8 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
         else
             gn_collapse<VEC>(s, q, static_cast<float>(visits), c, a, mine);
     }
+    // (before the cluster's barrier: in place, row 0 is overwritten after it)
+    for (int g = threadIdx.x; g < w.ng; g += blockDim.x) mid[g] = gn_elem(xs + int64_t(w.g0 + g) * a.D);
     __syncthreads();
     gn_merge_threads<VEC>(a, w, st, segs, vis, sh, gs);
     if (cs > 1)
@@ -314,17 +311,19 @@ __global__ void __launch_bounds__(kGnMaxThreads) gn_fwd_chip(const GnArgs a) {
         __syncthreads();
     gn_merge_cluster(gs, w.ng, sh.wpg, cs, [&](int g, const float4& t) {
         const float rstd = gn_rstd(t.z, t.w, a.eps);
-        fin[g] = make_float2(gn_mu(t), rstd);
-        // (in place: row 0 is this CTA's own, written after the barrier)
+        const float2 m = gn_mean(mid[g], t);
+        fin[g] = make_float2(m.y, rstd);
+        mid[g] = m.x;
         if (rank == 0) {
             const int64_t at = w.b * a.G + w.g0 + g;
-            if (a.mean) a.mean[at] = gn_mean(gn_elem(xs + int64_t(w.g0 + g) * a.D), t);
+            if (a.mean) a.mean[at] = m.x;
             if (a.rstd) a.rstd[at] = rstd;
         }
     });
     __syncthreads();
     if (cs > 1) cluster_arrive();  // this CTA has read its peers' states
     if (w.on) {
+        gn_per_group<T, VEC, ONE>(out.K, c, a, [&](int g) { return mid[min(g - w.g0, w.ng - 1)]; });
         out.init(rg, rb, c, a, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
         T* yp = static_cast<T*>(a.y) + w.b * a.yb + (row0 + w.r) * a.yr + c;
 #pragma unroll
@@ -443,8 +442,8 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
 template <class T, int VEC, bool ONE, int ACT>
 __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, int k, float2* sm, void* ring) {
     using X = GnVec<T, VEC>;
-    float2* fin = sm;                                   // (mu, rstd) per group of the tile
-    float* shift = reinterpret_cast<float*>(sm + w.ng);
+    float2* fin = sm;  // (rest of the mean, rstd) per group of the tile
+    float* mid = reinterpret_cast<float*>(sm + w.ng);  // its mean
     const int c = w.c0 + w.col * VEC;
     const int visits = w.on ? GnVisits(static_cast<int>(gn_chunk_len(a.S, a.out_rows, k)), a).of(w.r) : 0;
     // last rows first: what was summed last is the likeliest in L2
@@ -481,10 +480,11 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
         }, lanes);
         if (on && lane == 0) {
             const float rstd = gn_rstd(t.z, t.w, a.eps);
-            fin[g] = make_float2(gn_mu(t), rstd);
-            shift[g] = K;
+            const float2 m = gn_mean(K, t);
+            fin[g] = make_float2(m.y, rstd);
+            mid[g] = m.x;
             if (k == 0 && t0 == w.t) {
-                if (a.mean) a.mean[bg] = gn_mean(K, t);
+                if (a.mean) a.mean[bg] = m.x;
                 if (a.rstd) a.rstd[bg] = rstd;
             }
         }
@@ -492,7 +492,7 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
     __syncthreads();
     if (!w.on) return;
     GnOut<T, VEC, ONE, ACT> out;
-    gn_per_group<T, VEC, ONE>(out.K, c, a, [&](int g) { return shift[min(g - w.g0, w.ng - 1)]; });
+    gn_per_group<T, VEC, ONE>(out.K, c, a, [&](int g) { return mid[min(g - w.g0, w.ng - 1)]; });
     out.init(rg, rb, c, a, [&](int g) { return fin[min(g - w.g0, w.ng - 1)]; });
     T* yp = static_cast<T*>(a.y) + w.b * a.yb + row * a.yr + c;
     const int64_t ystep = -int64_t(a.par) * a.yr;
