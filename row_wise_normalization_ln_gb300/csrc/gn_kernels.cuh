@@ -398,7 +398,7 @@ struct GnStream {
 // (once per kernel and device; not a stream operation), and asks for the
 // largest share of the SM's memory for it: CTAs of two launches then fit side
 // by side (gn_bwd f32 3x1517x180 9.2 us instead of 11.2, larger calls alike).
-inline cudaError_t gn_opt_in(const void* fn) {
+inline cudaError_t gn_opt_in(const void* fn) try {
     static std::mutex mu;
     static std::map<std::pair<const void*, int>, bool> done;
     int dev = 0, most = 0;
@@ -415,6 +415,8 @@ inline cudaError_t gn_opt_in(const void* fn) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess) done[{fn, dev}] = true;
     return e;
+} catch (...) {  // (no exception leaves a C entry point)
+    return cudaErrorMemoryAllocation;
 }
 
 // A kernel on `grid` CTAs in clusters of `cluster`, with programmatic stream

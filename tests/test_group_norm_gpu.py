@@ -532,3 +532,68 @@ def test_plans_that_do_not_fit_are_refused():
     odd = torch.zeros(1000 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(1, 1000, 64)
     with pytest.raises(rn.NormError):  # 16-byte accesses on a tensor that is not 16-byte aligned
         rn.gn_fwd(odd, gamma, beta, 8, plan=good)
+
+
+@pytest.mark.parametrize("S,C,G", [(30, 64, 8), (3000, 64, 8), (9000, 70, 5), (70000, 64, 8)])
+def test_in_place_chain_equals_copies(S, C, G):
+    """Every call reads what the one before wrote, queued back to back and
+    replayed from a graph: the bits of calls with buffers of their own, each
+    finished before the next."""
+    x, dy, gamma, beta = make(2, S, C, torch.bfloat16, 13)
+    want = x
+    for _ in range(6):
+        want = rn.gn_fwd(want, gamma, beta, G, activation="silu")[0]
+        torch.cuda.synchronize()
+    mean, rstd = rn.gn_fwd(x, gamma, beta, G)[1:]
+    wdy = dy
+    for _ in range(4):
+        wdy = rn.gn_bwd(wdy, x, gamma, beta, mean, rstd, G, activation="gelu")[0]
+        torch.cuda.synchronize()
+
+    def chain(a, b):
+        for _ in range(6):
+            rn.gn_fwd(a, gamma, beta, G, activation="silu", out=a, stats=False)
+        for _ in range(4):
+            rn.gn_bwd(b, x, gamma, beta, mean, rstd, G, activation="gelu", dx=b)
+
+    a, b = x.clone(), dy.clone()
+    chain(a, b)
+    assert torch.equal(a, want) and torch.equal(b, wdy)
+    a.copy_(x)
+    b.copy_(dy)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain(a, b)
+    for _ in range(2):
+        a.copy_(x)
+        b.copy_(dy)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, wdy)
+
+
+def test_calls_from_two_threads():
+    import threading
+    cases = [make(2, 5000 + 40 * k, 64, torch.bfloat16, k) for k in range(2)]
+    want = [rn.gn_fwd(x, gamma, beta, 8, activation="gelu") for x, _, gamma, beta in cases]
+    norms = [rn.grad_norm([x, dy]) for x, dy, _, _ in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(k):
+        x, dy, gamma, beta = cases[k]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = rn.gn_fwd(x, gamma, beta, 8, activation="gelu")
+                n = rn.grad_norm([x, dy])
+                torch.cuda.current_stream().synchronize()
+                if not (all(torch.equal(a, b) for a, b in zip(got, want[k])) and torch.equal(n, norms[k])):
+                    bad.append(k)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
