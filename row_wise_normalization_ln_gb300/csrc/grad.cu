@@ -37,7 +37,8 @@ namespace {
 
 constexpr int kThreads = 256;          // of a team
 constexpr int kSmallTeams = 4;         // of the one CTA of grad_small
-constexpr int kSmallUnits = 64;        // the longest list it takes: 256 KB
+constexpr int kSmallInFlight = 6;      // its accesses per thread
+constexpr int kSmallUnits = kSmallTeams * kSmallInFlight;  // the longest list it takes: 96 KB
 constexpr int kSmallTensors = 64;      // and the most tensors
 constexpr int kUnroll = 8;             // accesses per thread in flight
 constexpr int kUnitBytes = kThreads * 16;
@@ -513,10 +514,8 @@ __device__ __forceinline__ float slot_squares(const uint4& r) {
 
 // The whole of a list of at most kSmallTensors tensors and kSmallUnits units
 // in one CTA and one launch: the norm, and with CLIP the scaling. Its teams
-// take the units in turn, kInFlight at a time, so that a list of many small
-// tensors waits for memory once or twice.
-constexpr int kInFlight = 4;
-
+// take the units in turn, all of them in flight at once and kept in registers,
+// so that the list waits for memory once.
 template <bool CLIP>
 __global__ void __launch_bounds__(kThreads* kSmallTeams) grad_small(const __grid_constant__ GradTable<kSmallTensors> t,
                                                                     float max_norm, float* norm) {
@@ -536,7 +535,8 @@ __global__ void __launch_bounds__(kThreads* kSmallTeams) grad_small(const __grid
         for (int k = 0; k < kSmallTensors; k += 32) i += __popc(__ballot_sync(kFullMask, ends[k + lane] <= u));
         return i;
     };
-    auto first = [&](int i) { return i > 0 ? ends[i - 1] : 0; };
+    // this thread's access within a unit's tensor
+    auto access = [&](int i, int u) { return int64_t(u - (i > 0 ? ends[i - 1] : 0)) * kThreads + tid; };
     auto load = [&](int i, int64_t j) {
         const int dt = t.dtype[i];
         return dt == NORM_F32    ? load_slot<NORM_F32>(t.data[i], j, t.numel[i])
@@ -544,47 +544,45 @@ __global__ void __launch_bounds__(kThreads* kSmallTeams) grad_small(const __grid
                                  : load_slot<NORM_F16>(t.data[i], j, t.numel[i]);
     };
     grid_wait();
-    // fp32 over a warp's values of one round (1024 at most), fp64 beyond:
-    // the whole warp goes to fp64 where a lane's or the warp's sum may have
-    // left fp32's range.
-    double sum = 0.0;  // lane 0
-#pragma unroll 1
-    for (int base = team; base < all; base += kSmallTeams * kInFlight) {
-        uint4 r[kInFlight];
-        int dt[kInFlight];
+    uint4 r[kSmallInFlight];
 #pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
-            const int u = base + k * kSmallTeams;
-            const int i = tensor(min(u, all - 1));
-            dt[k] = t.dtype[i];
-            r[k] = u < all ? load(i, int64_t(u - first(i)) * kThreads + tid) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kSmallInFlight; ++k) {
+        const int u = team + k * kSmallTeams;
+        r[k] = make_uint4(0, 0, 0, 0);
+        if (u < all) {
+            const int i = tensor(u);
+            r[k] = load(i, access(i, u));
         }
-        float s[kInFlight], v = 0.f;
-        bool lost = false;
+    }
+    // fp32 over a warp's values (32 per lane at most), fp64 beyond: the whole
+    // warp goes to fp64 where a lane's or the warp's sum may have left fp32's
+    // range.
+    float v = 0.f;
+    bool lost = false;
 #pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
-            s[k] = dt[k] == NORM_F32    ? slot_squares<NORM_F32>(r[k])
-                   : dt[k] == NORM_BF16 ? slot_squares<NORM_BF16>(r[k])
-                                        : slot_squares<NORM_F16>(r[k]);
-            lost |= !(s[k] >= kSmallSum) && (r[k].x | r[k].y | r[k].z | r[k].w) != 0;
-            v += s[k];
-        }
-        v = group_sum(v, 32);
-        if (__any_sync(kFullMask, lost) || !(v <= 3.0e38f)) {
-            double d = 0.0;
+    for (int k = 0; k < kSmallInFlight; ++k) {
+        const int u = team + k * kSmallTeams;
+        if (u >= all) break;
+        const int dt = t.dtype[tensor(u)];
+        const float s = dt == NORM_F32    ? slot_squares<NORM_F32>(r[k])
+                        : dt == NORM_BF16 ? slot_squares<NORM_BF16>(r[k])
+                                          : slot_squares<NORM_F16>(r[k]);
+        lost |= !(s >= kSmallSum) && (r[k].x | r[k].y | r[k].z | r[k].w) != 0;
+        v += s;
+    }
+    v = group_sum(v, 32);
+    double sum = static_cast<double>(v);
+    if (__any_sync(kFullMask, lost) || !(v <= 3.0e38f)) {
+        double d = 0.0;
 #pragma unroll 1
-            for (int k = 0; k < kInFlight; ++k) {
-                const int u = base + k * kSmallTeams;
-                const int i = tensor(min(u, all - 1));
-                const uint4 w = u < all ? load(i, int64_t(u - first(i)) * kThreads + tid) : make_uint4(0, 0, 0, 0);
-                d += t.dtype[i] == NORM_F32    ? exact_squares<NORM_F32>(&w, 1)
-                     : t.dtype[i] == NORM_BF16 ? exact_squares<NORM_BF16>(&w, 1)
-                                               : exact_squares<NORM_F16>(&w, 1);
-            }
-            sum += warp_sum(d);
-        } else {
-            sum += static_cast<double>(v);
+        for (int u = team; u < all; u += kSmallTeams) {
+            const int i = tensor(u);
+            const uint4 w = load(i, access(i, u));
+            d += t.dtype[i] == NORM_F32    ? exact_squares<NORM_F32>(&w, 1)
+                 : t.dtype[i] == NORM_BF16 ? exact_squares<NORM_BF16>(&w, 1)
+                                           : exact_squares<NORM_F16>(&w, 1);
         }
+        sum = warp_sum(d);
     }
     if (lane == 0) part[threadIdx.x >> 5] = sum;
     __syncthreads();
@@ -596,30 +594,19 @@ __global__ void __launch_bounds__(kThreads* kSmallTeams) grad_small(const __grid
         }
     }
     if constexpr (CLIP) {
-        // (every thread scales the values that it read itself)
         __syncthreads();
         const float coef = coefficient;
-#pragma unroll 1
-        for (int base = team; base < all; base += kSmallTeams * kInFlight) {
-            uint4 r[kInFlight];
-            int at[kInFlight];
 #pragma unroll
-            for (int k = 0; k < kInFlight; ++k) {
-                const int u = base + k * kSmallTeams;
-                const int i = tensor(min(u, all - 1));
-                at[k] = u < all && !(coef == 1.f && t.data[i] == t.out[i]) ? i : -1;  // x * 1 is x
-                r[k] = at[k] >= 0 ? load(i, int64_t(u - first(i)) * kThreads + tid) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int k = 0; k < kInFlight; ++k) {
-                const int i = at[k];
-                if (i < 0) continue;
-                const int64_t j = int64_t(base + k * kSmallTeams - first(i)) * kThreads + tid;
-                const int dt = t.dtype[i];
-                if (dt == NORM_F32) store_slot<NORM_F32>(t.out[i], j, t.numel[i], scaled<NORM_F32>(r[k], coef));
-                else if (dt == NORM_BF16) store_slot<NORM_BF16>(t.out[i], j, t.numel[i], scaled<NORM_BF16>(r[k], coef));
-                else store_slot<NORM_F16>(t.out[i], j, t.numel[i], scaled<NORM_F16>(r[k], coef));
-            }
+        for (int k = 0; k < kSmallInFlight; ++k) {
+            const int u = team + k * kSmallTeams;
+            if (u >= all) break;
+            const int i = tensor(u);
+            if (coef == 1.f && t.data[i] == t.out[i]) continue;  // x * 1 is x
+            const int64_t j = access(i, u);
+            const int dt = t.dtype[i];
+            if (dt == NORM_F32) store_slot<NORM_F32>(t.out[i], j, t.numel[i], scaled<NORM_F32>(r[k], coef));
+            else if (dt == NORM_BF16) store_slot<NORM_BF16>(t.out[i], j, t.numel[i], scaled<NORM_BF16>(r[k], coef));
+            else store_slot<NORM_F16>(t.out[i], j, t.numel[i], scaled<NORM_F16>(r[k], coef));
         }
     }
 }
@@ -761,8 +748,9 @@ norm_status run(const norm_tensor* ts, int64_t count, bool clip, float max_norm,
     size_t need = 0;
     grad_workspace_bytes(ts, count, sms, &need);
     if (ws_bytes < need) return NORM_ERR_ARG;
-    // Short lists: one launch and no workspace (24 tensors of 1024 fp32 values,
-    // on the host and the GPU: 3.8 and 4.5 us against 5.1 and 4.8 with two).
+    // Short lists: one launch and no workspace. Tensors of 512 fp32 values,
+    // norm / clipping in us against the two launches: 24 of them 4.0 / 6.3 to
+    // 4.2 / 6.5, 32 of them 4.7 / 7.5 to 4.2 / 6.5.
     if (shortlist) {
         e = small(ts, count, clip, max_norm, norm, stream);
         if (e == cudaSuccess) return NORM_OK;

@@ -2,7 +2,8 @@
 arithmetic.
 
 Tolerances: the norm's squares are added in fp32 over at most 64 values in
-two chains or more (short lists: 32 values, then a tree of 5 levels), then in
+two chains or more (short lists: over a warp, in chains of 5 and 8 and a
+tree of 5 levels), then in
 fp64 or as pairs of fp32 numbers with every error kept: relative error of the
 sum at most 33 u (u = 2^-24), of the norm 17 u, plus its own rounding: 18 u. A clipped value is
 v * coef with coef rounded once from fp64 (its error: u, and the norm's does
