@@ -75,7 +75,7 @@ def _link_native(obj: str) -> None:
     # the CUDA runtime the binding asks for the SM count is libnorm's kind: static
     cudart = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "lib64")
     cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libnorm.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}",
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}", f"-L{cudart}",
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}", f"-L{cudart}",
            "-lcudart_static", "-ldl", "-lrt", "-lpthread"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -12,7 +12,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/SmallVector.h>
@@ -63,9 +63,12 @@ norm_dtype dtype_of(const at::Tensor& t) {
 
 void* ptr(const at::Tensor& t) { return t.defined() && t.numel() > 0 ? t.mutable_data_ptr() : nullptr; }
 
-at::Tensor new_f32(at::IntArrayRef shape, const at::Tensor& like) {
-    return at::empty(shape, like.options().dtype(at::kFloat).requires_grad(false));
+// New tensors come straight from the caching allocator: gn_fwd with its three
+// new outputs takes 5.6 us of the host, 8.0 through the dispatcher.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType dtype, const at::Tensor& like) {
+    return at::Tensor(at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt));
 }
+at::Tensor new_f32(at::IntArrayRef shape, const at::Tensor& like) { return fresh(shape, at::kFloat, like); }
 
 // The caller's fp32 tensor of n values, checked; `name` for the message.
 at::Tensor given_f32(PyObject* o, int64_t n, const at::Tensor& x, const char* name) {
@@ -88,7 +91,7 @@ at::Tensor param(PyObject* o, const at::Tensor& x, int64_t C, const char* name) 
 
 at::Tensor scratch(PyObject* o, size_t bytes, const at::Tensor& x) {
     if (o == Py_None)
-        return bytes ? at::empty({static_cast<int64_t>(bytes)}, x.options().dtype(at::kByte).requires_grad(false)) : at::Tensor();
+        return bytes ? fresh({static_cast<int64_t>(bytes)}, at::kByte, x) : at::Tensor();
     const at::Tensor& t = tensor(o, "workspace");
     if (t.device() != x.device() || !t.is_contiguous()) refuse("workspace must be a contiguous tensor on " + x.device().str());
     return t;
@@ -162,7 +165,7 @@ void read_rows(at::Tensor* t, Rows* r) {
 at::Tensor output(PyObject* o, const at::Tensor& x, Rows* r, const char* name) {
     at::Tensor y;
     if (o == Py_None) {
-        y = at::empty(x.sizes(), x.options().requires_grad(false));
+        y = fresh(x.sizes(), x.scalar_type(), x);
     } else {
         y = tensor(o, name);
         if (y.sizes() != x.sizes() || y.scalar_type() != x.scalar_type() || y.device() != x.device())
