@@ -25,14 +25,16 @@ typedef struct {
 
 /*
  * norm = sqrt(sum over all tensors of v^2), one fp32 value in device memory.
- * Squares are added in fp32 over at most 1024 values (in chains of at most
- * 16 and trees) and in fp64 beyond; where fp32 squares leave the range (values
- * above 2^63 or sums below 2^-80) that part is summed again in fp64, so the
- * norm is right wherever it fits fp32, infinite or NaN where a value is. A tensor
- * that is listed twice counts twice. No tensors (or only empty ones): 0.
+ * Squares are added in fp32 over at most 64 values of a thread (short lists:
+ * over a warp's), and beyond in fp64 or in pairs of fp32 numbers that keep
+ * every addition's error; where fp32 squares leave the range (values above
+ * 2^60 or sums below 2^-80) that part is summed again in fp64, so the norm is
+ * right wherever it fits fp32, infinite or NaN where a value is. A tensor that
+ * is listed twice counts twice. No tensors (or only empty ones): 0.
  * `workspace`: 8-byte aligned device memory of the caller, at least
- * grad_workspace_bytes() (may be NULL when that is 0); nothing in it needs a value before the call. Calls
- * that share a workspace must not overlap on the GPU. The sums are added in a
+ * grad_workspace_bytes() (may be NULL when that is 0); nothing in it needs a
+ * value before the call. Calls that share a workspace must not overlap on the
+ * GPU. The sums are added in a
  * fixed order: the same tensors give the same bits on one device.
  */
 norm_status grad_norm(const norm_tensor* tensors, int64_t count, float* norm, void* workspace,

@@ -1,5 +1,6 @@
-"""GB300-native row-wise LayerNorm / RMSNorm forward: Python binding of the
-libnorm C ABI (include/libnorm.h).
+"""GB300-native row-wise LayerNorm / RMSNorm, group norm and the global norm of
+a step's gradients: Python binding of the libnorm C ABI (include/libnorm.h,
+libnorm_group.h, libnorm_grad.h).
 
 The binding only marshals arguments: it reshapes ``[..., N]`` inputs to
 ``[M, N]`` rows (the T3 drill's host wrapper, §④), allocates outputs with
@@ -20,7 +21,7 @@ import torch
 __all__ = [
     "ln_fwd", "rms_fwd", "ln_fwd_add", "rms_fwd_add", "ln_fwd_fp8", "rms_fwd_fp8", "ln_bwd", "rms_bwd",
     "make_plan", "make_bwd_plan", "NormPlan", "NormError", "LibraryNotBuilt", "library", "host_rows_pipeline",
-    "host_rows_wait", "gn_fwd", "gn_bwd", "make_gn_plan", "GnPlan", "grad_norm", "grad_clip",
+    "host_rows_wait", "gn_fwd", "gn_bwd", "make_gn_plan", "gn_workspace_bytes", "GnPlan", "grad_norm", "grad_clip",
     "NORM_F32", "NORM_BF16", "NORM_F16", "NORM_MAP_GROUP", "NORM_MAP_CTA",
 ]
 

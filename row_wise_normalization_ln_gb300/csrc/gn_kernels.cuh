@@ -5,9 +5,10 @@
 // tile and walks rows: channel parameters stay in registers, and `par` rows
 // are in flight per step. Groups of D channels: when D is a multiple of VEC
 // (ONE) an access lies within one group and a thread's state is one per
-// access, otherwise it is one per channel. The states of a CTA meet in shared
-// memory, one warp per group; those of a cluster in distributed shared
-// memory; those of a sample's clusters in the caller's workspace.
+// access, otherwise it is one per channel while it runs and one per group that
+// the access touches at the end. The states of a CTA meet in shared memory,
+// some lanes or warps per group; those of a cluster in distributed shared
+// memory; those of row chunks in the caller's workspace.
 #pragma once
 
 #include "gn_args.h"

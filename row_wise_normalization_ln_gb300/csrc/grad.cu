@@ -1,19 +1,22 @@
 // The global norm of a list of gradients, and clipping by it.
 //
-//   grad_sums    every team of 256 threads adds the squares of its share of
-//                the values, every CTA leaves one fp64 partial sum.
+//   grad_sums    every CTA adds the squares of its share of the values and
+//                leaves one fp64 partial sum.
 //   grad_finish  one CTA adds the partial sums: the norm.
 //   grad_scale   every CTA adds the partial sums itself (the same bits in
 //                each) and multiplies its share by the coefficient.
 //   grad_small   one CTA does it all for short lists, in one launch.
 //
 // The kernels stream: each value is read once per pass, which is all the
-// arithmetic needs (bound: HBM). The list is cut into units of one 16-byte
-// access per thread of a team; team i of G takes the units
-// [U i / G, U (i + 1) / G), so the shares differ by one unit at most however
-// the sizes are mixed, and a share is a run of neighbouring addresses but for
-// the steps between tensors. The scaling walks its shares from the end: what
-// a team read last for the sums is what L2 still holds.
+// arithmetic needs (bound: HBM; on one GB300 with a copy bandwidth of 6.8 TB/s,
+// the norm of 1.6 GB in bf16 228 us, 7.1 TB/s; clipping 1 GB in fp32 into other
+// buffers 465 us, 6.5 TB/s of its 3 GB: sums 150 us, scaling 311). The list is
+// cut into units of one 16-byte access per thread of a CTA; CTA i of G takes
+// the units [U i / G, U (i + 1) / G), so the shares differ by one unit at most
+// however the sizes are mixed, and a share is a run of neighbouring addresses
+// but for the steps between tensors. The scaling walks its shares from the
+// end: what a CTA read last for the sums is what L2 still holds. Calls on a few
+// MB are two launches of 3 to 6 us: 48 tensors of 45009 values, 6.5 MB, 12.6 us.
 //
 // The table of tensors travels in the kernel's argument block (up to 960
 // tensors per launch), so nothing is copied to the device and a captured
@@ -35,7 +38,7 @@
 namespace libnorm {
 namespace {
 
-constexpr int kThreads = 256;          // of a team
+constexpr int kThreads = 256;          // of a CTA, and of a team of grad_small
 constexpr int kSmallTeams = 4;         // of the one CTA of grad_small
 constexpr int kSmallInFlight = 6;      // its accesses per thread
 constexpr int kSmallUnits = kSmallTeams * kSmallInFlight;  // the longest list it takes: 96 KB
@@ -512,6 +515,8 @@ __device__ __forceinline__ float slot_squares(const uint4& r) {
     return a.x + a.y;
 }
 
+// (Bound: launch and one load's latency. 24 tensors of 1024 fp32 values 3.8 us,
+// one of 512 2.0.)
 // The whole of a list of at most kSmallTensors tensors and kSmallUnits units
 // in one CTA and one launch: the norm, and with CLIP the scaling. Its teams
 // take the units in turn, all of them in flight at once and kept in registers,
