@@ -412,6 +412,28 @@ __device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, floa
     }
 }
 
+// Row i of a.folds: the sum of the partial rows [P i / folds, P (i + 1) /
+// folds) of 2 C values, 32 columns per CTA. Order fixed as above.
+static __global__ void __launch_bounds__(256) gn_bwd_fold(const GnArgs a) {
+    __shared__ float sm[256];
+    grid_release();
+    grid_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int i = blockIdx.y, width = 2 * a.C, c = blockIdx.x * 32 + lane;
+    const int lo = static_cast<int>(int64_t(a.partials) * i / a.folds);
+    const int hi = static_cast<int>(int64_t(a.partials) * (i + 1) / a.folds);
+    float t = 0.f;
+    if (c < width)
+#pragma unroll 8
+        for (int p = lo + warp; p < hi; p += 8) t += a.colg[p * a.col_pitch + c];
+    sm[threadIdx.x] = t;
+    __syncthreads();
+    if (warp == 0 && c < width) {
+        for (int w = 1; w < 8; ++w) t += sm[w * 32 + lane];
+        a.fold[int64_t(i) * width + c] = t;
+    }
+}
+
 // The split path's two launches; the second also adds the partial rows of the
 // column gradients, in its first CTAs.
 template <class T, int VEC, bool ONE, int ACT>
@@ -495,6 +517,14 @@ cudaError_t gn_dispatch_bwd(const gn_plan& p, const GnArgs& a, norm_act act, int
     // The partial rows of the column gradients (none: zeros), in a fixed order.
     const float* ws = a.colg;
     int64_t partials = a.partials;
+    if (a.folds > 0) {
+        void* fargs[] = {const_cast<GnArgs*>(&a)};
+        const dim3 grid(static_cast<unsigned>((2 * a.C + 31) / 32), static_cast<unsigned>(a.folds));
+        const cudaError_t e = launch_pdl(reinterpret_cast<const void*>(gn_bwd_fold), grid, dim3(256), 0, 1, s, fargs);
+        if (e != cudaSuccess) return e;
+        ws = a.fold;
+        partials = a.folds;
+    }
     int32_t N = a.C;
     float *o0 = a.dgamma, *o1 = a.dbeta;
     void* cargs[] = {&ws, &partials, &N, &o0, &o1};
