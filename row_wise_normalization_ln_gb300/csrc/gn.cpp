@@ -122,6 +122,7 @@ norm_status derive(const gn_plan& p, const Shape& s, GnArgs* a) {
     a->cluster = p.cluster;
     a->cluster_bits = p.cluster == 8 ? 3 : p.cluster >> 1;
     a->join = 1;
+    a->folds = 0;
     a->segs = one_group(s, p.vec_elems) ? 1
                                         : static_cast<int32_t>(std::min<int64_t>(p.vec_elems, (p.vec_elems - 2 + s.D) / s.D + 1));
     const int states = a->tile * (s.bwd ? p.vec_elems : a->segs);

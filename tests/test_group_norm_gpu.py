@@ -161,7 +161,8 @@ SHAPES = [  # B, S, C, G: one value, one row, one channel a group, odd everythin
     (1, 1, 1, 1), (1, 1, 64, 8), (3, 1, 40, 4), (2, 2, 8, 8), (1, 7, 5, 1), (2, 33, 30, 6), (3, 64, 32, 32),
     (1, 61, 320, 32), (2, 256, 320, 32), (1, 100, 1280, 32), (2, 37 * 41, 180, 30), (5, 129, 75, 25),
     (1, 4096, 320, 32), (1, 1023, 96, 1), (2, 17, 4096, 2), (1, 9, 8200, 8), (2, 300, 250, 25), (1, 70, 16, 2),
-    (64, 4, 24, 3), (512, 3, 24, 3), (513, 3, 24, 3), (1300, 3, 40, 5), (20000, 2, 64, 8), (700, 1, 75, 25), (1, 20000, 64, 8), (1, 5000, 130, 13), (2, 16384, 128, 32), (1, 3, 5001, 1), (1, 2000, 1001, 7),
+    (64, 4, 24, 3), (1, 20000, 64, 8), (1, 5000, 130, 13), (2, 16384, 128, 32), (1, 3, 5001, 1), (1, 2000, 1001, 7),
+    (512, 3, 24, 3), (513, 3, 24, 3), (1300, 3, 40, 5), (20000, 2, 64, 8), (700, 1, 75, 25),  # many samples
 ]
 
 
