@@ -219,15 +219,39 @@ void split_plan(const Shape& s, int vec, int sms, gn_plan* p) {
     p->cluster = 1;
     const int64_t units = std::max<int64_t>(1, s.B * ceil_div(ncols, tile));
     const int64_t rows = p->threads / tile;
-    // One CTA per SM while a thread has few rows, two per SM otherwise; counts
-    // between leave some SMs with twice the rows of others. Measured in us with
+    // One CTA per SM while a thread has few rows, two per SM otherwise (four of
+    // narrower accesses, which have fewer bytes in flight each: f16 5x363654x25
+    // gn_fwd 98 us instead of 137, gn_bwd 151 instead of 220); counts between
+    // leave some SMs with twice the rows of others. Measured in us with
     // one / two per SM, at the rows per thread that one gives: gn_fwd bf16
     // 2x4096x320 (9 rows) 9.1 / 11.5, 1x16384x256 (14) 9.6 / 9.9, 2x8192x320
     // (18) 11.9 / 14.3, f32 2x4096x320 (19) 11.9 / 11.7, bf16 8x4096x320 (41)
     // 23.2 / 20.0; gn_bwd f32 3x1517x180 (6) 8.1 / 8.9, bf16 1x4096x512 (7)
-    // 11.1 / 9.7, 2x4096x320 (9) 12.9 / 12.5, 4x4096x320 (19) 19.4 / 16.0.
+    // 11.1 / 9.7, 2x4096x320 (9) 12.9 / 12.5, 4x4096x320 (19) 19.4 / 16.0. With
+    // narrower accesses, one / four per SM: gn_bwd f32 2x10000x30 (14) 8.3 /
+    // 11.3, gn_fwd f32 10x445x175 (21) 7.8 / 9.5, f16 8x1500x75 (40) 12.2 / 10.3.
     const int64_t once = std::max<int64_t>(1, sms / units);
-    const int64_t chunks = ceil_div(ceil_div(s.S, once), rows) <= (s.bwd ? 6 : 18) ? once : int64_t(sms) * 2 / units;
+    const bool whole = vec * es == 16;  // 16-byte accesses
+    const int64_t slots = int64_t(sms) * (whole ? 2 : 4);
+    const int64_t few = whole ? (s.bwd ? 6 : 18) : (s.bwd ? 24 : 36);
+    int64_t chunks = once;
+    if (ceil_div(ceil_div(s.S, once), rows) > few) {
+        // Where whole chunks of every sample and tile leave a tenth of the two
+        // CTAs per SM without work, up to 8 rounds of them, the first that
+        // leave less or the fullest, while a thread has 16 rows or more (gn_bwd
+        // f16 14x5390x768, 154 tiles: 105 us with 9 chunks each, 144 with 1;
+        // gn_fwd bf16 10x2897x1024 36 with 5, 45 with 1).
+        double best = 0.0;
+        for (int64_t round = 1; round <= 8 && best < 0.9; ++round) {
+            const int64_t c = std::max<int64_t>(1, round * slots / units);
+            if (round > 1 && s.S / (c * rows) < 16) break;
+            const double used = static_cast<double>(c * units) / static_cast<double>(round_up(c * units, slots));
+            if (used > best) {
+                best = used;
+                chunks = c;
+            }
+        }
+    }
     const int64_t most = std::max<int64_t>(1, ceil_div(s.S, rows));
     p->chunks = static_cast<int32_t>(std::max(std::min(std::max<int64_t>(1, chunks), most), ceil_div(s.S, int64_t(1) << 30)));
     p->out_chunks = p->chunks;

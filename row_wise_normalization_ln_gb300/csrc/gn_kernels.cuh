@@ -285,8 +285,11 @@ __device__ __forceinline__ float2 gn_peer(const float2* p, int i, uint32_t rank)
 // A slot is refilled one step after it was read. (Rings measured in us for
 // gn_fwd bf16 1x262144x256 / gn_bwd f16 8x4096x320 / bf16 4x65536x256: 4 steps
 // of 2 rows 69 / 22 / 104; 4 of 1 79 / 22 / 113; 8 of 1 69 / 23 / 107; 2 of 4
-// 75 / 22 / 105; 4 of 4 76 / 33 / 115.) Accesses of one 16-bit value, which
-// asynchronous copies do not have, are loaded kBatch rows at a time instead.
+// 75 / 22 / 105; 4 of 4 76 / 33 / 115. Of 4 bytes, gn_bwd f32 5x363654x25: 4 of
+// 4 278, 4 of 2 310, 8 of 4 293, with two CTAs per SM.) Accesses of one 16-bit
+// value, which asynchronous copies do not have, are loaded kBatch rows at a time
+// instead (gn_bwd f16 5x363654x25, two CTAs per SM: 8 rows 220 us, 4 287; four:
+// 8 rows 151, 16 190).
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
 __device__ __forceinline__ void copy_async_wait() {
@@ -306,8 +309,9 @@ struct GnStream {
     using Raw = typename X::Raw;
     static constexpr int kBytes = VEC * static_cast<int>(sizeof(T));
     static constexpr bool kAsync = kBytes >= 4;
-    static constexpr int kStep = 2, kSteps = 4;  // rows per step, steps in the ring
-    static constexpr int kBatch = 4;
+    // rows per step, steps in the ring
+    static constexpr int kStep = kBytes == 16 ? 2 : 4, kSteps = 4;
+    static constexpr int kBatch = 8;
 
     // Shared memory of the slots: those that `visits` rows per thread use.
     static size_t ring_bytes(int64_t visits, int threads) {
