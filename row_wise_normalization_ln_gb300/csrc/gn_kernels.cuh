@@ -142,14 +142,51 @@ __device__ __forceinline__ float2 gn_logistic2(float2 z) {
     return r;
 }
 
+// The normal distribution's tail of a pair: with m = min(|z|, 16), the limit
+// beyond which the tail is below fp32, e = exp(-m^2 / 2) and
+// tail = erfc(m / sqrt 2) / 2 = Q(t) e / 2, t = 1 / (1 + p m / sqrt 2). Q, of
+// degree 8 without a constant, is this file's own least-maximum fit of
+// exp(x^2) erfc(x) (relative 2.1e-8; the form with 1 / (1 + p x) is that of
+// Hastings, "Approximations for Digital Computers", 1955); in fp32 the tail is
+// within 3 u of the exact one, gelu within u (|z| + 1). One pass for every z,
+// and the slope's exp(-z^2 / 2) comes with it: with erff for each value, in two
+// branches, gn_bwd bf16 4x65536x256 took 173 us for the 123, gn_fwd 96 for 79.
+// (80 registers for gn_fwd_split_apply instead of 64 and a few spilled words:
+// 99, since the two launches then do not fit side by side.)
+struct GnTail {
+    float2 m, e, tail;
+};
+__device__ __forceinline__ GnTail gn_tail2(float2 z) {
+    GnTail r;
+    asm("min.NaN.f32 %0, %1, 0f41800000;" : "=f"(r.m.x) : "f"(fabsf(z.x)));  // (NaN stays)
+    asm("min.NaN.f32 %0, %1, 0f41800000;" : "=f"(r.m.y) : "f"(fabsf(z.y)));
+    const float2 d = __ffma2_rn(r.m, f2_splat(0.42f * 0.70710678118654752f), f2_splat(1.f));
+    const float2 u = __fmul2_rn(__fmul2_rn(r.m, r.m), f2_splat(-0.5f * 1.4426950408889634f));
+    float2 t;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(d.y));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.e.x) : "f"(u.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.e.y) : "f"(u.y));
+    constexpr float q[8] = {0.23681276939172055f,  0.2398510887911381f,  0.1925742656963855f,   0.2772031931709584f,
+                            -0.14858194757490237f, 0.46206568355798416f, -0.33348673756550784f, 0.07356170515362967f};
+    float2 s = f2_splat(0.5f * q[7]);
+#pragma unroll
+    for (int i = 6; i >= 0; --i) s = __ffma2_rn(s, t, f2_splat(0.5f * q[i]));
+    r.tail = __fmul2_rn(__fmul2_rn(s, t), r.e);
+    return r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float2 gn_act2(float2 z) {
     if constexpr (ACT == NORM_ACT_SILU) {
         return __fmul2_rn(z, gn_logistic2(z));
     }
     if constexpr (ACT == NORM_ACT_GELU) {
-        const float2 h = __fmul2_rn(z, f2_splat(0.5f)), t = __fmul2_rn(z, f2_splat(0.70710678118654752f));
-        return __ffma2_rn(h, make_float2(erff(t.x), erff(t.y)), h);
+        const GnTail k = gn_tail2(z);
+        // max(z, 0) - |z| tail
+        const float2 h = __fmul2_rn(z, f2_splat(0.5f));
+        const float2 up = __fadd2_rn(h, make_float2(fabsf(h.x), fabsf(h.y)));
+        return __ffma2_rn(make_float2(-k.m.x, -k.m.y), k.tail, up);
     }
     return z;
 }
@@ -163,11 +200,10 @@ __device__ __forceinline__ float2 gn_act_slope2(float2 z) {
         return __fadd2_rn(s, __ffma2_rn(make_float2(-zs.x, -zs.y), s, zs));
     }
     if constexpr (ACT == NORM_ACT_GELU) {
-        const float2 t = __fmul2_rn(z, f2_splat(0.70710678118654752f));
-        const float2 u = __fmul2_rn(t, make_float2(-t.x, -t.y));  // -z^2 / 2
-        const float2 phi = __fmul2_rn(z, f2_splat(0.39894228040143268f));
-        const float2 cdf = __ffma2_rn(f2_splat(0.5f), make_float2(erff(t.x), erff(t.y)), f2_splat(0.5f));
-        return __ffma2_rn(phi, make_float2(__expf(u.x), __expf(u.y)), cdf);
+        const GnTail k = gn_tail2(z);
+        // for z >= 0, 1 - (tail - m phi), and below, tail - m phi; phi = e / sqrt(2 pi)
+        const float2 v = __ffma2_rn(__fmul2_rn(k.m, f2_splat(-0.39894228040143268f)), k.e, k.tail);
+        return make_float2(z.x < 0.f ? v.x : 1.f - v.x, z.y < 0.f ? v.y : 1.f - v.y);
     }
     return f2_splat(1.f);
 }

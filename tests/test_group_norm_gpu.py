@@ -16,8 +16,8 @@ y: z = xhat gamma + beta has an error of at most 600 u |xhat gamma| from rstd
   and 64 u (|mean| rstd |gamma| + |xhat gamma| + |beta|) from the rest (the
   forward adds back what the rounding of the mean leaves, but 64-bit inputs
   share only fp32 gamma, beta). |act'| <= 1.13 for silu and gelu; the activation itself adds
-  at most 16 u (|z| + 1) (exp and the division are within a few ulp, erf
-  within 4). Then eta |y| for the output's rounding, and half the smallest
+  at most 16 u (|z| + 1) (exp and the division are within a few ulp, the
+  normal tail within 3 u). Then eta |y| for the output's rounding, and half the smallest
   subnormal of the type.
 dx = rstd (g - m1 - xhat m2): per value 64 u rstd (|g| + |m1| + |xhat m2|) for
   the arithmetic and the slope (|act''| <= 0.8: z's error 64 u (|xhat gamma| +
@@ -291,6 +291,21 @@ def test_extreme_activation_arguments():
         check_fwd(x, gamma, beta, 1, act, y, mean, rstd)
         dx, dg, db = rn.gn_bwd(torch.ones_like(x), x, gamma, beta, mean, rstd, 1, activation=act)
         check_bwd(torch.ones_like(x), x, gamma, beta, mean, rstd, 1, act, dx, dg, db)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_over_their_range(act):
+    """Arguments from -13 to 13 in steps of 1e-4, where the statistics leave
+    them as they are (mean 0, rstd 1 up to roundings): outputs and slopes of
+    every part of the approximations."""
+    half = torch.linspace(1e-4, 13, 130000)
+    x = torch.cat([half, -half]).view(1, -1, 1).cuda()
+    sigma = float(x.double().square().mean().sqrt())
+    gamma, beta = torch.full((1,), sigma, device="cuda"), torch.zeros(1, device="cuda")
+    y, mean, rstd = rn.gn_fwd(x, gamma, beta, 1, EPS, activation=act)
+    check_fwd(x, gamma, beta, 1, act, y, mean, rstd)
+    dx, dg, db = rn.gn_bwd(torch.ones_like(x), x, gamma, beta, mean, rstd, 1, activation=act)
+    check_bwd(torch.ones_like(x), x, gamma, beta, mean, rstd, 1, act, dx, dg, db)
 
 
 def test_gradient_against_differences():
