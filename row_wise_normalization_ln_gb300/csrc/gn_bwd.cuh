@@ -21,7 +21,7 @@
 //                 4x65536x256 105 us, 6.4 TB/s of its 671 MB (sums 48 us at 5.6
 //                 TB/s, two thirds of the issue slots in use; apply 65 at 6.0).
 //                 f16 8x4096x320 22 us; f32 3x1517x180, two launches of about
-//                 4 us, 9.2 us.
+//                 4 us, 8.4 us.
 // A persistent kernel over bands of rows that stay in L2 took 173 us where the
 // two launches then took 106.
 #pragma once
@@ -31,7 +31,9 @@
 
 namespace libnorm {
 
-constexpr int kGnSumRows = 128;
+// (128 is no faster and its sums are off by a third more: dgamma of f32
+// 13x28608x128 1.7e-7 with 32, 2.2e-7 with 128, against 64 bits.)
+constexpr int kGnSumRows = 32;
 
 // A thread's channels: d and dz of an access.
 template <class T, int VEC, bool ONE, int ACT>

@@ -26,7 +26,7 @@ dx = rstd (g - m1 - xhat m2): per value 64 u rstd (|g| + |m1| + |xhat m2|) for
   Then eta |dx|.
 dgamma, dbeta: 64 u times the sum of the absolute terms, plus the slope's and
   xhat's errors in each term: as for dx.
-Sums over n values in blocks of 128 and trees have an error below (128 + 32) u
+Sums over n values in blocks of 32 and trees have an error below (32 + 128) u
 of the absolute sum in the worst case and about 13 u in practice; 64 u leaves
 room and is far below any wrong formula (a dropped m2 is of order 1)."""
 import math
