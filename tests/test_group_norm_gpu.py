@@ -550,12 +550,13 @@ def test_plans_that_do_not_fit_are_refused():
         rn.gn_fwd(odd, gamma, beta, 8, plan=good)
 
 
-@pytest.mark.parametrize("S,C,G", [(30, 64, 8), (3000, 64, 8), (9000, 70, 5), (70000, 64, 8)])
-def test_in_place_chain_equals_copies(S, C, G):
+@pytest.mark.parametrize("B,S,C,G", [(2, 30, 64, 8), (2, 3000, 64, 8), (2, 9000, 70, 5), (2, 70000, 64, 8),
+                                     (2, 9000, 35, 5), (700, 3, 24, 3)])
+def test_in_place_chain_equals_copies(B, S, C, G):
     """Every call reads what the one before wrote, queued back to back and
     replayed from a graph: the bits of calls with buffers of their own, each
     finished before the next."""
-    x, dy, gamma, beta = make(2, S, C, torch.bfloat16, 13)
+    x, dy, gamma, beta = make(B, S, C, torch.bfloat16, 13)
     want = x
     for _ in range(6):
         want = rn.gn_fwd(want, gamma, beta, G, activation="silu")[0]
@@ -563,18 +564,19 @@ def test_in_place_chain_equals_copies(S, C, G):
     mean, rstd = rn.gn_fwd(x, gamma, beta, G)[1:]
     wdy = dy
     for _ in range(4):
-        wdy = rn.gn_bwd(wdy, x, gamma, beta, mean, rstd, G, activation="gelu")[0]
+        wdy, wdg, wdb = rn.gn_bwd(wdy, x, gamma, beta, mean, rstd, G, activation="gelu")
         torch.cuda.synchronize()
 
     def chain(a, b):
         for _ in range(6):
             rn.gn_fwd(a, gamma, beta, G, activation="silu", out=a, stats=False)
         for _ in range(4):
-            rn.gn_bwd(b, x, gamma, beta, mean, rstd, G, activation="gelu", dx=b)
+            rn.gn_bwd(b, x, gamma, beta, mean, rstd, G, activation="gelu", dx=b, dgamma=dg, dbeta=db)
 
+    dg, db = torch.empty_like(wdg), torch.empty_like(wdb)
     a, b = x.clone(), dy.clone()
     chain(a, b)
-    assert torch.equal(a, want) and torch.equal(b, wdy)
+    assert torch.equal(a, want) and torch.equal(b, wdy) and torch.equal(dg, wdg) and torch.equal(db, wdb)
     a.copy_(x)
     b.copy_(dy)
     torch.cuda.synchronize()
@@ -584,9 +586,10 @@ def test_in_place_chain_equals_copies(S, C, G):
     for _ in range(2):
         a.copy_(x)
         b.copy_(dy)
+        dg.fill_(7.0)
         g.replay()
         torch.cuda.synchronize()
-        assert torch.equal(a, want) and torch.equal(b, wdy)
+        assert torch.equal(a, want) and torch.equal(b, wdy) and torch.equal(dg, wdg) and torch.equal(db, wdb)
 
 
 def test_calls_from_two_threads():
