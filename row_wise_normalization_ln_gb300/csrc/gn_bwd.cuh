@@ -306,7 +306,6 @@ __device__ __forceinline__ void gn_bwd_sums(const GnArgs& a, const GnTile& w, in
                            static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c};
     const int64_t step[2] = {int64_t(a.par) * a.xr, int64_t(a.par) * a.dyr};
     grid_wait();
-    // (the second launch may now start, and read its inputs before it waits for this one)
     grid_release();
     GnStream<T, VEC, 2> rows_in(p, step, visits, ring);
     if (w.on) {
@@ -363,11 +362,10 @@ __device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, i
     const T* const p[2] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c,
                            static_cast<const T*>(a.dy) + w.b * a.dyb + row * a.dyr + c};
     const int64_t step[2] = {-int64_t(a.par) * a.xr, -int64_t(a.par) * a.dyr};
-    // (read before the wait for the sums, as in the forward)
+    grid_wait();  // before every read, as in the forward
     GnStream<T, VEC, 2> rows_in(p, step, visits, ring);
     GnBwdCh<T, VEC, ONE, ACT> ch;
     if (w.on) ch.init(a, w.b, c);
-    grid_wait();
     const GnShare sh(w.ng);
     const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);
     for (int base = 0; base < w.ng << sh.bits; base += blockDim.x) {

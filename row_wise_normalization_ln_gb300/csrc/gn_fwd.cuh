@@ -381,7 +381,6 @@ __device__ __forceinline__ void gn_fwd_sums(const GnArgs& a, const GnTile& w, in
     const T* const p[1] = {xs + (k * a.chunk_rows + w.r) * a.xr + c};
     const int64_t step[1] = {int64_t(a.par) * a.xr};
     grid_wait();
-    // (the second launch may now start, and read x before it waits for this one)
     grid_release();
     GnStream<T, VEC, 1> rows_in(p, step, visits, ring);
     if (w.on) {
@@ -464,16 +463,17 @@ __device__ __forceinline__ void gn_fwd_apply(const GnArgs& a, const GnTile& w, i
     const int64_t row = k * a.out_rows + w.r + int64_t(visits - 1) * a.par;
     const T* const p[1] = {static_cast<const T*>(a.x) + w.b * a.xb + row * a.xr + c};
     const int64_t step[1] = {-int64_t(a.par) * a.xr};
-    // The sums' launch lets this one start only once its own inputs are
-    // there (x, gamma, beta), and does not write them: they are read before
-    // the wait for the sums.
+    // Nothing is read before this launch's own wait, x and the parameters
+    // neither: the sums' wait orders what wrote them before this launch, but
+    // only a wait of its own makes those writes visible to it.
+    grid_wait();
+    // (the rows and parameters travel while the states are merged)
     GnStream<T, VEC, 1> rows_in(p, step, visits, ring);
     typename X::Raw rg = X::zero(), rb = X::zero();
     if (w.on) {
         rg = X::load(static_cast<const T*>(a.gamma) + c);
         rb = X::load(static_cast<const T*>(a.beta) + c);
     }
-    grid_wait();
     // The groups' states from every tile and chunk, lanes side by side.
     const GnShare sh(w.ng);
     const int lanes = sh.lanes, lane = threadIdx.x & (lanes - 1);

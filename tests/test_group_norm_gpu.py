@@ -616,3 +616,65 @@ def test_calls_from_two_threads():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("dtype,B,S,C,G", [
+    ("bf16", 2, 9000, 64, 8), ("bf16", 2, 9000, 70, 5), ("bf16", 2, 9000, 35, 5), ("f32", 2, 9000, 64, 8),
+    ("f32", 2, 9000, 35, 5), ("bf16", 2, 100, 64, 8), ("f32", 1, 40000, 30, 6)])
+def test_chain_that_rewrites_parameters_and_statistics(dtype, B, S, C, G):
+    """Everything a call reads is written by the call queued before it, into
+    the same buffers round after round, with no gap between the launches: x,
+    dy, gamma and beta by group norm calls of their own, the statistics by the
+    forward. Bits as from calls that are each finished before the next; on
+    every access width, queued back to back and replayed from a graph."""
+    dt, rounds = DT[dtype], 5
+    sets = [make(B, S, C, dt, 31 + k) for k in range(rounds)]
+    one, zero = torch.ones(C, dtype=dt, device="cuda"), torch.zeros(C, dtype=dt, device="cuda")
+
+    def renew(dst, src):  # dst = group norm of src: a short and a long kernel of the library as the writer
+        rn.gn_fwd(src.view(-1, *src.shape[-2:]) if src.dim() > 1 else src.view(1, 1, C), one, zero, 1,
+                  out=dst if dst.dim() > 1 else dst.view(1, 1, C), stats=False)
+
+    buf = [torch.empty_like(t) for t in sets[0]]
+    stats = [torch.empty(B, G, device="cuda") for _ in range(2)]
+    outs = [(torch.empty_like(buf[0]), torch.empty_like(buf[0]), torch.empty(C, device="cuda"), torch.empty(C, device="cuda"),
+             torch.empty(B, G, device="cuda"), torch.empty(B, G, device="cuda")) for _ in range(rounds)]
+
+    def chain(pause):
+        for (x, dy, gamma, beta), (y, dx, dg, db, m, r) in zip(sets, outs):
+            bx, bdy, bg, bb = buf
+            for step in (lambda: renew(bx, x), lambda: renew(bg, gamma), lambda: renew(bb, beta),
+                         lambda: rn.gn_fwd(bx, bg, bb, G, activation="silu", out=y, mean=stats[0], rstd=stats[1]),
+                         lambda: renew(bdy, dy),
+                         lambda: rn.gn_bwd(bdy, bx, bg, bb, stats[0], stats[1], G, activation="silu", dx=dx, dgamma=dg,
+                                           dbeta=db),
+                         # the parameters change straight before a backward, the statistics straight before another
+                         lambda: renew(bg, beta), lambda: renew(bb, gamma),
+                         lambda: rn.gn_bwd(bdy, bx, bg, bb, stats[0], stats[1], G, activation="silu", dx=dx, dgamma=dg,
+                                           dbeta=db),
+                         lambda: rn.gn_fwd(dx, bg, bb, G, activation="silu", out=y, mean=m, rstd=r),
+                         lambda: rn.gn_bwd(bdy, dx, bg, bb, m, r, G, activation="gelu", dx=dx, dgamma=dg, dbeta=db)):
+                step()
+                if pause:
+                    torch.cuda.synchronize()
+
+    chain(True)
+    want = [tuple(t.clone() for t in o) for o in outs]
+    assert all(torch.isfinite(t).all() for o in want for t in o)
+
+    def check():
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            for a, b in zip(o, w):
+                assert torch.equal(a, b)
+                a.fill_(3.0)
+
+    for _ in range(3):
+        chain(False)
+        check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain(False)
+    for _ in range(3):
+        g.replay()
+        check()
