@@ -242,12 +242,17 @@ __device__ __forceinline__ double root(double s) {
     return fma(fma(-y, y, s), static_cast<double>(0.5f / r), y);
 }
 
-// The coefficient of a norm, rounded once; NaN from a NaN norm.
+// The coefficient of a norm, 1 at most, rounded once; NaN from a NaN norm.
 __device__ __forceinline__ float coef_of(float max_norm, double norm) {
     const double d = norm + 1e-6, m = max_norm;
-    if (!(d < 1e30)) return static_cast<float>(m / d);  // infinite, NaN or beyond fp32's reach
-    const float r = 1.f / static_cast<float>(d);
-    const double c0 = m * static_cast<double>(r), c = fma(fma(-c0, d, m), static_cast<double>(r), c0);
+    double c;
+    if (d < 1e30) {
+        const float r = 1.f / static_cast<float>(d);
+        const double c0 = m * static_cast<double>(r);
+        c = fma(fma(-c0, d, m), static_cast<double>(r), c0);
+    } else {  // infinite, NaN or beyond the reach of fp32's reciprocal
+        c = m / d;
+    }
     return c > 1.0 ? 1.f : static_cast<float>(c);
 }
 

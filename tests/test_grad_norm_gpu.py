@@ -281,3 +281,23 @@ def test_clipping_a_training_step():
     for got, want in zip(keep, (ps[0].grad, ps[1].grad, ps[2].grad, ps[3].grad, xr.grad)):
         # y, h's statistics and dh pass through bf16: relative 2^-8 each, errors of many values add as random
         assert (got.double() - want).norm() <= 4 * 2.0 ** -8 * want.norm()
+
+
+@pytest.mark.parametrize("size", [1e28, 1e29, 1e30, 1e31, 1e34, 1e35])
+@pytest.mark.parametrize("shape", [[(1000,), (33, 77)], [(300001,), (50,)]], ids=["short", "long"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+def test_clipping_by_norms_far_out(dtype, shape, size):
+    """Norms from 5e29 to 6e37: clipped where the norm is above max_norm, and
+    left as they are where it is below, whatever max_norm is."""
+    ts = tensors(shape, [dtype], 3, size)
+    total = norm64(ts)
+    for max_norm in (1.0, 0.5 * total, 0.999 * total, 1.001 * total, 20 * total, 3.4e38):
+        max_norm = min(max_norm, 3.4e38)
+        outs = [torch.empty_like(t) for t in ts]
+        _, norm = rn.grad_clip(ts, max_norm, out=outs)
+        check_clip(ts, outs, max_norm, norm)
+        mine = [t.clone() for t in ts]
+        rn.grad_clip(mine, max_norm)
+        assert all(torch.equal(a, b) for a, b in zip(mine, outs))
+        if max_norm > 1.0005 * total:
+            assert all(torch.equal(a, b) for a, b in zip(outs, ts))
