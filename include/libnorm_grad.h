@@ -46,8 +46,9 @@ norm_status grad_norm(const norm_tensor* tensors, int64_t count, float* norm, vo
  * norm that is infinite gives coef 0, and a NaN norm NaN, as the formula
  * says: the caller who wants to skip such a step reads `norm`. With coef 1,
  * tensors clipped in place are not touched. Each `out` is its tensor's `data`
- * itself or apart from every other data and out of the list; overlaps return
- * NORM_ERR_ARG. max_norm: finite and >= 0.
+ * itself or apart from every other data and out of the list, and `norm` is
+ * apart from all of them; overlaps return NORM_ERR_ARG. max_norm: finite and
+ * >= 0.
  */
 norm_status grad_clip(const norm_tensor* tensors, int64_t count, float max_norm, float* norm, void* workspace,
                       size_t workspace_bytes, cudaStream_t stream);

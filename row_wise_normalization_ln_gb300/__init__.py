@@ -740,7 +740,8 @@ def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[S
     norm their global norm (grad_norm): in place, or into ``out``, a list of
     tensors of the same shapes, strides and types. Returns ``(out, norm)``.
     With an infinite norm the coefficient is 0, with a NaN norm NaN: read
-    ``norm`` to skip such a step. A tensor may be listed once only."""
+    ``norm`` to skip such a step. A tensor may be listed once only, and
+    ``norm`` may not lie within one of them."""
     norm = _grad_call("grad_clip", grads, out, float(max_norm), norm, workspace, stream)
     return (out if out is not None else grads), norm
 

@@ -709,8 +709,9 @@ norm_status check_tensors(const norm_tensor* ts, int64_t count, bool clip) {
 }
 
 // No output may overlap another tensor's output or input, or its own input
-// other than exactly.
-norm_status check_apart(const norm_tensor* ts, int64_t count) {
+// other than exactly; the norm is an output of its own (grad_scale writes it
+// while other CTAs read and write).
+norm_status check_apart(const norm_tensor* ts, int64_t count, const float* norm) {
     struct Piece {
         uintptr_t lo, hi;
         bool write;
@@ -718,6 +719,8 @@ norm_status check_apart(const norm_tensor* ts, int64_t count) {
     std::unique_ptr<Piece[]> p(new (std::nothrow) Piece[2 * static_cast<size_t>(count) + 1]);
     if (!p) return NORM_ERR_ARG;
     size_t n = 0;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(norm);
+    p[n++] = Piece{at, at + sizeof *norm, true};
     for (int64_t i = 0; i < count; ++i) {
         const uintptr_t bytes = static_cast<uintptr_t>(ts[i].numel) * elem_size(ts[i].dtype);
         if (bytes == 0) continue;
@@ -742,7 +745,7 @@ norm_status run(const norm_tensor* ts, int64_t count, bool clip, float max_norm,
     if (!norm || (clip && (!std::isfinite(max_norm) || max_norm < 0.f))) return NORM_ERR_ARG;
     const bool shortlist = is_short(ts, count);
     if (!shortlist && (!ws || (reinterpret_cast<uintptr_t>(ws) & 7u))) return NORM_ERR_ARG;
-    if (clip && (st = check_apart(ts, count)) != NORM_OK) return st;
+    if (clip && (st = check_apart(ts, count, norm)) != NORM_OK) return st;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     static std::atomic<int> cache[64];

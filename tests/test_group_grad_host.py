@@ -168,6 +168,19 @@ def test_overlapping_outputs_refused(lib, entries):
     assert clip(lib, entries) == rn.NORM_ERR_ARG
 
 
+@pytest.mark.parametrize("norm", [0x100000, 0x10fffc, 0x300000, 0x300ffc])
+@pytest.mark.parametrize("count", [1, 70])
+def test_norm_over_a_gradient_or_an_output_refused(lib, norm, count):
+    """grad_clip writes the norm while gradients are still read and outputs
+    written."""
+    entries = [(0x100000, 0x300000, 1 << 14, rn.NORM_F32)] + [(0x500000 + 64 * i, 0x700000 + 64 * i, 16, rn.NORM_F32)
+                                                             for i in range(count - 1)]
+    assert clip(lib, entries, norm=ctypes.c_void_p(norm)) == rn.NORM_ERR_ARG
+    inplace = [(d, d, n, t) for d, _, n, t in entries]
+    if norm < 0x200000:
+        assert clip(lib, inplace, norm=ctypes.c_void_p(norm)) == rn.NORM_ERR_ARG
+
+
 def test_workspace_bytes(lib):
     n = ctypes.c_size_t()
 
