@@ -11,7 +11,7 @@
  * sample's group. Rows (positions) may have a pitch of their own and samples
  * too: element (b, s, c) of x is x[b * x_batch + s * x_row + c], pitches in
  * elements, x_row >= C, x_batch >= (S - 1) * x_row + C (ignored where S or B
- * is 1). All pointers to tensors need their element's alignment; 16-byte
+ * is 1). Every pointer needs its element's alignment (others are refused); 16-byte
  * accesses are used when every tensor and parameter is 16-byte aligned and
  * C and all pitches are whole 16-byte vectors, 4-byte accesses of 16-bit
  * pairs when the same holds for 4 bytes, element accesses otherwise.

@@ -45,6 +45,9 @@ norm_status check_shape(int64_t B, int64_t S, int64_t C, int64_t G, norm_dtype d
     return NORM_OK;
 }
 
+// A null pointer or one on a boundary of `bytes`.
+bool on(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
 // One [B, S, C] tensor of a call.
 struct Tensor {
     const void* p;
@@ -62,7 +65,7 @@ norm_status check_tensor(const Shape& s, Tensor* t) {
     if (s.B == 1) t->batch = static_cast<int64_t>(span);
     if (t->batch < static_cast<int64_t>(span)) return NORM_ERR_ARG;
     if (static_cast<__int128>(s.B) * t->batch >= (static_cast<__int128>(1) << 61)) return NORM_ERR_ARG;
-    if (reinterpret_cast<uintptr_t>(t->p) % elem_size(s.dtype) != 0) return NORM_ERR_ARG;
+    if (!on(t->p, elem_size(s.dtype))) return NORM_ERR_ARG;
     return NORM_OK;
 }
 
@@ -355,7 +358,8 @@ norm_status gn_fwd_planned(const void* x, int64_t x_batch, int64_t x_row, const 
     if (st != NORM_OK) return st;
     if (!std::isfinite(eps) || eps < 0.f || !act_ok(act)) return NORM_ERR_ARG;
     if (B == 0 || S == 0) return NORM_OK;
-    if (!gamma || !beta) return NORM_ERR_ARG;
+    const int es = elem_size(dtype);
+    if (!gamma || !beta || !on(gamma, es) || !on(beta, es) || !on(mean, 4) || !on(rstd, 4)) return NORM_ERR_ARG;
     Tensor t[2] = {{x, x_batch, x_row}, {y, y_batch, y_row}};
     for (Tensor& i : t)
         if ((st = check_tensor(s, &i)) != NORM_OK) return st;
@@ -398,14 +402,16 @@ norm_status gn_bwd_planned(const void* dy, int64_t dy_batch, int64_t dy_row, con
     Shape s;
     norm_status st = check_shape(B, S, C, G, dtype, true, &s);
     if (st != NORM_OK) return st;
-    if (!act_ok(act) || !dgamma || !dbeta) return NORM_ERR_ARG;
+    if (!act_ok(act) || !dgamma || !dbeta || !on(dgamma, 4) || !on(dbeta, 4)) return NORM_ERR_ARG;
     gn_plan p{};
     GnArgs a{};
     a.C = static_cast<int32_t>(C);
     a.dgamma = dgamma;
     a.dbeta = dbeta;
     if (B > 0 && S > 0) {
+        const int es = elem_size(dtype);
         if (!gamma || !beta || !mean || !rstd) return NORM_ERR_ARG;
+        if (!on(gamma, es) || !on(beta, es) || !on(mean, 4) || !on(rstd, 4)) return NORM_ERR_ARG;
         Tensor t[3] = {{dy, dy_batch, dy_row}, {x, x_batch, x_row}, {dx, dx_batch, dx_row}};
         for (Tensor& i : t)
             if ((st = check_tensor(s, &i)) != NORM_OK) return st;

@@ -742,7 +742,8 @@ norm_status run(const norm_tensor* ts, int64_t count, bool clip, float max_norm,
                 size_t ws_bytes, cudaStream_t stream) {
     norm_status st = check_tensors(ts, count, clip);
     if (st != NORM_OK) return st;
-    if (!norm || (clip && (!std::isfinite(max_norm) || max_norm < 0.f))) return NORM_ERR_ARG;
+    if (!norm || (reinterpret_cast<uintptr_t>(norm) & 3u)) return NORM_ERR_ARG;
+    if (clip && (!std::isfinite(max_norm) || max_norm < 0.f)) return NORM_ERR_ARG;
     const bool shortlist = is_short(ts, count);
     if (!shortlist && (!ws || (reinterpret_cast<uintptr_t>(ws) & 7u))) return NORM_ERR_ARG;
     if (clip && (st = check_apart(ts, count, norm)) != NORM_OK) return st;

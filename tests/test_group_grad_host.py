@@ -125,6 +125,24 @@ def test_binding_refuses():
         rn.grad_clip([x], 1.0, out=[])
 
 
+def test_pointers_off_their_elements_alignment_refused(lib):
+    """Parameters, statistics, column gradients and the norm, like the
+    tensors: an access at such an address would be an error on the GPU."""
+    off = ctypes.c_void_p(0x1002)
+    for kw in (dict(g=off), dict(b=off)):
+        assert fwd(lib, **kw) == rn.NORM_ERR_ARG
+    for kw in (dict(g=off), dict(b=off), dict(m=off), dict(r=off), dict(dg=off), dict(db=off)):
+        assert bwd(lib, **kw) == rn.NORM_ERR_ARG
+    for kw in (dict(g=ctypes.c_void_p(0x1001)), dict(b=ctypes.c_void_p(0x1001))):
+        assert fwd(lib, dt=rn.NORM_BF16, **kw) == rn.NORM_ERR_ARG
+    for m, r in ((off, None), (None, off)):
+        assert lib.gn_fwd(P, 512, 64, P, P, ctypes.c_void_p(0x9000), 512, 64, m, r, P, 1 << 40, 2, 8, 64, 4, 1e-5, 0, 0,
+                          None) == rn.NORM_ERR_ARG
+    assert bwd(lib, B=0, dg=off) == rn.NORM_ERR_ARG
+    for call in ("grad_norm", "grad_clip"):
+        assert clip(lib, [(0x8000, 0x8000, 64, rn.NORM_F32)], norm=off, call=call) == rn.NORM_ERR_ARG
+
+
 # ------------------------------------------------------------ gradients
 
 class NormTensor(ctypes.Structure):
