@@ -23,6 +23,7 @@ constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSmem = 48 * 1024;
 constexpr int kMaxCluster = 8;
 constexpr int kFoldRows = 64, kMaxFolds = 256;  // partial rows per folded one, folded rows
+constexpr int kSplitFoldFrom = 4096;            // more partial rows than this are folded on the split path
 constexpr int kFwdMaxRows = 8, kBwdMaxRows = 4;  // rows a thread of the on-chip kernels can hold
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -164,6 +165,13 @@ norm_status derive(const gn_plan& p, const Shape& s, GnArgs* a) {
     const int64_t units = s.B * a->tiles, tall = std::max(p.chunks, p.out_chunks);
     if (tall > kMaxGrid / 4 / std::max<int64_t>(1, units) || s.B > kMaxGrid / p.chunks) return NORM_ERR_PLAN;
     a->partials = static_cast<int32_t>(s.B * p.chunks);
+    // The second launch's adders are a CTA per 32 columns: beyond some partial
+    // rows they finish after everything else, and the rows are added over the
+    // whole device instead, in two more launches. Adders / folds in us: gn_bwd
+    // bf16 1030x1100x64 (2060 rows) 121 / 127, 4096x1100x64 420 / 424, f32
+    // 16384x1100x8 508 / 454, bf16 65536x1100x8 1531 / 1240.
+    if (s.bwd && a->partials > kSplitFoldFrom)
+        a->folds = static_cast<int32_t>(std::min<int64_t>(kMaxFolds, ceil_div(a->partials, kFoldRows)));
     return NORM_OK;
 }
 

@@ -57,7 +57,7 @@ struct GnArgs {
     int64_t chunk_rows;    // rows per summed chunk (CHIP: per CTA of the cluster)
     int64_t out_rows;      // rows per written chunk
     int32_t partials;      // partial rows of the column gradients
-    int32_t folds;         // CHIP: rows they are added to first where they are many, otherwise 0
+    int32_t folds;         // rows they are added to first where they are many, otherwise 0
     float* fold;           // [folds, 2 C]
     int32_t ring_at;       // SPLIT: where the row stream's slots start in shared memory, in 16-byte units
     float *dgamma, *dbeta;

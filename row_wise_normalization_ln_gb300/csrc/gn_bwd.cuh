@@ -394,15 +394,22 @@ __device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, i
 }
 
 // dgamma and dbeta of 32 columns from the partial rows: warp w adds rows w,
-// w + warps, ... in that order, then the warps' sums in warp order.
+// w + warps, ... in that order, in blocks of kGnSumRows, then the warps' sums
+// in warp order. (One chain of 2048 rows was off by 424 u where all had one
+// sign.)
 __device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, float2* sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int c = block * 32 + lane;
     float2 t = make_float2(0.f, 0.f);
     if (c < a.C)
+        for (int p = warp; p < a.partials;) {
+            const int stop = min(a.partials, p + kGnSumRows * warps);
+            float2 block = make_float2(0.f, 0.f);
 #pragma unroll 8
-        for (int p = warp; p < a.partials; p += warps)
-            t = __fadd2_rn(t, make_float2(a.colg[p * a.col_pitch + c], a.colb[p * a.col_pitch + c]));
+            for (; p < stop; p += warps)
+                block = __fadd2_rn(block, make_float2(a.colg[p * a.col_pitch + c], a.colb[p * a.col_pitch + c]));
+            t = __fadd2_rn(t, block);
+        }
     sm[threadIdx.x] = t;
     __syncthreads();
     if (warp == 0 && c < a.C) {
@@ -424,8 +431,13 @@ static __global__ void __launch_bounds__(256) gn_bwd_fold(const GnArgs a) {
     const int hi = static_cast<int>(int64_t(a.partials) * (i + 1) / a.folds);
     float t = 0.f;
     if (c < width)
+        for (int p = lo + warp; p < hi;) {
+            const int stop = min(hi, p + kGnSumRows * 8);
+            float block = 0.f;
 #pragma unroll 8
-        for (int p = lo + warp; p < hi; p += 8) t += a.colg[p * a.col_pitch + c];
+            for (; p < stop; p += 8) block += a.colg[p * a.col_pitch + c];
+            t += block;
+        }
     sm[threadIdx.x] = t;
     __syncthreads();
     if (warp == 0 && c < width) {
@@ -435,7 +447,11 @@ static __global__ void __launch_bounds__(256) gn_bwd_fold(const GnArgs a) {
 }
 
 // The split path's two launches; the second also adds the partial rows of the
-// column gradients, in its first CTAs.
+// column gradients, in its first CTAs, where they are not folded first.
+__host__ __device__ __forceinline__ int gn_adders(const GnArgs& a) {
+    return a.partials > 1 && a.folds == 0 ? (a.C + 31) / 32 : 0;
+}
+
 template <class T, int VEC, bool ONE, int ACT>
 __global__ void __launch_bounds__(kGnMaxThreads, 2) gn_bwd_split_sums(const GnArgs a) {
     extern __shared__ __align__(16) float2 states[];  // the merges' states, then the row stream's slots
@@ -448,7 +464,7 @@ template <class T, int VEC, bool ONE, int ACT>
 __global__ void __launch_bounds__(kGnMaxThreads, 2) gn_bwd_split_apply(const GnArgs a) {
     extern __shared__ __align__(16) float2 states[];
     grid_release();
-    const int adders = a.partials > 1 ? (a.C + 31) / 32 : 0;
+    const int adders = gn_adders(a);
     const int i = static_cast<int>(blockIdx.x) - adders;
     if (i < 0) {
         grid_wait();
@@ -483,7 +499,7 @@ cudaError_t gn_launch_bwd(const gn_plan& p, const GnArgs& a, int64_t B, cudaStre
     const cudaError_t e = gn_launch(reinterpret_cast<const void*>(gn_bwd_split_sums<T, VEC, ONE, ACT>),
                                     units * a.chunks, p.threads, all(a.chunk_rows), 1, s, a);
     if (e != cudaSuccess) return e;
-    const int64_t adders = a.partials > 1 ? (a.C + 31) / 32 : 0;
+    const int64_t adders = gn_adders(a);
     return gn_launch(reinterpret_cast<const void*>(gn_bwd_split_apply<T, VEC, ONE, ACT>),
                      units * a.out_chunks + adders, p.threads, all(a.out_rows), 1, s, a);
 }
@@ -511,8 +527,8 @@ cudaError_t gn_dispatch_bwd(const gn_plan& p, const GnArgs& a, norm_act act, int
         else
             e = gn_launch_bwd_act<T, 1, true>(p, a, act, B, s);
         // one partial row: the kernel wrote dgamma and dbeta; the split path's
-        // second launch adds its partial rows itself
-        if (e != cudaSuccess || a.partials == 1 || p.path != GN_PATH_CHIP) return e;
+        // second launch adds a moderate number of them itself
+        if (e != cudaSuccess || a.partials == 1 || (p.path != GN_PATH_CHIP && a.folds == 0)) return e;
     }
     // The partial rows of the column gradients (none: zeros), in a fixed order.
     const float* ws = a.colg;

@@ -678,3 +678,38 @@ def test_chain_that_rewrites_parameters_and_statistics(dtype, B, S, C, G):
     for _ in range(3):
         g.replay()
         check()
+
+
+@pytest.mark.parametrize("dtype,B,S,C,G", [("f32", 16384, 1100, 8, 1), ("bf16", 3000, 1030, 6, 2), ("f32", 1500, 3001, 12, 3),
+                                           ("f32", 4096, 1100, 8, 1), ("f32", 4097, 1100, 8, 1),
+                                           ("f32", (1 << 21) + 3, 1, 4, 1)])
+def test_column_sums_of_many_samples(dtype, B, S, C, G):
+    """Thousands of samples with more positions than one CTA holds, and millions
+    of one: as many partial rows of the column gradients, all of one sign. Every
+    addition of a sum of positive terms rounds by at most u of the sum so far,
+    so the sum is off by u times the additions a term goes through: a thread's
+    32 rows and its blocks (2), the row slots of a CTA (40), and either the
+    partial rows folded by 8 warps (16) and their warps (8), the folded rows (8)
+    and their warps (32), or the partial rows in blocks of 32, at most 16
+    of them, and their warps (8): 138 at most. Chains of thousands of equal
+    terms are off by ten times that."""
+    dt = DT[dtype]
+    x, _, gamma, beta = make(1, S, C, dt, 17)
+    x = torch.cat([torch.randn(B // 500 + 1, S, C, device="cuda").to(dt)] * 500)[:B].contiguous()
+    v = (0.7 + 0.1 * torch.rand(C, generator=torch.Generator().manual_seed(3))).to(dt).cuda()
+    dy = v.expand(B, S, C).contiguous()
+    _, mean, rstd = rn.gn_fwd(x, gamma, beta, G, EPS)
+    dx, dg, db = rn.gn_bwd(dy, x, gamma, beta, mean, rstd, G)
+    want = v.to(F) * B * S
+    rel = ((db.to(F) - want) / want).abs().max().item()
+    assert rel <= 138 * U, rel / U
+    s = torch.zeros(C, dtype=F, device="cuda")
+    total = torch.zeros(C, dtype=F, device="cuda")
+    for k in range(0, B, 1000):
+        xh = (x[k:k + 1000].to(F) - spread(mean[k:k + 1000].to(F), C // G)) * spread(rstd[k:k + 1000].to(F), C // G)
+        s += xh.sum((0, 1)) * v
+        total += xh.abs().sum((0, 1)) * v
+    assert ((dg.to(F) - s).abs() <= 146 * U * total).all()  # (and 8 u for xh and the products)
+    for k in (0, B - 3):
+        check_bwd(dy[k:k + 3], x[k:k + 3], gamma, beta, mean[k:k + 3], rstd[k:k + 3], G, None, dx[k:k + 3],
+                  *rn.gn_bwd(dy[k:k + 3], x[k:k + 3], gamma, beta, mean[k:k + 3], rstd[k:k + 3], G)[1:])
