@@ -677,7 +677,9 @@ def gn_fwd(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, groups: int
     ``x.permute(0, 2, 3, 1)``.
 
     Returns ``(y, mean, rstd)``; mean and rstd are fp32 ``[B, groups]`` (None
-    when ``stats=False``). ``out`` may be ``x`` itself (in place).
+    when ``stats=False``; NaN where a sample has no positions, unless they are
+    the caller's, which are then left as they were). ``out`` may be ``x`` itself
+    (in place).
     ``workspace`` (gn_workspace_bytes; any dtype) is allocated when not given;
     calls that share one must not overlap on the GPU."""
     if stream is not None:

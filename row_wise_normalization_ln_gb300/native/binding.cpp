@@ -18,6 +18,7 @@
 #include <c10/util/SmallVector.h>
 
 #include <cstdint>
+#include <limits>
 #include <stdexcept>
 #include <string>
 #include <unordered_map>
@@ -230,6 +231,10 @@ PyObject* gn_fwd_py(PyObject* const* a) {
     if (a[9] == Py_True) {
         mean = f32(a[7], {c.B, c.G}, c.x, "mean");
         rstd = f32(a[8], {c.B, c.G}, c.x, "rstd");
+        if (c.rows.S == 0) {  // no call writes the statistics of no values: NaN, as the formula gives them
+            if (a[7] == Py_None) mean.fill_(std::numeric_limits<float>::quiet_NaN());
+            if (a[8] == Py_None) rstd.fill_(std::numeric_limits<float>::quiet_NaN());
+        }
     }
     const gn_plan* plan = a[11] == Py_None ? nullptr : static_cast<const gn_plan*>(PyLong_AsVoidPtr(a[11]));
     const at::Tensor ws = scratch(a[10], a[10] == Py_None ? gn_bytes(c, false, plan) : 0, c.x);

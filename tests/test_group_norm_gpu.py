@@ -713,3 +713,19 @@ def test_column_sums_of_many_samples(dtype, B, S, C, G):
     for k in (0, B - 3):
         check_bwd(dy[k:k + 3], x[k:k + 3], gamma, beta, mean[k:k + 3], rstd[k:k + 3], G, None, dx[k:k + 3],
                   *rn.gn_bwd(dy[k:k + 3], x[k:k + 3], gamma, beta, mean[k:k + 3], rstd[k:k + 3], G)[1:])
+
+
+def test_statistics_of_empty_samples_are_nan():
+    """The mean and the variance of no values are NaN, as the formula gives
+    them; the caller's own tensors are left as they were."""
+    gamma, beta = torch.ones(16, device="cuda"), torch.zeros(16, device="cuda")
+    e = torch.empty(2, 0, 16, device="cuda")
+    for _ in range(4):
+        old = [torch.full((2, 4), 7.0, device="cuda") for _ in range(4)]
+        del old  # (new tensors of this size find these values in memory)
+        y, mean, rstd = rn.gn_fwd(e, gamma, beta, 4)
+        assert y.shape == e.shape and mean.shape == rstd.shape == (2, 4)
+        assert torch.isnan(mean).all() and torch.isnan(rstd).all()
+    mine = [torch.full((2, 4), 7.0, device="cuda") for _ in range(2)]
+    _, mean, rstd = rn.gn_fwd(e, gamma, beta, 4, mean=mine[0], rstd=mine[1])
+    assert mean is mine[0] and rstd is mine[1] and (mean == 7).all() and (rstd == 7).all()
