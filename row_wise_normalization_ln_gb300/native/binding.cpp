@@ -10,6 +10,7 @@
 // again on the same stream only, so a workspace may be released as soon as
 // the call has queued its kernels.
 #define PY_SSIZE_T_CLEAN
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/cuda/EmptyTensor.h>
@@ -18,6 +19,7 @@
 #include <c10/util/SmallVector.h>
 
 #include <cstdint>
+#include <exception>
 #include <limits>
 #include <stdexcept>
 #include <string>
@@ -359,10 +361,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
         PyErr_SetString(PyExc_ValueError, e.what());
     } catch (const BadType& e) {
         PyErr_SetString(PyExc_TypeError, e.what());
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-    } catch (...) {
-        PyErr_SetString(PyExc_RuntimeError, "unknown error");
+    } catch (...) {  // torch's own, with the types its calls raise (torch.OutOfMemoryError), and any other
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

@@ -729,3 +729,29 @@ def test_statistics_of_empty_samples_are_nan():
     mine = [torch.full((2, 4), 7.0, device="cuda") for _ in range(2)]
     _, mean, rstd = rn.gn_fwd(e, gamma, beta, 4, mean=mine[0], rstd=mine[1])
     assert mean is mine[0] and rstd is mine[1] and (mean == 7).all() and (rstd == 7).all()
+
+
+def test_out_of_memory_has_torchs_type():
+    """An allocation that the allocator refuses raises torch.OutOfMemoryError, as from the
+    row norms, and the next call works."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()  # (so that x lies in a block of its own, with no free space beside it)
+    x = torch.zeros(1, 1 << 20, 64, device="cuda")  # 256 MB
+    gamma, beta = torch.ones(64, device="cuda"), torch.zeros(64, device="cuda")
+    small = x[:, :1000]
+    rn.gn_fwd(small, gamma, beta, 8)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    try:
+        # (the process's own limit, checked before the driver is asked)
+        torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (64 << 20)) /
+                                                   torch.cuda.get_device_properties(0).total_memory)
+        for call in (lambda: rn.ln_fwd(x[0], gamma, beta), lambda: rn.gn_fwd(x, gamma, beta, 8),
+                     lambda: rn.gn_bwd(x, x, gamma, beta, *(torch.zeros(1, 8, device="cuda"),) * 2, 8)):
+            with pytest.raises(torch.OutOfMemoryError):
+                call()
+        y, mean, rstd = rn.gn_fwd(small, gamma, beta, 8)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert (y == 0).all() and (mean == 0).all()
+    assert (rn.gn_fwd(x, gamma, beta, 8)[0] == 0).all()
