@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional, Sequence
+from typing import Iterable, Iterator, Optional
 
 import torch
 
@@ -713,8 +713,14 @@ def gn_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, beta: torch.T
 
 
 # ------------------------------------------------------------ gradients
+def _kept(tensors):
+    """What an iterator (a generator) gives can be read once only: a list of it."""
+    return list(tensors) if isinstance(tensors, Iterator) else tensors
+
+
 def _grad_call(what, grads, outs, max_norm, norm, workspace, stream):
     if stream is not None:
+        grads = grads if isinstance(grads, (list, tuple)) else list(grads)
         if not grads:
             raise ValueError(f"{what} needs at least one tensor")
         return _on_stream(stream, grads[0], lambda: _grad_call(what, grads, outs, max_norm, norm, workspace, None))
@@ -724,7 +730,7 @@ def _grad_call(what, grads, outs, max_norm, norm, workspace, stream):
     return r
 
 
-def grad_norm(grads: Sequence[torch.Tensor], *, norm: Optional[torch.Tensor] = None,
+def grad_norm(grads: Iterable[torch.Tensor], *, norm: Optional[torch.Tensor] = None,
               workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The global norm of a list of CUDA gradients, ``sqrt(sum of all
     squares)``: one fp32 value on the device. The tensors may differ in shape
@@ -735,15 +741,17 @@ def grad_norm(grads: Sequence[torch.Tensor], *, norm: Optional[torch.Tensor] = N
     return _grad_call("grad_norm", grads, None, None, norm, workspace, stream)
 
 
-def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[Sequence[torch.Tensor]] = None,
+def grad_clip(grads: Iterable[torch.Tensor], max_norm: float, *, out: Optional[Iterable[torch.Tensor]] = None,
               norm: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
               stream: Optional[torch.cuda.Stream] = None):
     """Scale a list of gradients by ``min(1, max_norm / (norm + 1e-6))`` with
     norm their global norm (grad_norm): in place, or into ``out``, a list of
-    tensors of the same shapes, strides and types. Returns ``(out, norm)``.
+    tensors of the same shapes, strides and types. Returns ``(out, norm)``, an
+    iterator's tensors as a list.
     With an infinite norm the coefficient is 0, with a NaN norm NaN: read
     ``norm`` to skip such a step. A tensor may be listed once only, and
     ``norm`` may not lie within one of them."""
+    grads, out = _kept(grads), _kept(out)
     norm = _grad_call("grad_clip", grads, out, float(max_norm), norm, workspace, stream)
     return (out if out is not None else grads), norm
 

@@ -301,3 +301,30 @@ def test_clipping_by_norms_far_out(dtype, shape, size):
         assert all(torch.equal(a, b) for a, b in zip(mine, outs))
         if max_norm > 1.0005 * total:
             assert all(torch.equal(a, b) for a, b in zip(outs, ts))
+
+
+def test_lists_from_iterators():
+    """Gradients that come from a generator or a dict's values, as a program
+    collects them from its parameters: used once, and the list of them is what
+    grad_clip hands back."""
+    ts = tensors([(1000,), (7, 5), (20001,)], DTYPES, 8)
+    n = rn.grad_norm(ts)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        for make in (lambda v: (t for t in v), lambda v: dict(enumerate(v)).values(), tuple, list):
+            assert torch.equal(rn.grad_norm(make(ts), stream=stream), n)
+            mine, outs = [t.clone() for t in ts], [torch.empty_like(t) for t in ts]
+            torch.cuda.synchronize()
+            got, norm = rn.grad_clip(make(mine), 0.5, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(norm, n) and all(a is b for a, b in zip(list(got), mine, strict=True))
+            check_clip(ts, mine, 0.5, norm)
+            got, norm = rn.grad_clip(make(ts), 0.5, out=make(outs), stream=stream)
+            torch.cuda.synchronize()
+            assert all(a is b for a, b in zip(list(got), outs, strict=True))
+            assert all(torch.equal(a, b) for a, b in zip(outs, mine))
+    for empty in ([], (t for t in ()), {}.values()):
+        for stream in (None, side):
+            with pytest.raises(ValueError):
+                rn.grad_norm(empty, stream=stream)
