@@ -22,6 +22,7 @@ constexpr int64_t kMaxC = int64_t(1) << 24;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSmem = 48 * 1024;
 constexpr int kMaxCluster = 8;
+constexpr int64_t kMaxChunk = int64_t(1) << 30;  // values of one access column in a row chunk
 constexpr int kFoldRows = 64, kMaxFolds = 256;  // partial rows per folded one, folded rows
 constexpr int kSplitFoldFrom = 4096;            // more partial rows than this are folded on the split path
 constexpr int kFwdMaxRows = 8, kBwdMaxRows = 4;  // rows a thread of the on-chip kernels can hold
@@ -160,7 +161,8 @@ norm_status derive(const gn_plan& p, const Shape& s, GnArgs* a) {
     a->by_out_chunks = libnorm::fast_div(p.out_chunks);
     a->chunk_rows = std::max<int64_t>(1, ceil_div(s.S, p.chunks));
     a->out_rows = std::max<int64_t>(1, ceil_div(s.S, p.out_chunks));
-    if (a->chunk_rows > (int64_t(1) << 30) || a->out_rows > (int64_t(1) << 30)) return NORM_ERR_PLAN;
+    // (a thread counts rows times an access's channels in 32 bits)
+    if (a->chunk_rows * p.vec_elems > kMaxChunk || a->out_rows > kMaxChunk) return NORM_ERR_PLAN;
     // CTAs of a launch, and partial rows of the column gradients
     const int64_t units = s.B * a->tiles, tall = std::max(p.chunks, p.out_chunks);
     if (tall > kMaxGrid / 4 / std::max<int64_t>(1, units) || s.B > kMaxGrid / p.chunks) return NORM_ERR_PLAN;
@@ -264,7 +266,7 @@ void split_plan(const Shape& s, int vec, int sms, gn_plan* p) {
         }
     }
     const int64_t most = std::max<int64_t>(1, ceil_div(s.S, rows));
-    p->chunks = static_cast<int32_t>(std::max(std::min(std::max<int64_t>(1, chunks), most), ceil_div(s.S, int64_t(1) << 30)));
+    p->chunks = static_cast<int32_t>(std::max(std::min(std::max<int64_t>(1, chunks), most), ceil_div(s.S * vec, kMaxChunk)));
     p->out_chunks = p->chunks;
 }
 

@@ -102,6 +102,28 @@ def test_every_shape_gets_a_fitting_plan(lib):
                         assert p["cluster"] * p["per_thread"] * (p["threads"] // p["tile"]) >= S
 
 
+def test_chunks_longer_than_a_thread_counts_are_refused(lib):
+    """A thread's count of the values it adds up (rows it visits times the
+    access's channels) is 32 bits: one CTA of one row at a time over 2^30 rows
+    in pairs would count 2^31."""
+    n = ctypes.c_size_t()
+
+    def need(S, vec, chunks, C=34, out_chunks=None):
+        p = rn.GnPlan.from_dict(dict(path=1, vec_elems=vec, tile=17, threads=32, per_thread=1, cluster=1, chunks=chunks,
+                                     out_chunks=out_chunks or chunks))
+        return lib.gn_workspace_bytes(1, S, C, 1, rn.NORM_BF16, 0, 0, ctypes.byref(p), ctypes.byref(n))
+
+    assert need(1 << 30, 2, 1) == rn.NORM_ERR_PLAN
+    assert need(1 << 29, 8, 2, C=136) == rn.NORM_ERR_PLAN
+    assert need(1 << 30, 2, 2) == need(1 << 29, 2, 1) == need(1 << 30, 1, 1) == rn.NORM_OK
+    # what the planner makes of such lengths fits
+    for S, C in ((1 << 31, 34), ((1 << 33) + 5, 8), ((1 << 35) + 1, 1)):
+        for vec in (8, 2, 1):
+            if C % vec == 0:
+                p = rn.make_gn_plan(1, S, C, 1, torch.bfloat16, False, vec_elems=vec)
+                assert -(-S // p["chunks"]) * vec <= 1 << 30
+
+
 def test_make_plan_refuses_bad_shapes():
     for a in ((0, 8, 64, 4), (1, 0, 64, 4), (1, 8, 64, 3)):
         with pytest.raises((rn.NormError, StopIteration)):
