@@ -607,12 +607,14 @@ def _native():
     the marshalling of the calls below."""
     global _binding_module
     if _binding_module is None:
+        from . import _build
+        how = "build it with `python -c 'import __graft_entry__ as g; g.build()'` (needs nvcc and g++)"
+        if not _build.native_matches():
+            raise LibraryNotBuilt(f"_binding.so was built for another torch or Python: {how}")
         try:
             from . import _binding as m
         except ImportError as e:
-            raise LibraryNotBuilt(
-                "_binding.so is missing or does not load: build it with "
-                "`python -c 'import __graft_entry__ as g; g.build()'` (needs nvcc and g++)") from e
+            raise LibraryNotBuilt(f"_binding.so is missing or does not load: {how}") from e
         _binding_module = m
     return _binding_module
 

@@ -18,6 +18,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnorm.so")
 NATIVE_SRC = os.path.join(PKG, "native", "binding.cpp")
 NATIVE = os.path.join(PKG, "_binding.so")
+NATIVE_KEY = os.path.join(BUILD, "binding.key")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -40,11 +41,42 @@ def _deps() -> list[str]:
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
+def _library_up_to_date() -> bool:
+    if not os.path.exists(LIB):
         return False
     t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps()) and os.path.getmtime(NATIVE_SRC) <= os.path.getmtime(NATIVE)
+    return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _native_key() -> str:
+    """What _binding.so is compiled against, beyond its sources."""
+    import platform
+    import sys
+
+    import torch
+
+    return "\n".join((sys.implementation.cache_tag, platform.machine(), torch.__version__, torch.__file__))
+
+
+def native_matches() -> bool:
+    """Whether _binding.so was compiled against this torch and interpreter
+    (unknown without its key: yes)."""
+    try:
+        with open(NATIVE_KEY) as f:
+            return f.read() == _native_key()
+    except FileNotFoundError:
+        return True
+
+
+def _native_up_to_date() -> bool:
+    if not os.path.exists(NATIVE) or not os.path.exists(NATIVE_KEY) or not native_matches():
+        return False
+    t = os.path.getmtime(NATIVE)
+    return all(os.path.getmtime(p) <= t for p in [NATIVE_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+
+
+def up_to_date() -> bool:
+    return _library_up_to_date() and _native_up_to_date()
 
 
 def _compile_native() -> str:
@@ -83,12 +115,9 @@ def _link_native(obj: str) -> None:
     os.replace(tmp, NATIVE)
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _build_library(verbose: bool, extra_flags: list[str]) -> None:
     cc = nvcc()
-    flags = NVCC_FLAGS + (extra_flags or [])
+    flags = NVCC_FLAGS + extra_flags
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
@@ -103,7 +132,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(sources()), os.cpu_count() or 4))) as ex:
-        native = ex.submit(_compile_native)
         objs = list(ex.map(compile_one, sources()))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
@@ -111,7 +139,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_native(native.result())
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
+    library, native = force or not _library_up_to_date(), force or not _native_up_to_date()
+    if not library and not native:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_compile_native) if native else None
+        if library:
+            _build_library(verbose, extra_flags or [])
+        if native:
+            _link_native(obj.result())
+            with open(NATIVE_KEY, "w") as f:
+                f.write(_native_key())
     return LIB
 
 

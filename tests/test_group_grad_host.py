@@ -5,6 +5,7 @@ import ctypes
 import os
 import random
 import re
+import sys
 
 import pytest
 import torch
@@ -236,3 +237,40 @@ def test_workspace_bytes(lib):
     assert need([-1]) == rn.NORM_ERR_ARG and need([1], 0) == rn.NORM_ERR_ARG
     assert lib.grad_workspace_bytes(None, 1, 152, ctypes.byref(n)) == rn.NORM_ERR_ARG
     assert lib.grad_workspace_bytes(None, 0, 152, None) == rn.NORM_ERR_ARG
+
+
+# ------------------------------------------------------------ building the binding
+
+def test_binding_of_another_torch_is_rebuilt(lib, monkeypatch, tmp_path):
+    """_binding.so holds for the torch and the interpreter it was compiled
+    against: after a change of either it is out of date, alone, and build()
+    makes it again."""
+    assert _build.up_to_date()
+    for where, name, other in ((torch, "__version__", "1.0"), (torch, "__file__", "/elsewhere/torch/__init__.py"),
+                               (sys.implementation, "cache_tag", "cpython-39")):
+        with monkeypatch.context() as m:
+            m.setattr(where, name, other)
+            assert not _build.up_to_date()
+    assert _build.up_to_date()
+    made = []
+    key = tmp_path / "binding.key"
+    key.write_text("another")
+    monkeypatch.setattr(_build, "NATIVE_KEY", str(key))
+    monkeypatch.setattr(_build, "_compile_native", lambda: made.append("compiled") or "obj")
+    monkeypatch.setattr(_build, "_link_native", lambda obj: made.append(obj))
+    before = os.path.getmtime(_build.LIB)
+    assert not _build.up_to_date()
+    _build.build()
+    assert made == ["compiled", "obj"] and os.path.getmtime(_build.LIB) == before and _build.up_to_date()
+    _build.build()
+    assert len(made) == 2
+
+
+def test_binding_of_another_torch_is_not_loaded(lib, monkeypatch, tmp_path):
+    """It may not fit, so a call says what to do instead of loading it."""
+    key = tmp_path / "binding.key"
+    key.write_text("another")
+    monkeypatch.setattr(_build, "NATIVE_KEY", str(key))
+    monkeypatch.setattr(rn, "_binding_module", None)
+    with pytest.raises(rn.LibraryNotBuilt, match="build"):
+        rn.grad_norm([torch.zeros(3)])
