@@ -274,3 +274,28 @@ def test_binding_of_another_torch_is_not_loaded(lib, monkeypatch, tmp_path):
     monkeypatch.setattr(rn, "_binding_module", None)
     with pytest.raises(rn.LibraryNotBuilt, match="build"):
         rn.grad_norm([torch.zeros(3)])
+
+
+def test_row_norms_build_without_the_binding(lib, monkeypatch, tmp_path):
+    """libnorm.so, and with it the row norms, needs nvcc alone: where the
+    binding of the group norm and gradient calls does not compile (no Python or
+    torch headers), build() says so and leaves none behind."""
+    native, key = tmp_path / "_binding.so", tmp_path / "binding.key"
+    native.write_text("stale")
+    key.write_text("another")
+    monkeypatch.setattr(_build, "NATIVE", str(native))
+    monkeypatch.setattr(_build, "NATIVE_KEY", str(key))
+
+    def fails():
+        raise RuntimeError("Python.h: No such file or directory")
+
+    monkeypatch.setattr(_build, "_compile_native", fails)
+    with pytest.warns(RuntimeWarning, match="Python.h"):
+        assert _build.build() == _build.LIB
+    assert not native.exists() and not key.exists() and not _build.up_to_date()
+    assert lib.norm_abi_version() > 0
+    built = []
+    monkeypatch.setattr(_build, "_build_library", lambda *a: built.append(a))
+    with pytest.warns(RuntimeWarning):
+        _build.build(force=True)
+    assert len(built) == 1
