@@ -788,3 +788,44 @@ def test_statistics_to_a_few_roundings(dtype, B, S, C, G, loc):
     off = (mean.to(F) - mu).abs()
     bar = U * (mu.abs() + 2 * var.sqrt() + 2 * (xg[:, 0, :, 0] - mu).abs())
     assert (off <= bar).all(), (off / bar).max().item()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_to_their_own_arithmetic(act):
+    """Outputs for arguments from -13 to 13 in steps of 1e-4, relative to the
+    output itself: in the negative tails too, where y is far below any
+    absolute bound. z is taken from the returned statistics: x - mean, rstd
+    gamma and the product round once each and what the rounding of the mean
+    left is added back, so z is off by zerr = 3 u |z| + u |mean| rstd gamma, y by
+    |act'| zerr + 0.4 zerr^2 (|act''| <= 0.8).
+    silu, z / (1 + e): e = 2^t with |t| ln 2 = |z| off by 2 u relative and the
+    hardware's 2^t by 4 u: (2 |z| + 4) u of e, e / (1 + e) of which is
+    passed on; the sum 1, the reciprocal 2, the product 1.
+    gelu, max(z, 0) - m tail, m = |z|: with t = 1 / (1 + p m) off by 4 u, the
+    polynomial Q(t) passes on 2.7 times that and its own roundings are at most
+    15.7 u (the sum of |coefficient| t^i times the roundings each goes through, over
+    Q, is below that on the whole range); exp(-m^2 / 2): 1.5 m^2 + 4; two
+    products 2; the fit itself 18 (1.06e-6). Together (52 + 1.5 m^2) u of
+    m tail, and one rounding of y."""
+    half = torch.linspace(1e-4, 13, 130000)
+    x = torch.cat([half, -half]).view(1, -1, 1).cuda()
+    sigma = float(x.double().square().mean().sqrt())
+    gamma, beta = torch.full((1,), sigma, device="cuda"), torch.zeros(1, device="cuda")
+    y, mean, rstd = rn.gn_fwd(x, gamma, beta, 1, EPS, activation=act)
+    mean, s = float(mean), float(rstd) * float(gamma)
+    z = (x.to(F) - mean) * s
+    assert z.min() < -12.9 and z.max() > 12.9
+    zerr = U * (3 * z.abs() + abs(mean) * s)
+    tol = slope64(z, act).abs() * zerr + 0.4 * zerr.square()
+    if act == "silu":
+        ref = z * torch.sigmoid(z)
+        own = (torch.sigmoid(-z) * (2 * z.abs() + 4) + 4) * U * ref.abs()
+    else:
+        tail = 0.5 * torch.erfc(z.abs() / math.sqrt(2))
+        ref = z.clamp(min=0) - z.abs() * tail
+        own = (52 + 1.5 * z.square()) * U * z.abs() * tail + U * ref.abs()
+    # (below fp32's smallest normal numbers the tail keeps 2^-149 steps)
+    tol = tol + own + 16 * 2.0 ** -149
+    err = (y.to(F) - ref).abs()
+    worst = (err / tol).max().item()
+    assert worst <= 1, (worst, float(z.flatten()[(err / tol).argmax()]))
