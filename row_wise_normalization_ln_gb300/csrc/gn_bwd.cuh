@@ -138,8 +138,11 @@ __device__ __forceinline__ void gn_bwd_put(float2* st, int tile, int col, const 
 template <class T, int VEC>
 __device__ __forceinline__ void gn_bwd_merge_threads(const GnArgs& a, const GnTile& w, float2* st, int stride,
                                                      float2* gs) {
-    // `deep` threads per state add every deep-th row slot, then one adds theirs
+    // `deep` threads per state add every deep-th row slot, halve what is left
+    // while it is more than 8, and one adds the rest. (Few channels leave up to
+    // 256: one chain of them was off by 5 u of the root of the terms' squares.)
     const int deep = min(a.par, max(1, small_quot(blockDim.x, stride)));
+    int left = a.par;
     if (deep > 1) {
         const int d = small_quot(threadIdx.x, stride), i = static_cast<int>(threadIdx.x) - d * stride;
         if (d < deep) {
@@ -149,8 +152,13 @@ __device__ __forceinline__ void gn_bwd_merge_threads(const GnArgs& a, const GnTi
             st[d * stride + i] = t;
         }
         __syncthreads();
+        for (left = deep; left > 8;) {
+            const int half = (left + 1) >> 1;
+            if (d + half < left) st[d * stride + i] = __fadd2_rn(st[d * stride + i], st[(d + half) * stride + i]);
+            __syncthreads();
+            left = half;
+        }
     }
-    const int left = deep > 1 ? deep : a.par;
     for (int i = threadIdx.x; i < stride; i += blockDim.x) {
         float2 t = st[i];
 #pragma unroll 4
@@ -394,16 +402,17 @@ __device__ __forceinline__ void gn_bwd_apply(const GnArgs& a, const GnTile& w, i
 }
 
 // dgamma and dbeta of 32 columns from the partial rows: warp w adds rows w,
-// w + warps, ... in that order, in blocks of kGnSumRows, then the warps' sums
+// w + warps, ... in that order, in blocks of kGnAddRows, then the warps' sums
 // in warp order. (One chain of 2048 rows was off by 424 u where all had one
 // sign.)
+constexpr int kGnAddRows = 16;
 __device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, float2* sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int c = block * 32 + lane;
     float2 t = make_float2(0.f, 0.f);
     if (c < a.C)
         for (int p = warp; p < a.partials;) {
-            const int stop = min(a.partials, p + kGnSumRows * warps);
+            const int stop = min(a.partials, p + kGnAddRows * warps);
             float2 block = make_float2(0.f, 0.f);
 #pragma unroll 8
             for (; p < stop; p += warps)

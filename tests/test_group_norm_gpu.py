@@ -829,3 +829,33 @@ def test_activations_to_their_own_arithmetic(act):
     err = (y.to(F) - ref).abs()
     worst = (err / tol).max().item()
     assert worst <= 1, (worst, float(z.flatten()[(err / tol).argmax()]))
+
+
+@pytest.mark.parametrize("dtype,B,S,C", [("f32", 1, 100003, 1), ("f32", 3, 20001, 1), ("bf16", 2, 30000, 2), ("f32", 2, 30000, 4),
+                                         ("bf16", 1, 60000, 8), ("f16", 9, 5001, 3), ("f32", 2, 1000, 1), ("f32", 1, 900000, 1)])
+def test_column_sums_of_few_channels(dtype, B, S, C):
+    """Few channels leave few sums with many threads each. A chain of L
+    additions of terms alike in size, of either sign, is off by u / sqrt 3
+    sqrt(L / 2) of the root of its terms' squares where every addition's
+    rounding is taken as even over half a step (at most; 0.73 of that over a
+    binade), and a tree by u / sqrt 3 a level. The sums go through chains of
+    32 rows a thread (2.3 u), their blocks (8 at most here: 1.2), a tree and
+    a chain of 8 over the CTA's row slots (5 levels and 1.2: 1.8), blocks of 16
+    partial rows (1.6), the blocks (6: 1) and 8 warps (1.2): together, as
+    independent, 3.9 u of the root of the squares. Held over 40 sums of 40 seeds
+    as their root mean square, whose own spread is a ninth: 1.3 times that
+    bound would be off by three of those, the bound itself leaves the 0.73.
+    One chain over 256 row slots alone is 6.5 u."""
+    dt = DT[dtype]
+    rel = []
+    for seed in range(-(-40 // C)):
+        x, dy, gamma, beta = make(B, S, C, dt, 1000 + seed)
+        _, mean, rstd = rn.gn_fwd(x, gamma, beta, 1, EPS)
+        _, dg, db = rn.gn_bwd(dy, x, gamma, beta, mean, rstd, 1)
+        xh = (x.to(F) - spread(mean.to(F), C)) * spread(rstd.to(F), C)
+        for got, terms in ((dg, dy.to(F) * xh), (db, dy.to(F))):
+            rel.append((got.to(F) - terms.sum((0, 1))) / terms.square().sum((0, 1)).sqrt())
+    rel = torch.stack(rel).view(-1, 2, C)
+    for k in range(2):
+        rms = rel[:, k].square().mean().sqrt().item()
+        assert rms <= 3.9 * U, (k, rms / U)
