@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Iterable, Iterator, Optional
+from typing import Iterable, Optional
 
 import torch
 
@@ -717,7 +717,7 @@ def gn_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, beta: torch.T
 # ------------------------------------------------------------ gradients
 def _kept(tensors):
     """What an iterator (a generator) gives can be read once only: a list of it."""
-    return list(tensors) if isinstance(tensors, Iterator) else tensors
+    return list(tensors) if hasattr(tensors, "__next__") else tensors
 
 
 def _grad_call(what, grads, outs, max_norm, norm, workspace, stream):

@@ -682,7 +682,7 @@ def test_chain_that_rewrites_parameters_and_statistics(dtype, B, S, C, G):
 
 @pytest.mark.parametrize("dtype,B,S,C,G", [("f32", 16384, 1100, 8, 1), ("bf16", 3000, 1030, 6, 2), ("f32", 1500, 3001, 12, 3),
                                            ("f32", 4096, 1100, 8, 1), ("f32", 4097, 1100, 8, 1),
-                                           ("f32", (1 << 21) + 3, 1, 4, 1)])
+                                           ("f32", (1 << 21) + 3, 1, 4, 1), ("bf16", 5000, 1030, 6, 2)])
 def test_column_sums_of_many_samples(dtype, B, S, C, G):
     """Thousands of samples with more positions than one CTA holds, and millions
     of one: as many partial rows of the column gradients, all of one sign. Every
