@@ -197,14 +197,14 @@ bool chip_plan(const Shape& s, int vec, int sms, gn_plan* p) {
         if (v > maxv) continue;
         // a backward whose samples do not meet in one cluster needs another
         // launch for the column sums, and clusters then lose to the split path
-        // (gn_bwd f32 3x1517x180 13 us against 10)
+        // (gn_bwd f32 3x1517x180 10.1 us against 8.6)
         if (s.bwd && cs > 1 && s.B * cs > kMaxCluster) break;
         if (found && (rows * tile < 256 || units * cs > 4 * int64_t(sms))) break;
         // The largest clusters lose to the split path where they are many CTAs
-        // per SM (gn_fwd f32 16x1024x1280 58 us against 45; in clusters of 4,
-        // f32 8x1024x640, 16.8 against 18.5), and, at the most rows per thread,
+        // per SM (gn_fwd f32 16x1024x1280 60 us against 45; in clusters of 4,
+        // f32 8x1024x640, 17.0 against 18.9), and, at the most rows per thread,
         // where they leave SMs without one (bf16 1x4096x512 9.6 us against
-        // 7.8, 2x2048x320 8.6 against 7.7).
+        // 8.1, 2x2048x320 8.0 against 7.4).
         if (cs == kMaxCluster && (units * cs > 4 * int64_t(sms) || (v == maxv && units * cs < sms))) break;
         p->path = GN_PATH_CHIP;
         p->vec_elems = vec;
@@ -234,15 +234,15 @@ void split_plan(const Shape& s, int vec, int sms, gn_plan* p) {
     const int64_t rows = p->threads / tile;
     // One CTA per SM while a thread has few rows, two per SM otherwise (four of
     // narrower accesses, which have fewer bytes in flight each: f16 5x363654x25
-    // gn_fwd 98 us instead of 137, gn_bwd 151 instead of 220); counts between
+    // gn_fwd 97 us instead of 146, gn_bwd 150 instead of 215); counts between
     // leave some SMs with twice the rows of others. Measured in us with
     // one / two per SM, at the rows per thread that one gives: gn_fwd bf16
-    // 2x4096x320 (9 rows) 9.1 / 11.5, 1x16384x256 (14) 9.6 / 9.9, 2x8192x320
-    // (18) 11.9 / 14.3, f32 2x4096x320 (19) 11.9 / 11.7, bf16 8x4096x320 (41)
-    // 23.2 / 20.0; gn_bwd f32 3x1517x180 (6) 8.1 / 8.9, bf16 1x4096x512 (7)
-    // 11.1 / 9.7, 2x4096x320 (9) 12.9 / 12.5, 4x4096x320 (19) 19.4 / 16.0. With
-    // narrower accesses, one / four per SM: gn_bwd f32 2x10000x30 (14) 8.3 /
-    // 11.3, gn_fwd f32 10x445x175 (21) 7.8 / 9.5, f16 8x1500x75 (40) 12.2 / 10.3.
+    // 2x4096x320 (9 rows) 9.4 / 11.8, 1x16384x256 (14) 10.0 / 10.4, 2x8192x320
+    // (18) 12.1 / 14.7, f32 2x4096x320 (19) 12.4 / 12.2, bf16 8x4096x320 (41)
+    // 23.3 / 20.4; gn_bwd f32 3x1517x180 (6) 8.7 / 9.8, bf16 1x4096x512 (7)
+    // 11.7 / 10.2, 2x4096x320 (9) 13.9 / 12.7, 4x4096x320 (19) 19.6 / 16.2. With
+    // narrower accesses, one / four per SM: gn_bwd f32 2x10000x30 (17) 9.5 /
+    // 12.5, gn_fwd f32 10x445x175 (22) 8.3 / 9.5, f16 8x1500x75 (56) 11.9 / 9.9.
     const int64_t once = std::max<int64_t>(1, sms / units);
     const bool whole = vec * es == 16;  // 16-byte accesses
     const int64_t slots = int64_t(sms) * (whole ? 2 : 4);
@@ -252,7 +252,7 @@ void split_plan(const Shape& s, int vec, int sms, gn_plan* p) {
         // Where whole chunks of every sample and tile leave a tenth of the two
         // CTAs per SM without work, up to 8 rounds of them, the first that
         // leave less or the fullest, while a thread has 16 rows or more (gn_bwd
-        // f16 14x5390x768, 154 tiles: 105 us with 9 chunks each, 144 with 1;
+        // f16 14x5390x768, 154 tiles: 112 us with 9 chunks each, 164 with 1;
         // gn_fwd bf16 10x2897x1024 36 with 5, 45 with 1).
         double best = 0.0;
         for (int64_t round = 1; round <= 8 && best < 0.9; ++round) {

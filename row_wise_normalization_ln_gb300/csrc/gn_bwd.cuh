@@ -18,10 +18,10 @@
 //   gn_bwd_chip   launch and latency: bf16 2x256x1280 6.7 us, its two samples
 //                 in clusters of 8 so that the column sums need no launch.
 //   split         HBM, with x and dy read twice where they exceed L2: bf16
-//                 4x65536x256 105 us, 6.4 TB/s of its 671 MB (sums 48 us at 5.6
-//                 TB/s, two thirds of the issue slots in use; apply 65 at 6.0).
-//                 f16 8x4096x320 22 us; f32 3x1517x180, two launches of about
-//                 4 us, 8.4 us.
+//                 4x65536x256 106 us, 6.3 TB/s of its 671 MB (sums 49 us at 5.7
+//                 TB/s, two thirds of the issue slots in use; apply 64 at 6.2).
+//                 f16 8x4096x320 23 us; f32 3x1517x180, two launches of about
+//                 4 us, 9.0 us.
 // A persistent kernel over bands of rows that stay in L2 took 173 us where the
 // two launches then took 106.
 #pragma once

@@ -20,14 +20,15 @@
 // over inputs beyond L2):
 //   gn_fwd_chip   launch and latency: a load, the merges, in a cluster two
 //                 barriers, a store. bf16 1x64x1280 3.4 us, f32 3x1517x180
-//                 (6.6 MB, clusters of 8) 7.3 us.
+//                 (6.6 MB, clusters of 8) 7.4 us.
 //   split         HBM, with x read twice where it exceeds L2: bf16
 //                 1x262144x256 69 us, 5.8 TB/s of its 403 MB (sums 26 us at
-//                 5.1 TB/s, apply 45 at 5.5). Small calls are two launches of
-//                 about 4 us: bf16 2x4096x320 9.0 us.
-// Kernels that keep a sample in shared memory, one persistent kernel that works
-// in bands of rows that stay in L2, and bands in launches of their own were
-// measured and were slower (the persistent one 91 us for the 69).
+//                 5.2 TB/s, apply 44 at 5.6). Small calls are two launches of
+//                 about 4 us, and the second's first rows, which it may not
+//                 read before its wait: bf16 2x4096x320 9.6 us.
+// One persistent kernel that works in bands of rows that stay in L2, and bands
+// in launches of their own, were measured and were slower (the persistent one
+// 91 us for the 69).
 #pragma once
 
 #include "gn_kernels.cuh"

@@ -324,7 +324,8 @@ __device__ __forceinline__ float2 gn_peer(const float2* p, int i, uint32_t rank)
 // A slot is refilled one step after it was read. (Rings measured in us for
 // gn_fwd bf16 1x262144x256 / gn_bwd f16 8x4096x320 / bf16 4x65536x256: 4 steps
 // of 2 rows 69 / 22 / 104; 4 of 1 79 / 22 / 113; 8 of 1 69 / 23 / 107; 2 of 4
-// 75 / 22 / 105; 4 of 4 76 / 33 / 115. Of 4 bytes, gn_bwd f32 5x363654x25: 4 of
+// 75 / 22 / 105; 4 of 4 76 / 33 / 115, when the second launch still read ahead of
+// its wait: 0.6 us less of the second case. Of 4 bytes, gn_bwd f32 5x363654x25: 4 of
 // 4 278, 4 of 2 310, 8 of 4 293, with two CTAs per SM.) Accesses of one 16-bit
 // value, which asynchronous copies do not have, are loaded kBatch rows at a time
 // instead (gn_bwd f16 5x363654x25, two CTAs per SM: 8 rows 220 us, 4 287; four:

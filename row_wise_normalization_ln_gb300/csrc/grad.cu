@@ -9,9 +9,9 @@
 //
 // The kernels stream: each value is read once per pass, which is all the
 // arithmetic needs (bound: HBM; on one GB300 with a copy bandwidth of 6.8 TB/s,
-// the norm of 1.6 GB in bf16 228 us, 7.1 TB/s; clipping 1 GB in fp32 into other
-// buffers 465 us, 6.5 TB/s of its 3 GB: sums 150 us, scaling 311). The list is
-// cut into units of one 16-byte access per thread of a CTA; CTA i of G takes
+// the norm of 1.6 GB in bf16 229 us, 7.0 TB/s; clipping 1 GB in fp32 into other
+// buffers 467 to 476 us, 6.4 TB/s of its 3 GB: sums 150 us, scaling 306 to
+// 315). The list is cut into units of one 16-byte access per thread of a CTA; CTA i of G takes
 // the units [U i / G, U (i + 1) / G), so the shares differ by one unit at most
 // however the sizes are mixed, and a share is a run of neighbouring addresses
 // but for the steps between tensors. The scaling walks its shares from the
