@@ -429,24 +429,28 @@ __device__ __forceinline__ void gn_bwd_add_cols(const GnArgs& a, int block, floa
 }
 
 // Row i of a.folds: the sum of the partial rows [P i / folds, P (i + 1) /
-// folds) of 2 C values, 32 columns per CTA. Order fixed as above.
+// folds) of 2 C values, 32 columns per CTA. Order fixed as above. Blocks of
+// kGnSumRows rows, and these with the error of each addition kept (Knuth's
+// two-sum): there may be 2^31 rows, which are counted in 64 bits for that.
 static __global__ void __launch_bounds__(256) gn_bwd_fold(const GnArgs a) {
     __shared__ float sm[256];
     grid_release();
     grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.y, width = 2 * a.C, c = blockIdx.x * 32 + lane;
-    const int lo = static_cast<int>(int64_t(a.partials) * i / a.folds);
-    const int hi = static_cast<int>(int64_t(a.partials) * (i + 1) / a.folds);
-    float t = 0.f;
+    const int64_t lo = int64_t(a.partials) * i / a.folds, hi = int64_t(a.partials) * (i + 1) / a.folds;
+    float t = 0.f, rest = 0.f;
     if (c < width)
-        for (int p = lo + warp; p < hi;) {
-            const int stop = min(hi, p + kGnSumRows * 8);
+        for (int64_t p = lo + warp; p < hi;) {
+            const int64_t stop = min(hi, p + kGnSumRows * 8);
             float block = 0.f;
 #pragma unroll 8
             for (; p < stop; p += 8) block += a.colg[p * a.col_pitch + c];
-            t += block;
+            const float s = t + block, b = s - t;
+            rest += (t - (s - b)) + (block - b);
+            t = s;
         }
+    if (isfinite(t)) t += rest;  // (an infinite sum has no rest)
     sm[threadIdx.x] = t;
     __syncthreads();
     if (warp == 0 && c < width) {

@@ -859,3 +859,39 @@ def test_column_sums_of_few_channels(dtype, B, S, C):
     for k in range(2):
         rms = rel[:, k].square().mean().sqrt().item()
         assert rms <= 3.9 * U, (k, rms / U)
+
+
+def test_most_samples():
+    """As many samples as the limits allow, of one value each: y is beta, dx
+    vanishes but for two roundings of rstd gamma dy, dgamma is 0, and dbeta's
+    additions are at most 32 partial rows, 8 warps, 8 folded rows and 32 warps, and
+    the blocks of rows, whose errors are kept: 80 u of a sum of one sign, and
+    8 more for the pair's last digits."""
+    B, v = (1 << 31) - 2, 0.7
+    x = torch.empty(B, 1, dtype=torch.bfloat16, device="cuda").normal_()
+    gamma, beta = torch.full((1,), 1.5, dtype=torch.bfloat16, device="cuda"), torch.full((1,), 0.25, dtype=torch.bfloat16, device="cuda")
+    y, mean, rstd = rn.gn_fwd(x, gamma, beta, 1, EPS)
+    assert (y == 0.25).all() and torch.equal(mean[-1000:], x[-1000:].float())
+    assert (rstd == rstd[0]).all() and abs(float(rstd[0]) * EPS ** 0.5 - 1) <= 4 * U
+    dy = y.fill_(v)
+    dx, dg, db = rn.gn_bwd(dy, x, gamma, beta, mean, rstd, 1)
+    assert dx.abs().max() <= 4 * U * float(rstd[0]) * 1.5 * v * 1.01 and float(dg) == 0.0
+    want = float(torch.tensor(v).bfloat16()) * B
+    assert abs(float(db) - want) <= 88 * U * want
+
+
+@pytest.mark.parametrize("B,S,C", [(3, 50, 8), (3000, 3, 8), (9000, 1030, 6), (40, 5000, 8)])
+def test_infinite_gradients_stay_in_their_channels(B, S, C):
+    """An infinity in dy is an infinite dbeta of its channel, however the
+    partial rows are added; the other channels' sums are as without it."""
+    x, dy, gamma, beta = make(1, S, C, torch.float32, 51)
+    x, dy = (torch.randn(B, S, C, device="cuda") for _ in range(2))
+    _, mean, rstd = rn.gn_fwd(x, gamma, beta, 1, EPS)
+    dy[B // 2, S // 2, 2] = 0.0
+    _, cg, cb = rn.gn_bwd(dy, x, gamma, beta, mean, rstd, 1)
+    for v in (math.inf, -math.inf):
+        dy[B // 2, S // 2, 2] = v
+        _, dg, db = rn.gn_bwd(dy, x, gamma, beta, mean, rstd, 1)
+        assert float(db[2]) == v and torch.isinf(dg[2])
+        keep = torch.arange(C, device="cuda") != 2
+        assert torch.equal(db[keep], cb[keep]) and torch.equal(dg[keep], cg[keep])
