@@ -22,6 +22,7 @@ __all__ = [
     "ln_fwd", "rms_fwd", "ln_fwd_add", "rms_fwd_add", "ln_fwd_fp8", "rms_fwd_fp8", "ln_bwd", "rms_bwd",
     "make_plan", "make_bwd_plan", "NormPlan", "NormError", "LibraryNotBuilt", "library", "host_rows_pipeline",
     "host_rows_wait", "gn_fwd", "gn_bwd", "make_gn_plan", "gn_workspace_bytes", "GnPlan", "grad_norm", "grad_clip",
+    "rms_fwd_rope", "rms_bwd_rope", "make_rope_plan", "RopePlan",
     "NORM_F32", "NORM_BF16", "NORM_F16", "NORM_MAP_GROUP", "NORM_MAP_CTA",
 ]
 
@@ -67,6 +68,19 @@ class GnPlan(ctypes.Structure):
 
     @classmethod
     def from_dict(cls, d: dict) -> "GnPlan":
+        return cls(**{k: int(v) for k, v in d.items()})
+
+
+class RopePlan(ctypes.Structure):
+    """Mirror of ``norm_rope_plan`` in include/libnorm_rope.h."""
+    _fields_ = [(k, ctypes.c_int32) for k in ("vec_elems", "pairs", "lanes", "slots", "warps", "reserved")] + \
+        [("ctas", ctypes.c_int64)]
+
+    def as_dict(self) -> dict:
+        return {k: getattr(self, k) for k, _ in self._fields_}
+
+    @classmethod
+    def from_dict(cls, d: dict) -> "RopePlan":
         return cls(**{k: int(v) for k, v in d.items()})
 
 
@@ -143,6 +157,16 @@ def library() -> ctypes.CDLL:
     L.grad_workspace_bytes.argtypes = [vp, i64, i32, ctypes.POINTER(sz)]
     for f in ("gn_fwd", "gn_bwd", "gn_fwd_planned", "gn_bwd_planned", "gn_make_plan", "gn_workspace_bytes",
               "grad_norm", "grad_clip", "grad_workspace_bytes"):
+        getattr(L, f).restype = ctypes.c_int
+    rp = ctypes.POINTER(RopePlan)
+    L.rope_make_plan.argtypes = [i64, i64, i64, i64, i64, i32, i32, i32, i32, i32, rp]
+    L.rope_workspace_bytes.argtypes = [i64, i64, i64, i64, i32, rp, ctypes.POINTER(sz)]
+    L.rms_fwd_rope.argtypes = [vp, vp, vp, i64, i64, i64, f32, i32, vp]
+    L.rms_bwd_rope.argtypes = [vp, vp, vp, vp, sz, i64, i64, i64, f32, i32, vp]
+    L.rms_fwd_rope_planned.argtypes = L.rms_fwd_rope.argtypes + [rp]
+    L.rms_bwd_rope_planned.argtypes = L.rms_bwd_rope.argtypes + [rp]
+    for f in ("rope_make_plan", "rope_workspace_bytes", "rms_fwd_rope", "rms_bwd_rope", "rms_fwd_rope_planned",
+              "rms_bwd_rope_planned"):
         getattr(L, f).restype = ctypes.c_int
     L.norm_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     L.norm_synchronize.argtypes = []
@@ -756,6 +780,83 @@ def grad_clip(grads: Iterable[torch.Tensor], max_norm: float, *, out: Optional[I
     grads, out = _kept(grads), _kept(out)
     norm = _grad_call("grad_clip", grads, out, float(max_norm), norm, workspace, stream)
     return (out if out is not None else grads), norm
+
+
+# ------------------------------------------------------------ head norms with rotation
+def make_rope_plan(tokens: int, q_heads: int, k_heads: int, D: int, R: int, dtype: torch.dtype,
+                   interleaved: bool = False, backward: bool = False, vec_elems: Optional[int] = None,
+                   num_sms: int = 152) -> dict:
+    """The plan rms_fwd_rope / rms_bwd_rope would choose (host only);
+    ``vec_elems``: values per access the tensors allow (default: the widest
+    that D and R allow)."""
+    code = _dtype_code(dtype)
+    if vec_elems is None:
+        vec_elems = next(v for v in ((4, 1) if code == NORM_F32 else (8, 2, 1))
+                         if v == 1 or D % v == 0 and (R if interleaved else R // 2) % v == 0)
+    p = RopePlan()
+    st = library().rope_make_plan(tokens, q_heads, k_heads, D, R, int(interleaved), code, int(backward), vec_elems,
+                                  num_sms, ctypes.byref(p))
+    if st != NORM_OK:
+        raise NormError(st, "rope_make_plan")
+    return p.as_dict()
+
+
+def _rope_plan(plan) -> Optional[RopePlan]:
+    return plan if plan is None or isinstance(plan, RopePlan) else RopePlan.from_dict(plan)
+
+
+def rms_fwd_rope(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, wk: Optional[torch.Tensor],
+                 cos: torch.Tensor, sin: torch.Tensor, positions: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
+                 interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None, plan=None):
+    """RMSNorm of every query and key head and the rotary rotation of its
+    first R values, in one pass. ``q``: ``[tokens, heads, D]`` or
+    ``[B, S, heads, D]`` (any strides of the leading dimensions: slices of a
+    packed projection, a transposed ``[B, heads, S, D]``); ``k``: as many
+    tokens, its own heads (None: queries alone, ``wk`` None too). ``wq``,
+    ``wk``: ``[D]``. ``cos``, ``sin``: fp32 tables ``[positions, R / 2]``;
+    value pairs (i, i + R/2) turn by angle i, or ``interleaved`` (2i, 2i + 1).
+    ``positions``: int64 or int32, one per token (default: 0, 1, ... along
+    each sequence). A negative position marks a padding token, whose outputs
+    are zeros; one beyond the tables gives NaN.
+
+    Returns ``(q_out, k_out)``; they may be ``q`` and ``k`` themselves (in
+    place), or views such as the step's rows of a cache. One token or many:
+    the same call."""
+    if stream is not None:
+        return _on_stream(stream, q, lambda: rms_fwd_rope(q, k, wq, wk, cos, sin, positions, eps,
+                                                          interleaved=interleaved, q_out=q_out, k_out=k_out, plan=plan))
+    p = _rope_plan(plan)
+    r = _native().rms_fwd_rope(q, k, wq, wk, cos, sin, positions, eps, bool(interleaved), q_out, k_out,
+                               None if p is None else ctypes.addressof(p))
+    if type(r) is int:
+        raise NormError(r, "rms_fwd_rope")
+    return r
+
+
+def rms_bwd_rope(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor],
+                 wq: torch.Tensor, wk: Optional[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor,
+                 positions: Optional[torch.Tensor] = None, eps: float = 1e-6, *, interleaved: bool = False,
+                 dq_out: Optional[torch.Tensor] = None, dk_out: Optional[torch.Tensor] = None,
+                 dwq: Optional[torch.Tensor] = None, dwk: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None, plan=None):
+    """Backward of rms_fwd_rope: ``dq``, ``dk`` are the gradients of its
+    outputs, the other arguments its own. Returns ``(dq_out, dk_out, dwq,
+    dwk)``: the gradients of q and k in their type (``dq_out`` may be ``dq``
+    or ``q`` itself, or a view of a packed gradient) and of the weights,
+    fp32 ``[D]``. Padding tokens get zeros. ``workspace`` (any dtype) is
+    allocated when not given; calls that share one must not overlap on the
+    GPU."""
+    if stream is not None:
+        return _on_stream(stream, q, lambda: rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, positions, eps,
+                                                          interleaved=interleaved, dq_out=dq_out, dk_out=dk_out,
+                                                          dwq=dwq, dwk=dwk, workspace=workspace, plan=plan))
+    p = _rope_plan(plan)
+    r = _native().rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, positions, eps, bool(interleaved), dq_out, dk_out, dwq,
+                               dwk, workspace, None if p is None else ctypes.addressof(p))
+    if type(r) is int:
+        raise NormError(r, "rms_bwd_rope")
+    return r
 
 
 # ------------------------------------------------------------ host buffers

@@ -1,7 +1,7 @@
-// Native half of the Python binding of the group norm and gradient calls:
-// checks the tensors, allocates what the caller did not give, and passes
-// pointers and the current stream to the C ABI (libnorm_group.h,
-// libnorm_grad.h). These calls are short and many (a step of a small network,
+// Native half of the Python binding of the group norm, gradient and head norm
+// calls: checks the tensors, allocates what the caller did not
+// give, and passes pointers and the current stream to the C ABI
+// (libnorm_group.h, libnorm_grad.h, libnorm_rope.h). These calls are short and many (a step of a small network,
 // lists of hundreds of gradients); marshalling them through ctypes took three
 // to five times as long as their kernels.
 //
@@ -18,6 +18,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/SmallVector.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <exception>
 #include <limits>
@@ -28,6 +29,7 @@
 
 #include "libnorm_grad.h"
 #include "libnorm_group.h"
+#include "libnorm_rope.h"
 
 namespace {
 
@@ -350,6 +352,188 @@ PyObject* grad_py(PyObject* const* a) {
     return a[3] == Py_None ? THPVariable_Wrap(norm) : Py_NewRef(a[3]);
 }
 
+// ------------------------------------------------------------ head norms with rotation
+// Heads [T, heads, D] or [B, S, heads, D] with unit stride of their values.
+bool heads_of(const at::Tensor& t, norm_heads* h) {
+    const int64_t n = t.dim();
+    h->data = ptr(t);
+    h->batch = n == 4 ? t.stride(0) : 0;
+    h->token = t.stride(n - 3);
+    h->head = t.stride(n - 2);
+    return t.size(n - 1) == 1 || t.stride(n - 1) == 1 || t.numel() == 0;
+}
+
+struct HeadCall {
+    at::Tensor x[2], dy[2], w[2], out[2], dw[2], cos, sin, positions;  // queries, keys
+    norm_rope_side side[2] = {};
+    norm_rope_angles angles = {};
+    norm_dtype dtype;
+    int64_t B = 1, S, D;
+};
+
+const char* const kHeadNames[2] = {"q", "k"};
+
+void same_kind(const at::Tensor& t, const at::Tensor& x, const std::string& name) {
+    if (t.device() != x.device() || t.scalar_type() != x.scalar_type())
+        refuse(name + " must be on " + x.device().str() + " with dtype " + c10::toString(x.scalar_type()));
+}
+
+// Checks shared by forward and backward; inputs whose values lie apart are copied.
+void read_heads(HeadCall* c, PyObject* const* x, PyObject* const* w, PyObject* cos, PyObject* sin, PyObject* positions,
+                PyObject* interleaved, const char* what) {
+    for (int i = 0; i < 2; ++i) {
+        if (i == 1 && x[1] == Py_None) {
+            if (w[1] != Py_None) refuse("wk is given without k");
+            break;
+        }
+        c->x[i] = tensor(x[i], kHeadNames[i]);
+        const at::Tensor& t = c->x[i];
+        if (!t.is_cuda()) refuse(std::string(what) + " needs CUDA tensors");
+        if (t.dim() != 3 && t.dim() != 4) refuse(std::string(kHeadNames[i]) + " must be [tokens, heads, D] or [B, S, heads, D]");
+        if (i == 0) {
+            c->dtype = dtype_of(t);
+            c->D = t.size(-1);
+            c->S = t.size(t.dim() - 3);
+            c->B = t.dim() == 4 ? t.size(0) : 1;
+        } else {
+            same_kind(t, c->x[0], "k");
+            if (t.dim() != c->x[0].dim() || t.size(-1) != c->D || t.size(t.dim() - 3) != c->S || (t.dim() == 4 && t.size(0) != c->B))
+                refuse("k must have q's tokens and head width");
+        }
+        c->w[i] = param(w[i], t, c->D, i == 0 ? "wq" : "wk");
+        c->side[i].heads = t.size(t.dim() - 2);
+        c->side[i].w = ptr(c->w[i]);
+        if (!heads_of(t, &c->side[i].x)) {
+            c->x[i] = t.contiguous();
+            heads_of(c->x[i], &c->side[i].x);
+        }
+    }
+    const at::Tensor& q = c->x[0];
+    c->cos = tensor(cos, "cos");
+    c->sin = tensor(sin, "sin");
+    for (const at::Tensor* t : {&c->cos, &c->sin}) {
+        if (t->scalar_type() != at::kFloat || t->dim() != 2 || t->device() != q.device() || t->sizes() != c->cos.sizes())
+            refuse("cos and sin must be fp32 tables [positions, R / 2] of one shape on " + q.device().str());
+        if (2 * t->size(1) > c->D) refuse("cos and sin have " + std::to_string(t->size(1)) + " angles, a head of " + std::to_string(c->D) + " values has room for " + std::to_string(c->D / 2));
+    }
+    const auto rows = [](const at::Tensor& t) {  // the pitch of a table's rows; -1: not rows
+        if (t.size(1) > 1 && t.stride(1) != 1) return int64_t(-1);
+        if (t.size(0) <= 1) return std::max<int64_t>(t.size(1), 1);
+        return t.stride(0) >= t.size(1) ? t.stride(0) : int64_t(-1);
+    };
+    if (rows(c->cos) < 0 || rows(c->cos) != rows(c->sin)) {
+        c->cos = c->cos.contiguous();
+        c->sin = c->sin.contiguous();
+    }
+    c->angles.cos = static_cast<const float*>(ptr(c->cos));
+    c->angles.sin = static_cast<const float*>(ptr(c->sin));
+    c->angles.table_pitch = rows(c->cos);
+    c->angles.P = c->cos.size(0);
+    c->angles.R = static_cast<int32_t>(2 * c->cos.size(1));
+    c->angles.interleaved = interleaved == Py_True;
+    if (c->angles.R > 0 && c->angles.P == 0 && q.numel() > 0) refuse("cos and sin have no positions");
+    if (positions != Py_None) {
+        c->positions = tensor(positions, "positions");
+        const at::ScalarType st = c->positions.scalar_type();
+        if ((st != at::kLong && st != at::kInt) || c->positions.device() != q.device() || c->positions.numel() != c->B * c->S)
+            refuse("positions must be int64 or int32 with one value per token (" + std::to_string(c->B * c->S) + ") on " + q.device().str());
+        if (!c->positions.is_contiguous()) c->positions = c->positions.contiguous();
+        c->angles.positions = ptr(c->positions);
+        c->angles.position_bytes = st == at::kLong ? 8 : 4;
+    }
+}
+
+void read_head_outputs(HeadCall* c, PyObject* const* out, const char* const* names) {
+    for (int i = 0; i < 2; ++i) {
+        const at::Tensor& x = c->x[i];
+        if (!x.defined()) {
+            if (out[i] != Py_None) refuse(std::string(names[i]) + " is given without k");
+            continue;
+        }
+        if (out[i] == Py_None) {
+            c->out[i] = fresh(x.sizes(), x.scalar_type(), x);
+        } else {
+            c->out[i] = tensor(out[i], names[i]);
+            if (c->out[i].sizes() != x.sizes() || c->out[i].scalar_type() != x.scalar_type() || c->out[i].device() != x.device())
+                refuse(std::string(names[i]) + " must have " + kHeadNames[i] + "'s shape, dtype and device");
+        }
+        bool ok = heads_of(c->out[i], &c->side[i].y);
+        for (int64_t d = 0; d < x.dim(); ++d) ok = ok && (x.size(d) <= 1 || c->out[i].stride(d) != 0 || x.numel() == 0);
+        if (!ok) refuse(std::string(names[i]) + " must have heads of unit stride that do not share memory");
+    }
+}
+
+PyObject* given_or(PyObject* given, const at::Tensor& t) {
+    return !t.defined() ? Py_NewRef(Py_None) : given == Py_None ? THPVariable_Wrap(t) : Py_NewRef(given);
+}
+
+PyObject* rope_fwd_py(PyObject* const* a) {
+    // q k wq wk cos sin positions eps interleaved q_out k_out plan
+    HeadCall c;
+    read_heads(&c, a, a + 2, a[4], a[5], a[6], a[8], "rms_fwd_rope");
+    const float eps = static_cast<float>(real(a[7]));
+    const c10::cuda::CUDAGuard guard(c.x[0].device());
+    static const char* const names[2] = {"q_out", "k_out"};
+    read_head_outputs(&c, a + 9, names);
+    const norm_rope_plan* plan = a[11] == Py_None ? nullptr : static_cast<const norm_rope_plan*>(PyLong_AsVoidPtr(a[11]));
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(c.x[0].get_device()).stream();
+    norm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = rms_fwd_rope_planned(&c.side[0], &c.side[1], &c.angles, c.B, c.S, c.D, eps, c.dtype, stream, plan);
+    Py_END_ALLOW_THREADS
+    if (st != NORM_OK) return PyLong_FromLong(st);
+    PyObject* out = PyTuple_New(2);
+    if (!out) throw PythonError{};
+    for (int i = 0; i < 2; ++i) PyTuple_SET_ITEM(out, i, given_or(a[9 + i], c.out[i]));
+    return out;
+}
+
+PyObject* rope_bwd_py(PyObject* const* a) {
+    // dq dk q k wq wk cos sin positions eps interleaved dq_out dk_out dwq dwk workspace plan
+    HeadCall c;
+    read_heads(&c, a + 2, a + 4, a[6], a[7], a[8], a[10], "rms_bwd_rope");
+    const float eps = static_cast<float>(real(a[9]));
+    const at::Tensor& q = c.x[0];
+    const c10::cuda::CUDAGuard guard(q.device());
+    for (int i = 0; i < 2; ++i) {
+        if (!c.x[i].defined()) {
+            if (a[i] != Py_None || a[14] != Py_None) refuse("dk or dwk is given without k");
+            continue;
+        }
+        const std::string name = i == 0 ? "dq" : "dk";
+        c.dy[i] = tensor(a[i], name.c_str());
+        same_kind(c.dy[i], q, name);
+        if (c.dy[i].sizes() != c.x[i].sizes()) refuse(name + " must have " + kHeadNames[i] + "'s shape");
+        if (!heads_of(c.dy[i], &c.side[i].dy)) {
+            c.dy[i] = c.dy[i].contiguous();
+            heads_of(c.dy[i], &c.side[i].dy);
+        }
+        c.dw[i] = f32(a[13 + i], {c.D}, q, i == 0 ? "dwq" : "dwk");
+        if (c.side[i].heads == 0) c.dw[i].zero_();
+        c.side[i].dw = static_cast<float*>(ptr(c.dw[i]));
+    }
+    static const char* const names[2] = {"dq_out", "dk_out"};
+    read_head_outputs(&c, a + 11, names);
+    const norm_rope_plan* plan = a[16] == Py_None ? nullptr : static_cast<const norm_rope_plan*>(PyLong_AsVoidPtr(a[16]));
+    size_t bytes = 0;
+    if (a[15] == Py_None)
+        rope_workspace_bytes(c.B * c.S, c.side[0].heads, c.side[1].heads, c.D, sm_count(q.get_device()), plan, &bytes);
+    const at::Tensor ws = scratch(a[15], bytes, q);
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(q.get_device()).stream();
+    norm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = rms_bwd_rope_planned(&c.side[0], &c.side[1], &c.angles, ptr(ws), bytes_of(ws), c.B, c.S, c.D, eps, c.dtype, stream, plan);
+    Py_END_ALLOW_THREADS
+    if (st != NORM_OK) return PyLong_FromLong(st);
+    PyObject* out = PyTuple_New(4);
+    if (!out) throw PythonError{};
+    for (int i = 0; i < 2; ++i) {
+        PyTuple_SET_ITEM(out, i, given_or(a[11 + i], c.out[i]));
+        PyTuple_SET_ITEM(out, 2 + i, given_or(a[13 + i], c.dw[i]));
+    }
+    return out;
+}
+
 // No C++ exception leaves a call: each becomes the Python error it stands for.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -375,6 +559,8 @@ PyMethodDef methods[] = {
     {"gn_fwd", fast(entry<gn_fwd_py, 12>), METH_FASTCALL, nullptr},
     {"gn_bwd", fast(entry<gn_bwd_py, 13>), METH_FASTCALL, nullptr},
     {"grad", fast(entry<grad_py, 5>), METH_FASTCALL, nullptr},
+    {"rms_fwd_rope", fast(entry<rope_fwd_py, 12>), METH_FASTCALL, nullptr},
+    {"rms_bwd_rope", fast(entry<rope_bwd_py, 17>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
