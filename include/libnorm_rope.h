@@ -47,7 +47,7 @@ typedef struct {
  * (>= R / 2), and the token's positions. */
 typedef struct {
     const float *cos, *sin;
-    int64_t table_pitch, P;
+    int64_t table_pitch, P; /* P >= 1 where R > 0 */
     const void* positions; /* [B * S] whole numbers of position_bytes each; NULL: token s of a sequence has position s */
     int32_t position_bytes; /* 8 or 4 (signed); ignored without positions */
     int32_t R;              /* values that rotate: even, 0 <= R <= D */
@@ -55,15 +55,15 @@ typedef struct {
     int32_t reserved;       /* 0 */
 } norm_rope_angles;
 
-/* A launch plan. A warp works on `slots` times (32 / lanes) heads of a token. */
+/* A launch plan. A warp works on `heads` heads of each of 32 / lanes tokens. */
 typedef struct {
-    int32_t vec_elems; /* values per access: 16 / sizeof(element), 2 (16-bit types) or 1 */
+    int32_t vec_elems; /* values per access: 16 / sizeof(element), 4 or 2 (16-bit types) or 1 */
     int32_t pairs;     /* pairs of accesses per lane */
     int32_t lanes;     /* lanes per head, a power of two, <= 32 */
-    int32_t slots;     /* head groups per warp and token */
+    int32_t heads;     /* heads per warp and token, >= 1 */
     int32_t warps;     /* warps per CTA, 1..8 */
-    int32_t reserved;  /* 0 */
-    int64_t ctas;      /* backward: CTAs of queries and keys together at most (persistent); forward: 0 */
+    int32_t few;       /* forward: 1: a warp has one task, without shared memory; 0: persistent, heads streamed */
+    int64_t ctas;      /* persistent: CTAs of queries and keys together at most (fewer if fewer fit), >= 2 */
 } norm_rope_plan;
 
 /*
@@ -75,9 +75,9 @@ typedef struct {
  * heads < 2^20, pitches below 2^40 in magnitude, B * S * heads * D < 2^62,
  * eps finite and >= 0. Every pointer needs its element's alignment. 16-byte
  * accesses are used when every tensor, weight and pitch is a multiple of 16
- * bytes, as are D and, not interleaved, R / 2, or, interleaved, R; 4-byte
- * accesses of 16-bit pairs when the same holds for 4 bytes; element accesses
- * otherwise.
+ * bytes, as are D and, not interleaved, R / 2, or, interleaved, R; 8- or 4-byte
+ * accesses of 16-bit values when the same holds for 8 or 4 bytes; element
+ * accesses otherwise.
  */
 norm_status rms_fwd_rope(const norm_rope_side* q, const norm_rope_side* k, const norm_rope_angles* angles, int64_t B,
                          int64_t S, int64_t D, float eps, norm_dtype dtype, cudaStream_t stream);

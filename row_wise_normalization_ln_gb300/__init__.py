@@ -73,7 +73,7 @@ class GnPlan(ctypes.Structure):
 
 class RopePlan(ctypes.Structure):
     """Mirror of ``norm_rope_plan`` in include/libnorm_rope.h."""
-    _fields_ = [(k, ctypes.c_int32) for k in ("vec_elems", "pairs", "lanes", "slots", "warps", "reserved")] + \
+    _fields_ = [(k, ctypes.c_int32) for k in ("vec_elems", "pairs", "lanes", "heads", "warps", "few")] + \
         [("ctas", ctypes.c_int64)]
 
     def as_dict(self) -> dict:
@@ -791,7 +791,7 @@ def make_rope_plan(tokens: int, q_heads: int, k_heads: int, D: int, R: int, dtyp
     that D and R allow)."""
     code = _dtype_code(dtype)
     if vec_elems is None:
-        vec_elems = next(v for v in ((4, 1) if code == NORM_F32 else (8, 2, 1))
+        vec_elems = next(v for v in ((4, 1) if code == NORM_F32 else (8, 4, 2, 1))
                          if v == 1 or D % v == 0 and (R if interleaved else R // 2) % v == 0)
     p = RopePlan()
     st = library().rope_make_plan(tokens, q_heads, k_heads, D, R, int(interleaved), code, int(backward), vec_elems,

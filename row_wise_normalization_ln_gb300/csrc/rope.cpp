@@ -22,7 +22,8 @@ using libnorm::kRopeMaxWarps;
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxHeads = int64_t(1) << 20;
 constexpr int64_t kMaxPitch = int64_t(1) << 40;
-constexpr int kBwdCtasPerSm = 4;
+constexpr int kCtasPerSm = 8;  // at most; a launch takes as many as fit
+constexpr int kFewHeads = 64;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int elem_size(norm_dtype d) { return d == NORM_F32 ? 4 : 2; }
@@ -81,15 +82,13 @@ void count_pairs(const Shape& s, int vec, int64_t* all, int64_t* rot) {
     *all = *rot + ceil_div((s.D - s.R) / vec, 2);
 }
 
-int64_t slots_of(int64_t heads, int lanes) { return ceil_div(heads, 32 / lanes); }
-
-bool vec_known(int vec, norm_dtype dtype) { return vec == 1 || vec == 16 / elem_size(dtype) || (vec == 2 && dtype != NORM_F32); }
+bool vec_known(int vec, norm_dtype dtype) { return vec == 1 || vec == 16 / elem_size(dtype) || ((vec == 2 || vec == 4) && dtype != NORM_F32); }
 
 // The instances there are: (access width, pairs per lane).
 bool pairs_known(int vec, int pairs, norm_dtype dtype) {
     if (vec == 1) return pairs == 4 || pairs == 8;
     if (vec == 2) return pairs == 2 || pairs == 4;
-    return pairs == 1 || (pairs == 2 && dtype == NORM_F32);
+    return pairs == 1 || (pairs == 2 && vec == 4);
 }
 
 norm_status make_plan(const Shape& s, int vec, int num_sms, norm_rope_plan* p) {
@@ -106,13 +105,13 @@ norm_status make_plan(const Shape& s, int vec, int num_sms, norm_rope_plan* p) {
         break;
     }
     if (p->pairs == 0) return NORM_ERR_ARG;
-    const int64_t slots[2] = {slots_of(s.heads[0], p->lanes), slots_of(s.heads[1], p->lanes)};
-    const int64_t most = std::max<int64_t>(1, std::max(slots[0], slots[1]));
+    const int64_t blocks = ceil_div(s.T, 32 / p->lanes), most = std::max<int64_t>(1, std::max(s.heads[0], s.heads[1]));
+    const int64_t total = blocks * (s.heads[0] + s.heads[1]);  // warps' heads
     p->warps = 4;
-    const int64_t total = s.T * (slots[0] + slots[1]);
-    const int64_t want = std::min(most, std::max<int64_t>(1, std::min<int64_t>(8, total / (int64_t(num_sms) * 16))));
-    p->slots = static_cast<int32_t>(ceil_div(most, ceil_div(most, want)));
-    if (s.bwd) p->ctas = std::max<int64_t>(2, std::min<int64_t>(int64_t(num_sms) * kBwdCtasPerSm, ceil_div(total, p->slots * p->warps)));
+    p->few = !s.bwd && total <= int64_t(num_sms) * kFewHeads;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(p->few ? 2 : 8, total / (int64_t(num_sms) * (p->few ? 4 : 16))));
+    p->heads = static_cast<int32_t>(ceil_div(most, ceil_div(most, want)));
+    p->ctas = std::max<int64_t>(2, std::min<int64_t>(int64_t(num_sms) * kCtasPerSm, ceil_div(total, p->heads * p->warps)));
     return NORM_OK;
 }
 
@@ -120,13 +119,14 @@ norm_status make_plan(const Shape& s, int vec, int num_sms, norm_rope_plan* p) {
 // does not fit the call.
 norm_status derive(const norm_rope_plan& p, const Shape& s, int vec, RopeArgs* a) {
     if (!vec_known(p.vec_elems, s.dtype) || !pairs_known(p.vec_elems, p.pairs, s.dtype)) return NORM_ERR_PLAN;
-    if (p.vec_elems > vec || !width_ok(s, p.vec_elems) || p.reserved != 0) return NORM_ERR_PLAN;
+    if (p.vec_elems > vec || !width_ok(s, p.vec_elems) || (p.few != 0 && (p.few != 1 || s.bwd))) return NORM_ERR_PLAN;
     if (p.lanes < 1 || p.lanes > 32 || (p.lanes & (p.lanes - 1)) != 0) return NORM_ERR_PLAN;
-    if (p.slots < 1 || p.warps < 1 || p.warps > kRopeMaxWarps) return NORM_ERR_PLAN;
+    if (p.heads < 1 || p.warps < 1 || p.warps > kRopeMaxWarps) return NORM_ERR_PLAN;
     int64_t all, rot;
     count_pairs(s, p.vec_elems, &all, &rot);
     if (all > int64_t(p.pairs) * p.lanes) return NORM_ERR_PLAN;
-    if (s.bwd ? (p.ctas < 2 || p.ctas > (1 << 20)) : p.ctas != 0) return NORM_ERR_PLAN;
+    if (p.ctas < 2 || p.ctas > (1 << 20)) return NORM_ERR_PLAN;
+    if (!p.few && libnorm::rope_smem_bytes(p.vec_elems, elem_size(s.dtype), p.pairs, p.warps, s.bwd) > libnorm::kRopeMaxSmem) return NORM_ERR_PLAN;
     a->lanes_log = 0;
     while ((1 << a->lanes_log) < p.lanes) ++a->lanes_log;
     a->npairs = static_cast<int32_t>(all);
@@ -134,33 +134,28 @@ norm_status derive(const norm_rope_plan& p, const Shape& s, int vec, RopeArgs* a
     a->D = static_cast<int32_t>(s.D);
     a->R = static_cast<int32_t>(s.R);
     a->invD = 1.f / static_cast<float>(s.D);
-    int64_t chunk = p.slots, slots[2];
-    for (int i = 0; i < 2; ++i) slots[i] = slots_of(s.heads[i], p.lanes);
+    a->T = static_cast<int32_t>(s.T);
+    const int64_t blocks = ceil_div(s.T, 32 / p.lanes);
+    int64_t chunk = p.heads;
     // tasks are counted in 31 bits: fewer, larger ones where they would not fit
-    while (ceil_div(std::max(slots[0], slots[1]), chunk) * s.T > kMaxTokens) chunk *= 2;
-    a->chunk_slots = static_cast<int32_t>(std::min<int64_t>(chunk, int64_t(1) << 30));
+    while (ceil_div(std::max(s.heads[0], s.heads[1]), chunk) * blocks > kMaxTokens) chunk *= 2;
+    a->chunk_heads = static_cast<int32_t>(chunk);
     for (int i = 0; i < 2; ++i) {
         RopeSide& d = a->side[i];
         d.heads = static_cast<int32_t>(s.heads[i]);
-        d.slots = static_cast<int32_t>(slots[i]);
-        d.chunks = static_cast<int32_t>(std::max<int64_t>(1, ceil_div(slots[i], chunk)));
+        d.chunks = static_cast<int32_t>(std::max<int64_t>(1, ceil_div(s.heads[i], chunk)));
         d.by_chunks = libnorm::fast_div(d.chunks);
-        d.tasks = d.heads > 0 ? static_cast<int32_t>(s.T * d.chunks) : 0;
+        d.tasks = d.heads > 0 ? static_cast<int32_t>(blocks * d.chunks) : 0;
         d.ctas = static_cast<int32_t>(ceil_div(d.tasks, p.warps));
-    }
-    if (s.bwd && s.T > 0) {
-        // the persistent CTAs are shared out by the heads' groups
-        const int64_t n = std::min<int64_t>(p.ctas, int64_t(a->side[0].ctas) + a->side[1].ctas);
-        int64_t first = slots[0] + slots[1] > 0 ? (n * slots[0] + (slots[0] + slots[1]) / 2) / (slots[0] + slots[1]) : 0;
-        if (slots[0] > 0 && slots[1] > 0) first = std::max<int64_t>(1, std::min(first, n - 1));
-        a->side[0].ctas = static_cast<int32_t>(std::min<int64_t>(a->side[0].ctas, first));
-        a->side[1].ctas = static_cast<int32_t>(std::min<int64_t>(a->side[1].ctas, n - first));
     }
     return int64_t(a->side[0].ctas) + a->side[1].ctas <= kMaxTokens ? NORM_OK : NORM_ERR_PLAN;
 }
 
-int64_t workspace_bytes(const RopeArgs& a) {
-    return (int64_t(a.side[0].ctas) + a.side[1].ctas) * a.D * 4;
+// A partial row of D values per CTA, of which there are at most the plan's and
+// one per head.
+int64_t workspace_bytes(int64_t ctas, int64_t tokens, int64_t heads, int64_t D) {
+    const __int128 all = static_cast<__int128>(tokens) * heads;
+    return (all < ctas ? static_cast<int64_t>(all) : ctas) * D * 4;
 }
 
 norm_status done(cudaError_t e) {
@@ -203,12 +198,12 @@ norm_status settle(const norm_rope_side* const (&in)[2], const norm_rope_angles*
     const bool work = s->T > 0 && (s->heads[0] > 0 || s->heads[1] > 0);
     int vec = 16 / es;
     const auto narrow = [&](auto ok) {
-        while (vec > 1 && !ok(vec)) vec = vec == 16 / es && es == 2 ? 2 : 1;
+        while (vec > 1 && !ok(vec)) vec = es == 4 || vec == 2 ? 1 : vec / 2;
     };
     if (work) {
         if (s->R > 0) {
             if (!angles->cos || !angles->sin || !on(angles->cos, 4) || !on(angles->sin, 4)) return NORM_ERR_ARG;
-            if (angles->table_pitch < s->R / 2 || angles->table_pitch >= kMaxPitch) return NORM_ERR_ARG;
+            if (angles->P < 1 || angles->table_pitch < s->R / 2 || angles->table_pitch >= kMaxPitch) return NORM_ERR_ARG;
         }
         if (angles->positions) {
             if (angles->position_bytes != 4 && angles->position_bytes != 8) return NORM_ERR_ARG;
@@ -240,7 +235,7 @@ norm_status settle(const norm_rope_side* const (&in)[2], const norm_rope_angles*
         a->P = angles->P;
         a->positions = angles->positions;
         a->pos_bytes = angles->positions ? angles->position_bytes : 0;
-        a->vec_table = on(angles->cos, 16) && on(angles->sin, 16) && angles->table_pitch % 4 == 0;
+        a->vec_table = on(angles->cos, 16) && on(angles->sin, 16) && angles->table_pitch % 4 == 0 && s->R % 8 == 0;
         a->S = static_cast<int32_t>(s->S);
         a->by_S = libnorm::fast_div(s->S);
         a->eps = eps;
@@ -263,7 +258,7 @@ norm_status settle(const norm_rope_side* const (&in)[2], const norm_rope_angles*
     return derive(*p, *s, vec, a);
 }
 
-cudaError_t launch(const norm_rope_plan& p, const RopeArgs& a, const Shape& s, cudaStream_t stream) {
+cudaError_t launch(const norm_rope_plan& p, RopeArgs& a, const Shape& s, cudaStream_t stream) {
     switch (s.dtype) {
         case NORM_F32: return libnorm::launch_rope_f32(p, a, s.interleaved, s.bwd, stream);
         case NORM_BF16: return libnorm::launch_rope_bf16(p, a, s.interleaved, s.bwd, stream);
@@ -302,10 +297,9 @@ norm_status rms_bwd_rope_planned(const norm_rope_side* q, const norm_rope_side* 
     const norm_status st = settle(in, angles, eps, &s, plan, &p, &a);
     if (st != NORM_OK || (s.heads[0] == 0 && s.heads[1] == 0)) return st;
     if (s.T > 0) {
-        const int64_t need = workspace_bytes(a);
+        const int64_t need = workspace_bytes(p.ctas, s.T, s.heads[0] + s.heads[1], D);
         if (need > 0 && (!workspace || !on(workspace, 16) || workspace_size < static_cast<size_t>(need))) return NORM_ERR_ARG;
         a.side[0].part = static_cast<float*>(workspace);
-        a.side[1].part = a.side[0].part + int64_t(a.side[0].ctas) * D;
         const cudaError_t e = launch(p, a, s, stream);
         if (e != cudaSuccess) return done(e);
     }
@@ -335,10 +329,7 @@ norm_status rope_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t k_head
     if (!bytes || (!plan && num_sms < 1) || (plan && plan->ctas < 0)) return NORM_ERR_ARG;
     *bytes = 0;
     if (tokens == 0) return NORM_OK;
-    // a partial row per CTA, and no more CTAs than heads
-    const int64_t ctas = plan ? plan->ctas : int64_t(num_sms) * kBwdCtasPerSm;
-    const __int128 heads = static_cast<__int128>(tokens) * (q_heads + k_heads);
-    *bytes = static_cast<size_t>(heads < ctas ? static_cast<int64_t>(heads) : ctas) * static_cast<size_t>(D) * 4;
+    *bytes = static_cast<size_t>(workspace_bytes(plan ? plan->ctas : int64_t(num_sms) * kCtasPerSm, tokens, q_heads + k_heads, D));
     return NORM_OK;
 }
 

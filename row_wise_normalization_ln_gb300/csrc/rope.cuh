@@ -11,11 +11,13 @@
 // (a, b) of VEC values whose elements are each other's partners in the
 // rotation (i and i + R / 2; interleaved vectors hold whole pairs, and any two
 // accesses do), so the rotation needs no exchange and a cosine is loaded once
-// per pair. A warp works on one token and walks its heads, 32 / lanes at a
-// time: the token's angles and the weight stay in registers, and a batch of
-// heads is in flight before the first is reduced. The sums of a head meet in
-// butterflies over its lanes; nothing meets across warps until the backward's
-// column sums.
+// per pair. Each lane group of a warp has a token of its own and walks its
+// heads: the token's angles and the weight stay in registers, and the next
+// heads are in flight while one is reduced. (With a warp's groups on
+// neighbouring heads of one token a task had a quarter of the heads for the
+// same preparation, and groups stood idle where the heads ran out.) The sums
+// of a head meet in butterflies over its lanes; nothing meets across warps
+// until the backward's column sums.
 #pragma once
 
 #include "gn_kernels.cuh"
@@ -23,10 +25,32 @@
 
 namespace libnorm {
 
+// GnVec, and accesses of four 16-bit values.
+template <class T, int VEC>
+struct RopeVec : GnVec<T, VEC> {};
+template <class T>
+struct RopeVec16x4 {
+    using Raw = uint2;
+    using P = typename Gn16<T>::Pair;
+    static constexpr int H = 2;
+    static __device__ __forceinline__ Raw zero() { return make_uint2(0, 0); }
+    static __device__ __forceinline__ Raw load(const T* p) { return *reinterpret_cast<const uint2*>(p); }
+    static __device__ __forceinline__ void store(T* p, const Raw& v) { *reinterpret_cast<uint2*>(p) = v; }
+    static __device__ __forceinline__ float2 get(const Raw& r, int i) { return P::widen(i == 0 ? r.x : r.y); }
+    static __device__ __forceinline__ void set(Raw& r, int i, float2 v) {
+        if (i == 0) r.x = P::pack(v.x, v.y);
+        else r.y = P::pack(v.x, v.y);
+    }
+};
+template <>
+struct RopeVec<__nv_bfloat16, 4> : RopeVec16x4<__nv_bfloat16> {};
+template <>
+struct RopeVec<__half, 4> : RopeVec16x4<__half> {};
+
 // VEC values of an access as fp32 pairs (one value: the second of the pair is 0).
 template <class T, int VEC>
 struct RopeVals {
-    using X = GnVec<T, VEC>;
+    using X = RopeVec<T, VEC>;
     static constexpr int H = X::H;
     float2 v[H];
     __device__ __forceinline__ void widen(const typename X::Raw& r) {
@@ -80,88 +104,109 @@ struct RopeLane {
     }
 };
 
-// A token's angles for a lane's pairs: cosines and sines of pairs of elements
-// (a, b); kInside: half of them a's, half b's.
-template <int VEC, int NP, bool ILV>
-struct RopeAngles {
-    static constexpr bool kInside = ILV && VEC > 1;
-    static constexpr int W = VEC == 1 ? 1 : VEC / 2;  // float2s per access and pair
-    float2 c[NP][W], s[NP][W];
+// How a token's rotation acts on a lane's values: access a becomes a * ca +
+// mate(a) * sa, access b becomes b * cb + mate(b) * sb, where the mate of a
+// value is its partner in the rotation. Values that do not rotate have c = 1
+// and s = 0 (with a mate of their own all the same: 0 * infinity is not 0,
+// which the kernels look after where it can happen). BACK: against the angle.
+template <class T, int VEC, int NP, bool ILV, bool BACK>
+struct RopeTurn {
+    using V = RopeVals<T, VEC>;
+    static constexpr int H = RopeVec<T, VEC>::H;
+    static constexpr bool kInside = ILV && VEC > 1;  // pairs lie within an access
+    float2 c[NP][kInside ? 2 * H : H], s[NP][2 * H];  // a's, then b's (not kInside: the same cosines)
 
-    // n floats of a table row (n <= 8, whole float4s where the rows are aligned and n >= 4)
-    template <int N>
-    static __device__ __forceinline__ void fetch(float* to, const float* p, bool vec) {
-        if constexpr (N % 4 == 0) {
-            if (vec) {
-#pragma unroll
-                for (int i = 0; i < N; i += 4) {
-                    const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
-                    to[i] = v.x;
-                    to[i + 1] = v.y;
-                    to[i + 2] = v.z;
-                    to[i + 3] = v.w;
-                }
-                return;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) to[i] = __ldg(p + i);
-    }
-    __device__ __forceinline__ void load(const RopeArgs& g, const RopeLane<VEC, NP, ILV>& l, int64_t pos) {
-        const float* cp = g.cos + pos * g.table_pitch;
-        const float* sp = g.sin + pos * g.table_pitch;
-        const bool vec = g.vec_table != 0;
+    // From a token's table rows; vec: they are on 16-byte boundaries.
+    __device__ __forceinline__ void set(const RopeLane<VEC, NP, ILV>& l, const float* cp, const float* sp, bool vec) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-            float tc[2 * W], ts[2 * W];
             if constexpr (kInside) {
-                if (l.ra[j]) {
-                    fetch<W>(tc, cp + l.ca[j], vec);
-                    fetch<W>(ts, sp + l.ca[j], vec);
-                }
-                if (l.rb[j]) {
-                    fetch<W>(tc + W, cp + l.cb[j], vec);
-                    fetch<W>(ts + W, sp + l.cb[j], vec);
-                }
-            } else if (l.ra[j]) {
-                fetch<VEC>(tc, cp + l.ca[j], vec);
-                fetch<VEC>(ts, sp + l.ca[j], vec);
-            }
-            if constexpr (VEC == 1) tc[1] = ts[1] = 0.f;
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                c[j][i] = make_float2(tc[2 * i], tc[2 * i + 1]);
-                s[j][i] = make_float2(ts[2 * i], ts[2 * i + 1]);
+                for (int h = 0; h < 2; ++h) {
+                    const bool on = h == 0 ? l.ra[j] : l.rb[j];
+                    const int at = h == 0 ? l.ca[j] : l.cb[j];
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const float co = on ? cp[at + i] : 1.f, si = on ? sp[at + i] : 0.f;
+                        c[j][h * H + i] = f2_splat(co);
+                        s[j][h * H + i] = BACK ? make_float2(si, -si) : make_float2(-si, si);
+                    }
+                }
+            } else {
+                float tc[VEC], ts[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) tc[i] = 1.f, ts[i] = 0.f;
+                if (l.ra[j]) {
+                    if (VEC % 4 == 0 && vec) {
+#pragma unroll
+                        for (int i = 0; i < VEC / 4 * 4; i += 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(cp + l.ca[j] + i);
+                            const float4 y = *reinterpret_cast<const float4*>(sp + l.ca[j] + i);
+                            tc[i] = x.x, tc[i + 1] = x.y, tc[i + 2] = x.z, tc[i + 3] = x.w;
+                            ts[i] = y.x, ts[i + 1] = y.y, ts[i + 2] = y.z, ts[i + 3] = y.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) tc[i] = cp[l.ca[j] + i], ts[i] = sp[l.ca[j] + i];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const float2 si = VEC == 1 ? make_float2(ts[0], 0.f) : make_float2(ts[2 * i], ts[2 * i + (VEC > 1)]);
+                    const float2 ni = make_float2(-si.x, -si.y);
+                    c[j][i] = VEC == 1 ? make_float2(tc[0], 0.f) : make_float2(tc[2 * i], tc[2 * i + (VEC > 1)]);
+                    s[j][i] = BACK ? si : ni;
+                    s[j][H + i] = BACK ? ni : si;
+                }
             }
         }
     }
-    // The pair j of accesses turned by the angle, or (BACK) against it.
-    template <bool BACK, class V>
-    __device__ __forceinline__ void turn(const RopeLane<VEC, NP, ILV>& l, int j, V& a, V& b) const {
+    // The weight taken in: a * ca + mate(a) * sa is then the rotation of a * w.
+    __device__ __forceinline__ float2 cos_of(int j, int i, bool b) const { return c[j][kInside && b ? H + i : i]; }
+    __device__ __forceinline__ float2 sin_of(int j, int i, bool b) const { return s[j][b ? H + i : i]; }
+    static __device__ __forceinline__ float2 mate(const V& a, const V& b, int i, bool of_b) {
         if constexpr (kInside) {
-            // (angles k of an access: element pair k)
-            const auto at = [](const float2* t, int k) { return (k & 1) ? t[k >> 1].y : t[k >> 1].x; };
+            const float2 v = of_b ? b.v[i] : a.v[i];
+            return make_float2(v.y, v.x);
+        }
+        return of_b ? a.v[i] : b.v[i];
+    }
+};
+
+// The rotation with the weight taken in, formed once per token: a head then
+// takes two instructions per pair of values.
+template <class T, int VEC, int NP, bool ILV>
+struct RopeWeightedTurn {
+    using R = RopeTurn<T, VEC, NP, ILV, false>;
+    using V = RopeVals<T, VEC>;
+    static constexpr int H = R::H;
+    float2 ca[NP][H], sa[NP][H], cb[NP][H], sb[NP][H];
+    __device__ __forceinline__ void set(const RopeLane<VEC, NP, ILV>& l, const V (&wa)[NP], const V (&wb)[NP], const float* cp,
+                                        const float* sp, bool vec) {
+        R t;
+        t.set(l, cp, sp, vec);
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-                if (l.ra[j]) {
-                    const float co = at(c[j], k), si = BACK ? -at(s[j], k) : at(s[j], k);
-                    const float2 v = a.v[k];
-                    a.v[k] = make_float2(fmaf(v.x, co, -(v.y * si)), fmaf(v.y, co, v.x * si));
-                }
-                if (l.rb[j]) {
-                    const float co = at(c[j], W + k), si = BACK ? -at(s[j], W + k) : at(s[j], W + k);
-                    const float2 v = b.v[k];
-                    b.v[k] = make_float2(fmaf(v.x, co, -(v.y * si)), fmaf(v.y, co, v.x * si));
-                }
-            }
-        } else if (l.ra[j]) {
+        for (int j = 0; j < NP; ++j)
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float2 si = BACK ? make_float2(-s[j][i].x, -s[j][i].y) : s[j][i];
-                const float2 va = a.v[i], vb = b.v[i];
-                a.v[i] = __ffma2_rn(va, c[j][i], __fmul2_rn(make_float2(-vb.x, -vb.y), si));
-                b.v[i] = __ffma2_rn(vb, c[j][i], __fmul2_rn(va, si));
+            for (int i = 0; i < H; ++i) {
+                ca[j][i] = __fmul2_rn(wa[j].v[i], t.cos_of(j, i, false));
+                cb[j][i] = __fmul2_rn(wb[j].v[i], t.cos_of(j, i, true));
+                sa[j][i] = __fmul2_rn(R::mate(wa[j], wb[j], i, false), t.sin_of(j, i, false));
+                sb[j][i] = __fmul2_rn(R::mate(wa[j], wb[j], i, true), t.sin_of(j, i, true));
             }
+    }
+    // SAFE: nothing of a mate reaches a value that does not rotate.
+    template <bool SAFE>
+    __device__ __forceinline__ void apply(const RopeLane<VEC, NP, ILV>& l, int j, const V& a, const V& b, float2 r2, V& oa,
+                                          V& ob) const {
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float2 va = __fmul2_rn(a.v[i], ca[j][i]), vb = __fmul2_rn(b.v[i], cb[j][i]);
+            float2 ta = __ffma2_rn(R::mate(a, b, i, false), sa[j][i], va), tb = __ffma2_rn(R::mate(a, b, i, true), sb[j][i], vb);
+            if (SAFE && !l.ra[j]) ta = va;
+            if (SAFE && !l.rb[j]) tb = vb;
+            oa.v[i] = __fmul2_rn(ta, r2);
+            ob.v[i] = __fmul2_rn(tb, r2);
         }
     }
 };
@@ -172,14 +217,18 @@ __device__ __forceinline__ int64_t rope_position(const RopeArgs& g, int t, int s
     return s;
 }
 
-// Where a warp's task lies: the token's offset in each tensor, the first head
-// group and the one after the last.
+// Where a lane group's task lies: its token (on: there is one), the first
+// head and how many.
 struct RopeTask {
-    int t, b, s, slot, end;
+    int t, b, s, head, n;
+    bool on;
     __device__ __forceinline__ RopeTask(const RopeArgs& g, const RopeSide& sd, int task) {
-        t = quot(task, sd.by_chunks);
-        slot = (task - t * sd.chunks) * g.chunk_slots;
-        end = min(sd.slots, slot + g.chunk_slots);
+        const int block = quot(task, sd.by_chunks);
+        head = (task - block * sd.chunks) * g.chunk_heads;
+        n = min(sd.heads - head, g.chunk_heads);
+        const int64_t at = (static_cast<int64_t>(block) << (5 - g.lanes_log)) + ((threadIdx.x & 31) >> g.lanes_log);
+        on = at < g.T;
+        t = on ? static_cast<int>(at) : 0;
         b = quot(t, g.by_S);
         s = t - b * g.S;
     }
@@ -187,7 +236,7 @@ struct RopeTask {
 
 template <class T>
 __device__ __forceinline__ T* rope_at(const norm_heads& h, const RopeTask& k) {
-    return static_cast<T*>(h.data) + k.b * h.batch + k.s * h.token;
+    return static_cast<T*>(h.data) + k.b * h.batch + k.s * h.token + k.head * h.head;
 }
 
 // The weight of a lane's accesses, widened.
@@ -195,7 +244,7 @@ template <class T, int VEC, int NP, bool ILV>
 struct RopeWeight {
     RopeVals<T, VEC> a[NP], b[NP];
     __device__ __forceinline__ RopeWeight(const RopeLane<VEC, NP, ILV>& l, const T* w) {
-        using X = GnVec<T, VEC>;
+        using X = RopeVec<T, VEC>;
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
             a[j].widen(l.a[j] >= 0 ? X::load(w + l.a[j]) : X::zero());
@@ -204,84 +253,292 @@ struct RopeWeight {
     }
 };
 
-// ------------------------------------------------------------ forward
-// U heads per lane group are loaded before the first is reduced.
-template <class T, int VEC, int NP, bool ILV, int U>
-__global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_fwd(const __grid_constant__ RopeArgs g) {
-    using X = GnVec<T, VEC>;
-    using V = RopeVals<T, VEC>;
-    grid_release();
-    const bool second = static_cast<int>(blockIdx.x) >= g.side[0].ctas;
-    const RopeSide& sd = g.side[second];
-    const int cta = static_cast<int>(blockIdx.x) - (second ? g.side[0].ctas : 0);
-    const int64_t task = int64_t(cta) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const int lanes = 1 << g.lanes_log, groups = 32 >> g.lanes_log;
-    const int group = lane >> g.lanes_log;
-    const RopeLane<VEC, NP, ILV> l(g, lane & (lanes - 1));
-    grid_wait();
-    if (task >= sd.tasks) return;  // (a whole warp)
-    const RopeTask k(g, sd, static_cast<int>(task));
-    const int64_t pos = rope_position(g, k.t, k.s);
-    const T* x = rope_at<const T>(sd.x, k);
-    T* y = rope_at<T>(sd.y, k);
-
-    typename X::Raw xa[U][NP], xb[U][NP];
-    const auto load = [&](int slot) {
+// Sums of N values over aligned groups of `lanes` lanes, side by side.
+template <int N>
+__device__ __forceinline__ void rope_sum(float (&v)[N], int lanes) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = (slot + u) * groups + group;
-            const bool on = slot + u < k.end && h < sd.heads;
-            const T* p = x + h * sd.x.head;
+    for (int off = 1; off < 32; off <<= 1) {
+        if (off >= lanes) return;
 #pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                xa[u][j] = on && l.a[j] >= 0 ? X::load(p + l.a[j]) : X::zero();
-                xb[u][j] = on && l.b[j] >= 0 ? X::load(p + l.b[j]) : X::zero();
-            }
-        }
-    };
-    load(k.slot);  // before the position is known: its latency and the table's pass meanwhile
-    const RopeWeight<T, VEC, NP, ILV> w(l, static_cast<const T*>(sd.w));
-    RopeAngles<VEC, NP, ILV> ang;
-    const bool pad = pos < 0, none = pos >= g.P;
-    if (!pad && !none) ang.load(g, l, pos);
-    for (int slot = k.slot; slot < k.end;) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = (slot + u) * groups + group;
-            const bool on = slot + u < k.end && h < sd.heads;
-            V va[NP], vb[NP];
-            float2 ss = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                va[j].widen(xa[u][j]);
-                vb[j].widen(xb[u][j]);
-#pragma unroll
-                for (int i = 0; i < X::H; ++i) {
-                    ss = __ffma2_rn(va[j].v[i], va[j].v[i], ss);
-                    ss = __ffma2_rn(vb[j].v[i], vb[j].v[i], ss);
-                }
-            }
-            const float sum = group_sum(ss.x + ss.y, lanes);
-            float r = rsqrtf(fmaf(sum, g.invD, g.eps));
-            if (none) r = __int_as_float(0x7fffffff);  // no angle: NaN
-            const float2 r2 = f2_splat(r);
-            T* p = y + h * sd.y.head;
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-#pragma unroll
-                for (int i = 0; i < X::H; ++i) {
-                    va[j].v[i] = __fmul2_rn(__fmul2_rn(va[j].v[i], r2), w.a[j].v[i]);
-                    vb[j].v[i] = __fmul2_rn(__fmul2_rn(vb[j].v[i], r2), w.b[j].v[i]);
-                }
-                ang.template turn<false>(l, j, va[j], vb[j]);
-                if (on && l.a[j] >= 0) X::store(p + l.a[j], pad ? X::zero() : va[j].round());
-                if (on && l.b[j] >= 0) X::store(p + l.b[j], pad ? X::zero() : vb[j].round());
-            }
-        }
-        slot += U;
-        if (slot < k.end) load(slot);
+        for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(kFullMask, v[n], off);
     }
+}
+
+// A CTA's side and a warp's first task and step.
+struct RopeShare {
+    bool second;
+    int cta, first, step;
+    __device__ __forceinline__ explicit RopeShare(const RopeArgs& g) {
+        second = static_cast<int>(blockIdx.x) >= g.side[0].ctas;
+        cta = static_cast<int>(blockIdx.x) - (second ? g.side[0].ctas : 0);
+        const int warps = blockDim.x >> 5;
+        first = cta * warps + static_cast<int>(threadIdx.x >> 5);
+        step = g.side[second].ctas * warps;
+    }
+};
+
+// Whether some access of the warp does not rotate: a mate's infinity must then
+// be kept out of it.
+template <int VEC, int NP, bool ILV>
+__device__ __forceinline__ bool rope_mixed(const RopeLane<VEC, NP, ILV>& l) {
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) any = any || (l.a[j] >= 0 && !l.ra[j]) || (l.b[j] >= 0 && !l.rb[j]);
+    return __any_sync(kFullMask, any);
+}
+
+// What a token's position says.
+struct RopePlace {
+    bool pad, none;
+    int64_t row;  // of the tables; 0 where there is no angle
+    __device__ __forceinline__ RopePlace(const RopeArgs& g, const RopeTask& k) {
+        const int64_t pos = rope_position(g, k.t, k.s);
+        pad = pos < 0;
+        none = pos >= g.P && g.R > 0;
+        row = pad || none ? 0 : pos;
+    }
+};
+
+// A warp's heads, task after task, with the next ones in flight: every lane
+// copies its own accesses asynchronously into slots of shared memory of its
+// own (no barrier, no registers while they travel), kRopeRing - 1 heads ahead and
+// across tasks; a slot is refilled one head after it was read. Accesses of one
+// 16-bit value, which asynchronous copies do not have, are loaded when their
+// head's turn comes.
+template <class T, int VEC, int NP, int N>  // N tensors: x, or x and dy
+struct RopeStream {
+    using X = RopeVec<T, VEC>;
+    using Raw = typename X::Raw;
+    static constexpr int kBytes = VEC * static_cast<int>(sizeof(T));
+    static constexpr bool kAsync = kBytes >= 4;
+    static constexpr int kAccess = 32 * kBytes;         // a warp's copy of one access
+    static constexpr int kUnit = N * NP * 2 * kAccess;  // of a head
+    static constexpr int kWarp = kAsync ? kRopeRing * kUnit : 0;
+
+    uint32_t ring;  // this lane's first slot
+    int task, step, left = 0, sent = 0;
+    bool on = false;
+    const T* p[N];
+    int64_t stride[N];
+
+    template <class L>
+    __device__ __forceinline__ RopeStream(const RopeArgs& g, const RopeSide& sd, const L& l, void* smem, int first, int step_)
+        : task(first), step(step_) {
+        ring = smem_addr(smem) + (threadIdx.x >> 5) * kWarp + (threadIdx.x & 31) * kBytes;
+        stride[0] = sd.x.head;
+        if constexpr (N == 2) stride[1] = sd.dy.head;
+        if constexpr (kAsync) {
+            // places that no copy goes to are zero throughout
+#pragma unroll
+            for (int i = 0; i < kRopeRing * N * NP; ++i) {
+                if (l.a[i % NP] < 0) zero(ring + 2 * i * kAccess);
+                if (l.b[i % NP] < 0) zero(ring + (2 * i + 1) * kAccess);
+            }
+#pragma unroll
+            for (int i = 0; i < kRopeRing - 1; ++i) send(g, sd, l);
+        }
+    }
+    static __device__ __forceinline__ void zero(uint32_t at) {
+#pragma unroll
+        for (int i = 0; i < kBytes; i += 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + i), "r"(0) : "memory");
+    }
+    __device__ __forceinline__ void enter(const RopeArgs& g, const RopeSide& sd) {
+        const RopeTask k(g, sd, task);
+        p[0] = rope_at<const T>(sd.x, k);
+        if constexpr (N == 2) p[1] = rope_at<const T>(sd.dy, k);
+        left = k.n;
+        on = k.on;
+        task = task < sd.tasks - step ? task + step : sd.tasks;
+    }
+    // Issues the copies of the next head; a group of copies is committed even
+    // when none is left.
+    template <class L>
+    __device__ __forceinline__ void send(const RopeArgs& g, const RopeSide& sd, const L& l) {
+        if (left == 0 && task < sd.tasks) enter(g, sd);
+        if (left > 0) {
+            const uint32_t at = ring + (sent & (kRopeRing - 1)) * kUnit;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    if (on && l.a[j] >= 0) copy_async<kBytes>(at + ((n * NP + j) * 2) * kAccess, p[n] + l.a[j]);
+                    if (on && l.b[j] >= 0) copy_async<kBytes>(at + ((n * NP + j) * 2 + 1) * kAccess, p[n] + l.b[j]);
+                }
+                p[n] += stride[n];
+            }
+            --left;
+        }
+        ++sent;
+        copy_async_commit();
+    }
+    static __device__ __forceinline__ Raw shared(uint32_t at) {
+        Raw r;
+        if constexpr (kBytes == 16)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+        else if constexpr (kBytes == 8)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
+        else
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+        return r;
+    }
+    // The accesses of the next head; `live`: this lane's token has values, `all`: every lane's of the warp.
+    template <class L>
+    __device__ __forceinline__ void take(const RopeArgs& g, const RopeSide& sd, const L& l, bool live, bool all, Raw (&raw)[N][NP][2]) {
+        if constexpr (kAsync) {
+            copy_async_wait<kRopeRing - 2>();  // this head's copies have landed
+            const uint32_t from = ring + ((sent + 1) & (kRopeRing - 1)) * kUnit;  // kRopeRing - 1 heads were sent beyond it
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    raw[n][j][0] = shared(from + ((n * NP + j) * 2) * kAccess);
+                    raw[n][j][1] = shared(from + ((n * NP + j) * 2 + 1) * kAccess);
+                }
+            send(g, sd, l);  // into the slot read one head ago
+            if (!all) {
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int j = 0; j < NP; ++j)
+                        if (!live) raw[n][j][0] = raw[n][j][1] = X::zero();
+            }
+        } else {
+            if (left == 0) enter(g, sd);
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    raw[n][j][0] = live && l.a[j] >= 0 ? X::load(p[n] + l.a[j]) : X::zero();
+                    raw[n][j][1] = live && l.b[j] >= 0 ? X::load(p[n] + l.b[j]) : X::zero();
+                }
+                p[n] += stride[n];
+            }
+            --left;
+        }
+    }
+};
+
+// ------------------------------------------------------------ forward
+// One head of the forward from its accesses; `on`: there is a token.
+template <class T, int VEC, int NP, bool ILV>
+__device__ __forceinline__ void rope_fwd_head(const RopeArgs& g, const RopeLane<VEC, NP, ILV>& l,
+                                              const RopeWeightedTurn<T, VEC, NP, ILV>& turn,
+                                              const typename RopeVec<T, VEC>::Raw (&raw)[1][NP][2], T* y, bool on, bool mixed,
+                                              int lanes, float eps) {
+    using X = RopeVec<T, VEC>;
+    using V = RopeVals<T, VEC>;
+    V va[NP], vb[NP];
+    float2 qa = make_float2(0.f, 0.f), qb = qa;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        va[j].widen(raw[0][j][0]);
+        vb[j].widen(raw[0][j][1]);
+#pragma unroll
+        for (int i = 0; i < X::H; ++i) {
+            qa = __ffma2_rn(va[j].v[i], va[j].v[i], qa);
+            qb = __ffma2_rn(vb[j].v[i], vb[j].v[i], qb);
+        }
+    }
+    qa = __fadd2_rn(qa, qb);
+    float ss[1] = {qa.x + qa.y};
+    rope_sum(ss, lanes);
+    const float2 r2 = f2_splat(rsqrtf(fmaf(ss[0], g.invD, eps)));
+    V oa[NP], ob[NP];
+    if (mixed && __any_sync(kFullMask, !isfinite(ss[0]))) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) turn.template apply<true>(l, j, va[j], vb[j], r2, oa[j], ob[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) turn.template apply<false>(l, j, va[j], vb[j], r2, oa[j], ob[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        if (on && l.a[j] >= 0) X::store(y + l.a[j], oa[j].round());
+        if (on && l.b[j] >= 0) X::store(y + l.b[j], ob[j].round());
+    }
+}
+
+// Persistent, over the stream of heads.
+template <class T, int VEC, int NP, bool ILV>
+__global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_fwd(const __grid_constant__ RopeArgs g) {
+    extern __shared__ __align__(16) char smem[];
+    grid_release();
+    const RopeShare share(g);
+    const RopeSide& sd = g.side[share.second];
+    const int lanes = 1 << g.lanes_log;
+    const RopeLane<VEC, NP, ILV> l(g, threadIdx.x & (lanes - 1));
+    const bool mixed = rope_mixed(l);
+    grid_wait();
+    RopeStream<T, VEC, NP, 1> in(g, sd, l, smem, share.first, share.step);
+    const RopeWeight<T, VEC, NP, ILV> w(l, static_cast<const T*>(sd.w));
+    for (int task = share.first; task < sd.tasks; task = task < sd.tasks - share.step ? task + share.step : sd.tasks) {
+        const RopeTask k(g, sd, task);
+        const RopePlace at(g, k);
+        RopeWeightedTurn<T, VEC, NP, ILV> turn;
+        turn.set(l, w.a, w.b, g.cos + at.row * g.table_pitch, g.sin + at.row * g.table_pitch, g.vec_table != 0);
+        const bool live = k.on && !at.pad, all = __all_sync(kFullMask, live);  // (padding: zeros in, zeros out)
+        const float eps = at.none ? __int_as_float(0x7fffffff) : g.eps;        // no angle: NaN
+        T* y = rope_at<T>(sd.y, k);
+        for (int h = 0; h < k.n; ++h, y += sd.y.head) {
+            typename RopeVec<T, VEC>::Raw raw[1][NP][2];
+            in.take(g, sd, l, live, all, raw);
+            rope_fwd_head<T, VEC, NP, ILV>(g, l, turn, raw, y, k.on, mixed, lanes, eps);
+        }
+    }
+}
+
+// For few heads: a warp has one task and its heads come straight into
+// registers, the first before its position is known. No shared memory to go
+// through: one token of 36 heads 1.7 us instead of 2.2, 501 x 16 heads of 80
+// 2.2 instead of 2.7 (but 16384 x 40 heads of 128 66 instead of 56: a load per
+// lane and access in flight is too little for the latency under load).
+template <class T, int VEC, int NP, bool ILV>
+__global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_fwd_few(const __grid_constant__ RopeArgs g) {
+    using X = RopeVec<T, VEC>;
+    constexpr int DEPTH = 2;
+    grid_release();
+    const RopeShare share(g);
+    const RopeSide& sd = g.side[share.second];
+    const int lanes = 1 << g.lanes_log;
+    const RopeLane<VEC, NP, ILV> l(g, threadIdx.x & (lanes - 1));
+    const bool mixed = rope_mixed(l);
+    grid_wait();
+    if (share.first >= sd.tasks) return;  // (a whole warp)
+    const RopeTask k(g, sd, share.first);
+    const T* x = rope_at<const T>(sd.x, k);
+    typename X::Raw raw[DEPTH][1][NP][2];
+    const auto load = [&](int d, int h) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            raw[d][0][j][0] = k.on && h < k.n && l.a[j] >= 0 ? X::load(x + l.a[j]) : X::zero();
+            raw[d][0][j][1] = k.on && h < k.n && l.b[j] >= 0 ? X::load(x + l.b[j]) : X::zero();
+        }
+        x += sd.x.head;
+    };
+    const RopePlace at(g, k);
+    load(0, 0);
+    load(1, 1);
+    RopeWeightedTurn<T, VEC, NP, ILV> turn;
+    {
+        const RopeWeight<T, VEC, NP, ILV> w(l, static_cast<const T*>(sd.w));
+        turn.set(l, w.a, w.b, g.cos + at.row * g.table_pitch, g.sin + at.row * g.table_pitch, g.vec_table != 0);
+    }
+    const float eps = at.none ? __int_as_float(0x7fffffff) : g.eps;
+    const bool some = __any_sync(kFullMask, at.pad);
+    T* y = rope_at<T>(sd.y, k);
+    for (int h = 0; h < k.n; h += DEPTH)
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (h + d < k.n) {
+                typename X::Raw now[1][NP][2];
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) now[0][j][i] = some && at.pad ? X::zero() : raw[d][0][j][i];
+                load(d, h + d + DEPTH);
+                rope_fwd_head<T, VEC, NP, ILV>(g, l, turn, now, y, k.on, mixed, lanes, eps);
+                y += sd.y.head;
+            }
 }
 
 // ------------------------------------------------------------ backward
@@ -290,37 +547,37 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_fwd(const __grid_cons
 // added in this lane's slots of shared memory.
 constexpr int kRopeChain = 64;
 
-template <class T, int VEC, int NP, bool ILV, int U>
+template <class T, int VEC, int NP, bool ILV>
 __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_bwd(const __grid_constant__ RopeArgs g) {
-    using X = GnVec<T, VEC>;
+    using X = RopeVec<T, VEC>;
     using V = RopeVals<T, VEC>;
+    using R = RopeTurn<T, VEC, NP, ILV, true>;
     constexpr int H = X::H;
-    extern __shared__ float2 sums[];  // [NP * 2 * H][threads]
+    extern __shared__ __align__(16) char smem[];
+    float2* sums = reinterpret_cast<float2*>(smem);  // [NP * 2 * H][threads], before the stream
     grid_release();
-    const bool second = static_cast<int>(blockIdx.x) >= g.side[0].ctas;
-    const RopeSide& sd = g.side[second];
-    const int cta = static_cast<int>(blockIdx.x) - (second ? g.side[0].ctas : 0);
-    const int warps = blockDim.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const int lanes = 1 << g.lanes_log, groups = 32 >> g.lanes_log;
-    const int group = lane >> g.lanes_log;
-    const RopeLane<VEC, NP, ILV> l(g, lane & (lanes - 1));
+    const RopeShare share(g);
+    const RopeSide& sd = g.side[share.second];
+    const int lanes = 1 << g.lanes_log;
+    const RopeLane<VEC, NP, ILV> l(g, threadIdx.x & (lanes - 1));
+    const bool mixed = rope_mixed(l);
     V da[NP], db[NP];  // this lane's share of dw
+    float2* mine_sums = sums + threadIdx.x;
 #pragma unroll
     for (int j = 0; j < NP; ++j)
 #pragma unroll
-        for (int i = 0; i < H; ++i) da[j].v[i] = db[j].v[i] = make_float2(0.f, 0.f);
-    float2* mine = sums + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < NP * 2 * H; ++i) mine[i * blockDim.x] = make_float2(0.f, 0.f);
+        for (int i = 0; i < H; ++i) {
+            da[j].v[i] = db[j].v[i] = make_float2(0.f, 0.f);
+            mine_sums[((j * 2) * H + i) * blockDim.x] = mine_sums[((j * 2 + 1) * H + i) * blockDim.x] = make_float2(0.f, 0.f);
+        }
     int chain = 0;
     const auto fold = [&] {
 #pragma unroll
         for (int j = 0; j < NP; ++j)
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                float2& fa = mine[((j * 2) * H + i) * blockDim.x];
-                float2& fb = mine[((j * 2 + 1) * H + i) * blockDim.x];
+                float2& fa = mine_sums[((j * 2) * H + i) * blockDim.x];
+                float2& fb = mine_sums[((j * 2 + 1) * H + i) * blockDim.x];
                 fa = __fadd2_rn(fa, da[j].v[i]);
                 fb = __fadd2_rn(fb, db[j].v[i]);
                 da[j].v[i] = db[j].v[i] = make_float2(0.f, 0.f);
@@ -328,93 +585,78 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_bwd(const __grid_cons
         chain = 0;
     };
     grid_wait();
+    RopeStream<T, VEC, NP, 2> in(g, sd, l, smem + NP * 2 * H * sizeof(float2) * blockDim.x, share.first, share.step);
     const RopeWeight<T, VEC, NP, ILV> w(l, static_cast<const T*>(sd.w));
-    const int64_t step = int64_t(sd.ctas) * warps;
-    for (int64_t task = int64_t(cta) * warps + (threadIdx.x >> 5); task < sd.tasks; task += step) {
-        const RopeTask k(g, sd, static_cast<int>(task));
-        const int64_t pos = rope_position(g, k.t, k.s);
-        const T* x = rope_at<const T>(sd.x, k);
-        const T* dy = rope_at<const T>(sd.dy, k);
+    for (int task = share.first; task < sd.tasks; task = task < sd.tasks - share.step ? task + share.step : sd.tasks) {
+        const RopeTask k(g, sd, task);
+        const RopePlace at(g, k);
+        R turn;
+        turn.set(l, g.cos + at.row * g.table_pitch, g.sin + at.row * g.table_pitch, g.vec_table != 0);
+        const bool live = k.on && !at.pad, all = __all_sync(kFullMask, live);
+        const float eps = at.none ? __int_as_float(0x7fffffff) : g.eps;
         T* dx = rope_at<T>(sd.y, k);
-        typename X::Raw xa[U][NP], xb[U][NP], ya[U][NP], yb[U][NP];
-        const auto load = [&](int slot) {
+        for (int h = 0; h < k.n; ++h) {
+            typename X::Raw raw[2][NP][2];
+            in.take(g, sd, l, live, all, raw);
+            V va[NP], vb[NP], ta[NP], tb[NP], za[NP], zb[NP];  // x, dy, dz
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = (slot + u) * groups + group;
-                const bool on = slot + u < k.end && h < sd.heads;
-                const T* p = x + h * sd.x.head;
-                const T* q = dy + h * sd.dy.head;
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    xa[u][j] = on && l.a[j] >= 0 ? X::load(p + l.a[j]) : X::zero();
-                    xb[u][j] = on && l.b[j] >= 0 ? X::load(p + l.b[j]) : X::zero();
-                    ya[u][j] = on && l.a[j] >= 0 ? X::load(q + l.a[j]) : X::zero();
-                    yb[u][j] = on && l.b[j] >= 0 ? X::load(q + l.b[j]) : X::zero();
-                }
+            for (int j = 0; j < NP; ++j) {
+                va[j].widen(raw[0][j][0]);
+                vb[j].widen(raw[0][j][1]);
+                ta[j].widen(raw[1][j][0]);
+                tb[j].widen(raw[1][j][1]);
             }
-        };
-        load(k.slot);
-        RopeAngles<VEC, NP, ILV> ang;
-        const bool pad = pos < 0, none = pos >= g.P;
-        if (!pad && !none) ang.load(g, l, pos);
-        for (int slot = k.slot; slot < k.end;) {
+            float s2[2];
+            const auto sums_of = [&](auto safe) {
+                float2 ssa = make_float2(0.f, 0.f), ssb = ssa, sga = ssa, sgb = ssa;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = (slot + u) * groups + group;
-                const bool on = slot + u < k.end && h < sd.heads;
-                V za[NP], zb[NP];
-                float2 ss = make_float2(0.f, 0.f), sg = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    za[j].widen(ya[u][j]);
-                    zb[j].widen(yb[u][j]);
-                    ang.template turn<true>(l, j, za[j], zb[j]);
-                    V va, vb;
-                    va.widen(xa[u][j]);
-                    vb.widen(xb[u][j]);
+                for (int j = 0; j < NP; ++j)
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
-                        ss = __ffma2_rn(va.v[i], va.v[i], ss);
-                        ss = __ffma2_rn(vb.v[i], vb.v[i], ss);
-                        sg = __ffma2_rn(__fmul2_rn(za[j].v[i], w.a[j].v[i]), va.v[i], sg);
-                        sg = __ffma2_rn(__fmul2_rn(zb[j].v[i], w.b[j].v[i]), vb.v[i], sg);
+                        za[j].v[i] = __ffma2_rn(ta[j].v[i], turn.cos_of(j, i, false),
+                                                __fmul2_rn(R::mate(ta[j], tb[j], i, false), turn.sin_of(j, i, false)));
+                        zb[j].v[i] = __ffma2_rn(tb[j].v[i], turn.cos_of(j, i, true),
+                                                __fmul2_rn(R::mate(ta[j], tb[j], i, true), turn.sin_of(j, i, true)));
+                        if (decltype(safe)::value && !l.ra[j]) za[j].v[i] = ta[j].v[i];
+                        if (decltype(safe)::value && !l.rb[j]) zb[j].v[i] = tb[j].v[i];
+                        ssa = __ffma2_rn(va[j].v[i], va[j].v[i], ssa);
+                        ssb = __ffma2_rn(vb[j].v[i], vb[j].v[i], ssb);
+                        sga = __ffma2_rn(__fmul2_rn(za[j].v[i], w.a[j].v[i]), va[j].v[i], sga);
+                        sgb = __ffma2_rn(__fmul2_rn(zb[j].v[i], w.b[j].v[i]), vb[j].v[i], sgb);
                     }
-                }
-                float s0 = ss.x + ss.y, s1 = sg.x + sg.y;
-                group_sum2(s0, s1, lanes);
-                float r = rsqrtf(fmaf(s0, g.invD, g.eps));
-                if (none) r = __int_as_float(0x7fffffff);
-                const float2 r2 = f2_splat(r), m2 = f2_splat(-(r * r * r * (s1 * g.invD)));
-                T* p = dx + h * sd.y.head;
+                ssa = __fadd2_rn(ssa, ssb);
+                sga = __fadd2_rn(sga, sgb);
+                s2[0] = ssa.x + ssa.y;
+                s2[1] = sga.x + sga.y;
+                rope_sum(s2, lanes);
+            };
+            sums_of(std::false_type{});
+            if (mixed && __any_sync(kFullMask, !isfinite(s2[0]) || !isfinite(s2[1]))) sums_of(std::true_type{});
+            const float r = rsqrtf(fmaf(s2[0], g.invD, eps));
+            // dx = r (g - x r (r mean(g x)))
+            const float2 r2 = f2_splat(r), m2 = f2_splat(-(r * (s2[1] * g.invD)) * r);
 #pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    V va, vb, oa, ob;
-                    va.widen(xa[u][j]);
-                    vb.widen(xb[u][j]);
+            for (int j = 0; j < NP; ++j) {
+                V oa, ob;
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        oa.v[i] = __ffma2_rn(va.v[i], m2, __fmul2_rn(__fmul2_rn(za[j].v[i], w.a[j].v[i]), r2));
-                        ob.v[i] = __ffma2_rn(vb.v[i], m2, __fmul2_rn(__fmul2_rn(zb[j].v[i], w.b[j].v[i]), r2));
-                        if (on && !pad) {
-                            da[j].v[i] = __ffma2_rn(__fmul2_rn(va.v[i], r2), za[j].v[i], da[j].v[i]);
-                            db[j].v[i] = __ffma2_rn(__fmul2_rn(vb.v[i], r2), zb[j].v[i], db[j].v[i]);
-                        }
-                    }
-                    if (on && l.a[j] >= 0) X::store(p + l.a[j], pad ? X::zero() : oa.round());
-                    if (on && l.b[j] >= 0) X::store(p + l.b[j], pad ? X::zero() : ob.round());
+                for (int i = 0; i < H; ++i) {
+                    oa.v[i] = __fmul2_rn(__ffma2_rn(va[j].v[i], m2, __fmul2_rn(za[j].v[i], w.a[j].v[i])), r2);
+                    ob.v[i] = __fmul2_rn(__ffma2_rn(vb[j].v[i], m2, __fmul2_rn(zb[j].v[i], w.b[j].v[i])), r2);
+                    da[j].v[i] = __ffma2_rn(__fmul2_rn(va[j].v[i], r2), za[j].v[i], da[j].v[i]);
+                    db[j].v[i] = __ffma2_rn(__fmul2_rn(vb[j].v[i], r2), zb[j].v[i], db[j].v[i]);
                 }
+                if (k.on && l.a[j] >= 0) X::store(dx + l.a[j], oa.round());
+                if (k.on && l.b[j] >= 0) X::store(dx + l.b[j], ob.round());
             }
-            slot += U;
-            if (slot < k.end) load(slot);
-            chain += U;
-            if (chain >= kRopeChain) fold();
+            dx += sd.y.head;
+            if (++chain == kRopeChain) fold();
         }
     }
     fold();
     __syncthreads();
     // A column's terms lie with the lanes of its place in every group of
     // every warp: added in that order, each column by one thread.
-    float* part = sd.part + int64_t(cta) * g.D;
+    float* part = sd.part + int64_t(share.cta) * g.D;
     const float* flat = reinterpret_cast<const float*>(sums);
     for (int i = threadIdx.x; i < lanes * NP * 2 * VEC; i += blockDim.x) {
         // element e of access `side` of pair j of lane q
@@ -435,15 +677,45 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_bwd(const __grid_cons
 }
 
 // ------------------------------------------------------------ launch
-template <class T, int VEC, int NP, bool ILV, int UF, int UB>
-cudaError_t rope_launch(const norm_rope_plan& p, const RopeArgs& a, bool backward, cudaStream_t s) {
-    const void* fn = backward ? reinterpret_cast<const void*>(rope_bwd<T, VEC, NP, ILV, UB>)
-                              : reinterpret_cast<const void*>(rope_fwd<T, VEC, NP, ILV, UF>);
+// CTAs of a kernel that fit on the device at once, asked once per kernel,
+// size and device.
+inline cudaError_t rope_resident(const void* fn, int threads, size_t smem, int64_t* out) try {
+    static std::mutex mu;
+    static std::map<std::tuple<const void*, int, int>, int64_t> cache;  // (smem follows from the kernel and threads)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    int64_t& n = cache[{fn, threads, dev}];
+    if (n == 0) {
+        int per = 0, sms = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, threads, smem);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        n = int64_t(per) * sms;
+    }
+    *out = n;
+    return n > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
+} catch (...) {  // (no exception leaves a C entry point)
+    return cudaErrorMemoryAllocation;
+}
+
+template <class T, int VEC, int NP, bool ILV>
+cudaError_t rope_launch(const norm_rope_plan& p, RopeArgs& a, bool backward, cudaStream_t s) {
+    const void* fn = backward ? reinterpret_cast<const void*>(rope_bwd<T, VEC, NP, ILV>)
+                     : p.few  ? reinterpret_cast<const void*>(rope_fwd_few<T, VEC, NP, ILV>)
+                              : reinterpret_cast<const void*>(rope_fwd<T, VEC, NP, ILV>);
     const int threads = p.warps * 32;
-    const size_t smem = backward ? size_t(NP) * 2 * GnVec<T, VEC>::H * sizeof(float2) * threads : 0;
-    if (smem > 48 * 1024) {
+    const size_t smem = p.few ? 0 : static_cast<size_t>(rope_smem_bytes(VEC, sizeof(T), NP, p.warps, backward));
+    if (smem > 16 * 1024) {
         const cudaError_t e = gn_opt_in(fn);
         if (e != cudaSuccess) return e;
+    }
+    if (!p.few) {
+        int64_t most = 0;
+        const cudaError_t e = rope_resident(fn, threads, smem, &most);
+        if (e != cudaSuccess) return e;
+        rope_share(&a, std::min(p.ctas, most));
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.side[0].ctas + a.side[1].ctas));
@@ -455,28 +727,26 @@ cudaError_t rope_launch(const norm_rope_plan& p, const RopeArgs& a, bool backwar
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    void* args[] = {const_cast<RopeArgs*>(&a)};
+    void* args[] = {&a};
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-template <class T, int VEC, int NP, int UF, int UB>
-cudaError_t rope_style(const norm_rope_plan& p, const RopeArgs& a, bool interleaved, bool backward, cudaStream_t s) {
-    return interleaved ? rope_launch<T, VEC, NP, true, UF, UB>(p, a, backward, s)
-                       : rope_launch<T, VEC, NP, false, UF, UB>(p, a, backward, s);
+template <class T, int VEC, int NP>
+cudaError_t rope_style(const norm_rope_plan& p, RopeArgs& a, bool interleaved, bool backward, cudaStream_t s) {
+    return interleaved ? rope_launch<T, VEC, NP, true>(p, a, backward, s) : rope_launch<T, VEC, NP, false>(p, a, backward, s);
 }
 
 template <class T>
-cudaError_t rope_dispatch(const norm_rope_plan& p, const RopeArgs& a, bool interleaved, bool backward, cudaStream_t s) {
-    if constexpr (sizeof(T) == 4) {
-        if (p.vec_elems == 4 && p.pairs == 1) return rope_style<T, 4, 1, 4, 2>(p, a, interleaved, backward, s);
-        if (p.vec_elems == 4 && p.pairs == 2) return rope_style<T, 4, 2, 2, 1>(p, a, interleaved, backward, s);
-    } else {
-        if (p.vec_elems == 8 && p.pairs == 1) return rope_style<T, 8, 1, 4, 2>(p, a, interleaved, backward, s);
-        if (p.vec_elems == 2 && p.pairs == 2) return rope_style<T, 2, 2, 4, 2>(p, a, interleaved, backward, s);
-        if (p.vec_elems == 2 && p.pairs == 4) return rope_style<T, 2, 4, 2, 1>(p, a, interleaved, backward, s);
+cudaError_t rope_dispatch(const norm_rope_plan& p, RopeArgs& a, bool interleaved, bool backward, cudaStream_t s) {
+    if (p.vec_elems == 4 && p.pairs == 1) return rope_style<T, 4, 1>(p, a, interleaved, backward, s);
+    if (p.vec_elems == 4 && p.pairs == 2) return rope_style<T, 4, 2>(p, a, interleaved, backward, s);
+    if constexpr (sizeof(T) == 2) {
+        if (p.vec_elems == 8 && p.pairs == 1) return rope_style<T, 8, 1>(p, a, interleaved, backward, s);
+        if (p.vec_elems == 2 && p.pairs == 2) return rope_style<T, 2, 2>(p, a, interleaved, backward, s);
+        if (p.vec_elems == 2 && p.pairs == 4) return rope_style<T, 2, 4>(p, a, interleaved, backward, s);
     }
-    if (p.vec_elems == 1 && p.pairs == 4) return rope_style<T, 1, 4, 2, 2>(p, a, interleaved, backward, s);
-    if (p.vec_elems == 1 && p.pairs == 8) return rope_style<T, 1, 8, 1, 1>(p, a, interleaved, backward, s);
+    if (p.vec_elems == 1 && p.pairs == 4) return rope_style<T, 1, 4>(p, a, interleaved, backward, s);
+    if (p.vec_elems == 1 && p.pairs == 8) return rope_style<T, 1, 8>(p, a, interleaved, backward, s);
     return cudaErrorInvalidValue;
 }
 

@@ -3,7 +3,7 @@
 
 namespace libnorm {
 
-cudaError_t launch_rope_bf16(const norm_rope_plan& p, const RopeArgs& a, bool interleaved, bool backward, cudaStream_t s) {
+cudaError_t launch_rope_bf16(const norm_rope_plan& p, RopeArgs& a, bool interleaved, bool backward, cudaStream_t s) {
     return rope_dispatch<__nv_bfloat16>(p, a, interleaved, backward, s);
 }
 

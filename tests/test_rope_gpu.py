@@ -309,19 +309,17 @@ def test_every_plan(dtype):
     """Narrow accesses, every lane count, chunk and CTA size give the same as the default, to rounding of the sums."""
     dt = DT[dtype]
     q, k, wq, wk, cos, sin, pos, dq, dk = case(50, 6, 3, 64, 32, dt)
-    full = 4 if dt == torch.float32 else 8
     tried = 0
-    for vec, slots, warps in itertools.product((full, 2, 1), (1, 2, 5), (1, 4, 8)):
-        if vec == 2 and dt == torch.float32:
-            continue
+    for vec, heads, warps in itertools.product((4, 1) if dt == torch.float32 else (8, 4, 2, 1), (1, 2, 5), (1, 4, 8)):
         for backward in (False, True):
             p = rn.make_rope_plan(50, 6, 3, 64, 32, dt, backward=backward, vec_elems=vec)
             for lanes in {p["lanes"], 32}:
-                p = dict(p, slots=slots, warps=warps, lanes=lanes, ctas=7 if backward else 0)
+                p = dict(p, heads=heads, warps=warps, lanes=lanes, ctas=7)
                 if backward:
                     both(q, k, wq, wk, cos, sin, pos, False, dq, dk, bplan=p)
                 else:
-                    both(q, k, wq, wk, cos, sin, pos, False, dq, dk, plan=p)
+                    for few in (0, 1):
+                        both(q, k, wq, wk, cos, sin, pos, False, dq, dk, plan=dict(p, few=few))
                 tried += 1
     assert tried > 30
 
