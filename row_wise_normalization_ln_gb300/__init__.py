@@ -22,7 +22,8 @@ __all__ = [
     "ln_fwd", "rms_fwd", "ln_fwd_add", "rms_fwd_add", "ln_fwd_fp8", "rms_fwd_fp8", "ln_bwd", "rms_bwd",
     "make_plan", "make_bwd_plan", "NormPlan", "NormError", "LibraryNotBuilt", "library", "host_rows_pipeline",
     "host_rows_wait", "gn_fwd", "gn_bwd", "make_gn_plan", "gn_workspace_bytes", "GnPlan", "grad_norm", "grad_clip",
-    "rms_fwd_rope", "rms_bwd_rope", "make_rope_plan", "RopePlan",
+    "rms_fwd_rope", "rms_bwd_rope", "make_rope_plan", "RopePlan", "ln_fwd_dropout_add", "rms_fwd_dropout_add",
+    "ln_bwd_dropout_add", "rms_bwd_dropout_add", "ln_bwd_add", "rms_bwd_add", "make_drop_plan",
     "NORM_F32", "NORM_BF16", "NORM_F16", "NORM_MAP_GROUP", "NORM_MAP_CTA",
 ]
 
@@ -165,6 +166,23 @@ def library() -> ctypes.CDLL:
     L.rms_bwd_rope.argtypes = [vp, vp, vp, vp, sz, i64, i64, i64, f32, i32, vp]
     L.rms_fwd_rope_planned.argtypes = L.rms_fwd_rope.argtypes + [rp]
     L.rms_bwd_rope_planned.argtypes = L.rms_bwd_rope.argtypes + [rp]
+    f64 = ctypes.c_double
+    L.drop_fwd_planned.argtypes = [i32, vp, vp, vp, vp, f64, vp, vp, vp, vp, vp, i64, i64, f32, i32, vp,
+                                   ctypes.POINTER(NormPlan)]
+    L.drop_bwd_planned.argtypes = [i32, vp, vp, vp, vp, vp, vp, f64, vp, vp, vp, vp, vp, vp, sz, i64, i64, f32, i32, vp,
+                                   ctypes.POINTER(NormPlan)]
+    L.ln_fwd_dropout_add.argtypes = [vp, vp, vp, vp, f64, vp, vp, vp, vp, vp, i64, i64, f32, i32, vp]
+    L.rms_fwd_dropout_add.argtypes = [vp, vp, vp, f64, vp, vp, vp, i64, i64, f32, i32, vp]
+    L.ln_bwd_dropout_add.argtypes = [vp, vp, vp, vp, vp, vp, f64, vp, vp, vp, vp, vp, vp, sz, i64, i64, i32, vp]
+    L.rms_bwd_dropout_add.argtypes = [vp, vp, vp, vp, f64, vp, vp, vp, vp, vp, sz, i64, i64, f32, i32, vp]
+    L.ln_bwd_add.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i64, i64, i32, vp]
+    L.rms_bwd_add.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, i64, i64, f32, i32, vp]
+    L.drop_make_plan.argtypes = [i64, i64, i32, i32, i32, i32, i32, ctypes.POINTER(NormPlan)]
+    L.drop_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, ctypes.POINTER(NormPlan), ctypes.POINTER(sz)]
+    for f in ("drop_fwd_planned", "drop_bwd_planned", "ln_fwd_dropout_add", "rms_fwd_dropout_add",
+              "ln_bwd_dropout_add", "rms_bwd_dropout_add", "ln_bwd_add", "rms_bwd_add", "drop_make_plan",
+              "drop_workspace_bytes"):
+        getattr(L, f).restype = ctypes.c_int
     for f in ("rope_make_plan", "rope_workspace_bytes", "rms_fwd_rope", "rms_bwd_rope", "rms_fwd_rope_planned",
               "rms_bwd_rope_planned"):
         getattr(L, f).restype = ctypes.c_int
@@ -857,6 +875,123 @@ def rms_bwd_rope(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, 
     if type(r) is int:
         raise NormError(r, "rms_bwd_rope")
     return r
+
+
+# ------------------------------------------------------------ dropout, add and norm
+def make_drop_plan(M: int, N: int, dtype: torch.dtype, layer_norm: bool, backward: bool = False,
+                   aligned: bool = True, num_sms: int = 152) -> dict:
+    """The plan the dropout + add + norm calls would choose (host only)."""
+    p = NormPlan()
+    st = library().drop_make_plan(M, N, _dtype_code(dtype), int(layer_norm), int(backward), int(aligned), num_sms,
+                                  ctypes.byref(p))
+    if st != NORM_OK:
+        raise NormError(st, "drop_make_plan")
+    return p.as_dict()
+
+
+def _drop_plan(plan):
+    return plan if plan is None or isinstance(plan, NormPlan) else NormPlan.from_dict(plan)
+
+
+def _drop_fwd(what, ln, x, residual, gamma, beta, p, rng, eps, h_out, out, mean, rstd, stats, stream, plan):
+    if stream is not None:
+        return _on_stream(stream, x, lambda: _drop_fwd(what, ln, x, residual, gamma, beta, p, rng, eps, h_out, out,
+                                                       mean, rstd, stats, None, plan))
+    pl = _drop_plan(plan)
+    r = _native().drop_fwd(ln, x, residual, gamma, beta, p, rng, eps, h_out, out, mean, rstd, bool(stats),
+                           None if pl is None else ctypes.addressof(pl))
+    if type(r) is int:
+        raise NormError(r, what)
+    return r
+
+
+def _drop_bwd(what, ln, dropout, dy, dh, h, gamma, mean, rstd, p, rng, eps, dx, dresidual, dgamma, dbeta, workspace,
+              stream, plan):
+    if stream is not None:
+        return _on_stream(stream, h, lambda: _drop_bwd(what, ln, dropout, dy, dh, h, gamma, mean, rstd, p, rng, eps,
+                                                       dx, dresidual, dgamma, dbeta, workspace, None, plan))
+    pl = _drop_plan(plan)
+    r = _native().drop_bwd(ln, dropout, dy, dh, h, gamma, mean, rstd, p, rng, eps, dx, dresidual, dgamma, dbeta,
+                           workspace, None if pl is None else ctypes.addressof(pl))
+    if type(r) is int:
+        raise NormError(r, what)
+    return r
+
+
+def ln_fwd_dropout_add(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, p: float,
+                       rng, eps: float = 1e-5, *, h_out: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                       rstd: Optional[torch.Tensor] = None, stats: bool = True,
+                       stream: Optional[torch.cuda.Stream] = None, plan=None):
+    """Dropout, residual add and LayerNorm in one pass: ``h = residual + x *
+    keep / P(keep)`` (rounded to x's dtype), ``y = LayerNorm(h)``. Returns
+    ``(h, y, mean, rstd)`` as ``ln_fwd_add`` does, in place alike.
+
+    ``p``: the probability of being dropped, held to 1/65536. ``rng``: where
+    the mask comes from, ``(seed, offset)`` as whole numbers, or a CUDA int64
+    tensor of the two, read when the kernel runs (a captured graph then takes
+    a new mask for each replay once the tensor is changed). The mask is a
+    function of seed, offset, p and a value's place in the flattened x; it is
+    never stored, and the backward makes it again from the same arguments. Give
+    every call of every step an offset of its own. ``rng`` may be None where
+    ``p`` is 0."""
+    return _drop_fwd("ln_fwd_dropout_add", True, x, residual, gamma, beta, p, rng, eps, h_out, out, mean, rstd, stats,
+                     stream, plan)
+
+
+def rms_fwd_dropout_add(x: torch.Tensor, residual: torch.Tensor, w: torch.Tensor, p: float, rng, eps: float = 1e-6, *,
+                        h_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None, plan=None):
+    """Dropout, residual add and RMSNorm: ``(h, y)``; see ln_fwd_dropout_add."""
+    return _drop_fwd("rms_fwd_dropout_add", False, x, residual, w, None, p, rng, eps, h_out, out, None, None, False,
+                     stream, plan)
+
+
+def ln_bwd_dropout_add(dy: torch.Tensor, dh: Optional[torch.Tensor], h: torch.Tensor, gamma: torch.Tensor,
+                       mean: torch.Tensor, rstd: torch.Tensor, p: float, rng, *, dx: Optional[torch.Tensor] = None,
+                       dresidual: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
+                       dbeta: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None, plan=None):
+    """Backward of ln_fwd_dropout_add from its h, mean and rstd: ``dy`` and
+    ``dh`` are the gradients of y and of h (None: nothing else uses h).
+    Returns ``(dx, dresidual, dgamma, dbeta)``: with ``d = dh + LayerNorm's
+    gradient of its input``, dresidual is d and dx is ``d * keep / P(keep)``
+    with the forward's mask. dgamma and dbeta are fp32 ``[N]``. dx and
+    dresidual may each be dy, dh or h itself. ``workspace`` (any dtype) is
+    allocated when not given; calls that share one must not overlap on the
+    GPU."""
+    return _drop_bwd("ln_bwd_dropout_add", True, True, dy, dh, h, gamma, mean, rstd, p, rng, 0.0, dx, dresidual,
+                     dgamma, dbeta, workspace, stream, plan)
+
+
+def rms_bwd_dropout_add(dy: torch.Tensor, dh: Optional[torch.Tensor], h: torch.Tensor, w: torch.Tensor, p: float, rng,
+                        eps: float = 1e-6, *, dx: Optional[torch.Tensor] = None,
+                        dresidual: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                        plan=None):
+    """Backward of rms_fwd_dropout_add from its h: ``(dx, dresidual, dw)``;
+    see ln_bwd_dropout_add."""
+    return _drop_bwd("rms_bwd_dropout_add", False, True, dy, dh, h, w, None, None, p, rng, eps, dx, dresidual, dw,
+                     None, workspace, stream, plan)
+
+
+def ln_bwd_add(dy: torch.Tensor, dh: Optional[torch.Tensor], h: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor,
+               rstd: torch.Tensor, *, d: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
+               dbeta: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None, plan=None):
+    """Backward of ln_fwd_add from its h, mean and rstd: ``(d, dgamma,
+    dbeta)`` with ``d = dh + LayerNorm's gradient of its input``, the gradient
+    of x and of the residual alike; see ln_bwd_dropout_add."""
+    return _drop_bwd("ln_bwd_add", True, False, dy, dh, h, gamma, mean, rstd, 0.0, None, 0.0, None, d, dgamma, dbeta,
+                     workspace, stream, plan)
+
+
+def rms_bwd_add(dy: torch.Tensor, dh: Optional[torch.Tensor], h: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, *,
+                d: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None, plan=None):
+    """Backward of rms_fwd_add from its h: ``(d, dw)``; see ln_bwd_add."""
+    return _drop_bwd("rms_bwd_add", False, False, dy, dh, h, w, None, None, 0.0, None, eps, None, d, dw, None,
+                     workspace, stream, plan)
 
 
 # ------------------------------------------------------------ host buffers

@@ -1,0 +1,358 @@
+// Dropout + add + norm entry points of the C ABI: argument checks, the launch
+// planner and dispatch. Every argument error is caught here, before any CUDA
+// call.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_runtime_api.h>
+
+#include "drop_args.h"
+#include "norm_args.h"
+
+namespace {
+
+using libnorm::DropArgs;
+using libnorm::kDropMaxSmem;
+using libnorm::kDropMaxStages;
+using libnorm::kDropMaxThreads;
+
+constexpr int64_t kMaxN = 65536;
+constexpr int64_t kMaxGrid = int64_t(1) << 20;
+constexpr int kMaxCluster = 8;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
+int elem_size(norm_dtype d) { return d == NORM_F32 ? 4 : 2; }
+bool on(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+struct Shape {
+    int64_t M, N;
+    norm_dtype dtype;
+    bool ln, bwd;
+    int es() const { return elem_size(dtype); }
+    int streams() const { return bwd ? 3 : 2; }
+};
+
+norm_status check_shape(const Shape& s) {
+    if (s.dtype != NORM_F32 && s.dtype != NORM_BF16 && s.dtype != NORM_F16) return NORM_ERR_DTYPE;
+    if (s.M < 0 || s.N < 1 || s.N > kMaxN || s.M > (int64_t(1) << 62) / s.N) return NORM_ERR_ARG;
+    return NORM_OK;
+}
+
+// The instances there are: accesses per thread.
+bool per_known(const Shape& s, int vec, int per) {
+    if (vec == 1) return per == 4 || per == 16;
+    return per == 1 || per == 2 || (per == 4 && vec * per <= libnorm::drop_max_elems(s.bwd));
+}
+
+int64_t smem_bytes(const Shape& s, const norm_plan& p, int stages) {
+    const int lanes = p.mapping == NORM_MAP_GROUP ? p.group : 0;
+    return libnorm::drop_ring_bytes(p.vec_elems, s.es(), p.per_thread, p.threads, stages, s.streams()) +
+           libnorm::drop_mask_bytes(p.vec_elems, p.per_thread, p.threads, lanes) +
+           (s.bwd && lanes > 0 ? libnorm::drop_sums_bytes(s.ln, p.vec_elems, p.per_thread, p.threads) : 0);
+}
+
+norm_status make_plan(const Shape& s, bool aligned, int num_sms, norm_plan* p) {
+    std::memset(p, 0, sizeof *p);
+    const int vec = aligned && s.N * s.es() % 16 == 0 ? 16 / s.es() : 1;
+    const int64_t nacc = ceil_div(s.N, vec);
+    int most = 16;
+    while (!per_known(s, vec, most)) most /= 2;
+    p->vec_elems = vec;
+    p->cluster = 1;
+    p->rounds = 1;
+    int per = 1;
+    while (per < most && (!per_known(s, vec, per) || per * 32 < nacc)) per *= 2;
+    int teams = 1;
+    if (nacc <= int64_t(per) * 32) {
+        p->mapping = NORM_MAP_GROUP;
+        p->group = 1;
+        while (p->group * per < nacc) p->group *= 2;
+        p->threads = 128;
+        teams = p->threads / p->group;
+    } else {
+        p->mapping = NORM_MAP_CTA;
+        int64_t threads = round_up(ceil_div(nacc, per), 32);
+        while (threads > kDropMaxThreads && p->cluster < kMaxCluster) {
+            p->cluster *= 2;
+            threads = round_up(ceil_div(nacc, int64_t(p->cluster) * per), 32);
+        }
+        if (threads > kDropMaxThreads) return NORM_ERR_ARG;
+        // few rows: more threads for each
+        while (per > 1 && s.M * p->cluster * threads < int64_t(num_sms) * 256) {
+            int q = per / 2;
+            while (q > 0 && !per_known(s, vec, q)) q /= 2;
+            const int64_t t2 = q > 0 ? round_up(ceil_div(nacc, p->cluster * q), 32) : kDropMaxThreads + 1;
+            if (t2 > kDropMaxThreads) break;
+            per = q;
+            threads = t2;
+        }
+        p->threads = static_cast<int32_t>(threads);
+    }
+    p->per_thread = per;
+    if (vec * s.es() >= 4) {
+        // as many stages as leave room for the CTAs that registers allow
+        const int64_t ctas = std::max<int64_t>(1, 512 / p->threads);
+        p->stages = kDropMaxStages;
+        while (p->stages > 2 && smem_bytes(s, *p, p->stages) * ctas > kDropMaxSmem) --p->stages;
+    }
+    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(16, 1024 / p->threads));
+    p->grid = std::max<int64_t>(1, std::min<int64_t>(ceil_div(s.M, teams), std::max<int64_t>(1, num_sms * per_sm / p->cluster))) * p->cluster;
+    return NORM_OK;
+}
+
+norm_status check_plan(const norm_plan& p, const Shape& s, bool aligned) {
+    const int es = s.es();
+    if (p.vec_elems != 1 && (p.vec_elems != 16 / es || !aligned || s.N * es % 16 != 0)) return NORM_ERR_PLAN;
+    if (!per_known(s, p.vec_elems, p.per_thread)) return NORM_ERR_PLAN;
+    if (p.threads < 32 || p.threads > kDropMaxThreads || p.threads % 32 != 0) return NORM_ERR_PLAN;
+    const int64_t nacc = ceil_div(s.N, p.vec_elems);
+    if (p.mapping == NORM_MAP_GROUP) {
+        if (!is_pow2(p.group) || p.group > 32 || int64_t(p.group) * p.per_thread < nacc || p.cluster != 1) return NORM_ERR_PLAN;
+    } else if (p.mapping == NORM_MAP_CTA) {
+        if (!is_pow2(p.cluster) || p.cluster > kMaxCluster) return NORM_ERR_PLAN;
+        if (int64_t(p.cluster) * p.threads * p.per_thread < nacc) return NORM_ERR_PLAN;
+    } else {
+        return NORM_ERR_PLAN;
+    }
+    const bool ring = p.vec_elems * es >= 4;
+    if (ring ? (p.stages < 2 || p.stages > kDropMaxStages) : p.stages != 0) return NORM_ERR_PLAN;
+    if (smem_bytes(s, p, p.stages) > kDropMaxSmem) return NORM_ERR_PLAN;
+    if (p.grid < p.cluster || p.grid > kMaxGrid || p.grid % p.cluster != 0) return NORM_ERR_PLAN;
+    return NORM_OK;
+}
+
+int64_t workspace_bytes(const Shape& s, const norm_plan& p) { return p.grid / p.cluster * (s.ln ? 2 : 1) * s.N * 4; }
+
+norm_status done(cudaError_t e) {
+    if (e == cudaSuccess) return NORM_OK;
+    libnorm::note_cuda_error(static_cast<int>(e));
+    return NORM_ERR_CUDA;
+}
+
+// The current device's SM count, read once per device.
+norm_status device_sms(int* sms) {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return done(e);
+    int n = dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return done(e);
+        if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
+    return NORM_OK;
+}
+
+// The dropout's threshold and scale; rng may be missing where nothing is dropped.
+norm_status settle_mask(double p, const norm_rng* rng, DropArgs* a) {
+    if (!(p >= 0.0) || !(p < 1.0)) return NORM_ERR_ARG;
+    const int64_t t = static_cast<int64_t>(std::floor(p * 65536.0 + 0.5));
+    if (t > 65535) return NORM_ERR_ARG;
+    if (t > 0 && !rng) return NORM_ERR_ARG;
+    a->limit = static_cast<uint32_t>(t) << 16;
+    a->scale = static_cast<float>(65536.0 / static_cast<double>(65536 - t));
+    if (t > 0) {
+        if (!on(rng->device, 8)) return NORM_ERR_ARG;
+        a->rng = rng->device;
+        a->seed = rng->seed;
+        a->offset = rng->offset;
+    }
+    return NORM_OK;
+}
+
+norm_status settle(const Shape& s, bool aligned, const norm_plan* plan, norm_plan* p, DropArgs* a) {
+    if (plan) {
+        *p = *plan;
+        if (p->mapping == NORM_MAP_GROUP) p->cluster = 1;
+    } else {
+        int sms = 0;
+        norm_status st = device_sms(&sms);
+        if (st != NORM_OK) return st;
+        st = make_plan(s, aligned, sms, p);
+        if (st != NORM_OK) return st;
+    }
+    const norm_status st = check_plan(*p, s, aligned);
+    if (st != NORM_OK) return st;
+    a->M = s.M;
+    a->N = static_cast<int32_t>(s.N);
+    a->invN = 1.f / static_cast<float>(s.N);
+    a->lanes = p->mapping == NORM_MAP_GROUP ? p->group : 0;
+    a->cluster = p->cluster;
+    a->stages = p->stages;
+    return NORM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+norm_status drop_fwd_planned(int layer_norm, const void* x, const void* residual, const void* gamma, const void* beta,
+                             double prob, const norm_rng* rng, void* h, void* y, float* mean, float* rstd, int64_t M,
+                             int64_t N, float eps, norm_dtype dtype, cudaStream_t stream, const norm_plan* plan) {
+    const Shape s{M, N, dtype, layer_norm != 0, false};
+    norm_status st = check_shape(s);
+    if (st != NORM_OK) return st;
+    if (!std::isfinite(eps) || eps < 0.f) return NORM_ERR_ARG;
+    DropArgs a{};
+    st = settle_mask(prob, rng, &a);
+    if (st != NORM_OK || M == 0) return st;
+    const int es = s.es();
+    bool aligned = true;
+    for (const void* p : {x, residual, gamma, static_cast<const void*>(h), static_cast<const void*>(y), s.ln ? beta : gamma}) {
+        if (!p || !on(p, es)) return NORM_ERR_ARG;
+        aligned = aligned && on(p, 16);
+    }
+    if (h == y || !on(mean, 4) || !on(rstd, 4)) return NORM_ERR_ARG;
+    norm_plan p;
+    st = settle(s, aligned, plan, &p, &a);
+    if (st != NORM_OK) return st;
+    a.x = x;
+    a.residual = residual;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.h = h;
+    a.y = y;
+    a.mean = s.ln ? mean : nullptr;
+    a.rstd = s.ln ? rstd : nullptr;
+    a.eps = eps;
+    switch (dtype) {
+        case NORM_F32: return done(libnorm::launch_drop_fwd_f32(p, a, s.ln, stream));
+        case NORM_BF16: return done(libnorm::launch_drop_fwd_bf16(p, a, s.ln, stream));
+        default: return done(libnorm::launch_drop_fwd_f16(p, a, s.ln, stream));
+    }
+}
+
+norm_status drop_bwd_planned(int layer_norm, const void* dy, const void* dh, const void* h, const void* gamma,
+                             const float* mean, const float* rstd, double prob, const norm_rng* rng, void* dx,
+                             void* dresidual, float* dgamma, float* dbeta, void* workspace, size_t workspace_size,
+                             int64_t M, int64_t N, float eps, norm_dtype dtype, cudaStream_t stream,
+                             const norm_plan* plan) {
+    const Shape s{M, N, dtype, layer_norm != 0, true};
+    norm_status st = check_shape(s);
+    if (st != NORM_OK) return st;
+    if (!s.ln && (!std::isfinite(eps) || eps < 0.f)) return NORM_ERR_ARG;
+    if (!dgamma || !on(dgamma, 4) || (s.ln && (!dbeta || !on(dbeta, 4)))) return NORM_ERR_ARG;
+    DropArgs a{};
+    st = settle_mask(prob, rng, &a);
+    if (st != NORM_OK) return st;
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
+    a.N = static_cast<int32_t>(N);
+    if (M == 0) return done(libnorm::launch_drop_colsum(a, 0, s.ln, stream));
+    if (a.limit != 0 && !dx) return NORM_ERR_ARG;
+    const int es = s.es();
+    bool aligned = on(dh, 16) && on(dx, 16);
+    if (!on(dh, es) || !on(dx, es)) return NORM_ERR_ARG;
+    for (const void* p : {dy, h, gamma, static_cast<const void*>(dresidual)}) {
+        if (!p || !on(p, es)) return NORM_ERR_ARG;
+        aligned = aligned && on(p, 16);
+    }
+    if (dx == dresidual) return NORM_ERR_ARG;
+    if (s.ln && (!mean || !rstd || !on(mean, 4) || !on(rstd, 4))) return NORM_ERR_ARG;
+    norm_plan p;
+    st = settle(s, aligned, plan, &p, &a);
+    if (st != NORM_OK) return st;
+    if (!workspace || !on(workspace, 16) || workspace_size < static_cast<size_t>(workspace_bytes(s, p))) return NORM_ERR_ARG;
+    a.dy = dy;
+    a.dh = dh;
+    a.hin = h;
+    a.gamma = gamma;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.dx = dx;
+    a.dres = dresidual;
+    a.ws = static_cast<float*>(workspace);
+    a.eps = eps;
+    switch (dtype) {
+        case NORM_F32: return done(libnorm::launch_drop_bwd_f32(p, a, s.ln, stream));
+        case NORM_BF16: return done(libnorm::launch_drop_bwd_bf16(p, a, s.ln, stream));
+        default: return done(libnorm::launch_drop_bwd_f16(p, a, s.ln, stream));
+    }
+}
+
+norm_status ln_fwd_dropout_add(const void* x, const void* residual, const void* gamma, const void* beta, double p,
+                               const norm_rng* rng, void* h, void* y, float* mean, float* rstd, int64_t M, int64_t N,
+                               float eps, norm_dtype dtype, cudaStream_t stream) {
+    return drop_fwd_planned(1, x, residual, gamma, beta, p, rng, h, y, mean, rstd, M, N, eps, dtype, stream, nullptr);
+}
+
+norm_status rms_fwd_dropout_add(const void* x, const void* residual, const void* w, double p, const norm_rng* rng,
+                                void* h, void* y, int64_t M, int64_t N, float eps, norm_dtype dtype,
+                                cudaStream_t stream) {
+    return drop_fwd_planned(0, x, residual, w, nullptr, p, rng, h, y, nullptr, nullptr, M, N, eps, dtype, stream, nullptr);
+}
+
+norm_status ln_bwd_dropout_add(const void* dy, const void* dh, const void* h, const void* gamma, const float* mean,
+                               const float* rstd, double p, const norm_rng* rng, void* dx, void* dresidual,
+                               float* dgamma, float* dbeta, void* workspace, size_t workspace_size, int64_t M,
+                               int64_t N, norm_dtype dtype, cudaStream_t stream) {
+    if (M > 0 && !dx) return NORM_ERR_ARG;
+    return drop_bwd_planned(1, dy, dh, h, gamma, mean, rstd, p, rng, dx, dresidual, dgamma, dbeta, workspace,
+                            workspace_size, M, N, 0.f, dtype, stream, nullptr);
+}
+
+norm_status rms_bwd_dropout_add(const void* dy, const void* dh, const void* h, const void* w, double p,
+                                const norm_rng* rng, void* dx, void* dresidual, float* dw, void* workspace,
+                                size_t workspace_size, int64_t M, int64_t N, float eps, norm_dtype dtype,
+                                cudaStream_t stream) {
+    if (M > 0 && !dx) return NORM_ERR_ARG;
+    return drop_bwd_planned(0, dy, dh, h, w, nullptr, nullptr, p, rng, dx, dresidual, dw, nullptr, workspace,
+                            workspace_size, M, N, eps, dtype, stream, nullptr);
+}
+
+norm_status ln_bwd_add(const void* dy, const void* dh, const void* h, const void* gamma, const float* mean,
+                       const float* rstd, void* d, float* dgamma, float* dbeta, void* workspace, size_t workspace_size,
+                       int64_t M, int64_t N, norm_dtype dtype, cudaStream_t stream) {
+    return drop_bwd_planned(1, dy, dh, h, gamma, mean, rstd, 0.0, nullptr, nullptr, d, dgamma, dbeta, workspace,
+                            workspace_size, M, N, 0.f, dtype, stream, nullptr);
+}
+
+norm_status rms_bwd_add(const void* dy, const void* dh, const void* h, const void* w, void* d, float* dw,
+                        void* workspace, size_t workspace_size, int64_t M, int64_t N, float eps, norm_dtype dtype,
+                        cudaStream_t stream) {
+    return drop_bwd_planned(0, dy, dh, h, w, nullptr, nullptr, 0.0, nullptr, nullptr, d, dw, nullptr, workspace,
+                            workspace_size, M, N, eps, dtype, stream, nullptr);
+}
+
+norm_status drop_make_plan(int64_t M, int64_t N, norm_dtype dtype, int layer_norm, int backward, int aligned16,
+                           int num_sms, norm_plan* plan) {
+    const Shape s{M, N, dtype, layer_norm != 0, backward != 0};
+    const norm_status st = check_shape(s);
+    if (st != NORM_OK) return st;
+    if (!plan || num_sms < 1) return NORM_ERR_ARG;
+    return make_plan(s, aligned16 != 0, num_sms, plan);
+}
+
+norm_status drop_workspace_bytes(int64_t M, int64_t N, norm_dtype dtype, int layer_norm, int num_sms,
+                                 const norm_plan* plan, size_t* bytes) {
+    const Shape s{M, N, dtype, layer_norm != 0, true};
+    norm_status st = check_shape(s);
+    if (st != NORM_OK) return st;
+    if (!bytes || (!plan && num_sms < 1)) return NORM_ERR_ARG;
+    *bytes = 0;
+    if (M == 0) return NORM_OK;
+    if (plan) {
+        if (plan->cluster < 1 && plan->mapping != NORM_MAP_GROUP) return NORM_ERR_ARG;
+        norm_plan p = *plan;
+        if (p.mapping == NORM_MAP_GROUP) p.cluster = 1;
+        if (p.grid < 0 || p.grid > kMaxGrid) return NORM_ERR_ARG;
+        *bytes = static_cast<size_t>(workspace_bytes(s, p));
+        return NORM_OK;
+    }
+    for (bool aligned : {true, false}) {
+        norm_plan p;
+        st = make_plan(s, aligned, num_sms, &p);
+        if (st == NORM_OK) *bytes = std::max(*bytes, static_cast<size_t>(workspace_bytes(s, p)));
+        else if (aligned) return st;
+    }
+    return NORM_OK;
+}
+
+}  // extern "C"

@@ -1,7 +1,7 @@
-// Native half of the Python binding of the group norm, gradient and head norm
-// calls: checks the tensors, allocates what the caller did not
-// give, and passes pointers and the current stream to the C ABI
-// (libnorm_group.h, libnorm_grad.h, libnorm_rope.h). These calls are short and many (a step of a small network,
+// Native half of the Python binding of the group norm, gradient, head norm and
+// dropout calls: checks the tensors, allocates what the caller did not give,
+// and passes pointers and the current stream to the C ABI (libnorm_group.h,
+// libnorm_grad.h, libnorm_rope.h, libnorm_dropout.h). These calls are short and many (a step of a small network,
 // lists of hundreds of gradients); marshalling them through ctypes took three
 // to five times as long as their kernels.
 //
@@ -27,6 +27,7 @@
 #include <unordered_map>
 #include <vector>
 
+#include "libnorm_dropout.h"
 #include "libnorm_grad.h"
 #include "libnorm_group.h"
 #include "libnorm_rope.h"
@@ -534,6 +535,141 @@ PyObject* rope_bwd_py(PyObject* const* a) {
     return out;
 }
 
+// ------------------------------------------------------------ dropout, add and norm
+struct RowCall {
+    at::Tensor x;  // the rows' type, device and shape
+    norm_dtype dtype;
+    int64_t M, N;
+};
+
+void read_shape(RowCall* c, const at::Tensor& x, const char* what) {
+    if (!x.is_cuda()) refuse(std::string(what) + " needs CUDA tensors");
+    c->x = x;
+    c->dtype = dtype_of(x);
+    if (x.dim() == 0) refuse("rows need at least one dimension");
+    c->N = x.size(-1);
+    if (c->N == 0) refuse("rows must have at least one element");
+    c->M = x.numel() / c->N;
+}
+
+// A tensor of the rows' shape, type and device, made contiguous.
+at::Tensor rows_like(PyObject* o, const RowCall& c, const char* name) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.sizes() != c.x.sizes() || t.scalar_type() != c.x.scalar_type() || t.device() != c.x.device())
+        refuse(std::string(name) + " must have the rows' shape, dtype and device");
+    return t.is_contiguous() ? t : t.contiguous();
+}
+
+at::Tensor rows_out(PyObject* o, const RowCall& c, const char* name) {
+    if (o == Py_None) return fresh(c.x.sizes(), c.x.scalar_type(), c.x);
+    const at::Tensor& t = tensor(o, name);
+    if (t.sizes() != c.x.sizes() || t.scalar_type() != c.x.scalar_type() || t.device() != c.x.device() || !t.is_contiguous())
+        refuse(std::string(name) + " must be a contiguous tensor of the rows' shape, dtype and device");
+    return t;
+}
+
+// Where the random numbers come from: (seed, offset), or a CUDA tensor of both.
+const norm_rng* read_rng(PyObject* o, const RowCall& c, norm_rng* out) {
+    if (o == Py_None) return nullptr;
+    *out = norm_rng{0, 0, nullptr};
+    if (THPVariable_Check(o)) {
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (t.scalar_type() != at::kLong || t.numel() != 2 || !t.is_contiguous() || t.device() != c.x.device())
+            refuse("rng must be (seed, offset) or a contiguous int64 tensor of both on " + c.x.device().str());
+        out->device = static_cast<const uint64_t*>(ptr(t));
+        return out;
+    }
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 2) throw BadType("rng must be (seed, offset) or an int64 tensor of both");
+    uint64_t* to[2] = {&out->seed, &out->offset};
+    for (int i = 0; i < 2; ++i) {
+        *to[i] = PyLong_AsUnsignedLongLongMask(PyTuple_GET_ITEM(o, i));
+        if (PyErr_Occurred()) throw PythonError{};
+    }
+    return out;
+}
+
+PyObject* drop_fwd_py(PyObject* const* a) {
+    // ln x residual gamma beta p rng eps h_out out mean rstd stats plan
+    const bool ln = a[0] == Py_True;
+    RowCall c;
+    read_shape(&c, tensor(a[1], "x"), ln ? "ln_fwd_dropout_add" : "rms_fwd_dropout_add");
+    const at::Tensor gamma = param(a[3], c.x, c.N, ln ? "gamma" : "w"), beta = ln ? param(a[4], c.x, c.N, "beta") : at::Tensor();
+    const double p = real(a[5]);
+    const float eps = static_cast<float>(real(a[7]));
+    norm_rng rng;
+    const norm_rng* r = read_rng(a[6], c, &rng);
+    const c10::cuda::CUDAGuard guard(c.x.device());
+    const at::Tensor x = rows_like(a[1], c, "x"), res = rows_like(a[2], c, "residual");
+    const at::Tensor h = rows_out(a[8], c, "h_out"), y = rows_out(a[9], c, "out");
+    at::Tensor mean, rstd;
+    if (ln && a[12] == Py_True) {
+        mean = f32(a[10], {c.M}, c.x, "mean");
+        rstd = f32(a[11], {c.M}, c.x, "rstd");
+    }
+    const norm_plan* plan = a[13] == Py_None ? nullptr : static_cast<const norm_plan*>(PyLong_AsVoidPtr(a[13]));
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(c.x.get_device()).stream();
+    norm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = drop_fwd_planned(ln, ptr(x), ptr(res), ptr(gamma), ptr(beta), p, r, ptr(h), ptr(y), static_cast<float*>(ptr(mean)),
+                          static_cast<float*>(ptr(rstd)), c.M, c.N, eps, c.dtype, stream, plan);
+    Py_END_ALLOW_THREADS
+    if (st != NORM_OK) return PyLong_FromLong(st);
+    PyObject* out = PyTuple_New(ln ? 4 : 2);
+    if (!out) throw PythonError{};
+    PyTuple_SET_ITEM(out, 0, given_or(a[8], h));
+    PyTuple_SET_ITEM(out, 1, given_or(a[9], y));
+    if (ln) {
+        PyTuple_SET_ITEM(out, 2, given_or(a[10], mean));
+        PyTuple_SET_ITEM(out, 3, given_or(a[11], rstd));
+    }
+    return out;
+}
+
+PyObject* drop_bwd_py(PyObject* const* a) {
+    // ln dropout dy dh h gamma mean rstd p rng eps dx dresidual dgamma dbeta workspace plan
+    const bool ln = a[0] == Py_True, dropout = a[1] == Py_True;
+    RowCall c;
+    const char* what = ln ? (dropout ? "ln_bwd_dropout_add" : "ln_bwd_add") : (dropout ? "rms_bwd_dropout_add" : "rms_bwd_add");
+    read_shape(&c, tensor(a[4], "h"), what);
+    const at::Tensor gamma = param(a[5], c.x, c.N, ln ? "gamma" : "w");
+    const double p = real(a[8]);
+    const float eps = static_cast<float>(real(a[10]));
+    norm_rng rng;
+    const norm_rng* r = read_rng(a[9], c, &rng);
+    const c10::cuda::CUDAGuard guard(c.x.device());
+    const at::Tensor dy = rows_like(a[2], c, "dy"), h = rows_like(a[4], c, "h");
+    const at::Tensor dh = a[3] == Py_None ? at::Tensor() : rows_like(a[3], c, "dh");
+    at::Tensor mean, rstd, dx;
+    if (ln) {
+        mean = given_f32(a[6], c.M, c.x, "mean");
+        rstd = given_f32(a[7], c.M, c.x, "rstd");
+    }
+    if (dropout) dx = rows_out(a[11], c, "dx");
+    const at::Tensor dres = rows_out(a[12], c, "dresidual");
+    const at::Tensor dgamma = f32(a[13], {c.N}, c.x, ln ? "dgamma" : "dw");
+    const at::Tensor dbeta = ln ? f32(a[14], {c.N}, c.x, "dbeta") : at::Tensor();
+    const norm_plan* plan = a[16] == Py_None ? nullptr : static_cast<const norm_plan*>(PyLong_AsVoidPtr(a[16]));
+    size_t bytes = 0;
+    if (a[15] == Py_None) drop_workspace_bytes(c.M, c.N, c.dtype, ln, sm_count(c.x.get_device()), plan, &bytes);
+    const at::Tensor ws = scratch(a[15], bytes, c.x);
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(c.x.get_device()).stream();
+    norm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = drop_bwd_planned(ln, ptr(dy), ptr(dh), ptr(h), ptr(gamma), static_cast<float*>(ptr(mean)), static_cast<float*>(ptr(rstd)), p, r,
+                          ptr(dx), ptr(dres), static_cast<float*>(ptr(dgamma)), static_cast<float*>(ptr(dbeta)), ptr(ws), bytes_of(ws),
+                          c.M, c.N, eps, c.dtype, stream, plan);
+    Py_END_ALLOW_THREADS
+    if (st != NORM_OK) return PyLong_FromLong(st);
+    PyObject* out = PyTuple_New(2 + dropout + ln);
+    if (!out) throw PythonError{};
+    Py_ssize_t i = 0;
+    if (dropout) PyTuple_SET_ITEM(out, i++, given_or(a[11], dx));
+    PyTuple_SET_ITEM(out, i++, given_or(a[12], dres));
+    PyTuple_SET_ITEM(out, i++, given_or(a[13], dgamma));
+    if (ln) PyTuple_SET_ITEM(out, i++, given_or(a[14], dbeta));
+    return out;
+}
+
 // No C++ exception leaves a call: each becomes the Python error it stands for.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -561,6 +697,8 @@ PyMethodDef methods[] = {
     {"grad", fast(entry<grad_py, 5>), METH_FASTCALL, nullptr},
     {"rms_fwd_rope", fast(entry<rope_fwd_py, 12>), METH_FASTCALL, nullptr},
     {"rms_bwd_rope", fast(entry<rope_bwd_py, 17>), METH_FASTCALL, nullptr},
+    {"drop_fwd", fast(entry<drop_fwd_py, 14>), METH_FASTCALL, nullptr},
+    {"drop_bwd", fast(entry<drop_bwd_py, 17>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
