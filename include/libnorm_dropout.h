@@ -47,8 +47,8 @@ typedef struct {
  * not looked at and h, y are those of the plain fused add, to the rounding of
  * the statistics.
  * Limits: 1 <= N <= 65536 with 16-byte vectors (every pointer 16-byte aligned,
- * rows whole vectors), N <= 32768 with element accesses; longer rows return
- * NORM_ERR_ARG. Every pointer needs its element's alignment.
+ * rows whole vectors), N <= 32768 otherwise; longer rows return NORM_ERR_ARG.
+ * Every pointer needs its element's alignment.
  */
 norm_status ln_fwd_dropout_add(const void* x, const void* residual, const void* gamma, const void* beta, double p,
                                const norm_rng* rng, void* h, void* y, float* mean, float* rstd, int64_t M, int64_t N,
@@ -97,11 +97,12 @@ norm_status rms_bwd_add(const void* dy, const void* dh, const void* h, const voi
 /* The plan the calls would choose for M rows of N elements on a device with
  * `num_sms` SMs (fields of norm_plan: `mapping` NORM_MAP_GROUP with `group`
  * lanes of a warp per row, or NORM_MAP_CTA with `cluster` CTAs of `threads`
- * threads per row; `per_thread` accesses of `vec_elems` elements per thread,
- * which cover the row; `stages` rows in a CTA's shared memory ring, 0 where
- * accesses are single 16-bit elements; `grid` CTAs at most, persistent).
- * `aligned16`: every pointer is 16-byte aligned. Host only: makes no CUDA
- * call. NORM_ERR_ARG for rows beyond the limits. */
+ * threads per row; `per_thread` accesses of `vec_elems` elements per thread
+ * (vec_elems 1: of two elements), which cover the row; `rounds` rows at a time;
+ * `stages` steps of them in shared memory, 2 to 4 (vec_elems 1: 3 or 4);
+ * `grid` CTAs at most, persistent). `aligned16`: every pointer is 16-byte
+ * aligned. Host only: makes no CUDA call. NORM_ERR_ARG for rows beyond the
+ * limits. */
 norm_status drop_make_plan(int64_t M, int64_t N, norm_dtype dtype, int layer_norm, int backward, int aligned16,
                            int num_sms, norm_plan* plan);
 

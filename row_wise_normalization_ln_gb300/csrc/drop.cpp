@@ -43,84 +43,80 @@ norm_status check_shape(const Shape& s) {
     return NORM_OK;
 }
 
-// The instances there are: accesses per thread.
-bool per_known(const Shape& s, int vec, int per) {
-    if (vec == 1) return per == 4 || per == 16;
-    return per == 1 || per == 2 || (per == 4 && vec * per <= libnorm::drop_max_elems(s.bwd));
-}
+bool known(const Shape& s, bool group, int vec, int per, int rows) { return libnorm::drop_known(s.bwd, group, vec, s.es(), per, rows); }
 
 int64_t smem_bytes(const Shape& s, const norm_plan& p, int stages) {
-    const int lanes = p.mapping == NORM_MAP_GROUP ? p.group : 0;
-    return libnorm::drop_ring_bytes(p.vec_elems, s.es(), p.per_thread, p.threads, stages, s.streams()) +
-           libnorm::drop_mask_bytes(p.vec_elems, p.per_thread, p.threads, lanes) +
-           (s.bwd && lanes > 0 ? libnorm::drop_sums_bytes(s.ln, p.vec_elems, p.per_thread, p.threads) : 0);
+    return libnorm::drop_ring_bytes(p.vec_elems, s.es(), p.per_thread, p.threads, p.rounds, stages, s.streams()) +
+           libnorm::drop_words_bytes(p.vec_elems, p.per_thread, p.threads) +
+           (s.bwd && p.mapping == NORM_MAP_GROUP ? libnorm::drop_sums_bytes(s.ln, p.vec_elems, p.per_thread, p.threads) : 0);
 }
 
 norm_status make_plan(const Shape& s, bool aligned, int num_sms, norm_plan* p) {
     std::memset(p, 0, sizeof *p);
     const int vec = aligned && s.N * s.es() % 16 == 0 ? 16 / s.es() : 1;
-    const int64_t nacc = ceil_div(s.N, vec);
-    int most = 16;
-    while (!per_known(s, vec, most)) most /= 2;
+    const int least = vec == 1 ? 3 : 2;  // stages
     p->vec_elems = vec;
     p->cluster = 1;
-    p->rounds = 1;
-    int per = 1;
-    while (per < most && (!per_known(s, vec, per) || per * 32 < nacc)) per *= 2;
     int teams = 1;
-    if (nacc <= int64_t(per) * 32) {
+    const int64_t nacc = ceil_div(s.N, vec == 1 ? 2 : vec);
+    if (vec > 1 && nacc <= 64) {
         p->mapping = NORM_MAP_GROUP;
+        p->per_thread = nacc <= 32 ? 1 : 2;
         p->group = 1;
-        while (p->group * per < nacc) p->group *= 2;
+        while (p->group * p->per_thread < nacc) p->group *= 2;
         p->threads = 128;
+        p->rounds = p->per_thread == 1 ? 4 : 2;
         teams = p->threads / p->group;
     } else {
         p->mapping = NORM_MAP_CTA;
-        int64_t threads = round_up(ceil_div(nacc, per), 32);
-        while (threads > kDropMaxThreads && p->cluster < kMaxCluster) {
-            p->cluster *= 2;
-            threads = round_up(ceil_div(nacc, int64_t(p->cluster) * per), 32);
+        if (vec > 1 && nacc <= kDropMaxThreads && s.M <= int64_t(num_sms) * 4) {
+            // few rows: one access per thread, one row at a time
+            p->per_thread = 1;
+            p->rounds = 1;
+            p->threads = static_cast<int32_t>(round_up(nacc, 32));
+        } else {
+            // the smallest cluster, then the fewest accesses per thread, then the most rows whose stages fit
+            bool found = false;
+            for (int c = 1; c <= kMaxCluster && !found; c *= 2)
+                for (int per : {1, 2, 4, 8}) {
+                    if (found || (vec == 1 && per == 2 && nacc > 64)) continue;
+                    const int64_t threads = round_up(ceil_div(nacc, int64_t(c) * per), 32);
+                    if (threads > kDropMaxThreads || (per == 1 && threads > 128)) continue;
+                    for (int rows : {4, 2, 1}) {
+                        if (found || !known(s, false, vec, per, rows)) continue;
+                        p->cluster = c;
+                        p->per_thread = per;
+                        p->rounds = rows;
+                        p->threads = static_cast<int32_t>(threads);
+                        found = smem_bytes(s, *p, least) <= kDropMaxSmem;
+                    }
+                }
+            if (!found) return NORM_ERR_ARG;
         }
-        if (threads > kDropMaxThreads) return NORM_ERR_ARG;
-        // few rows: more threads for each
-        while (per > 1 && s.M * p->cluster * threads < int64_t(num_sms) * 256) {
-            int q = per / 2;
-            while (q > 0 && !per_known(s, vec, q)) q /= 2;
-            const int64_t t2 = q > 0 ? round_up(ceil_div(nacc, p->cluster * q), 32) : kDropMaxThreads + 1;
-            if (t2 > kDropMaxThreads) break;
-            per = q;
-            threads = t2;
-        }
-        p->threads = static_cast<int32_t>(threads);
     }
-    p->per_thread = per;
-    if (vec * s.es() >= 4) {
-        // as many stages as leave room for the CTAs that registers allow
-        const int64_t ctas = std::max<int64_t>(1, 512 / p->threads);
-        p->stages = kDropMaxStages;
-        while (p->stages > 2 && smem_bytes(s, *p, p->stages) * ctas > kDropMaxSmem) --p->stages;
-    }
+    // as many stages as leave room for the CTAs that registers allow
+    const int64_t ctas = std::max<int64_t>(1, 512 / p->threads);
+    p->stages = kDropMaxStages;
+    while (p->stages > least && smem_bytes(s, *p, p->stages) * ctas > kDropMaxSmem) --p->stages;
     const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(16, 1024 / p->threads));
-    p->grid = std::max<int64_t>(1, std::min<int64_t>(ceil_div(s.M, teams), std::max<int64_t>(1, num_sms * per_sm / p->cluster))) * p->cluster;
+    p->grid = std::max<int64_t>(1, std::min<int64_t>(ceil_div(s.M, int64_t(teams) * p->rounds), std::max<int64_t>(1, num_sms * per_sm / p->cluster))) * p->cluster;
     return NORM_OK;
 }
 
 norm_status check_plan(const norm_plan& p, const Shape& s, bool aligned) {
     const int es = s.es();
     if (p.vec_elems != 1 && (p.vec_elems != 16 / es || !aligned || s.N * es % 16 != 0)) return NORM_ERR_PLAN;
-    if (!per_known(s, p.vec_elems, p.per_thread)) return NORM_ERR_PLAN;
+    if (p.mapping != NORM_MAP_GROUP && p.mapping != NORM_MAP_CTA) return NORM_ERR_PLAN;
+    if (!known(s, p.mapping == NORM_MAP_GROUP, p.vec_elems, p.per_thread, p.rounds)) return NORM_ERR_PLAN;
     if (p.threads < 32 || p.threads > kDropMaxThreads || p.threads % 32 != 0) return NORM_ERR_PLAN;
-    const int64_t nacc = ceil_div(s.N, p.vec_elems);
+    const int64_t nacc = ceil_div(s.N, p.vec_elems == 1 ? 2 : p.vec_elems);
     if (p.mapping == NORM_MAP_GROUP) {
         if (!is_pow2(p.group) || p.group > 32 || int64_t(p.group) * p.per_thread < nacc || p.cluster != 1) return NORM_ERR_PLAN;
-    } else if (p.mapping == NORM_MAP_CTA) {
+    } else {
         if (!is_pow2(p.cluster) || p.cluster > kMaxCluster) return NORM_ERR_PLAN;
         if (int64_t(p.cluster) * p.threads * p.per_thread < nacc) return NORM_ERR_PLAN;
-    } else {
-        return NORM_ERR_PLAN;
     }
-    const bool ring = p.vec_elems * es >= 4;
-    if (ring ? (p.stages < 2 || p.stages > kDropMaxStages) : p.stages != 0) return NORM_ERR_PLAN;
+    if (p.stages < (p.vec_elems == 1 ? 3 : 2) || p.stages > kDropMaxStages) return NORM_ERR_PLAN;
     if (smem_bytes(s, p, p.stages) > kDropMaxSmem) return NORM_ERR_PLAN;
     if (p.grid < p.cluster || p.grid > kMaxGrid || p.grid % p.cluster != 0) return NORM_ERR_PLAN;
     return NORM_OK;

@@ -13,7 +13,7 @@ namespace libnorm {
 constexpr int kDropMaxThreads = 512;
 constexpr int kDropMaxStages = 4;
 constexpr int64_t kDropMaxSmem = 220 * 1024;  // dynamic, per CTA (beside the kernels' own few KB)
-constexpr int kDropChain = 64;                // rows whose column terms are added one after the other
+constexpr int kDropChain = 64;                // rows whose column terms are added one after the other, at most
 
 struct DropArgs {
     const void *x, *residual;       // forward
@@ -31,26 +31,38 @@ struct DropArgs {
     int32_t lanes;                  // lanes of a warp per row; 0: a CTA or a cluster
     int32_t cluster;
     int32_t stages;
+    int32_t pitch;                  // elements: bytes from one tensor's part of a row to the next
     int32_t words_at, sums_at;      // where the masks' words and the column sums lie in shared memory
     uint32_t limit;                 // dropped where the word is below limit >> 16
     float scale, eps, invN;
 };
 
-// Elements per thread: 16 at most in the backward (its column sums stay in
-// registers), 32 in the forward.
-inline int drop_max_elems(bool backward) { return backward ? 16 : 32; }
-
-// Dynamic shared memory of a launch: the ring of upcoming rows' accesses (of
-// each thread its own; none where an access is one 16-bit element), the words
-// of the mask where accesses are elements (16 bytes per group of 8 elements
-// that a warp, or the lanes of a row, touch: two more than they have), and for
-// rows that lanes share the backward's column sums.
-inline int64_t drop_mask_bytes(int vec, int per_thread, int threads, int lanes) {
-    const int unit = lanes > 0 ? lanes : 32;
-    return vec == 1 ? 16 * int64_t(threads / unit) * ((unit * per_thread + 7) / 8 + 2) : 0;
+// The instances there are: accesses per thread V (of elements: pairs) and rows
+// at a time R. A forward thread holds at most 32 values, a backward one the
+// column sums of at most 16 columns.
+inline bool drop_known(bool backward, bool group, int vec, int elem, int per_thread, int rows) {
+    if (vec == 1) return !group && rows == 1 && (per_thread == 2 || per_thread == 8);
+    if (vec * elem != 16) return false;
+    if (group) return (per_thread == 1 && rows == 4) || (per_thread == 2 && rows == 2);
+    if (per_thread == 1) return rows == 1 || rows == 4;
+    if (elem == 4) return per_thread == 4 && (rows == 1 || rows == 2);
+    return (per_thread == 2 && rows == 2) || (per_thread == 4 && !backward && rows == 1);
 }
-inline int64_t drop_ring_bytes(int vec, int elem, int per_thread, int threads, int stages, int streams) {
-    return vec * elem >= 4 ? int64_t(stages) * streams * per_thread * threads * vec * elem : 0;
+
+// Columns of a CTA's part of a row.
+inline int64_t drop_cta_cols(int vec, int per_thread, int threads) { return int64_t(threads) * per_thread * (vec == 1 ? 2 : vec); }
+
+// Shared memory of the stages: of each thread's own accesses, or of the CTA's
+// part of a row of elements in whole 16-byte chunks at a pitch; of the masks'
+// words of two rows of elements; and of the backward's column sums of rows
+// that lanes share.
+inline int64_t drop_pitch(int elem, int per_thread, int threads) { return (drop_cta_cols(1, per_thread, threads) * elem + 30) / 16 * 16; }
+inline int64_t drop_ring_bytes(int vec, int elem, int per_thread, int threads, int rows, int stages, int streams) {
+    return vec == 1 ? stages * streams * drop_pitch(elem, per_thread, threads)
+                    : int64_t(stages) * streams * rows * per_thread * threads * 16;
+}
+inline int64_t drop_words_bytes(int vec, int per_thread, int threads) {
+    return vec == 1 ? 2 * 16 * (drop_cta_cols(1, per_thread, threads) / 8 + 2) : 0;
 }
 inline int64_t drop_sums_bytes(bool ln, int vec, int per_thread, int threads) {
     return int64_t(ln ? 2 : 1) * vec * per_thread * threads * 4;

@@ -1,15 +1,23 @@
 // Building blocks of the dropout + residual add + norm kernels, forward
 // (drop_fwd.cuh) and backward (drop_bwd.cuh).
 //
-// Rows are walked by persistent CTAs. A row belongs to some lanes of a warp
-// (short rows), a CTA, or a cluster of CTAs; a thread owns the same columns in
-// every row it visits, so the parameters and, in the backward, the column sums
-// stay in its registers. Upcoming rows travel through a ring of shared memory
-// that every thread fills and reads for itself with asynchronous copies of its
-// own accesses: no barrier and no registers while they travel. The mask is
-// computed where it is used: one call of the generator for 8 elements, which
-// are one access of a 16-bit row, half of the calls' outputs used on fp32
-// rows; element accesses share the calls of a warp through shared memory.
+// Rows are walked by persistent CTAs, R neighbouring ones at a time (the cost
+// of a step, its barrier, sums and addresses, is that of many elements). A row
+// belongs to some lanes of a warp (short rows), a CTA, or a cluster of CTAs; a
+// thread owns the same columns in every row it visits, so the parameters and,
+// in the backward, the column sums stay in its registers.
+//
+// Rows of whole 16-byte vectors: a thread's values come in accesses of 16
+// bytes, through a ring of shared memory that it fills and reads for itself
+// with asynchronous copies (DropRing): no barrier and no registers while they
+// travel. Other rows (odd widths, any offset): the CTA copies the aligned 16
+// bytes that hold its part of a row together (DropStage), and a thread takes
+// its elements, every 32nd of its warp's, from there; what it stores goes out
+// element by element.
+//
+// The mask is computed where it is used: one call of the generator for 8
+// elements. On 16-bit rows that is an access, on fp32 rows half of the call is
+// used, rows of elements share the calls of the CTA through shared memory.
 #pragma once
 
 #include "drop_args.h"
@@ -56,231 +64,337 @@ struct DropMask {
 
 __device__ __forceinline__ uint32_t drop_word(const uint4& w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
 
-// ------------------------------------------------------------ a thread's place
-struct DropPlace {
-    int unit;        // lanes that share sums by butterflies: those of a row, or a warp
-    int f0, step;    // first access within the row, from one to the next
-    int nv;          // accesses that lie within the row
-    int64_t row, rows_step;
-    int64_t iters;   // rows the CTA's first team visits (the others' last may lie beyond M)
-    bool first;      // writes the row's statistics
-    int warps;       // warps of a CTA that share a row (1: a row's lanes lie in one warp)
-    int rank, C;
+// ------------------------------------------------------------ accesses
+// What a thread takes at a time, as fp32 pairs: a 16-byte vector, or (VEC 1)
+// two elements of its warp's run, 32 apart.
+template <class T, int VEC>
+struct DropVec : GnVec<T, VEC> {};
+template <class T>
+struct DropVec<T, 1> {
+    using E = GnVec<T, 1>;
+    struct Raw {
+        uint32_t lo, hi;
+    };
+    static constexpr int H = 1;
+    static __device__ __forceinline__ Raw zero() { return Raw{0, 0}; }
+    static __device__ __forceinline__ float2 get(const Raw& r, int) { return make_float2(E::get(r.lo, 0).x, E::get(r.hi, 0).x); }
+    static __device__ __forceinline__ void set(Raw& r, int, float2 v) {
+        if constexpr (sizeof(T) == 4) {
+            r.lo = __float_as_uint(v.x);
+            r.hi = __float_as_uint(v.y);
+        } else {
+            const uint32_t w = Gn16<T>::Pair::pack(v.x, v.y);
+            r.lo = w & 0xffff;
+            r.hi = w >> 16;
+        }
+    }
+};
 
-    template <int VEC, int V>
-    __device__ __forceinline__ void set(const DropArgs& a) {
-        const int T = blockDim.x, tid = threadIdx.x;
-        const int nacc = (a.N + VEC - 1) / VEC;
-        C = a.cluster;
+// A thread's place: its columns, and how far its accesses lie apart.
+template <int VEC, int V, bool GROUP>
+struct DropPlace {
+    static constexpr int kRun = VEC == 1 ? 64 * V : 32 * V * VEC;  // columns of a warp's run
+    int unit;        // lanes that share sums by butterflies: those of a row, or a warp
+    int col, step;   // first column; columns from one access to the next
+    int nv;          // accesses that lie within the row; VEC 1: elements
+    int warps;       // warps of a CTA that share a row
+    int rank, C;
+    int64_t block, blocks_step;  // blocks of R rows: the first, from one to the next
+    bool first;                  // writes the row's statistics
+
+    __device__ __forceinline__ explicit DropPlace(const DropArgs& a) {
+        const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31;
+        C = GROUP ? 1 : a.cluster;
         rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
-        int64_t first_row;
-        if (a.lanes > 0) {
+        if constexpr (GROUP) {
             unit = a.lanes;
             warps = 1;
+            col = (tid & (unit - 1)) * VEC;
+            step = unit * VEC;
             const int teams = T / unit;
-            f0 = tid & (unit - 1);
-            step = unit;
-            first_row = static_cast<int64_t>(blockIdx.x) * teams;
-            row = first_row + tid / unit;
-            rows_step = static_cast<int64_t>(gridDim.x) * teams;
-            first = f0 == 0;
+            block = static_cast<int64_t>(blockIdx.x) * teams + tid / unit;
+            blocks_step = static_cast<int64_t>(gridDim.x) * teams;
+            first = col == 0;
         } else {
             unit = 32;
             warps = T >> 5;
-            f0 = (rank * T + (tid >> 5 << 5)) * V + (tid & 31);
-            step = 32;
-            first_row = row = blockIdx.x / C;
-            rows_step = gridDim.x / C;
+            col = (rank * warps + (tid >> 5)) * kRun + lane * VEC;
+            step = 32 * VEC;
+            block = blockIdx.x / C;
+            blocks_step = gridDim.x / C;
             first = rank == 0 && tid == 0;
         }
-        nv = f0 < nacc ? min(V, (nacc - f0 + step - 1) / step) : 0;
-        iters = first_row < a.M ? (a.M - first_row + rows_step - 1) / rows_step : 0;
+        nv = col < a.N ? min(VEC == 1 ? 2 * V : V, (a.N - col + step - 1) / step) : 0;
+    }
+    __device__ __forceinline__ bool on(int j) const { return (VEC == 1 ? 2 * j : j) < nv; }
+    // Columns from the first to access j (a constant but where lanes share rows).
+    __device__ __forceinline__ int at(int j) const { return VEC == 1 ? 64 * j : GROUP ? j * step : 32 * VEC * j; }
+    // Loads and stores of a row's access straight from memory; p: the first column's element.
+    template <class T>
+    __device__ __forceinline__ typename DropVec<T, VEC>::Raw load(const T* p, int j) const {
+        if constexpr (VEC == 1) {
+            using E = GnVec<T, 1>;
+            typename DropVec<T, 1>::Raw r = DropVec<T, 1>::zero();
+            if (2 * j < nv) r.lo = E::load(p + at(j));
+            if (2 * j + 1 < nv) r.hi = E::load(p + at(j) + 32);
+            return r;
+        } else {
+            return DropVec<T, VEC>::load(p + at(j));
+        }
+    }
+    template <class T>
+    __device__ __forceinline__ void store(T* p, int j, const typename DropVec<T, VEC>::Raw& r) const {
+        if constexpr (VEC == 1) {
+            using E = GnVec<T, 1>;
+            if (2 * j < nv) E::store(p + at(j), r.lo);
+            if (2 * j + 1 < nv) E::store(p + at(j) + 32, r.hi);
+        } else {
+            DropVec<T, VEC>::store(p + at(j), r);
+        }
+    }
+    // Elements of warp w of CTA k of the cluster.
+    static __device__ __forceinline__ float count(const DropArgs& a, int k, int w) {
+        const int at = (k * static_cast<int>(blockDim.x >> 5) + w) * kRun;
+        return static_cast<float>(max(0, min(a.N - at, kRun)));
+    }
+    static __device__ __forceinline__ float count_cta(const DropArgs& a, int k) {
+        const int run = static_cast<int>(blockDim.x >> 5) * kRun;
+        return static_cast<float>(max(0, min(a.N - k * run, run)));
     }
 };
 
 // ------------------------------------------------------------ sums
-// Two values per thread, over the row; every thread gets the same bits. One
-// barrier of the CTA per call (and one of the cluster); slots alternate by
-// `parity`, so that a slot is written again only after a barrier that every
-// reader of its last value has passed.
+// Sums of K values (1, 2, 4 or 8) over a warp, transposed on the way: lane l
+// ends with the sum of value l / (32 / K), the same in its whole block of
+// lanes. log2 K steps that halve the values, then single butterflies: 6
+// exchanges for 4 values instead of 20.
+template <int K>
+__device__ __forceinline__ float warp_sums(const float (&in)[K]) {
+    float v[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = in[k];
+    int off = 16;
+#pragma unroll
+    for (int n = K; n > 1; n /= 2, off /= 2) {
+        const bool up = (threadIdx.x & off) != 0;
+#pragma unroll
+        for (int k = 0; k < n / 2; ++k) {
+            const float keep = up ? v[k + n / 2] : v[k], give = up ? v[k] : v[k + n / 2];
+            v[k] = keep + __shfl_xor_sync(kFullMask, give, off);
+        }
+    }
+#pragma unroll
+    for (; off > 0; off /= 2) v[0] += __shfl_xor_sync(kFullMask, v[0], off);
+    return v[0];
+}
+
+// K values of each warp of a CTA, and of each CTA of a cluster; slots
+// alternate by parity, so that one is written again only after a barrier that
+// every reader of its last values has passed.
+template <int K>
 struct DropSums {
-    float2 warp[2][kDropMaxThreads / 32];
-    float2 cta[2];
+    float warp[2][K][kDropMaxThreads / 32];  // those of warps that are not there stay 0
+    float cta[2][K];
+    __device__ __forceinline__ void clear() {
+        for (int i = threadIdx.x; i < 2 * K * (kDropMaxThreads / 32); i += blockDim.x) (&warp[0][0][0])[i] = 0.f;
+        __syncthreads();
+    }
 };
 
-__device__ __forceinline__ float2 drop_peer(const float2* p, uint32_t rank) {
-    float2 v;
-    const uint32_t at = peer_smem_addr(p, rank);
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
-    return v;
-}
+__device__ __forceinline__ float drop_peer(const float* p, uint32_t rank) { return ld_peer_f32(peer_smem_addr(p, rank)); }
 
-__device__ __forceinline__ int drop_pow2(int n) {
-    int w = 1;
-    while (w < n) w <<= 1;
-    return w;
-}
-
-// Plain sums of both values.
-__device__ __forceinline__ float2 drop_sum(DropSums& sm, const DropPlace& p, int parity, float2 v) {
-    group_sum2(v.x, v.y, p.unit);
-    if (p.warps > 1) {
+// How the lanes of a warp share the K x 16 values of the warps: LPI lanes per
+// value, FPL of its warps each.
+template <int K>
+struct DropShare {
+    static constexpr int kLanes = K == 1 ? 16 : 32 / K;
+    static constexpr int kEach = (kDropMaxThreads / 32) / kLanes;
+    int idx, w0;
+    __device__ __forceinline__ DropShare() {
         const int lane = threadIdx.x & 31;
-        if (lane == 0) sm.warp[parity][threadIdx.x >> 5] = v;
+        idx = K == 1 ? 0 : lane / kLanes;
+        w0 = (lane & (kLanes - 1)) * kEach;
+    }
+};
+
+// Sums over the row of K values per thread; every thread gets all of them.
+template <int K, class P>
+__device__ __forceinline__ void drop_sum(DropSums<K>& sm, const P& p, int parity, float (&v)[K]) {
+    constexpr int L = 32 / K;
+    if (p.unit < 32) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = group_sum(v[k], p.unit);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    float s = warp_sums<K>(v);
+    int from = L;  // lanes between the values
+    if (p.warps > 1) {
+        if ((lane & (L - 1)) == 0) sm.warp[parity][lane / L][threadIdx.x >> 5] = s;
         __syncthreads();
-        v = lane < p.warps ? sm.warp[parity][lane] : make_float2(0.f, 0.f);
-        group_sum2(v.x, v.y, 16);  // (at most 16 warps: both halves have the sum of the first 16 lanes or of none)
-        v.x = __shfl_sync(kFullMask, v.x, 0);
-        v.y = __shfl_sync(kFullMask, v.y, 0);
+        const DropShare<K> sh;
+        const float* w = &sm.warp[parity][sh.idx][sh.w0];
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < DropShare<K>::kEach; ++i) s += w[i];
+#pragma unroll
+        for (int off = DropShare<K>::kLanes / 2; off > 0; off /= 2) s += __shfl_xor_sync(kFullMask, s, off);
+        from = DropShare<K>::kLanes;
     }
     if (p.C > 1) {
-        const int lane = threadIdx.x & 31;
-        if (threadIdx.x == 0) sm.cta[parity] = v;
+        // value idx of this CTA, then the CTAs' in rank order
+        if (threadIdx.x < 32 && (lane & (L - 1)) == 0) sm.cta[parity][lane / L] = s;
         cluster_barrier();
-        v = lane < p.C ? drop_peer(&sm.cta[parity], static_cast<uint32_t>(lane)) : make_float2(0.f, 0.f);
-        group_sum2(v.x, v.y, 8);
-        v.x = __shfl_sync(kFullMask, v.x, 0);
-        v.y = __shfl_sync(kFullMask, v.y, 0);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float t = lane < p.C ? drop_peer(&sm.cta[parity][k], static_cast<uint32_t>(lane)) : 0.f;
+            t = group_sum(t, 8);
+            v[k] = __shfl_sync(kFullMask, t, 0);
+        }
+        return;
     }
-    return v;
-}
-
-// The merge of states (n, sum, M2 about the state's own mean) of the lanes
-// [0, width), by the rule in its k-way form: mean = sum / n in all and
-// M2 = sum (M2_i + n_i (mean_i - mean)^2). Returns (sum, M2) in every lane.
-__device__ __forceinline__ float2 drop_merge(float n, float2 v, float inv_all, int width) {
-    const float total = __shfl_sync(kFullMask, group_sum(v.x, width), 0);
-    const float d = (n > 0.f ? v.x / n : 0.f) - total * inv_all;
-    const float m2 = __shfl_sync(kFullMask, group_sum(fmaf(n * d, d, v.y), width), 0);
-    return make_float2(total, m2);
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = __shfl_sync(kFullMask, s, K == 1 ? 0 : k * from);
 }
 
 // ------------------------------------------------------------ the ring
-// NS tensors' accesses of upcoming rows, each thread its own.
-template <class T, int VEC, int V, int NS>
+// NS tensors' accesses of upcoming blocks of R rows, each thread its own.
+template <class T, int VEC, int V, int R, int NS, class P>
 struct DropRing {
-    using X = GnVec<T, VEC>;
-    using Raw = typename X::Raw;
-    static constexpr int kBytes = VEC * static_cast<int>(sizeof(T));
-    static constexpr bool kAsync = kBytes >= 4;
-    static constexpr int kAccess = 32 * kBytes;
-    static constexpr int kStage = NS * V * kAccess;  // of a warp
-    const T* p[NS];      // this thread's first access of the next row to send (null: a tensor that is not there)
-    int64_t step;        // elements from one row to the next
-    int64_t left;        // rows not yet sent, this thread's
+    using Raw = typename DropVec<T, VEC>::Raw;
+    static constexpr int kStage = R * NS * V * 32 * 16;  // of a warp
+    const T* p[NS];      // this thread's first access of the next block to send (null: a tensor that is not there)
+    int64_t step;        // elements from one block to the next
+    int64_t rows;        // rows from the next block to send to the end
+    int64_t rows_step;
     uint32_t base, at_send, at_read, end;
-    int stages, nv, acc;  // acc: elements from one access to the next
-    Raw next[kAsync ? 1 : NS][kAsync ? 1 : V];
+    int stages, N;
 
-    __device__ __forceinline__ DropRing(const DropArgs& a, const DropPlace& pl, void* smem, const void* const (&from)[NS])
-        : stages(a.stages), nv(pl.nv), acc(pl.step * VEC) {
-        step = pl.rows_step * a.N;
-        left = pl.row < a.M ? (a.M - pl.row + pl.rows_step - 1) / pl.rows_step : 0;
+    __device__ __forceinline__ DropRing(const DropArgs& a, const P& pl, void* smem, const void* const (&from)[NS])
+        : stages(a.stages), N(a.N) {
+        rows_step = pl.blocks_step * R;
+        step = rows_step * a.N;
+        rows = a.M - pl.block * R;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) p[n] = from[n] ? static_cast<const T*>(from[n]) + pl.block * R * a.N + pl.col : nullptr;
+        base = smem_addr(smem) + (threadIdx.x >> 5) * stages * kStage + (threadIdx.x & 31) * 16;
+        end = base + stages * kStage;
+        at_send = at_read = base;
+        for (int i = 0; i < stages - 1; ++i) send(pl);
+    }
+    // Sends the next block; a group of copies is committed even when none is left.
+    __device__ __forceinline__ void send(const P& pl) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (r < rows) {
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    if (p[n]) {
+                        const T* q = p[n] + r * N;
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            if (pl.on(j)) copy_async<16>(at_send + ((r * NS + n) * V + j) * 512, q + pl.at(j));
+                    }
+            }
 #pragma unroll
         for (int n = 0; n < NS; ++n)
-            p[n] = from[n] ? static_cast<const T*>(from[n]) + pl.row * a.N + static_cast<int64_t>(pl.f0) * VEC : nullptr;
-        if constexpr (kAsync) {
-            base = smem_addr(smem) + (threadIdx.x >> 5) * stages * kStage + (threadIdx.x & 31) * kBytes;
-            end = base + stages * kStage;
-            at_send = at_read = base;
-            for (int i = 0; i < stages - 1; ++i) send();
-        } else {
-            send();
-        }
+            if (p[n]) p[n] += step;
+        rows -= rows_step;
+        copy_async_commit();
+        at_send = at_send + kStage == end ? base : at_send + kStage;
     }
-    // Sends (or loads) the next row; a group of copies is committed even when none is left.
-    __device__ __forceinline__ void send() {
-        if (left > 0) {
+    __device__ __forceinline__ void wait() const {
+        if (stages == 2) copy_async_wait<0>();
+        else if (stages == 3) copy_async_wait<1>();
+        else copy_async_wait<2>();
+    }
+    // Access j of tensor n of row r of the block that was waited for.
+    __device__ __forceinline__ Raw get(int r, int n, int j) const {
+        Raw v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(at_read + ((r * NS + n) * V + j) * 512)
+                     : "memory");
+        return v;
+    }
+    __device__ __forceinline__ void advance() { at_read = at_read + kStage == end ? base : at_read + kStage; }
+};
+
+// Rows of any width and offset: the CTA's part of a row of NS tensors, as the
+// aligned 16-byte chunks that hold it. A chunk starts no earlier than its
+// allocation does (those start on larger boundaries), and bytes behind the
+// part are not read. Rows are sent together, and read after a barrier that
+// follows every thread's wait for its copies.
+template <class T, int NS>
+struct DropStage {
+    static constexpr int kE = static_cast<int>(sizeof(T));
+    const char* p[NS];  // the CTA's first element of the first row, or null
+    int64_t rows_step, M, first;
+    int N, cols, pitch, stages;
+    uint32_t base;
+    char* smem;
+
+    __device__ __forceinline__ DropStage(const DropArgs& a, int64_t row, int64_t rows_step_, int c0, int cols_, char* smem_,
+                                         const void* const (&from)[NS])
+        : rows_step(rows_step_), M(a.M), first(row), N(a.N), cols(cols_), pitch(a.pitch), stages(a.stages), base(smem_addr(smem_)), smem(smem_) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) p[n] = from[n] ? static_cast<const char*>(from[n]) + static_cast<int64_t>(c0) * kE : nullptr;
+    }
+    __device__ __forceinline__ const char* row_of(int n, int64_t it) const { return p[n] + (first + it * rows_step) * N * kE; }
+    __device__ __forceinline__ int slot(int64_t it) const { return static_cast<int>(it % stages) * (NS * pitch); }
+    __device__ __forceinline__ void send(int64_t it) {
+        if (first + it * rows_step < M && cols > 0) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
                 if (p[n]) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        if (j < nv) {
-                            if constexpr (kAsync)
-                                copy_async<kBytes>(at_send + (n * V + j) * kAccess, p[n] + j * acc);
-                            else
-                                next[n][j] = X::load(p[n] + j * acc);
-                        }
-                    p[n] += step;
+                    const char* q = row_of(n, it);
+                    const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
+                    const int bytes = lead + cols * kE;
+                    const uint32_t to = base + slot(it) + n * pitch;
+                    for (int c = threadIdx.x * 16; c < bytes; c += blockDim.x * 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + c), "l"(q - lead + c), "r"(min(16, bytes - c)) : "memory");
                 }
-            --left;
         }
-        if constexpr (kAsync) {
-            copy_async_commit();
-            at_send = at_send + kStage == end ? base : at_send + kStage;
-        }
+        copy_async_commit();
     }
-    // Access j of tensor n of the row that was waited for.
-    __device__ __forceinline__ Raw get(int n, int j) const {
-        if constexpr (!kAsync) {
-            return next[n][j];
-        } else {
-            Raw r;
-            const uint32_t at = at_read + (n * V + j) * kAccess;
-            if constexpr (kBytes == 16)
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
-            else
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
-            return r;
-        }
+    // Where the CTA's first element of tensor n of a row lies in shared memory.
+    __device__ __forceinline__ const T* row(int n, int64_t it) const {
+        const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(row_of(n, it)) & 15);
+        return reinterpret_cast<const T*>(smem + slot(it) + n * pitch + lead);
     }
-    __device__ __forceinline__ void wait() const {
-        if constexpr (kAsync) {
-            if (stages == 2) copy_async_wait<0>();
-            else if (stages == 3) copy_async_wait<1>();
-            else copy_async_wait<2>();
-        }
-    }
-    // On to the next row: its slot is the one that `send` fills next but one.
-    __device__ __forceinline__ void advance() {
-        if constexpr (kAsync) at_read = at_read + kStage == end ? base : at_read + kStage;
+    template <class P>
+    static __device__ __forceinline__ typename DropVec<T, 1>::Raw get(const P& pl, const T* s, int j) {
+        return pl.load(s, j);
     }
 };
 
 // ------------------------------------------------------------ masks of a row
-// keep(j, i): whether pair i of elements of access j is kept, both of it.
-template <class T, int VEC, int V>
-struct DropRowMask {
-    const DropMask& m;
-    const bool on;
-    uint64_t group;   // VEC > 1: of the thread's first access; in halves for fp32 rows
-    int acc;          // accesses from one to the next
-    const unsigned short* words;  // VEC == 1: this thread's first element's word
+// The words of access j of a row: `group` is the generator's group of the
+// thread's first element (vectors of fp32: half groups).
+template <int VEC>
+struct DropWords {
     uint4 w;
-
-    __device__ __forceinline__ DropRowMask(const DropMask& m_, bool on_, const DropArgs& a, const DropPlace& p, int64_t row, uint4* smem)
-        : m(m_), on(on_), acc(p.step), words(nullptr) {
-        if constexpr (VEC > 1) {
-            group = static_cast<uint64_t>(row) * static_cast<uint32_t>(a.N / VEC) + static_cast<uint32_t>(p.f0);
-        } else if (on) {
-            // The words of the unit's columns, computed together: those of the
-            // last row are no longer read, and those of this one complete
-            // before they are.
-            const int u = threadIdx.x & (p.unit - 1), per = (p.unit * V + 7) / 8 + 2;
-            uint4* mine = smem + (threadIdx.x / p.unit) * per;
-            const int64_t e = row * a.N + (p.f0 - u);
-            const uint64_t g0 = static_cast<uint64_t>(e) >> 3;
-            __syncwarp();
-            for (int g = u; g < per; g += p.unit) mine[g] = m.words(g0 + g);
-            __syncwarp();
-            words = reinterpret_cast<const unsigned short*>(mine) + (e & 7) + u;
-        }
-    }
-    __device__ __forceinline__ void access(int j) {
-        if (!on) return;
-        if constexpr (VEC == 8) w = m.words(group + j * acc);
+    __device__ __forceinline__ void take(const DropMask& m, uint64_t group) {
+        if constexpr (VEC == 8) w = m.words(group);
         if constexpr (VEC == 4) {
-            const uint64_t g = group + j * acc;
-            const uint4 t = m.words(g >> 1);
-            w.x = (g & 1) ? t.z : t.x;
-            w.y = (g & 1) ? t.w : t.y;
+            const uint4 t = m.words(group >> 1);
+            w.x = (group & 1) ? t.z : t.x;
+            w.y = (group & 1) ? t.w : t.y;
         }
-        if constexpr (VEC == 1) w.x = words[j * acc];
     }
-    __device__ __forceinline__ bool lo(int i) const { return !on || m.low(drop_word(w, i)); }
-    __device__ __forceinline__ bool hi(int i) const { return VEC > 1 && (!on || m.high(drop_word(w, i))); }
+    // VEC 1: two elements' words
+    __device__ __forceinline__ void take(const unsigned short* s) { w.x = s[0] | static_cast<uint32_t>(s[32]) << 16; }
+    __device__ __forceinline__ bool lo(const DropMask& m, int i) const { return m.low(drop_word(w, i)); }
+    __device__ __forceinline__ bool hi(const DropMask& m, int i) const { return m.high(drop_word(w, i)); }
 };
+
+// The words of `cols` elements from flat element e on, by the CTA together;
+// element e + i's is word (e & 7) + i.
+__device__ __forceinline__ void drop_stage_words(const DropMask& m, uint64_t e, int cols, uint4* to) {
+    const uint64_t g0 = e >> 3;
+    const int n = static_cast<int>(((e + cols + 7) >> 3) - g0);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) to[i] = m.words(g0 + i);
+}
 
 // ------------------------------------------------------------ launch
 inline cudaError_t drop_resident(const void* fn, int threads, size_t smem, int cluster, int64_t* out) try {
