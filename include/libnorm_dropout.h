@@ -96,13 +96,14 @@ norm_status rms_bwd_add(const void* dy, const void* dh, const void* h, const voi
 
 /* The plan the calls would choose for M rows of N elements on a device with
  * `num_sms` SMs (fields of norm_plan: `mapping` NORM_MAP_GROUP with `group`
- * lanes of a warp per row, or NORM_MAP_CTA with `cluster` CTAs of `threads`
- * threads per row; `per_thread` accesses of `vec_elems` elements per thread
- * (vec_elems 1: of two elements), which cover the row; `rounds` rows at a time;
- * `stages` steps of them in shared memory, 2 to 4 (vec_elems 1: 3 or 4);
- * `grid` CTAs at most, persistent). `aligned16`: every pointer is 16-byte
- * aligned. Host only: makes no CUDA call. NORM_ERR_ARG for rows beyond the
- * limits. */
+ * lanes of a warp per row, or NORM_MAP_CTA with `cluster` CTAs per row, or
+ * teams of `group` threads of a CTA (0: all `threads` of it); `per_thread`
+ * accesses of `vec_elems` elements per thread (vec_elems 1: of two elements),
+ * which cover the row; `rounds` rows at a time; `stages` steps of them in
+ * shared memory, up to 4, from 2 in the forward on 16-byte vectors, from 3
+ * otherwise; `grid` CTAs at most, persistent). `aligned16`: every pointer is
+ * 16-byte aligned. Host only: makes no CUDA call. NORM_ERR_ARG for rows beyond
+ * the limits. */
 norm_status drop_make_plan(int64_t M, int64_t N, norm_dtype dtype, int layer_norm, int backward, int aligned16,
                            int num_sms, norm_plan* plan);
 

@@ -20,6 +20,7 @@ using libnorm::kDropMaxStages;
 using libnorm::kDropMaxThreads;
 
 constexpr int64_t kMaxN = 65536;
+constexpr int64_t kMaxElems = 32768;  // of rows that are not 16-byte aligned
 constexpr int64_t kMaxGrid = int64_t(1) << 20;
 constexpr int kMaxCluster = 8;
 
@@ -34,7 +35,6 @@ struct Shape {
     norm_dtype dtype;
     bool ln, bwd;
     int es() const { return elem_size(dtype); }
-    int streams() const { return bwd ? 3 : 2; }
 };
 
 norm_status check_shape(const Shape& s) {
@@ -45,20 +45,32 @@ norm_status check_shape(const Shape& s) {
 
 bool known(const Shape& s, bool group, int vec, int per, int rows) { return libnorm::drop_known(s.bwd, group, vec, s.es(), per, rows); }
 
-int64_t smem_bytes(const Shape& s, const norm_plan& p, int stages) {
-    return libnorm::drop_ring_bytes(p.vec_elems, s.es(), p.per_thread, p.threads, p.rounds, stages, s.streams()) +
-           libnorm::drop_words_bytes(p.vec_elems, p.per_thread, p.threads) +
-           (s.bwd && p.mapping == NORM_MAP_GROUP ? libnorm::drop_sums_bytes(s.ln, p.vec_elems, p.per_thread, p.threads) : 0);
+// Threads that share a row of a CTA.
+int team_of(const norm_plan& p) { return p.mapping == NORM_MAP_CTA && p.group > 0 ? p.group : p.threads; }
+
+int teams_of(const norm_plan& p) { return p.threads / (p.mapping == NORM_MAP_GROUP ? p.group : team_of(p)); }
+
+int stat_bytes(const Shape& s, const norm_plan& p) {
+    return libnorm::drop_stat_bytes(s.ln, s.bwd, p.vec_elems, p.mapping == NORM_MAP_GROUP ? p.group : 0, p.rounds);
 }
 
-norm_status make_plan(const Shape& s, bool aligned, int num_sms, norm_plan* p) {
+int64_t smem_bytes(const Shape& s, const norm_plan& p, int stages) {
+    return libnorm::drop_ring_bytes(p.vec_elems, s.es(), p.per_thread, p.threads, p.rounds, stages, s.bwd ? 3 : 2, stat_bytes(s, p)) +
+           libnorm::drop_words_bytes(p.vec_elems, p.per_thread, p.threads) +
+           (s.bwd && teams_of(p) > 1 ? libnorm::drop_sums_bytes(s.ln, p.vec_elems, p.per_thread, p.threads) : 0);
+}
+
+// Vectors, or pairs of elements, that a row touches.
+int64_t accesses(const Shape& s, int vec) { return vec == 1 ? ceil_div(s.N, 2) : libnorm::drop_vectors(s.N, vec); }
+
+norm_status plan_of(const Shape& s, int vec, int num_sms, norm_plan* p) {
     std::memset(p, 0, sizeof *p);
-    const int vec = aligned && s.N * s.es() % 16 == 0 ? 16 / s.es() : 1;
     const int least = vec == 1 ? 3 : 2;  // stages
+    if (vec == 1 && s.N > kMaxElems) return NORM_ERR_ARG;
     p->vec_elems = vec;
     p->cluster = 1;
-    int teams = 1;
-    const int64_t nacc = ceil_div(s.N, vec == 1 ? 2 : vec);
+    p->stages = least;
+    const int64_t nacc = accesses(s, vec);
     if (vec > 1 && nacc <= 64) {
         p->mapping = NORM_MAP_GROUP;
         p->per_thread = nacc <= 32 ? 1 : 2;
@@ -66,59 +78,69 @@ norm_status make_plan(const Shape& s, bool aligned, int num_sms, norm_plan* p) {
         while (p->group * p->per_thread < nacc) p->group *= 2;
         p->threads = 128;
         p->rounds = p->per_thread == 1 ? 4 : 2;
-        teams = p->threads / p->group;
+    } else if (vec > 1 && nacc <= kDropMaxThreads && s.M <= int64_t(num_sms) * 4) {
+        // few rows: one access per thread, one row at a time
+        p->mapping = NORM_MAP_CTA;
+        p->per_thread = 1;
+        p->rounds = 1;
+        p->threads = static_cast<int32_t>(round_up(nacc, 32));
     } else {
         p->mapping = NORM_MAP_CTA;
-        if (vec > 1 && nacc <= kDropMaxThreads && s.M <= int64_t(num_sms) * 4) {
-            // few rows: one access per thread, one row at a time
-            p->per_thread = 1;
-            p->rounds = 1;
-            p->threads = static_cast<int32_t>(round_up(nacc, 32));
-        } else {
-            // the smallest cluster, then the fewest accesses per thread, then the most rows whose stages fit
-            bool found = false;
-            for (int c = 1; c <= kMaxCluster && !found; c *= 2)
-                for (int per : {1, 2, 4, 8}) {
-                    if (found || (vec == 1 && per == 2 && nacc > 64)) continue;
-                    const int64_t threads = round_up(ceil_div(nacc, int64_t(c) * per), 32);
-                    if (threads > kDropMaxThreads || (per == 1 && threads > 128)) continue;
-                    for (int rows : {4, 2, 1}) {
-                        if (found || !known(s, false, vec, per, rows)) continue;
-                        p->cluster = c;
-                        p->per_thread = per;
-                        p->rounds = rows;
-                        p->threads = static_cast<int32_t>(threads);
-                        found = smem_bytes(s, *p, least) <= kDropMaxSmem;
-                    }
-                }
-            if (!found) return NORM_ERR_ARG;
+        // the smallest cluster whose CTAs' stages fit
+        int per = vec == 1 ? 8 : s.bwd && s.es() == 2 ? 2 : 4;
+        if (vec > 1 && nacc < per * 32) per = 1;
+        p->per_thread = per;
+        bool found = false;
+        for (p->cluster = 1; p->cluster <= kMaxCluster; p->cluster *= 2) {
+            const int64_t threads = round_up(ceil_div(nacc, int64_t(p->cluster) * per), 32);
+            if (threads > libnorm::drop_max_threads(vec, per)) continue;
+            p->threads = static_cast<int32_t>(threads);
+            for (int rows : {4, 2, 1}) {
+                if (found || !known(s, false, vec, per, rows)) continue;
+                p->rounds = rows;
+                found = smem_bytes(s, *p, least) <= kDropMaxSmem;
+            }
+            if (found) break;
         }
+        if (!found) return NORM_ERR_ARG;
+        while (s.bwd && p->stages < 3 && smem_bytes(s, *p, p->stages + 1) <= kDropMaxSmem) ++p->stages;
     }
-    // as many stages as leave room for the CTAs that registers allow
-    const int64_t ctas = std::max<int64_t>(1, 512 / p->threads);
-    p->stages = kDropMaxStages;
-    while (p->stages > least && smem_bytes(s, *p, p->stages) * ctas > kDropMaxSmem) --p->stages;
     const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(16, 1024 / p->threads));
-    p->grid = std::max<int64_t>(1, std::min<int64_t>(ceil_div(s.M, int64_t(teams) * p->rounds), std::max<int64_t>(1, num_sms * per_sm / p->cluster))) * p->cluster;
+    const int teams = teams_of(*p), unit = libnorm::drop_grid_unit(libnorm::drop_phases(s.N, vec), teams);
+    const int64_t wanted = std::min<int64_t>(ceil_div(s.M, int64_t(teams) * p->rounds), num_sms * per_sm / p->cluster);
+    p->grid = std::max<int64_t>(1, ceil_div(wanted, unit)) * unit * p->cluster;
     return NORM_OK;
+}
+
+norm_status make_plan(const Shape& s, bool aligned, int num_sms, norm_plan* p) {
+    if (aligned) {
+        const norm_status st = plan_of(s, 16 / s.es(), num_sms, p);
+        if (st == NORM_OK) return st;
+    }
+    return plan_of(s, 1, num_sms, p);
 }
 
 norm_status check_plan(const norm_plan& p, const Shape& s, bool aligned) {
     const int es = s.es();
-    if (p.vec_elems != 1 && (p.vec_elems != 16 / es || !aligned || s.N * es % 16 != 0)) return NORM_ERR_PLAN;
+    if (p.vec_elems != 1 && (p.vec_elems != 16 / es || !aligned)) return NORM_ERR_PLAN;
+    if (p.vec_elems == 1 && s.N > kMaxElems) return NORM_ERR_PLAN;
     if (p.mapping != NORM_MAP_GROUP && p.mapping != NORM_MAP_CTA) return NORM_ERR_PLAN;
     if (!known(s, p.mapping == NORM_MAP_GROUP, p.vec_elems, p.per_thread, p.rounds)) return NORM_ERR_PLAN;
-    if (p.threads < 32 || p.threads > kDropMaxThreads || p.threads % 32 != 0) return NORM_ERR_PLAN;
-    const int64_t nacc = ceil_div(s.N, p.vec_elems == 1 ? 2 : p.vec_elems);
+    if (p.threads < 32 || p.threads > libnorm::drop_max_threads(p.vec_elems, p.per_thread) || p.threads % 32 != 0) return NORM_ERR_PLAN;
+    const int64_t nacc = accesses(s, p.vec_elems);
     if (p.mapping == NORM_MAP_GROUP) {
         if (!is_pow2(p.group) || p.group > 32 || int64_t(p.group) * p.per_thread < nacc || p.cluster != 1) return NORM_ERR_PLAN;
     } else {
         if (!is_pow2(p.cluster) || p.cluster > kMaxCluster) return NORM_ERR_PLAN;
-        if (int64_t(p.cluster) * p.threads * p.per_thread < nacc) return NORM_ERR_PLAN;
+        const int team = team_of(p);
+        if (team < 32 || team % 32 != 0 || p.threads % team != 0) return NORM_ERR_PLAN;
+        if (team < p.threads && (p.cluster > 1 || p.vec_elems == 1)) return NORM_ERR_PLAN;
+        if (int64_t(p.cluster) * team * p.per_thread < nacc) return NORM_ERR_PLAN;
     }
     if (p.stages < (p.vec_elems == 1 ? 3 : 2) || p.stages > kDropMaxStages) return NORM_ERR_PLAN;
     if (smem_bytes(s, p, p.stages) > kDropMaxSmem) return NORM_ERR_PLAN;
-    if (p.grid < p.cluster || p.grid > kMaxGrid || p.grid % p.cluster != 0) return NORM_ERR_PLAN;
+    const int unit = p.cluster * libnorm::drop_grid_unit(libnorm::drop_phases(s.N, p.vec_elems), teams_of(p));
+    if (p.grid < unit || p.grid > kMaxGrid || p.grid % unit != 0) return NORM_ERR_PLAN;
     return NORM_OK;
 }
 
@@ -180,8 +202,11 @@ norm_status settle(const Shape& s, bool aligned, const norm_plan* plan, norm_pla
     a->N = static_cast<int32_t>(s.N);
     a->invN = 1.f / static_cast<float>(s.N);
     a->lanes = p->mapping == NORM_MAP_GROUP ? p->group : 0;
+    a->team = team_of(*p);
     a->cluster = p->cluster;
     a->stages = p->stages;
+    a->phases = libnorm::drop_phases(s.N, p->vec_elems);
+    a->stat_bytes = stat_bytes(s, *p);
     return NORM_OK;
 }
 
