@@ -57,6 +57,7 @@ int stat_bytes(const Shape& s, const norm_plan& p) {
 int64_t smem_bytes(const Shape& s, const norm_plan& p, int stages) {
     return libnorm::drop_ring_bytes(p.vec_elems, s.es(), p.per_thread, p.threads, p.rounds, stages, s.bwd ? 3 : 2, stat_bytes(s, p)) +
            libnorm::drop_words_bytes(p.vec_elems, p.per_thread, p.threads) +
+           (s.bwd ? 0 : libnorm::drop_param_bytes(s.ln, p.vec_elems, p.per_thread, p.threads)) +
            (s.bwd && teams_of(p) > 1 ? libnorm::drop_sums_bytes(s.ln, p.vec_elems, p.per_thread, p.threads) : 0);
 }
 
@@ -65,50 +66,60 @@ int64_t accesses(const Shape& s, int vec) { return vec == 1 ? ceil_div(s.N, 2) :
 
 norm_status plan_of(const Shape& s, int vec, int num_sms, norm_plan* p) {
     std::memset(p, 0, sizeof *p);
-    const int least = vec == 1 ? 3 : 2;  // stages
     if (vec == 1 && s.N > kMaxElems) return NORM_ERR_ARG;
     p->vec_elems = vec;
     p->cluster = 1;
-    p->stages = least;
+    p->stages = vec == 1 ? 3 : 2;
     const int64_t nacc = accesses(s, vec);
-    if (vec > 1 && nacc <= 64) {
+    if (vec > 1 && nacc <= (s.bwd ? 16 : 64)) {
         p->mapping = NORM_MAP_GROUP;
-        p->per_thread = nacc <= 32 ? 1 : 2;
+        p->per_thread = 2;
         p->group = 1;
-        while (p->group * p->per_thread < nacc) p->group *= 2;
+        while (p->group * 2 < nacc) p->group *= 2;
         p->threads = 128;
-        p->rounds = p->per_thread == 1 ? 4 : 2;
-    } else if (vec > 1 && nacc <= kDropMaxThreads && s.M <= int64_t(num_sms) * 4) {
-        // few rows: one access per thread, one row at a time
+        p->rounds = 2;
+    } else if (vec > 1 && nacc <= kDropMaxThreads && (s.bwd || nacc < 128 || s.M <= int64_t(num_sms) * 4)) {
         p->mapping = NORM_MAP_CTA;
         p->per_thread = 1;
-        p->rounds = 1;
+        p->rounds = !s.bwd && s.M <= int64_t(num_sms) * 4 ? 1 : 4;
         p->threads = static_cast<int32_t>(round_up(nacc, 32));
     } else {
         p->mapping = NORM_MAP_CTA;
-        // the smallest cluster whose CTAs' stages fit
-        int per = vec == 1 ? 8 : s.bwd && s.es() == 2 ? 2 : 4;
-        if (vec > 1 && nacc < per * 32) per = 1;
+        const int per = vec == 1 ? 8 : s.bwd && s.es() == 2 ? 2 : 4;
         p->per_thread = per;
-        bool found = false;
-        for (p->cluster = 1; p->cluster <= kMaxCluster; p->cluster *= 2) {
-            const int64_t threads = round_up(ceil_div(nacc, int64_t(p->cluster) * per), 32);
-            if (threads > libnorm::drop_max_threads(vec, per)) continue;
-            p->threads = static_cast<int32_t>(threads);
-            for (int rows : {4, 2, 1}) {
-                if (found || !known(s, false, vec, per, rows)) continue;
-                p->rounds = rows;
-                found = smem_bytes(s, *p, least) <= kDropMaxSmem;
-            }
-            if (found) break;
+        p->rounds = per == 2 ? 2 : 1;
+        // the smallest cluster whose CTAs' stages fit
+        for (;; p->cluster *= 2) {
+            if (p->cluster > kMaxCluster) return NORM_ERR_ARG;
+            p->threads = static_cast<int32_t>(round_up(ceil_div(nacc, int64_t(p->cluster) * per), 32));
+            if (p->threads <= libnorm::drop_max_threads(vec, per) && smem_bytes(s, *p, p->stages) <= kDropMaxSmem) break;
         }
-        if (!found) return NORM_ERR_ARG;
-        while (s.bwd && p->stages < 3 && smem_bytes(s, *p, p->stages + 1) <= kDropMaxSmem) ++p->stages;
     }
-    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(16, 1024 / p->threads));
+    int64_t per_sm = s.bwd ? 512 : 1024;  // threads
+    const int64_t steps = ceil_div(s.M, p->rounds);
+    if (p->mapping == NORM_MAP_CTA && vec > 1 && p->cluster == 1) {
+        const int most = s.bwd ? kDropMaxThreads : 128;
+        const int32_t team = p->threads;
+        int64_t teams = std::min<int64_t>(most / team, ceil_div(steps, num_sms));
+        for (; teams > 1; --teams) {
+            p->group = team;
+            p->threads = static_cast<int32_t>(team * teams);
+            if (smem_bytes(s, *p, p->stages) <= kDropMaxSmem) break;
+        }
+        if (teams <= 1) {
+            p->group = 0;
+            p->threads = team;
+        }
+        if (!s.bwd && p->per_thread == 4 && p->threads <= 128) {
+            p->stages = 3;
+            per_sm = s.ln ? 512 : 256;
+        }
+    }
     const int teams = teams_of(*p), unit = libnorm::drop_grid_unit(libnorm::drop_phases(s.N, vec), teams);
-    const int64_t wanted = std::min<int64_t>(ceil_div(s.M, int64_t(teams) * p->rounds), num_sms * per_sm / p->cluster);
+    const int64_t wanted = std::min<int64_t>(ceil_div(steps, teams), num_sms * std::max<int64_t>(1, per_sm / p->threads) / p->cluster);
     p->grid = std::max<int64_t>(1, ceil_div(wanted, unit)) * unit * p->cluster;
+    // few rows forward: every SM the same number of CTAs
+    if (!s.bwd && p->per_thread == 1 && p->rounds == 1) p->grid = round_up(round_up(p->grid, num_sms), unit);
     return NORM_OK;
 }
 
@@ -144,7 +155,7 @@ norm_status check_plan(const norm_plan& p, const Shape& s, bool aligned) {
     return NORM_OK;
 }
 
-int64_t workspace_bytes(const Shape& s, const norm_plan& p) { return p.grid / p.cluster * (s.ln ? 2 : 1) * s.N * 4; }
+int64_t workspace_bytes(const Shape& s, const norm_plan& p) { return p.grid / p.cluster * libnorm::drop_partial_pitch(static_cast<int32_t>((s.ln ? 2 : 1) * s.N)) * 4; }
 
 norm_status done(cudaError_t e) {
     if (e == cudaSuccess) return NORM_OK;

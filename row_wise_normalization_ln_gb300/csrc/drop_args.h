@@ -22,7 +22,7 @@ struct DropArgs {
     void *h, *y;                    // forward
     void *dx, *dres;                // backward; dx: null without dropout
     float *mean, *rstd;             // written by the forward, read by the backward (LayerNorm)
-    float* ws;                      // backward: partial rows [partials][NA][N]
+    float* ws;                      // backward: partial rows [partials][partial_pitch]
     float *dgamma, *dbeta;
     const uint64_t* rng;            // seed, offset in device memory, or null:
     uint64_t seed, offset;
@@ -31,6 +31,7 @@ struct DropArgs {
     int32_t lanes;                  // lanes of a warp per row; 0: a team of warps or a cluster
     int32_t team;                   // threads of a team
     int32_t cluster;
+    int32_t partial_pitch;
     int32_t phases;                 // rows after which one begins at the same place of a 16-byte vector
     int32_t stat_bytes;             // means and rstds of a warp's rows of a step
     int32_t stages;
@@ -46,9 +47,9 @@ struct DropArgs {
 inline bool drop_known(bool backward, bool group, int vec, int elem, int per_thread, int rows) {
     if (vec == 1) return !group && rows == 1 && per_thread == 8;
     if (vec * elem != 16) return false;
-    if (group) return (per_thread == 1 && rows == 4) || (per_thread == 2 && rows == 2);
-    if (per_thread == 1) return rows == 1 || rows == 4;
-    return elem == 2 && backward ? per_thread == 2 && rows <= 2 : per_thread == 4 && rows == 1;
+    if (group) return per_thread == 2 && rows == 2;
+    if (per_thread == 1) return rows == 4 || (rows == 1 && !backward);
+    return elem == 2 && backward ? per_thread == 2 && rows == 2 : per_thread == 4 && rows == 1;
 }
 
 // Threads of a CTA, at most: what 32 values of a thread need in registers
@@ -79,7 +80,8 @@ inline int64_t drop_cta_cols(int vec, int per_thread, int threads) { return int6
 // Shared memory of the stages: of each thread's own accesses (and, `stats`
 // bytes a warp, the rows' statistics), or of the CTA's part of a row of
 // elements in whole 16-byte chunks at a pitch; of the masks' words of two rows
-// of elements; and of the backward's column sums of a CTA of several teams.
+// of elements; of parameters; and of the backward's column sums of a CTA of
+// several teams.
 inline int64_t drop_pitch(int elem, int per_thread, int threads) { return (drop_cta_cols(1, per_thread, threads) * elem + 30) / 16 * 16; }
 inline int64_t drop_ring_bytes(int vec, int elem, int per_thread, int threads, int rows, int stages, int streams, int stats) {
     return vec == 1 ? stages * streams * drop_pitch(elem, per_thread, threads)
@@ -91,9 +93,15 @@ inline int drop_stat_bytes(bool ln, bool bwd, int vec, int lanes, int rows) {
 inline int64_t drop_words_bytes(int vec, int per_thread, int threads) {
     return vec == 1 ? 2 * 16 * (drop_cta_cols(1, per_thread, threads) / 8 + 2) : 0;
 }
+inline int64_t drop_param_bytes(bool ln, int vec, int per_thread, int threads) {  // forward
+    return ln && vec > 1 && per_thread == 4 ? int64_t(2) * per_thread * threads * 16 : 0;
+}
 inline int64_t drop_sums_bytes(bool ln, int vec, int per_thread, int threads) {
     return int64_t(ln ? 2 : 1) * vec * per_thread * threads * 4;
 }
+
+// Floats from one partial row of column sums to the next.
+inline int32_t drop_partial_pitch(int32_t values) { return (values + 3) / 4 * 4; }
 
 cudaError_t launch_drop_fwd_f32(const norm_plan& p, DropArgs& a, bool ln, cudaStream_t s);
 cudaError_t launch_drop_fwd_bf16(const norm_plan& p, DropArgs& a, bool ln, cudaStream_t s);

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
             for (int i = 0; i < H; ++i) acc[k][j][i] = make_float2(0.f, 0.f);
     // Where the sums of chains go: this thread's columns of the CTA's (or
     // cluster's) partial row, or its slots of shared memory.
-    float* const part = a.ws + static_cast<int64_t>(blockIdx.x / pl.C) * NA * a.N;
+    float* const part = a.ws + static_cast<int64_t>(blockIdx.x / pl.C) * a.partial_pitch;
     float* const shared_cols = reinterpret_cast<float*>(smem + a.sums_at);
     const int team_size = GROUP ? a.lanes : a.team;
     const bool teams = VEC > 1 && static_cast<int>(blockDim.x) > team_size;
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
         else return ring.stat(pl, r);
     };
     const auto read = [&](auto whole, int r, int n, int j) {
-        constexpr bool FULL = decltype(whole)::value;
+        [[maybe_unused]] constexpr bool FULL = decltype(whole)::value;
         if constexpr (kElems) return ring.template get<FULL>(ring.row(n) + in * sizeof(T), j, pl.nv);
         else return ring.get(r, n, j);
     };
@@ -133,9 +133,8 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                                 s0 = __fadd2_rn(s0, g);
                                 s1 = __ffma2_rn(g, X::plus(hr, i, -mean), s1);
                             } else {
-                                const float2 hv = X::get(hr, i);
-                                s0 = __ffma2_rn(hv, hv, s0);
-                                s1 = __ffma2_rn(g, hv, s1);
+                                s0 = X::fma(hr, hr, i, s0);
+                                s1 = __ffma2_rn(g, X::get(hr, i), s1);
                             }
                         }
                     }
@@ -272,6 +271,7 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
 template <class T, int VEC, int V, int R, bool LN, bool GROUP>
 cudaError_t drop_launch_bwd(const norm_plan& p, DropArgs& a, cudaStream_t s) {
     const void* fn = reinterpret_cast<const void*>(drop_bwd<T, VEC, V, R, LN, GROUP>);
+    a.partial_pitch = drop_partial_pitch((LN ? 2 : 1) * a.N);
     a.pitch = static_cast<int32_t>(VEC == 1 ? drop_pitch(sizeof(T), V, p.threads) : 0);
     a.words_at = static_cast<int32_t>(drop_ring_bytes(VEC, sizeof(T), V, p.threads, R, a.stages, 3, a.stat_bytes));
     a.sums_at = static_cast<int32_t>(a.words_at + drop_words_bytes(VEC, V, p.threads));
@@ -290,17 +290,12 @@ cudaError_t drop_launch_bwd(const norm_plan& p, DropArgs& a, cudaStream_t s) {
 template <class T, bool LN>
 cudaError_t drop_bwd_of(const norm_plan& p, DropArgs& a, cudaStream_t s) {
     constexpr int full = 16 / sizeof(T);
-    const int V = p.per_thread, R = p.rounds;
+    const int V = p.per_thread;
     if (p.vec_elems == 1) return drop_launch_bwd<T, 1, 8, 1, LN, false>(p, a, s);
-    if (p.mapping == NORM_MAP_GROUP) {
-        if (V == 1) return drop_launch_bwd<T, full, 1, 4, LN, true>(p, a, s);
-        return drop_launch_bwd<T, full, 2, 2, LN, true>(p, a, s);
-    }
-    if (V == 1) return R == 1 ? drop_launch_bwd<T, full, 1, 1, LN, false>(p, a, s) : drop_launch_bwd<T, full, 1, 4, LN, false>(p, a, s);
-    if constexpr (sizeof(T) == 4)
-        return drop_launch_bwd<T, full, 4, 1, LN, false>(p, a, s);
-    else
-        return R == 1 ? drop_launch_bwd<T, full, 2, 1, LN, false>(p, a, s) : drop_launch_bwd<T, full, 2, 2, LN, false>(p, a, s);
+    if (p.mapping == NORM_MAP_GROUP) return drop_launch_bwd<T, full, 2, 2, LN, true>(p, a, s);
+    if (V == 1) return drop_launch_bwd<T, full, 1, 4, LN, false>(p, a, s);
+    if constexpr (sizeof(T) == 4) return drop_launch_bwd<T, full, 4, 1, LN, false>(p, a, s);
+    else return drop_launch_bwd<T, full, 2, 2, LN, false>(p, a, s);
 }
 
 template <class T>

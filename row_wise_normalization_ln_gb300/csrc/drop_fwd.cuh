@@ -1,14 +1,15 @@
 // Dropout, residual add and norm, forward:
 //   h = residual + x keep / P(keep)  (rounded to the row's type),  y = norm(h).
 //
-// A thread holds its values of R rows as fp32 pairs from the add to the
+// A thread holds its values of R rows, as they are stored, from the add to the
 // output. LayerNorm: a warp's values are shifted by its first one, K (a mean
-// that dwarfs the spread costs no digits), its mean and M2 formed in two
-// passes over the registers, and the warps' states (n, K + mean, M2) meet
-// behind one barrier by the merge rule in its k-way form, the means as
-// differences from the first warp's K:
+// that dwarfs the spread costs the statistics no digits), its mean and M2
+// formed in two passes over the registers, and the warps' states
+// (n, K + mean, M2) meet behind one barrier by the merge rule in its k-way
+// form, the means as differences from the first warp's K:
 //   m_w = (K_w - K_0) + mean_w,  mean = sum n_w m_w / N,  M2 = sum M2_w + n_w (m_w - mean)^2.
-// RMSNorm: sums of squares.
+// (The second pass takes differences from K + mean rounded, whose error counts
+// in the square alone.) RMSNorm: sums of squares.
 #pragma once
 
 #include "drop_kernels.cuh"
@@ -70,16 +71,35 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
         if constexpr (kElems) ring.send();
         else ring.send(a, pl, from, row + i * rows_step);
     row_words(0, row);
-    Raw gv[V], bv[LN ? V : 1];
+    // The parameters of the thread's columns: in registers, or, LayerNorm's of 32
+    // columns (32 registers of 128), in shared memory.
+    constexpr bool kAside = LN && VEC > 1 && V == 4;
+    Raw params[kAside ? 1 : V][LN ? 2 : 1];
+    const uint32_t aside = words_at + threadIdx.x * 16;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        gv[j] = X::zero();
-        if (pl.on(j)) gv[j] = pl.param(static_cast<const T*>(a.gamma), j);
-        if constexpr (LN) {
-            bv[j] = X::zero();
-            if (pl.on(j)) bv[j] = pl.param(static_cast<const T*>(a.beta), j);
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int k = 0; k < (LN ? 2 : 1); ++k) {
+            Raw v = X::zero();
+            if (pl.on(j)) v = pl.param(static_cast<const T*>(k == 0 ? a.gamma : a.beta), j);
+            if constexpr (kAside) {
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(aside + (2 * j + k) * blockDim.x * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+            } else {
+                params[j][k] = v;
+            }
         }
-    }
+    const auto param = [&](int j, int k) {
+        if constexpr (kAside) {
+            Raw v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(aside + (2 * j + k) * blockDim.x * 16)
+                         : "memory");
+            return v;
+        } else {
+            return params[j][k];
+        }
+    };
     // LayerNorm: elements of this warp's part, of the warps whose states this
     // lane merges, of the CTA's.
     const DropShare<R> sh;
@@ -105,7 +125,7 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
     for (; first < a.M; first += rows_step, row += rows_step, parity ^= 1) {
         const int64_t at = row * a.N + pl.col;  // the thread's first element of the step's first row
         const uint64_t group = VEC > 1 ? static_cast<uint64_t>(at) / VEC : 0;
-        float2 d[R][V][H];
+        Raw h[R][V];
         float s[R];
         if constexpr (!kElems) {
             ring.wait();
@@ -129,10 +149,7 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    if (!FULL) {
-#pragma unroll
-                        for (int i = 0; i < H; ++i) d[r][j][i] = make_float2(0.f, 0.f);
-                    }
+                    if (!FULL) h[r][j] = X::zero();
                     if (FULL || (on && (!kElems || pl.on(j)))) {
                         Raw xr, rr, hr = X::zero();
                         if constexpr (kElems) {
@@ -156,10 +173,10 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                             X::set(hr, i, hv);
                         }
                         pl.template store<FULL>(hp, j, hr);
+                        h[r][j] = hr;
+                        if (!LN) {
 #pragma unroll
-                        for (int i = 0; i < H; ++i) {
-                            d[r][j][i] = X::get(hr, i);
-                            if (!LN) sum = __ffma2_rn(d[r][j][i], d[r][j][i], sum);
+                            for (int i = 0; i < H; ++i) sum = X::fma(hr, hr, i, sum);
                         }
                     }
                 }
@@ -179,50 +196,17 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
         float rstd[R], mu[R];
         if constexpr (LN) {
             float K[R], K0[R], mean[R], q[R];
-            // Differences from K, and their sums.
-            const auto shift = [&](auto whole) {
+            // The sum of the differences from c[r], or of their squares.
+            const auto differences = [&](auto whole, auto square, const float (&c)[R], float (&out)[R]) {
                 constexpr bool FULL = decltype(whole)::value;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    // the first value of the warp's part (of a row that begins within a vector: the row's first)
-                    K[r] = d[r][0][0].x;
-                    if (!FULL && VEC > 1) {
-#pragma unroll
-                        for (int e = 1; e < VEC; ++e)
-                            if (pl.col == -e) K[r] = e & 1 ? d[r][0][e / 2].y : d[r][0][e / 2].x;
-                    }
-                    K[r] = __shfl_sync(kFullMask, K[r], GROUP ? lane & ~(pl.unit - 1) : 0);
-                    const float2 k2 = f2_splat(-K[r]);
-                    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-#pragma unroll
-                        for (int i = 0; i < H; ++i) d[r][j][i] = __fadd2_rn(d[r][j][i], k2);
-                        if (!FULL && (kElems || !pl.whole(j))) {
-#pragma unroll
-                            for (int i = 0; i < H; ++i) {
-                                if (!pl.valid(j, 2 * i)) d[r][j][i].x = 0.f;
-                                if (!pl.valid(j, 2 * i + 1)) d[r][j][i].y = 0.f;
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < H; ++i) sum = __fadd2_rn(sum, d[r][j][i]);
-                    }
-                    s[r] = sum.x + sum.y;
-                }
-            };
-            // Squares about the mean.
-            const auto squares = [&](auto whole) {
-                constexpr bool FULL = decltype(whole)::value;
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float2 nm = f2_splat(-mean[r]);
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         float2 e[H];
 #pragma unroll
-                        for (int i = 0; i < H; ++i) e[i] = __fadd2_rn(d[r][j][i], nm);
+                        for (int i = 0; i < H; ++i) e[i] = X::plus(h[r][j], i, -c[r]);
                         if (!FULL && (kElems || !pl.whole(j))) {
 #pragma unroll
                             for (int i = 0; i < H; ++i) {
@@ -231,14 +215,25 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < H; ++i) sum = __ffma2_rn(e[i], e[i], sum);
+                        for (int i = 0; i < H; ++i) sum = decltype(square)::value ? __ffma2_rn(e[i], e[i], sum) : __fadd2_rn(sum, e[i]);
                     }
-                    q[r] = sum.x + sum.y;
-                    K0[r] = K[r];
+                    out[r] = sum.x + sum.y;
                 }
             };
-            if (full) shift(std::true_type{});
-            else shift(std::false_type{});
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                // the first value of the warp's part (of a row that begins within a vector: the row's first)
+                K[r] = X::get(h[r][0], 0).x;
+                if (VEC > 1 && pl.col < 0) {
+#pragma unroll
+                    for (int e = 1; e < VEC; ++e)
+                        if (pl.col == -e) K[r] = e & 1 ? X::get(h[r][0], e / 2).y : X::get(h[r][0], e / 2).x;
+                }
+                K[r] = __shfl_sync(kFullMask, K[r], GROUP ? lane & ~(pl.unit - 1) : 0);
+                K0[r] = K[r];
+            }
+            if (full) differences(std::true_type{}, std::false_type{}, K, s);
+            else differences(std::false_type{}, std::false_type{}, K, s);
             if (GROUP) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) mean[r] = group_sum(s[r], pl.unit) * inv_warp;
@@ -247,8 +242,11 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
 #pragma unroll
                 for (int r = 0; r < R; ++r) mean[r] = __shfl_sync(kFullMask, t, R == 1 ? 0 : r * (32 / R)) * inv_warp;
             }
-            if (full) squares(std::true_type{});
-            else squares(std::false_type{});
+            float about[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) about[r] = K[r] + mean[r];
+            if (full) differences(std::true_type{}, std::true_type{}, about, q);
+            else differences(std::false_type{}, std::true_type{}, about, q);
             if (GROUP) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) q[r] = group_sum(q[r], pl.unit);
@@ -311,6 +309,12 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                 } else {
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
+                        if (R == 1) {  // (every lane has the row's)
+                            mean[r] = m;
+                            q[r] = m2;
+                            K0[r] = k;
+                            continue;
+                        }
                         mean[r] = __shfl_sync(kFullMask, m, r * S);
                         q[r] = __shfl_sync(kFullMask, m2, r * S);
                         K0[r] = __shfl_sync(kFullMask, k, r * S);
@@ -320,9 +324,9 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 rstd[r] = rsqrtf(fmaf(q[r], a.invN, a.eps));
-                mu[r] = mean[r] - (K[r] - K0[r]);  // from this warp's K
+                mu[r] = K0[r] + mean[r];
                 if (has(r) && pl.first) {
-                    if (a.mean) a.mean[row + r * pl.stride] = K0[r] + mean[r];
+                    if (a.mean) a.mean[row + r * pl.stride] = mu[r];
                     if (a.rstd) a.rstd[row + r * pl.stride] = rstd[r];
                 }
             }
@@ -340,18 +344,21 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
             constexpr bool FULL = decltype(whole)::value;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float2 rs2 = f2_splat(rstd[r]), nmr = f2_splat(LN ? -mu[r] * rstd[r] : 0.f);
+                const float2 rs2 = f2_splat(rstd[r]);
                 T* const yp = static_cast<T*>(a.y) + at + r * row_step;
 #pragma unroll
                 for (int j = 0; j < V; ++j)
                     if (FULL || (has(r) && (!kElems || pl.on(j)))) {
                         Raw yr = X::zero();
+                        const Raw gv = param(j, 0);
+                        [[maybe_unused]] Raw bv;
+                        if constexpr (LN) bv = param(j, 1);
 #pragma unroll
                         for (int i = 0; i < H; ++i) {
                             if constexpr (LN)
-                                X::set(yr, i, __ffma2_rn(__ffma2_rn(d[r][j][i], rs2, nmr), X::get(gv[j], i), X::get(bv[j], i)));
+                                X::set(yr, i, __ffma2_rn(__fmul2_rn(X::plus(h[r][j], i, -mu[r]), rs2), X::get(gv, i), X::get(bv, i)));
                             else
-                                X::set(yr, i, __fmul2_rn(__fmul2_rn(d[r][j][i], X::get(gv[j], i)), rs2));
+                                X::set(yr, i, __fmul2_rn(X::mul(h[r][j], gv, i), rs2));
                         }
                         pl.template store<FULL>(yp, j, yr);
                     }
@@ -368,7 +375,7 @@ cudaError_t drop_launch_fwd(const norm_plan& p, DropArgs& a, cudaStream_t s) {
     const void* fn = reinterpret_cast<const void*>(drop_fwd<T, VEC, V, R, LN, GROUP>);
     a.pitch = static_cast<int32_t>(VEC == 1 ? drop_pitch(sizeof(T), V, p.threads) : 0);
     a.words_at = static_cast<int32_t>(drop_ring_bytes(VEC, sizeof(T), V, p.threads, R, a.stages, 2, 0));
-    const size_t smem = static_cast<size_t>(a.words_at + drop_words_bytes(VEC, V, p.threads));
+    const size_t smem = static_cast<size_t>(a.words_at + drop_words_bytes(VEC, V, p.threads) + drop_param_bytes(LN, VEC, V, p.threads));
     int64_t grid = 0;
     const cudaError_t e = drop_grid(fn, p, a, smem, &grid);
     if (e != cudaSuccess) return e;
@@ -380,10 +387,7 @@ cudaError_t drop_fwd_of(const norm_plan& p, DropArgs& a, cudaStream_t s) {
     constexpr int full = 16 / sizeof(T);
     const int V = p.per_thread, R = p.rounds;
     if (p.vec_elems == 1) return drop_launch_fwd<T, 1, 8, 1, LN, false>(p, a, s);
-    if (p.mapping == NORM_MAP_GROUP) {
-        if (V == 1) return drop_launch_fwd<T, full, 1, 4, LN, true>(p, a, s);
-        return drop_launch_fwd<T, full, 2, 2, LN, true>(p, a, s);
-    }
+    if (p.mapping == NORM_MAP_GROUP) return drop_launch_fwd<T, full, 2, 2, LN, true>(p, a, s);
     if (V == 1) return R == 1 ? drop_launch_fwd<T, full, 1, 1, LN, false>(p, a, s) : drop_launch_fwd<T, full, 1, 4, LN, false>(p, a, s);
     return drop_launch_fwd<T, full, 4, 1, LN, false>(p, a, s);
 }

@@ -76,13 +76,13 @@ __device__ __forceinline__ uint32_t drop_word(const uint4& w, int i) { return i 
 // ------------------------------------------------------------ accesses
 // What a thread takes at a time, as fp32 pairs: a 16-byte vector, or (VEC 1)
 // two elements of its warp's run, 32 apart.
-// a b and a + c of 16-bit a and b in fp32: one instruction an element, without
-// widening first (exact products; one rounding of the sum).
+// a b + c and a + c of 16-bit a and b in fp32: one instruction an element,
+// without widening first (exact products; one rounding of the sum).
 template <class T>
-__device__ __forceinline__ float mixed_mul(unsigned short a, unsigned short b) {
+__device__ __forceinline__ float mixed_fma(unsigned short a, unsigned short b, float c) {
     float d;
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(a), "h"(b), "f"(0.f));
-    else asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(a), "h"(b), "f"(0.f));
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(a), "h"(b), "f"(c));
+    else asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(a), "h"(b), "f"(c));
     return d;
 }
 template <class T>
@@ -97,10 +97,12 @@ template <class T, int VEC>
 struct DropVec : GnVec<T, VEC> {
     using Raw = uint4;
     static constexpr int kPer = 4 / sizeof(T);  // elements of a 32-bit word
-    static __device__ __forceinline__ float2 mul(const Raw& a, const Raw& b, int i) {
-        if constexpr (kPer == 1) return __fmul2_rn(DropVec::get(a, i), DropVec::get(b, i));
-        else return make_float2(mixed_mul<T>(half(a, 2 * i), half(b, 2 * i)), mixed_mul<T>(half(a, 2 * i + 1), half(b, 2 * i + 1)));
+    // Pairs i of a and b: a b + c, a b, a + c.
+    static __device__ __forceinline__ float2 fma(const Raw& a, const Raw& b, int i, float2 c) {
+        if constexpr (kPer == 1) return __ffma2_rn(DropVec::get(a, i), DropVec::get(b, i), c);
+        else return make_float2(mixed_fma<T>(half(a, 2 * i), half(b, 2 * i), c.x), mixed_fma<T>(half(a, 2 * i + 1), half(b, 2 * i + 1), c.y));
     }
+    static __device__ __forceinline__ float2 mul(const Raw& a, const Raw& b, int i) { return fma(a, b, i, make_float2(-0.f, -0.f)); }
     static __device__ __forceinline__ float2 plus(const Raw& a, int i, float c) {
         if constexpr (kPer == 1) return __fadd2_rn(DropVec::get(a, i), f2_splat(c));
         else return make_float2(mixed_add<T>(half(a, 2 * i), c), mixed_add<T>(half(a, 2 * i + 1), c));
@@ -146,6 +148,7 @@ struct DropVec<T, 1> {
         uint32_t lo, hi;
     };
     static constexpr int H = 1;
+    static __device__ __forceinline__ float2 fma(const Raw& a, const Raw& b, int, float2 c) { return __ffma2_rn(get(a, 0), get(b, 0), c); }
     static __device__ __forceinline__ float2 mul(const Raw& a, const Raw& b, int) { return __fmul2_rn(get(a, 0), get(b, 0)); }
     static __device__ __forceinline__ float2 plus(const Raw& a, int, float c) { return __fadd2_rn(get(a, 0), f2_splat(c)); }
     static __device__ __forceinline__ Raw zero() { return Raw{0, 0}; }
