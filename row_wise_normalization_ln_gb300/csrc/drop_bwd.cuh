@@ -30,7 +30,6 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
     grid_wait();
     const DropMask mask(a);
     const bool drop = a.limit != 0 && a.dx;
-    const bool full = pl.full;
     const void* const from[3] = {a.hin, a.dy, a.dh};
     using Ring = std::conditional_t<kElems, DropStage<T, 3>, DropRing<T, VEC, V, R, 3, LN, P>>;
     // Elements: the CTA's part of a row.
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
         __syncthreads();
     }
     for (; first < a.M; first += rows_step, row += rows_step, parity ^= 1) {
-        const bool whole_step = full && has(R - 1);
+        const bool whole_step = pl.clean && has(R - 1);
         if constexpr (!kElems) {
             ring.wait();
             ring.clear_head(pl);

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                 if (!LN) s[r] = sum.x + sum.y;
             }
         };
-        const bool whole_step = full && has(R - 1);
+        const bool whole_step = pl.clean && has(R - 1);
         if (whole_step) add(std::true_type{});
         else add(std::false_type{});
         ring.advance();

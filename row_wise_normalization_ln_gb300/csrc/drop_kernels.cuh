@@ -183,6 +183,7 @@ struct DropPlace {
     int64_t first_row, teams;  // of the first step; teams of the grid
     bool first;             // writes the row's statistics
     bool full;              // every access of the warp lies within the row
+    bool clean;             // each lies within the row or outside, none partly
 
     __device__ __forceinline__ explicit DropPlace(const DropArgs& a, int R) : N(a.N) {
         const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31;
@@ -214,6 +215,7 @@ struct DropPlace {
         col -= lead;
         nv = col < N ? min(VEC == 1 ? 2 * V : V, (N - col + step - 1) / step) : 0;
         full = __all_sync(kFullMask, nv == (VEC == 1 ? 2 * V : V) && col >= 0 && (VEC == 1 || col + at(V - 1) + VEC <= N));
+        clean = VEC == 1 ? full : __all_sync(kFullMask, nv == 0 || (col >= 0 && col + at(nv - 1) + VEC <= N));
     }
     // Elements between a vector's beginning and that of the rows of team t.
     static __device__ __forceinline__ int lead_of(const DropArgs& a, int64_t t) {
@@ -261,7 +263,7 @@ struct DropPlace {
             return stride > 1 ? DropVec<T, VEC>::load_some(p, lo(j), hi(j)) : DropVec<T, VEC>::load(p);
         }
     }
-    // Access j of a row; p: the thread's first element there.
+    // Access j of a row; p: the thread's first element there. FULL: where the warp is clean.
     template <bool FULL, class T>
     __device__ __forceinline__ void store(T* p, int j, const typename DropVec<T, VEC>::Raw& r) const {
         if constexpr (VEC == 1) {
@@ -270,7 +272,7 @@ struct DropPlace {
             if (FULL || 2 * j + 1 < nv) E::store(p + at(j) + 32, r.hi);
         } else {
             if constexpr (FULL) {
-                DropVec<T, VEC>::store(p + at(j), r);
+                if (on(j)) DropVec<T, VEC>::store(p + at(j), r);
             } else {
                 const int l = lo(j), h = l + N;
                 if (l <= 0 && h >= VEC) DropVec<T, VEC>::store(p + at(j), r);

@@ -4,14 +4,16 @@
 
 namespace libnorm {
 
-// dw of 8 neighbouring columns of a side per CTA: 32 threads share a column,
-// each adds every 32nd partial row, and their sums meet in a tree in shared
-// memory. D <= 512 columns and some hundreds of partial rows: the whole
-// launch is latency, so its CTAs are many and their chains short.
-constexpr int kRopeSumCols = 8, kRopeSumRows = 32;
+// dw of 8 neighbouring columns of a side per CTA: 128 threads share a column,
+// each adds every 128th partial row, eight of them on the way at a time, then
+// the threads' sums meet in a warp, in shared memory and in a warp again. D <=
+// 512 columns and some hundreds of partial rows: the whole launch is latency,
+// so its CTAs are many and their chains short.
+constexpr int kRopeSumCols = 8, kRopeSumRows = 128, kRopeSumLoads = 8;
+constexpr int kRopeSumWarps = kRopeSumCols * kRopeSumRows / 32;
 
 static __global__ void __launch_bounds__(kRopeSumCols* kRopeSumRows) rope_colsum(const __grid_constant__ RopeArgs g) {
-    __shared__ float sm[kRopeSumRows][kRopeSumCols + 1];
+    __shared__ float sm[kRopeSumWarps][kRopeSumCols];
     grid_release();
     grid_wait();
     const int tiles = (g.D + kRopeSumCols - 1) / kRopeSumCols;
@@ -22,14 +24,27 @@ static __global__ void __launch_bounds__(kRopeSumCols* kRopeSumRows) rope_colsum
     const int c = tile * kRopeSumCols + col;
     float t = 0.f;
     if (c < g.D)
-#pragma unroll 4
-        for (int p = row; p < sd.ctas; p += kRopeSumRows) t += sd.part[int64_t(p) * g.D + c];
-    sm[row][col] = t;
-    for (int half = kRopeSumRows / 2; half > 0; half >>= 1) {
-        __syncthreads();
-        if (row < half) sm[row][col] += sm[row + half][col];
-    }
-    if (row == 0 && c < g.D) sd.dw[c] = sm[0][col];
+        for (int p0 = row; p0 < sd.ctas; p0 += kRopeSumLoads * kRopeSumRows) {
+            float v[kRopeSumLoads];
+#pragma unroll
+            for (int k = 0; k < kRopeSumLoads; ++k) {
+                const int p = p0 + k * kRopeSumRows;
+                v[k] = p < sd.ctas ? sd.part[int64_t(p) * g.D + c] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kRopeSumLoads; ++k) t += v[k];
+        }
+    t += __shfl_xor_sync(kFullMask, t, 8);
+    t += __shfl_xor_sync(kFullMask, t, 16);
+    if ((threadIdx.x & 31) < kRopeSumCols) sm[threadIdx.x >> 5][col] = t;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    t = 0.f;
+#pragma unroll
+    for (int k = 0; k < kRopeSumWarps / 4; ++k) t += sm[row + 4 * k][col];
+    t += __shfl_xor_sync(kFullMask, t, 8);
+    t += __shfl_xor_sync(kFullMask, t, 16);
+    if (row == 0 && c < g.D) sd.dw[c] = t;
 }
 
 cudaError_t launch_rope_colsum(const RopeArgs& a, cudaStream_t s) {
