@@ -40,7 +40,7 @@ norm_status check_counts(const Shape& s) {
     if (s.D < 1 || s.D > kRopeMaxD || s.R < 0 || s.R > s.D || s.R % 2 != 0) return NORM_ERR_ARG;
     if (s.T < 0 || s.T > kMaxTokens) return NORM_ERR_ARG;
     for (int64_t h : s.heads) {
-        if (h < 0 || h > kMaxHeads) return NORM_ERR_ARG;
+        if (h < 0 || h >= kMaxHeads) return NORM_ERR_ARG;
         if (h > 0 && s.T > (int64_t(1) << 62) / (h * s.D)) return NORM_ERR_ARG;
     }
     return NORM_OK;

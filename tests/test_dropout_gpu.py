@@ -18,8 +18,9 @@ Backward, A = |xhat| + |mean| rstd (LayerNorm), G = |dy gamma|:
   LayerNorm d: 64 u rstd (G + mean G + A mean(G A)) + 2 u |dh| + eta |d|
   RMSNorm d: 64 u rstd G + 200 u |h| rstd^3 mean(G |h|) + 2 u |dh| + eta |d|
   dx: scale times the part before the rounding, 2 u |d scale|, then eta |dx|.
-Column sums: a chain of at most 64 rows, then of M / 64 such, then of 32 and 32 partial ones: (64 + M / 64 + 64 + c) u of
-  the sum of the absolute terms, c = 8 for LayerNorm's terms (|dy| A) and 48 for RMSNorm's (|dy h| rstd)."""
+Column sums: a chain of at most 64 rows, then of M / 64 such, then of at most 16 teams of a CTA, of 24 of at most 760
+  partial rows by each of 32 warps and of those 32: (64 + M / 64 + 80 + c) u of the sum of the absolute terms, c = 8 for
+  LayerNorm's terms (|dy| A) and 48 for RMSNorm's (|dy h| rstd)."""
 import numpy as np
 import pytest
 import torch
@@ -163,7 +164,7 @@ def check_bwd(ln, got, dy, dh, h, gamma, mean, rstd, p, rng, eps=EPS):
         keep, scale = mask64(rng, p, M, N)
         ref = torch.where(keep, d * scale, 0.0)
         within(dx, ref, torch.where(keep, tol * scale + (2 * U + e) * ref.abs() + tiny(h.dtype), 0.0), "dx")
-    depth = 64 + M / 64 + 64
+    depth = 64 + M / 64 + 80
     within(dg, cg, (depth + per) * U * term.sum(0) + 1e-45, "dgamma")
     assert dg.dtype == torch.float32 and dg.shape == (N,)
     if ln:
@@ -206,6 +207,46 @@ def test_long_rows(N, dtype, ln):
 @pytest.mark.parametrize("ln", [True, False])
 def test_counts(M, N, dtype, ln):
     both(M, N, dtype, ln, 0.2, seed=M)
+
+
+@pytest.mark.parametrize("M,N,dtype", [(700, 4096, "f32"), (1301, 4096, "bf16"), (900, 5001, "bf16"), (650, 5003, "f32"), (2000, 1000, "f16"),
+                                       (3001, 1001, "bf16"), (4003, 301, "f16"), (5000, 96, "bf16"), (9001, 17, "f32"), (20001, 3, "bf16"),
+                                       (10007, 130, "f32"), (640, 2051, "f32"), (333, 10001, "bf16"), (200, 16411, "f32")])
+@pytest.mark.parametrize("ln", [True, False])
+def test_many_rows(M, N, dtype, ln):
+    """Several teams to a CTA, several rows to a team, rows that begin anywhere in a vector."""
+    both(M, N, dtype, ln, 0.25, seed=M)
+
+
+@pytest.mark.parametrize("N,dtype", [(1001, "bf16"), (1001, "f32"), (1000, "f16"), (5001, "bf16"), (31, "f32")])
+@pytest.mark.parametrize("ln", [True, False])
+def test_views_off_the_vectors(N, dtype, ln):
+    """Rows of a larger buffer from any element on, alone or all of them; what lies around them stays."""
+    dt, M, p = DT[dtype], 70, 0.25
+    gamma, beta = params(N, dt, 1)
+    x, r, dy, dh = (make(M, N, dt, i) for i in range(4))
+    h, y, mean, rstd = fwd(ln, x, r, gamma, beta, p, RNG)
+    grads = bwd(ln, True, dy, dh, h, gamma, mean, rstd, p, RNG)
+
+    def view(t, off):
+        buf = torch.full((t.numel() + 16,), 77.0, dtype=dt, device="cuda")
+        v = buf[off:off + t.numel()].view(M, N)
+        if t is not None:
+            v.copy_(t)
+        return buf, v
+
+    for offs in ((1, 1, 1, 1, 1), (8, 8, 8, 8, 8), (3, 0, 0, 0, 0), (0, 0, 0, 0, 5), (1, 2, 3, 4, 5)):
+        bufs, v = zip(*(view(t, o) for t, o in zip((x, r, dy, dh, h), offs)))
+        out = [view(x, o) for o in offs[:2][::-1]]
+        got = fwd(ln, v[0], v[1], gamma, beta, p, RNG, h_out=out[0][1], out=out[1][1])
+        assert torch.equal(got[0], h)
+        check_y(ln, got[0], got[1], x, r, gamma, beta, got[2], got[3])
+        back = [view(x, o) for o in offs[3:]]
+        got = bwd(ln, True, v[2], v[3], v[4], gamma, mean, rstd, p, RNG, dx=back[0][1], dresidual=back[1][1])
+        check_bwd(ln, got, dy, dh, h, gamma, mean, rstd, p, RNG)
+        assert torch.equal(got[0] == 0, grads[0] == 0)
+        for (buf, t), o in list(zip(out, offs[:2][::-1])) + list(zip(back, offs[3:])):
+            assert (buf[:o] == 77).all() and (buf[o + t.numel():] == 77).all()
 
 
 @pytest.mark.parametrize("p", [0.0, 1e-6, 0.05, 0.5, 0.99, 0.9999])
