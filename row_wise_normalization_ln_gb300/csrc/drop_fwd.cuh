@@ -2,14 +2,15 @@
 //   h = residual + x keep / P(keep)  (rounded to the row's type),  y = norm(h).
 //
 // A thread holds its values of R rows, as they are stored, from the add to the
-// output. LayerNorm: a warp's values are shifted by its first one, K (a mean
-// that dwarfs the spread costs the statistics no digits), its mean and M2
-// formed in two passes over the registers, and the warps' states
-// (n, K + mean, M2) meet behind one barrier by the merge rule in its k-way
-// form, the means as differences from the first warp's K:
-//   m_w = (K_w - K_0) + mean_w,  mean = sum n_w m_w / N,  M2 = sum M2_w + n_w (m_w - mean)^2.
-// (The second pass takes differences from K + mean rounded, whose error counts
-// in the square alone.) RMSNorm: sums of squares.
+// output. LayerNorm, in two passes over the registers: a warp's sum gives a
+// first mean A, rounded; about A the sum r of the differences and that of
+// their squares, q, are formed. A + r / n is the mean and q - r^2 / n = M2
+// whatever A's error is: neither a mean that dwarfs the spread nor one that
+// vanishes beside it costs digits. The warps' states (n, A + c, M2), c = r / n,
+// meet behind one barrier by the merge rule in its k-way form, the means as
+// differences from the first warp's A:
+//   m_w = (A_w - A_0) + c_w,  mean = sum n_w m_w / N,  M2 = sum M2_w + n_w (m_w - mean)^2.
+// RMSNorm: sums of squares.
 #pragma once
 
 #include "drop_kernels.cuh"
@@ -19,7 +20,7 @@ namespace libnorm {
 // The states of a CTA's warps (and of a cluster's CTAs) of R rows.
 template <int R>
 struct DropStates {
-    float K[2][R][kDropMaxThreads / 32], mean[2][R][kDropMaxThreads / 32], m2[2][R][kDropMaxThreads / 32];
+    float A[2][R][kDropMaxThreads / 32], mean[2][R][kDropMaxThreads / 32], m2[2][R][kDropMaxThreads / 32];
     float cta[2][3][R];
 };
 
@@ -174,13 +175,12 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                         }
                         pl.template store<FULL>(hp, j, hr);
                         h[r][j] = hr;
-                        if (!LN) {
+                        // (what is not in the row is 0)
 #pragma unroll
-                            for (int i = 0; i < H; ++i) sum = X::fma(hr, hr, i, sum);
-                        }
+                        for (int i = 0; i < H; ++i) sum = LN ? X::sum(hr, i, sum) : X::fma(hr, hr, i, sum);
                     }
                 }
-                if (!LN) s[r] = sum.x + sum.y;
+                s[r] = sum.x + sum.y;
             }
         };
         const bool whole_step = pl.clean && has(R - 1);
@@ -195,18 +195,26 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
         }
         float rstd[R], mu[R];
         if constexpr (LN) {
-            float K[R], K0[R], mean[R], q[R];
-            // The sum of the differences from c[r], or of their squares.
-            const auto differences = [&](auto whole, auto square, const float (&c)[R], float (&out)[R]) {
+            float A[R], A0[R], mean[R], q[R];
+            if (GROUP) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) A[r] = group_sum(s[r], pl.unit) * inv_warp;
+            } else {
+                const float t = warp_sums<R>(s);
+#pragma unroll
+                for (int r = 0; r < R; ++r) A[r] = __shfl_sync(kFullMask, t, R == 1 ? 0 : r * (32 / R)) * inv_warp;
+            }
+            float qr[2 * R];  // of the rows: sums of squares, sums of differences
+            const auto differences = [&](auto whole) {
                 constexpr bool FULL = decltype(whole)::value;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    float2 sum = make_float2(0.f, 0.f);
+                    float2 squares = make_float2(0.f, 0.f), sum = squares;
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         float2 e[H];
 #pragma unroll
-                        for (int i = 0; i < H; ++i) e[i] = X::plus(h[r][j], i, -c[r]);
+                        for (int i = 0; i < H; ++i) e[i] = X::plus(h[r][j], i, -A[r]);
                         if (!FULL && (kElems || !pl.whole(j))) {
 #pragma unroll
                             for (int i = 0; i < H; ++i) {
@@ -215,63 +223,52 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < H; ++i) sum = decltype(square)::value ? __ffma2_rn(e[i], e[i], sum) : __fadd2_rn(sum, e[i]);
+                        for (int i = 0; i < H; ++i) {
+                            squares = __ffma2_rn(e[i], e[i], squares);
+                            sum = __fadd2_rn(sum, e[i]);
+                        }
                     }
-                    out[r] = sum.x + sum.y;
+                    qr[r] = squares.x + squares.y;
+                    qr[R + r] = sum.x + sum.y;
                 }
             };
+            if (full) differences(std::true_type{});
+            else differences(std::false_type{});
+            if (GROUP) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                // the first value of the warp's part (of a row that begins within a vector: the row's first)
-                K[r] = X::get(h[r][0], 0).x;
-                if (VEC > 1 && pl.col < 0) {
-#pragma unroll
-                    for (int e = 1; e < VEC; ++e)
-                        if (pl.col == -e) K[r] = e & 1 ? X::get(h[r][0], e / 2).y : X::get(h[r][0], e / 2).x;
+                for (int r = 0; r < R; ++r) {
+                    const float d = group_sum(qr[R + r], pl.unit);
+                    mean[r] = d * inv_warp;
+                    q[r] = fmaf(-d, mean[r], group_sum(qr[r], pl.unit));
+                    q[r] = q[r] < 0.f ? 0.f : q[r];  // (of equal values)
+                    A0[r] = A[r];
                 }
-                K[r] = __shfl_sync(kFullMask, K[r], GROUP ? lane & ~(pl.unit - 1) : 0);
-                K0[r] = K[r];
-            }
-            if (full) differences(std::true_type{}, std::false_type{}, K, s);
-            else differences(std::false_type{}, std::false_type{}, K, s);
-            if (GROUP) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) mean[r] = group_sum(s[r], pl.unit) * inv_warp;
             } else {
-                const float t = warp_sums<R>(s);
-#pragma unroll
-                for (int r = 0; r < R; ++r) mean[r] = __shfl_sync(kFullMask, t, R == 1 ? 0 : r * (32 / R)) * inv_warp;
-            }
-            float about[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) about[r] = K[r] + mean[r];
-            if (full) differences(std::true_type{}, std::true_type{}, about, q);
-            else differences(std::false_type{}, std::true_type{}, about, q);
-            if (GROUP) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) q[r] = group_sum(q[r], pl.unit);
-            } else {
-                float m2 = warp_sums<R>(q);  // of row lane / (32 / R)
-                float m = mean[0], k = K[0];
+                const float t = warp_sums<2 * R>(qr);
+                const int mine = lane / (32 / R);  // the row whose state this lane has
+                const float d = __shfl_sync(kFullMask, t, 16 + mine * (16 / R));
+                float k = A[0], m = d * inv_warp;
+                float m2 = fmaf(-d, m, __shfl_sync(kFullMask, t, mine * (16 / R)));
+                m2 = m2 < 0.f ? 0.f : m2;  // (of equal values)
 #pragma unroll
                 for (int r = 1; r < R; ++r)
-                    if (lane / (32 / R) == r) m = mean[r], k = K[r];
+                    if (mine == r) k = A[r];
                 if (pl.warps > 1) {
                     if ((lane & (32 / R - 1)) == 0) {
                         const int r = lane / (32 / R);
-                        sums.K[parity][r][warp] = k;
+                        sums.A[parity][r][warp] = k;
                         sums.mean[parity][r][warp] = m;
                         sums.m2[parity][r][warp] = m2;
                     }
                     pl.sync();
                     const int w0 = pl.warp0 + sh.w0;
-                    k = sums.K[parity][sh.idx][pl.warp0];
+                    k = sums.A[parity][sh.idx][pl.warp0];
                     float t = 0.f, dm[E];
 #pragma unroll
                     for (int i = 0; i < E; ++i) {
                         dm[i] = 0.f;
                         if (n_of[i] > 0.f) {
-                            dm[i] = (sums.K[parity][sh.idx][w0 + i] - k) + sums.mean[parity][sh.idx][w0 + i];
+                            dm[i] = (sums.A[parity][sh.idx][w0 + i] - k) + sums.mean[parity][sh.idx][w0 + i];
                             t = fmaf(n_of[i], dm[i], t);
                         }
                     }
@@ -301,8 +298,8 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                             pm = drop_peer(&sums.cta[parity][1][r], static_cast<uint32_t>(lane));
                             pq = drop_peer(&sums.cta[parity][2][r], static_cast<uint32_t>(lane));
                         }
-                        K0[r] = __shfl_sync(kFullMask, pk, 0);
-                        const float dm = n > 0.f ? (pk - K0[r]) + pm : 0.f;
+                        A0[r] = __shfl_sync(kFullMask, pk, 0);
+                        const float dm = n > 0.f ? (pk - A0[r]) + pm : 0.f;
                         mean[r] = __shfl_sync(kFullMask, drop_down<8>(n * dm), 0) * a.invN;
                         q[r] = __shfl_sync(kFullMask, drop_down<8>(fmaf(n * (dm - mean[r]), dm - mean[r], pq)), 0);
                     }
@@ -312,19 +309,19 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                         if (R == 1) {  // (every lane has the row's)
                             mean[r] = m;
                             q[r] = m2;
-                            K0[r] = k;
+                            A0[r] = k;
                             continue;
                         }
                         mean[r] = __shfl_sync(kFullMask, m, r * S);
                         q[r] = __shfl_sync(kFullMask, m2, r * S);
-                        K0[r] = __shfl_sync(kFullMask, k, r * S);
+                        A0[r] = __shfl_sync(kFullMask, k, r * S);
                     }
                 }
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 rstd[r] = rsqrtf(fmaf(q[r], a.invN, a.eps));
-                mu[r] = K0[r] + mean[r];
+                mu[r] = A0[r] + mean[r];
                 if (has(r) && pl.first) {
                     if (a.mean) a.mean[row + r * pl.stride] = mu[r];
                     if (a.rstd) a.rstd[row + r * pl.stride] = rstd[r];

@@ -97,7 +97,7 @@ template <class T, int VEC>
 struct DropVec : GnVec<T, VEC> {
     using Raw = uint4;
     static constexpr int kPer = 4 / sizeof(T);  // elements of a 32-bit word
-    // Pairs i of a and b: a b + c, a b, a + c.
+    // Pairs i of a and b: a b + c, a b, a + c (one c, or each its own).
     static __device__ __forceinline__ float2 fma(const Raw& a, const Raw& b, int i, float2 c) {
         if constexpr (kPer == 1) return __ffma2_rn(DropVec::get(a, i), DropVec::get(b, i), c);
         else return make_float2(mixed_fma<T>(half(a, 2 * i), half(b, 2 * i), c.x), mixed_fma<T>(half(a, 2 * i + 1), half(b, 2 * i + 1), c.y));
@@ -106,6 +106,10 @@ struct DropVec : GnVec<T, VEC> {
     static __device__ __forceinline__ float2 plus(const Raw& a, int i, float c) {
         if constexpr (kPer == 1) return __fadd2_rn(DropVec::get(a, i), f2_splat(c));
         else return make_float2(mixed_add<T>(half(a, 2 * i), c), mixed_add<T>(half(a, 2 * i + 1), c));
+    }
+    static __device__ __forceinline__ float2 sum(const Raw& a, int i, float2 c) {
+        if constexpr (kPer == 1) return __fadd2_rn(DropVec::get(a, i), c);
+        else return make_float2(mixed_add<T>(half(a, 2 * i), c.x), mixed_add<T>(half(a, 2 * i + 1), c.y));
     }
     static __device__ __forceinline__ unsigned short half(const Raw& r, int e) {
         return static_cast<unsigned short>(word(r, e / 2) >> (16 * (e % 2)));
@@ -151,6 +155,7 @@ struct DropVec<T, 1> {
     static __device__ __forceinline__ float2 fma(const Raw& a, const Raw& b, int, float2 c) { return __ffma2_rn(get(a, 0), get(b, 0), c); }
     static __device__ __forceinline__ float2 mul(const Raw& a, const Raw& b, int) { return __fmul2_rn(get(a, 0), get(b, 0)); }
     static __device__ __forceinline__ float2 plus(const Raw& a, int, float c) { return __fadd2_rn(get(a, 0), f2_splat(c)); }
+    static __device__ __forceinline__ float2 sum(const Raw& a, int, float2 c) { return __fadd2_rn(get(a, 0), c); }
     static __device__ __forceinline__ Raw zero() { return Raw{0, 0}; }
     static __device__ __forceinline__ float2 get(const Raw& r, int) { return make_float2(E::get(r.lo, 0).x, E::get(r.hi, 0).x); }
     static __device__ __forceinline__ void set(Raw& r, int, float2 v) {
