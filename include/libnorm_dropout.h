@@ -46,8 +46,9 @@ typedef struct {
  * overlap is undefined. 0 <= p and round(65536 p) < 65536; with p = 0 rng is
  * not looked at and h, y are those of the plain fused add, to the rounding of
  * the statistics.
- * Limits: 1 <= N <= 65536 with 16-byte vectors (every pointer 16-byte aligned,
- * rows whole vectors), N <= 32768 otherwise; longer rows return NORM_ERR_ARG.
+ * Limits: 1 <= N <= 65536 where every pointer is 16-byte aligned and the rows
+ * are whole 16-byte vectors, N <= 65520 where they are not, N <= 32768 where a
+ * pointer is not 16-byte aligned; longer rows return NORM_ERR_ARG.
  * Every pointer needs its element's alignment.
  */
 norm_status ln_fwd_dropout_add(const void* x, const void* residual, const void* gamma, const void* beta, double p,
@@ -99,11 +100,13 @@ norm_status rms_bwd_add(const void* dy, const void* dh, const void* h, const voi
  * lanes of a warp per row, or NORM_MAP_CTA with `cluster` CTAs per row, or
  * teams of `group` threads of a CTA (0: all `threads` of it); `per_thread`
  * accesses of `vec_elems` elements per thread (vec_elems 1: of two elements),
- * which cover the row; `rounds` rows at a time; `stages` steps of them in
- * shared memory, up to 4, from 2 in the forward on 16-byte vectors, from 3
- * otherwise; `grid` CTAs at most, persistent). `aligned16`: every pointer is
- * 16-byte aligned. Host only: makes no CUDA call. NORM_ERR_ARG for rows beyond
- * the limits. */
+ * which cover the row and, where rows are no whole number of vectors, up to
+ * vec_elems - 1 elements before it; `rounds` rows at a time; `stages` steps of
+ * them in shared memory, up to 4, from 2 on 16-byte vectors, from 3 on
+ * elements; `grid` CTAs at most, persistent, whose teams are a multiple of the
+ * 1, 2, 4 or 8 rows after which one begins at the same place of a vector).
+ * `aligned16`: every pointer is 16-byte aligned. Host only: makes no CUDA
+ * call. NORM_ERR_ARG for rows beyond the limits. */
 norm_status drop_make_plan(int64_t M, int64_t N, norm_dtype dtype, int layer_norm, int backward, int aligned16,
                            int num_sms, norm_plan* plan);
 

@@ -1,6 +1,7 @@
-"""GB300-native row-wise LayerNorm / RMSNorm, group norm and the global norm of
-a step's gradients: Python binding of the libnorm C ABI (include/libnorm.h,
-libnorm_group.h, libnorm_grad.h).
+"""GB300-native row-wise LayerNorm / RMSNorm, group norm, the global norm of a
+step's gradients, head norms with rotation and dropout + add + norm: Python
+binding of the libnorm C ABI (include/libnorm.h, libnorm_group.h,
+libnorm_grad.h, libnorm_rope.h, libnorm_dropout.h).
 
 The binding only marshals arguments: it reshapes ``[..., N]`` inputs to
 ``[M, N]`` rows (the T3 drill's host wrapper, §④), allocates outputs with

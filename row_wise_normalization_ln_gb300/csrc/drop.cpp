@@ -64,6 +64,28 @@ int64_t smem_bytes(const Shape& s, const norm_plan& p, int stages) {
 // Vectors, or pairs of elements, that a row touches.
 int64_t accesses(const Shape& s, int vec) { return vec == 1 ? ceil_div(s.N, 2) : libnorm::drop_vectors(s.N, vec); }
 
+// Which threads share a row, from sweeps of the instances (bf16 unless said;
+// the other side in brackets):
+// - Few vectors a row: lanes of a warp, two accesses a lane and two rows a step.
+//   Forward up to 64 vectors: LayerNorm 65536 x 256 23.8 us [a team of a warp,
+//   one access, four rows: 27.7], 32768 x 512 24.1 [29.0]. Backward up to 16:
+//   131072 x 96 43.8 [60.5]; above, a team's steps of four rows need fewer
+//   instructions: 65536 x 256 34.0 [42.6], 32768 x 512 34.6 [43.5].
+// - Backward up to 512 vectors: one access a thread, four rows a step: LayerNorm
+//   16384 x 1024 35.4 us [two accesses, two rows: 54], 8192 x 4096 66.2 [76.8].
+//   Above, two accesses and two rows (16-bit), or four and one: more threads do
+//   not fit the columns' sums into their registers.
+// - Forward: four accesses, one row: LayerNorm 16384 x 2048 48.2 us [one access,
+//   four rows: 58.2]; below 128 vectors too few lanes would be busy. Few rows
+//   (four per SM): one access, one row, for latency: f32 128 x 1024 2.2 us [3.6].
+// CTAs hold several teams, one row each at a time, so that one computes while
+// another waits: backward up to 512 threads, one CTA an SM (LayerNorm 16384 x 1024
+// 35.4 us, CTAs of one team 39.2; fewer partial rows to add up, too), forward
+// up to 128 (LayerNorm 16384 x 1024 25.4 us, of 32 threads 45.6). RMSNorm's
+// forward of narrow rows is at its best with two such CTAs an SM (65536 x 2048
+// 171 us; four: 181), LayerNorm's, whose rows wait for one another longer, with
+// four. Few rows forward: the same number of CTAs on every SM, idle ones too,
+// so that a following launch finds room (f32 128 x 1024 2.2 us, 128 CTAs 2.6).
 norm_status plan_of(const Shape& s, int vec, int num_sms, norm_plan* p) {
     std::memset(p, 0, sizeof *p);
     if (vec == 1 && s.N > kMaxElems) return NORM_ERR_ARG;
