@@ -37,8 +37,12 @@ __device__ __forceinline__ float drop_down(float v) {  // sum over aligned block
     return v;
 }
 
-template <class T, int VEC, int V, int R, bool LN, bool GROUP>
-__global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V >= 32 && !LN ? 2 : 1) drop_fwd(const __grid_constant__ DropArgs a) {
+// ASIDE: the parameters lie in shared memory: LayerNorm's of four accesses are
+// 32 registers, without which wide rows have two CTAs an SM rather than one
+// (bf16 4096 x 8192 54 -> 48 us, 4096 x 5001 45 -> 37). Narrow rows, in CTAs of at
+// most 128 threads, do without (16384 x 1024 25.4 -> 22.9 us).
+template <class T, int VEC, int V, int R, bool LN, bool GROUP, bool ASIDE = false>
+__global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V >= 32 && !LN ? 2 : 1) drop_fwd(const __grid_constant__ DropArgs a) {
     using P = DropPlace<VEC, V, GROUP>;
     using X = DropVec<T, VEC>;
     using Raw = typename X::Raw;
@@ -78,10 +82,8 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
         if constexpr (kElems) ring.send();
         else ring.send(a, pl, from, row + i * rows_step);
     row_words(0, row);
-    // The parameters of the thread's columns: in registers, or, LayerNorm's of 32
-    // columns (32 registers of 128), in shared memory.
-    constexpr bool kAside = LN && VEC > 1 && V == 4;
-    Raw params[kAside ? 1 : V][LN ? 2 : 1];
+    // The parameters of the thread's columns.
+    Raw params[ASIDE ? 1 : V][LN ? 2 : 1];
     const uint32_t aside = words_at + threadIdx.x * 16;
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -89,14 +91,14 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
         for (int k = 0; k < (LN ? 2 : 1); ++k) {
             Raw v = X::zero();
             if (pl.on(j)) v = pl.param(static_cast<const T*>(k == 0 ? a.gamma : a.beta), j);
-            if constexpr (kAside) {
+            if constexpr (ASIDE) {
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(aside + (2 * j + k) * blockDim.x * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
             } else {
                 params[j][k] = v;
             }
         }
     const auto param = [&](int j, int k) {
-        if constexpr (kAside) {
+        if constexpr (ASIDE) {
             Raw v;
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -373,9 +375,9 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
     if (pl.C > 1) cluster_barrier();  // no CTA leaves while a peer may read its state
 }
 
-template <class T, int VEC, int V, int R, bool LN, bool GROUP>
+template <class T, int VEC, int V, int R, bool LN, bool GROUP, bool ASIDE = false>
 cudaError_t drop_launch_fwd(const norm_plan& p, DropArgs& a, cudaStream_t s) {
-    const void* fn = reinterpret_cast<const void*>(drop_fwd<T, VEC, V, R, LN, GROUP>);
+    const void* fn = reinterpret_cast<const void*>(drop_fwd<T, VEC, V, R, LN, GROUP, ASIDE>);
     a.pitch = static_cast<int32_t>(VEC == 1 ? drop_pitch(sizeof(T), V, p.threads) : 0);
     a.words_at = static_cast<int32_t>(drop_ring_bytes(VEC, sizeof(T), V, p.threads, R, a.stages, 2, 0));
     const size_t smem = static_cast<size_t>(a.words_at + drop_words_bytes(VEC, V, p.threads) + drop_param_bytes(LN, VEC, V, p.threads));
@@ -392,6 +394,7 @@ cudaError_t drop_fwd_of(const norm_plan& p, DropArgs& a, cudaStream_t s) {
     if (p.vec_elems == 1) return drop_launch_fwd<T, 1, 8, 1, LN, false>(p, a, s);
     if (p.mapping == NORM_MAP_GROUP) return drop_launch_fwd<T, full, 2, 2, LN, true>(p, a, s);
     if (V == 1) return R == 1 ? drop_launch_fwd<T, full, 1, 1, LN, false>(p, a, s) : drop_launch_fwd<T, full, 1, 4, LN, false>(p, a, s);
+    if (LN && p.threads > kDropNarrow) return drop_launch_fwd<T, full, 4, 1, LN, false, LN>(p, a, s);
     return drop_launch_fwd<T, full, 4, 1, LN, false>(p, a, s);
 }
 

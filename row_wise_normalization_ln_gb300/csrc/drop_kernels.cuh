@@ -3,7 +3,7 @@
 //
 // Rows are walked by persistent CTAs, R neighbouring ones at a time (the cost
 // of a step, its barrier, sums and addresses, is that of many elements). A row
-// belongs to some lanes of a warp (short rows), a CTA, or a cluster of CTAs; a
+// belongs to a team: some lanes of a warp (short rows), warps, or a cluster; a
 // thread owns the same columns in every row it visits, so the parameters and,
 // in the backward, the column sums stay in its registers.
 //
@@ -48,7 +48,9 @@ struct DropMask {
         limit = a.limit;
     }
     // LEAN: the rounds' keys are formed for each call (two additions a round),
-    // rather than kept in 14 registers.
+    // rather than kept in 14 registers, which LayerNorm's kernels lack (bf16
+    // 4096 x 8192 forward 60 -> 48 us, backward 87 -> 73) and RMSNorm's do not
+    // (forward 65536 x 2048 177 us with additions, 165 without).
     template <bool LEAN>
     __device__ __forceinline__ uint4 words(uint64_t group) const {
         uint32_t x0 = static_cast<uint32_t>(group), x1 = static_cast<uint32_t>(group >> 32), x2 = c2, x3 = c3;
@@ -74,10 +76,9 @@ struct DropMask {
 __device__ __forceinline__ uint32_t drop_word(const uint4& w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
 
 // ------------------------------------------------------------ accesses
-// What a thread takes at a time, as fp32 pairs: a 16-byte vector, or (VEC 1)
-// two elements of its warp's run, 32 apart.
 // a b + c and a + c of 16-bit a and b in fp32: one instruction an element,
-// without widening first (exact products; one rounding of the sum).
+// without widening first (exact products; one rounding of the sum). LayerNorm
+// backward bf16 4096 x 8192 73 us, with widened products 83.
 template <class T>
 __device__ __forceinline__ float mixed_fma(unsigned short a, unsigned short b, float c) {
     float d;
@@ -93,6 +94,8 @@ __device__ __forceinline__ float mixed_add(unsigned short a, float c) {
     return d;
 }
 
+// What a thread takes at a time, as fp32 pairs: a 16-byte vector, or (VEC 1)
+// two elements of its warp's run, 32 apart.
 template <class T, int VEC>
 struct DropVec : GnVec<T, VEC> {
     using Raw = uint4;
