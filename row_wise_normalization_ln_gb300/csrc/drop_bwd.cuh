@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                 const float mean = stat(r).x;
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    if (FULL || !kElems || pl.on(j)) {
+                    if (FULL || pl.looks(j)) {
                         const Raw hr = read(whole, r, 0, j), yr = read(whole, r, 1, j);
 #pragma unroll
                         for (int i = 0; i < H; ++i) {
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
                 if constexpr (kElems) ws = words_at + parity * words_row * 16 + (static_cast<uint32_t>((at - in) & 7) + in) * 2;
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    if (FULL || !kElems || pl.on(j)) {
+                    if (FULL || pl.looks(j)) {
                         const Raw hr = read(whole, r, 0, j), yr = read(whole, r, 1, j);
                         Raw er = X::zero(), orr = X::zero(), oxr = X::zero();
                         if (a.dh) er = read(whole, r, 2, j);
@@ -215,14 +215,14 @@ __global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V
         __syncthreads();
     }
     for (; first < a.M; first += rows_step, row += rows_step, parity ^= 1) {
-        const bool whole_step = pl.clean && has(R - 1);
+        const bool whole_step = pl.straight && has(R - 1);
         if constexpr (!kElems) {
             ring.wait();
             ring.clear_head(pl);
             if (LN) __syncwarp();  // everyone's copies of the statistics; everyone is done with the last step's
             ring.send(a, pl, from, row + (a.stages - 1) * rows_step);
         }
-        if (kElems ? whole_step : has(R - 1)) total(std::true_type{});
+        if (kElems ? whole_step : pl.most == V && has(R - 1)) total(std::true_type{});
         else total(std::false_type{});
         drop_put<2 * R>(sums, pl, parity, s);
         if constexpr (!GROUP) {

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     if (!FULL) h[r][j] = X::zero();
-                    if (FULL || (on && (!kElems || pl.on(j)))) {
+                    if (FULL || (on && pl.looks(j))) {
                         Raw xr, rr, hr = X::zero();
                         if constexpr (kElems) {
                             xr = ring.template get<FULL>(xs, j, pl.nv);
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V
                 s[r] = sum.x + sum.y;
             }
         };
-        const bool whole_step = pl.clean && has(R - 1);
+        const bool whole_step = pl.straight && has(R - 1);
         if (whole_step) add(std::true_type{});
         else add(std::false_type{});
         ring.advance();
@@ -219,23 +219,24 @@ __global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V
                 for (int r = 0; r < R; ++r) {
                     float2 squares = make_float2(0.f, 0.f), sum = squares;
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        float2 e[H];
+                    for (int j = 0; j < V; ++j)
+                        if (FULL || pl.looks(j)) {
+                            float2 e[H];
 #pragma unroll
-                        for (int i = 0; i < H; ++i) e[i] = X::plus(h[r][j], i, -A[r]);
-                        if (!FULL && (kElems || !pl.whole(j))) {
+                            for (int i = 0; i < H; ++i) e[i] = X::plus(h[r][j], i, -A[r]);
+                            if (!FULL && (kElems || !pl.whole(j))) {
+#pragma unroll
+                                for (int i = 0; i < H; ++i) {
+                                    if (!pl.valid(j, 2 * i)) e[i].x = 0.f;
+                                    if (!pl.valid(j, 2 * i + 1)) e[i].y = 0.f;
+                                }
+                            }
 #pragma unroll
                             for (int i = 0; i < H; ++i) {
-                                if (!pl.valid(j, 2 * i)) e[i].x = 0.f;
-                                if (!pl.valid(j, 2 * i + 1)) e[i].y = 0.f;
+                                squares = __ffma2_rn(e[i], e[i], squares);
+                                sum = __fadd2_rn(sum, e[i]);
                             }
                         }
-#pragma unroll
-                        for (int i = 0; i < H; ++i) {
-                            squares = __ffma2_rn(e[i], e[i], squares);
-                            sum = __fadd2_rn(sum, e[i]);
-                        }
-                    }
                     qr[r] = squares.x + squares.y;
                     qr[R + r] = sum.x + sum.y;
                 }
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V
                 T* const yp = static_cast<T*>(a.y) + at + r * row_step;
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    if (FULL || (has(r) && (!kElems || pl.on(j)))) {
+                    if (FULL || (has(r) && pl.looks(j))) {
                         Raw yr = X::zero();
                         const Raw gv = param(j, 0);
                         [[maybe_unused]] Raw bv;

@@ -191,7 +191,8 @@ struct DropPlace {
     int64_t first_row, teams;  // of the first step; teams of the grid
     bool first;             // writes the row's statistics
     bool full;              // every access of the warp lies within the row
-    bool clean;             // each lies within the row or outside, none partly
+    int most;               // accesses of the warp's lane that has most
+    bool straight;          // the warp has V accesses, each within the row or outside, none partly
 
     __device__ __forceinline__ explicit DropPlace(const DropArgs& a, int R) : N(a.N) {
         const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31;
@@ -223,13 +224,16 @@ struct DropPlace {
         col -= lead;
         nv = col < N ? min(VEC == 1 ? 2 * V : V, (N - col + step - 1) / step) : 0;
         full = __all_sync(kFullMask, nv == (VEC == 1 ? 2 * V : V) && col >= 0 && (VEC == 1 || col + at(V - 1) + VEC <= N));
-        clean = VEC == 1 ? full : __all_sync(kFullMask, nv == 0 || (col >= 0 && col + at(nv - 1) + VEC <= N));
+        most = VEC == 1 ? V : __reduce_max_sync(kFullMask, nv);
+        straight = VEC == 1 ? full : most == V && __all_sync(kFullMask, nv == 0 || (col >= 0 && col + at(nv - 1) + VEC <= N));
     }
     // Elements between a vector's beginning and that of the rows of team t.
     static __device__ __forceinline__ int lead_of(const DropArgs& a, int64_t t) {
         return VEC == 1 ? 0 : ((static_cast<int>(t) & (a.phases - 1)) * a.N) & (VEC - 1);
     }
     __device__ __forceinline__ bool on(int j) const { return (VEC == 1 ? 2 * j : j) < nv; }
+    // Whether the thread looks at access j (vectors: the warp does, and finds zeros where the row is not).
+    __device__ __forceinline__ bool looks(int j) const { return VEC == 1 ? on(j) : j < most; }
     // The first column of access j, where single elements matter: formed anew
     // each time, as a row's comparisons kept from one step to the next would
     // take the registers of the warps that need none (LayerNorm bf16: 102 -> 128).
@@ -271,7 +275,7 @@ struct DropPlace {
             return stride > 1 ? DropVec<T, VEC>::load_some(p, lo(j), hi(j)) : DropVec<T, VEC>::load(p);
         }
     }
-    // Access j of a row; p: the thread's first element there. FULL: where the warp is clean.
+    // Access j of a row; p: the thread's first element there. FULL: where the warp is straight.
     template <bool FULL, class T>
     __device__ __forceinline__ void store(T* p, int j, const typename DropVec<T, VEC>::Raw& r) const {
         if constexpr (VEC == 1) {
