@@ -95,7 +95,7 @@ inline int64_t drop_words_bytes(int vec, int per_thread, int threads) {
     return vec == 1 ? 2 * 16 * (drop_cta_cols(1, per_thread, threads) / 8 + 2) : 0;
 }
 inline int64_t drop_param_bytes(bool ln, int vec, int per_thread, int threads) {  // forward
-    return ln && vec > 1 && per_thread == 4 && threads > kDropNarrow ? int64_t(2) * per_thread * threads * 16 : 0;
+    return ln && vec > 1 && per_thread == 4 && threads > kDropNarrow ? int64_t(per_thread) * threads * 16 : 0;
 }
 inline int64_t drop_sums_bytes(bool ln, int vec, int per_thread, int threads) {
     return int64_t(ln ? 2 : 1) * vec * per_thread * threads * 4;

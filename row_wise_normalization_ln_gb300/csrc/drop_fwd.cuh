@@ -37,12 +37,13 @@ __device__ __forceinline__ float drop_down(float v) {  // sum over aligned block
     return v;
 }
 
-// ASIDE: the parameters lie in shared memory: LayerNorm's of four accesses are
-// 32 registers, without which wide rows have two CTAs an SM rather than one
-// (bf16 4096 x 8192 54 -> 48 us, 4096 x 5001 45 -> 37). Narrow rows, in CTAs of at
-// most 128 threads, do without (16384 x 1024 25.4 -> 22.9 us).
+// ASIDE: beta lies in shared memory: LayerNorm's parameters of four accesses
+// are 32 registers, and with all of them wide rows have one CTA an SM rather
+// than two (bf16 4096 x 8192 54 us, with beta aside 45.4, with both 47.6; 4096 x 5001
+// 45, 35.9, 36.2). Narrow rows, in CTAs of at most 128 threads, do without
+// (16384 x 1024 22.9 us, aside 25.4).
 template <class T, int VEC, int V, int R, bool LN, bool GROUP, bool ASIDE = false>
-__global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V >= 32 && !LN ? 2 : 1) drop_fwd(const __grid_constant__ DropArgs a) {
+__global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V >= 32 ? 2 : 1) drop_fwd(const __grid_constant__ DropArgs a) {
     using P = DropPlace<VEC, V, GROUP>;
     using X = DropVec<T, VEC>;
     using Raw = typename X::Raw;
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V
         else ring.send(a, pl, from, row + i * rows_step);
     row_words(0, row);
     // The parameters of the thread's columns.
-    Raw params[ASIDE ? 1 : V][LN ? 2 : 1];
+    Raw params[V][LN && !ASIDE ? 2 : 1];
     const uint32_t aside = words_at + threadIdx.x * 16;
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -92,22 +93,25 @@ __global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V
             Raw v = X::zero();
             if (pl.on(j)) v = pl.param(static_cast<const T*>(k == 0 ? a.gamma : a.beta), j);
             if constexpr (ASIDE) {
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(aside + (2 * j + k) * blockDim.x * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-            } else {
-                params[j][k] = v;
+                if (k == 1) {
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(aside + j * blockDim.x * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+                    continue;
+                }
             }
+            params[j][LN && !ASIDE ? k : 0] = v;
         }
     const auto param = [&](int j, int k) {
         if constexpr (ASIDE) {
-            Raw v;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(aside + (2 * j + k) * blockDim.x * 16)
-                         : "memory");
-            return v;
-        } else {
-            return params[j][k];
+            if (k == 1) {
+                Raw v;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                             : "r"(aside + j * blockDim.x * 16)
+                             : "memory");
+                return v;
+            }
         }
+        return params[j][LN && !ASIDE ? k : 0];
     };
     // LayerNorm: elements of this warp's part, of the warps whose states this
     // lane merges, of the CTA's.
