@@ -75,13 +75,13 @@ int64_t accesses(const Shape& s, int vec) { return vec == 1 ? ceil_div(s.N, 2) :
 //   16384 x 1024 35.4 us [two accesses, two rows: 54], 8192 x 4096 66.2 [76.8].
 //   Above, two accesses and two rows (16-bit), or four and one: more threads do
 //   not fit the columns' sums into their registers.
-// - Forward: four accesses, one row: LayerNorm 16384 x 2048 48.2 us [one access,
+// - Forward: four accesses, one row: LayerNorm 16384 x 2048 46.3 us [one access,
 //   four rows: 58.2]; below 128 vectors too few lanes would be busy. Few rows
 //   (four per SM): one access, one row, for latency: f32 128 x 1024 2.2 us [3.6].
 // CTAs hold several teams, one row each at a time, so that one computes while
 // another waits: backward up to 512 threads, one CTA an SM (LayerNorm 16384 x 1024
 // 35.4 us, CTAs of one team 39.2; fewer partial rows to add up, too), forward
-// up to 128 (LayerNorm 16384 x 1024 25.4 us, of 32 threads 45.6). RMSNorm's
+// up to 128 (LayerNorm 16384 x 1024 23.0 us, of 32 threads 33.2). RMSNorm's
 // forward of narrow rows is at its best with two such CTAs an SM (65536 x 2048
 // 171 us; four: 181), LayerNorm's, whose rows wait for one another longer, with
 // four. Few rows forward: the same number of CTAs on every SM, idle ones too,

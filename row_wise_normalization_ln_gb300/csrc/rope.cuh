@@ -18,6 +18,11 @@
 // same preparation, and groups stood idle where the heads ran out.) The sums
 // of a head meet in butterflies over its lanes; nothing meets across warps
 // until the backward's column sums.
+//
+// bf16, 16384 tokens of 32 + 8 heads of 128: forward 56.3 us, 6.0 TB/s, backward
+// 86, 5.9 TB/s, bound by memory (with a group on a head each and all of a task's
+// heads in registers 73 and 168). One token 1.65 us, f16 501 x 16 x 80 2.25, f32
+// backward 1023 x 24 x 96 11.5: launches and latency.
 #pragma once
 
 #include "gn_kernels.cuh"
