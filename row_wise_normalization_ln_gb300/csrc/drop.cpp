@@ -72,7 +72,10 @@ int64_t accesses(const Shape& s, int vec) { return vec == 1 ? ceil_div(s.N, 2) :
 //   131072 x 96 43.8 [60.5]; above, a team's steps of four rows need fewer
 //   instructions: 65536 x 256 34.0 [42.6], 32768 x 512 34.6 [43.5].
 // - Backward up to 512 vectors: one access a thread, four rows a step: LayerNorm
-//   16384 x 1024 35.4 us [two accesses, two rows: 54], 8192 x 4096 66.2 [76.8].
+//   16384 x 1024 35.4 us [two accesses, two rows: 54], 8192 x 4096 66.2 [76.8]. Two
+//   teams of 192 or 224 threads would leave much of an SM idle: 16-bit rows of 161
+//   to 224 vectors take the other form (RMSNorm 24876 x 1424 53.2 us [60.1],
+//   17692 x 1656 62.8 [65.9]).
 //   Above, two accesses and two rows (16-bit), or four and one: more threads do
 //   not fit the columns' sums into their registers.
 // - Forward: four accesses, one row: LayerNorm 16384 x 2048 46.3 us [one access,
@@ -82,9 +85,10 @@ int64_t accesses(const Shape& s, int vec) { return vec == 1 ? ceil_div(s.N, 2) :
 // another waits: backward up to 512 threads, one CTA an SM (LayerNorm 16384 x 1024
 // 35.4 us, CTAs of one team 39.2; fewer partial rows to add up, too), forward
 // up to 128 (LayerNorm 16384 x 1024 23.0 us, of 32 threads 33.2). RMSNorm's
-// forward of narrow rows is at its best with two such CTAs an SM (65536 x 2048
-// 171 us; four: 181), LayerNorm's, whose rows wait for one another longer, with
-// four. Few rows forward: the same number of CTAs on every SM, idle ones too,
+// forward of narrow rows that fill their teams is at its best with two such CTAs
+// an SM and three steps in shared memory (65536 x 2048 170 us; four: 177); rows that
+// do not, and LayerNorm's, with four and two steps (RMSNorm 16384 x 1500 37.0 us;
+// two: 51.9). Few rows forward: the same number of CTAs on every SM, idle ones too,
 // so that a following launch finds room (f32 128 x 1024 2.2 us, 128 CTAs 2.6).
 norm_status plan_of(const Shape& s, int vec, int num_sms, norm_plan* p) {
     std::memset(p, 0, sizeof *p);
@@ -100,7 +104,7 @@ norm_status plan_of(const Shape& s, int vec, int num_sms, norm_plan* p) {
         while (p->group * 2 < nacc) p->group *= 2;
         p->threads = 128;
         p->rounds = 2;
-    } else if (vec > 1 && nacc <= kDropMaxThreads && (s.bwd || nacc < 128 || s.M <= int64_t(num_sms) * 4)) {
+    } else if (vec > 1 && nacc <= kDropMaxThreads && (s.bwd ? s.es() == 4 || nacc <= 160 || nacc > 224 : nacc < 128 || s.M <= int64_t(num_sms) * 4)) {
         p->mapping = NORM_MAP_CTA;
         p->per_thread = 1;
         p->rounds = !s.bwd && s.M <= int64_t(num_sms) * 4 ? 1 : 4;
@@ -133,8 +137,11 @@ norm_status plan_of(const Shape& s, int vec, int num_sms, norm_plan* p) {
             p->threads = team;
         }
         if (!s.bwd && p->per_thread == 4 && p->threads <= 128) {
-            p->stages = 3;
-            per_sm = s.ln ? 512 : 256;
+            per_sm = 512;
+            if (!s.ln && nacc == int64_t(4) * team_of(*p)) {
+                p->stages = 3;
+                per_sm = 256;
+            }
         }
     }
     const int teams = teams_of(*p), unit = libnorm::drop_grid_unit(libnorm::drop_phases(s.N, vec), teams);
