@@ -121,14 +121,14 @@ struct RopeTurn {
     static constexpr bool kInside = ILV && VEC > 1;  // pairs lie within an access
     float2 c[NP][kInside ? 2 * H : H], s[NP][2 * H];  // a's, then b's (not kInside: the same cosines)
 
-    // From a token's table rows; vec: they are on 16-byte boundaries.
-    __device__ __forceinline__ void set(const RopeLane<VEC, NP, ILV>& l, const float* cp, const float* sp, bool vec) {
+    // From a token's table rows; vec: they are on 16-byte boundaries. Not live: no angle is read, nothing turns.
+    __device__ __forceinline__ void set(const RopeLane<VEC, NP, ILV>& l, const float* cp, const float* sp, bool vec, bool live = true) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
             if constexpr (kInside) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const bool on = h == 0 ? l.ra[j] : l.rb[j];
+                    const bool on = live && (h == 0 ? l.ra[j] : l.rb[j]);
                     const int at = h == 0 ? l.ca[j] : l.cb[j];
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
@@ -141,7 +141,7 @@ struct RopeTurn {
                 float tc[VEC], ts[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) tc[i] = 1.f, ts[i] = 0.f;
-                if (l.ra[j]) {
+                if (live && l.ra[j]) {
                     if (VEC % 4 == 0 && vec) {
 #pragma unroll
                         for (int i = 0; i < VEC / 4 * 4; i += 4) {
@@ -304,6 +304,20 @@ struct RopePlace {
     }
 };
 
+// Zeros to the heads of a padding token.
+template <class T, int VEC, int NP, bool ILV>
+__device__ __forceinline__ void rope_zeros(const RopeLane<VEC, NP, ILV>& l, T* y, int64_t stride, int n) {
+    using X = RopeVec<T, VEC>;
+#pragma unroll 1
+    for (int h = 0; h < n; ++h, y += stride) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            if (l.a[j] >= 0) X::store(y + l.a[j], X::zero());
+            if (l.b[j] >= 0) X::store(y + l.b[j], X::zero());
+        }
+    }
+}
+
 // A warp's heads, task after task, with the next ones in flight: every lane
 // copies its own accesses asynchronously into slots of shared memory of its
 // own (no barrier, no registers while they travel), kRopeRing - 1 heads ahead and
@@ -386,7 +400,8 @@ struct RopeStream {
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
         return r;
     }
-    // The accesses of the next head; `live`: this lane's token has values, `all`: every lane's of the warp.
+    // The accesses of the next head. `live`: this lane's token has values, `all`: every lane's of the warp (the
+    // backward's others get zeros; the forward chooses its outputs).
     template <class L>
     __device__ __forceinline__ void take(const RopeArgs& g, const RopeSide& sd, const L& l, bool live, bool all, Raw (&raw)[N][NP][2]) {
         if constexpr (kAsync) {
@@ -400,7 +415,7 @@ struct RopeStream {
                     raw[n][j][1] = shared(from + ((n * NP + j) * 2 + 1) * kAccess);
                 }
             send(g, sd, l);  // into the slot read one head ago
-            if (!all) {
+            if (N == 2 && !all) {
 #pragma unroll
                 for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -424,12 +439,14 @@ struct RopeStream {
 };
 
 // ------------------------------------------------------------ forward
-// One head of the forward from its accesses; `on`: there is a token.
+// One head of the forward from its accesses. `on`: there is a token; `pad`: it
+// is padding, whose zeros are chosen, not formed (0 times an infinite root,
+// angle or weight is not 0).
 template <class T, int VEC, int NP, bool ILV>
 __device__ __forceinline__ void rope_fwd_head(const RopeArgs& g, const RopeLane<VEC, NP, ILV>& l,
                                               const RopeWeightedTurn<T, VEC, NP, ILV>& turn,
-                                              const typename RopeVec<T, VEC>::Raw (&raw)[1][NP][2], T* y, bool on, bool mixed,
-                                              int lanes, float eps) {
+                                              const typename RopeVec<T, VEC>::Raw (&raw)[1][NP][2], T* y, bool on, bool pad,
+                                              bool mixed, int lanes, float eps) {
     using X = RopeVec<T, VEC>;
     using V = RopeVals<T, VEC>;
     V va[NP], vb[NP];
@@ -449,7 +466,7 @@ __device__ __forceinline__ void rope_fwd_head(const RopeArgs& g, const RopeLane<
     rope_sum(ss, lanes);
     const float2 r2 = f2_splat(rsqrtf(fmaf(ss[0], g.invD, eps)));
     V oa[NP], ob[NP];
-    if (mixed && __any_sync(kFullMask, !isfinite(ss[0]))) {
+    if (mixed && __any_sync(kFullMask, !pad && !isfinite(ss[0]))) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) turn.template apply<true>(l, j, va[j], vb[j], r2, oa[j], ob[j]);
     } else {
@@ -458,8 +475,8 @@ __device__ __forceinline__ void rope_fwd_head(const RopeArgs& g, const RopeLane<
     }
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-        if (on && l.a[j] >= 0) X::store(y + l.a[j], oa[j].round());
-        if (on && l.b[j] >= 0) X::store(y + l.b[j], ob[j].round());
+        if (on && l.a[j] >= 0) X::store(y + l.a[j], pad ? X::zero() : oa[j].round());
+        if (on && l.b[j] >= 0) X::store(y + l.b[j], pad ? X::zero() : ob[j].round());
     }
 }
 
@@ -481,13 +498,13 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_fwd(const __grid_cons
         const RopePlace at(g, k);
         RopeWeightedTurn<T, VEC, NP, ILV> turn;
         turn.set(l, w.a, w.b, g.cos + at.row * g.table_pitch, g.sin + at.row * g.table_pitch, g.vec_table != 0);
-        const bool live = k.on && !at.pad, all = __all_sync(kFullMask, live);  // (padding: zeros in, zeros out)
-        const float eps = at.none ? __int_as_float(0x7fffffff) : g.eps;        // no angle: NaN
+        const bool live = k.on && !at.pad, all = __all_sync(kFullMask, live);
+        const float eps = at.none ? __int_as_float(0x7fffffff) : g.eps;  // no angle: NaN
         T* y = rope_at<T>(sd.y, k);
         for (int h = 0; h < k.n; ++h, y += sd.y.head) {
             typename RopeVec<T, VEC>::Raw raw[1][NP][2];
             in.take(g, sd, l, live, all, raw);
-            rope_fwd_head<T, VEC, NP, ILV>(g, l, turn, raw, y, k.on, mixed, lanes, eps);
+            rope_fwd_head<T, VEC, NP, ILV>(g, l, turn, raw, y, k.on, !all && at.pad, mixed, lanes, eps);
         }
     }
 }
@@ -539,9 +556,9 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_fwd_few(const __grid_
 #pragma unroll
                 for (int j = 0; j < NP; ++j)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) now[0][j][i] = some && at.pad ? X::zero() : raw[d][0][j][i];
+                    for (int i = 0; i < 2; ++i) now[0][j][i] = raw[d][0][j][i];
                 load(d, h + d + DEPTH);
-                rope_fwd_head<T, VEC, NP, ILV>(g, l, turn, now, y, k.on, mixed, lanes, eps);
+                rope_fwd_head<T, VEC, NP, ILV>(g, l, turn, now, y, k.on, some && at.pad, mixed, lanes, eps);
                 y += sd.y.head;
             }
 }
@@ -595,10 +612,12 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_bwd(const __grid_cons
     for (int task = share.first; task < sd.tasks; task = task < sd.tasks - share.step ? task + share.step : sd.tasks) {
         const RopeTask k(g, sd, task);
         const RopePlace at(g, k);
-        R turn;
-        turn.set(l, g.cos + at.row * g.table_pitch, g.sin + at.row * g.table_pitch, g.vec_table != 0);
         const bool live = k.on && !at.pad, all = __all_sync(kFullMask, live);
-        const float eps = at.none ? __int_as_float(0x7fffffff) : g.eps;
+        R turn;
+        turn.set(l, g.cos + at.row * g.table_pitch, g.sin + at.row * g.table_pitch, g.vec_table != 0, live);
+        // A lane whose token has no values works on zeros, which have to stay
+        // zeros on their way to dw: its root is that of 1, finite for eps = 0 too.
+        const float eps = !live ? 1.f : at.none ? __int_as_float(0x7fffffff) : g.eps;
         T* dx = rope_at<T>(sd.y, k);
         for (int h = 0; h < k.n; ++h) {
             typename X::Raw raw[2][NP][2];
@@ -650,12 +669,13 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_bwd(const __grid_cons
                     da[j].v[i] = __ffma2_rn(__fmul2_rn(va[j].v[i], r2), za[j].v[i], da[j].v[i]);
                     db[j].v[i] = __ffma2_rn(__fmul2_rn(vb[j].v[i], r2), zb[j].v[i], db[j].v[i]);
                 }
-                if (k.on && l.a[j] >= 0) X::store(dx + l.a[j], oa.round());
-                if (k.on && l.b[j] >= 0) X::store(dx + l.b[j], ob.round());
+                if (live && l.a[j] >= 0) X::store(dx + l.a[j], oa.round());
+                if (live && l.b[j] >= 0) X::store(dx + l.b[j], ob.round());
             }
             dx += sd.y.head;
             if (++chain == kRopeChain) fold();
         }
+        if (k.on && at.pad) rope_zeros<T, VEC, NP, ILV>(l, rope_at<T>(sd.y, k), sd.y.head, k.n);
     }
     fold();
     __syncthreads();

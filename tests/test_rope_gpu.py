@@ -429,3 +429,53 @@ def test_refusals():
     big = torch.zeros(1, 1, 513, device="cuda")
     with pytest.raises(rn.NormError):
         rn.rms_fwd_rope(big, None, big[0, 0], None, cos, sin)
+
+
+# ------------------------------------------------------------ tokens without values, weights without bounds
+def finite(*ts):
+    return all(t is None or bool(t.isfinite().all()) for t in ts)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-50, 1e-6, 100.0])
+@pytest.mark.parametrize("T,D,R,interleaved", [(1, 128, 128, False), (3, 128, 64, True), (5, 128, 128, False), (37, 80, 32, True), (50, 7, 4, False)])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_every_eps(dtype, T, D, R, interleaved, eps):
+    """Padding and token counts that leave lane groups idle, where nothing but the values keeps the root from 0."""
+    q, k, wq, wk, cos, sin, pos, dq, dk = case(T, 5, 2, D, R, DT[dtype], seed=T)
+    if T > 2:
+        pos[1] = -1
+    plan, bplan = (rn.make_rope_plan(T, 5, 2, D, R, DT[dtype], interleaved, backward=b) for b in (False, True))
+    for few in (0, 1):
+        y = rn.rms_fwd_rope(q, k, wq, wk, cos, sin, pos, eps, interleaved=interleaved, plan=dict(plan, few=few))
+        assert finite(*y)
+        check_fwd(y[0], q, wq, cos, sin, pos, interleaved, eps)
+        check_fwd(y[1], k, wk, cos, sin, pos, interleaved, eps)
+    for ctas in (2, bplan["ctas"]):
+        g = rn.rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, pos, eps, interleaved=interleaved, plan=dict(bplan, ctas=ctas))
+        assert finite(*g)
+        check_bwd(g[0], g[2], dq, q, wq, cos, sin, pos, interleaved, eps)
+        check_bwd(g[1], g[3], dk, k, wk, cos, sin, pos, interleaved, eps)
+
+
+@pytest.mark.parametrize("v", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_padding_is_zero_beside_any_weight_and_table(interleaved, dtype, v):
+    """Padding reads no angle and no weight: its outputs are zeros and it adds nothing to dw."""
+    for D, R in ((128, 64), (50, 20)):
+        q, k, wq, wk, cos, sin, pos, dq, dk = case(11, 3, 2, D, R, DT[dtype], seed=5)
+        pos[pos == 0] = 1  # row 0 belongs to nobody
+        pos[2] = -1
+        pad = pos < 0
+        want = rn.rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, pos, EPS, interleaved=interleaved)
+        cos[0], sin[0] = v, v
+        got = rn.rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, pos, EPS, interleaved=interleaved)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        wq[3], wq[D - 1], wk[0] = v, v, v
+        plan = rn.make_rope_plan(11, 3, 2, D, R, DT[dtype], interleaved)
+        for few in (0, 1):
+            y = rn.rms_fwd_rope(q, k, wq, wk, cos, sin, pos, EPS, interleaved=interleaved, plan=dict(plan, few=few))
+            assert (y[0][pad] == 0).all() and (y[1][pad] == 0).all()
+        got = rn.rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, pos, EPS, interleaved=interleaved)
+        assert (got[0][pad] == 0).all() and (got[1][pad] == 0).all()
+        assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])  # (dw has no weight in it)
