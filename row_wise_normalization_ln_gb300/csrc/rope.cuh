@@ -196,8 +196,10 @@ struct RopeWeightedTurn {
             for (int i = 0; i < H; ++i) {
                 ca[j][i] = __fmul2_rn(wa[j].v[i], t.cos_of(j, i, false));
                 cb[j][i] = __fmul2_rn(wb[j].v[i], t.cos_of(j, i, true));
-                sa[j][i] = __fmul2_rn(R::mate(wa[j], wb[j], i, false), t.sin_of(j, i, false));
-                sb[j][i] = __fmul2_rn(R::mate(wa[j], wb[j], i, true), t.sin_of(j, i, true));
+                // (a mate's infinite weight times the sine 0 is not 0)
+                sa[j][i] = sb[j][i] = make_float2(0.f, 0.f);
+                if (l.ra[j]) sa[j][i] = __fmul2_rn(R::mate(wa[j], wb[j], i, false), t.sin_of(j, i, false));
+                if (l.rb[j]) sb[j][i] = __fmul2_rn(R::mate(wa[j], wb[j], i, true), t.sin_of(j, i, true));
             }
     }
     // SAFE: nothing of a mate reaches a value that does not rotate.

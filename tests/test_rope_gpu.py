@@ -479,3 +479,25 @@ def test_padding_is_zero_beside_any_weight_and_table(interleaved, dtype, v):
         got = rn.rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, pos, EPS, interleaved=interleaved)
         assert (got[0][pad] == 0).all() and (got[1][pad] == 0).all()
         assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])  # (dw has no weight in it)
+
+
+@pytest.mark.parametrize("v", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_weights_reach_their_own_column(interleaved, dtype, v):
+    """A weight that is not finite reaches its column, and its partner's where that one rotates, alone."""
+    for D, R, at in ((128, 64, 70), (128, 64, 100), (128, 64, 3), (96, 24, 95), (50, 20, 21), (50, 20, 49)):
+        q, _, wq, _, cos, sin, pos, _, _ = case(9, 3, 1, D, R, DT[dtype], seed=at, pad=False)
+        cos, sin = cos.clamp(min=0.1), sin.clamp(min=0.1)  # no angle hides a partner
+        plain = wq.clone()
+        wq[at] = v
+        hit = {at} if at >= R else {at, int(pairs(R, interleaved)[0][at])}
+        rest = [i for i in range(D) if i not in hit]
+        widest = rn.make_rope_plan(9, 3, 0, D, R, DT[dtype], interleaved)["vec_elems"]
+        for vec in [w for w in ((4, 1) if dtype == "f32" else (8, 4, 2, 1)) if w <= widest]:
+            for few in (0, 1):
+                plan = dict(rn.make_rope_plan(9, 3, 0, D, R, DT[dtype], interleaved, vec_elems=vec), few=few)
+                want, _ = rn.rms_fwd_rope(q, None, plain, None, cos, sin, pos, EPS, interleaved=interleaved, plan=plan)
+                y, _ = rn.rms_fwd_rope(q, None, wq, None, cos, sin, pos, EPS, interleaved=interleaved, plan=plan)
+                assert torch.equal(y[..., rest], want[..., rest]), (D, R, at, vec, few)
+                assert not y[..., sorted(hit)].isfinite().any()
