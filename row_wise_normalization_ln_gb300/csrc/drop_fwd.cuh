@@ -10,6 +10,9 @@
 // meet behind one barrier by the merge rule in its k-way form, the means as
 // differences from the first warp's A:
 //   m_w = (A_w - A_0) + c_w,  mean = sum n_w m_w / N,  M2 = sum M2_w + n_w (m_w - mean)^2.
+// The output is ((h - A_0) rstd - mean rstd) gamma + beta: the row's mean A_0 + mean
+// is rounded for the caller alone (a mean of 3e4 beside a spread of 1 would lose
+// its last 2e-3).
 // RMSNorm: sums of squares.
 //
 // RMSNorm bf16 65536 x 2048 170 us, 6.3 TB/s, memory bound; 4096 x 5001 29.9;
@@ -205,9 +208,9 @@ __global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V
             if (a.stages == 3) copy_async_wait<1>();
             else copy_async_wait<2>();     // the next row has landed; the barrier below makes it everyone's
         }
-        float rstd[R], mu[R];
+        float rstd[R], A0[R], off[R];  // LayerNorm: y = ((h - A0) rstd + off) gamma + beta
         if constexpr (LN) {
-            float A[R], A0[R], mean[R], q[R];
+            float A[R], mean[R], q[R];
             if (GROUP) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) A[r] = group_sum(s[r], pl.unit) * inv_warp;
@@ -334,9 +337,9 @@ __global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 rstd[r] = rsqrtf(fmaf(q[r], a.invN, a.eps));
-                mu[r] = A0[r] + mean[r];
+                off[r] = -mean[r] * rstd[r];
                 if (has(r) && pl.first) {
-                    if (a.mean) a.mean[row + r * pl.stride] = mu[r];
+                    if (a.mean) a.mean[row + r * pl.stride] = A0[r] + mean[r];
                     if (a.rstd) a.rstd[row + r * pl.stride] = rstd[r];
                 }
             }
@@ -355,6 +358,7 @@ __global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const float2 rs2 = f2_splat(rstd[r]);
+                [[maybe_unused]] const float2 off2 = f2_splat(LN ? off[r] : 0.f);
                 T* const yp = static_cast<T*>(a.y) + at + r * row_step;
 #pragma unroll
                 for (int j = 0; j < V; ++j)
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(LN && V == 4 && !ASIDE ? kDropNarrow : VEC * V
 #pragma unroll
                         for (int i = 0; i < H; ++i) {
                             if constexpr (LN)
-                                X::set(yr, i, __ffma2_rn(__fmul2_rn(X::plus(h[r][j], i, -mu[r]), rs2), X::get(gv, i), X::get(bv, i)));
+                                X::set(yr, i, __ffma2_rn(__ffma2_rn(X::plus(h[r][j], i, -A0[r]), rs2, off2), X::get(gv, i), X::get(bv, i)));
                             else
                                 X::set(yr, i, __fmul2_rn(X::mul(h[r][j], gv, i), rs2));
                         }

@@ -545,3 +545,26 @@ def test_refusals():
         rn.ln_bwd_dropout_add(y, h, h, gamma, mean, rstd, 0.1, RNG, dx=y, dresidual=y)
     with pytest.raises(rn.NormError, match="status -4"):
         rn.ln_fwd_dropout_add(x, r, gamma, beta, 0.1, RNG, plan=dict(rn.make_drop_plan(4, 64, x.dtype, True), per_thread=3))
+
+
+@pytest.mark.parametrize("loc", [300.0, 3e4, -2e5])
+@pytest.mark.parametrize("M,N", [(7, 96), (1000, 96), (5, 513), (33, 768), (9, 1024), (700, 1024), (33, 769), (6, 5001), (64, 4096), (300, 8192), (4, 16388)])
+def test_outputs_keep_their_digits_under_a_large_mean(M, N, loc):
+    """LayerNorm's y from h - A and mean - A, A near the mean: no rounding of the size of the mean itself. |h - A| <= S = 2 max|h - mu|
+    + 40 u mean|h| for each warp's A; mean - A is within 40 u S (32 u of a sum of such differences, the merge's), h - A within u S, the
+    fused multiply-add within 2 u of both: 44 u S rstd |gamma| beside rstd's own bar, and the output's roundings."""
+    for off in (0, 1):  # vectors, elements
+        x = torch.empty(M * N + off, device="cuda")[off:].view(M, N)
+        x.copy_(make(M, N, torch.float32, 0))
+        r = make(M, N, torch.float32, 1, loc, 2.0)
+        gamma, beta = params(N, torch.float32, 2)
+        for p in (0.0, 0.1):
+            h, y, mean, rstd = rn.ln_fwd_dropout_add(x, r, gamma, beta, p, RNG, EPS)
+            v, g, b = h.to(F), gamma.to(F), beta.to(F)
+            d = v - v.mean(1, keepdim=True)
+            rs = (d.square().mean(1, keepdim=True) + EPS) ** -0.5
+            S = 2 * d.abs().amax(1, keepdim=True) + 40 * U * v.abs().mean(1, keepdim=True)
+            t_rs = 64 * U * (1 + (40 * U * v.abs().mean(1, keepdim=True) * rs) ** 2)
+            xg = (d * rs * g).abs()
+            tol = xg * t_rs + 44 * U * S * rs * g.abs() + 4 * U * (xg + b.abs()) + U * (1 + 64 * U) * (d * rs * g + b).abs()
+            within(y, d * rs * g + b, tol, "y")
