@@ -835,8 +835,8 @@ def rms_fwd_rope(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, w
     tokens, its own heads (None: queries alone, ``wk`` None too). ``wq``,
     ``wk``: ``[D]``. ``cos``, ``sin``: fp32 tables ``[positions, R / 2]``;
     value pairs (i, i + R/2) turn by angle i, or ``interleaved`` (2i, 2i + 1).
-    ``positions``: int64 or int32, one per token (default: 0, 1, ... along
-    each sequence). A negative position marks a padding token, whose outputs
+    ``positions``: int64 or int32, one per token, flat or ``[B, S]`` (default:
+    0, 1, ... along each sequence). A negative position marks a padding token, whose outputs
     are zeros; one beyond the tables gives NaN.
 
     Returns ``(q_out, k_out)``; they may be ``q`` and ``k`` themselves (in

@@ -364,6 +364,19 @@ bool heads_of(const at::Tensor& t, norm_heads* h) {
     return t.size(n - 1) == 1 || t.stride(n - 1) == 1 || t.numel() == 0;
 }
 
+// Whether a tensor of one position per token lists them in the tokens' order:
+// flat, or, for [B, S, heads, D], as [B, S] (dimensions of one value aside).
+// [S, B] has as many values, in another order.
+bool in_token_order(const at::Tensor& p, const at::Tensor& q) {
+    if (q.dim() == 3) return true;
+    c10::SmallVector<int64_t, 4> have, want;
+    for (int64_t n : p.sizes())
+        if (n != 1) have.push_back(n);
+    for (int64_t n : {q.size(0), q.size(1)})
+        if (n != 1) want.push_back(n);
+    return have.size() <= 1 || have == want;
+}
+
 struct HeadCall {
     at::Tensor x[2], dy[2], w[2], out[2], dw[2], cos, sin, positions;  // queries, keys
     norm_rope_side side[2] = {};
@@ -436,8 +449,8 @@ void read_heads(HeadCall* c, PyObject* const* x, PyObject* const* w, PyObject* c
     if (positions != Py_None) {
         c->positions = tensor(positions, "positions");
         const at::ScalarType st = c->positions.scalar_type();
-        if ((st != at::kLong && st != at::kInt) || c->positions.device() != q.device() || c->positions.numel() != c->B * c->S)
-            refuse("positions must be int64 or int32 with one value per token (" + std::to_string(c->B * c->S) + ") on " + q.device().str());
+        if ((st != at::kLong && st != at::kInt) || c->positions.device() != q.device() || c->positions.numel() != c->B * c->S || !in_token_order(c->positions, q))
+            refuse("positions must be int64 or int32 with one value per token (" + std::to_string(c->B * c->S) + "), flat or [B, S], on " + q.device().str());
         if (!c->positions.is_contiguous()) c->positions = c->positions.contiguous();
         c->angles.positions = ptr(c->positions);
         c->angles.position_bytes = st == at::kLong ? 8 : 4;

@@ -501,3 +501,24 @@ def test_weights_reach_their_own_column(interleaved, dtype, v):
                 y, _ = rn.rms_fwd_rope(q, None, wq, None, cos, sin, pos, EPS, interleaved=interleaved, plan=plan)
                 assert torch.equal(y[..., rest], want[..., rest]), (D, R, at, vec, few)
                 assert not y[..., sorted(hit)].isfinite().any()
+
+
+def test_positions_of_another_shape():
+    """Sequences' positions come as [B, S] (or flat): another shape with as many values is another order."""
+    B, S = 3, 5
+    q, _, wq, _, cos, sin, pos, dq, _ = case(B * S, 2, 1, 64, 32, torch.bfloat16)
+    q, dq = q.view(B, S, 2, 64), dq.view(B, S, 2, 64)
+    want = rn.rms_fwd_rope(q, None, wq, None, cos, sin, pos, EPS)[0]
+    for good in (pos.view(B, S), pos.view(B, S, 1), pos.view(1, B, S), pos.view(1, -1), pos.view(B, S).t().contiguous().t()):
+        assert torch.equal(rn.rms_fwd_rope(q, None, wq, None, cos, sin, good, EPS)[0], want)
+    for bad in (pos.view(S, B), pos.view(B, S).t(), pos.view(S, 1, B)):
+        with pytest.raises(ValueError, match="one value per token"):
+            rn.rms_fwd_rope(q, None, wq, None, cos, sin, bad, EPS)
+        with pytest.raises(ValueError, match="one value per token"):
+            rn.rms_bwd_rope(dq, None, q, None, wq, None, cos, sin, bad, EPS)
+    # one sequence, and one token a sequence: the dimension of one counts for nothing
+    one = rn.rms_fwd_rope(q.reshape(1, B * S, 2, 64), None, wq, None, cos, sin, pos.view(-1, 1), EPS)[0]
+    assert torch.equal(one.view(B, S, 2, 64), want)
+    # tokens without sequences: any shape, in its order
+    flat = rn.rms_fwd_rope(q.reshape(B * S, 2, 64), None, wq, None, cos, sin, pos.view(B, S), EPS)[0]
+    assert torch.equal(flat.view(B, S, 2, 64), want)
