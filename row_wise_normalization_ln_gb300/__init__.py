@@ -840,8 +840,8 @@ def rms_fwd_rope(q: torch.Tensor, k: Optional[torch.Tensor], wq: torch.Tensor, w
     are zeros; one beyond the tables gives NaN.
 
     Returns ``(q_out, k_out)``; they may be ``q`` and ``k`` themselves (in
-    place), or views such as the step's rows of a cache. One token or many:
-    the same call."""
+    place), or views such as the step's rows of a cache, of which no two
+    values share memory. One token or many: the same call."""
     if stream is not None:
         return _on_stream(stream, q, lambda: rms_fwd_rope(q, k, wq, wk, cos, sin, positions, eps,
                                                           interleaved=interleaved, q_out=q_out, k_out=k_out, plan=plan))

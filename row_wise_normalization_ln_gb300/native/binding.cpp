@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 #include <exception>
 #include <limits>
 #include <stdexcept>
@@ -457,6 +458,39 @@ void read_heads(HeadCall* c, PyObject* const* x, PyObject* const* w, PyObject* c
     }
 }
 
+// Whether some address belongs to two values of t, heads of unit stride.
+bool shares_memory(const at::Tensor& t) {
+    if (t.numel() == 0) return false;
+    struct Dim {
+        int64_t size, stride;
+    };
+    c10::SmallVector<Dim, 4> d;
+    for (int64_t i = 0; i + 1 < t.dim(); ++i)
+        if (t.size(i) > 1) d.push_back({t.size(i), t.stride(i)});
+    std::sort(d.begin(), d.end(), [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    int64_t span = t.size(-1);  // of the dimensions so far: nested ones share nothing
+    bool nested = true;
+    for (const Dim& k : d) {
+        nested = nested && k.stride >= span;
+        span += (k.size - 1) * k.stride;
+    }
+    if (nested) return false;
+    // Two heads share memory if a sum of steps i_k stride_k, not all 0, is less
+    // than a head: every choice of the shorter dimensions' steps (of one sign
+    // for the first of them), and the nearest steps of the longest.
+    std::sort(d.begin(), d.end(), [](const Dim& a, const Dim& b) { return a.size < b.size; });
+    while (d.size() < 3) d.insert(d.begin(), {1, 0});
+    const Dim a = d[0], b = d[1], c = d[2];
+    if (c.stride == 0) return true;
+    for (int64_t i = 0; i < a.size; ++i)
+        for (int64_t j = i == 0 ? 0 : 1 - b.size; j < b.size; ++j) {
+            const int64_t at = i * a.stride + j * b.stride, near = -at / c.stride;
+            for (int64_t k = std::max(near - 1, 1 - c.size); k <= std::min(near + 1, c.size - 1); ++k)
+                if ((i || j || k) && std::abs(at + k * c.stride) < t.size(-1)) return true;
+        }
+    return false;
+}
+
 void read_head_outputs(HeadCall* c, PyObject* const* out, const char* const* names) {
     for (int i = 0; i < 2; ++i) {
         const at::Tensor& x = c->x[i];
@@ -471,9 +505,7 @@ void read_head_outputs(HeadCall* c, PyObject* const* out, const char* const* nam
             if (c->out[i].sizes() != x.sizes() || c->out[i].scalar_type() != x.scalar_type() || c->out[i].device() != x.device())
                 refuse(std::string(names[i]) + " must have " + kHeadNames[i] + "'s shape, dtype and device");
         }
-        bool ok = heads_of(c->out[i], &c->side[i].y);
-        for (int64_t d = 0; d < x.dim(); ++d) ok = ok && (x.size(d) <= 1 || c->out[i].stride(d) != 0 || x.numel() == 0);
-        if (!ok) refuse(std::string(names[i]) + " must have heads of unit stride that do not share memory");
+        if (!heads_of(c->out[i], &c->side[i].y) || (out[i] != Py_None && shares_memory(c->out[i]))) refuse(std::string(names[i]) + " must have heads of unit stride that do not share memory");
     }
 }
 

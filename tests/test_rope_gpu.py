@@ -522,3 +522,17 @@ def test_positions_of_another_shape():
     # tokens without sequences: any shape, in its order
     flat = rn.rms_fwd_rope(q.reshape(B * S, 2, 64), None, wq, None, cos, sin, pos.view(B, S), EPS)[0]
     assert torch.equal(flat.view(B, S, 2, 64), want)
+
+
+def test_outputs_that_share_memory_are_refused():
+    q, k, wq, wk, cos, sin, pos, dq, dk = case(4, 2, 1, 64, 32, torch.bfloat16)
+    buf = torch.zeros(4 * 2 * 64, dtype=torch.bfloat16, device="cuda")
+    for strides in ((64, 64, 1), (128, 32, 1), (32, 128, 1), (127, 64, 1), (64, 192, 1)):
+        out = buf.as_strided((4, 2, 64), strides)
+        with pytest.raises(ValueError, match="do not share memory"):
+            rn.rms_fwd_rope(q, k, wq, wk, cos, sin, pos, EPS, q_out=out)
+        with pytest.raises(ValueError, match="do not share memory"):
+            rn.rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, pos, EPS, dq_out=out)
+    for strides in ((128, 64, 1), (64, 256, 1)):  # tokens of heads, heads of tokens
+        out = buf.as_strided((4, 2, 64), strides)
+        assert torch.equal(rn.rms_fwd_rope(q, k, wq, wk, cos, sin, pos, EPS, q_out=out)[0], rn.rms_fwd_rope(q, k, wq, wk, cos, sin, pos, EPS)[0])
