@@ -148,6 +148,9 @@ norm_status derive(const norm_rope_plan& p, const Shape& s, int vec, RopeArgs* a
         d.tasks = d.heads > 0 ? static_cast<int32_t>(blocks * d.chunks) : 0;
         d.ctas = static_cast<int32_t>(ceil_div(d.tasks, p.warps));
     }
+    // a warp without a loop counts its task in 31 bits, the last CTA's idle warps too
+    for (const RopeSide& d : a->side)
+        if (p.few && int64_t(d.ctas) * p.warps > kMaxTokens + 1) return NORM_ERR_PLAN;
     return int64_t(a->side[0].ctas) + a->side[1].ctas <= kMaxTokens ? NORM_OK : NORM_ERR_PLAN;
 }
 

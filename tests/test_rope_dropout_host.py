@@ -225,3 +225,12 @@ def test_every_head_width_gets_a_plan(lib, dtype):
                 n = ctypes.c_size_t()
                 plan = rn.RopePlan.from_dict(p)
                 assert lib.rope_workspace_bytes(tokens, hq, hk, D, 152, ctypes.byref(plan), ctypes.byref(n)) == rn.NORM_OK
+
+
+def test_tasks_of_a_plan_fit_their_counter(lib):
+    """A warp of the forward without a loop counts its task in 31 bits: with the last CTA's idle warps, too."""
+    T = (1 << 31) - 1
+    base = dict(rn.make_rope_plan(T, 1, 0, 1, 0, torch.bfloat16, vec_elems=1), few=1, lanes=32, heads=1)
+    for warps in (3, 5, 6, 7):  # (2^31 - 1 tasks in CTAs of these end beyond 2^31 - 1)
+        p = ctypes.byref(rn.RopePlan.from_dict(dict(base, warps=warps)))
+        assert rope(lib, B=1, S=T, D=1, R=0, heads=1, pitch=1, dt=rn.NORM_BF16, plan=p) == rn.NORM_ERR_PLAN, warps
