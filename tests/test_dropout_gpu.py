@@ -568,3 +568,27 @@ def test_outputs_keep_their_digits_under_a_large_mean(M, N, loc):
             xg = (d * rs * g).abs()
             tol = xg * t_rs + 44 * U * S * rs * g.abs() + 4 * U * (xg + b.abs()) + U * (1 + 64 * U) * (d * rs * g + b).abs()
             within(y, d * rs * g + b, tol, "y")
+
+
+def test_groups_beyond_32_bits():
+    """The counter's upper word: elements from 2^35 on, 64 GB a tensor. Only the last rows, and those before the border, are looked at."""
+    N = 8192
+    M, border = (1 << 35) // N + 3, (1 << 35) // N
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GB of the device")
+    x = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    x[-6:] = make(6, N, torch.bfloat16, 1)
+    x[-6:] += (x[-6:] == 0)
+    was = x[-6:].clone()
+    w = torch.ones(N, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty_like(x)
+    h, _ = rn.rms_fwd_dropout_add(x, x, w, 0.25, RNG, h_out=x, out=y)  # x is its own residual: x (1 + keep / P(keep))
+    keep = torch.from_numpy(keep_mask(*RNG, 0.25, M, N, rows=(M - 6, M))).cuda()
+    assert M - 6 < border < M
+    ref = was.to(F) * (1 + keep * (65536 / (65536 - threshold(0.25))))
+    within(h[-6:], ref, (3 * U + eta(torch.bfloat16) * (1 + 8 * U)) * ref.abs() + tiny(torch.bfloat16), "h")
+    dx, dr, _ = rn.rms_bwd_dropout_add(h, h, h, w, 0.25, RNG, dx=y, dresidual=h)
+    assert torch.equal(dx[-6:] != 0, keep & (dr[-6:] != 0)) and (dr[-6:] != 0).float().mean() > 0.9
+    del x, y, h, dx, dr
+    torch.cuda.empty_cache()

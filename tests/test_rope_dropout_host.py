@@ -234,3 +234,31 @@ def test_tasks_of_a_plan_fit_their_counter(lib):
     for warps in (3, 5, 6, 7):  # (2^31 - 1 tasks in CTAs of these end beyond 2^31 - 1)
         p = ctypes.byref(rn.RopePlan.from_dict(dict(base, warps=warps)))
         assert rope(lib, B=1, S=T, D=1, R=0, heads=1, pitch=1, dt=rn.NORM_BF16, plan=p) == rn.NORM_ERR_PLAN, warps
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_workspaces_of_the_head_norms(lib, dtype):
+    rng = random.Random(4)
+    for _ in range(300):
+        tokens, hq, hk, D = int(2 ** rng.uniform(0, 20)), rng.randint(1, 64), rng.randint(0, 16), rng.randint(1, 512)
+        p = rn.make_rope_plan(tokens, hq, hk, D, 2 * rng.randint(0, D // 2), dtype, backward=True, vec_elems=1)
+        n, whole = ctypes.c_size_t(), ctypes.c_size_t()
+        assert lib.rope_workspace_bytes(tokens, hq, hk, D, 0, ctypes.byref(rn.RopePlan.from_dict(p)), ctypes.byref(n)) == rn.NORM_OK
+        assert n.value == min(p["ctas"], tokens * (hq + hk)) * D * 4
+        assert lib.rope_workspace_bytes(tokens, hq, hk, D, 152, None, ctypes.byref(whole)) == rn.NORM_OK
+        assert whole.value >= n.value
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_every_kernel_of_the_dropout_norms_is_planned(lib, backward):
+    """Each instance (accesses a thread, rows a step, who shares a row) is some shape's."""
+    for dtype in DT:
+        got = set()
+        for ln in (True, False):
+            for M in (1, 100, 608, 609, 5000, 100000):
+                for N in [8, 64, 128, 256, 500, 512, 1000, 1400, 2000, 2040, 4096, 5001, 8192, 20000]:
+                    for aligned in (True, False):
+                        p = rn.make_drop_plan(M, N, dtype, ln, backward, aligned)
+                        got.add((p["vec_elems"] > 1, p["mapping"], p["per_thread"], p["rounds"]))
+        wide = (True, 1, 2, 2) if backward and dtype.itemsize == 2 else (True, 1, 4, 1)
+        assert got == {(False, 1, 8, 1), (True, 0, 2, 2), (True, 1, 1, 4), wide} | (set() if backward else {(True, 1, 1, 1)}), dtype

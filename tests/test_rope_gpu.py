@@ -536,3 +536,17 @@ def test_outputs_that_share_memory_are_refused():
     for strides in ((128, 64, 1), (64, 256, 1)):  # tokens of heads, heads of tokens
         out = buf.as_strided((4, 2, 64), strides)
         assert torch.equal(rn.rms_fwd_rope(q, k, wq, wk, cos, sin, pos, EPS, q_out=out)[0], rn.rms_fwd_rope(q, k, wq, wk, cos, sin, pos, EPS)[0])
+
+
+def test_workspace_of_exactly_its_size():
+    for dtype, T, hq, hk, D in ((torch.float32, 700, 5, 2, 80), (torch.bfloat16, 3, 1, 1, 64), (torch.bfloat16, 5000, 16, 4, 128)):
+        q, k, wq, wk, cos, sin, pos, dq, dk = case(T, hq, hk, D, D // 8 * 4, dtype)
+        want = rn.rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, pos, EPS)
+        n = min(rn.make_rope_plan(T, hq, hk, D, D // 8 * 4, dtype, backward=True,
+                                  num_sms=torch.cuda.get_device_properties(0).multi_processor_count)["ctas"], T * (hq + hk)) * D * 4
+        buf = torch.full((n + 256,), 77, dtype=torch.uint8, device="cuda")
+        got = rn.rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, pos, EPS, workspace=buf[:n])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert (buf[n:] == 77).all()
+        with pytest.raises(rn.NormError, match="status -1"):
+            rn.rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, pos, EPS, workspace=buf[:n - 16])
