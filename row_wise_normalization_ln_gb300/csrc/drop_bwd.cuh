@@ -23,7 +23,7 @@
 namespace libnorm {
 
 template <class T, int VEC, int V, int R, bool LN, bool GROUP>
-__global__ void __launch_bounds__(VEC * V >= 32 ? 256 : kDropMaxThreads, VEC * V >= 32 && !LN ? 2 : 1) drop_bwd(const __grid_constant__ DropArgs a) {
+__global__ void __launch_bounds__(kDropMaxThreads, 1) drop_bwd(const __grid_constant__ DropArgs a) {
     using P = DropPlace<VEC, V, GROUP>;
     using X = DropVec<T, VEC>;
     using Raw = typename X::Raw;
@@ -283,12 +283,10 @@ cudaError_t drop_launch_bwd(const norm_plan& p, DropArgs& a, cudaStream_t s) {
     const bool teams = p.threads > (GROUP ? a.lanes : a.team);
     const size_t smem = static_cast<size_t>(a.sums_at + (teams ? drop_sums_bytes(LN, VEC, V, p.threads) : 0));
     int64_t grid = 0;
-    if (a.M > 0) {
-        cudaError_t e = drop_grid(fn, p, a, smem, &grid);
-        if (e != cudaSuccess) return e;
-        e = drop_launch(fn, grid, p.threads, smem, p.cluster, s, a);
-        if (e != cudaSuccess) return e;
-    }
+    cudaError_t e = drop_grid(fn, p, a, smem, &grid);
+    if (e != cudaSuccess) return e;
+    e = drop_launch(fn, grid, p.threads, smem, p.cluster, s, a);
+    if (e != cudaSuccess) return e;
     return launch_drop_colsum(a, grid / p.cluster, LN, s);
 }
 
