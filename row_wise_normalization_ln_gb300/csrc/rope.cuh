@@ -196,10 +196,11 @@ struct RopeWeightedTurn {
             for (int i = 0; i < H; ++i) {
                 ca[j][i] = __fmul2_rn(wa[j].v[i], t.cos_of(j, i, false));
                 cb[j][i] = __fmul2_rn(wb[j].v[i], t.cos_of(j, i, true));
+                sa[j][i] = __fmul2_rn(R::mate(wa[j], wb[j], i, false), t.sin_of(j, i, false));
+                sb[j][i] = __fmul2_rn(R::mate(wa[j], wb[j], i, true), t.sin_of(j, i, true));
                 // (a mate's infinite weight times the sine 0 is not 0)
-                sa[j][i] = sb[j][i] = make_float2(0.f, 0.f);
-                if (l.ra[j]) sa[j][i] = __fmul2_rn(R::mate(wa[j], wb[j], i, false), t.sin_of(j, i, false));
-                if (l.rb[j]) sb[j][i] = __fmul2_rn(R::mate(wa[j], wb[j], i, true), t.sin_of(j, i, true));
+                if (!l.ra[j]) sa[j][i] = make_float2(0.f, 0.f);
+                if (!l.rb[j]) sb[j][i] = make_float2(0.f, 0.f);
             }
     }
     // SAFE: nothing of a mate reaches a value that does not rotate.
@@ -595,6 +596,7 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_bwd(const __grid_cons
             mine_sums[((j * 2) * H + i) * blockDim.x] = mine_sums[((j * 2 + 1) * H + i) * blockDim.x] = make_float2(0.f, 0.f);
         }
     int chain = 0;
+    bool padded = false;  // this lane met padding
     const auto fold = [&] {
 #pragma unroll
         for (int j = 0; j < NP; ++j)
@@ -620,6 +622,7 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_bwd(const __grid_cons
         // A lane whose token has no values works on zeros, which have to stay
         // zeros on their way to dw: its root is that of 1, finite for eps = 0 too.
         const float eps = !live ? 1.f : at.none ? __int_as_float(0x7fffffff) : g.eps;
+        padded = padded || at.pad;
         T* dx = rope_at<T>(sd.y, k);
         for (int h = 0; h < k.n; ++h) {
             typename X::Raw raw[2][NP][2];
@@ -677,9 +680,17 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_bwd(const __grid_cons
             dx += sd.y.head;
             if (++chain == kRopeChain) fold();
         }
-        if (k.on && at.pad) rope_zeros<T, VEC, NP, ILV>(l, rope_at<T>(sd.y, k), sd.y.head, k.n);
     }
     fold();
+    // Padding's zeros, behind everything: in the loop over the heads they cost a
+    // choice per store (16384 tokens 89.8 us instead of 86.9), behind a token's
+    // heads registers, and with them CTAs (f32 715 x 64 heads of 128 17.5 instead
+    // of 13.4).
+    if (padded)
+        for (int task = share.first; task < sd.tasks; task = task < sd.tasks - share.step ? task + share.step : sd.tasks) {
+            const RopeTask k(g, sd, task);
+            if (k.on && rope_position(g, k.t, k.s) < 0) rope_zeros<T, VEC, NP, ILV>(l, rope_at<T>(sd.y, k), sd.y.head, k.n);
+        }
     __syncthreads();
     // A column's terms lie with the lanes of its place in every group of
     // every warp: added in that order, each column by one thread.
