@@ -444,7 +444,8 @@ struct RopeStream {
 // ------------------------------------------------------------ forward
 // One head of the forward from its accesses. `on`: there is a token; `pad`: it
 // is padding, whose zeros are chosen, not formed (0 times an infinite root,
-// angle or weight is not 0).
+// angle or weight is not 0), or there is none; what such lanes hold has no say
+// in how the others' heads are turned.
 template <class T, int VEC, int NP, bool ILV>
 __device__ __forceinline__ void rope_fwd_head(const RopeArgs& g, const RopeLane<VEC, NP, ILV>& l,
                                               const RopeWeightedTurn<T, VEC, NP, ILV>& turn,
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_fwd(const __grid_cons
         for (int h = 0; h < k.n; ++h, y += sd.y.head) {
             typename RopeVec<T, VEC>::Raw raw[1][NP][2];
             in.take(g, sd, l, live, all, raw);
-            rope_fwd_head<T, VEC, NP, ILV>(g, l, turn, raw, y, k.on, !all && at.pad, mixed, lanes, eps);
+            rope_fwd_head<T, VEC, NP, ILV>(g, l, turn, raw, y, k.on, !all && !live, mixed, lanes, eps);
         }
     }
 }

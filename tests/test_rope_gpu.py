@@ -550,3 +550,24 @@ def test_workspace_of_exactly_its_size():
         assert (buf[n:] == 77).all()
         with pytest.raises(rn.NormError, match="status -1"):
             rn.rms_bwd_rope(dq, dk, q, k, wq, wk, cos, sin, pos, EPS, workspace=buf[:n - 16])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_what_ran_before_changes_no_bit(interleaved, dtype):
+    """Lanes without a token hold what an earlier kernel left; the sign of a resting -0 shows whether it counts."""
+    T, H, D, R = 5, 4, 128, 64
+    q, _, wq, _, cos, sin, pos, _, _ = case(T, H, 1, D, R, DT[dtype], pad=False)
+    wq = wq.abs() + 0.5
+    q[..., R:] = q[..., R:].abs() + 0.5
+    q[..., R::3] = -0.0
+    before = make((4096, H, D), DT[dtype], 1)
+    plan = dict(rn.make_rope_plan(T, H, 0, D, R, DT[dtype], interleaved), few=0)
+    far = torch.zeros(4096, dtype=torch.int64, device="cuda")
+    bits = []
+    for v in (0.0, float("inf")):
+        rn.rms_fwd_rope(before.fill_(v), None, wq, None, cos, sin, far, EPS, interleaved=interleaved, plan=dict(plan, ctas=1216, heads=4))
+        y, _ = rn.rms_fwd_rope(q, None, wq, None, cos, sin, pos, EPS, interleaved=interleaved, plan=plan)
+        assert y.isfinite().all()
+        bits.append(y.view(torch.int32 if DT[dtype] == torch.float32 else torch.int16))
+    assert torch.equal(*bits)
