@@ -67,8 +67,9 @@ typedef struct {
 } norm_rope_plan;
 
 /*
- * Forward. A token whose position is negative is padding: its heads are not
- * read and its outputs are zeros. One whose position is P or beyond has no
+ * Forward. A token whose position is negative is padding: its outputs are
+ * zeros, whatever its heads (which may be read all the same), the weight and
+ * the tables hold, and for every eps. One whose position is P or beyond has no
  * angle: its outputs are NaN (nothing beyond the tables is read). Outputs
  * may be the inputs themselves (same data and pitches); any other overlap is
  * undefined. Limits: 1 <= D <= 512, B, S, heads >= 0, B * S < 2^31,

@@ -1,7 +1,7 @@
 """Build libnorm.so in-tree: nvcc for sm_103a, one object per translation
 unit compiled in parallel, static CUDA runtime, no cmake. Next to it
-_binding.so, the native half of the Python binding of the group norm and
-gradient calls (g++ against the installed torch's headers, linked with
+_binding.so, the native half of the Python binding of the group norm, gradient,
+head norm and dropout calls (g++ against the installed torch's headers, linked with
 libnorm.so); where that does not build, the rest does."""
 from __future__ import annotations
 

@@ -75,7 +75,13 @@ int64_t accesses(const Shape& s, int vec) { return vec == 1 ? ceil_div(s.N, 2) :
 //   16384 x 1024 35.4 us [two accesses, two rows: 54], 8192 x 4096 66.2 [76.8]. Two
 //   teams of 192 or 224 threads would leave much of an SM idle: 16-bit rows of 161
 //   to 224 vectors take the other form (RMSNorm 24876 x 1424 53.2 us [60.1],
-//   17692 x 1656 62.8 [65.9]).
+//   17692 x 1656 62.8 [65.9]). One team of 288 to 448 threads leaves as much idle,
+//   yet rows of 257 to 448 vectors stay with the first form, which is right for
+//   most fp32 rows alone (LayerNorm with dropout f32 13084 x 1280 62.9 us [62.6],
+//   9344 x 1792 58.6 [65.3], RMSNorm 14536 x 1152 64.8 [61.0], 9344 x 1792 56.7 [61.3];
+//   bf16 LayerNorm 14536 x 2304 82.2 [71.3], 10064 x 3328 75.9 [70.5], 9344 x 3584 73.7
+//   [69.6], RMSNorm 14536 x 2304 79.3 [59.2], 10064 x 3328 72.1 [65.9]; the other form
+//   at its best number of teams and CTAs).
 //   Above, two accesses and two rows (16-bit), or four and one: more threads do
 //   not fit the columns' sums into their registers.
 // - Forward: four accesses, one row: LayerNorm 16384 x 2048 46.3 us [one access,

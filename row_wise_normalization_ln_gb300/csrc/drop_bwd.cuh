@@ -11,11 +11,14 @@
 // a partial row (in the workspace; in shared memory where the teams of a CTA
 // have columns in common), so that no chain of additions is long.
 //
-// LayerNorm bf16 4096 x 8192 70 us, 4.8 TB/s; RMSNorm 62; RMSNorm f32 2047 x 5000
-// 42.6; RMSNorm bf16 65536 x 2048 211, 6.4 TB/s. Wide rows are bound by their
-// instructions' latency: the columns' sums leave room for 16 warps an SM, which
-// issue in 58% of the cycles; without the generator the first takes 71, too.
-// Rows of up to 512 vectors have several teams an SM and come near the copy.
+// LayerNorm bf16 4096 x 8192 72 us, 4.7 TB/s; RMSNorm 61.5; RMSNorm f32 2047 x 5000
+// 42; RMSNorm bf16 65536 x 2048 208, 6.5 TB/s. Wide rows are bound by instructions
+// and their latency: one team of 16 warps is all that an SM has, it waits as a
+// whole at each barrier, and issues in 53% of the cycles; both readings of a row
+// unpack it and form dy gamma and h - mean, 40 instructions an element where the
+// plain norm's backward, with the row in registers, takes 22. The mask is little
+// of it (without dropout 68). Rows of up to 512 vectors that fill their teams
+// have several of them an SM and come near the copy.
 #pragma once
 
 #include "drop_kernels.cuh"

@@ -15,8 +15,8 @@
 // its last 2e-3).
 // RMSNorm: sums of squares.
 //
-// RMSNorm bf16 65536 x 2048 170 us, 6.3 TB/s, memory bound; 4096 x 5001 29.9;
-// LayerNorm 8192 x 4096 44, 6.1 TB/s; 4096 x 8192 45.4, 4096 x 5001 35.5: the chain of
+// RMSNorm bf16 65536 x 2048 171 us, 6.3 TB/s, memory bound; 4096 x 5001 29.2;
+// LayerNorm 8192 x 4096 42.7, 6.3 TB/s; 4096 x 8192 43.4, 4096 x 5001 35.3: the chain of
 // sums, barrier and merge of a row is longer than its bytes take, and 2 (3) CTAs an
 // SM hide part of it. 23 (RMSNorm) and 34 instructions an element, half of them
 // the mask's and the conversions'. f32 128 x 1024 2.2 us: latency.

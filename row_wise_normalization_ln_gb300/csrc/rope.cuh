@@ -20,9 +20,9 @@
 // until the backward's column sums.
 //
 // bf16, 16384 tokens of 32 + 8 heads of 128: forward 56.3 us, 6.0 TB/s, backward
-// 86, 5.9 TB/s, bound by memory (with a group on a head each and all of a task's
-// heads in registers 73 and 168). One token 1.65 us, f16 501 x 16 x 80 2.25, f32
-// backward 1023 x 24 x 96 11.5: launches and latency.
+// 87, 5.8 TB/s, bound by memory (with a group on a head each and all of a task's
+// heads in registers 73 and 168). One token 1.67 us, f16 501 x 16 x 80 2.3, f32
+// backward 1023 x 24 x 96 11.7: launches and latency.
 #pragma once
 
 #include "gn_kernels.cuh"
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_fwd(const __grid_cons
 // For few heads: a warp has one task and its heads come straight into
 // registers, the first before its position is known. No shared memory to go
 // through: one token of 36 heads 1.7 us instead of 2.2, 501 x 16 heads of 80
-// 2.2 instead of 2.7 (but 16384 x 40 heads of 128 66 instead of 56: a load per
+// 2.3 instead of 2.7 (but 16384 x 40 heads of 128 66 instead of 56: a load per
 // lane and access in flight is too little for the latency under load).
 template <class T, int VEC, int NP, bool ILV>
 __global__ void __launch_bounds__(kRopeMaxWarps * 32) rope_fwd_few(const __grid_constant__ RopeArgs g) {
